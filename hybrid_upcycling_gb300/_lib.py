@@ -1,4 +1,4 @@
-"""ctypes binding of libhylo_kl.so (include/hylo_kl.h): argument marshalling only.
+"""ctypes binding of libhylo_kl.so (include/hylo_kl.h, include/hylo_ops.h): argument marshalling only.
 
 Every function here has the name of the C entry point it calls and does no arithmetic of the
 loss: it checks tensor dtypes/shapes/devices, passes raw device pointers, sizes and the
@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -30,7 +31,11 @@ STATUS = {
 EXPORTS = ("hylo_kl_workspace_bytes", "hylo_kl_forward", "hylo_kl_backward", "hylo_kl_sync_status",
            "hylo_kl_workspace_bytes_split", "hylo_kl_backward_split",
            "hylo_kl_last_error", "hylo_kl_forward_noalloc", "hylo_kl_selftest_wait_timeout",
-           "hylo_fused_kl_logits", "hylo_ild_loss")
+           "hylo_fused_kl_logits", "hylo_ild_loss", "hylo_token_logprobs", "hylo_token_logprobs_backward",
+           "hylo_grad_norm_workspace_bytes", "hylo_grad_norm", "hylo_adamw_step")
+
+DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}  # hylo_dtype
+TOP_MAX = 64  # HYLO_TOP_MAX
 
 
 class HyloError(RuntimeError):
@@ -67,6 +72,17 @@ def load() -> ctypes.CDLL:
     L.hylo_fused_kl_logits.restype = ctypes.c_int
     L.hylo_ild_loss.argtypes = [vp, vp, i64, i64, i64, f32, vp, vp, vp, vp]
     L.hylo_ild_loss.restype = ctypes.c_int
+    i32, f64 = ctypes.c_int, ctypes.c_double
+    L.hylo_token_logprobs.argtypes = [vp, i32, i64, i64, i64, f32, vp, i32, vp, vp, vp, vp, vp, vp, vp]
+    L.hylo_token_logprobs.restype = ctypes.c_int
+    L.hylo_token_logprobs_backward.argtypes = [vp, i32, i64, i64, i64, f32, vp, vp, vp, vp, vp, vp, i64, vp]
+    L.hylo_token_logprobs_backward.restype = ctypes.c_int
+    L.hylo_grad_norm_workspace_bytes.argtypes = []
+    L.hylo_grad_norm_workspace_bytes.restype = sz
+    L.hylo_grad_norm.argtypes = [vp, vp, i32, i32, vp, vp, sz, vp]
+    L.hylo_grad_norm.restype = ctypes.c_int
+    L.hylo_adamw_step.argtypes = [vp, i32, i32, i32, i32, f64, f64, f64, i64, f32, vp, f32, ctypes.c_uint32, vp]
+    L.hylo_adamw_step.restype = ctypes.c_int
     L.hylo_kl_selftest_wait_timeout.argtypes = [ctypes.c_int, vp]
     L.hylo_kl_selftest_wait_timeout.restype = ctypes.c_int
     L.hylo_kl_sync_status.argtypes = [vp]
@@ -178,6 +194,94 @@ def hylo_ild_loss(S, T, grad_scale: float, norms, loss, dS=None, stream=None) ->
     P, N, d = S.shape
     _check(load().hylo_ild_loss(_ptr(S), _ptr(T), P, N, d, float(grad_scale), _ptr(norms), _ptr(loss), _ptr(dS),
                                 _stream(stream)))
+
+
+def _need_cuda(**tensors) -> None:
+    """Every tensor (None is skipped) must lie on the current CUDA device: the library launches there."""
+    dev = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if dev is None:
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor")
+            dev = torch.cuda.current_device()
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be on the current CUDA device ({dev})")
+
+
+def _need(name: str, t: Optional[torch.Tensor], dtype, shape) -> None:
+    if t is not None and (t.dtype != dtype or t.shape != shape or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+
+
+def _row_stride(name: str, z) -> int:
+    """Row stride of a 2-D tensor with unit column stride (one row: any stride the tensor reports)."""
+    if z.dim() != 2 or (z.shape[1] > 1 and z.stride(1) != 1):
+        raise ValueError(f"{name} must be 2-D with unit column stride")
+    N, V = z.shape
+    ld = z.stride(0) if N > 1 else max(V, z.stride(0))
+    if ld < V:
+        raise ValueError(f"{name} has overlapping rows")
+    return ld
+
+
+def hylo_token_logprobs(z, tokens, tau: float, k: int, logp, entropy=None, lse=None, stats=None, top_logp=None,
+                        top_ids=None, stream=None) -> None:
+    """Log-probabilities of `tokens` (int64 [N]) under logits z [N, V] (fp32, bf16 or fp16; unit column stride)."""
+    if z.dtype not in DTYPES:
+        raise ValueError("z must be float32, bfloat16 or float16")
+    ld = _row_stride("z", z)
+    N, V = z.shape
+    _need_cuda(z=z, tokens=tokens, logp=logp, entropy=entropy, lse=lse, stats=stats, top_logp=top_logp, top_ids=top_ids)
+    _need("tokens", tokens, torch.int64, (N,))
+    for name, t in (("logp", logp), ("entropy", entropy), ("lse", lse)):
+        _need(name, t, torch.float32, (N,))
+    _need("stats", stats, torch.float32, (N, 2))
+    _need("top_logp", top_logp, torch.float32, (N, k))
+    _need("top_ids", top_ids, torch.int64, (N, k))
+    _check(load().hylo_token_logprobs(z.data_ptr(), DTYPES[z.dtype], N, V, ld, float(tau), tokens.data_ptr(), int(k),
+                                      _ptr(logp), _ptr(entropy), _ptr(lse), _ptr(stats), _ptr(top_logp), _ptr(top_ids),
+                                      _stream(stream)))
+
+
+def hylo_token_logprobs_backward(z, tokens, tau: float, stats, entropy, g_logp, g_entropy, dz, stream=None) -> None:
+    """Gradient dz (dtype and shape of z, unit column stride) for the upstream g_logp, g_entropy [N] (either None)."""
+    if z.dtype not in DTYPES or dz.dtype != z.dtype or dz.shape != z.shape:
+        raise ValueError("z must be float32, bfloat16 or float16, and dz of z's dtype and shape")
+    ld, ldd = _row_stride("z", z), _row_stride("dz", dz)
+    N, V = z.shape
+    _need_cuda(z=z, tokens=tokens, stats=stats, entropy=entropy, g_logp=g_logp, g_entropy=g_entropy, dz=dz)
+    _need("tokens", tokens, torch.int64, (N,))
+    for name, t in (("entropy", entropy), ("g_logp", g_logp), ("g_entropy", g_entropy)):
+        _need(name, t, torch.float32, (N,))
+    _need("stats", stats, torch.float32, (N, 2))
+    _check(load().hylo_token_logprobs_backward(z.data_ptr(), DTYPES[z.dtype], N, V, ld, float(tau), tokens.data_ptr(),
+                                               _ptr(stats), _ptr(entropy), _ptr(g_logp), _ptr(g_entropy), dz.data_ptr(),
+                                               ldd, _stream(stream)))
+
+
+def hylo_grad_norm_workspace_bytes() -> int:
+    return int(load().hylo_grad_norm_workspace_bytes())
+
+
+def hylo_grad_norm(pointers, sizes, dtype, norm, workspace, stream=None) -> None:
+    """Global norm of gradients given as lists of device pointers and element counts (see optim.grad_norm)."""
+    n = len(pointers)
+    _check(load().hylo_grad_norm((ctypes.c_uint64 * n)(*pointers), (ctypes.c_int64 * n)(*sizes), n, DTYPES[dtype],
+                                 norm.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                 _stream(stream)))
+
+
+ADAMW_TENSOR = "QQQQQQQqdd"  # hylo_adamw_tensor: seven pointers, the element count, lr, weight_decay
+
+
+def hylo_adamw_step(fields, count: int, param_dtype, grad_dtype, state_bits: int, betas, eps: float, step: int,
+                    grad_scale: float, norm, max_norm: float, seed: int, stream=None) -> None:
+    """One AdamW step; fields: the hylo_adamw_tensor members of all tensors, one after another (see optim.adamw_step)."""
+    table = struct.pack("=" + ADAMW_TENSOR * count, *fields)
+    _check(load().hylo_adamw_step(table, count, DTYPES[param_dtype], DTYPES[grad_dtype], state_bits, betas[0], betas[1],
+                                  eps, step, grad_scale, _ptr(norm), max_norm, seed & 0xFFFFFFFF, _stream(stream)))
 
 
 def hylo_kl_selftest_wait_timeout(limit_ms: int, stream=None) -> None:

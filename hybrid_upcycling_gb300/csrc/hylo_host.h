@@ -1,0 +1,45 @@
+// Host-side helpers shared by the files that implement the C ABI: error text, the per-device
+// state, tensor maps. Defined in hylo_kl_api.cu.
+#pragma once
+
+#include <string>
+
+#include "../../include/hylo_kl.h"
+#include "hylo_internal.h"
+
+namespace hylo {
+
+struct DeviceState {
+  bool init = false;
+  bool sm103 = false;
+  int sms = 0;
+  int fused_clusters = 0;  // 2-CTA clusters of the fused kernels resident at once
+  int logits_clusters = 0; // clusters of the logits kernel resident at once
+  int pipe_clusters = 0;   // 2-CTA clusters of the pipelined backward resident at once
+  unsigned pace_epoch = 0;  // epoch of the last paced fused launch on this device
+  int* status = nullptr;
+  std::string why;
+};
+
+void clear_error();
+hylo_status fail(hylo_status s, const char* fmt, ...);
+hylo_status cuda_fail(cudaError_t e, const char* what);
+
+// Time limit of one device-side wait.
+unsigned long long wait_limit_ns();
+
+// The current device's state, set up on first use; HYLO_ERR_ARCH if it is not sm_103.
+hylo_status current_device(DeviceState** out);
+
+// 2-D tensor map, 128-byte swizzle, zero fill outside the tensor.
+hylo_status make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t inner, uint64_t outer,
+                     uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer);
+// 3-D tensor map [outer2][outer1][inner] (contiguous), zero fill outside.
+hylo_status make_map_3d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t inner, uint64_t outer1,
+                        uint64_t outer2, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer1,
+                        CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
+
+inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+}  // namespace hylo

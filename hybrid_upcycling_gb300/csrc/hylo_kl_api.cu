@@ -11,33 +11,24 @@
 
 #include <cudaTypedefs.h>
 
-#include "../../include/hylo_kl.h"
-#include "hylo_internal.h"
+#include "hylo_host.h"
 
 namespace hylo {
-namespace {
 
+namespace {
 __device__ int g_device_status;  // 0, or the first device-side error code since the last read
 
 thread_local std::string g_last_error;
 
 constexpr int kMaxDevices = 64;
 
-struct DeviceState {
-  bool init = false;
-  bool sm103 = false;
-  int sms = 0;
-  int fused_clusters = 0;  // 2-CTA clusters of the fused kernels resident at once
-  int logits_clusters = 0; // clusters of the logits kernel resident at once
-  int pipe_clusters = 0;   // 2-CTA clusters of the pipelined backward resident at once
-  unsigned pace_epoch = 0;  // epoch of the last paced fused launch on this device
-  int* status = nullptr;
-  std::string why;
-};
-
 std::mutex g_mu;
 DeviceState g_dev[kMaxDevices];
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+
+}  // namespace
+
+void clear_error() { g_last_error.clear(); }
 
 hylo_status fail(hylo_status s, const char* fmt, ...) {
   char buf[512];
@@ -53,8 +44,11 @@ hylo_status cuda_fail(cudaError_t e, const char* what) {
   return fail(HYLO_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+namespace {
 // Vocabulary columns per fused pair tile.
 constexpr int fused_bn() { return kFusedBN; }
+
+}  // namespace
 
 unsigned long long wait_limit_ns() {
   static const unsigned long long v = [] {
@@ -126,6 +120,7 @@ hylo_status make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, u
   return HYLO_OK;
 }
 
+namespace {
 // A fresh epoch (1..65535) for a paced fused launch: the pacing counters are never cleared,
 // their words carry the epoch of the launch that wrote them.
 unsigned next_epoch(DeviceState* d) {
@@ -134,12 +129,13 @@ unsigned next_epoch(DeviceState* d) {
   return d->pace_epoch;
 }
 
+}  // namespace
 
 // 3-D tensor map [outer2][outer1][inner] (contiguous), zero fill outside; 128-byte swizzle
 // unless `swizzle` says otherwise.
 hylo_status make_map_3d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t inner, uint64_t outer1,
                         uint64_t outer2, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer1,
-                        CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+                        CUtensorMapSwizzle swizzle) {
   cuuint64_t dims[3] = {inner, outer1, outer2};
   cuuint64_t strides[2] = {row_bytes, row_bytes * outer1};
   cuuint32_t box[3] = {box_inner, box_outer1, 1};
@@ -150,10 +146,7 @@ hylo_status make_map_3d(CUtensorMap* m, const void* base, CUtensorMapDataType dt
   return HYLO_OK;
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
+namespace {
 // The backward stages G = dL/dz_s (bf16) in a ring of kGRing blocks of R tokens x bw words:
 // at most kGBlockBytes in all, whatever N, V or token_chunk. R = token_chunk rounded up to a
 // multiple of 256 (at most kMaxBlockTokens, at most N rounded up), so bw is at least

@@ -1,0 +1,156 @@
+// Host side of the C ABI declared in include/hylo_ops.h: argument checks and launches.
+#include <cmath>
+
+#include "hylo_host.h"
+#include "hylo_ops_internal.h"
+
+using namespace hylo;
+
+namespace {
+
+bool dtype_ok(int d) { return d == HYLO_F32 || d == HYLO_BF16 || d == HYLO_F16; }
+uintptr_t dtype_bytes(int d) { return d == HYLO_F32 ? 4 : 2; }
+
+hylo_status check_rows(const void* z, int dtype, int64_t N, int64_t V, int64_t ld, float tau, const int64_t* tokens) {
+  if (!z || !tokens) return fail(HYLO_ERR_NULL, "a required pointer is NULL");
+  if (!dtype_ok(dtype)) return fail(HYLO_ERR_DIM, "unknown dtype %d", dtype);
+  if (N < 1 || V < 1 || N > 0x7fffffffLL || V > 0x7fffffffLL || ld < V || ld > (int64_t(1) << 40))
+    return fail(HYLO_ERR_DIM, "invalid sizes N=%lld V=%lld ld=%lld (need 1 <= N, V < 2^31, ld >= V)",
+                static_cast<long long>(N), static_cast<long long>(V), static_cast<long long>(ld));
+  if (!aligned(z, dtype_bytes(dtype))) return fail(HYLO_ERR_ALIGN, "logits must be element-aligned");
+  if (!aligned(tokens, 8)) return fail(HYLO_ERR_ALIGN, "tokens must be 8-byte aligned");
+  if (!(std::isfinite(tau) && tau > 0.f) || !std::isfinite(1.0f / tau))
+    return fail(HYLO_ERR_TAU, "tau must be finite and > 0, and so must 1 / tau");
+  return HYLO_OK;
+}
+
+TokenRows rows_of(const void* z, int64_t N, int64_t V, int64_t ld, float tau, const int64_t* tokens) {
+  return TokenRows{z, ld, static_cast<int>(N), static_cast<int>(V), 1.0f / tau, 1.4426950408889634f / tau, tokens};
+}
+
+}  // namespace
+
+extern "C" {
+
+hylo_status hylo_token_logprobs(const void* z, int dtype, int64_t N, int64_t V, int64_t ld, float tau,
+                                const int64_t* tokens, int k, float* logp, float* entropy, float* lse, float* stats,
+                                float* top_logp, int64_t* top_ids, cudaStream_t stream) {
+  clear_error();
+  hylo_status st = check_rows(z, dtype, N, V, ld, tau, tokens);
+  if (st != HYLO_OK) return st;
+  if (!logp || (k > 0 && (!top_logp || !top_ids))) return fail(HYLO_ERR_NULL, "an output pointer is NULL");
+  if (k < 0 || k > HYLO_TOP_MAX || k > V)
+    return fail(HYLO_ERR_DIM, "k=%d alternatives (0 <= k <= min(V, %d))", k, HYLO_TOP_MAX);
+  if (!aligned(logp, 4) || !aligned(entropy, 4) || !aligned(lse, 4) || !aligned(stats, 8) || !aligned(top_logp, 4) ||
+      !aligned(top_ids, 8))
+    return fail(HYLO_ERR_ALIGN, "output pointers must be aligned to their elements (stats: 8 bytes)");
+  DeviceState* dev = nullptr;
+  if ((st = current_device(&dev)) != HYLO_OK) return st;
+  const TokenOut out{k, logp, entropy, lse, reinterpret_cast<float2*>(stats), top_logp, top_ids};
+  const cudaError_t e = launch_token_logprobs(rows_of(z, N, V, ld, tau, tokens), out, dtype, dev->sms, stream);
+  return e == cudaSuccess ? HYLO_OK : cuda_fail(e, "launch token log-probabilities");
+}
+
+hylo_status hylo_token_logprobs_backward(const void* z, int dtype, int64_t N, int64_t V, int64_t ld, float tau,
+                                         const int64_t* tokens, const float* stats, const float* entropy,
+                                         const float* g_logp, const float* g_entropy, void* dz, int64_t ldd,
+                                         cudaStream_t stream) {
+  clear_error();
+  hylo_status st = check_rows(z, dtype, N, V, ld, tau, tokens);
+  if (st != HYLO_OK) return st;
+  if (!stats || !dz || (g_entropy && !entropy)) return fail(HYLO_ERR_NULL, "a required pointer is NULL");
+  if (ldd < V || ldd > (int64_t(1) << 40))
+    return fail(HYLO_ERR_DIM, "invalid gradient row stride %lld", static_cast<long long>(ldd));
+  if (!aligned(dz, dtype_bytes(dtype)) || !aligned(stats, 8) || !aligned(entropy, 4) || !aligned(g_logp, 4) ||
+      !aligned(g_entropy, 4))
+    return fail(HYLO_ERR_ALIGN, "pointers must be aligned to their elements (stats: 8 bytes)");
+  DeviceState* dev = nullptr;
+  if ((st = current_device(&dev)) != HYLO_OK) return st;
+  const TokenGrad g{reinterpret_cast<const float2*>(stats), entropy, g_logp, g_entropy, dz, ldd};
+  const cudaError_t e = launch_token_logprobs_bwd(rows_of(z, N, V, ld, tau, tokens), g, dtype, dev->sms, stream);
+  return e == cudaSuccess ? HYLO_OK : cuda_fail(e, "launch token log-probabilities backward");
+}
+
+size_t hylo_grad_norm_workspace_bytes(void) {
+  clear_error();
+  return kNormPartials * sizeof(float);
+}
+
+hylo_status hylo_grad_norm(const void* const* grads, const int64_t* sizes, int count, int dtype, float* norm,
+                           void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  clear_error();
+  if (!norm || !workspace || (count > 0 && (!grads || !sizes))) return fail(HYLO_ERR_NULL, "a required pointer is NULL");
+  if (count < 0) return fail(HYLO_ERR_DIM, "count=%d", count);
+  if (dtype != HYLO_F32 && dtype != HYLO_BF16) return fail(HYLO_ERR_DIM, "gradients are fp32 or bf16 (dtype %d)", dtype);
+  for (int i = 0; i < count; ++i) {
+    if (sizes[i] < 0 || sizes[i] > (int64_t(1) << 40))
+      return fail(HYLO_ERR_DIM, "gradient %d has %lld elements", i, static_cast<long long>(sizes[i]));
+    if (sizes[i] > 0 && !grads[i]) return fail(HYLO_ERR_NULL, "gradient %d is NULL", i);
+    if (!aligned(grads[i], dtype_bytes(dtype))) return fail(HYLO_ERR_ALIGN, "gradient %d is not element-aligned", i);
+  }
+  if (!aligned(norm, 4) || !aligned(workspace, 16)) return fail(HYLO_ERR_ALIGN, "workspace must be 16-byte aligned");
+  if (workspace_bytes < kNormPartials * sizeof(float))
+    return fail(HYLO_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu required", workspace_bytes,
+                kNormPartials * sizeof(float));
+  DeviceState* dev = nullptr;
+  const hylo_status st = current_device(&dev);
+  if (st != HYLO_OK) return st;
+  const cudaError_t e =
+      launch_grad_norm(grads, sizes, count, dtype, norm, static_cast<float*>(workspace), dev->sms, stream);
+  return e == cudaSuccess ? HYLO_OK : cuda_fail(e, "launch gradient norm");
+}
+
+hylo_status hylo_adamw_step(const hylo_adamw_tensor* tensors, int count, int param_dtype, int grad_dtype,
+                            int state_bits, double beta1, double beta2, double eps, int64_t step, float grad_scale,
+                            const float* norm, float max_norm, uint32_t seed, cudaStream_t stream) {
+  clear_error();
+  if (count < 0) return fail(HYLO_ERR_DIM, "count=%d", count);
+  if (count > 0 && !tensors) return fail(HYLO_ERR_NULL, "tensors is NULL");
+  if ((param_dtype != HYLO_F32 && param_dtype != HYLO_BF16) || (grad_dtype != HYLO_F32 && grad_dtype != HYLO_BF16) ||
+      (state_bits != 32 && state_bits != 8))
+    return fail(HYLO_ERR_DIM, "param_dtype=%d grad_dtype=%d state_bits=%d (fp32 or bf16; 32 or 8)", param_dtype,
+                grad_dtype, state_bits);
+  if (!(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1) || !(eps >= 0) || !std::isfinite(eps) || step < 1)
+    return fail(HYLO_ERR_DIM, "beta1=%g beta2=%g eps=%g step=%lld (0 <= beta < 1, eps >= 0, step >= 1)", beta1, beta2,
+                eps, static_cast<long long>(step));
+  if (!std::isfinite(grad_scale) || (norm && !(max_norm > 0)))
+    return fail(HYLO_ERR_TAU, "grad_scale must be finite and max_norm > 0");
+  int some = -1;  // the first tensor that has elements
+  for (int i = 0; i < count; ++i) {
+    const hylo_adamw_tensor& t = tensors[i];
+    if (t.n < 0 || t.n > (int64_t(1) << 40))
+      return fail(HYLO_ERR_DIM, "tensor %d has %lld elements", i, static_cast<long long>(t.n));
+    if (!std::isfinite(t.lr) || !std::isfinite(t.weight_decay))
+      return fail(HYLO_ERR_TAU, "lr and weight_decay of tensor %d must be finite", i);
+    if (t.n == 0) continue;
+    if (some < 0) some = i;
+    if ((t.master != nullptr) != (tensors[some].master != nullptr) || (t.master && param_dtype == HYLO_F32))
+      return fail(HYLO_ERR_DIM, "tensor %d: masters go with bf16 parameters, for all tensors or none", i);
+    if (!t.param || !t.grad || !t.m || !t.v || (state_bits == 8 && (!t.m_exp || !t.v_exp)))
+      return fail(HYLO_ERR_NULL, "a required pointer of tensor %d is NULL", i);
+    const uintptr_t s = state_bits == 8 ? 1 : 4;
+    if (!aligned(t.param, dtype_bytes(param_dtype)) || !aligned(t.grad, dtype_bytes(grad_dtype)) ||
+        !aligned(t.master, 4) || !aligned(t.m, s) || !aligned(t.v, s))
+      return fail(HYLO_ERR_ALIGN, "tensor %d is not element-aligned", i);
+  }
+  DeviceState* dev = nullptr;
+  const hylo_status st = current_device(&dev);
+  if (st != HYLO_OK) return st;
+  if (some < 0) return HYLO_OK;
+  AdamWHyper h;
+  h.beta1 = static_cast<float>(beta1);
+  h.beta2 = static_cast<float>(beta2);
+  h.one_minus_beta1 = static_cast<float>(1.0 - beta1);
+  h.one_minus_beta2 = static_cast<float>(1.0 - beta2);
+  h.eps = static_cast<float>(eps);
+  h.rbc2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(beta2, static_cast<double>(step))));
+  h.grad_scale = grad_scale;
+  h.norm = norm;
+  h.max_norm = max_norm;
+  h.seed = seed;
+  const double bias1 = 1.0 - std::pow(beta1, static_cast<double>(step));
+  const cudaError_t e = launch_adamw(tensors, count, param_dtype, grad_dtype, state_bits, tensors[some].master != nullptr, bias1, h, stream);
+  return e == cudaSuccess ? HYLO_OK : cuda_fail(e, "launch AdamW");
+}
+
+}  // extern "C"

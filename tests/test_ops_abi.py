@@ -1,0 +1,116 @@
+"""Refusals of the operators in include/hylo_ops.h: the C entry points with bad arguments (these calls never
+reach the GPU) and the checks of the Python functions."""
+import ctypes
+import struct
+
+import pytest
+import torch
+
+from hybrid_upcycling_gb300 import _lib, build
+
+FAKE = 0x10000
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return _lib.load()
+
+
+def _fwd(lib, **kw):
+    a = dict(z=FAKE, dt=1, N=4, V=100, ld=100, tau=1.0, tok=FAKE, k=5, logp=FAKE, ent=FAKE, lse=None, stats=FAKE,
+             top=FAKE, ids=FAKE)
+    a.update(kw)
+    return lib.hylo_token_logprobs(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(z=None), -1), (dict(tok=None), -1), (dict(logp=None), -1), (dict(top=None), -1), (dict(ids=None), -1),
+    (dict(dt=3), -2), (dict(dt=-1), -2), (dict(N=0), -2), (dict(V=0), -2), (dict(V=1 << 31, ld=1 << 31), -2),
+    (dict(ld=99), -2), (dict(k=-1), -2), (dict(k=65), -2), (dict(V=4, k=5), -2), (dict(z=FAKE + 1), -3),
+    (dict(dt=0, z=FAKE + 2), -3), (dict(tok=FAKE + 4), -3), (dict(stats=FAKE + 4), -3), (dict(ids=FAKE + 4), -3),
+    (dict(tau=0.0), -4), (dict(tau=-1.0), -4), (dict(tau=float("nan")), -4), (dict(tau=float("inf")), -4),
+    (dict(tau=1e-45), -4),
+])
+def test_token_logprobs_refuses(lib, kw, status):
+    assert _fwd(lib, **kw) == status
+    assert lib.hylo_kl_last_error()
+
+
+def _bwd(lib, **kw):
+    a = dict(z=FAKE, dt=1, N=4, V=100, ld=100, tau=1.0, tok=FAKE, stats=FAKE, ent=FAKE, gl=FAKE, ge=FAKE, dz=FAKE, ldd=100)
+    a.update(kw)
+    return lib.hylo_token_logprobs_backward(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(z=None), -1), (dict(stats=None), -1), (dict(dz=None), -1), (dict(ent=None), -1), (dict(ldd=99), -2),
+    (dict(N=-1), -2), (dict(dz=FAKE + 1), -3), (dict(stats=FAKE + 4), -3), (dict(gl=FAKE + 2), -3), (dict(tau=0.0), -4),
+])
+def test_token_logprobs_backward_refuses(lib, kw, status):
+    assert _bwd(lib, **kw) == status
+    assert lib.hylo_kl_last_error()
+
+
+def _norm(lib, grads=(FAKE,), sizes=(8,), count=None, dt=0, norm=FAKE, ws=FAKE, nbytes=1 << 20):
+    n = len(grads)
+    return lib.hylo_grad_norm((ctypes.c_uint64 * max(n, 1))(*grads), (ctypes.c_int64 * max(n, 1))(*sizes),
+                              n if count is None else count, dt, norm, ws, nbytes, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(norm=None), -1), (dict(ws=None), -1), (dict(grads=(0,)), -1), (dict(count=-1), -2), (dict(sizes=(-1,)), -2),
+    (dict(dt=2), -2), (dict(grads=(FAKE + 2,)), -3), (dict(ws=FAKE + 8), -3), (dict(nbytes=16), -5),
+])
+def test_grad_norm_refuses(lib, kw, status):
+    assert _norm(lib, **kw) == status
+    assert lib.hylo_kl_last_error()
+
+
+def _step(lib, tensors=None, pdt=0, gdt=0, bits=32, b1=0.9, b2=0.999, eps=1e-8, step=1, scale=1.0, norm=None,
+          max_norm=1.0, **kw):
+    t = dict(p=FAKE, g=FAKE, w=0, m=FAKE, v=FAKE, me=FAKE if bits == 8 else 0, ve=FAKE if bits == 8 else 0, n=10,
+             lr=1e-3, wd=0.1)
+    t.update(kw)
+    rows = [t] if tensors is None else [{**t, **x} for x in tensors]
+    table = b"".join(struct.pack("=" + _lib.ADAMW_TENSOR, *r.values()) for r in rows)
+    return lib.hylo_adamw_step(table, len(rows), pdt, gdt, bits, b1, b2, eps, step, scale, norm, max_norm, 0, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(p=0), -1), (dict(g=0), -1), (dict(m=0), -1), (dict(v=0), -1), (dict(bits=8, me=0), -1),
+    (dict(bits=8, ve=0), -1), (dict(pdt=2), -2), (dict(gdt=2), -2), (dict(bits=16), -2), (dict(n=-1), -2),
+    (dict(b1=1.0), -2), (dict(b2=-0.1), -2), (dict(eps=-1.0), -2), (dict(step=0), -2), (dict(w=FAKE), -2),
+    (dict(pdt=1, tensors=[dict(w=FAKE), dict(w=0)]), -2), (dict(b1=float("nan")), -2),
+    (dict(p=FAKE + 2), -3), (dict(m=FAKE + 1), -3), (dict(lr=float("inf")), -4), (dict(wd=float("nan")), -4),
+    (dict(scale=float("inf")), -4), (dict(norm=FAKE, max_norm=0.0), -4),
+])
+def test_adamw_refuses(lib, kw, status):
+    assert _step(lib, **kw) == status
+    assert lib.hylo_kl_last_error()
+
+
+def test_table_layout_is_the_headers():
+    assert struct.calcsize("=" + _lib.ADAMW_TENSOR) == 80
+
+
+def test_python_checks():
+    from hybrid_upcycling_gb300 import AdamW, State8, adamw_step, grad_norm, token_logprobs
+    z, t = torch.zeros(3, 10), torch.zeros(3, dtype=torch.int64)
+    for bad in (lambda: token_logprobs(z, t),                       # not on a GPU
+                lambda: token_logprobs(z.double(), t),
+                lambda: token_logprobs(z, t[:2]),
+                lambda: token_logprobs(z, t.int()),
+                lambda: token_logprobs(z, t, top_k=11),
+                lambda: token_logprobs(z[:, :0], t),
+                lambda: grad_norm([]),
+                lambda: grad_norm([z]),
+                lambda: adamw_step([z], [z], [z], [z], step=1, lr=1e-3),
+                lambda: adamw_step([z], [z], [z], [], step=1, lr=1e-3),
+                lambda: AdamW([z], state_bits=4),
+                lambda: AdamW([]),
+                lambda: AdamW([z, z.bfloat16()])):
+        with pytest.raises(ValueError):
+            bad()
+    s = State8.zeros_like(torch.zeros(257))
+    assert s.codes.numel() == 257 and s.exponents.numel() == 2 and torch.all(s.values() == 0)
