@@ -8,10 +8,10 @@ AdamW step that applies the gradients; ``synthetic`` draws the seeded benchmark 
 from . import synthetic  # noqa: F401
 
 __all__ = ["synthetic", "fused_hidden_state_kl", "fused_logits_kl", "ild_loss", "token_logprobs", "TokenLogprobs",
-           "grad_norm", "adamw_step", "AdamW", "State8"]
+           "head_logprobs", "grad_norm", "adamw_step", "AdamW", "State8"]
 
-_LAZY = {"token_logprobs": "logprobs", "TokenLogprobs": "logprobs", "grad_norm": "optim", "adamw_step": "optim",
-         "AdamW": "optim", "State8": "optim"}
+_LAZY = {"token_logprobs": "logprobs", "TokenLogprobs": "logprobs", "head_logprobs": "logprobs", "grad_norm": "optim",
+         "adamw_step": "optim", "AdamW": "optim", "State8": "optim"}
 
 
 def __getattr__(name):

@@ -32,6 +32,7 @@ EXPORTS = ("hylo_kl_workspace_bytes", "hylo_kl_forward", "hylo_kl_backward", "hy
            "hylo_kl_workspace_bytes_split", "hylo_kl_backward_split",
            "hylo_kl_last_error", "hylo_kl_forward_noalloc", "hylo_kl_selftest_wait_timeout",
            "hylo_fused_kl_logits", "hylo_ild_loss", "hylo_token_logprobs", "hylo_token_logprobs_backward",
+           "hylo_head_logprobs_workspace_bytes", "hylo_head_logprobs", "hylo_head_logprobs_backward",
            "hylo_grad_norm_workspace_bytes", "hylo_grad_norm", "hylo_adamw_step")
 
 DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}  # hylo_dtype
@@ -77,6 +78,12 @@ def load() -> ctypes.CDLL:
     L.hylo_token_logprobs.restype = ctypes.c_int
     L.hylo_token_logprobs_backward.argtypes = [vp, i32, i64, i64, i64, f32, vp, vp, vp, vp, vp, vp, i64, vp]
     L.hylo_token_logprobs_backward.restype = ctypes.c_int
+    L.hylo_head_logprobs_workspace_bytes.argtypes = [i64, i64, i64, i64, i32]
+    L.hylo_head_logprobs_workspace_bytes.restype = sz
+    L.hylo_head_logprobs.argtypes = [vp, vp, i64, i64, i64, f32, vp, vp, vp, vp, vp, sz, vp]
+    L.hylo_head_logprobs.restype = ctypes.c_int
+    L.hylo_head_logprobs_backward.argtypes = [vp, vp, i64, i64, i64, f32, i64, vp, vp, vp, vp, vp, i32, vp, vp, vp, sz, vp]
+    L.hylo_head_logprobs_backward.restype = ctypes.c_int
     L.hylo_grad_norm_workspace_bytes.argtypes = []
     L.hylo_grad_norm_workspace_bytes.restype = sz
     L.hylo_grad_norm.argtypes = [vp, vp, i32, i32, vp, vp, sz, vp]
@@ -259,6 +266,48 @@ def hylo_token_logprobs_backward(z, tokens, tau: float, stats, entropy, g_logp, 
     _check(load().hylo_token_logprobs_backward(z.data_ptr(), DTYPES[z.dtype], N, V, ld, float(tau), tokens.data_ptr(),
                                                _ptr(stats), _ptr(entropy), _ptr(g_logp), _ptr(g_entropy), dz.data_ptr(),
                                                ldd, _stream(stream)))
+
+
+def _head_dims(h, W):
+    for name, t in (("h", h), ("W", W)):
+        if t.dtype != torch.bfloat16 or t.dim() != 2 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous 2-D bfloat16 tensor")
+    if h.shape[1] != W.shape[1]:
+        raise ValueError("h and W must have the same hidden size")
+    return h.shape[0], h.shape[1], W.shape[0]
+
+
+def hylo_head_logprobs_workspace_bytes(N: int, d: int, V: int, token_chunk: int = 4096, split_g: bool = False) -> int:
+    return int(load().hylo_head_logprobs_workspace_bytes(N, d, V, token_chunk, int(split_g)))
+
+
+def hylo_head_logprobs(h, W, tokens, tau: float, logp, entropy, lse, workspace, stream=None) -> None:
+    """Log-probabilities of `tokens` (int64 [N]) under softmax(h W^T / tau); entropy and lse [N] may be None."""
+    N, d, V = _head_dims(h, W)
+    _need_cuda(h=h, W=W, tokens=tokens, logp=logp, entropy=entropy, lse=lse, workspace=workspace)
+    _need("tokens", tokens, torch.int64, (N,))
+    for name, t in (("logp", logp), ("entropy", entropy), ("lse", lse)):
+        _need(name, t, torch.float32, (N,))
+    _check(load().hylo_head_logprobs(h.data_ptr(), W.data_ptr(), N, d, V, float(tau), tokens.data_ptr(), _ptr(logp),
+                                     _ptr(entropy), _ptr(lse), workspace.data_ptr(),
+                                     workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def hylo_head_logprobs_backward(h, W, tokens, tau: float, token_chunk: int, lse, entropy, g_logp, g_entropy, dh, dW,
+                                workspace, split_g: bool = False, stream=None) -> None:
+    """fp32 gradients dh [N, d], dW [V, d] (overwritten) for the upstream g_logp, g_entropy [N] (either None)."""
+    N, d, V = _head_dims(h, W)
+    _need_cuda(h=h, W=W, tokens=tokens, lse=lse, entropy=entropy, g_logp=g_logp, g_entropy=g_entropy, dh=dh, dW=dW,
+               workspace=workspace)
+    _need("tokens", tokens, torch.int64, (N,))
+    for name, t in (("lse", lse), ("entropy", entropy), ("g_logp", g_logp), ("g_entropy", g_entropy)):
+        _need(name, t, torch.float32, (N,))
+    _need("dh", dh, torch.float32, (N, d))
+    _need("dW", dW, torch.float32, (V, d))
+    _check(load().hylo_head_logprobs_backward(h.data_ptr(), W.data_ptr(), N, d, V, float(tau), int(token_chunk),
+                                              tokens.data_ptr(), _ptr(lse), _ptr(entropy), _ptr(g_logp),
+                                              _ptr(g_entropy), int(split_g), _ptr(dh), _ptr(dW), workspace.data_ptr(),
+                                              workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def hylo_grad_norm_workspace_bytes() -> int:

@@ -16,6 +16,7 @@ struct DeviceState {
   int fused_clusters = 0;  // 2-CTA clusters of the fused kernels resident at once
   int logits_clusters = 0; // clusters of the logits kernel resident at once
   int pipe_clusters = 0;   // 2-CTA clusters of the pipelined backward resident at once
+  int head_clusters = 0;   // 2-CTA clusters of the head log-probability kernel resident at once
   unsigned pace_epoch = 0;  // epoch of the last paced fused launch on this device
   int* status = nullptr;
   std::string why;
@@ -41,5 +42,17 @@ hylo_status make_map_3d(CUtensorMap* m, const void* base, CUtensorMapDataType dt
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+inline size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+// Vocabulary segments per 256-token tile (at most `most`) for `workers` persistent clusters.
+int choose_segments(int64_t token_tiles, int64_t vtiles, int workers, int most);
+
+// Bytes of the pipelined backward's G ring for one bf16 term; its counters follow the ring(s).
+size_t bwd_bytes(int64_t N, int64_t V, int64_t token_chunk);
+constexpr size_t kPipeCtrlBytes = 256;
+hylo_status pipe_setup(const uint16_t* h, const uint16_t* W, int64_t N, int64_t d, int64_t V, float tau,
+                       int64_t token_chunk, float* dh, float* dW, void* workspace, size_t g_total, bool split,
+                       DeviceState** dev, CUtensorMap* maps, BwdPipeParams* p, int* clusters);
 
 }  // namespace hylo

@@ -12,6 +12,7 @@
 #include <cudaTypedefs.h>
 
 #include "hylo_host.h"
+#include "hylo_ops_internal.h"
 
 namespace hylo {
 
@@ -86,9 +87,10 @@ hylo_status current_device(DeviceState** out) {
       d.status = static_cast<int*>(p);
       if ((e = fused_prepare(fused_bn(), &d.fused_clusters)) != cudaSuccess ||
           (e = bwd_pipe_prepare(&d.pipe_clusters)) != cudaSuccess ||
-          (e = kl_logits_prepare(&d.logits_clusters)) != cudaSuccess)
+          (e = kl_logits_prepare(&d.logits_clusters)) != cudaSuccess ||
+          (e = head_prepare(&d.head_clusters)) != cudaSuccess)
         return cuda_fail(e, "kernel set-up");
-      if (d.pipe_clusters < 1 || d.fused_clusters < 1 || d.logits_clusters < 1)
+      if (d.pipe_clusters < 1 || d.fused_clusters < 1 || d.logits_clusters < 1 || d.head_clusters < 1)
         return fail(HYLO_ERR_CUDA, "no thread-block cluster of the kernels fits on the device");
       if (!g_encode) {
         cudaDriverEntryPointQueryResult q;
@@ -106,6 +108,19 @@ hylo_status current_device(DeviceState** out) {
   return HYLO_OK;
 }
 
+namespace {
+// Encodes a tensor map. A thread whose first CUDA call this is (an autograd worker) has no
+// context yet, which the driver call needs and does not create: the runtime then makes one current.
+template <typename Encode>
+CUresult encode_map(Encode&& encode) {
+  CUresult r = encode();
+  int dev = -1;
+  if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess)
+    r = encode();
+  return r;
+}
+}  // namespace
+
 // 2-D tensor map, 128-byte swizzle, zero fill outside the tensor.
 hylo_status make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t inner, uint64_t outer,
                      uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer) {
@@ -113,9 +128,10 @@ hylo_status make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, u
   cuuint64_t strides[1] = {row_bytes};
   cuuint32_t box[2] = {box_inner, box_outer};
   cuuint32_t es[2] = {1, 1};
-  CUresult r = g_encode(m, dt, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = encode_map([&] {
+    return g_encode(m, dt, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  });
   if (r != CUDA_SUCCESS) return fail(HYLO_ERR_CUDA, "cuTensorMapEncodeTiled failed with CUresult %d", static_cast<int>(r));
   return HYLO_OK;
 }
@@ -140,13 +156,14 @@ hylo_status make_map_3d(CUtensorMap* m, const void* base, CUtensorMapDataType dt
   cuuint64_t strides[2] = {row_bytes, row_bytes * outer1};
   cuuint32_t box[3] = {box_inner, box_outer1, 1};
   cuuint32_t es[3] = {1, 1, 1};
-  CUresult r = g_encode(m, dt, 3, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = encode_map([&] {
+    return g_encode(m, dt, 3, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  });
   if (r != CUDA_SUCCESS) return fail(HYLO_ERR_CUDA, "cuTensorMapEncodeTiled (3-D) failed with CUresult %d", static_cast<int>(r));
   return HYLO_OK;
 }
 
-namespace {
 // The backward stages G = dL/dz_s (bf16) in a ring of kGRing blocks of R tokens x bw words:
 // at most kGBlockBytes in all, whatever N, V or token_chunk. R = token_chunk rounded up to a
 // multiple of 256 (at most kMaxBlockTokens, at most N rounded up), so bw is at least
@@ -167,6 +184,7 @@ int64_t pipe_width(int64_t R, int64_t V) {
   return w < vmax ? w : vmax;
 }
 
+namespace {
 bool sizes_ok(int64_t N, int64_t d_s, int64_t d_t, int64_t V) {
   return N >= 1 && V >= 1 && N <= 0x7fffffffLL && V <= 0x7fffffffLL && d_s >= 8 && d_t >= 8 && d_s <= 65536 &&
          d_t <= 65536 && d_s % 8 == 0 && d_t % 8 == 0;
@@ -174,14 +192,15 @@ bool sizes_ok(int64_t N, int64_t d_s, int64_t d_t, int64_t V) {
 
 size_t fwd_bytes(int64_t N) { return static_cast<size_t>(kStatFields) * kMaxSegments * N * sizeof(float); }
 
+}  // namespace
+
 // Bytes of the backward's G ring (one bf16 term): at most kGBlockBytes.
 size_t bwd_bytes(int64_t N, int64_t V, int64_t token_chunk) {
   const int64_t R = pipe_rows(N, token_chunk);
   return static_cast<size_t>(kGRing) * R * pipe_width(R, V) * 2;
 }
 
-size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-
+namespace {
 // The fused kernels' pacing counters (one per cluster, then the switch that turns pacing off)
 // follow the statistics or G region.
 constexpr size_t kProgressBytes = ((kMaxClusters + 1) * sizeof(unsigned long long) + 255) & ~size_t(255);
@@ -219,10 +238,12 @@ double segment_cost(int64_t token_tiles, int64_t vtiles, int workers, int s) {
   return static_cast<double>(waves * per) * (1.0 + 0.002 * s);
 }
 
-int choose_segments(int64_t token_tiles, int64_t vtiles, int workers) {
+}  // namespace
+
+int choose_segments(int64_t token_tiles, int64_t vtiles, int workers, int most) {
   int best = 1;
   double best_cost = 1e300;
-  for (int s = 1; s <= kMaxSegments && s <= vtiles; ++s) {
+  for (int s = 1; s <= most && s <= vtiles; ++s) {
     const double cost = segment_cost(token_tiles, vtiles, workers, s);
     if (cost < best_cost) {
       best_cost = cost;
@@ -232,6 +253,7 @@ int choose_segments(int64_t token_tiles, int64_t vtiles, int workers) {
   return best;
 }
 
+namespace {
 hylo_status check_common(const void* h_s, const void* W_s, const void* h_t, const void* W_t, int64_t N, int64_t d_s,
                          int64_t d_t, int64_t V, float tau, void* workspace, size_t workspace_bytes,
                          size_t need) {
@@ -250,6 +272,57 @@ hylo_status check_common(const void* h_s, const void* W_s, const void* h_t, cons
 }
 
 }  // namespace
+
+// Everything of a pipelined backward that does not depend on what G is: the tensor maps of the student side, of
+// the gradients and of the G ring (maps 1 and 3, the teacher's, are the caller's), the block
+// geometry, and how many clusters to launch. The counters at p->ctrl are the caller's to clear.
+hylo_status pipe_setup(const uint16_t* h, const uint16_t* W, int64_t N, int64_t d, int64_t V, float tau,
+                       int64_t token_chunk, float* dh, float* dW, void* workspace, size_t g_total, bool split,
+                       DeviceState** dev, CUtensorMap* maps, BwdPipeParams* p, int* clusters) {
+  hylo_status st;
+  const int64_t R = pipe_rows(N, token_chunk), bw = pipe_width(R, V);
+  const int64_t TB = cdiv(N, R), VB = cdiv(V, bw), ntd = cdiv(d, kGemmBN);
+  // work items: per block, its 256 x 256 G tiles and its dW_s and dh_s tiles (< 2^30 so that
+  // the queue index and the completion counts fit their 32-bit counters)
+  const int64_t items = cdiv(N, 256) * cdiv(V, 256) + (TB * cdiv(V, 256) + VB * cdiv(N, 256)) * ntd;
+  if (items >= (int64_t(1) << 30))
+    return fail(HYLO_ERR_DIM, "N=%lld x V=%lld needs %lld backward work items, more than 2^30",
+                static_cast<long long>(N), static_cast<long long>(V), static_cast<long long>(items));
+  if ((st = current_device(dev)) != HYLO_OK) return st;
+
+  const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUtensorMapDataType f32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+  uint16_t* G = static_cast<uint16_t*>(workspace);
+  const uint64_t slots = static_cast<uint64_t>(split ? 2 * kGRing : kGRing);
+  if ((st = make_map(&maps[0], h, bf, d, N, d * 2, kBK, kBM)) != HYLO_OK) return st;
+  if ((st = make_map(&maps[2], W, bf, d, V, d * 2, kBK, kFusedBN / 2)) != HYLO_OK) return st;
+  if ((st = make_map(&maps[4], W, bf, d, V, d * 2, 64, kBK)) != HYLO_OK) return st;  // MN-major B of dh
+  if ((st = make_map(&maps[5], h, bf, d, N, d * 2, 64, kBK)) != HYLO_OK) return st;  // MN-major B of dW
+  if ((st = make_map(&maps[6], dh, f32, d, N, d * 4, 32, 32)) != HYLO_OK) return st;
+  if ((st = make_map(&maps[7], dW, f32, d, V, d * 4, 32, 32)) != HYLO_OK) return st;
+  if ((st = make_map_3d(&maps[8], G, bf, bw, R, slots, bw * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) != HYLO_OK)
+    return st;  // G tile stores (32 x 32)
+  if ((st = make_map_3d(&maps[9], G, bf, bw, R, slots, bw * 2, kBK, kBM)) != HYLO_OK) return st;  // K-major A of dh
+  if ((st = make_map_3d(&maps[10], G, bf, bw, R, slots, bw * 2, 64, kBK)) != HYLO_OK) return st;  // MN-major A of dW
+
+  p->N = static_cast<int>(N);
+  p->V = static_cast<int>(V);
+  p->d_s = static_cast<int>(d);
+  p->kb_s = static_cast<int>(cdiv(d, kBK));
+  p->ntd = static_cast<int>(ntd);
+  p->R = static_cast<int>(R);
+  p->bw = static_cast<int>(bw);
+  p->TB = static_cast<int>(TB);
+  p->VB = static_cast<int>(VB);
+  p->B = static_cast<int>(TB * VB);
+  p->c = 1.4426950408889634f / tau;
+  p->split = split ? 1 : 0;
+  p->ctrl = reinterpret_cast<unsigned*>(static_cast<char*>(workspace) + g_total);
+  p->ctl = WaitCtl{(*dev)->status, wait_limit_ns()};
+  *clusters = static_cast<int>(items < (*dev)->pipe_clusters ? items : (*dev)->pipe_clusters);
+  return HYLO_OK;
+}
+
 }  // namespace hylo
 
 using namespace hylo;
@@ -298,7 +371,7 @@ hylo_status hylo_kl_forward(const uint16_t* h_s, const uint16_t* W_s, const uint
   p.kb_t = static_cast<int>(cdiv(d_t, kBK));
   p.token_tiles = static_cast<int>(cdiv(N, 2 * kBM));
   p.vtiles = static_cast<int>(cdiv(V, fused_bn()));
-  p.nseg = choose_segments(p.token_tiles, p.vtiles, dev->fused_clusters);
+  p.nseg = choose_segments(p.token_tiles, p.vtiles, dev->fused_clusters, kMaxSegments);
   p.units = p.token_tiles * p.nseg;
   p.group = 1;  // tile-major: least DRAM traffic (measured at 64K: 229 GB per launch against 291-417 GB
                 // for raster groups of 4-32 pair tiles, 58.7 against up to 66.7 ms)
@@ -345,58 +418,23 @@ hylo_status backward_impl(const uint16_t* h_s, const uint16_t* W_s, const uint16
   if (st != HYLO_OK) return st;
   if (!std::isfinite(grad_scale)) return fail(HYLO_ERR_TAU, "grad_scale must be finite");
   if (!aligned(dh_s, 16) || !aligned(dW_s, 16)) return fail(HYLO_ERR_ALIGN, "gradient pointers must be 16-byte aligned");
-  const int64_t R = pipe_rows(N, token_chunk), bw = pipe_width(R, V);
-  const int64_t TB = cdiv(N, R), VB = cdiv(V, bw), ntd = cdiv(d_s, kGemmBN);
-  // work items: per block, its 256 x 256 G tiles and its dW_s and dh_s tiles (< 2^30 so that
-  // the queue index and the completion counts fit their 32-bit counters)
-  const int64_t items = cdiv(N, 256) * cdiv(V, 256) + (TB * cdiv(V, 256) + VB * cdiv(N, 256)) * ntd;
-  if (items >= (int64_t(1) << 30))
-    return fail(HYLO_ERR_DIM, "N=%lld x V=%lld needs %lld backward work items, more than 2^30",
-                static_cast<long long>(N), static_cast<long long>(V), static_cast<long long>(items));
   DeviceState* dev = nullptr;
-  if ((st = current_device(&dev)) != HYLO_OK) return st;
-
-  const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const CUtensorMapDataType f32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
   CUtensorMap maps[kPipeMaps];
-  uint16_t* G = static_cast<uint16_t*>(workspace);
-  const uint64_t slots = static_cast<uint64_t>(split ? 2 * kGRing : kGRing);
-  if ((st = make_map(&maps[0], h_s, bf, d_s, N, d_s * 2, kBK, kBM)) != HYLO_OK) return st;
-  if ((st = make_map(&maps[1], h_t, bf, d_t, N, d_t * 2, kBK, kBM)) != HYLO_OK) return st;
-  if ((st = make_map(&maps[2], W_s, bf, d_s, V, d_s * 2, kBK, fused_bn() / 2)) != HYLO_OK) return st;
-  if ((st = make_map(&maps[3], W_t, bf, d_t, V, d_t * 2, kBK, fused_bn() / 2)) != HYLO_OK) return st;
-  if ((st = make_map(&maps[4], W_s, bf, d_s, V, d_s * 2, 64, kBK)) != HYLO_OK) return st;  // MN-major B of dh
-  if ((st = make_map(&maps[5], h_s, bf, d_s, N, d_s * 2, 64, kBK)) != HYLO_OK) return st;  // MN-major B of dW
-  if ((st = make_map(&maps[6], dh_s, f32, d_s, N, d_s * 4, 32, 32)) != HYLO_OK) return st;
-  if ((st = make_map(&maps[7], dW_s, f32, d_s, V, d_s * 4, 32, 32)) != HYLO_OK) return st;
-  if ((st = make_map_3d(&maps[8], G, bf, bw, R, slots, bw * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) != HYLO_OK)
-    return st;  // G tile stores (32 x 32)
-  if ((st = make_map_3d(&maps[9], G, bf, bw, R, slots, bw * 2, kBK, kBM)) != HYLO_OK) return st;  // K-major A of dh
-  if ((st = make_map_3d(&maps[10], G, bf, bw, R, slots, bw * 2, 64, kBK)) != HYLO_OK) return st;  // MN-major A of dW
-
   BwdPipeParams p{};
-  p.N = static_cast<int>(N);
-  p.V = static_cast<int>(V);
-  p.d_s = static_cast<int>(d_s);
-  p.kb_s = static_cast<int>(cdiv(d_s, kBK));
+  int clusters = 0;
+  if ((st = pipe_setup(h_s, W_s, N, d_s, V, tau, token_chunk, dh_s, dW_s, workspace, g_total, split, &dev, maps,
+                       &p, &clusters)) != HYLO_OK)
+    return st;
+  const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  if ((st = make_map(&maps[1], h_t, bf, d_t, N, d_t * 2, kBK, kBM)) != HYLO_OK) return st;
+  if ((st = make_map(&maps[3], W_t, bf, d_t, V, d_t * 2, kBK, fused_bn() / 2)) != HYLO_OK) return st;
   p.kb_t = static_cast<int>(cdiv(d_t, kBK));
-  p.ntd = static_cast<int>(ntd);
-  p.R = static_cast<int>(R);
-  p.bw = static_cast<int>(bw);
-  p.TB = static_cast<int>(TB);
-  p.VB = static_cast<int>(VB);
-  p.B = static_cast<int>(TB * VB);
-  p.c = 1.4426950408889634f / tau;
   p.gscale = static_cast<float>(static_cast<double>(grad_scale) / (static_cast<double>(tau) * N));
   p.lse_s = lse_s;
   p.lse_t = lse_t;
   p.lse_gap = lse_gap;
-  p.split = split ? 1 : 0;
-  p.ctrl = reinterpret_cast<unsigned*>(static_cast<char*>(workspace) + g_total);
-  p.ctl = WaitCtl{dev->status, wait_limit_ns()};
   cudaError_t e = cudaMemsetAsync(p.ctrl, 0, kPipeCtrlWords * sizeof(unsigned), stream);
   if (e != cudaSuccess) return cuda_fail(e, "clear the backward's work counters");
-  const int clusters = static_cast<int>(items < dev->pipe_clusters ? items : dev->pipe_clusters);
   e = launch_bwd_pipe(maps, p, clusters, stream);
   if (e != cudaSuccess) return cuda_fail(e, "launch pipelined backward");
   return HYLO_OK;
@@ -606,7 +644,7 @@ extern "C" hylo_status hylo_kl_forward_noalloc(const uint16_t* h_s, const uint16
   p.vtiles = static_cast<int>(cdiv(V, fused_bn()));
   // as many vocabulary segments as the heuristic wants, but no more than the scratch holds
   const int64_t fit = static_cast<int64_t>(kNoAllocStatFloats) / (static_cast<int64_t>(kStatFields) * N);
-  const int want = choose_segments(p.token_tiles, p.vtiles, dev->fused_clusters);
+  const int want = choose_segments(p.token_tiles, p.vtiles, dev->fused_clusters, kMaxSegments);
   p.nseg = static_cast<int>(want < fit ? want : fit);
   p.units = p.token_tiles * p.nseg;
   p.group = 1;  // tile-major, as in hylo_kl_forward

@@ -28,6 +28,38 @@ TokenRows rows_of(const void* z, int64_t N, int64_t V, int64_t ld, float tau, co
   return TokenRows{z, ld, static_cast<int>(N), static_cast<int>(V), 1.0f / tau, 1.4426950408889634f / tau, tokens};
 }
 
+bool head_sizes_ok(int64_t N, int64_t d, int64_t V) {
+  return N >= 1 && V >= 1 && N <= 0x7fffffffLL && V <= 0x7fffffffLL && d >= 8 && d <= 65536 && d % 8 == 0;
+}
+
+// The forward's vocabulary segments per 256-token tile at most: enough for every cluster of a large device
+// to have a unit when there are few tiles.
+int head_segments(int64_t N) {
+  const int64_t s = cdiv(kMaxClusters, cdiv(N, 2 * kBM));
+  return s > kMaxSegments ? static_cast<int>(s) : kMaxSegments;
+}
+
+// The tokens' logits, then two partial sums per token and segment.
+size_t head_fwd_bytes(int64_t N) {
+  return round256(N * sizeof(float)) + static_cast<size_t>(N) * 2 * head_segments(N) * sizeof(float4);
+}
+
+hylo_status check_head(const uint16_t* h, const uint16_t* W, int64_t N, int64_t d, int64_t V, float tau,
+                       const int64_t* tokens, void* workspace, size_t workspace_bytes, size_t need) {
+  if (!h || !W || !tokens || !workspace) return fail(HYLO_ERR_NULL, "a required pointer is NULL");
+  if (!head_sizes_ok(N, d, V))
+    return fail(HYLO_ERR_DIM, "invalid sizes N=%lld d=%lld V=%lld (d must be a multiple of 8, 8..65536)",
+                static_cast<long long>(N), static_cast<long long>(d), static_cast<long long>(V));
+  if (!aligned(h, 16) || !aligned(W, 16)) return fail(HYLO_ERR_ALIGN, "h and W must be 16-byte aligned");
+  if (!aligned(tokens, 8)) return fail(HYLO_ERR_ALIGN, "tokens must be 8-byte aligned");
+  if (!aligned(workspace, 256)) return fail(HYLO_ERR_ALIGN, "workspace must be 256-byte aligned");
+  if (!(std::isfinite(tau) && tau > 0.f) || !std::isfinite(1.0f / tau))
+    return fail(HYLO_ERR_TAU, "tau must be finite and > 0, and so must 1 / tau");
+  if (workspace_bytes < need)
+    return fail(HYLO_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu required", workspace_bytes, need);
+  return HYLO_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -69,6 +101,78 @@ hylo_status hylo_token_logprobs_backward(const void* z, int dtype, int64_t N, in
   const TokenGrad g{reinterpret_cast<const float2*>(stats), entropy, g_logp, g_entropy, dz, ldd};
   const cudaError_t e = launch_token_logprobs_bwd(rows_of(z, N, V, ld, tau, tokens), g, dtype, dev->sms, stream);
   return e == cudaSuccess ? HYLO_OK : cuda_fail(e, "launch token log-probabilities backward");
+}
+
+size_t hylo_head_logprobs_workspace_bytes(int64_t N, int64_t d, int64_t V, int64_t token_chunk, int split_g) {
+  clear_error();
+  if (!head_sizes_ok(N, d, V)) return 0;
+  const size_t f = head_fwd_bytes(N), b = round256(bwd_bytes(N, V, token_chunk)) * (split_g ? 2 : 1) + kPipeCtrlBytes;
+  return f > b ? f : b;
+}
+
+hylo_status hylo_head_logprobs(const uint16_t* h, const uint16_t* W, int64_t N, int64_t d, int64_t V, float tau,
+                               const int64_t* tokens, float* logp, float* entropy, float* lse, void* workspace,
+                               size_t workspace_bytes, cudaStream_t stream) {
+  clear_error();
+  if (!logp) return fail(HYLO_ERR_NULL, "logp is NULL");
+  if (!aligned(logp, 4) || !aligned(entropy, 4) || !aligned(lse, 4))
+    return fail(HYLO_ERR_ALIGN, "output pointers must be 4-byte aligned");
+  hylo_status st = check_head(h, W, N, d, V, tau, tokens, workspace, workspace_bytes,
+                              head_sizes_ok(N, d, V) ? head_fwd_bytes(N) : 0);
+  if (st != HYLO_OK) return st;
+  DeviceState* dev = nullptr;
+  if ((st = current_device(&dev)) != HYLO_OK) return st;
+  CUtensorMap m_h, m_W;
+  const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  if ((st = make_map(&m_h, h, bf, d, N, d * 2, kBK, kBM)) != HYLO_OK) return st;
+  if ((st = make_map(&m_W, W, bf, d, V, d * 2, kBK, kFusedBN / 2)) != HYLO_OK) return st;
+  HeadParams p{};
+  p.N = static_cast<int>(N);
+  p.V = static_cast<int>(V);
+  p.kb = static_cast<int>(cdiv(d, kBK));
+  p.token_tiles = static_cast<int>(cdiv(N, 2 * kBM));
+  p.vtiles = static_cast<int>(cdiv(V, kFusedBN));
+  p.nseg = choose_segments(p.token_tiles, p.vtiles, dev->head_clusters, head_segments(N));
+  p.units = p.token_tiles * p.nseg;
+  p.c = 1.4426950408889634f / tau;
+  p.inv_tau = 1.0f / tau;
+  p.tokens = tokens;
+  p.z_token = static_cast<float*>(workspace);
+  p.part = reinterpret_cast<float4*>(static_cast<char*>(workspace) + round256(N * sizeof(float)));
+  p.ctl = WaitCtl{dev->status, wait_limit_ns()};
+  const int clusters = p.units < dev->head_clusters ? p.units : dev->head_clusters;
+  const cudaError_t e = launch_head_logprobs(m_h, m_W, p, logp, entropy, lse, clusters, stream);
+  return e == cudaSuccess ? HYLO_OK : cuda_fail(e, "launch head log-probabilities");
+}
+
+hylo_status hylo_head_logprobs_backward(const uint16_t* h, const uint16_t* W, int64_t N, int64_t d, int64_t V,
+                                        float tau, int64_t token_chunk, const int64_t* tokens, const float* lse,
+                                        const float* entropy, const float* g_logp, const float* g_entropy, int split_g,
+                                        float* dh, float* dW, void* workspace, size_t workspace_bytes,
+                                        cudaStream_t stream) {
+  clear_error();
+  if (!lse || !dh || !dW || (g_entropy && !entropy)) return fail(HYLO_ERR_NULL, "a required pointer is NULL");
+  const bool split = split_g != 0;
+  const size_t g_total = head_sizes_ok(N, d, V) ? round256(bwd_bytes(N, V, token_chunk)) * (split ? 2 : 1) : 0;
+  hylo_status st = check_head(h, W, N, d, V, tau, tokens, workspace, workspace_bytes, g_total + kPipeCtrlBytes);
+  if (st != HYLO_OK) return st;
+  if (!aligned(dh, 16) || !aligned(dW, 16)) return fail(HYLO_ERR_ALIGN, "gradient pointers must be 16-byte aligned");
+  if (!aligned(lse, 4) || !aligned(entropy, 4) || !aligned(g_logp, 4) || !aligned(g_entropy, 4))
+    return fail(HYLO_ERR_ALIGN, "per-token pointers must be 4-byte aligned");
+  DeviceState* dev = nullptr;
+  CUtensorMap maps[kPipeMaps];
+  BwdPipeParams p{};
+  int clusters = 0;
+  if ((st = pipe_setup(h, W, N, d, V, tau, token_chunk, dh, dW, workspace, g_total, split, &dev, maps, &p,
+                       &clusters)) != HYLO_OK)
+    return st;
+  maps[1] = maps[0];  // no teacher: never loaded from
+  maps[3] = maps[2];
+  cudaError_t e = cudaMemsetAsync(p.ctrl, 0, kPipeCtrlWords * sizeof(unsigned), stream);
+  if (e != cudaSuccess) return cuda_fail(e, "clear the backward's work counters");
+  const HeadGrad g{tokens, lse, entropy, g_logp, g_entropy, 1.0f / tau};
+  e = launch_bwd_pipe_head(maps, p, g, clusters, stream);
+  return e == cudaSuccess ? HYLO_OK : cuda_fail(e, "launch head log-probabilities backward");
 }
 
 size_t hylo_grad_norm_workspace_bytes(void) {

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/hylo_ops.h"
+#include "hylo_internal.h"
 
 namespace hylo {
 
@@ -38,6 +39,39 @@ struct TokenGrad {
 
 cudaError_t launch_token_logprobs(const TokenRows& in, const TokenOut& out, int dtype, int sms, cudaStream_t stream);
 cudaError_t launch_token_logprobs_bwd(const TokenRows& in, const TokenGrad& g, int dtype, int sms, cudaStream_t stream);
+
+// Forward of the log-probabilities from hidden states (head_logprobs.cu).
+struct HeadParams {
+  int N, V;
+  int kb;           // 64-wide k-blocks of d
+  int token_tiles;  // ceil(N / 256)
+  int vtiles;       // ceil(V / 256)
+  int nseg;         // vocabulary segments per token tile
+  int units;        // token_tiles * nseg
+  float c;          // log2(e) / tau
+  float inv_tau;
+  const int64_t* tokens;
+  float4* part;     // partial sums [N][2 nseg]
+  float* z_token;   // the tokens' logits [N]
+  WaitCtl ctl;
+};
+cudaError_t head_prepare(int* max_clusters);
+cudaError_t launch_head_logprobs(const CUtensorMap& h, const CUtensorMap& W, const HeadParams& p, float* logp,
+                                 float* entropy, float* lse, int clusters, cudaStream_t stream);
+
+// Backward of the same: the pipelined backward (kl_bwd_pipe.cu) with
+//   G[n, v] = dL/dz = p (A + B log2 p) + 1[v = tokens[n]] g_logp / tau,
+//   A = -(g_logp + g_entropy entropy) / tau, B = -g_entropy ln 2 / tau, log2 p = c z - log2(e) lse.
+struct HeadGrad {
+  const int64_t* tokens;
+  const float* lse;
+  const float* entropy;
+  const float* g_logp;     // or null
+  const float* g_entropy;  // or null
+  float inv_tau;
+};
+cudaError_t launch_bwd_pipe_head(const CUtensorMap* maps, const BwdPipeParams& p, const HeadGrad& g, int clusters,
+                                 cudaStream_t stream);
 
 // Gradient-norm partial sums: one per block of the norm kernel.
 constexpr int kNormPartials = 2048;

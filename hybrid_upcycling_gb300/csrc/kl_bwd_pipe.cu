@@ -37,6 +37,10 @@
 // (w - 4) >> 2 of each 256-column accumulator). Warpgroup 0 gives registers to the two epilogue
 // warpgroups (setmaxnreg: 56 and 224 per thread).
 //
+// The same launch also runs the backward of the token log-probabilities from hidden states
+// (kHead: there is no teacher; G is formed from the student tile, the row's log-sum-exp, entropy
+// and upstream gradients, see HeadGrad). Its F items take one TMEM half, like M items.
+//
 // TMEM holds two 256-column halves. An M item takes one; an F item takes one for the teacher
 // tile and the other for the student tile. The UMMA warp signals the teacher half as soon as its
 // tiles are done, and the epilogue copies all 128 teacher logits of its row into registers and
@@ -45,8 +49,9 @@
 // freed first (after an F item, its teacher half; after an M item, the other half), so the
 // epilogue's work overlaps the UMMAs of the next item instead of stalling them.
 #include <cmath>
+#include <type_traits>
 
-#include "hylo_internal.h"
+#include "hylo_ops_internal.h"
 #include "kl_stats.cuh"
 
 namespace hylo {
@@ -255,9 +260,52 @@ __device__ __forceinline__ int m_kblocks(const Geo& g, int kind) {
   return SPLIT ? 2 * k : k;
 }
 
-template <bool SPLIT>
+struct NoHead {};
+
+// G for 32 columns of one row of the token log-probabilities: z becomes dL/dz.
+struct HeadRow {
+  float A, B, hit, l2;  // see HeadGrad; hit = g_logp / tau, l2 = log2(e) lse
+  int tcol;             // the token, or -1
+};
+
+__device__ __forceinline__ HeadRow head_row(const HeadGrad& g, int token, int N, int V) {
+  HeadRow r{0.f, 0.f, 0.f, 0.f, -1};
+  if (token >= N) return r;
+  const int64_t t = g.tokens[token];
+  float gl = g.g_logp != nullptr && t >= 0 ? g.g_logp[token] : 0.f;
+  if (t >= V) gl = __uint_as_float(0x7fffffffu);  // not a token: NaN, as in the forward
+  const float gh = g.g_entropy != nullptr ? g.g_entropy[token] : 0.f;
+  r.A = -g.inv_tau * (gh != 0.f ? fmaf(gh, g.entropy[token], gl) : gl);
+  r.B = -g.inv_tau * gh * 0.6931471805599453f;
+  r.hit = g.inv_tau * gl;
+  r.l2 = g.lse[token] * kLog2e;
+  r.tcol = t >= 0 && t < V ? static_cast<int>(t) : -1;
+  return r;
+}
+
+__device__ __forceinline__ void head_grad32(const HeadRow& r, float (&z)[32], int col, float c) {
+  const float2 c2 = make_float2(c, c), nl = make_float2(-r.l2, -r.l2), A2 = make_float2(r.A, r.A),
+               B2 = make_float2(r.B, r.B);
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const float2 y = __ffma2_rn(make_float2(z[2 * j], z[2 * j + 1]), c2, nl);
+    const float2 g = __fmul2_rn(ex2_approx2(y), __ffma2_rn(B2, y, A2));
+    z[2 * j] = g.x;
+    z[2 * j + 1] = g.y;
+  }
+  const int rel = r.tcol - col;
+  if (__any_sync(0xffffffffu, rel >= 0 && rel < 32)) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j == rel) z[j] += r.hit;
+  }
+}
+
+// Head: NoHead for the distillation loss, HeadGrad for the token log-probabilities.
+template <bool SPLIT, typename Head>
 __global__ void __launch_bounds__(kThreads, 1)
-bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p) {
+bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p, const Head head) {
+  constexpr bool kHead = !std::is_same<Head, NoHead>::value;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* staging_all = smem + STAGES * STAGE_BYTES;
@@ -475,7 +523,7 @@ bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p) {
         mbar_arrive(iempty + slot);
         if (it.kind == kItemEnd) break;
         const Geo g = geo(p, it.b);
-        if (it.kind == kItemF) {
+        if (!kHead && it.kind == kItemF) {
           // teacher tile (K = d_t) into half t = hp, student tile (K = d_s) into the other; each
           // half is awaited just before its own UMMAs, and the teacher half is signalled as soon
           // as its UMMAs are done
@@ -524,10 +572,11 @@ bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p) {
             break;
           }
           tc_fence_after();
+          const bool fwd = kHead && it.kind == kItemF;  // one tile z = h W^T
           const bool amn = it.kind == kItemDW;
-          const uint32_t idesc = amn ? kIdescDW : kIdescDH;
+          const uint32_t idesc = fwd ? kIdescF : amn ? kIdescDW : kIdescDH;
           const uint32_t d = tmem_base + static_cast<uint32_t>(h * BN);
-          const int nkb = m_kblocks<SPLIT>(g, it.kind);
+          const int nkb = fwd ? p.kb_s : m_kblocks<SPLIT>(g, it.kind);
           for (int kb = 0; kb < nkb; ++kb) {
             if (!wait_bounded(full + stage, phase, abort_flag, p.ctl, 30)) {
               ok = false;
@@ -538,7 +587,7 @@ bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p) {
             const uint32_t sb = sa + A_BYTES;
 #pragma unroll
             for (int q = 0; q < kBK / 16; ++q) {
-              umma_bf16_pair(d, slice_desc(amn, sa, q), slice_desc(true, sb, q), idesc, (kb > 0 || q > 0) ? 1u : 0u);
+              umma_bf16_pair(d, slice_desc(amn, sa, q), slice_desc(!fwd, sb, q), idesc, (kb > 0 || q > 0) ? 1u : 0u);
             }
             umma_commit_pair(empty + stage, 0x3);
             issued = true;
@@ -594,31 +643,40 @@ bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p) {
         const int ti = it.idx % g.tt, vi = it.idx / g.tt;
         const int row_local = ti * BN + static_cast<int>(rank) * kBM + q * 32;  // first slot row of this warp
         const int token = g.r0 + row_local + lane;
+        HeadRow hr{};
+        if constexpr (kHead) hr = head_row(head, token, p.N, p.V);
         float bt = 0.f, bs = 0.f, ngl = 0.f;
-        if (token < p.N) {
+        if (!kHead && token < p.N) {
           const float lt_ = p.lse_t[token], ls_ = p.lse_s[token];
           bt = lt_ * kLog2e;
           bs = ls_ * kLog2e;
           ngl = -(p.lse_gap != nullptr ? p.lse_gap[token] : ls_ - lt_) * kLog2e;
         }
-        const int t = hp, sh = hp ^ 1;
-        // the teacher tile: all 128 logits of this row and column half into registers, then the
-        // half goes back to the UMMAs
-        const bool wt = wait_bounded(tfull + t, uses[t] & 1u, abort_flag, p.ctl, 32);
-        if (!__all_sync(0xffffffffu, wt)) break;
-        tc_fence_after();
-        float zt[HB];
+        const int t = hp, sh = kHead ? hp : hp ^ 1;
+        float zt[kHead ? 1 : HB];
+        if constexpr (!kHead) {
+          // the teacher tile: all 128 logits of this row and column half into registers, then the
+          // half goes back to the UMMAs
+          const bool wt = wait_bounded(tfull + t, uses[t] & 1u, abort_flag, p.ctl, 32);
+          if (!__all_sync(0xffffffffu, wt)) break;
+          tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < HB / 32; ++c) tmem_ld32_at(lane_base + static_cast<uint32_t>(t * BN + c * 32), zt + 32 * c);
-        tmem_ld_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(lead_tempty + t * 8);
+          for (int c = 0; c < HB / 32; ++c) tmem_ld32_at(lane_base + static_cast<uint32_t>(t * BN + c * 32), zt + 32 * c);
+          tmem_ld_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(lead_tempty + t * 8);
+        }
         const bool ws = wait_bounded(tfull + sh, uses[sh] & 1u, abort_flag, p.ctl, 32);
         if (!__all_sync(0xffffffffu, ws)) break;
         tc_fence_after();
-        ++uses[0];
-        ++uses[1];
+        if constexpr (kHead) {
+          ++uses[sh];
+          hp ^= 1;
+        } else {
+          ++uses[0];
+          ++uses[1];
+        }
         const int col_local = vi * BN + hc * HB;  // first block column of this warp
         const float2 c2v = make_float2(p.c, p.c), gs2 = make_float2(p.gscale, p.gscale);
         const float2 nbt = make_float2(-bt, -bt), nbs = make_float2(-bs, -bs), ngl2 = make_float2(ngl, ngl);
@@ -627,13 +685,15 @@ bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p) {
           float zs[32];
           tmem_ld32(lane_base + static_cast<uint32_t>(sh * BN + c * 32), zs);
           tmem_ld_wait();
+          if constexpr (kHead) head_grad32(hr, zs, g.v0 + col_local + c * 32, p.c);
           const int vcols = g.Vb - (col_local + c * 32);  // columns of this chunk inside the vocabulary
           uint32_t pk[16], pl[16];  // G in bf16 and (split) its bf16 rounding remainder
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            float2 gv = __fmul2_rn(prob_diff2(make_float2(zt[32 * c + 2 * j], zt[32 * c + 2 * j + 1]),
-                                              make_float2(zs[2 * j], zs[2 * j + 1]), c2v, nbt, nbs, ngl2),
-                                   gs2);
+            float2 gv = make_float2(zs[2 * j], zs[2 * j + 1]);
+            if constexpr (!kHead)
+              gv = __fmul2_rn(prob_diff2(make_float2(zt[32 * c + 2 * j], zt[32 * c + 2 * j + 1]), gv, c2v, nbt, nbs, ngl2),
+                              gs2);
             if (vcols < 32) {  // the vocabulary ends inside this chunk: G = 0 past it
               if (2 * j >= vcols) gv.x = 0.f;
               if (2 * j + 1 >= vcols) gv.y = 0.f;
@@ -777,23 +837,40 @@ cudaLaunchConfig_t pipe_config(cudaLaunchAttribute* attr, int clusters, cudaStre
 }  // namespace
 
 cudaError_t bwd_pipe_prepare(int* max_clusters) {
-  cudaError_t e = cudaFuncSetAttribute(bwd_pipe_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-  if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(bwd_pipe_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-  if (e != cudaSuccess) return e;
+  const void* kernels[] = {reinterpret_cast<const void*>(bwd_pipe_kernel<false, NoHead>),
+                           reinterpret_cast<const void*>(bwd_pipe_kernel<true, NoHead>),
+                           reinterpret_cast<const void*>(bwd_pipe_kernel<false, HeadGrad>),
+                           reinterpret_cast<const void*>(bwd_pipe_kernel<true, HeadGrad>)};
+  for (const void* k : kernels) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = pipe_config(attr, 1, nullptr);
   cfg.numAttrs = 1;  // occupancy: the cluster shape only
-  return cudaOccupancyMaxActiveClusters(max_clusters, bwd_pipe_kernel<false>, &cfg);
+  return cudaOccupancyMaxActiveClusters(max_clusters, bwd_pipe_kernel<false, NoHead>, &cfg);
 }
 
-cudaError_t launch_bwd_pipe(const CUtensorMap* maps, const BwdPipeParams& p, int clusters, cudaStream_t stream) {
+namespace {
+template <typename Head>
+cudaError_t launch_pipe(const CUtensorMap* maps, const BwdPipeParams& p, const Head& head, int clusters,
+                        cudaStream_t stream) {
   PipeMaps pm;
   for (int m = 0; m < kPipeMaps; ++m) pm.m[m] = maps[m];
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = pipe_config(attr, clusters, stream);
-  return p.split ? cudaLaunchKernelEx(&cfg, bwd_pipe_kernel<true>, pm, p)
-                 : cudaLaunchKernelEx(&cfg, bwd_pipe_kernel<false>, pm, p);
+  return p.split ? cudaLaunchKernelEx(&cfg, bwd_pipe_kernel<true, Head>, pm, p, head)
+                 : cudaLaunchKernelEx(&cfg, bwd_pipe_kernel<false, Head>, pm, p, head);
+}
+}  // namespace
+
+cudaError_t launch_bwd_pipe(const CUtensorMap* maps, const BwdPipeParams& p, int clusters, cudaStream_t stream) {
+  return launch_pipe(maps, p, NoHead{}, clusters, stream);
+}
+
+cudaError_t launch_bwd_pipe_head(const CUtensorMap* maps, const BwdPipeParams& p, const HeadGrad& g, int clusters,
+                                 cudaStream_t stream) {
+  return launch_pipe(maps, p, g, clusters, stream);
 }
 
 }  // namespace hylo

@@ -50,6 +50,29 @@ hylo_status hylo_token_logprobs_backward(const void* z, int dtype, int64_t N, in
                                          const float* g_logp, const float* g_entropy, void* dz, int64_t ldd,
                                          cudaStream_t stream);
 
+/* The same log-probabilities and entropies for z = h W^T, without storing z: h [N, d] final hidden
+ * states, W [V, d] LM head, bf16 bit patterns, row-major and contiguous, 16-byte aligned, d a multiple
+ * of 8 in 8..65536. Inputs are meant finite (where they are not, the results of the tokens
+ * concerned are NaN or infinite). tokens as above. entropy and lse may be NULL; the backward needs lse
+ * (and entropy, if g_entropy is given). workspace: at least hylo_head_logprobs_workspace_bytes(),
+ * 256-byte aligned, not shared with a call still running on another stream; the forward uses O(N) of it,
+ * the backward the G ring of hylo_kl_backward (at most 128 MiB, twice that with split_g).
+ * Returns 0 for invalid sizes; token_chunk <= 0 means 4096. */
+size_t hylo_head_logprobs_workspace_bytes(int64_t N, int64_t d, int64_t V, int64_t token_chunk, int split_g);
+hylo_status hylo_head_logprobs(const uint16_t* h, const uint16_t* W, int64_t N, int64_t d, int64_t V, float tau,
+                               const int64_t* tokens, float* logp, float* entropy, float* lse, void* workspace,
+                               size_t workspace_bytes, cudaStream_t stream);
+
+/* Gradients of sum_n g_logp[n] logp[n] + g_entropy[n] entropy[n]: with G = dL/dz as in
+ * hylo_token_logprobs_backward (recomputed tile by tile, rounded to bf16 once, or with split_g != 0
+ * kept as two bf16 terms), dh = G W [N, d] and dW = G^T h [V, d], fp32, OVERWRITTEN. lse and
+ * entropy are the forward's for the same inputs. token_chunk as in hylo_kl_backward. Deterministic. */
+hylo_status hylo_head_logprobs_backward(const uint16_t* h, const uint16_t* W, int64_t N, int64_t d, int64_t V,
+                                        float tau, int64_t token_chunk, const int64_t* tokens, const float* lse,
+                                        const float* entropy, const float* g_logp, const float* g_entropy, int split_g,
+                                        float* dh, float* dW, void* workspace, size_t workspace_bytes,
+                                        cudaStream_t stream);
+
 /* One tensor of an optimizer step. All arrays have `n` elements and start element-aligned. */
 typedef struct {
   void* param;        /* fp32, or bf16 (see hylo_adamw_step) */

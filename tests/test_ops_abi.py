@@ -114,3 +114,57 @@ def test_python_checks():
             bad()
     s = State8.zeros_like(torch.zeros(257))
     assert s.codes.numel() == 257 and s.exponents.numel() == 2 and torch.all(s.values() == 0)
+
+
+def _head(lib, **kw):
+    a = dict(h=FAKE, W=FAKE, N=16, d=64, V=100, tau=1.0, tok=FAKE, logp=FAKE, ent=None, lse=None, ws=FAKE, nbytes=1 << 30)
+    a.update(kw)
+    return lib.hylo_head_logprobs(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(h=None), -1), (dict(tok=None), -1), (dict(logp=None), -1), (dict(ws=None), -1), (dict(N=0), -2), (dict(d=60), -2),
+    (dict(d=65544), -2), (dict(V=1 << 31), -2), (dict(h=FAKE + 8), -3), (dict(tok=FAKE + 4), -3), (dict(ws=FAKE + 16), -3),
+    (dict(ent=FAKE + 2), -3), (dict(tau=0.0), -4), (dict(nbytes=64), -5),
+])
+def test_head_logprobs_refuses(lib, kw, status):
+    assert _head(lib, **kw) == status
+    assert lib.hylo_kl_last_error()
+
+
+def _head_bwd(lib, **kw):
+    a = dict(h=FAKE, W=FAKE, N=16, d=64, V=100, tau=1.0, chunk=0, tok=FAKE, lse=FAKE, ent=FAKE, gl=FAKE, ge=FAKE, split=0,
+             dh=FAKE, dW=FAKE, ws=FAKE, nbytes=1 << 30)
+    a.update(kw)
+    return lib.hylo_head_logprobs_backward(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(W=None), -1), (dict(lse=None), -1), (dict(dh=None), -1), (dict(dW=None), -1), (dict(ent=None), -1),
+    (dict(N=-1), -2), (dict(d=12), -2), (dict(N=1 << 30, V=1 << 30), -2), (dict(dh=FAKE + 8), -3), (dict(gl=FAKE + 1), -3),
+    (dict(tau=float("nan")), -4), (dict(nbytes=256), -5),
+])
+def test_head_logprobs_backward_refuses(lib, kw, status):
+    if kw.get("N") == 1 << 30:
+        kw = dict(kw, nbytes=1 << 62)
+    assert _head_bwd(lib, **kw) == status
+    assert lib.hylo_kl_last_error()
+
+
+def test_head_workspace(lib):
+    q = _lib.hylo_head_logprobs_workspace_bytes
+    ring = 3 * 4096 * 5376 * 2
+    assert q(4096, 2048, 128256) == ring + 256 and q(4096, 2048, 128256, split_g=True) == 2 * ring + 256
+    assert q(1 << 20, 2048, 128256) == (1 << 20) * (4 + 2 * 32 * 16)
+    assert q(1, 64, 256) == 3 * 256 * 256 * 2 + 256
+    assert q(0, 64, 10) == 0 and q(1, 60, 10) == 0 and q(1, 64, 0) == 0
+
+
+def test_head_python_checks():
+    from hybrid_upcycling_gb300 import head_logprobs
+    h, W, t = torch.zeros(3, 16).bfloat16(), torch.zeros(10, 16).bfloat16(), torch.zeros(3, dtype=torch.int64)
+    for bad in (lambda: head_logprobs(h, W, t), lambda: head_logprobs(h.float(), W, t), lambda: head_logprobs(h, W[:, :8], t),
+                lambda: head_logprobs(h, W, t[:2]), lambda: head_logprobs(h, W, t.int()),
+                lambda: head_logprobs(h[:, :12], W[:, :12], t)):
+        with pytest.raises(ValueError):
+            bad()
