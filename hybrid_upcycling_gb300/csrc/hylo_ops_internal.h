@@ -37,6 +37,7 @@ struct TokenGrad {
   int64_t ldd;
 };
 
+cudaError_t token_logprobs_prepare();  // once per device
 cudaError_t launch_token_logprobs(const TokenRows& in, const TokenOut& out, int dtype, int sms, cudaStream_t stream);
 cudaError_t launch_token_logprobs_bwd(const TokenRows& in, const TokenGrad& g, int dtype, int sms, cudaStream_t stream);
 

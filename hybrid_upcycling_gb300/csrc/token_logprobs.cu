@@ -6,12 +6,12 @@
 // Both directions are bound by HBM: the forward reads each logit once, the backward reads it
 // once and writes the gradient once.
 //
-// Alternatives. While a row streams by, each 256-word block's largest logit is kept ("group
-// maximum"). Order the groups by (maximum, lower position first): a word of any group behind the
-// first k is beaten by the k words that are the maxima of those k groups, also under the tie
-// rule, because groups are contiguous runs of words. So only k groups are read again
-// (from L2), and of those only words not below the k-th group maximum are candidates; each
-// candidate's rank is the number of candidates that beat it.
+// Alternatives. While a row streams by, the largest logit of each of at most kMaxGroups contiguous
+// groups of words is kept. Order the groups by (maximum, lower position first): a word of any
+// group behind the first k is beaten by the k words that are the maxima of those k groups, also
+// under the tie rule, because groups are contiguous. So only k groups are read again (from
+// L2): of their words, those above the k-th group maximum T are candidates, and the first
+// k equal to T; each candidate's rank is the number of candidates that beat it.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -26,13 +26,8 @@ constexpr float kLn2F = 0.6931471805599453f;
 // log2-probabilities below this are taken as this: e^y is 0 there in fp32, and products with it stay finite
 constexpr float kFloor = -200.f;
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
-constexpr int kBlock = 256;      // words per block: one group unless the vocabulary is very long
-constexpr int kBatch = 4;        // blocks a warp has in flight
-constexpr int kMaxGroups = 1024; // group maxima kept per row
-constexpr int kCand = 1024;      // candidates held at once
-constexpr int kCandBatch = (kCand - HYLO_TOP_MAX) / kBlock;  // blocks gathered at once when all do not fit
+constexpr int kMaxGroups = 512;  // group maxima kept per row
+constexpr int kMaxSplit = 16;    // CTAs of a cluster that share a row
 
 // Maximum that keeps a NaN (a row with one has NaN results).
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -47,13 +42,20 @@ __device__ __forceinline__ float warp_max_nan(float v) {
   return r;
 }
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 template <typename T>
 struct Elem;
 template <>
 struct Elem<float> {
   static constexpr int kVec = 4;
-  static constexpr int kKeyBits = 32;  // leading bits of the order key in which values differ
+  static constexpr int kKeyBits = 32;  // leading bits of the order key in which values of the type differ
   static __device__ __forceinline__ float get(float x) { return x; }
+  static constexpr uint32_t kMasked = 0xff800000u;  // a 32-bit word of -inf
+  static __device__ __forceinline__ float vec_max(uint4 v) {
+    return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)), max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
+  }
   static __device__ __forceinline__ void unpack(uint4 v, float* z) {
     z[0] = __uint_as_float(v.x);
     z[1] = __uint_as_float(v.y);
@@ -70,6 +72,16 @@ struct Elem<__nv_bfloat16> {
   static constexpr int kVec = 8;
   static constexpr int kKeyBits = 16;
   static __device__ __forceinline__ float get(__nv_bfloat16 x) { return __bfloat162float(x); }
+  static constexpr uint32_t kMasked = 0xff80ff80u;
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  static __device__ __forceinline__ float vec_max(uint4 v) {
+    const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
+    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
   static __device__ __forceinline__ void unpack(uint4 v, float* z) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -88,6 +100,17 @@ struct Elem<__half> {
   static constexpr int kVec = 8;
   static constexpr int kKeyBits = 19;
   static __device__ __forceinline__ float get(__half x) { return __half2float(x); }
+  static constexpr uint32_t kMasked = 0xfc00fc00u;
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  static __device__ __forceinline__ float vec_max(uint4 v) {
+    const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&m));
+    return max_nan(f.x, f.y);
+  }
   static __device__ __forceinline__ void unpack(uint4 v, float* z) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -162,193 +185,463 @@ struct Row {
     base = p - lead;
     end = static_cast<int64_t>(lead) + V;
   }
-  // The vector at u0 (a multiple of kVec); words outside the row read as -inf. kInPlace: the kernel
-  // may write over the logits, so the read-only path is not used.
+  __device__ __forceinline__ bool inside(int64_t u0, int64_t u1) const { return u0 >= lead && u1 <= end; }
+  // The vector at u0 (a multiple of kVec), which lies inside the row. kInPlace: the kernel may write
+  // over the logits, so the read-only path is not used.
   template <bool kInPlace = false>
-  __device__ __forceinline__ void load(int64_t u0, float* z) const {
+  __device__ __forceinline__ uint4 whole(int64_t u0) const {
+    const uint4* p = reinterpret_cast<const uint4*>(base + u0);
+    return kInPlace ? *p : __ldg(p);
+  }
+  // The same where it may reach over the row's ends, word by word; words outside are -inf.
+  template <bool kInPlace = false>
+  __device__ uint4 edge(int64_t u0) const {
     constexpr int VE = Elem<T>::kVec;
-    if (u0 >= lead && u0 + VE <= end) {
-      const uint4* p = reinterpret_cast<const uint4*>(base + u0);
-      Elem<T>::unpack(kInPlace ? *p : __ldg(p), z);
-    } else {
+    if (inside(u0, u0 + VE)) return whole<kInPlace>(u0);
+    uint4 v = make_uint4(Elem<T>::kMasked, Elem<T>::kMasked, Elem<T>::kMasked, Elem<T>::kMasked);
+    T* t = reinterpret_cast<T*>(&v);
 #pragma unroll
-      for (int i = 0; i < VE; ++i) z[i] = u0 + i >= lead && u0 + i < end ? Elem<T>::get(base[u0 + i]) : -INFINITY;
-    }
+    for (int i = 0; i < VE; ++i)
+      if (u0 + i >= lead && u0 + i < end) t[i] = base[u0 + i];
+    return v;
   }
 };
 
+// Folds the words of one vector, relative to the maximum m0: y = (z - m0) c. The difference comes first: it is
+// exact where it matters, and finite logits of any size cannot give inf - inf.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const TokenRows in, const TokenOut out, int group_shift) {
-  constexpr int VE = Elem<T>::kVec;
-  constexpr int VL = kBlock / (32 * VE);  // vectors of a block per lane
-  __shared__ Sums warp_sums[kWarps];
-  __shared__ uint32_t group_key[kMaxGroups];
-  __shared__ uint64_t cand[kCand];
-  __shared__ uint64_t top[HYLO_TOP_MAX];
-  __shared__ int sel[HYLO_TOP_MAX];
-  __shared__ uint32_t bound_key;
-  __shared__ int count;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int group_blocks = 1 << group_shift;
-  const int run = max(kBatch, group_blocks);  // consecutive blocks of one warp
+__device__ __forceinline__ void fold(uint4 v, float m0, float c, float2& s, float2& a) {
+  float z[Elem<T>::kVec];
+  Elem<T>::unpack(v, z);
+  const float2 nm = make_float2(-m0, -m0), c2 = make_float2(c, c);
+#pragma unroll
+  for (int j = 0; j < Elem<T>::kVec / 2; ++j) {
+    float2 y = __fmul2_rn(__fadd2_rn(make_float2(z[2 * j], z[2 * j + 1]), nm), c2);
+    y.x = max_nan(y.x, kFloor);
+    y.y = max_nan(y.y, kFloor);
+    const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+    s = __fadd2_rn(s, e);
+    a = __ffma2_rn(e, y, a);
+  }
+}
 
-  for (int64_t n = blockIdx.x; n < in.N; n += gridDim.x) {
+template <int kWarps>
+struct Shared {
+  static constexpr int kCand = kWarps > 1 ? 1024 : 512;  // candidates held at once
+  static constexpr int kHits = kWarps > 1 ? 256 : 96;    // vectors with candidates
+  Sums warp_sums[kWarps];
+  Sums cta_sums[kMaxSplit];        // in the first CTA of a cluster: every CTA's
+  union {
+    uint32_t group_key[kMaxGroups];  // in the first CTA: the whole row's
+    struct {                         // once the groups are chosen
+      uint4 vec[kHits];
+      int at[kHits];  // which vector of the row
+    } hit;
+  };
+  uint64_t cand[kCand];
+  uint64_t top[HYLO_TOP_MAX];
+  int sel[HYLO_TOP_MAX];
+  int enough[2][kWarps];
+  int count_a[kWarps];
+  int count_b[2][kWarps];
+  uint32_t bound_key;
+  int count;
+  int hits;
+};
+
+// A row's groups: 2^vec_shift vectors each (`count` of them).
+struct Groups {
+  int vec_shift;
+  int count;
+};
+
+// The best k of cand[0..have), in order, into top: an entry's rank is the number of entries that beat it.
+template <int kWarps>
+__device__ __forceinline__ void rank_all(Shared<kWarps>& sh, int have, int k) {
+  for (int i = threadIdx.x; i < have; i += kWarps * 32) {
+    const uint64_t mine = sh.cand[i];
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < have; ++j) rank += sh.cand[j] > mine;
+    if (rank < k) sh.top[rank] = mine;
+  }
+}
+
+// The first kk groups by (maximum, position) into sh.sel, ascending by position; the kk-th largest maximum (in the
+// leading bits of its key) into sh.bound_key. Ends with a barrier. (Loops are kept rolled here and below: this
+// code runs once per row, and in a call of few rows its instructions come from L2. Unrolled, it took 24 us
+// of a 31 us call.)
+template <typename T, int kWarps>
+__device__ void choose_groups(Shared<kWarps>& sh, int groups, int kk, int k) {
+  constexpr uint32_t kHigh = Elem<T>::kKeyBits == 32 ? ~0u : ~0u << (32 - Elem<T>::kKeyBits);
+  constexpr int kPer = kMaxGroups / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t t = 0;  // from the top, the largest t that at least kk maxima reach
+  {
+    uint32_t key[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) key[j] = j * 32 + lane < groups ? sh.group_key[j * 32 + lane] & kHigh : 0u;
+    constexpr int kBits = kWarps > 1 ? 3 : 1;  // per step: warp w tries the value w of the next bits (one warp: 1)
+    static_assert(kWarps == 1 || kWarps == 8, "three bits take eight warps");
+    int buf = 0;
+#pragma unroll 1
+    for (int hi = 32; hi > 32 - Elem<T>::kKeyBits; hi -= kBits, buf ^= 1) {
+      const int nb = min(kBits, hi), shift = hi - nb;
+      const uint32_t mine = kWarps > 1 ? warp : 1u;
+      const uint32_t probe = t | (mine << shift);
+      int h0 = 0, h1 = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; j += 2) {
+        h0 += key[j] >= probe;
+        h1 += key[j + 1] >= probe;
+      }
+      const bool enough = __reduce_add_sync(~0u, h0 + h1) >= kk && (mine >> nb) == 0u;
+      if (kWarps > 1) {
+        if (lane == 0) sh.enough[buf][warp] = enough;
+        __syncthreads();
+        const uint32_t ok = __ballot_sync(~0u, lane < kWarps && sh.enough[buf][lane & (kWarps - 1)] != 0);
+        t |= static_cast<uint32_t>(31 - __clz(ok | 1u)) << shift;  // the largest value that is enough
+      } else if (enough) {
+        t = probe;
+      }
+    }
+  }
+  // Places: a group above t comes after the ones above t before it and the equal ones taken before it.
+  int over = 0;
+#pragma unroll 1
+  for (int g = tid; g < groups; g += kWarps * 32) over += (sh.group_key[g] & kHigh) > t;
+  over = __reduce_add_sync(~0u, over);
+  if (lane == 0) sh.count_a[warp] = over;
+  __syncthreads();
+  int need = kk;  // equal ones to take
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) need -= sh.count_a[w];
+  const uint32_t below = (1u << lane) - 1u;
+  int gt_before = 0, eq_before = 0;
+#pragma unroll 1
+  for (int g0 = 0; g0 < groups; g0 += kWarps * 32) {
+    const int g = g0 + tid;
+    const uint32_t key = g < groups ? sh.group_key[g] & kHigh : 0u;
+    const uint32_t gts = __ballot_sync(~0u, key > t), eqs = __ballot_sync(~0u, key == t);
+    if (kWarps > 1) {
+      if (lane == 0) sh.count_b[(g0 / (kWarps * 32)) & 1][warp] = __popc(gts) | (__popc(eqs) << 16);
+      __syncthreads();
+    }
+    int gt = gt_before + __popc(gts & below), eq = eq_before + __popc(eqs & below);
+    if (kWarps > 1) {
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const int c = sh.count_b[(g0 / (kWarps * 32)) & 1][w];
+        gt += w < warp ? c & 0xffff : 0;
+        eq += w < warp ? c >> 16 : 0;
+        gt_before += c & 0xffff;
+        eq_before += c >> 16;
+      }
+    } else {
+      gt_before += __popc(gts);
+      eq_before += __popc(eqs);
+    }
+    if (key > t || (key == t && eq < need)) sh.sel[gt + min(eq, need)] = g;
+  }
+  if (tid == 0) sh.bound_key = kk == k ? t : 0u;  // fewer groups than k: any word may be among the k
+  __syncthreads();
+}
+
+// The row's best k words into sh.top, in order, from the group maxima in sh.group_key (sh.count is 0). Ends with a barrier.
+template <typename T, int kWarps>
+__device__ void best_words(Shared<kWarps>& sh, const Row<T>& row, const Groups gr, int k) {
+  constexpr int VE = Elem<T>::kVec;
+  constexpr uint32_t kHigh = Elem<T>::kKeyBits == 32 ? ~0u : ~0u << (32 - Elem<T>::kKeyBits);
+  constexpr int kCand = Shared<kWarps>::kCand;
+  constexpr int kDeep = 4;  // 32-vector chunks a warp has in flight
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int kk = min(k, gr.count);
+  choose_groups<T>(sh, gr.count, kk, k);
+  const uint32_t bound = sh.bound_key;
+  const int64_t nv = static_cast<int64_t>(kk) << gr.vec_shift;  // vectors of the chosen groups, in their order
+  auto vector_at = [&](int64_t t) {  // where the t-th of them starts
+    const int64_t g = sh.sel[t >> gr.vec_shift];
+    return ((g << gr.vec_shift) + (t & ((int64_t(1) << gr.vec_shift) - 1))) * VE;
+  };
+  auto push = [&](uint64_t cd) {
+    const int at = atomicAdd(&sh.count, 1);
+    if (at < kCand) sh.cand[at] = cd;
+  };
+  // The vectors with a word not below the bound are set down in shared memory, and then every thread looks at
+  // one word of them. That is all unless very many words equal the bound.
+#pragma unroll 1
+  for (int64_t t0 = tid; t0 < nv; t0 += kWarps * kDeep * 32) {
+    uint4 v[kDeep];
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i)
+      if (t0 + i * kWarps * 32 < nv) v[i] = row.edge(vector_at(t0 + i * kWarps * 32));
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) {
+      const int64_t t = t0 + i * kWarps * 32;
+      if (t < nv && (order_key(Elem<T>::vec_max(v[i])) & kHigh) >= bound) {
+        const int at = atomicAdd(&sh.hits, 1);
+        if (at < Shared<kWarps>::kHits) {
+          sh.hit.vec[at] = v[i];
+          sh.hit.at[at] = static_cast<int>(vector_at(t) / VE);
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (sh.hits <= Shared<kWarps>::kHits) {
+    const int words = sh.hits * VE;
+#pragma unroll 1
+    for (int e = tid; e < words; e += kWarps * 32) {
+      const int64_t u = static_cast<int64_t>(sh.hit.at[e / VE]) * VE + e % VE;
+      const uint32_t key = order_key(Elem<T>::get(reinterpret_cast<const T*>(sh.hit.vec)[e]));
+      if ((key & kHigh) >= bound && row.inside(u, u + 1)) push(cand_of(key, static_cast<int>(u - row.lead)));
+    }
+    __syncthreads();
+    const int have = sh.count;
+    if (have <= kCand) {
+      rank_all(sh, have, k);
+      __syncthreads();
+      return;
+    }
+  }
+  // Otherwise in order: the words above the bound, and of those equal to it only the first k.
+  __syncthreads();
+  if (tid == 0) sh.count = 0;
+  __syncthreads();
+  int equal_before = 0;
+#pragma unroll 1
+  for (int64_t t0 = 0; t0 < nv; t0 += kWarps * kDeep * 32) {
+    const int64_t tw = t0 + warp * kDeep * 32 + lane;
+    float top[kDeep];
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) top[i] = tw + i * 32 < nv ? Elem<T>::vec_max(row.edge(vector_at(tw + i * 32))) : -INFINITY;
+    uint32_t hits = 0u;  // bit i: this lane's vector of chunk i holds a word not below the bound
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) hits |= (tw + i * 32 < nv && (order_key(top[i]) & kHigh) >= bound) << i;
+    const uint32_t any = __reduce_or_sync(~0u, hits);
+    uint32_t equal = 0u;  // bit 8 i + q: word q of that vector equals the bound
+#pragma unroll 1
+    for (int i = 0; i < kDeep; ++i) {
+      if (!((hits >> i) & 1u)) continue;
+      const int64_t u = vector_at(tw + i * 32);
+#pragma unroll 1
+      for (int q = 0; q < VE; ++q) {
+        if (!row.inside(u + q, u + q + 1)) continue;
+        const uint32_t key = order_key(Elem<T>::get(row.base[u + q]));
+        if ((key & kHigh) > bound) push(cand_of(key, static_cast<int>(u + q - row.lead)));
+        equal |= static_cast<uint32_t>((key & kHigh) == bound) << (8 * i + q);
+      }
+    }
+    __syncwarp();
+    const int equals = __reduce_add_sync(~0u, __popc(equal));
+    if (lane == 0) sh.count_a[warp] = equals;
+    __syncthreads();
+    int rank = equal_before;  // of this warp's first equal word among all of them
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      rank += w < warp ? sh.count_a[w] : 0;
+      equal_before += sh.count_a[w];
+    }
+    if (equals > 0 && rank < k) {
+      const uint64_t base = static_cast<uint64_t>((bound & 0x80000000u) ? bound : bound | ~kHigh) << 32;  // the full key
+#pragma unroll 1
+      for (int i = 0; i < kDeep; ++i) {
+        if (!((any >> i) & 1u)) continue;
+        uint32_t bits = (equal >> (8 * i)) & 0xffu;
+        int pre = __popc(bits);  // inclusive prefix over the lanes
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int o = __shfl_up_sync(~0u, pre, off);
+          if (lane >= off) pre += o;
+        }
+        int r = rank + pre - __popc(bits);
+        rank += __shfl_sync(~0u, pre, 31);
+        if (bits == 0u) continue;
+        const int64_t v0 = vector_at(tw + i * 32) - row.lead;
+        for (; bits != 0u && r < k; bits &= bits - 1u, ++r)
+          push(base | (0xffffffffu - static_cast<uint32_t>(v0 + __ffs(static_cast<int>(bits)) - 1)));
+      }
+    }
+    __syncthreads();
+  }
+  const int have = sh.count;
+  if (have <= kCand) {
+    rank_all(sh, have, k);
+    __syncthreads();
+    return;
+  }
+  // More candidates than fit (a row in rising order, say): some words at a time, under a rising bound.
+  constexpr int kStep = (kCand - HYLO_TOP_MAX) / (32 * VE) * 32;  // vectors
+  uint64_t least = static_cast<uint64_t>(bound) << 32;  // candidates are not below it
+  int best = 0;
+  for (int64_t t0 = 0; t0 < nv; t0 += kStep) {
+    __syncthreads();
+    if (tid == 0) sh.count = best;
+    for (int i = tid; i < best; i += kWarps * 32) sh.cand[i] = sh.top[i];
+    __syncthreads();
+    for (int64_t t = t0 + tid; t < min(nv, t0 + kStep); t += kWarps * 32) {
+      const int64_t u = vector_at(t);
+#pragma unroll 1
+      for (int q = 0; q < VE; ++q) {
+        if (!row.inside(u + q, u + q + 1)) continue;
+        const uint64_t cd = cand_of(order_key(Elem<T>::get(row.base[u + q])), static_cast<int>(u + q - row.lead));
+        if (cd >= least) sh.cand[atomicAdd(&sh.count, 1)] = cd;
+      }
+    }
+    __syncthreads();
+    const int all = sh.count;
+    rank_all(sh, all, k);
+    best = min(k, all);
+    __syncthreads();
+    if (best == k) least = sh.top[k - 1];
+  }
+  __syncthreads();
+}
+
+// A cluster of S CTAs takes a row at a time, each CTA `span` consecutive blocks of it (a multiple of 4, so that a
+// warp's loads never reach into the next CTA's words). A block is one vector of each lane of a warp.
+template <typename T, int kWarps, bool kTop>
+__global__ void __launch_bounds__(kWarps * 32, 32 / kWarps)
+token_logprobs_kernel(const TokenRows in, const TokenOut out, int span, int vec_shift) {
+  constexpr int VE = Elem<T>::kVec;
+  constexpr int kBlock = 32 * VE;  // words of a block
+  constexpr int kBatch = 4;        // blocks a warp has in flight
+  __shared__ Shared<kWarps> sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t S = 1, q = 0;
+  if (kWarps > 1) {
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(S));
+    q = cluster_ctarank();
+  }
+  const int group_blocks = vec_shift > 5 ? 1 << (vec_shift - 5) : 1;
+  const int run = max(kBatch, group_blocks);  // consecutive blocks of one warp
+  // Between an arrive and its wait the first CTA's shared memory is not written by the others: it may not
+  // have started yet, or still be reading the previous row's.
+  if (S > 1) cluster_arrive();
+
+  for (int64_t n = blockIdx.x / S; n < in.N; n += gridDim.x / S) {
     const Row<T> row(in.z, n * in.ld, in.V);
-    const int64_t blocks = (row.end + kBlock - 1) / kBlock;
-    const int groups = static_cast<int>((blocks + group_blocks - 1) >> group_shift);
+    const int all_blocks = static_cast<int>((row.end + kBlock - 1) / kBlock);
+    const int blk0 = min(all_blocks, static_cast<int>(q) * span), blk1 = min(all_blocks, blk0 + span);
     Sums r{-INFINITY, 0.f, 0.f};
-    for (int64_t b0 = static_cast<int64_t>(warp) * run; b0 < blocks; b0 += kWarps * run) {
-      const int64_t b1 = min(blocks, b0 + run);
+    for (int b0 = blk0 + warp * run; b0 < blk1; b0 += kWarps * run) {
+      const int b1 = min(blk1, b0 + run);
       float gm = -INFINITY;
-      for (int64_t b = b0; b < b1; b += kBatch) {
-        float z[kBatch][VL * VE];
+      for (int b = b0; b < b1; b += kBatch) {
+        const int64_t u0 = static_cast<int64_t>(b) * kBlock + lane * VE;
+        uint4 v[kBatch];
+        if (row.inside(static_cast<int64_t>(b) * kBlock, static_cast<int64_t>(b + kBatch) * kBlock)) {
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
+          for (int i = 0; i < kBatch; ++i) v[i] = row.whole(u0 + i * kBlock);
+        } else {
 #pragma unroll
-          for (int j = 0; j < VL; ++j) row.load((b + i) * kBlock + (j * 32 + lane) * VE, z[i] + j * VE);
+          for (int i = 0; i < kBatch; ++i) v[i] = row.edge(u0 + i * kBlock);
         }
         float mx = r.mx;
+float bm[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-          float bm = z[i][0];
+          bm[i] = Elem<T>::vec_max(v[i]);
+          mx = max_nan(mx, bm[i]);
+        }
+        if (kTop) {
+          if (vec_shift == 5) {  // a group is a block; lane i stores block i's
+            float mine = -INFINITY;
 #pragma unroll
-          for (int j = 1; j < VL * VE; ++j) bm = max_nan(bm, z[i][j]);
-          mx = max_nan(mx, bm);
-          if (out.k > 0 && b + i < b1) {
-            gm = max_nan(gm, bm);
-            if (((b + i + 1) & (group_blocks - 1)) == 0 || b + i + 1 == blocks) {
-              gm = warp_max_nan(gm);
-              if (lane == 0) group_key[(b + i) >> group_shift] = order_key(gm);
+            for (int i = 0; i < kBatch; ++i) {
+              const float m = warp_max_nan(bm[i]);
+              mine = lane == i ? m : mine;
+            }
+            if (lane < kBatch && b + lane < b1) sh.group_key[b + lane] = order_key(mine);
+          } else if (vec_shift < 5) {  // several groups per block
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              float m = bm[i];
+              for (int off = 1; off < (1 << vec_shift); off <<= 1) m = max_nan(m, __shfl_xor_sync(~0u, m, off));
+              if (b + i < b1 && (lane & ((1 << vec_shift) - 1)) == 0)
+                sh.group_key[((b + i) << (5 - vec_shift)) + (lane >> vec_shift)] = order_key(m);
+            }
+          } else {  // a group is a run of batches of this warp
+            gm = max_nan(gm, max_nan(max_nan(bm[0], bm[1]), max_nan(bm[2], bm[3])));
+            if (((b + kBatch) & (group_blocks - 1)) == 0 || b + kBatch >= b1) {
+              const float m = warp_max_nan(gm);
+              if (lane == 0) sh.group_key[b >> (vec_shift - 5)] = order_key(m);
               gm = -INFINITY;
             }
           }
         }
         rebase(r, mx, in.c);
         const float m0 = base_of(mx);
+        float2 s = make_float2(0.f, 0.f), a = s;
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-#pragma unroll
-          for (int j = 0; j < VL * VE; ++j) {
-            const float y = max_nan((z[i][j] - m0) * in.c, kFloor);
-            const float e = ex2_approx(y);
-            r.s += e;
-            r.a = fmaf(e, y, r.a);
-          }
-        }
+        for (int i = 0; i < kBatch; ++i) fold<T>(v[i], m0, in.c, s, a);
+        r.s += s.x + s.y;
+        r.a += a.x + a.y;
       }
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
       merge(r, Sums{__shfl_xor_sync(~0u, r.mx, off), __shfl_xor_sync(~0u, r.s, off), __shfl_xor_sync(~0u, r.a, off)}, in.c);
-    if (lane == 0) warp_sums[warp] = r;
-    if (tid == 0) count = 0;
-    __syncthreads();
-    r = warp_sums[0];
-    for (int w = 1; w < kWarps; ++w) merge(r, warp_sums[w], in.c);  // every thread the same
-    const float log_s = logf(r.s);
-    if (tid == 0) {
-      const int64_t t = in.tokens[n];
-      float lp = 0.f;
-      if (t >= in.V)
-        lp = __uint_as_float(0x7fffffffu);
-      else if (t >= 0)
-        lp = r.mx == -INFINITY ? -INFINITY : (Elem<T>::get(row.base[t + row.lead]) - r.mx) * in.inv_tau - log_s;
-      out.logp[n] = lp;
-      if (out.entropy) out.entropy[n] = r.mx == -INFINITY ? 0.f : log_s - kLn2F * r.a / r.s;
-      if (out.lse) out.lse[n] = r.mx == -INFINITY ? -INFINITY : r.mx * in.inv_tau + log_s;
-      if (out.stats) out.stats[n] = make_float2(r.mx, log_s);
+    if (kWarps > 1) {
+      if (lane == 0) sh.warp_sums[warp] = r;
+      if (tid == 0) sh.count = sh.hits = 0;
+      __syncthreads();
+      r = sh.warp_sums[0];
+      for (int w = 1; w < kWarps; ++w) merge(r, sh.warp_sums[w], in.c);  // every thread the same
+    } else {
+      if (tid == 0) sh.count = sh.hits = 0;
+      __syncthreads();
     }
-    if (out.k > 0) {
-      // ---- the k-th largest group maximum, bit by bit from the top, and the k first groups
-      const int kk = min(out.k, groups);
-      if (warp == 0) {
-        uint32_t t = 0;
-        for (int bit = 31; bit >= 32 - Elem<T>::kKeyBits; --bit) {
-          const uint32_t probe = t | (1u << bit);
-          int have = 0;
-          for (int g = lane; g < groups; g += 32) have += group_key[g] >= probe;
-          if (__reduce_add_sync(~0u, have) >= kk) t = probe;
-        }
-        constexpr uint32_t kHigh = Elem<T>::kKeyBits == 32 ? ~0u : ~0u << (32 - Elem<T>::kKeyBits);
-        int over = 0;
-        for (int g = lane; g < groups; g += 32) over += (group_key[g] & kHigh) > t;
-        over = __reduce_add_sync(~0u, over);
-        int placed = 0, equal_left = kk - over;  // equal maxima: the first groups
-        for (int g0 = 0; g0 < groups; g0 += 32) {
-          const uint32_t key = g0 + lane < groups ? group_key[g0 + lane] & kHigh : 0u;
-          const bool eq = g0 + lane < groups && key == t;
-          const uint32_t eqs = __ballot_sync(~0u, eq);
-          const bool take = (g0 + lane < groups && key > t) || (eq && __popc(eqs & ((1u << lane) - 1u)) < equal_left);
-          const uint32_t takes = __ballot_sync(~0u, take);
-          if (take) sel[placed + __popc(takes & ((1u << lane) - 1u))] = g0 + lane;
-          placed += __popc(takes);
-          equal_left -= min(equal_left, __popc(eqs));
-        }
-        if (lane == 0) bound_key = kk == out.k ? t : 0u;  // fewer groups than k: any word may be among the k
+    if (S > 1) {  // the first CTA of the cluster joins the others' sums and maxima
+      cluster_wait();
+      if (tid == 0) {
+        const uint32_t to = mapa_shared(smem_u32(&sh.cta_sums[q]), 0);
+        st_cluster_u32(to, __float_as_uint(r.mx));
+        st_cluster_u32(to + 4, __float_as_uint(r.s));
+        st_cluster_u32(to + 8, __float_as_uint(r.a));
       }
-      __syncthreads();
-      // ---- candidates: all at once if they fit, else some blocks at a time under a rising bound
-      uint64_t bound = static_cast<uint64_t>(bound_key) << 32;  // candidates are not below it
-      const int64_t nblk = static_cast<int64_t>(kk) << group_shift;  // blocks of the chosen groups
-      auto gather = [&](int64_t i0, int64_t i1) {
-        for (int64_t i = i0 + warp; i < i1; i += kWarps) {
-          const int64_t b = (static_cast<int64_t>(sel[i >> group_shift]) << group_shift) + (i & (group_blocks - 1));
-#pragma unroll
-          for (int j = 0; j < VL; ++j) {
-            const int64_t u = b * kBlock + (j * 32 + lane) * VE;
-            float z[VE];
-            row.load(u, z);
-#pragma unroll
-            for (int q = 0; q < VE; ++q) {
-              if (u + q < row.lead || u + q >= row.end) continue;
-              const uint64_t cd = cand_of(order_key(z[q]), static_cast<int>(u + q - row.lead));
-              if (cd >= bound) {
-                const int at = atomicAdd(&count, 1);
-                if (at < kCand) cand[at] = cd;
-              }
-            }
-          }
-        }
-      };
-      auto rank_all = [&](int have) {  // the best k of cand[0..have), in order, into top
-        for (int i = tid; i < have; i += kThreads) {
-          const uint64_t mine = cand[i];
-          int rank = 0;
-          for (int j = 0; j < have; ++j) rank += cand[j] > mine;
-          if (rank < out.k) top[rank] = mine;
-        }
-      };
-      gather(0, nblk);
-      __syncthreads();
-      int have = count;
-      if (have > kCand) {
-        have = 0;
-        for (int64_t i0 = 0; i0 < nblk; i0 += kCandBatch) {
-          __syncthreads();
-          if (tid == 0) count = have;
-          for (int i = tid; i < have; i += kThreads) cand[i] = top[i];
-          __syncthreads();
-          gather(i0, min(nblk, i0 + kCandBatch));
-          __syncthreads();
-          const int all = count;
-          rank_all(all);
-          have = min(out.k, all);
-          __syncthreads();
-          if (have == out.k) bound = top[out.k - 1];
-        }
-      } else {
-        rank_all(have);
-        __syncthreads();
+      if (kTop && q != 0) {
+        const int per = vec_shift < 5 ? 5 - vec_shift : 0, down = vec_shift > 5 ? vec_shift - 5 : 0;
+        const int g1 = ((blk1 << per) + (1 << down) - 1) >> down;
+        for (int g = ((blk0 << per) >> down) + tid; g < g1; g += kWarps * 32)
+          st_cluster_u32(mapa_shared(smem_u32(&sh.group_key[g]), 0), sh.group_key[g]);
       }
-      for (int i = tid; i < out.k; i += kThreads) {
-        const uint64_t cd = top[i];
-        const float z = key_value(static_cast<uint32_t>(cd >> 32));
-        out.top_logp[n * out.k + i] = r.mx == -INFINITY ? -INFINITY : (z - r.mx) * in.inv_tau - log_s;
-        out.top_ids[n * out.k + i] = cand_index(cd);
+      cluster_sync_all();
+      if (q == 0) {
+        r = sh.cta_sums[0];
+        for (uint32_t c = 1; c < S; ++c) merge(r, sh.cta_sums[c], in.c);
       }
     }
-    __syncthreads();  // shared memory is free for the next row
+    if (q == 0) {
+      const float log_s = logf(r.s);
+      if (tid == 0) {
+        const int64_t t = in.tokens[n];
+        float lp = 0.f;
+        if (t >= in.V)
+          lp = __uint_as_float(0x7fffffffu);
+        else if (t >= 0)
+          lp = r.mx == -INFINITY ? -INFINITY : (Elem<T>::get(row.base[t + row.lead]) - r.mx) * in.inv_tau - log_s;
+        out.logp[n] = lp;
+        if (out.entropy) out.entropy[n] = r.mx == -INFINITY ? 0.f : log_s - kLn2F * r.a / r.s;
+        if (out.lse) out.lse[n] = r.mx == -INFINITY ? -INFINITY : r.mx * in.inv_tau + log_s;
+        if (out.stats) out.stats[n] = make_float2(r.mx, log_s);
+      }
+      if (kTop) {
+        const int64_t vectors = (row.end + VE - 1) / VE;
+        const Groups gr{vec_shift, static_cast<int>((vectors + (int64_t(1) << vec_shift) - 1) >> vec_shift)};
+        best_words<T>(sh, row, gr, out.k);
+        for (int i = tid; i < out.k; i += kWarps * 32) {
+          const uint64_t cd = sh.top[i];
+          const float z = key_value(static_cast<uint32_t>(cd >> 32));
+          out.top_logp[n * out.k + i] = r.mx == -INFINITY ? -INFINITY : (z - r.mx) * in.inv_tau - log_s;
+          out.top_ids[n * out.k + i] = cand_index(cd);
+        }
+      }
+    }
+    __syncthreads();  // this CTA's shared memory is free for the next row
+    if (S > 1) cluster_arrive();
   }
+  if (S > 1) cluster_wait();
 }
 
 constexpr int kBwdThreads = 256;
@@ -381,38 +674,86 @@ __global__ void __launch_bounds__(kBwdThreads) token_logprobs_bwd_kernel(const T
     const float hit = empty ? 0.f : in.inv_tau * gl;
     const int64_t ut = tok >= 0 && tok < in.V ? tok + row.lead : -1;
     const float m0 = base_of(st.x), l2 = empty ? 0.f : st.y * kLog2eF;
-    float z[kBwdVecs][VE];
+    uint4 v[kBwdVecs];
+    if (row.inside(u0, u0 + kPiece)) {
 #pragma unroll
-    for (int i = 0; i < kBwdVecs; ++i) row.template load<true>(u0 + (i * kBwdThreads + threadIdx.x) * VE, z[i]);
+      for (int i = 0; i < kBwdVecs; ++i) v[i] = row.template whole<true>(u0 + (i * kBwdThreads + threadIdx.x) * VE);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kBwdVecs; ++i) v[i] = row.template edge<true>(u0 + (i * kBwdThreads + threadIdx.x) * VE);
+    }
+    const float2 nm = make_float2(-m0, -m0), c2 = make_float2(in.c, in.c), nl = make_float2(-l2, -l2),
+                 A2 = make_float2(A, A), B2 = make_float2(B, B);
 #pragma unroll
     for (int i = 0; i < kBwdVecs; ++i) {
       const int64_t u = u0 + (i * kBwdThreads + threadIdx.x) * VE;
+      float z[VE];
+      Elem<T>::unpack(v[i], z);
 #pragma unroll
-      for (int j = 0; j < VE; ++j) {
-        const float y = max_nan(fmaf(z[i][j] - m0, in.c, -l2), kFloor);
-        float d = ex2_approx(y) * fmaf(B, y, A);
-        if (u + j == ut) d += hit;
-        z[i][j] = d;
+      for (int j = 0; j < VE / 2; ++j) {
+        float2 y = __ffma2_rn(__fadd2_rn(make_float2(z[2 * j], z[2 * j + 1]), nm), c2, nl);
+        y.x = max_nan(y.x, kFloor);
+        y.y = max_nan(y.y, kFloor);
+        const float2 d = __fmul2_rn(make_float2(ex2_approx(y.x), ex2_approx(y.y)), __ffma2_rn(B2, y, A2));
+        z[2 * j] = d.x;
+        z[2 * j + 1] = d.y;
       }
-      if (vec && u >= row.lead && u + VE <= row.end) {
-        __stcs(reinterpret_cast<uint4*>(dst + u), Elem<T>::pack(z[i]));
+      if (static_cast<uint64_t>(ut - u) < VE) {  // the row's token is in this vector
+#pragma unroll
+        for (int j = 0; j < VE; ++j)
+          if (u + j == ut) z[j] += hit;
+      }
+      if (vec && row.inside(u, u + VE)) {
+        __stcs(reinterpret_cast<uint4*>(dst + u), Elem<T>::pack(z));
       } else {
 #pragma unroll
         for (int j = 0; j < VE; ++j)
-          if (u + j >= row.lead && u + j < row.end) dst[u + j] = Elem<T>::put(z[i][j]);
+          if (row.inside(u + j, u + j + 1)) dst[u + j] = Elem<T>::put(z[j]);
       }
     }
   }
 }
 
-template <typename T>
+// CTAs per row: a row is split until the rows' CTAs fill the device or a CTA has less than `kMinSpan` blocks.
+constexpr int kMinSpan = 32;
+int choose_split(int64_t N, int64_t blocks, int sms) {
+  int S = 1;
+  while (S < kMaxSplit && N * S * 2 <= 2 * sms && blocks / (2 * S) >= kMinSpan) S *= 2;
+  return S;
+}
+
+template <typename T, int kWarps, bool kTop>
+cudaError_t launch_rows(const TokenRows& in, const TokenOut& out, int S, int64_t blocks, int sms, cudaStream_t stream) {
+  int vec_shift = 0;  // the smallest groups that fit
+  while (((blocks * 32 + (int64_t(1) << vec_shift) - 1) >> vec_shift) > kMaxGroups) ++vec_shift;
+  if (vec_shift == 6) vec_shift = 7;  // runs of whole batches
+  const int64_t unit = vec_shift > 7 ? int64_t(1) << (vec_shift - 5) : 4;  // whole groups, whole warp loads
+  const int span = static_cast<int>(((blocks + S - 1) / S + unit - 1) / unit * unit);
+  const int64_t cap = static_cast<int64_t>(sms) * (32 / kWarps) / S;
+  const int64_t rows = in.N < cap ? in.N : cap;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(S);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows * S), 1, 1);
+  cfg.blockDim = dim3(kWarps * 32, 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, kWarps, kTop>, in, out, span, vec_shift);
+}
+
+constexpr int kWideWarps = 8;
+constexpr int kShortRow = 16;  // blocks
+
+template <typename T, bool kTop>
 cudaError_t launch_fwd(const TokenRows& in, const TokenOut& out, int sms, cudaStream_t stream) {
-  const int64_t blocks = (static_cast<int64_t>(in.V) + Elem<T>::kVec + kBlock - 1) / kBlock;
-  int shift = 0;
-  while ((blocks >> shift) >= kMaxGroups) ++shift;
-  const int grid = in.N < 4 * sms ? in.N : 4 * sms;
-  token_logprobs_kernel<T><<<grid, kThreads, 0, stream>>>(in, out, shift);
-  return cudaGetLastError();
+  constexpr int VE = Elem<T>::kVec;
+  const int64_t blocks = (static_cast<int64_t>(in.V) + VE - 1 + 32 * VE - 1) / (32 * VE);
+  if (blocks <= kShortRow && in.N >= 4 * sms) return launch_rows<T, 1, kTop>(in, out, 1, blocks, sms, stream);
+  return launch_rows<T, kWideWarps, kTop>(in, out, choose_split(in.N, blocks, sms), blocks, sms, stream);
 }
 
 template <typename T>
@@ -425,13 +766,33 @@ cudaError_t launch_bwd(const TokenRows& in, const TokenGrad& g, int sms, cudaStr
   return cudaGetLastError();
 }
 
+template <typename T>
+cudaError_t launch_fwd_any(const TokenRows& in, const TokenOut& out, int sms, cudaStream_t stream) {
+  return out.k > 0 ? launch_fwd<T, true>(in, out, sms, stream) : launch_fwd<T, false>(in, out, sms, stream);
+}
+
+template <typename T>
+cudaError_t prepare() {
+  const cudaError_t e =
+      cudaFuncSetAttribute(token_logprobs_kernel<T, kWideWarps, true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(token_logprobs_kernel<T, kWideWarps, false>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+}
+
 }  // namespace
+
+cudaError_t token_logprobs_prepare() {
+  cudaError_t e = prepare<float>();
+  if (e == cudaSuccess) e = prepare<__nv_bfloat16>();
+  if (e == cudaSuccess) e = prepare<__half>();
+  return e;
+}
 
 cudaError_t launch_token_logprobs(const TokenRows& in, const TokenOut& out, int dtype, int sms, cudaStream_t stream) {
   switch (dtype) {
-    case HYLO_F32: return launch_fwd<float>(in, out, sms, stream);
-    case HYLO_BF16: return launch_fwd<__nv_bfloat16>(in, out, sms, stream);
-    default: return launch_fwd<__half>(in, out, sms, stream);
+    case HYLO_F32: return launch_fwd_any<float>(in, out, sms, stream);
+    case HYLO_BF16: return launch_fwd_any<__nv_bfloat16>(in, out, sms, stream);
+    default: return launch_fwd_any<__half>(in, out, sms, stream);
   }
 }
 
