@@ -6,6 +6,7 @@
 
 #include "../../include/hylo_kl.h"
 #include "hylo_internal.h"
+#include "hylo_ops_internal.h"
 
 namespace hylo {
 
@@ -17,6 +18,7 @@ struct DeviceState {
   int logits_clusters = 0; // clusters of the logits kernel resident at once
   int pipe_clusters = 0;   // 2-CTA clusters of the pipelined backward resident at once
   int head_clusters = 0;   // 2-CTA clusters of the head log-probability kernel resident at once
+  TokenOccupancy token;    // of the token log-probability kernels
   unsigned pace_epoch = 0;  // epoch of the last paced fused launch on this device
   int* status = nullptr;
   std::string why;

@@ -12,7 +12,6 @@
 #include <cudaTypedefs.h>
 
 #include "hylo_host.h"
-#include "hylo_ops_internal.h"
 
 namespace hylo {
 
@@ -88,7 +87,7 @@ hylo_status current_device(DeviceState** out) {
       if ((e = fused_prepare(fused_bn(), &d.fused_clusters)) != cudaSuccess ||
           (e = bwd_pipe_prepare(&d.pipe_clusters)) != cudaSuccess ||
           (e = kl_logits_prepare(&d.logits_clusters)) != cudaSuccess ||
-          (e = head_prepare(&d.head_clusters)) != cudaSuccess || (e = token_logprobs_prepare()) != cudaSuccess)
+          (e = head_prepare(&d.head_clusters)) != cudaSuccess || (e = token_logprobs_prepare(d.sms, &d.token)) != cudaSuccess)
         return cuda_fail(e, "kernel set-up");
       if (d.pipe_clusters < 1 || d.fused_clusters < 1 || d.logits_clusters < 1 || d.head_clusters < 1)
         return fail(HYLO_ERR_CUDA, "no thread-block cluster of the kernels fits on the device");

@@ -2,7 +2,6 @@
 #include <cmath>
 
 #include "hylo_host.h"
-#include "hylo_ops_internal.h"
 
 using namespace hylo;
 
@@ -79,7 +78,7 @@ hylo_status hylo_token_logprobs(const void* z, int dtype, int64_t N, int64_t V, 
   DeviceState* dev = nullptr;
   if ((st = current_device(&dev)) != HYLO_OK) return st;
   const TokenOut out{k, logp, entropy, lse, reinterpret_cast<float2*>(stats), top_logp, top_ids};
-  const cudaError_t e = launch_token_logprobs(rows_of(z, N, V, ld, tau, tokens), out, dtype, dev->sms, stream);
+  const cudaError_t e = launch_token_logprobs(rows_of(z, N, V, ld, tau, tokens), out, dtype, dev->token, stream);
   return e == cudaSuccess ? HYLO_OK : cuda_fail(e, "launch token log-probabilities");
 }
 

@@ -37,8 +37,14 @@ struct TokenGrad {
   int64_t ldd;
 };
 
-cudaError_t token_logprobs_prepare();  // once per device
-cudaError_t launch_token_logprobs(const TokenRows& in, const TokenOut& out, int dtype, int sms, cudaStream_t stream);
+// What fits on the device at once: clusters of 1, 2, 4, 8 and 16 CTAs of the kernels that split rows.
+struct TokenOccupancy {
+  int sms = 0;
+  int clusters[5] = {};
+};
+cudaError_t token_logprobs_prepare(int sms, TokenOccupancy* occ);  // once per device
+cudaError_t launch_token_logprobs(const TokenRows& in, const TokenOut& out, int dtype, const TokenOccupancy& occ,
+                                  cudaStream_t stream);
 cudaError_t launch_token_logprobs_bwd(const TokenRows& in, const TokenGrad& g, int dtype, int sms, cudaStream_t stream);
 
 // Forward of the log-probabilities from hidden states (head_logprobs.cu).

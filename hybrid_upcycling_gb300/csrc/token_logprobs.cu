@@ -26,7 +26,7 @@ constexpr float kLn2F = 0.6931471805599453f;
 // log2-probabilities below this are taken as this: e^y is 0 there in fp32, and products with it stay finite
 constexpr float kFloor = -200.f;
 
-constexpr int kMaxGroups = 512;  // group maxima kept per row
+constexpr int kMaxGroups = 256;  // group maxima kept per row
 constexpr int kMaxSplit = 16;    // CTAs of a cluster that share a row
 
 // Maximum that keeps a NaN (a row with one has NaN results).
@@ -165,12 +165,18 @@ __device__ __forceinline__ void rebase(Sums& r, float mx, float c) {
   r.mx = mx;
 }
 
-__device__ __forceinline__ void merge(Sums& r, Sums o, float c) {
-  const float mx = max_nan(r.mx, o.mx);
-  rebase(r, mx, c);
-  rebase(o, mx, c);
-  r.s += o.s;
-  r.a += o.a;
+// The sums of `width` lanes (a power of two; the other lanes hold copies of theirs) together, the same in every lane:
+// a fixed tree of additions.
+__device__ __forceinline__ Sums join_lanes(Sums r, int width, float c) {
+  rebase(r, warp_max_nan(r.mx), c);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    if (off < width) {
+      r.s += __shfl_xor_sync(~0u, r.s, off);
+      r.a += __shfl_xor_sync(~0u, r.a, off);
+    }
+  }
+  return r;
 }
 
 // A row in aligned coordinates: word v lies at u = v + lead, and u = 0 is 16-byte aligned.
@@ -193,7 +199,7 @@ struct Row {
     const uint4* p = reinterpret_cast<const uint4*>(base + u0);
     return kInPlace ? *p : __ldg(p);
   }
-  // The same where it may reach over the row's ends, word by word; words outside are -inf.
+  // The vector at u0 where it may reach over the row's ends, word by word; words outside are -inf.
   template <bool kInPlace = false>
   __device__ uint4 edge(int64_t u0) const {
     constexpr int VE = Elem<T>::kVec;
@@ -208,8 +214,9 @@ struct Row {
 };
 
 // Folds the words of one vector, relative to the maximum m0: y = (z - m0) c. The difference comes first: it is
-// exact where it matters, and finite logits of any size cannot give inf - inf.
-template <typename T>
+// exact where it matters, and finite logits of any size cannot give inf - inf. A word of -inf has e^y y = 0
+// only with kMasked, which floors y; otherwise it makes `a` NaN.
+template <typename T, bool kMasked>
 __device__ __forceinline__ void fold(uint4 v, float m0, float c, float2& s, float2& a) {
   float z[Elem<T>::kVec];
   Elem<T>::unpack(v, z);
@@ -217,37 +224,39 @@ __device__ __forceinline__ void fold(uint4 v, float m0, float c, float2& s, floa
 #pragma unroll
   for (int j = 0; j < Elem<T>::kVec / 2; ++j) {
     float2 y = __fmul2_rn(__fadd2_rn(make_float2(z[2 * j], z[2 * j + 1]), nm), c2);
-    y.x = max_nan(y.x, kFloor);
-    y.y = max_nan(y.y, kFloor);
+    if (kMasked) {
+      y.x = max_nan(y.x, kFloor);
+      y.y = max_nan(y.y, kFloor);
+    }
     const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
     s = __fadd2_rn(s, e);
     a = __ffma2_rn(e, y, a);
   }
 }
 
+// What the selection of alternatives works with, for the kWarps warps that do it.
 template <int kWarps>
-struct Shared {
+struct Choice {
   static constexpr int kCand = kWarps > 1 ? 1024 : 512;  // candidates held at once
   static constexpr int kHits = kWarps > 1 ? 256 : 96;    // vectors with candidates
-  Sums warp_sums[kWarps];
-  Sums cta_sums[kMaxSplit];        // in the first CTA of a cluster: every CTA's
-  union {
-    uint32_t group_key[kMaxGroups];  // in the first CTA: the whole row's
-    struct {                         // once the groups are chosen
-      uint4 vec[kHits];
-      int at[kHits];  // which vector of the row
-    } hit;
-  };
   uint64_t cand[kCand];
   uint64_t top[HYLO_TOP_MAX];
+  uint4 hit_vec[kHits];
+  int hit_at[kHits];  // which vector of the row
   int sel[HYLO_TOP_MAX];
-  int enough[2][kWarps];
-  int count_a[kWarps];
-  int count_b[2][kWarps];
+  int equal[kWarps];
   uint32_t bound_key;
   int count;
   int hits;
 };
+
+template <int kWarps>
+__device__ __forceinline__ void sync_warps() {
+  if (kWarps > 1)
+    __syncthreads();
+  else
+    __syncwarp();
+}
 
 // A row's groups: 2^vec_shift vectors each (`count` of them).
 struct Groups {
@@ -257,8 +266,8 @@ struct Groups {
 
 // The best k of cand[0..have), in order, into top: an entry's rank is the number of entries that beat it.
 template <int kWarps>
-__device__ __forceinline__ void rank_all(Shared<kWarps>& sh, int have, int k) {
-  for (int i = threadIdx.x; i < have; i += kWarps * 32) {
+__device__ __forceinline__ void rank_all(Choice<kWarps>& sh, int have, int k, int tid) {
+  for (int i = tid; i < have; i += kWarps * 32) {
     const uint64_t mine = sh.cand[i];
     int rank = 0;
 #pragma unroll 4
@@ -267,96 +276,96 @@ __device__ __forceinline__ void rank_all(Shared<kWarps>& sh, int have, int k) {
   }
 }
 
-// The first kk groups by (maximum, position) into sh.sel, ascending by position; the kk-th largest maximum (in the
-// leading bits of its key) into sh.bound_key. Ends with a barrier. (Loops are kept rolled here and below: this
-// code runs once per row, and in a call of few rows its instructions come from L2. Unrolled, it took 24 us
-// of a 31 us call.)
+// The first kk groups by (maximum, position) into sh.sel, and the kk-th largest maximum (in the leading bits of its
+// key) into sh.bound_key. (Loops are kept rolled here and below: this code runs once per row.)
+//
+// Eight warps: a thread per group counts the groups before its own. It is the quickest for the few rows that are
+// split over clusters.
 template <typename T, int kWarps>
-__device__ void choose_groups(Shared<kWarps>& sh, int groups, int kk, int k) {
+__device__ void rank_groups(Choice<kWarps>& sh, uint32_t* group_key, int groups, int kk, int k, int tid) {
+  constexpr uint32_t kHigh = Elem<T>::kKeyBits == 32 ? ~0u : ~0u << (32 - Elem<T>::kKeyBits);
+  static_assert(kWarps * 32 == kMaxGroups, "a thread per group");
+  // Where the key has low bits that do not matter they hold the position, and all keys differ.
+  constexpr bool kUnique = Elem<T>::kKeyBits <= 24;
+  const uint32_t key = tid < groups ? group_key[tid] : 0u;
+  const uint32_t mine = kUnique && tid < groups ? (key & kHigh) | (kMaxGroups - 1 - tid) : key;
+  group_key[tid] = mine;  // (groups that do not exist: 0, before none)
+  sync_warps<kWarps>();
+  int gt = 0, eq = 0;
+#pragma unroll 2
+  for (int g = 0; g < groups; g += 4) {
+    const uint4 o = *reinterpret_cast<const uint4*>(group_key + g);
+    gt += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+    if (!kUnique) eq += (o.x == mine) + (o.y == mine) + (o.z == mine) + (o.w == mine);
+  }
+  if (!kUnique && eq > 1 && tid < groups)
+    for (int g = 0; g < tid; ++g) gt += group_key[g] == mine;
+  if (tid < groups && gt < kk) sh.sel[gt] = tid;
+  if (tid < groups && gt == kk - 1) sh.bound_key = kk == k ? mine & kHigh : 0u;  // fewer groups than k: any word may count
+}
+
+// One warp: a search for the kk-th largest, which takes fewer instructions; sh.sel ascends by position.
+template <typename T, int kWarps>
+__device__ void choose_groups(Choice<kWarps>& sh, const uint32_t* group_key, int groups, int kk, int k) {
   constexpr uint32_t kHigh = Elem<T>::kKeyBits == 32 ? ~0u : ~0u << (32 - Elem<T>::kKeyBits);
   constexpr int kPer = kMaxGroups / 32;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  uint32_t t = 0;  // from the top, the largest t that at least kk maxima reach
+  const int lane = threadIdx.x & 31;
+  uint32_t t = 0;  // two bits at a time from the top: the largest t that at least kk maxima reach
   {
     uint32_t key[kPer];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) key[j] = j * 32 + lane < groups ? sh.group_key[j * 32 + lane] & kHigh : 0u;
-    constexpr int kBits = kWarps > 1 ? 3 : 1;  // per step: warp w tries the value w of the next bits (one warp: 1)
-    static_assert(kWarps == 1 || kWarps == 8, "three bits take eight warps");
-    int buf = 0;
+    for (int j = 0; j < kPer; ++j) key[j] = j * 32 + lane < groups ? group_key[j * 32 + lane] & kHigh : 0u;
 #pragma unroll 1
-    for (int hi = 32; hi > 32 - Elem<T>::kKeyBits; hi -= kBits, buf ^= 1) {
-      const int nb = min(kBits, hi), shift = hi - nb;
-      const uint32_t mine = kWarps > 1 ? warp : 1u;
-      const uint32_t probe = t | (mine << shift);
-      int h0 = 0, h1 = 0;
+    for (int shift = 30; shift + 2 > 32 - Elem<T>::kKeyBits; shift -= 2) {
+      const uint32_t p1 = t | (1u << shift), p2 = t | (2u << shift), p3 = t | (3u << shift);
+      int h1 = 0, h2 = 0, h3 = 0;
 #pragma unroll
-      for (int j = 0; j < kPer; j += 2) {
-        h0 += key[j] >= probe;
-        h1 += key[j + 1] >= probe;
+      for (int j = 0; j < kPer; ++j) {
+        h1 += key[j] >= p1;
+        h2 += key[j] >= p2;
+        h3 += key[j] >= p3;
       }
-      const bool enough = __reduce_add_sync(~0u, h0 + h1) >= kk && (mine >> nb) == 0u;
-      if (kWarps > 1) {
-        if (lane == 0) sh.enough[buf][warp] = enough;
-        __syncthreads();
-        const uint32_t ok = __ballot_sync(~0u, lane < kWarps && sh.enough[buf][lane & (kWarps - 1)] != 0);
-        t |= static_cast<uint32_t>(31 - __clz(ok | 1u)) << shift;  // the largest value that is enough
-      } else if (enough) {
-        t = probe;
-      }
+      h1 = __reduce_add_sync(~0u, h1 | (h2 << 16));  // at most 256 each
+      h3 = __reduce_add_sync(~0u, h3);
+      t = h3 >= kk ? p3 : (h1 >> 16) >= kk ? p2 : (h1 & 0xffff) >= kk ? p1 : t;
     }
   }
-  // Places: a group above t comes after the ones above t before it and the equal ones taken before it.
   int over = 0;
 #pragma unroll 1
-  for (int g = tid; g < groups; g += kWarps * 32) over += (sh.group_key[g] & kHigh) > t;
-  over = __reduce_add_sync(~0u, over);
-  if (lane == 0) sh.count_a[warp] = over;
-  __syncthreads();
-  int need = kk;  // equal ones to take
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) need -= sh.count_a[w];
+  for (int g = lane; g < groups; g += 32) over += (group_key[g] & kHigh) > t;
+  int equal_left = kk - __reduce_add_sync(~0u, over), placed = 0;  // equal maxima: the first groups
   const uint32_t below = (1u << lane) - 1u;
-  int gt_before = 0, eq_before = 0;
 #pragma unroll 1
-  for (int g0 = 0; g0 < groups; g0 += kWarps * 32) {
-    const int g = g0 + tid;
-    const uint32_t key = g < groups ? sh.group_key[g] & kHigh : 0u;
-    const uint32_t gts = __ballot_sync(~0u, key > t), eqs = __ballot_sync(~0u, key == t);
-    if (kWarps > 1) {
-      if (lane == 0) sh.count_b[(g0 / (kWarps * 32)) & 1][warp] = __popc(gts) | (__popc(eqs) << 16);
-      __syncthreads();
-    }
-    int gt = gt_before + __popc(gts & below), eq = eq_before + __popc(eqs & below);
-    if (kWarps > 1) {
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const int c = sh.count_b[(g0 / (kWarps * 32)) & 1][w];
-        gt += w < warp ? c & 0xffff : 0;
-        eq += w < warp ? c >> 16 : 0;
-        gt_before += c & 0xffff;
-        eq_before += c >> 16;
-      }
-    } else {
-      gt_before += __popc(gts);
-      eq_before += __popc(eqs);
-    }
-    if (key > t || (key == t && eq < need)) sh.sel[gt + min(eq, need)] = g;
+  for (int g0 = 0; g0 < groups; g0 += 32) {
+    const uint32_t key = g0 + lane < groups ? group_key[g0 + lane] & kHigh : 0u;
+    const uint32_t eqs = __ballot_sync(~0u, key == t);
+    const bool take = key > t || (key == t && __popc(eqs & below) < equal_left);
+    const uint32_t takes = __ballot_sync(~0u, take);
+    if (take) sh.sel[placed + __popc(takes & below)] = g0 + lane;
+    placed += __popc(takes);
+    equal_left -= min(equal_left, __popc(eqs));
   }
-  if (tid == 0) sh.bound_key = kk == k ? t : 0u;  // fewer groups than k: any word may be among the k
-  __syncthreads();
+  if (lane == 0) sh.bound_key = kk == k ? t : 0u;  // fewer groups than k: any word may be among the k
 }
 
-// The row's best k words into sh.top, in order, from the group maxima in sh.group_key (sh.count is 0). Ends with a barrier.
+// The row's best k words into sh.top, in order, from its group maxima. `tid` counts the threads of the kWarps warps.
+// Begins and ends with a barrier of those.
 template <typename T, int kWarps>
-__device__ void best_words(Shared<kWarps>& sh, const Row<T>& row, const Groups gr, int k) {
+__device__ void best_words(Choice<kWarps>& sh, uint32_t* group_key, const Row<T>& row, const Groups gr, int k,
+                           int tid) {
   constexpr int VE = Elem<T>::kVec;
   constexpr uint32_t kHigh = Elem<T>::kKeyBits == 32 ? ~0u : ~0u << (32 - Elem<T>::kKeyBits);
-  constexpr int kCand = Shared<kWarps>::kCand;
-  constexpr int kDeep = 4;  // 32-vector chunks a warp has in flight
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kCand = Choice<kWarps>::kCand;
+  constexpr int kDeep = 4;  // 32-vector chunks a warp has in flight (in the ordered path: 8 bits of `equal` each)
+  constexpr int kFirst = kWarps > 1 ? 6 : 4;  // the same in the usual path
+  const int lane = tid & 31, warp = tid >> 5;
   const int kk = min(k, gr.count);
-  choose_groups<T>(sh, gr.count, kk, k);
+  if (tid == 0) sh.count = sh.hits = 0;
+  if constexpr (kWarps > 1)
+    rank_groups<T>(sh, group_key, gr.count, kk, k, tid);
+  else
+    choose_groups<T>(sh, group_key, gr.count, kk, k);
+  sync_warps<kWarps>();
   const uint32_t bound = sh.bound_key;
   const int64_t nv = static_cast<int64_t>(kk) << gr.vec_shift;  // vectors of the chosen groups, in their order
   auto vector_at = [&](int64_t t) {  // where the t-th of them starts
@@ -370,44 +379,53 @@ __device__ void best_words(Shared<kWarps>& sh, const Row<T>& row, const Groups g
   // The vectors with a word not below the bound are set down in shared memory, and then every thread looks at
   // one word of them. That is all unless very many words equal the bound.
 #pragma unroll 1
-  for (int64_t t0 = tid; t0 < nv; t0 += kWarps * kDeep * 32) {
-    uint4 v[kDeep];
+  for (int64_t t0 = tid; t0 < nv; t0 += kWarps * kFirst * 32) {
+    uint4 v[kFirst];
 #pragma unroll
-    for (int i = 0; i < kDeep; ++i)
+    for (int i = 0; i < kFirst; ++i)
       if (t0 + i * kWarps * 32 < nv) v[i] = row.edge(vector_at(t0 + i * kWarps * 32));
 #pragma unroll
-    for (int i = 0; i < kDeep; ++i) {
+    for (int i = 0; i < kFirst; ++i) {
       const int64_t t = t0 + i * kWarps * 32;
       if (t < nv && (order_key(Elem<T>::vec_max(v[i])) & kHigh) >= bound) {
         const int at = atomicAdd(&sh.hits, 1);
-        if (at < Shared<kWarps>::kHits) {
-          sh.hit.vec[at] = v[i];
-          sh.hit.at[at] = static_cast<int>(vector_at(t) / VE);
+        if (at < Choice<kWarps>::kHits) {
+          sh.hit_vec[at] = v[i];
+          sh.hit_at[at] = static_cast<int>(vector_at(t) / VE);
         }
       }
     }
   }
-  __syncthreads();
-  if (sh.hits <= Shared<kWarps>::kHits) {
+  sync_warps<kWarps>();
+  if (sh.hits <= Choice<kWarps>::kHits) {
     const int words = sh.hits * VE;
 #pragma unroll 1
     for (int e = tid; e < words; e += kWarps * 32) {
-      const int64_t u = static_cast<int64_t>(sh.hit.at[e / VE]) * VE + e % VE;
-      const uint32_t key = order_key(Elem<T>::get(reinterpret_cast<const T*>(sh.hit.vec)[e]));
+      const int64_t u = static_cast<int64_t>(sh.hit_at[e / VE]) * VE + e % VE;
+      const uint32_t key = order_key(Elem<T>::get(reinterpret_cast<const T*>(sh.hit_vec)[e]));
       if ((key & kHigh) >= bound && row.inside(u, u + 1)) push(cand_of(key, static_cast<int>(u - row.lead)));
     }
-    __syncthreads();
+    sync_warps<kWarps>();
     const int have = sh.count;
     if (have <= kCand) {
-      rank_all(sh, have, k);
-      __syncthreads();
+      rank_all(sh, have, k, tid);
+      sync_warps<kWarps>();
       return;
     }
   }
   // Otherwise in order: the words above the bound, and of those equal to it only the first k.
-  __syncthreads();
+  sync_warps<kWarps>();
   if (tid == 0) sh.count = 0;
-  __syncthreads();
+  if constexpr (kWarps > 1) {  // the chosen groups by position
+    int mine = 0, before = 0;
+    if (tid < kk) {
+      mine = sh.sel[tid];
+      for (int j = 0; j < kk; ++j) before += sh.sel[j] < mine;
+    }
+    __syncthreads();
+    if (tid < kk) sh.sel[before] = mine;
+  }
+  sync_warps<kWarps>();
   int equal_before = 0;
 #pragma unroll 1
   for (int64_t t0 = 0; t0 < nv; t0 += kWarps * kDeep * 32) {
@@ -434,13 +452,13 @@ __device__ void best_words(Shared<kWarps>& sh, const Row<T>& row, const Groups g
     }
     __syncwarp();
     const int equals = __reduce_add_sync(~0u, __popc(equal));
-    if (lane == 0) sh.count_a[warp] = equals;
-    __syncthreads();
+    if (lane == 0) sh.equal[warp] = equals;
+    sync_warps<kWarps>();
     int rank = equal_before;  // of this warp's first equal word among all of them
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      rank += w < warp ? sh.count_a[w] : 0;
-      equal_before += sh.count_a[w];
+      rank += w < warp ? sh.equal[w] : 0;
+      equal_before += sh.equal[w];
     }
     if (equals > 0 && rank < k) {
       const uint64_t base = static_cast<uint64_t>((bound & 0x80000000u) ? bound : bound | ~kHigh) << 32;  // the full key
@@ -462,12 +480,12 @@ __device__ void best_words(Shared<kWarps>& sh, const Row<T>& row, const Groups g
           push(base | (0xffffffffu - static_cast<uint32_t>(v0 + __ffs(static_cast<int>(bits)) - 1)));
       }
     }
-    __syncthreads();
+    sync_warps<kWarps>();
   }
   const int have = sh.count;
   if (have <= kCand) {
-    rank_all(sh, have, k);
-    __syncthreads();
+    rank_all(sh, have, k, tid);
+    sync_warps<kWarps>();
     return;
   }
   // More candidates than fit (a row in rising order, say): some words at a time, under a rising bound.
@@ -475,10 +493,10 @@ __device__ void best_words(Shared<kWarps>& sh, const Row<T>& row, const Groups g
   uint64_t least = static_cast<uint64_t>(bound) << 32;  // candidates are not below it
   int best = 0;
   for (int64_t t0 = 0; t0 < nv; t0 += kStep) {
-    __syncthreads();
+    sync_warps<kWarps>();
     if (tid == 0) sh.count = best;
     for (int i = tid; i < best; i += kWarps * 32) sh.cand[i] = sh.top[i];
-    __syncthreads();
+    sync_warps<kWarps>();
     for (int64_t t = t0 + tid; t < min(nv, t0 + kStep); t += kWarps * 32) {
       const int64_t u = vector_at(t);
 #pragma unroll 1
@@ -488,109 +506,169 @@ __device__ void best_words(Shared<kWarps>& sh, const Row<T>& row, const Groups g
         if (cd >= least) sh.cand[atomicAdd(&sh.count, 1)] = cd;
       }
     }
-    __syncthreads();
+    sync_warps<kWarps>();
     const int all = sh.count;
-    rank_all(sh, all, k);
+    rank_all(sh, all, k, tid);
     best = min(k, all);
-    __syncthreads();
+    sync_warps<kWarps>();
     if (best == k) least = sh.top[k - 1];
   }
-  __syncthreads();
+  sync_warps<kWarps>();
 }
 
-// A cluster of S CTAs takes a row at a time, each CTA `span` consecutive blocks of it (a multiple of 4, so that a
-// warp's loads never reach into the next CTA's words). A block is one vector of each lane of a warp.
+// Streams blocks blk0 .. blk1 of a row through warps 0 .. kWarps - 1: the lane's sums, and (kTop) the groups' maxima. A
+// block is one vector of each lane of a warp.
 template <typename T, int kWarps, bool kTop>
-__global__ void __launch_bounds__(kWarps * 32, 32 / kWarps)
-token_logprobs_kernel(const TokenRows in, const TokenOut out, int span, int vec_shift) {
+__device__ __forceinline__ Sums stream_row(const Row<T>& row, int blk0, int blk1, int vec_shift, float c, int warp, int lane,
+                                           uint32_t* group_key) {
   constexpr int VE = Elem<T>::kVec;
   constexpr int kBlock = 32 * VE;  // words of a block
   constexpr int kBatch = 4;        // blocks a warp has in flight
-  __shared__ Shared<kWarps> sh;
+  const int group_blocks = vec_shift > 5 ? 1 << (vec_shift - 5) : 1;
+  const int run = max(kBatch, group_blocks);  // consecutive blocks of one warp
+  Sums r{-INFINITY, 0.f, 0.f};
+  bool masked = false;
+  for (int b0 = blk0 + warp * run; b0 < blk1; b0 += kWarps * run) {
+    const int b1 = min(blk1, b0 + run);
+    float gm = -INFINITY;
+    for (int b = b0; b < b1; b += kBatch) {
+      const int64_t u0 = static_cast<int64_t>(b) * kBlock + lane * VE;
+      uint4 v[kBatch];
+      if (row.inside(static_cast<int64_t>(b) * kBlock, static_cast<int64_t>(b + kBatch) * kBlock)) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) v[i] = row.whole(u0 + i * kBlock);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) v[i] = row.edge(u0 + i * kBlock);
+      }
+      float mx = r.mx;
+      float bm[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        bm[i] = Elem<T>::vec_max(v[i]);
+        mx = max_nan(mx, bm[i]);
+      }
+      if (kTop) {
+        if (vec_shift == 6) {  // a group is two blocks; lane i stores pair i's
+          const float m0 = warp_max_nan(max_nan(bm[0], bm[1])), m1 = warp_max_nan(max_nan(bm[2], bm[3]));
+          if (lane < 2 && b + 2 * lane < b1) group_key[(b >> 1) + lane] = order_key(lane == 0 ? m0 : m1);
+        } else if (vec_shift == 5) {  // a group is a block; lane i stores block i's
+          float mine = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const float m = warp_max_nan(bm[i]);
+            mine = lane == i ? m : mine;
+          }
+          if (lane < kBatch && b + lane < b1) group_key[b + lane] = order_key(mine);
+        } else if (vec_shift < 5) {  // several groups per block
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            float m = bm[i];
+            for (int off = 1; off < (1 << vec_shift); off <<= 1) m = max_nan(m, __shfl_xor_sync(~0u, m, off));
+            if (b + i < b1 && (lane & ((1 << vec_shift) - 1)) == 0)
+              group_key[((b + i) << (5 - vec_shift)) + (lane >> vec_shift)] = order_key(m);
+          }
+        } else {  // a group is a batch, or a run of batches, of this warp
+          gm = max_nan(gm, max_nan(max_nan(bm[0], bm[1]), max_nan(bm[2], bm[3])));
+          if (((b + kBatch) & (group_blocks - 1)) == 0 || b + kBatch >= b1) {
+            const float m = warp_max_nan(gm);
+            if (lane == 0) group_key[b >> (vec_shift - 5)] = order_key(m);
+            gm = -INFINITY;
+          }
+        }
+      }
+      if (mx != r.mx) rebase(r, mx, c);
+      const float m0 = base_of(mx);
+      float2 s = make_float2(0.f, 0.f), a = s;
+      // The floor costs an operation per word in the busiest pipe, so it is left out until a masked word shows.
+      if (!masked) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) fold<T, false>(v[i], m0, c, s, a);
+        masked = isnan(a.x + a.y);
+      }
+      if (masked) {
+        s = a = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) fold<T, true>(v[i], m0, c, s, a);
+      }
+      r.s += s.x + s.y;
+      r.a += a.x + a.y;
+    }
+  }
+  return join_lanes(r, 32, c);
+}
+
+// Row n's results but the alternatives; one thread.
+template <typename T>
+__device__ __forceinline__ void write_row(const TokenRows& in, const TokenOut& out, int64_t n, const Row<T>& row, const Sums& r,
+                                          float log_s) {
+  const int64_t t = in.tokens[n];
+  float lp = 0.f;
+  if (t >= in.V)
+    lp = __uint_as_float(0x7fffffffu);
+  else if (t >= 0)
+    lp = r.mx == -INFINITY ? -INFINITY : (Elem<T>::get(row.base[t + row.lead]) - r.mx) * in.inv_tau - log_s;
+  out.logp[n] = lp;
+  if (out.entropy) out.entropy[n] = r.mx == -INFINITY ? 0.f : log_s - kLn2F * r.a / r.s;
+  if (out.lse) out.lse[n] = r.mx == -INFINITY ? -INFINITY : r.mx * in.inv_tau + log_s;
+  if (out.stats) out.stats[n] = make_float2(r.mx, log_s);
+}
+
+// Row n's alternatives from top[0..k); thread tid of `threads`.
+__device__ __forceinline__ void write_top(const TokenRows& in, const TokenOut& out, int64_t n, const uint64_t* top,
+                                          const Sums& r, float log_s, int tid, int threads) {
+  for (int i = tid; i < out.k; i += threads) {
+    const float z = key_value(static_cast<uint32_t>(top[i] >> 32));
+    out.top_logp[n * out.k + i] = r.mx == -INFINITY ? -INFINITY : (z - r.mx) * in.inv_tau - log_s;
+    out.top_ids[n * out.k + i] = cand_index(top[i]);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ Groups groups_of(const Row<T>& row, int vec_shift) {
+  const int64_t vectors = (row.end + Elem<T>::kVec - 1) / Elem<T>::kVec;
+  return Groups{vec_shift, static_cast<int>((vectors + (int64_t(1) << vec_shift) - 1) >> vec_shift)};
+}
+
+template <typename T>
+__device__ __forceinline__ int blocks_of(const Row<T>& row) {
+  return static_cast<int>((row.end + 32 * Elem<T>::kVec - 1) / (32 * Elem<T>::kVec));
+}
+
+template <int kWarps, bool kTop>
+struct Shared {
+  Sums warp_sums[kWarps];
+  Sums cta_sums[kMaxSplit];                   // in the first CTA of a cluster: every CTA's
+  alignas(16) uint32_t group_key[kTop ? kMaxGroups : 1];  // in the first CTA: the whole row's
+  Choice<kTop ? kWarps : 1> choice;
+};
+
+// A cluster of S CTAs takes a row at a time, each CTA `span` consecutive blocks of it (a multiple of 4, so that a
+// warp's loads never reach into the next CTA's words); the first CTA joins the results.
+template <typename T, int kWarps, bool kTop>
+__global__ void __launch_bounds__(kWarps * 32, 32 / kWarps)
+token_logprobs_kernel(const TokenRows in, const TokenOut out, int span, int vec_shift) {
+  __shared__ Shared<kWarps, kTop> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t S = 1, q = 0;
   if (kWarps > 1) {
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(S));
     q = cluster_ctarank();
   }
-  const int group_blocks = vec_shift > 5 ? 1 << (vec_shift - 5) : 1;
-  const int run = max(kBatch, group_blocks);  // consecutive blocks of one warp
   // Between an arrive and its wait the first CTA's shared memory is not written by the others: it may not
   // have started yet, or still be reading the previous row's.
   if (S > 1) cluster_arrive();
 
   for (int64_t n = blockIdx.x / S; n < in.N; n += gridDim.x / S) {
     const Row<T> row(in.z, n * in.ld, in.V);
-    const int all_blocks = static_cast<int>((row.end + kBlock - 1) / kBlock);
+    const int all_blocks = blocks_of(row);
     const int blk0 = min(all_blocks, static_cast<int>(q) * span), blk1 = min(all_blocks, blk0 + span);
-    Sums r{-INFINITY, 0.f, 0.f};
-    for (int b0 = blk0 + warp * run; b0 < blk1; b0 += kWarps * run) {
-      const int b1 = min(blk1, b0 + run);
-      float gm = -INFINITY;
-      for (int b = b0; b < b1; b += kBatch) {
-        const int64_t u0 = static_cast<int64_t>(b) * kBlock + lane * VE;
-        uint4 v[kBatch];
-        if (row.inside(static_cast<int64_t>(b) * kBlock, static_cast<int64_t>(b + kBatch) * kBlock)) {
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) v[i] = row.whole(u0 + i * kBlock);
-        } else {
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) v[i] = row.edge(u0 + i * kBlock);
-        }
-        float mx = r.mx;
-float bm[kBatch];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          bm[i] = Elem<T>::vec_max(v[i]);
-          mx = max_nan(mx, bm[i]);
-        }
-        if (kTop) {
-          if (vec_shift == 5) {  // a group is a block; lane i stores block i's
-            float mine = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-              const float m = warp_max_nan(bm[i]);
-              mine = lane == i ? m : mine;
-            }
-            if (lane < kBatch && b + lane < b1) sh.group_key[b + lane] = order_key(mine);
-          } else if (vec_shift < 5) {  // several groups per block
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-              float m = bm[i];
-              for (int off = 1; off < (1 << vec_shift); off <<= 1) m = max_nan(m, __shfl_xor_sync(~0u, m, off));
-              if (b + i < b1 && (lane & ((1 << vec_shift) - 1)) == 0)
-                sh.group_key[((b + i) << (5 - vec_shift)) + (lane >> vec_shift)] = order_key(m);
-            }
-          } else {  // a group is a run of batches of this warp
-            gm = max_nan(gm, max_nan(max_nan(bm[0], bm[1]), max_nan(bm[2], bm[3])));
-            if (((b + kBatch) & (group_blocks - 1)) == 0 || b + kBatch >= b1) {
-              const float m = warp_max_nan(gm);
-              if (lane == 0) sh.group_key[b >> (vec_shift - 5)] = order_key(m);
-              gm = -INFINITY;
-            }
-          }
-        }
-        rebase(r, mx, in.c);
-        const float m0 = base_of(mx);
-        float2 s = make_float2(0.f, 0.f), a = s;
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) fold<T>(v[i], m0, in.c, s, a);
-        r.s += s.x + s.y;
-        r.a += a.x + a.y;
-      }
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-      merge(r, Sums{__shfl_xor_sync(~0u, r.mx, off), __shfl_xor_sync(~0u, r.s, off), __shfl_xor_sync(~0u, r.a, off)}, in.c);
+    Sums r = stream_row<T, kWarps, kTop>(row, blk0, blk1, vec_shift, in.c, warp, lane, sh.group_key);
     if (kWarps > 1) {
       if (lane == 0) sh.warp_sums[warp] = r;
-      if (tid == 0) sh.count = sh.hits = 0;
       __syncthreads();
-      r = sh.warp_sums[0];
-      for (int w = 1; w < kWarps; ++w) merge(r, sh.warp_sums[w], in.c);  // every thread the same
-    } else {
-      if (tid == 0) sh.count = sh.hits = 0;
-      __syncthreads();
+      // every warp the same; lanes w, w + kWarps, ... take the same sums, so that all lanes end with the total
+      r = join_lanes(sh.warp_sums[lane & (kWarps - 1)], kWarps, in.c);
     }
     if (S > 1) {  // the first CTA of the cluster joins the others' sums and maxima
       cluster_wait();
@@ -607,35 +685,15 @@ float bm[kBatch];
           st_cluster_u32(mapa_shared(smem_u32(&sh.group_key[g]), 0), sh.group_key[g]);
       }
       cluster_sync_all();
-      if (q == 0) {
-        r = sh.cta_sums[0];
-        for (uint32_t c = 1; c < S; ++c) merge(r, sh.cta_sums[c], in.c);
-      }
+      if (q == 0) r = join_lanes(sh.cta_sums[lane & (S - 1)], static_cast<int>(S), in.c);
     }
     if (q == 0) {
       const float log_s = logf(r.s);
-      if (tid == 0) {
-        const int64_t t = in.tokens[n];
-        float lp = 0.f;
-        if (t >= in.V)
-          lp = __uint_as_float(0x7fffffffu);
-        else if (t >= 0)
-          lp = r.mx == -INFINITY ? -INFINITY : (Elem<T>::get(row.base[t + row.lead]) - r.mx) * in.inv_tau - log_s;
-        out.logp[n] = lp;
-        if (out.entropy) out.entropy[n] = r.mx == -INFINITY ? 0.f : log_s - kLn2F * r.a / r.s;
-        if (out.lse) out.lse[n] = r.mx == -INFINITY ? -INFINITY : r.mx * in.inv_tau + log_s;
-        if (out.stats) out.stats[n] = make_float2(r.mx, log_s);
-      }
-      if (kTop) {
-        const int64_t vectors = (row.end + VE - 1) / VE;
-        const Groups gr{vec_shift, static_cast<int>((vectors + (int64_t(1) << vec_shift) - 1) >> vec_shift)};
-        best_words<T>(sh, row, gr, out.k);
-        for (int i = tid; i < out.k; i += kWarps * 32) {
-          const uint64_t cd = sh.top[i];
-          const float z = key_value(static_cast<uint32_t>(cd >> 32));
-          out.top_logp[n * out.k + i] = r.mx == -INFINITY ? -INFINITY : (z - r.mx) * in.inv_tau - log_s;
-          out.top_ids[n * out.k + i] = cand_index(cd);
-        }
+      if (tid == 0) write_row(in, out, n, row, r, log_s);
+      if constexpr (kTop) {
+        __syncthreads();  // (one warp: its group maxima)
+        best_words<T>(sh.choice, sh.group_key, row, groups_of(row, vec_shift), out.k, tid);
+        write_top(in, out, n, sh.choice.top, r, log_s, tid, kWarps * 32);
       }
     }
     __syncthreads();  // this CTA's shared memory is free for the next row
@@ -644,17 +702,66 @@ float bm[kBatch];
   if (S > 1) cluster_wait();
 }
 
-constexpr int kBwdThreads = 256;
-constexpr int kBwdVecs = 4;  // vectors of a thread per piece
+// Many whole rows with alternatives: eight warps stream row after row and never wait for a selection; a ninth warp joins
+// each row's sums and chooses its alternatives while the next row streams. (8192 x 128256, 16 alternatives: with the eight
+// warps choosing between rows, 489 us; so, XXX us.)
+constexpr int kStreamWarps = 8;
+constexpr int kRowThreads = 32 * (kStreamWarps + 1);
 
-// A block takes pieces of kBwdThreads * kBwdVecs vectors, rows one after another.
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(int id, int threads) {
+  asm volatile("bar.arrive %0, %1;" :: "r"(id), "r"(threads) : "memory");
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads, 4)
+token_logprobs_rows_kernel(const TokenRows in, const TokenOut out, int vec_shift) {
+  __shared__ Sums warp_sums[2][kStreamWarps];
+  __shared__ uint32_t group_key[2][kMaxGroups];
+  __shared__ Choice<1> choice;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // Barriers 1, 2: buffer 0, 1 full; 3, 4: free again.
+  int buf = 0;
+  if (warp < kStreamWarps) {
+    bool first[2] = {true, true};
+    for (int64_t n = blockIdx.x; n < in.N; n += gridDim.x, buf ^= 1) {
+      const Row<T> row(in.z, n * in.ld, in.V);
+      if (!(buf == 0 ? first[0] : first[1])) bar_sync(3 + buf, kRowThreads);
+      (buf == 0 ? first[0] : first[1]) = false;
+      const Sums r = stream_row<T, kStreamWarps, true>(row, 0, blocks_of(row), vec_shift, in.c, warp, lane, group_key[buf]);
+      if (lane == 0) warp_sums[buf][warp] = r;
+      __threadfence_block();
+      bar_arrive(1 + buf, kRowThreads);
+    }
+  } else {
+    for (int64_t n = blockIdx.x; n < in.N; n += gridDim.x, buf ^= 1) {
+      const Row<T> row(in.z, n * in.ld, in.V);
+      bar_sync(1 + buf, kRowThreads);
+      const Sums r = join_lanes(warp_sums[buf][lane & (kStreamWarps - 1)], kStreamWarps, in.c);
+      const float log_s = logf(r.s);
+      if (lane == 0) write_row(in, out, n, row, r, log_s);
+      best_words<T>(choice, group_key[buf], row, groups_of(row, vec_shift), out.k, lane);
+      write_top(in, out, n, choice.top, r, log_s, lane, 32);
+      __syncwarp();
+      if (n + 2 * static_cast<int64_t>(gridDim.x) < in.N) bar_arrive(3 + buf, kRowThreads);  // someone waits for it
+    }
+  }
+}
+
+constexpr int kBwdThreads = 256;
+constexpr int kBwdVecs = 4;  // vectors a lane has in flight
+
+// A warp takes pieces of 32 * kBwdVecs vectors, rows one after another.
 template <typename T>
 __global__ void __launch_bounds__(kBwdThreads) token_logprobs_bwd_kernel(const TokenRows in, const TokenGrad g,
                                                                          int pieces) {
   constexpr int VE = Elem<T>::kVec;
-  constexpr int64_t kPiece = static_cast<int64_t>(kBwdThreads) * kBwdVecs * VE;
-  const int64_t total = static_cast<int64_t>(in.N) * pieces;
-  for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
+  constexpr int64_t kPiece = 32 * kBwdVecs * VE;
+  const int lane = threadIdx.x & 31;
+  const int64_t total = static_cast<int64_t>(in.N) * pieces, warps = static_cast<int64_t>(gridDim.x) * (kBwdThreads / 32);
+  for (int64_t w = static_cast<int64_t>(blockIdx.x) * (kBwdThreads / 32) + (threadIdx.x >> 5); w < total; w += warps) {
     const int64_t n = w / pieces;
     const int64_t u0 = (w - n * pieces) * kPiece;
     const Row<T> row(in.z, n * in.ld, in.V);
@@ -677,16 +784,16 @@ __global__ void __launch_bounds__(kBwdThreads) token_logprobs_bwd_kernel(const T
     uint4 v[kBwdVecs];
     if (row.inside(u0, u0 + kPiece)) {
 #pragma unroll
-      for (int i = 0; i < kBwdVecs; ++i) v[i] = row.template whole<true>(u0 + (i * kBwdThreads + threadIdx.x) * VE);
+      for (int i = 0; i < kBwdVecs; ++i) v[i] = row.template whole<true>(u0 + (i * 32 + lane) * VE);
     } else {
 #pragma unroll
-      for (int i = 0; i < kBwdVecs; ++i) v[i] = row.template edge<true>(u0 + (i * kBwdThreads + threadIdx.x) * VE);
+      for (int i = 0; i < kBwdVecs; ++i) v[i] = row.template edge<true>(u0 + (i * 32 + lane) * VE);
     }
     const float2 nm = make_float2(-m0, -m0), c2 = make_float2(in.c, in.c), nl = make_float2(-l2, -l2),
                  A2 = make_float2(A, A), B2 = make_float2(B, B);
 #pragma unroll
     for (int i = 0; i < kBwdVecs; ++i) {
-      const int64_t u = u0 + (i * kBwdThreads + threadIdx.x) * VE;
+      const int64_t u = u0 + (i * 32 + lane) * VE;
       float z[VE];
       Elem<T>::unpack(v[i], z);
 #pragma unroll
@@ -714,85 +821,131 @@ __global__ void __launch_bounds__(kBwdThreads) token_logprobs_bwd_kernel(const T
   }
 }
 
-// CTAs per row: a row is split until the rows' CTAs fill the device or a CTA has less than `kMinSpan` blocks.
-constexpr int kMinSpan = 32;
-int choose_split(int64_t N, int64_t blocks, int sms) {
-  int S = 1;
-  while (S < kMaxSplit && N * S * 2 <= 2 * sms && blocks / (2 * S) >= kMinSpan) S *= 2;
-  return S;
+// CTAs per row for the clusters of eight-warp CTAs: the power of two with the least
+// ceil(rows / clusters at once) * (a CTA's blocks + what a row costs beside its words, in blocks).
+int choose_split(int64_t N, int64_t blocks, int row_cost, const TokenOccupancy& occ) {
+  int best = 1;
+  int64_t best_cost = INT64_MAX;
+  for (int S = 1, i = 0; S <= kMaxSplit && (S == 1 || blocks / S >= 32); S *= 2, ++i) {
+    if (occ.clusters[i] < 1) continue;
+    const int64_t cost = (N + occ.clusters[i] - 1) / occ.clusters[i] * ((blocks + S - 1) / S + row_cost);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = S;
+    }
+  }
+  return best;
 }
 
-template <typename T, int kWarps, bool kTop>
-cudaError_t launch_rows(const TokenRows& in, const TokenOut& out, int S, int64_t blocks, int sms, cudaStream_t stream) {
-  int vec_shift = 0;  // the smallest groups that fit
-  while (((blocks * 32 + (int64_t(1) << vec_shift) - 1) >> vec_shift) > kMaxGroups) ++vec_shift;
-  if (vec_shift == 6) vec_shift = 7;  // runs of whole batches
-  const int64_t unit = vec_shift > 7 ? int64_t(1) << (vec_shift - 5) : 4;  // whole groups, whole warp loads
-  const int span = static_cast<int>(((blocks + S - 1) / S + unit - 1) / unit * unit);
-  const int64_t cap = static_cast<int64_t>(sms) * (32 / kWarps) / S;
-  const int64_t rows = in.N < cap ? in.N : cap;
-  cudaLaunchAttribute attr[1];
+cudaLaunchConfig_t split_config(cudaLaunchAttribute* attr, int S, int warps, int64_t rows, cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(S);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(rows * S), 1, 1);
-  cfg.blockDim = dim3(kWarps * 32, 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(warps * 32), 1, 1);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  return cfg;
+}
+
+template <typename T, int kWarps, bool kTop>
+cudaError_t launch_split(const TokenRows& in, const TokenOut& out, int S, int64_t at_once, int64_t blocks, int vec_shift,
+                         cudaStream_t stream) {
+  const int64_t unit = vec_shift > 7 ? int64_t(1) << (vec_shift - 5) : 4;  // whole groups, whole warp loads
+  const int span = static_cast<int>(((blocks + S - 1) / S + unit - 1) / unit * unit);
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = split_config(attr, S, kWarps, in.N < at_once ? in.N : at_once, stream);
   return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, kWarps, kTop>, in, out, span, vec_shift);
 }
 
-constexpr int kWideWarps = 8;
 constexpr int kShortRow = 16;  // blocks
 
+// What a row costs beside its words, in blocks of streaming (about 76 clocks each on a busy SM): the joins, and the
+// selection of alternatives.
+constexpr int kJoinCost = 40, kTopCost = 200;
+
 template <typename T, bool kTop>
-cudaError_t launch_fwd(const TokenRows& in, const TokenOut& out, int sms, cudaStream_t stream) {
+cudaError_t launch_fwd(const TokenRows& in, const TokenOut& out, const TokenOccupancy& occ, cudaStream_t stream) {
   constexpr int VE = Elem<T>::kVec;
   const int64_t blocks = (static_cast<int64_t>(in.V) + VE - 1 + 32 * VE - 1) / (32 * VE);
-  if (blocks <= kShortRow && in.N >= 4 * sms) return launch_rows<T, 1, kTop>(in, out, 1, blocks, sms, stream);
-  return launch_rows<T, kWideWarps, kTop>(in, out, choose_split(in.N, blocks, sms), blocks, sms, stream);
+  int vec_shift = 0;  // the smallest groups that fit
+  while (((blocks * 32 + (int64_t(1) << vec_shift) - 1) >> vec_shift) > kMaxGroups) ++vec_shift;
+  if (blocks <= kShortRow && in.N >= 4 * occ.sms)
+    return launch_split<T, 1, kTop>(in, out, 1, 32 * occ.sms, blocks, vec_shift, stream);
+  const int S = choose_split(in.N, blocks, kTop ? kTopCost : kJoinCost, occ);
+  const int whole = 4 * occ.sms;  // CTAs at once that take whole rows
+  if (kTop && in.N > whole) {
+    // whole rows, their alternatives chosen beside the streaming: a row costs its words alone
+    int i = 0;
+    while ((1 << i) < S) ++i;
+    const int64_t split_cost = (in.N + occ.clusters[i] - 1) / occ.clusters[i] * ((blocks + S - 1) / S + kTopCost);
+    if ((in.N + whole - 1) / whole * blocks + kTopCost <= split_cost) {
+      token_logprobs_rows_kernel<T><<<whole, kRowThreads, 0, stream>>>(in, out, vec_shift);
+      return cudaGetLastError();
+    }
+  }
+  int i = 0;
+  while ((1 << i) < S) ++i;
+  return launch_split<T, kStreamWarps, kTop>(in, out, S, occ.clusters[i], blocks, vec_shift, stream);
 }
 
 template <typename T>
 cudaError_t launch_bwd(const TokenRows& in, const TokenGrad& g, int sms, cudaStream_t stream) {
-  const int64_t piece = static_cast<int64_t>(kBwdThreads) * kBwdVecs * Elem<T>::kVec;
+  const int64_t piece = 32 * kBwdVecs * Elem<T>::kVec;
   const int64_t pieces = (static_cast<int64_t>(in.V) + Elem<T>::kVec - 1 + piece - 1) / piece;
-  const int64_t total = pieces * in.N, cap = static_cast<int64_t>(sms) * 64;
+  const int64_t total = (pieces * in.N + kBwdThreads / 32 - 1) / (kBwdThreads / 32), cap = static_cast<int64_t>(sms) * 64;
   token_logprobs_bwd_kernel<T>
       <<<static_cast<int>(total < cap ? total : cap), kBwdThreads, 0, stream>>>(in, g, static_cast<int>(pieces));
   return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t launch_fwd_any(const TokenRows& in, const TokenOut& out, int sms, cudaStream_t stream) {
-  return out.k > 0 ? launch_fwd<T, true>(in, out, sms, stream) : launch_fwd<T, false>(in, out, sms, stream);
+cudaError_t launch_fwd_any(const TokenRows& in, const TokenOut& out, const TokenOccupancy& occ, cudaStream_t stream) {
+  return out.k > 0 ? launch_fwd<T, true>(in, out, occ, stream) : launch_fwd<T, false>(in, out, occ, stream);
+}
+
+template <typename T, bool kTop>
+cudaError_t prepare_one(TokenOccupancy* occ) {
+  cudaError_t e =
+      cudaFuncSetAttribute(token_logprobs_kernel<T, kStreamWarps, kTop>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  for (int S = 1, i = 0; e == cudaSuccess && S <= kMaxSplit; S *= 2, ++i) {
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = split_config(attr, S, kStreamWarps, 1, nullptr);
+    int n = 0;
+    if ((e = cudaOccupancyMaxActiveClusters(&n, token_logprobs_kernel<T, kStreamWarps, kTop>, &cfg)) != cudaSuccess) break;
+    n = n < 4 * occ->sms / S ? n : 4 * occ->sms / S;  // more per SM than the four planned for shares the same memory
+    if (n < occ->clusters[i]) occ->clusters[i] = n;
+  }
+  return e;
 }
 
 template <typename T>
-cudaError_t prepare() {
-  const cudaError_t e =
-      cudaFuncSetAttribute(token_logprobs_kernel<T, kWideWarps, true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(token_logprobs_kernel<T, kWideWarps, false>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+cudaError_t prepare(TokenOccupancy* occ) {
+  const cudaError_t e = prepare_one<T, true>(occ);
+  return e == cudaSuccess ? prepare_one<T, false>(occ) : e;
 }
 
 }  // namespace
 
-cudaError_t token_logprobs_prepare() {
-  cudaError_t e = prepare<float>();
-  if (e == cudaSuccess) e = prepare<__nv_bfloat16>();
-  if (e == cudaSuccess) e = prepare<__half>();
+cudaError_t token_logprobs_prepare(int sms, TokenOccupancy* occ) {
+  occ->sms = sms;
+  for (int& c : occ->clusters) c = 1 << 30;
+  cudaError_t e = prepare<float>(occ);
+  if (e == cudaSuccess) e = prepare<__nv_bfloat16>(occ);
+  if (e == cudaSuccess) e = prepare<__half>(occ);
+  if (e == cudaSuccess && occ->clusters[0] < 1) e = cudaErrorInvalidConfiguration;
   return e;
 }
 
-cudaError_t launch_token_logprobs(const TokenRows& in, const TokenOut& out, int dtype, int sms, cudaStream_t stream) {
+cudaError_t launch_token_logprobs(const TokenRows& in, const TokenOut& out, int dtype, const TokenOccupancy& occ,
+                                  cudaStream_t stream) {
   switch (dtype) {
-    case HYLO_F32: return launch_fwd_any<float>(in, out, sms, stream);
-    case HYLO_BF16: return launch_fwd_any<__nv_bfloat16>(in, out, sms, stream);
-    default: return launch_fwd_any<__half>(in, out, sms, stream);
+    case HYLO_F32: return launch_fwd_any<float>(in, out, occ, stream);
+    case HYLO_BF16: return launch_fwd_any<__nv_bfloat16>(in, out, occ, stream);
+    default: return launch_fwd_any<__half>(in, out, occ, stream);
   }
 }
 
