@@ -4,6 +4,9 @@
 and the LM head and never stores the logits. Log-probabilities and entropies of both are
 differentiable. They run in the sm_103a kernels of libhylo_kl.so through the C ABI
 (include/hylo_ops.h); PyTorch only allocates the outputs and the workspace.
+
+A decoding loop calls these once per token, so each tensor is looked at once and the C entry points are
+called directly (the functions of the same names in ``_lib`` check their arguments a second time).
 """
 from __future__ import annotations
 
@@ -12,6 +15,9 @@ from typing import NamedTuple, Tuple
 import torch
 
 from . import _lib
+from ._lib import _check, current_raw_stream, load
+
+_empty, _f32 = torch.empty, torch.float32
 
 
 class TokenLogprobs(NamedTuple):
@@ -19,6 +25,21 @@ class TokenLogprobs(NamedTuple):
     entropy: torch.Tensor       # [...]: entropy of each distribution, in nats
     top_logprobs: torch.Tensor  # [..., top_k], largest first
     top_tokens: torch.Tensor    # [..., top_k] int64; equal logits: lowest token first
+
+
+def _on_device(*tensors: torch.Tensor) -> int:
+    """The current CUDA device, which must be that of every tensor."""
+    if not tensors[0].is_cuda:
+        raise ValueError("the tensors must be CUDA tensors")
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t.get_device() != dev:
+            raise ValueError(f"every tensor must be on the current CUDA device ({dev})")
+    return dev
+
+
+def _row_stride(z: torch.Tensor) -> int:
+    return z.stride(0) if z.shape[0] > 1 else max(z.shape[1], z.stride(0))
 
 
 def _rows(z: torch.Tensor) -> torch.Tensor:
@@ -38,41 +59,55 @@ def _grad_rows(z: torch.Tensor) -> torch.Tensor:
     lead = z.data_ptr() % 16 // z.element_size()
     ld = V + (z.stride(0) - V) % unit if N > 1 else V
     if lead == 0 and ld == V:
-        return torch.empty(N, V, dtype=z.dtype, device=z.device)
-    buf = torch.empty(lead + N * ld, dtype=z.dtype, device=z.device)
+        return _empty((N, V), dtype=z.dtype, device=z.device)
+    buf = _empty(lead + N * ld, dtype=z.dtype, device=z.device)
     return buf.as_strided((N, V), (ld, 1), lead)
 
 
-def _forward(z, tokens, tau, k, train):
-    N = z.shape[0]
-    f = dict(dtype=torch.float32, device=z.device)
-    logp, entropy = torch.empty(N, **f), torch.empty(N, **f)
-    stats = torch.empty(N, 2, **f) if train else None
-    top = torch.empty(N, k, **f)
-    ids = torch.empty(N, k, dtype=torch.int64, device=z.device)
+def _forward(z, tokens, tau, k, dev, train):
+    N, V = z.shape
+    device = z.device
+    logp, entropy = _empty(N, dtype=_f32, device=device), _empty(N, dtype=_f32, device=device)
+    stats = _empty((N, 2), dtype=_f32, device=device) if train else None
+    top, ids = _empty((N, k), dtype=_f32, device=device), _empty((N, k), dtype=torch.int64, device=device)
     if N > 0:
-        _lib.hylo_token_logprobs(z, tokens, tau, k, logp, entropy, None, stats, top, ids)
+        _check(load().hylo_token_logprobs(
+            z.data_ptr(), _lib.DTYPES[z.dtype], N, V, _row_stride(z), tau, tokens.data_ptr(), k, logp.data_ptr(),
+            entropy.data_ptr(), None, stats.data_ptr() if train else None, top.data_ptr(), ids.data_ptr(),
+            current_raw_stream(dev)))
     return logp, entropy, top, ids, stats
+
+
+def _upstream(g):
+    return None if g is None else g.to(_f32).contiguous()
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 class _TokenLogprobs(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, z, tokens, tau, k):
-        logp, entropy, top, ids, stats = _forward(z, tokens, tau, k, True)
+    def forward(ctx, z, tokens, tau, k, dev, alternatives):
+        logp, entropy, top, ids, stats = _forward(z, tokens, tau, k, dev, True)
+        alternatives += (top, ids)  # not differentiable
         ctx.save_for_backward(z, tokens, stats, entropy)
         ctx.tau = tau
-        ctx.mark_non_differentiable(top, ids)
         ctx.set_materialize_grads(False)
-        return logp, entropy, top, ids
+        return logp, entropy
 
     @staticmethod
-    def backward(ctx, g_logp, g_entropy, _top, _ids):
+    def backward(ctx, g_logp, g_entropy):
         z, tokens, stats, entropy = ctx.saved_tensors
         dz = _grad_rows(z)
-        if z.shape[0] > 0:
-            g_logp, g_entropy = (None if g is None else g.float().contiguous() for g in (g_logp, g_entropy))
-            _lib.hylo_token_logprobs_backward(z, tokens, ctx.tau, stats, entropy, g_logp, g_entropy, dz)
-        return dz, None, None, None
+        N, V = z.shape
+        if N > 0:
+            g_logp, g_entropy = _upstream(g_logp), _upstream(g_entropy)
+            _check(load().hylo_token_logprobs_backward(
+                z.data_ptr(), _lib.DTYPES[z.dtype], N, V, _row_stride(z), ctx.tau, tokens.data_ptr(), stats.data_ptr(),
+                entropy.data_ptr(), _ptr(g_logp), _ptr(g_entropy), dz.data_ptr(), _row_stride(dz),
+                current_raw_stream(z.get_device())))
+        return dz, None, None, None, None, None
 
 
 def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, tau: float = 1.0, top_k: int = 0) -> TokenLogprobs:
@@ -82,46 +117,51 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, tau: float = 1.0,
     logits may have any strides; rows with unit column stride are read in place. A negative token is
     ignored (log-probability 0, no gradient); -inf logits are masked words. logprobs and entropy
     are differentiable with respect to logits (gradient in the logits' dtype)."""
-    if logits.dtype not in _lib.DTYPES or logits.dim() < 1 or logits.shape[-1] < 1:
+    shape = logits.shape
+    if logits.dtype not in _lib.DTYPES or not shape or shape[-1] < 1:
         raise ValueError("logits must be float32, bfloat16 or float16 with a last dimension of at least one word")
-    if tokens.dtype != torch.int64 or tokens.shape != logits.shape[:-1]:
+    if tokens.dtype != torch.int64 or tokens.shape != shape[:-1]:
         raise ValueError("tokens must be int64 with the shape of logits without its last dimension")
-    if not 0 <= top_k <= min(_lib.TOP_MAX, logits.shape[-1]):
+    if not 0 <= top_k <= min(_lib.TOP_MAX, shape[-1]):
         raise ValueError(f"top_k must be in [0, min(V, {_lib.TOP_MAX})]")
-    z, t = _rows(logits), tokens.reshape(-1).contiguous()
-    if torch.is_grad_enabled() and logits.requires_grad:
-        r = _TokenLogprobs.apply(z, t, float(tau), int(top_k))
+    dev = _on_device(logits, tokens)
+    plain = len(shape) == 2
+    z, t = _rows(logits), (tokens if plain else tokens.reshape(-1)).contiguous()
+    if logits.requires_grad and torch.is_grad_enabled():
+        alternatives = []
+        logp, entropy = _TokenLogprobs.apply(z, t, float(tau), int(top_k), dev, alternatives)
+        top, ids = alternatives
     else:
-        r = _forward(z, t, float(tau), int(top_k), False)
-    logp, entropy, top, ids = r[:4]
-    if tokens.dim() != 1:
+        logp, entropy, top, ids, _ = _forward(z, t, float(tau), int(top_k), dev, False)
+    if not plain:
         logp, entropy = logp.view(tokens.shape), entropy.view(tokens.shape)
         top, ids = top.view(*tokens.shape, top_k), ids.view(*tokens.shape, top_k)
     return TokenLogprobs(logp, entropy, top, ids)
 
 
-def _workspace(h, W, token_chunk, split_g):
-    N, d = h.shape
-    n = _lib.hylo_head_logprobs_workspace_bytes(N, d, W.shape[0], token_chunk, split_g)
+def _workspace(N, d, V, token_chunk, split_g, device):
+    n = load().hylo_head_logprobs_workspace_bytes(N, d, V, token_chunk, int(split_g))
     if n == 0:
         raise ValueError("invalid sizes (the hidden size must be a multiple of 8 in 8..65536)")
-    return torch.empty(n, dtype=torch.uint8, device=h.device)  # from the caching allocator of the current stream
+    return _empty(n, dtype=torch.uint8, device=device), n  # from the caching allocator of the current stream
 
 
-def _head_forward(h, W, tokens, tau, train):
-    N = h.shape[0]
-    f = dict(dtype=torch.float32, device=h.device)
-    logp, entropy = torch.empty(N, **f), torch.empty(N, **f)
-    lse = torch.empty(N, **f) if train else None
+def _head_forward(h, W, tokens, tau, dev, train):
+    (N, d), V = h.shape, W.shape[0]
+    device = h.device
+    logp, entropy = _empty(N, dtype=_f32, device=device), _empty(N, dtype=_f32, device=device)
+    lse = _empty(N, dtype=_f32, device=device) if train else None
     if N > 0:
-        _lib.hylo_head_logprobs(h, W, tokens, tau, logp, entropy, lse, _workspace(h, W, 0, False))
+        ws, n = _workspace(N, d, V, 0, False, device)
+        _check(load().hylo_head_logprobs(h.data_ptr(), W.data_ptr(), N, d, V, tau, tokens.data_ptr(), logp.data_ptr(),
+                                         entropy.data_ptr(), _ptr(lse), ws.data_ptr(), n, current_raw_stream(dev)))
     return logp, entropy, lse
 
 
 class _HeadLogprobs(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, h, W, tokens, tau, token_chunk, split_g):
-        logp, entropy, lse = _head_forward(h, W, tokens, tau, True)
+    def forward(ctx, h, W, tokens, tau, token_chunk, split_g, dev):
+        logp, entropy, lse = _head_forward(h, W, tokens, tau, dev, True)
         ctx.save_for_backward(h, W, tokens, lse, entropy)
         ctx.args = (tau, token_chunk, split_g)
         ctx.set_materialize_grads(False)
@@ -131,15 +171,18 @@ class _HeadLogprobs(torch.autograd.Function):
     def backward(ctx, g_logp, g_entropy):
         h, W, tokens, lse, entropy = ctx.saved_tensors
         tau, token_chunk, split_g = ctx.args
-        if h.shape[0] == 0:
-            return torch.zeros_like(h), torch.zeros_like(W), None, None, None, None
-        f = dict(dtype=torch.float32, device=h.device)
-        dh, dW = torch.empty(h.shape, **f), torch.empty(W.shape, **f)
-        g_logp, g_entropy = (None if g is None else g.float().contiguous() for g in (g_logp, g_entropy))
-        _lib.hylo_head_logprobs_backward(h, W, tokens, tau, token_chunk, lse, entropy, g_logp, g_entropy, dh, dW,
-                                         _workspace(h, W, token_chunk, split_g), split_g)
+        (N, d), V = h.shape, W.shape[0]
+        if N == 0:
+            return torch.zeros_like(h), torch.zeros_like(W), None, None, None, None, None
+        dh, dW = _empty((N, d), dtype=_f32, device=h.device), _empty((V, d), dtype=_f32, device=h.device)
+        g_logp, g_entropy = _upstream(g_logp), _upstream(g_entropy)
+        ws, n = _workspace(N, d, V, token_chunk, split_g, h.device)
+        _check(load().hylo_head_logprobs_backward(
+            h.data_ptr(), W.data_ptr(), N, d, V, tau, token_chunk, tokens.data_ptr(), lse.data_ptr(), entropy.data_ptr(),
+            _ptr(g_logp), _ptr(g_entropy), int(split_g), dh.data_ptr(), dW.data_ptr(), ws.data_ptr(), n,
+            current_raw_stream(h.get_device())))
         return (dh.to(h.dtype) if ctx.needs_input_grad[0] else None, dW.to(W.dtype) if ctx.needs_input_grad[1] else None,
-                None, None, None, None)
+                None, None, None, None, None)
 
 
 def head_logprobs(h: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, tau: float = 1.0, token_chunk: int = 4096,
@@ -151,13 +194,17 @@ def head_logprobs(h: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, tau: f
     with respect to h and W (bfloat16 gradients; the C ABI gives fp32). token_chunk and split_g as in
     fused_hidden_state_kl: the backward's token block, and whether the gradient of the logits is
     kept to 16 bits of precision instead of 8 inside the gradient products."""
-    if h.dtype != torch.bfloat16 or W.dtype != torch.bfloat16 or h.dim() < 1 or W.dim() != 2 or h.shape[-1] != W.shape[1]:
+    shape = h.shape
+    if h.dtype != torch.bfloat16 or W.dtype != torch.bfloat16 or not shape or W.dim() != 2 or shape[-1] != W.shape[1]:
         raise ValueError("h [..., d] and W [V, d] must be bfloat16 with the same hidden size")
-    if tokens.dtype != torch.int64 or tokens.shape != h.shape[:-1]:
+    if tokens.dtype != torch.int64 or tokens.shape != shape[:-1]:
         raise ValueError("tokens must be int64 with the shape of h without its last dimension")
-    hh, WW, t = h.reshape(-1, h.shape[-1]).contiguous(), W.contiguous(), tokens.reshape(-1).contiguous()
-    if torch.is_grad_enabled() and (h.requires_grad or W.requires_grad):
-        logp, entropy = _HeadLogprobs.apply(hh, WW, t, float(tau), int(token_chunk), bool(split_g))
+    dev = _on_device(h, W, tokens)
+    plain = len(shape) == 2
+    hh, t = (h, tokens) if plain else (h.reshape(-1, shape[-1]), tokens.reshape(-1))
+    hh, WW, t = hh.contiguous(), W.contiguous(), t.contiguous()
+    if (h.requires_grad or W.requires_grad) and torch.is_grad_enabled():
+        logp, entropy = _HeadLogprobs.apply(hh, WW, t, float(tau), int(token_chunk), bool(split_g), dev)
     else:
-        logp, entropy, _ = _head_forward(hh, WW, t, float(tau), False)
-    return logp.view(tokens.shape), entropy.view(tokens.shape)
+        logp, entropy, _ = _head_forward(hh, WW, t, float(tau), dev, False)
+    return (logp, entropy) if plain else (logp.view(tokens.shape), entropy.view(tokens.shape))

@@ -34,13 +34,16 @@ class State8(NamedTuple):
         return q * torch.exp2(self.exponents.float()).repeat_interleave(BLOCK)[: q.numel()]
 
 
-def _check_list(name: str, tensors: Sequence[torch.Tensor], dtypes, device, sizes=None) -> None:
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _check_list(name: str, tensors: Sequence[torch.Tensor], dtypes, device: int, counts=None) -> None:
     for i, t in enumerate(tensors):
         if t.dtype not in dtypes or not t.is_contiguous() or t.get_device() != device:
             raise ValueError(f"{name}[{i}] must be a contiguous {' or '.join(map(str, dtypes))} tensor on the current "
                              f"CUDA device")
-        if sizes is not None and t.numel() != sizes[i]:
-            raise ValueError(f"{name}[{i}] has {t.numel()} elements instead of {sizes[i]}")
+    if counts is not None and [t.numel() for t in tensors] != counts:
+        raise ValueError(f"{name} must have the element counts {counts}")
 
 
 def grad_norm(grads: Iterable[torch.Tensor]) -> torch.Tensor:
@@ -52,17 +55,30 @@ def grad_norm(grads: Iterable[torch.Tensor]) -> torch.Tensor:
     if dtype not in (torch.float32, torch.bfloat16) or not grads[0].is_cuda:
         raise ValueError("gradients must be float32 or bfloat16 CUDA tensors")
     _check_list("grads", grads, (dtype,), torch.cuda.current_device())
-    norm = torch.empty(1, dtype=torch.float32, device=grads[0].device)
-    ws = torch.empty(_lib.hylo_grad_norm_workspace_bytes(), dtype=torch.uint8, device=norm.device)
-    _lib.hylo_grad_norm([g.data_ptr() for g in grads], [g.numel() for g in grads], dtype, norm, ws)
+    device = grads[0].device
+    norm = torch.empty(1, dtype=torch.float32, device=device)
+    ws = torch.empty(_norm_workspace(), dtype=torch.uint8, device=device)
+    _lib.hylo_grad_norm([g.data_ptr() for g in grads], [g.numel() for g in grads], dtype, norm, ws,
+                        _lib.current_raw_stream(device.index))
     return norm
 
 
-def _per_tensor(x, n: int) -> List[float]:
-    x = list(x) if isinstance(x, (list, tuple)) else [x] * n
+_norm_bytes = 0
+
+
+def _norm_workspace() -> int:
+    global _norm_bytes
+    if _norm_bytes == 0:
+        _norm_bytes = _lib.hylo_grad_norm_workspace_bytes()
+    return _norm_bytes
+
+
+def _per_tensor(x, n: int) -> Sequence[float]:
+    if not isinstance(x, (list, tuple)):
+        return [float(x)] * n
     if len(x) != n:
         raise ValueError("lr and weight_decay are numbers, or lists with one number per tensor")
-    return [float(v) for v in x]
+    return x
 
 
 Moments = Sequence[Union[torch.Tensor, State8]]
@@ -93,41 +109,37 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
     for name, dt in (("params", pdt), ("grads", gdt)):
         if dt not in (torch.float32, torch.bfloat16):
             raise ValueError(f"{name} must be float32 or bfloat16")
-    sizes = [p.numel() for p in params]
-    _check_list("params", params, (pdt,), dev)
-    _check_list("grads", grads, (gdt,), dev, sizes)
-    if masters is not None:
-        if pdt != torch.bfloat16:
-            raise ValueError("masters go with bfloat16 params")
-        _check_list("masters", masters, (torch.float32,), dev, sizes)
-    bits = 8 if isinstance(exp_avgs[0], State8) else 32
-    none = [0] * n
-    exps = (none, none)
-    if bits == 8:
-        if not all(isinstance(s, State8) for s in (*exp_avgs, *exp_avg_sqs)):
-            raise ValueError("exp_avgs and exp_avg_sqs must be State8 throughout, or tensors throughout")
-        blocks = [-(-k // BLOCK) for k in sizes]
-        codes = []
-        for name, states in (("exp_avgs", exp_avgs), ("exp_avg_sqs", exp_avg_sqs)):
-            codes.append([s.codes for s in states])
-            _check_list(name + ".codes", codes[-1], (torch.float8_e4m3fn, torch.uint8), dev, sizes)
-            _check_list(name + ".exponents", [s.exponents for s in states], (torch.int8,), dev, blocks)
-        exps = tuple([s.exponents.data_ptr() for s in states] for states in (exp_avgs, exp_avg_sqs))
-        m, v = codes
-    else:
-        m, v = exp_avgs, exp_avg_sqs
-        if any(isinstance(s, State8) for s in (*m, *v)):
-            raise ValueError("exp_avgs and exp_avg_sqs must be State8 throughout, or tensors throughout")
-        _check_list("exp_avgs", m, (torch.float32,), dev, sizes)
-        _check_list("exp_avg_sqs", v, (torch.float32,), dev, sizes)
+    if masters is not None and pdt != torch.bfloat16:
+        raise ValueError("masters go with bfloat16 params")
     if norm is not None and (norm.dtype != torch.float32 or norm.numel() != 1 or norm.get_device() != dev):
         raise ValueError("norm must be one float32 value on the current CUDA device")
+    bits = 8 if isinstance(exp_avgs[0], State8) else 32
+    if any(isinstance(s, State8) != (bits == 8) for s in (*exp_avgs, *exp_avg_sqs)):
+        raise ValueError("exp_avgs and exp_avg_sqs must be State8 throughout, or tensors throughout")
+    m, v = exp_avgs, exp_avg_sqs
+    sizes = [p.numel() for p in params]
+    none = [0] * n
+    exps = (none, none)
+    lists = [("params", params, (pdt,), sizes), ("grads", grads, (gdt,), sizes)]
+    if bits == 8:
+        blocks = [-(-k // BLOCK) for k in sizes]
+        for name, states in (("exp_avgs", m), ("exp_avg_sqs", v)):
+            lists += [(name + ".codes", [s.codes for s in states], _CODES, sizes),
+                      (name + ".exponents", [s.exponents for s in states], (torch.int8,), blocks)]
+        exps = tuple([s.exponents.data_ptr() for s in states] for states in (m, v))
+        m, v = [s.codes for s in m], [s.codes for s in v]
+    else:
+        lists += [("exp_avgs", m, (torch.float32,), sizes), ("exp_avg_sqs", v, (torch.float32,), sizes)]
+    if masters is not None:
+        lists.append(("masters", masters, (torch.float32,), sizes))
+    for name, tensors, dtypes, counts in lists:
+        _check_list(name, tensors, dtypes, dev, counts)
     mast = none if masters is None else [t.data_ptr() for t in masters]
     columns = ([t.data_ptr() for t in params], [t.data_ptr() for t in grads], mast, [t.data_ptr() for t in m],
                [t.data_ptr() for t in v], *exps, sizes, _per_tensor(lr, n), _per_tensor(weight_decay, n))
     fields = [x for row in zip(*columns) for x in row]
-    _lib.hylo_adamw_step(fields, n, pdt, gdt, bits, betas, float(eps), int(step), float(grad_scale), norm,
-                         float(max_norm), int(seed))
+    _lib.hylo_adamw_step(fields, n, pdt, gdt, bits, betas, eps, int(step), grad_scale, norm, max_norm, int(seed),
+                         _lib.current_raw_stream(dev))
 
 
 class AdamW:
