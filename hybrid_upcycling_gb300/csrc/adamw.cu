@@ -10,6 +10,7 @@
 #include <cuda_fp16.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "hylo_ops_internal.h"
 #include "sm103_ptx.cuh"
@@ -42,6 +43,7 @@ template <int CAP>
 struct AdamTable {
   AdamTensor t[CAP];
   int count;
+  int steps;  // 8-bit states: blocks of 256 elements that a warp takes one after another
 };
 constexpr int kSmallTable = 32;
 constexpr int kLargeTable = 320;
@@ -107,72 +109,6 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, int64_t i, int left, bo
   }
 }
 
-// ---- 8-bit states: e4m3 codes with one power of two per block
-__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
-
-__device__ __forceinline__ float2 decode2(uint32_t two) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
-__device__ __forceinline__ uint32_t encode2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-__device__ __forceinline__ void load_codes(const uint8_t* p, int64_t i, int left, bool vec, float scale, float* z) {
-  uint2 w = make_uint2(0u, 0u);
-  if (vec && left >= 8) {
-    w = *reinterpret_cast<const uint2*>(p + i);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t b = j < left ? p[i + j] : 0u;
-      if (j < 4)
-        w.x |= b << (8 * j);
-      else
-        w.y |= b << (8 * (j - 4));
-    }
-  }
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const uint32_t two = ((q < 2 ? w.x : w.y) >> (16 * (q & 1))) & 0xffffu;
-    const float2 f = decode2(two);
-    z[2 * q] = f.x * scale;
-    z[2 * q + 1] = f.y * scale;
-  }
-}
-
-// The block's exponent: its largest magnitude (bit pattern `top`) lies in [128, 256) 2^e.
-__device__ __forceinline__ int block_exponent(uint32_t top) {
-  return min(120, max(-120, static_cast<int>(top >> 23) - 127 - 7));
-}
-
-// |x| 2^-e rounded to an e4m3 value: the bits below the three of the mantissa are cut off after
-// adding `random` (20 bits) to them. Magnitudes under 2^-6 (codes of a fixed step 2^-9) take the
-// same steps once 2^-6 is added.
-__device__ __forceinline__ float round_code(float x, float inv_scale, uint32_t random, bool keep) {
-  const float a = fabsf(x) * inv_scale;
-  const float low = a < 0.015625f ? 0.015625f : 0.f;
-  float q = __uint_as_float((__float_as_uint(a + low) + random) & 0xfff00000u) - low;
-  if (keep && a > 0.f) q = fmaxf(q, 0.001953125f);
-  return copysignf(q, x);
-}
-
-__device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int left, bool vec, const float* q) {
-  uint32_t w[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) w[k] = encode2(q[2 * k], q[2 * k + 1]);
-  if (vec && left >= 8) {
-    *reinterpret_cast<uint2*>(p + i) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < left) p[i + j] = static_cast<uint8_t>(w[j >> 1] >> (8 * (j & 1)));
-  }
-}
-
 // The entry whose blocks include block `b` (entries ascend by chunk0).
 template <typename Table>
 __device__ __forceinline__ int find_entry(const Table& tab, uint32_t b) {
@@ -187,16 +123,36 @@ __device__ __forceinline__ int find_entry(const Table& tab, uint32_t b) {
   return lo;
 }
 
-// P, G: types of parameter and gradient; MASTER: the step is taken on fp32 masters; BITS8: 8-bit states.
-template <typename P, typename G, bool MASTER, bool BITS8, int CAP>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamTable<CAP> tab, const AdamWHyper h) {
-  constexpr bool kRandomParam = sizeof(P) == 2 && !MASTER;
-  float gs = h.grad_scale;
+// The factor on the gradients; false if the step is skipped.
+__device__ __forceinline__ bool gradient_factor(const AdamWHyper& h, float& gs) {
+  gs = h.grad_scale;
   if (h.norm != nullptr) {
     const float norm = h.norm[0];
-    if (!isfinite(norm)) return;
+    if (!isfinite(norm)) return false;
     gs *= fminf(1.f, h.max_norm / (norm * fabsf(h.grad_scale) + 1e-6f));
   }
+  return true;
+}
+
+// Random bits of eight consecutive positions from c on (a multiple of 8, so they share the high half).
+__device__ __forceinline__ void random8(uint32_t seed, uint64_t c, uint32_t (&bits)[8]) {
+  const uint32_t start = static_cast<uint32_t>(c) + mix32(seed + 0x9E3779B9u * (static_cast<uint32_t>(c >> 32) + 1u));
+#pragma unroll
+  for (int j = 0; j < 8; ++j) bits[j] = mix32(start + j);
+}
+
+// w rounded to bf16, up with the probability of the part cut off (w finite).
+__device__ __forceinline__ float round_bf16(float w, uint32_t bits) {
+  return __uint_as_float((__float_as_uint(w) + ((bits * 0x9E3779B1u) >> 16)) & 0xffff0000u);
+}
+
+// The step with fp32 moments. P, G: types of parameter and gradient; MASTER: the step is taken on fp32 masters.
+// HBM-bound: XXX.
+template <typename P, typename G, bool MASTER, int CAP>
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamTable<CAP> tab, const AdamWHyper h) {
+  constexpr bool kRandomParam = sizeof(P) == 2 && !MASTER;
+  float gs;
+  if (!gradient_factor(h, gs)) return;
   const AdamTensor& t = tab.t[find_entry(tab, blockIdx.x)];
   const int lane = threadIdx.x & 31;
   const int64_t b0 = (static_cast<int64_t>(blockIdx.x - t.chunk0) * kWarps + (threadIdx.x >> 5)) * kBlock;
@@ -210,63 +166,250 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     load8(t.master, i, left, vec, w);
   else
     load8(static_cast<const P*>(t.p), i, left, vec, w);
-  if (BITS8) {
-    load_codes(static_cast<const uint8_t*>(t.m), i, left, vec, pow2(t.me[b0 / kBlock]), m);
-    load_codes(static_cast<const uint8_t*>(t.v), i, left, vec, pow2(t.ve[b0 / kBlock]), v);
-  } else {
-    load8(static_cast<const float*>(t.m), i, left, vec, m);
-    load8(static_cast<const float*>(t.v), i, left, vec, v);
-  }
-  float mtop = 0.f, rtop = 0.f;
+  load8(static_cast<const float*>(t.m), i, left, vec, m);
+  load8(static_cast<const float*>(t.v), i, left, vec, v);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float gj = g[j] * gs;
     m[j] = fmaf(h.beta1, m[j], h.one_minus_beta1 * gj);
-    const float old = BITS8 ? v[j] * v[j] : v[j];
-    const float nv = fmaf(h.beta2, old, h.one_minus_beta2 * gj * gj);
-    const float r = sqrt_approx(nv);
-    w[j] = fmaf(w[j], t.decay, -t.step * __fdividef(m[j], fmaf(r, h.rbc2, h.eps)));
-    v[j] = BITS8 ? r : nv;
-    if (BITS8) {
-      mtop = fmaxf(mtop, fabsf(m[j]));
-      rtop = fmaxf(rtop, r);
+    v[j] = fmaf(h.beta2, v[j], h.one_minus_beta2 * gj * gj);
+    w[j] = fmaf(w[j], t.decay, -t.step * __fdividef(m[j], fmaf(sqrt_approx(v[j]), h.rbc2, h.eps)));
+  }
+  store8(static_cast<float*>(t.m), i, left, vec, m);
+  store8(static_cast<float*>(t.v), i, left, vec, v);
+  if (MASTER) store8(t.master, i, left, vec, w);
+  if (kRandomParam) {
+    uint32_t bits[8];
+    random8(h.seed, t.pos + static_cast<uint64_t>(i), bits);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (isfinite(w[j])) w[j] = round_bf16(w[j], bits[j]);
+  }
+  store8(static_cast<P*>(t.p), i, left, vec, w);
+}
+
+// ---- 8-bit states: e4m3 codes with one power of two per block
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
+
+__device__ __forceinline__ float2 decode2(uint32_t two) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// The block's exponent: its largest magnitude (bit pattern `top`) lies in [128, 256) 2^e.
+__device__ __forceinline__ int block_exponent(uint32_t top) {
+  return min(120, max(-120, static_cast<int>(top >> 23) - 127 - 7));
+}
+
+__device__ __forceinline__ float sqrt_ftz(float x) {
+  float r;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_ftz(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// Eight elements as they lie in memory.
+template <typename T>
+struct Raw8 {
+  uint4 q[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p, int64_t i, int left, bool vec) {
+    if (vec && left >= 8) {
+#pragma unroll
+      for (int k = 0; k < static_cast<int>(sizeof(T) / 2); ++k) q[k] = *reinterpret_cast<const uint4*>(p + i + k * (16 / sizeof(T)));
+    } else {
+      float z[8];
+      load8(p, i, left, false, z);
+      if constexpr (sizeof(T) == 4) {
+        q[0] = make_uint4(__float_as_uint(z[0]), __float_as_uint(z[1]), __float_as_uint(z[2]), __float_as_uint(z[3]));
+        q[1] = make_uint4(__float_as_uint(z[4]), __float_as_uint(z[5]), __float_as_uint(z[6]), __float_as_uint(z[7]));
+      } else {
+        q[0] = make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]), pack_bf16x2(z[4], z[5]), pack_bf16x2(z[6], z[7]));
+      }
     }
   }
-  uint32_t bits[8];
-  if (BITS8 || kRandomParam) {
-    const uint64_t c = t.pos + static_cast<uint64_t>(i);  // eight positions with the same high half
-    const uint32_t key = mix32(h.seed + 0x9E3779B9u * (static_cast<uint32_t>(c >> 32) + 1u));
-#pragma unroll
-    for (int j = 0; j < 8; ++j) bits[j] = mix32(static_cast<uint32_t>(c) + j + key);
+  __device__ __forceinline__ float2 pair(int j) const {  // elements 2 j, 2 j + 1
+    if constexpr (sizeof(T) == 4) {
+      const uint4 v = q[j >> 1];
+      return j & 1 ? make_float2(__uint_as_float(v.z), __uint_as_float(v.w)) : make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+    } else {
+      const uint32_t w = j == 0 ? q[0].x : j == 1 ? q[0].y : j == 2 ? q[0].z : q[0].w;
+      return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
   }
-  if (BITS8) {
+};
+
+__device__ __forceinline__ uint2 load_codes(const uint8_t* p, int64_t i, int left, bool vec) {
+  if (vec && left >= 8) return *reinterpret_cast<const uint2*>(p + i);
+  uint2 w = make_uint2(0u, 0u);
+  for (int j = 0; j < left; ++j) (j < 4 ? w.x : w.y) |= static_cast<uint32_t>(p[i + j]) << (8 * (j & 3));
+  return w;
+}
+__device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int left, bool vec, uint2 w) {
+  if (vec && left >= 8) {
+    *reinterpret_cast<uint2*>(p + i) = w;
+  } else {
+    for (int j = 0; j < left; ++j) p[i + j] = static_cast<uint8_t>((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
+  }
+}
+
+// The code of |y| (< 256), y = x 2^-e, in the top byte, rounded up with the probability of the part cut off. Times
+// 2^-120 the smallest normal code, 2^-6, becomes fp32's smallest normal number: the bits of |y| 2^-120 are
+// then the code's exponent and mantissa (bits 26..20) with 20 more below, for subnormal codes too. The random number,
+// 16 bits at `random` bits 23..8, goes to the upper 16 of those 20; times 16 the sign leaves the word at its
+// top, so that rounding is one multiply-add.
+__device__ __forceinline__ uint32_t round_code(float y120, uint32_t random) {
+  return __float_as_uint(y120) * 16u + random;
+}
+__device__ __forceinline__ uint32_t low_random(uint32_t bits) { return __byte_perm(bits, 0u, 0x4104); }   // low half << 8
+__device__ __forceinline__ uint32_t high_random(uint32_t bits) { return __byte_perm(bits, 0u, 0x4324); }  // high half << 8
+// The top bytes of four words.
+__device__ __forceinline__ uint32_t tops4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
+}
+
+// Blocks per warp: enough that a thread block's set-up (finding its tensor, the clip factor) is paid rarely, but no more
+// than leave every SM four thread blocks (200M bf16 elements without masters: 493 us with one, 433 with 4,
+// 404 with 16).
+constexpr int kMaxSteps8 = 16;
+
+// The step with 8-bit moments. Eight elements of a lane in packed fp32 pairs.
+// Bound by instructions, not by HBM: XXX.
+template <typename P, typename G, bool MASTER, int CAP>
+__global__ void __launch_bounds__(kThreads, 4) adamw8_kernel(const __grid_constant__ AdamTable<CAP> tab, const AdamWHyper h) {
+  using W = typename std::conditional<MASTER, float, P>::type;
+  constexpr bool kRandomParam = sizeof(P) == 2 && !MASTER;
+  float gs;
+  if (!gradient_factor(h, gs)) return;
+  const AdamTensor& t = tab.t[find_entry(tab, blockIdx.x)];
+  const int64_t chunk = static_cast<int64_t>(tab.steps) * (kWarps * kBlock);
+  const int lane = threadIdx.x & 31;
+  const bool vec = t.vec != 0;
+  const W* wp = MASTER ? reinterpret_cast<const W*>(t.master) : static_cast<const W*>(t.p);
+  uint8_t* mp = static_cast<uint8_t*>(t.m);
+  uint8_t* vp = static_cast<uint8_t*>(t.v);
+  const float gm = gs * h.one_minus_beta1, gv = gs * sqrtf(h.one_minus_beta2), rb2 = sqrtf(h.beta2);
+
+  struct Block {
+    Raw8<W> w;
+    Raw8<G> g;
+    uint2 m, v;
+    float sm, sv;  // the blocks' powers of two
+  };
+  auto load = [&](Block& b, int64_t b0) {
+    const int64_t i = b0 + lane * 8;
+    const int left = static_cast<int>(max(int64_t(0), min(int64_t(8), t.n - i)));
+    b.w.load(wp, i, left, vec);
+    b.g.load(static_cast<const G*>(t.g), i, left, vec);
+    b.m = load_codes(mp, i, left, vec);
+    b.v = load_codes(vp, i, left, vec);
+    b.sm = pow2(t.me[b0 / kBlock]);
+    b.sv = pow2(t.ve[b0 / kBlock]);
+  };
+  int64_t b0 = static_cast<int64_t>(blockIdx.x - t.chunk0) * chunk + (threadIdx.x >> 5) * kBlock;
+  if (b0 >= t.n) return;
+  const int64_t end = min(t.n, (static_cast<int64_t>(blockIdx.x - t.chunk0) + 1) * chunk);
+#pragma unroll 1
+  for (; b0 < end; b0 += kWarps * kBlock) {
+    Block cur;
+    load(cur, b0);
+    const int64_t i = b0 + lane * 8;
+    const int left = static_cast<int>(max(int64_t(0), min(int64_t(8), t.n - i)));
+    const float2 b1 = both(h.beta1 * cur.sm), b2 = both(rb2 * cur.sv);
+    float2 w[4], m[4], r[4];
+    float mtop = 0.f, rtop = 0.f;
+    float2 odd = make_float2(0.f, 0.f);  // NaN if a value is not finite
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t two = 16 * (j & 1);
+      const float2 g = cur.g.pair(j);
+      m[j] = __ffma2_rn(decode2((j < 2 ? cur.m.x : cur.m.y) >> two & 0xffffu), b1, __fmul2_rn(g, both(gm)));
+      const float2 ro = __fmul2_rn(decode2((j < 2 ? cur.v.x : cur.v.y) >> two & 0xffffu), b2), g2 = __fmul2_rn(g, both(gv));
+      const float2 v = __ffma2_rn(ro, ro, __fmul2_rn(g2, g2));
+      r[j] = make_float2(sqrt_ftz(v.x), sqrt_ftz(v.y));
+      const float2 den = __ffma2_rn(r[j], both(h.rbc2), both(h.eps));
+      const float2 u = __fmul2_rn(m[j], make_float2(rcp_ftz(den.x), rcp_ftz(den.y)));
+      w[j] = __ffma2_rn(u, both(-t.step), __fmul2_rn(cur.w.pair(j), both(t.decay)));
+      mtop = fmaxf(mtop, fmaxf(fabsf(m[j].x), fabsf(m[j].y)));
+      rtop = fmaxf(rtop, fmaxf(r[j].x, r[j].y));
+      odd = __ffma2_rn(w[j], make_float2(0.f, 0.f), odd);
+    }
     const int em = block_exponent(__reduce_max_sync(~0u, __float_as_uint(mtop)));
     const int er = block_exponent(__reduce_max_sync(~0u, __float_as_uint(rtop)));
-    const float im = pow2(-em), ir = pow2(-er);
+    const float2 im = both(pow2(-em)), ir = both(pow2(-er)), low = both(7.52316384526264e-37f);  // 2^-120
+    uint32_t bits[8];
+    random8(h.seed, t.pos + static_cast<uint64_t>(i), bits);
+    uint2 mc, rc;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      m[j] = round_code(m[j], im, (bits[j] << 4) & 0xffff0u, false);
-      v[j] = round_code(v[j], ir, (bits[j] >> 12) & 0xffff0u, true);
+    for (int k = 0; k < 2; ++k) {
+      uint32_t cm[4], cr[4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int p2 = 2 * k + j;
+        const float2 ym = __fmul2_rn(__fmul2_rn(m[p2], im), low), yr = __fmul2_rn(__fmul2_rn(r[p2], ir), low);
+        cm[2 * j] = round_code(ym.x, low_random(bits[2 * p2]));
+        cm[2 * j + 1] = round_code(ym.y, low_random(bits[2 * p2 + 1]));
+        cr[2 * j] = round_code(yr.x, high_random(bits[2 * p2]));
+        cr[2 * j + 1] = round_code(yr.y, high_random(bits[2 * p2 + 1]));
+      }
+      const uint32_t signs = tops4(__float_as_uint(m[2 * k].x), __float_as_uint(m[2 * k].y), __float_as_uint(m[2 * k + 1].x),
+                                   __float_as_uint(m[2 * k + 1].y)) & 0x80808080u;
+      (k == 0 ? mc.x : mc.y) = tops4(cm[0], cm[1], cm[2], cm[3]) | signs;
+      (k == 0 ? rc.x : rc.y) = tops4(cr[0], cr[1], cr[2], cr[3]);
     }
-    store_codes(static_cast<uint8_t*>(t.m), i, left, vec, m);
-    store_codes(static_cast<uint8_t*>(t.v), i, left, vec, v);
+    // A byte of 0 among r's codes (rare), or a value that is not finite: element by element.
+    const uint32_t zero = ((rc.x - 0x01010101u) & ~rc.x & 0x80808080u) | ((rc.y - 0x01010101u) & ~rc.y & 0x80808080u);
+    const bool bad = !(odd.x + odd.y == 0.f) || !(mtop < INFINITY) || !(rtop < INFINITY);
+    if (zero != 0u || bad) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float mj = j & 1 ? m[j / 2].y : m[j / 2].x, rj = j & 1 ? r[j / 2].y : r[j / 2].x;
+        uint32_t& mw = j < 4 ? mc.x : mc.y;
+        uint32_t& rw = j < 4 ? rc.x : rc.y;
+        const int at = 8 * (j & 3);
+        const uint32_t was = (rw >> at) & 0xffu;
+        if (rj > 0.f && was == 0u) rw |= 1u << at;  // a non-zero r is not stored as 0
+        if (!isfinite(rj)) rw |= 0x7fu << at;        // NaN
+        if (!isfinite(mj)) mw |= 0x7fu << at;
+      }
+    }
+    store_codes(mp, i, left, vec, mc);
+    store_codes(vp, i, left, vec, rc);
     if (lane == 0) {
       t.me[b0 / kBlock] = static_cast<int8_t>(em);
       t.ve[b0 / kBlock] = static_cast<int8_t>(er);
     }
-  } else {
-    store8(static_cast<float*>(t.m), i, left, vec, m);
-    store8(static_cast<float*>(t.v), i, left, vec, v);
-  }
-  if (MASTER) store8(t.master, i, left, vec, w);
-  if (kRandomParam) {
+    float wf[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t up = (bits[j] * 0x9E3779B1u) >> 16;
-      if (isfinite(w[j])) w[j] = __uint_as_float((__float_as_uint(w[j]) + up) & 0xffff0000u);
+    for (int j = 0; j < 4; ++j) wf[2 * j] = w[j].x, wf[2 * j + 1] = w[j].y;
+    if (MASTER) store8(t.master, i, left, vec, wf);
+    if constexpr (kRandomParam) {
+      uint32_t wb[8];  // rounded in the upper half
+#pragma unroll
+      for (int j = 0; j < 8; ++j) wb[j] = __float_as_uint(wf[j]) + ((bits[j] * 0x9E3779B1u) >> 16);
+      if (bad) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (!isfinite(wf[j])) wb[j] = isnan(wf[j]) ? 0x7fc00000u : __float_as_uint(wf[j]);
+      }
+      uint16_t* dst = static_cast<uint16_t*>(t.p) + i;
+      if (vec && left >= 8) {
+        *reinterpret_cast<uint4*>(dst) = make_uint4(__byte_perm(wb[0], wb[1], 0x7632), __byte_perm(wb[2], wb[3], 0x7632),
+                                                    __byte_perm(wb[4], wb[5], 0x7632), __byte_perm(wb[6], wb[7], 0x7632));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < left) dst[j] = static_cast<uint16_t>(wb[j] >> 16);
+      }
+    } else {
+      store8(static_cast<P*>(t.p), i, left, vec, wf);
     }
   }
-  store8(static_cast<P*>(t.p), i, left, vec, w);
 }
 
 // ------------------------------------------------------------------------------------- gradient norm
@@ -346,9 +489,13 @@ __global__ void __launch_bounds__(1024) grad_norm_final_kernel(const float* part
 bool multiple_of(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 template <int CAP, typename P, typename G, bool MASTER, bool BITS8>
-cudaError_t step_list(const hylo_adamw_tensor* tensors, int count, double bias1, const AdamWHyper& h,
+cudaError_t step_list(const hylo_adamw_tensor* tensors, int count, double bias1, const AdamWHyper& h, int sms,
                       cudaStream_t stream) {
   AdamTable<CAP> tab;
+  int64_t total = 0;
+  for (int k = 0; k < count; ++k) total += tensors[k].n;
+  const int64_t fill = total / (static_cast<int64_t>(4) * sms * kChunk);
+  tab.steps = BITS8 ? static_cast<int>(fill < 1 ? 1 : fill > kMaxSteps8 ? kMaxSteps8 : fill) : 1;
   uint64_t pos = 0;
   int i = 0;
   while (i < count) {
@@ -357,7 +504,8 @@ cudaError_t step_list(const hylo_adamw_tensor* tensors, int count, double bias1,
     for (; i < count && tab.count < CAP; ++i) {
       const hylo_adamw_tensor& x = tensors[i];
       const uint64_t padded = static_cast<uint64_t>((x.n + kBlock - 1) / kBlock) * kBlock;
-      const int64_t need = (x.n + kChunk - 1) / kChunk;
+      const int64_t chunk = static_cast<int64_t>(tab.steps) * kChunk;
+      const int64_t need = (x.n + chunk - 1) / chunk;
       if (need > 0) {
         if (chunks + static_cast<uint64_t>(need) > 0x7fffffffu) break;  // the grid is full: next launch
         AdamTensor& t = tab.t[tab.count++];
@@ -374,7 +522,10 @@ cudaError_t step_list(const hylo_adamw_tensor* tensors, int count, double bias1,
       pos += padded;
     }
     if (tab.count == 0) continue;
-    adamw_kernel<P, G, MASTER, BITS8, CAP><<<chunks, kThreads, 0, stream>>>(tab, h);
+    if (BITS8)
+      adamw8_kernel<P, G, MASTER, CAP><<<chunks, kThreads, 0, stream>>>(tab, h);
+    else
+      adamw_kernel<P, G, MASTER, CAP><<<chunks, kThreads, 0, stream>>>(tab, h);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
@@ -382,20 +533,20 @@ cudaError_t step_list(const hylo_adamw_tensor* tensors, int count, double bias1,
 }
 
 template <typename P, typename G, bool MASTER, bool BITS8>
-cudaError_t step_any(const hylo_adamw_tensor* tensors, int count, double bias1, const AdamWHyper& h,
+cudaError_t step_any(const hylo_adamw_tensor* tensors, int count, double bias1, const AdamWHyper& h, int sms,
                      cudaStream_t stream) {
-  return count <= kSmallTable ? step_list<kSmallTable, P, G, MASTER, BITS8>(tensors, count, bias1, h, stream)
-                              : step_list<kLargeTable, P, G, MASTER, BITS8>(tensors, count, bias1, h, stream);
+  return count <= kSmallTable ? step_list<kSmallTable, P, G, MASTER, BITS8>(tensors, count, bias1, h, sms, stream)
+                              : step_list<kLargeTable, P, G, MASTER, BITS8>(tensors, count, bias1, h, sms, stream);
 }
 
 template <typename P, bool MASTER>
 cudaError_t step_types(const hylo_adamw_tensor* tensors, int count, int grad_dtype, int state_bits, double bias1,
-                       const AdamWHyper& h, cudaStream_t stream) {
+                       const AdamWHyper& h, int sms, cudaStream_t stream) {
   if (grad_dtype == HYLO_F32)
-    return state_bits == 8 ? step_any<P, float, MASTER, true>(tensors, count, bias1, h, stream)
-                           : step_any<P, float, MASTER, false>(tensors, count, bias1, h, stream);
-  return state_bits == 8 ? step_any<P, __nv_bfloat16, MASTER, true>(tensors, count, bias1, h, stream)
-                         : step_any<P, __nv_bfloat16, MASTER, false>(tensors, count, bias1, h, stream);
+    return state_bits == 8 ? step_any<P, float, MASTER, true>(tensors, count, bias1, h, sms, stream)
+                           : step_any<P, float, MASTER, false>(tensors, count, bias1, h, sms, stream);
+  return state_bits == 8 ? step_any<P, __nv_bfloat16, MASTER, true>(tensors, count, bias1, h, sms, stream)
+                         : step_any<P, __nv_bfloat16, MASTER, false>(tensors, count, bias1, h, sms, stream);
 }
 
 template <typename G>
@@ -431,11 +582,11 @@ cudaError_t launch_grad_norm(const void* const* grads, const int64_t* sizes, int
 }
 
 cudaError_t launch_adamw(const hylo_adamw_tensor* tensors, int count, int param_dtype, int grad_dtype, int state_bits,
-                         bool masters, double bias1, const AdamWHyper& h, cudaStream_t stream) {
-  if (param_dtype == HYLO_F32) return step_types<float, false>(tensors, count, grad_dtype, state_bits, bias1, h, stream);
+                         bool masters, double bias1, const AdamWHyper& h, int sms, cudaStream_t stream) {
+  if (param_dtype == HYLO_F32) return step_types<float, false>(tensors, count, grad_dtype, state_bits, bias1, h, sms, stream);
   return masters
-             ? step_types<__nv_bfloat16, true>(tensors, count, grad_dtype, state_bits, bias1, h, stream)
-             : step_types<__nv_bfloat16, false>(tensors, count, grad_dtype, state_bits, bias1, h, stream);
+             ? step_types<__nv_bfloat16, true>(tensors, count, grad_dtype, state_bits, bias1, h, sms, stream)
+             : step_types<__nv_bfloat16, false>(tensors, count, grad_dtype, state_bits, bias1, h, sms, stream);
 }
 
 }  // namespace hylo

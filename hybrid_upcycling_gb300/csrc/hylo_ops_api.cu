@@ -252,7 +252,7 @@ hylo_status hylo_adamw_step(const hylo_adamw_tensor* tensors, int count, int par
   h.max_norm = max_norm;
   h.seed = seed;
   const double bias1 = 1.0 - std::pow(beta1, static_cast<double>(step));
-  const cudaError_t e = launch_adamw(tensors, count, param_dtype, grad_dtype, state_bits, tensors[some].master != nullptr, bias1, h, stream);
+  const cudaError_t e = launch_adamw(tensors, count, param_dtype, grad_dtype, state_bits, tensors[some].master != nullptr, bias1, h, dev->sms, stream);
   return e == cudaSuccess ? HYLO_OK : cuda_fail(e, "launch AdamW");
 }
 

@@ -94,6 +94,6 @@ struct AdamWHyper {
   uint32_t seed;
 };
 cudaError_t launch_adamw(const hylo_adamw_tensor* tensors, int count, int param_dtype, int grad_dtype, int state_bits,
-                         bool masters, double bias1, const AdamWHyper& h, cudaStream_t stream);
+                         bool masters, double bias1, const AdamWHyper& h, int sms, cudaStream_t stream);
 
 }  // namespace hylo
