@@ -276,7 +276,7 @@ head_logprobs_kernel(const __grid_constant__ CUtensorMap tm_h, const __grid_cons
       }
       if (!ok) break;
       if (token < p.N)
-        p.part[static_cast<int64_t>(token) * (2 * p.nseg) + 2 * seg + hc] = make_float4(r.mx, r.s, r.a, 0.f);
+        p.part[static_cast<int64_t>(token) * p.slots + 2 * seg + hc] = make_float4(r.mx, r.s, r.a, 0.f);
     }
   }
 
@@ -289,12 +289,110 @@ head_logprobs_kernel(const __grid_constant__ CUtensorMap tm_h, const __grid_cons
   }
 }
 
-// One warp per token joins its 2 nseg partial sums (a fixed tree).
+// ---- A few tokens (one decoding step): the LM head's bytes are the cost, and the tensor cores would spend their
+// 256-row tiles on them. Every warp takes kRows words at a time, its lanes walk the hidden dimension with
+// 16-byte loads of W and the tokens' states in fp32 from shared memory, and the dot products end in
+// a warp reduction; lane t keeps token t's running sums. fp32 multiply-adds: no drift of
+// long tensor-core accumulations. Measured beside the tensor-core path (128256 words): one token, d = 4096 147 us
+// (7.1 TB/s) against 165, d = 2048 78 against 83; two tokens 152 against 165 and 90 against 83; four
+// tokens 172 against 165, where the multiply-adds and not the loads set the time. So it takes one or two.
+constexpr int kFewThreads = 512;
+constexpr int kFewWarps = kFewThreads / 32;
+constexpr int kRows = 4;
+
+template <int NT>
+__global__ void __launch_bounds__(kFewThreads, 1)
+head_few_kernel(const uint16_t* __restrict__ h, const uint16_t* __restrict__ W, int d, const HeadParams p) {
+  extern __shared__ float hs[];  // [NT][d]
+  __shared__ Sums sums[kFewWarps][NT];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < NT * d; i += kFewThreads)
+    hs[i] = i < p.N * d ? __uint_as_float(static_cast<uint32_t>(h[i]) << 16) : 0.f;
+  __syncthreads();
+  const int64_t want = lane < p.N ? p.tokens[lane] : -1;
+  Sums r{-INFINITY, 0.f, 0.f};
+  const int nvec = d / 8;
+  const int64_t groups = (static_cast<int64_t>(p.V) + kRows - 1) / kRows;
+  for (int64_t g = static_cast<int64_t>(blockIdx.x) * kFewWarps + warp; g < groups; g += static_cast<int64_t>(gridDim.x) * kFewWarps) {
+    const int64_t v0 = g * kRows;
+    const uint4* row[kRows];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) row[k] = reinterpret_cast<const uint4*>(W + min(v0 + k, static_cast<int64_t>(p.V) - 1) * d);
+    float2 acc[kRows][NT];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) acc[k][t] = make_float2(0.f, 0.f);
+#pragma unroll 4
+    for (int i = lane; i < nvec; i += 32) {
+      uint4 w[kRows];
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) w[k] = __ldcs(row[k] + i);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const float4 a = *reinterpret_cast<const float4*>(hs + t * d + i * 8), b = *reinterpret_cast<const float4*>(hs + t * d + i * 8 + 4);
+        const float2 x[4] = {make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)};
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+          const uint32_t q[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            acc[k][t] = __ffma2_rn(make_float2(__uint_as_float(q[j] << 16), __uint_as_float(q[j] & 0xffff0000u)), x[j], acc[k][t]);
+        }
+      }
+    }
+    float z[kRows];  // this lane's token's logits (lanes from NT on: token 0's)
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      z[k] = 0.f;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float s = acc[k][t].x + acc[k][t].y;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(~0u, s, off);
+        z[k] = t == 0 || lane == t ? s : z[k];
+      }
+    }
+    const int rows = static_cast<int>(min(static_cast<int64_t>(kRows), p.V - v0));
+    float mx = r.mx;
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
+      if (k < rows) mx = fmaxf(mx, z[k]);
+    rebase(r, mx, p.c);
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      if (k < rows) {
+        const float y = (z[k] - mx) * p.c;
+        const float e = ex2_approx(y);
+        r.s += e;
+        r.a = fmaf(e, y, r.a);
+        if (want == v0 + k) p.z_token[lane] = z[k];
+      }
+    }
+  }
+  if (lane < NT) sums[warp][lane] = r;
+  __syncthreads();
+  if (tid < NT && tid < p.N) {
+    Sums total = sums[0][tid];
+    for (int w = 1; w < kFewWarps; ++w) {
+      Sums o = sums[w][tid];
+      if (o.mx == -INFINITY) continue;  // a warp without words
+      const float m = fmaxf(total.mx, o.mx);
+      rebase(total, m, p.c);
+      rebase(o, m, p.c);
+      total.s += o.s;
+      total.a += o.a;
+    }
+    p.part[static_cast<int64_t>(tid) * p.slots + blockIdx.x] = make_float4(total.mx, total.s, total.a, 0.f);
+  }
+}
+
+// One warp per token joins its partial sums (a fixed tree).
 __global__ void __launch_bounds__(256) head_combine_kernel(const HeadParams p, float* logp, float* entropy, float* lse) {
   const int lane = threadIdx.x & 31;
   const int64_t n = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (n >= p.N) return;
-  const int slots = 2 * p.nseg;
+  const int slots = p.slots;
   Sums r{-INFINITY, 0.f, 0.f};
   auto add = [&](float mx, float s, float a) {
     if (mx == -INFINITY) return;  // a half without columns (the vocabulary ends before it)
@@ -341,13 +439,45 @@ cudaLaunchConfig_t head_config(cudaLaunchAttribute* attr, int clusters, cudaStre
 
 }  // namespace
 
+cudaError_t head_few_prepare();
+
 cudaError_t head_prepare(int* max_clusters) {
-  cudaError_t e = cudaFuncSetAttribute(head_logprobs_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  cudaError_t e = head_few_prepare();
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(head_logprobs_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = head_config(attr, 1, nullptr);
   cfg.numAttrs = 1;  // occupancy: the cluster shape only
   return cudaOccupancyMaxActiveClusters(max_clusters, head_logprobs_kernel, &cfg);
+}
+
+constexpr int kFewTokens = 2;
+constexpr size_t kFewSmem = 200 * 1024;
+
+template <int NT>
+cudaError_t launch_few(const uint16_t* h, const uint16_t* W, int d, const HeadParams& p, int ctas, cudaStream_t stream) {
+  head_few_kernel<NT><<<ctas, kFewThreads, static_cast<size_t>(NT) * d * sizeof(float), stream>>>(h, W, d, p);
+  return cudaGetLastError();
+}
+
+bool head_few_fits(int64_t N, int64_t d) { return N <= kFewTokens && static_cast<size_t>(N) * d * sizeof(float) <= kFewSmem; }
+
+cudaError_t head_few_prepare() {
+  const void* kernels[] = {reinterpret_cast<const void*>(head_few_kernel<1>), reinterpret_cast<const void*>(head_few_kernel<2>)};
+  for (const void* k : kernels) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kFewSmem));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_head_few(const uint16_t* h, const uint16_t* W, int d, const HeadParams& p, float* logp, float* entropy,
+                            float* lse, cudaStream_t stream) {
+  const cudaError_t e = p.N == 1 ? launch_few<1>(h, W, d, p, p.slots, stream) : launch_few<2>(h, W, d, p, p.slots, stream);
+  if (e != cudaSuccess) return e;
+  head_combine_kernel<<<(p.N + 7) / 8, 256, 0, stream>>>(p, logp, entropy, lse);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_head_logprobs(const CUtensorMap& h, const CUtensorMap& W, const HeadParams& p, float* logp,

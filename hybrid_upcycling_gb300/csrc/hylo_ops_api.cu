@@ -121,24 +121,30 @@ hylo_status hylo_head_logprobs(const uint16_t* h, const uint16_t* W, int64_t N, 
   if (st != HYLO_OK) return st;
   DeviceState* dev = nullptr;
   if ((st = current_device(&dev)) != HYLO_OK) return st;
-  CUtensorMap m_h, m_W;
-  const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  if ((st = make_map(&m_h, h, bf, d, N, d * 2, kBK, kBM)) != HYLO_OK) return st;
-  if ((st = make_map(&m_W, W, bf, d, V, d * 2, kBK, kFusedBN / 2)) != HYLO_OK) return st;
   HeadParams p{};
   p.N = static_cast<int>(N);
   p.V = static_cast<int>(V);
-  p.kb = static_cast<int>(cdiv(d, kBK));
-  p.token_tiles = static_cast<int>(cdiv(N, 2 * kBM));
-  p.vtiles = static_cast<int>(cdiv(V, kFusedBN));
-  p.nseg = choose_segments(p.token_tiles, p.vtiles, dev->head_clusters, head_segments(N));
-  p.units = p.token_tiles * p.nseg;
   p.c = 1.4426950408889634f / tau;
   p.inv_tau = 1.0f / tau;
   p.tokens = tokens;
   p.z_token = static_cast<float*>(workspace);
   p.part = reinterpret_cast<float4*>(static_cast<char*>(workspace) + round256(N * sizeof(float)));
   p.ctl = WaitCtl{dev->status, wait_limit_ns()};
+  if (head_few_fits(N, d)) {
+    p.slots = dev->sms < 2 * head_segments(N) ? dev->sms : 2 * head_segments(N);
+    const cudaError_t e = launch_head_few(h, W, static_cast<int>(d), p, logp, entropy, lse, stream);
+    return e == cudaSuccess ? HYLO_OK : cuda_fail(e, "launch head log-probabilities of few tokens");
+  }
+  CUtensorMap m_h, m_W;
+  const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  if ((st = make_map(&m_h, h, bf, d, N, d * 2, kBK, kBM)) != HYLO_OK) return st;
+  if ((st = make_map(&m_W, W, bf, d, V, d * 2, kBK, kFusedBN / 2)) != HYLO_OK) return st;
+  p.kb = static_cast<int>(cdiv(d, kBK));
+  p.token_tiles = static_cast<int>(cdiv(N, 2 * kBM));
+  p.vtiles = static_cast<int>(cdiv(V, kFusedBN));
+  p.nseg = choose_segments(p.token_tiles, p.vtiles, dev->head_clusters, head_segments(N));
+  p.units = p.token_tiles * p.nseg;
+  p.slots = 2 * p.nseg;
   const int clusters = p.units < dev->head_clusters ? p.units : dev->head_clusters;
   const cudaError_t e = launch_head_logprobs(m_h, m_W, p, logp, entropy, lse, clusters, stream);
   return e == cudaSuccess ? HYLO_OK : cuda_fail(e, "launch head log-probabilities");

@@ -58,13 +58,19 @@ struct HeadParams {
   float c;          // log2(e) / tau
   float inv_tau;
   const int64_t* tokens;
-  float4* part;     // partial sums [N][2 nseg]
+  int slots;        // partial sums per token
+  float4* part;     // partial sums [N][slots]
   float* z_token;   // the tokens' logits [N]
   WaitCtl ctl;
 };
 cudaError_t head_prepare(int* max_clusters);
 cudaError_t launch_head_logprobs(const CUtensorMap& h, const CUtensorMap& W, const HeadParams& p, float* logp,
                                  float* entropy, float* lse, int clusters, cudaStream_t stream);
+
+// The forward of few tokens, without the tensor cores; p.slots CTAs.
+bool head_few_fits(int64_t N, int64_t d);
+cudaError_t launch_head_few(const uint16_t* h, const uint16_t* W, int d, const HeadParams& p, float* logp, float* entropy,
+                            float* lse, cudaStream_t stream);
 
 // Backward of the same: the pipelined backward (kl_bwd_pipe.cu) with
 //   G[n, v] = dL/dz = p (A + B log2 p) + 1[v = tokens[n]] g_logp / tau,
