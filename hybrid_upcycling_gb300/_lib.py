@@ -78,11 +78,12 @@ def load() -> ctypes.CDLL:
     L.hylo_token_logprobs.restype = ctypes.c_int
     L.hylo_token_logprobs_backward.argtypes = [vp, i32, i64, i64, i64, f32, vp, vp, vp, vp, vp, vp, i64, vp]
     L.hylo_token_logprobs_backward.restype = ctypes.c_int
-    L.hylo_head_logprobs_workspace_bytes.argtypes = [i64, i64, i64, i64, i32]
+    L.hylo_head_logprobs_workspace_bytes.argtypes = [i64, i64, i64, i64, i32, i32]
     L.hylo_head_logprobs_workspace_bytes.restype = sz
     L.hylo_head_logprobs.argtypes = [vp, vp, i64, i64, i64, f32, vp, vp, vp, vp, vp, sz, vp]
     L.hylo_head_logprobs.restype = ctypes.c_int
-    L.hylo_head_logprobs_backward.argtypes = [vp, vp, i64, i64, i64, f32, i64, vp, vp, vp, vp, vp, i32, vp, vp, vp, sz, vp]
+    L.hylo_head_logprobs_backward.argtypes = [vp, vp, i64, i64, i64, f32, i64, vp, vp, vp, vp, vp, i32, i32, vp, vp, vp, sz,
+                                              vp]
     L.hylo_head_logprobs_backward.restype = ctypes.c_int
     L.hylo_grad_norm_workspace_bytes.argtypes = []
     L.hylo_grad_norm_workspace_bytes.restype = sz
@@ -284,8 +285,9 @@ def _head_dims(h, W):
     return h.shape[0], h.shape[1], W.shape[0]
 
 
-def hylo_head_logprobs_workspace_bytes(N: int, d: int, V: int, token_chunk: int = 4096, split_g: bool = False) -> int:
-    return int(load().hylo_head_logprobs_workspace_bytes(N, d, V, token_chunk, int(split_g)))
+def hylo_head_logprobs_workspace_bytes(N: int, d: int, V: int, token_chunk: int = 4096, split_g: bool = False,
+                                       grad_dtype=torch.float32) -> int:
+    return int(load().hylo_head_logprobs_workspace_bytes(N, d, V, token_chunk, int(split_g), DTYPES[grad_dtype]))
 
 
 def hylo_head_logprobs(h, W, tokens, tau: float, logp, entropy, lse, workspace, stream=None) -> None:
@@ -302,18 +304,22 @@ def hylo_head_logprobs(h, W, tokens, tau: float, logp, entropy, lse, workspace, 
 
 def hylo_head_logprobs_backward(h, W, tokens, tau: float, token_chunk: int, lse, entropy, g_logp, g_entropy, dh, dW,
                                 workspace, split_g: bool = False, stream=None) -> None:
-    """fp32 gradients dh [N, d], dW [V, d] (overwritten) for the upstream g_logp, g_entropy [N] (either None)."""
+    """Gradients dh [N, d], dW [V, d] (overwritten; both float32 or both bfloat16) for the upstream g_logp, g_entropy
+    [N] (either None)."""
     N, d, V = _head_dims(h, W)
     _need_cuda(h=h, W=W, tokens=tokens, lse=lse, entropy=entropy, g_logp=g_logp, g_entropy=g_entropy, dh=dh, dW=dW,
                workspace=workspace)
     _need("tokens", tokens, torch.int64, (N,))
     for name, t in (("lse", lse), ("entropy", entropy), ("g_logp", g_logp), ("g_entropy", g_entropy)):
         _need(name, t, torch.float32, (N,))
-    _need("dh", dh, torch.float32, (N, d))
-    _need("dW", dW, torch.float32, (V, d))
+    if dh.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("dh and dW must be float32 or bfloat16")
+    _need("dh", dh, dh.dtype, (N, d))
+    _need("dW", dW, dh.dtype, (V, d))
     _check(load().hylo_head_logprobs_backward(h.data_ptr(), W.data_ptr(), N, d, V, float(tau), int(token_chunk),
                                               tokens.data_ptr(), _ptr(lse), _ptr(entropy), _ptr(g_logp),
-                                              _ptr(g_entropy), int(split_g), _ptr(dh), _ptr(dW), workspace.data_ptr(),
+                                              _ptr(g_entropy), int(split_g), DTYPES[dh.dtype], _ptr(dh), _ptr(dW),
+                                              workspace.data_ptr(),
                                               workspace.numel() * workspace.element_size(), _stream(stream)))
 
 

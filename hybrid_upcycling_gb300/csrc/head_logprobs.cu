@@ -420,6 +420,14 @@ __global__ void __launch_bounds__(256) head_combine_kernel(const HeadParams p, f
   if (lse) lse[n] = r.mx * inv_tau + log_s;
 }
 
+// Eight values per thread and step; n is a multiple of 8.
+__global__ void __launch_bounds__(256) round_bf16_kernel(const float4* __restrict__ x, uint4* __restrict__ y, int64_t n8) {
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n8; i += static_cast<int64_t>(gridDim.x) * 256) {
+    const float4 a = __ldcs(x + 2 * i), b = __ldcs(x + 2 * i + 1);
+    y[i] = make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
+  }
+}
+
 cudaLaunchConfig_t head_config(cudaLaunchAttribute* attr, int clusters, cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
@@ -438,6 +446,13 @@ cudaLaunchConfig_t head_config(cudaLaunchAttribute* attr, int clusters, cudaStre
 }
 
 }  // namespace
+
+cudaError_t launch_round_bf16(const float* x, uint16_t* y, int64_t n, int sms, cudaStream_t stream) {
+  const int64_t want = (n / 8 + 255) / 256, cap = static_cast<int64_t>(sms) * 8;
+  round_bf16_kernel<<<static_cast<int>(want < cap ? want : cap), 256, 0, stream>>>(reinterpret_cast<const float4*>(x),
+                                                                                  reinterpret_cast<uint4*>(y), n / 8);
+  return cudaGetLastError();
+}
 
 cudaError_t head_few_prepare();
 

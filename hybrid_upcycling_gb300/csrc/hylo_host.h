@@ -52,6 +52,8 @@ int choose_segments(int64_t token_tiles, int64_t vtiles, int workers, int most);
 
 // Bytes of the pipelined backward's G ring for one bf16 term; its counters follow the ring(s).
 size_t bwd_bytes(int64_t N, int64_t V, int64_t token_chunk);
+// Rows of its token blocks.
+int64_t pipe_rows(int64_t N, int64_t token_chunk);
 constexpr size_t kPipeCtrlBytes = 256;
 hylo_status pipe_setup(const uint16_t* h, const uint16_t* W, int64_t N, int64_t d, int64_t V, float tau,
                        int64_t token_chunk, float* dh, float* dW, void* workspace, size_t g_total, bool split,

@@ -43,6 +43,23 @@ size_t head_fwd_bytes(int64_t N) {
   return round256(N * sizeof(float)) + static_cast<size_t>(N) * 2 * head_segments(N) * sizeof(float4);
 }
 
+// The backward's workspace: the G ring(s), the counters, and for bf16 gradients the fp32 sums that are rounded at the end.
+struct HeadBwd {
+  size_t ctrl, dh, dW, total;
+  bool dW_direct;  // dW is written in bf16 by the pipelined backward itself
+};
+HeadBwd head_bwd_layout(int64_t N, int64_t d, int64_t V, int64_t token_chunk, bool split, int grad_dtype) {
+  HeadBwd l{};
+  l.ctrl = round256(bwd_bytes(N, V, token_chunk)) * (split ? 2 : 1);
+  l.dh = l.dW = l.total = l.ctrl + kPipeCtrlBytes;
+  if (grad_dtype == HYLO_BF16) {
+    l.dW_direct = N <= pipe_rows(N, token_chunk);
+    l.dW = l.dh + round256(static_cast<size_t>(N) * d * sizeof(float));
+    l.total = l.dW + (l.dW_direct ? 0 : round256(static_cast<size_t>(V) * d * sizeof(float)));
+  }
+  return l;
+}
+
 hylo_status check_head(const uint16_t* h, const uint16_t* W, int64_t N, int64_t d, int64_t V, float tau,
                        const int64_t* tokens, void* workspace, size_t workspace_bytes, size_t need) {
   if (!h || !W || !tokens || !workspace) return fail(HYLO_ERR_NULL, "a required pointer is NULL");
@@ -102,10 +119,11 @@ hylo_status hylo_token_logprobs_backward(const void* z, int dtype, int64_t N, in
   return e == cudaSuccess ? HYLO_OK : cuda_fail(e, "launch token log-probabilities backward");
 }
 
-size_t hylo_head_logprobs_workspace_bytes(int64_t N, int64_t d, int64_t V, int64_t token_chunk, int split_g) {
+size_t hylo_head_logprobs_workspace_bytes(int64_t N, int64_t d, int64_t V, int64_t token_chunk, int split_g,
+                                          int grad_dtype) {
   clear_error();
-  if (!head_sizes_ok(N, d, V)) return 0;
-  const size_t f = head_fwd_bytes(N), b = round256(bwd_bytes(N, V, token_chunk)) * (split_g ? 2 : 1) + kPipeCtrlBytes;
+  if (!head_sizes_ok(N, d, V) || (grad_dtype != HYLO_F32 && grad_dtype != HYLO_BF16)) return 0;
+  const size_t f = head_fwd_bytes(N), b = head_bwd_layout(N, d, V, token_chunk, split_g != 0, grad_dtype).total;
   return f > b ? f : b;
 }
 
@@ -153,30 +171,43 @@ hylo_status hylo_head_logprobs(const uint16_t* h, const uint16_t* W, int64_t N, 
 hylo_status hylo_head_logprobs_backward(const uint16_t* h, const uint16_t* W, int64_t N, int64_t d, int64_t V,
                                         float tau, int64_t token_chunk, const int64_t* tokens, const float* lse,
                                         const float* entropy, const float* g_logp, const float* g_entropy, int split_g,
-                                        float* dh, float* dW, void* workspace, size_t workspace_bytes,
+                                        int grad_dtype, void* dh, void* dW, void* workspace, size_t workspace_bytes,
                                         cudaStream_t stream) {
   clear_error();
   if (!lse || !dh || !dW || (g_entropy && !entropy)) return fail(HYLO_ERR_NULL, "a required pointer is NULL");
+  if (grad_dtype != HYLO_F32 && grad_dtype != HYLO_BF16) return fail(HYLO_ERR_DIM, "gradients are fp32 or bf16 (dtype %d)", grad_dtype);
   const bool split = split_g != 0;
-  const size_t g_total = head_sizes_ok(N, d, V) ? round256(bwd_bytes(N, V, token_chunk)) * (split ? 2 : 1) : 0;
-  hylo_status st = check_head(h, W, N, d, V, tau, tokens, workspace, workspace_bytes, g_total + kPipeCtrlBytes);
+  const HeadBwd l = head_sizes_ok(N, d, V) ? head_bwd_layout(N, d, V, token_chunk, split, grad_dtype) : HeadBwd{};
+  hylo_status st = check_head(h, W, N, d, V, tau, tokens, workspace, workspace_bytes, l.total);
   if (st != HYLO_OK) return st;
   if (!aligned(dh, 16) || !aligned(dW, 16)) return fail(HYLO_ERR_ALIGN, "gradient pointers must be 16-byte aligned");
   if (!aligned(lse, 4) || !aligned(entropy, 4) || !aligned(g_logp, 4) || !aligned(g_entropy, 4))
     return fail(HYLO_ERR_ALIGN, "per-token pointers must be 4-byte aligned");
+  // The sums are fp32: for bf16 gradients they are formed in the workspace and rounded once, or, where dW has one token
+  // block, as they leave the tensor cores.
+  char* ws = static_cast<char*>(workspace);
+  const bool bf16 = grad_dtype == HYLO_BF16;
+  float* dh32 = bf16 ? reinterpret_cast<float*>(ws + l.dh) : static_cast<float*>(dh);
+  float* dW32 = l.dW_direct ? static_cast<float*>(dW) : bf16 ? reinterpret_cast<float*>(ws + l.dW) : static_cast<float*>(dW);
   DeviceState* dev = nullptr;
   CUtensorMap maps[kPipeMaps];
   BwdPipeParams p{};
   int clusters = 0;
-  if ((st = pipe_setup(h, W, N, d, V, tau, token_chunk, dh, dW, workspace, g_total, split, &dev, maps, &p,
-                       &clusters)) != HYLO_OK)
+  if ((st = pipe_setup(h, W, N, d, V, tau, token_chunk, dh32, dW32, workspace, l.ctrl, split, &dev, maps, &p, &clusters)) !=
+      HYLO_OK)
     return st;
   maps[1] = maps[0];  // no teacher: never loaded from
   maps[3] = maps[2];
+  if (l.dW_direct && (st = make_map_3d(&maps[7], dW, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d, V, 1, d * 2, 32, 32,
+                                       CU_TENSOR_MAP_SWIZZLE_64B)) != HYLO_OK)
+    return st;
   cudaError_t e = cudaMemsetAsync(p.ctrl, 0, kPipeCtrlWords * sizeof(unsigned), stream);
   if (e != cudaSuccess) return cuda_fail(e, "clear the backward's work counters");
-  const HeadGrad g{tokens, lse, entropy, g_logp, g_entropy, 1.0f / tau};
+  const HeadGrad g{tokens, lse, entropy, g_logp, g_entropy, 1.0f / tau, l.dW_direct ? 1 : 0};
   e = launch_bwd_pipe_head(maps, p, g, clusters, stream);
+  if (e == cudaSuccess && bf16) e = launch_round_bf16(dh32, static_cast<uint16_t*>(dh), N * d, dev->sms, stream);
+  if (e == cudaSuccess && bf16 && !l.dW_direct)
+    e = launch_round_bf16(dW32, static_cast<uint16_t*>(dW), V * d, dev->sms, stream);
   return e == cudaSuccess ? HYLO_OK : cuda_fail(e, "launch head log-probabilities backward");
 }
 

@@ -82,7 +82,10 @@ struct HeadGrad {
   const float* g_logp;     // or null
   const float* g_entropy;  // or null
   float inv_tau;
+  int dw_bf16;             // one token block: map kMapDW is a bf16 tensor of 32 x 32 tiles with 64-byte swizzle
 };
+// n fp32 values rounded to bf16 (16-byte aligned).
+cudaError_t launch_round_bf16(const float* x, uint16_t* y, int64_t n, int sms, cudaStream_t stream);
 cudaError_t launch_bwd_pipe_head(const CUtensorMap* maps, const BwdPipeParams& p, const HeadGrad& g, int clusters,
                                  cudaStream_t stream);
 

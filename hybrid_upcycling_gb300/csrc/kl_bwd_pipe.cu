@@ -746,8 +746,36 @@ bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p, co
         const int col0 = nj * BN + hc * HB;
         const int n_valid = p.d_s - col0;
         const uint32_t acc = lane_base + static_cast<uint32_t>(h * BN);
+        bool stored = false;
+        if constexpr (kHead) {
+          // One token block: the tile is dW's final value, and goes out rounded to bf16 (64-byte rows and swizzle, as G).
+          if (dw && head.dw_bf16) {
+            stored = true;
 #pragma unroll 1
-        for (int ch = 0; ch < HB / 32; ++ch) {
+            for (int ch = 0; ch < HB / 32; ++ch) {
+              if (ch * 32 >= n_valid) break;
+              float v[32];
+              tmem_ld32(acc + ch * 32, v);
+              tmem_ld_wait();
+              const uint32_t buf = static_cast<uint32_t>((ch & 1) * 2048);
+              if (lane == 0) bulk_wait_group_read<1>();
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                st_shared_v4(row64 + buf + ((static_cast<uint32_t>(i) ^ swz64) << 4), pack_bf16x2(v[8 * i], v[8 * i + 1]),
+                             pack_bf16x2(v[8 * i + 2], v[8 * i + 3]), pack_bf16x2(v[8 * i + 4], v[8 * i + 5]),
+                             pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0 && row < rows_total) {
+                tma_store_3d(mc, staging + buf, col0 + ch * 32, row, 0);
+                bulk_commit_group();
+              }
+            }
+          }
+        }
+#pragma unroll 1
+        for (int ch = 0; !stored && ch < HB / 32; ++ch) {
           if (ch * 32 >= n_valid) break;  // warp-uniform: nothing of this chunk lies inside the output
           float v[32];
           tmem_ld32(acc + ch * 32, v);

@@ -18,6 +18,7 @@ from . import _lib
 from ._lib import _check, current_raw_stream, load
 
 _empty, _f32 = torch.empty, torch.float32
+_BF16 = _lib.DTYPES[torch.bfloat16]
 
 
 class TokenLogprobs(NamedTuple):
@@ -79,7 +80,7 @@ def _forward(z, tokens, tau, k, dev, train):
 
 
 def _upstream(g):
-    return None if g is None else g.to(_f32).contiguous()
+    return g if g is None or (g.dtype is _f32 and g.is_contiguous()) else g.to(_f32).contiguous()
 
 
 def _ptr(t):
@@ -140,7 +141,7 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, tau: float = 1.0,
 
 
 def _workspace(N, d, V, token_chunk, split_g, device):
-    n = load().hylo_head_logprobs_workspace_bytes(N, d, V, token_chunk, int(split_g))
+    n = load().hylo_head_logprobs_workspace_bytes(N, d, V, token_chunk, int(split_g), _BF16)
     if n == 0:
         raise ValueError("invalid sizes (the hidden size must be a multiple of 8 in 8..65536)")
     return _empty(n, dtype=torch.uint8, device=device), n  # from the caching allocator of the current stream
@@ -174,15 +175,15 @@ class _HeadLogprobs(torch.autograd.Function):
         (N, d), V = h.shape, W.shape[0]
         if N == 0:
             return torch.zeros_like(h), torch.zeros_like(W), None, None, None, None, None
-        dh, dW = _empty((N, d), dtype=_f32, device=h.device), _empty((V, d), dtype=_f32, device=h.device)
+        dh, dW = torch.empty_like(h), torch.empty_like(W)
         g_logp, g_entropy = _upstream(g_logp), _upstream(g_entropy)
         ws, n = _workspace(N, d, V, token_chunk, split_g, h.device)
         _check(load().hylo_head_logprobs_backward(
             h.data_ptr(), W.data_ptr(), N, d, V, tau, token_chunk, tokens.data_ptr(), lse.data_ptr(), entropy.data_ptr(),
-            _ptr(g_logp), _ptr(g_entropy), int(split_g), dh.data_ptr(), dW.data_ptr(), ws.data_ptr(), n,
+            _ptr(g_logp), _ptr(g_entropy), int(split_g), _BF16, dh.data_ptr(), dW.data_ptr(), ws.data_ptr(), n,
             current_raw_stream(h.get_device())))
-        return (dh.to(h.dtype) if ctx.needs_input_grad[0] else None, dW.to(W.dtype) if ctx.needs_input_grad[1] else None,
-                None, None, None, None, None)
+        return (dh if ctx.needs_input_grad[0] else None, dW if ctx.needs_input_grad[1] else None, None, None, None, None,
+                None)
 
 
 def head_logprobs(h: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, tau: float = 1.0, token_chunk: int = 4096,

@@ -56,21 +56,24 @@ hylo_status hylo_token_logprobs_backward(const void* z, int dtype, int64_t N, in
  * concerned are NaN or infinite). tokens as above. entropy and lse may be NULL; the backward needs lse
  * (and entropy, if g_entropy is given). workspace: at least hylo_head_logprobs_workspace_bytes(),
  * 256-byte aligned, not shared with a call still running on another stream; the forward uses O(N) of it,
- * the backward the G ring of hylo_kl_backward (at most 128 MiB, twice that with split_g).
- * Returns 0 for invalid sizes; token_chunk <= 0 means 4096. */
-size_t hylo_head_logprobs_workspace_bytes(int64_t N, int64_t d, int64_t V, int64_t token_chunk, int split_g);
+ * the backward the G ring of hylo_kl_backward (at most 128 MiB, twice that with split_g) and, for
+ * bf16 gradients, the fp32 sums behind them: N d, and V d if N is more than one token block.
+ * Returns 0 for invalid sizes; token_chunk <= 0 means 4096; grad_dtype as in the backward. */
+size_t hylo_head_logprobs_workspace_bytes(int64_t N, int64_t d, int64_t V, int64_t token_chunk, int split_g,
+                                          int grad_dtype);
 hylo_status hylo_head_logprobs(const uint16_t* h, const uint16_t* W, int64_t N, int64_t d, int64_t V, float tau,
                                const int64_t* tokens, float* logp, float* entropy, float* lse, void* workspace,
                                size_t workspace_bytes, cudaStream_t stream);
 
 /* Gradients of sum_n g_logp[n] logp[n] + g_entropy[n] entropy[n]: with G = dL/dz as in
  * hylo_token_logprobs_backward (recomputed tile by tile, rounded to bf16 once, or with split_g != 0
- * kept as two bf16 terms), dh = G W [N, d] and dW = G^T h [V, d], fp32, OVERWRITTEN. lse and
+ * kept as two bf16 terms), dh = G W [N, d] and dW = G^T h [V, d], summed in fp32 and OVERWRITTEN as
+ * grad_dtype (HYLO_F32 or HYLO_BF16, rounded once). lse and
  * entropy are the forward's for the same inputs. token_chunk as in hylo_kl_backward. Deterministic. */
 hylo_status hylo_head_logprobs_backward(const uint16_t* h, const uint16_t* W, int64_t N, int64_t d, int64_t V,
                                         float tau, int64_t token_chunk, const int64_t* tokens, const float* lse,
                                         const float* entropy, const float* g_logp, const float* g_entropy, int split_g,
-                                        float* dh, float* dW, void* workspace, size_t workspace_bytes,
+                                        int grad_dtype, void* dh, void* dW, void* workspace, size_t workspace_bytes,
                                         cudaStream_t stream);
 
 /* One tensor of an optimizer step. All arrays have `n` elements and start element-aligned. */

@@ -98,6 +98,14 @@ def test_fp32_gradients_of_the_c_abi(split, tol):
     G = oo.token_logprobs_grad(f64(h) @ f64(W).T, tok.cpu().numpy(), tau, f64(g), f64(g))
     for got, ref in ((dh, G @ f64(W)), (dW, G.T @ f64(h))):
         assert np.linalg.norm(f64(got) - ref) <= tol * np.linalg.norm(ref)
+    b = dict(dtype=torch.bfloat16, device="cuda")
+    for chunk in (256, 4096):  # bf16 gradients are the fp32 ones rounded: by a pass of their own, or at once (one token block)
+        wb = torch.empty(_lib.hylo_head_logprobs_workspace_bytes(N, d, V, chunk, split, torch.bfloat16), dtype=torch.uint8,
+                         device="cuda")
+        f_h, f_W, b_h, b_W = torch.empty(N, d, **f), torch.empty(V, d, **f), torch.empty(N, d, **b), torch.empty(V, d, **b)
+        _lib.hylo_head_logprobs_backward(h, W, tok, tau, chunk, lse, H, g, g, f_h, f_W, wb, split)
+        _lib.hylo_head_logprobs_backward(h, W, tok, tau, chunk, lse, H, g, g, b_h, b_W, wb, split)
+        assert torch.equal(b_h, f_h.bfloat16()) and torch.equal(b_W, f_W.bfloat16())
     again_h, again_W = torch.empty_like(dh), torch.empty_like(dW)
     _lib.hylo_head_logprobs_backward(h, W, tok, tau, 256, lse, H, g, g, again_h, again_W, ws, split)
     assert torch.equal(dh, again_h) and torch.equal(dW, again_W)
@@ -192,7 +200,7 @@ def test_first_cuda_call_of_a_thread():
 
     def work():
         st = _lib.load().hylo_head_logprobs_backward(
-            h.data_ptr(), W.data_ptr(), 20, 64, 500, 1.0, 0, tok.data_ptr(), lse.data_ptr(), None, g.data_ptr(), None, 0,
+            h.data_ptr(), W.data_ptr(), 20, 64, 500, 1.0, 0, tok.data_ptr(), lse.data_ptr(), None, g.data_ptr(), None, 0, 0,
             dh.data_ptr(), dW.data_ptr(), ws.data_ptr(), ws.numel(), stream)
         errors.append(st)
 

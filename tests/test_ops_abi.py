@@ -133,7 +133,7 @@ def test_head_logprobs_refuses(lib, kw, status):
 
 
 def _head_bwd(lib, **kw):
-    a = dict(h=FAKE, W=FAKE, N=16, d=64, V=100, tau=1.0, chunk=0, tok=FAKE, lse=FAKE, ent=FAKE, gl=FAKE, ge=FAKE, split=0,
+    a = dict(h=FAKE, W=FAKE, N=16, d=64, V=100, tau=1.0, chunk=0, tok=FAKE, lse=FAKE, ent=FAKE, gl=FAKE, ge=FAKE, split=0, dt=0,
              dh=FAKE, dW=FAKE, ws=FAKE, nbytes=1 << 30)
     a.update(kw)
     return lib.hylo_head_logprobs_backward(*a.values(), None)
@@ -142,7 +142,7 @@ def _head_bwd(lib, **kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(W=None), -1), (dict(lse=None), -1), (dict(dh=None), -1), (dict(dW=None), -1), (dict(ent=None), -1),
     (dict(N=-1), -2), (dict(d=12), -2), (dict(N=1 << 30, V=1 << 30), -2), (dict(dh=FAKE + 8), -3), (dict(gl=FAKE + 1), -3),
-    (dict(tau=float("nan")), -4), (dict(nbytes=256), -5),
+    (dict(tau=float("nan")), -4), (dict(nbytes=256), -5), (dict(dt=2), -2), (dict(dt=-1), -2), (dict(dt=1, dW=FAKE + 2), -3),
 ])
 def test_head_logprobs_backward_refuses(lib, kw, status):
     if kw.get("N") == 1 << 30:
@@ -157,6 +157,10 @@ def test_head_workspace(lib):
     assert q(4096, 2048, 128256) == ring + 256 and q(4096, 2048, 128256, split_g=True) == 2 * ring + 256
     assert q(1 << 20, 2048, 128256) == (1 << 20) * (4 + 2 * 32 * 16)
     assert q(1, 64, 256) == 3 * 256 * 256 * 2 + 256
+    bf = dict(grad_dtype=torch.bfloat16)  # the fp32 sums: of dh, and of dW where the tokens are more than one block
+    assert q(4096, 2048, 128256, **bf) == ring + 256 + 4096 * 2048 * 4
+    assert q(4097, 2048, 128256, **bf) == ring + 256 + (4097 + 128256) * 2048 * 4
+    assert q(4096, 2048, 128256, grad_dtype=torch.float16) == 0
     assert q(0, 64, 10) == 0 and q(1, 60, 10) == 0 and q(1, 64, 0) == 0
 
 
