@@ -420,11 +420,23 @@ __global__ void __launch_bounds__(256) head_combine_kernel(const HeadParams p, f
   if (lse) lse[n] = r.mx * inv_tau + log_s;
 }
 
-// Eight values per thread and step; n is a multiple of 8.
-__global__ void __launch_bounds__(256) round_bf16_kernel(const float4* __restrict__ x, uint4* __restrict__ y, int64_t n8) {
+// Eight values per thread and step.
+template <bool BF16>
+__global__ void __launch_bounds__(256) join_parts_kernel(const float4* __restrict__ x, int parts, void* __restrict__ y, int64_t n8) {
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n8; i += static_cast<int64_t>(gridDim.x) * 256) {
-    const float4 a = __ldcs(x + 2 * i), b = __ldcs(x + 2 * i + 1);
-    y[i] = make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
+    float4 a = __ldcs(x + 2 * i), b = __ldcs(x + 2 * i + 1);
+#pragma unroll 4
+    for (int k = 1; k < parts; ++k) {
+      const float4 c = __ldcs(x + 2 * (k * n8 + i)), d = __ldcs(x + 2 * (k * n8 + i) + 1);
+      a = make_float4(a.x + c.x, a.y + c.y, a.z + c.z, a.w + c.w);
+      b = make_float4(b.x + d.x, b.y + d.y, b.z + d.z, b.w + d.w);
+    }
+    if (BF16) {
+      static_cast<uint4*>(y)[i] = make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
+    } else {
+      static_cast<float4*>(y)[2 * i] = a;
+      static_cast<float4*>(y)[2 * i + 1] = b;
+    }
   }
 }
 
@@ -447,10 +459,14 @@ cudaLaunchConfig_t head_config(cudaLaunchAttribute* attr, int clusters, cudaStre
 
 }  // namespace
 
-cudaError_t launch_round_bf16(const float* x, uint16_t* y, int64_t n, int sms, cudaStream_t stream) {
+cudaError_t launch_join_parts(const float* x, int parts, void* y, bool bf16, int64_t n, int sms, cudaStream_t stream) {
   const int64_t want = (n / 8 + 255) / 256, cap = static_cast<int64_t>(sms) * 8;
-  round_bf16_kernel<<<static_cast<int>(want < cap ? want : cap), 256, 0, stream>>>(reinterpret_cast<const float4*>(x),
-                                                                                  reinterpret_cast<uint4*>(y), n / 8);
+  const int grid = static_cast<int>(want < cap ? want : cap);
+  const float4* x4 = reinterpret_cast<const float4*>(x);
+  if (bf16)
+    join_parts_kernel<true><<<grid, 256, 0, stream>>>(x4, parts, y, n / 8);
+  else
+    join_parts_kernel<false><<<grid, 256, 0, stream>>>(x4, parts, y, n / 8);
   return cudaGetLastError();
 }
 

@@ -54,9 +54,11 @@ int choose_segments(int64_t token_tiles, int64_t vtiles, int workers, int most);
 size_t bwd_bytes(int64_t N, int64_t V, int64_t token_chunk);
 // Rows of its token blocks.
 int64_t pipe_rows(int64_t N, int64_t token_chunk);
+// Words of its vocabulary blocks (pipe_setup takes another number of them in `width`, a multiple of 256, or 0).
+int64_t pipe_width(int64_t R, int64_t V);
 constexpr size_t kPipeCtrlBytes = 256;
 hylo_status pipe_setup(const uint16_t* h, const uint16_t* W, int64_t N, int64_t d, int64_t V, float tau,
-                       int64_t token_chunk, float* dh, float* dW, void* workspace, size_t g_total, bool split,
+                       int64_t token_chunk, int64_t width, float* dh, float* dW, void* workspace, size_t g_total, bool split,
                        DeviceState** dev, CUtensorMap* maps, BwdPipeParams* p, int* clusters);
 
 }  // namespace hylo

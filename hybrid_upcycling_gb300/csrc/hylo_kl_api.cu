@@ -276,10 +276,10 @@ hylo_status check_common(const void* h_s, const void* W_s, const void* h_t, cons
 // the gradients and of the G ring (maps 1 and 3, the teacher's, are the caller's), the block
 // geometry, and how many clusters to launch. The counters at p->ctrl are the caller's to clear.
 hylo_status pipe_setup(const uint16_t* h, const uint16_t* W, int64_t N, int64_t d, int64_t V, float tau,
-                       int64_t token_chunk, float* dh, float* dW, void* workspace, size_t g_total, bool split,
-                       DeviceState** dev, CUtensorMap* maps, BwdPipeParams* p, int* clusters) {
+                       int64_t token_chunk, int64_t width, float* dh, float* dW, void* workspace, size_t g_total,
+                       bool split, DeviceState** dev, CUtensorMap* maps, BwdPipeParams* p, int* clusters) {
   hylo_status st;
-  const int64_t R = pipe_rows(N, token_chunk), bw = pipe_width(R, V);
+  const int64_t R = pipe_rows(N, token_chunk), bw = width > 0 ? width : pipe_width(R, V);
   const int64_t TB = cdiv(N, R), VB = cdiv(V, bw), ntd = cdiv(d, kGemmBN);
   // work items: per block, its 256 x 256 G tiles and its dW_s and dh_s tiles (< 2^30 so that
   // the queue index and the completion counts fit their 32-bit counters)
@@ -421,7 +421,7 @@ hylo_status backward_impl(const uint16_t* h_s, const uint16_t* W_s, const uint16
   CUtensorMap maps[kPipeMaps];
   BwdPipeParams p{};
   int clusters = 0;
-  if ((st = pipe_setup(h_s, W_s, N, d_s, V, tau, token_chunk, dh_s, dW_s, workspace, g_total, split, &dev, maps,
+  if ((st = pipe_setup(h_s, W_s, N, d_s, V, tau, token_chunk, 0, dh_s, dW_s, workspace, g_total, split, &dev, maps,
                        &p, &clusters)) != HYLO_OK)
     return st;
   const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;

@@ -43,19 +43,39 @@ size_t head_fwd_bytes(int64_t N) {
   return round256(N * sizeof(float)) + static_cast<size_t>(N) * 2 * head_segments(N) * sizeof(float4);
 }
 
-// The backward's workspace: the G ring(s), the counters, and for bf16 gradients the fp32 sums that are rounded at the end.
+// The backward's workspace: the G ring(s), the counters, and the fp32 sums that are joined or rounded at the end.
 struct HeadBwd {
   size_t ctrl, dh, dW, total;
+  int64_t width;   // words of a vocabulary block, or 0 (pipe_width)
+  int64_t parts;   // dh is stored in this many parts, or 0
   bool dW_direct;  // dW is written in bf16 by the pipelined backward itself
 };
+// Few tokens: dh in parts, one per vocabulary block. A block is 8192 words (32 G tiles and, at d = 2048, 264 gradient
+// tiles for 76 clusters), less where that leaves fewer than three blocks, more where it makes more than 16. N d is bounded
+// so that a part is at most 8 MiB; with more tokens the chain of additions is short beside the rest.
+constexpr int64_t kPartTokens = 1024, kPartElems = int64_t(1) << 21, kPartWords = 8192, kMaxParts = 16;
+
 HeadBwd head_bwd_layout(int64_t N, int64_t d, int64_t V, int64_t token_chunk, bool split, int grad_dtype) {
   HeadBwd l{};
-  l.ctrl = round256(bwd_bytes(N, V, token_chunk)) * (split ? 2 : 1);
+  const int64_t R = pipe_rows(N, token_chunk);
+  size_t ring = bwd_bytes(N, V, token_chunk);
+  if (N <= R && N <= kPartTokens && N * d <= kPartElems) {
+    int64_t w = cdiv(V, kGRing) < kPartWords ? cdiv(V, kGRing) : kPartWords;
+    if (w < cdiv(V, kMaxParts)) w = cdiv(V, kMaxParts);
+    w = cdiv(w, 256) * 256;
+    if (kGRing * R * w * 2 <= kGBlockBytes) {
+      l.width = w;
+      l.parts = cdiv(V, w);
+      ring = static_cast<size_t>(kGRing) * R * w * 2;
+    }
+  }
+  l.ctrl = round256(ring) * (split ? 2 : 1);
   l.dh = l.dW = l.total = l.ctrl + kPipeCtrlBytes;
+  if (grad_dtype == HYLO_BF16 || l.parts > 0)
+    l.dW = l.total = l.dh + round256(static_cast<size_t>(l.parts > 0 ? l.parts : 1) * N * d * sizeof(float));
   if (grad_dtype == HYLO_BF16) {
-    l.dW_direct = N <= pipe_rows(N, token_chunk);
-    l.dW = l.dh + round256(static_cast<size_t>(N) * d * sizeof(float));
-    l.total = l.dW + (l.dW_direct ? 0 : round256(static_cast<size_t>(V) * d * sizeof(float)));
+    l.dW_direct = N <= R;
+    if (!l.dW_direct) l.total = l.dW + round256(static_cast<size_t>(V) * d * sizeof(float));
   }
   return l;
 }
@@ -187,13 +207,13 @@ hylo_status hylo_head_logprobs_backward(const uint16_t* h, const uint16_t* W, in
   // block, as they leave the tensor cores.
   char* ws = static_cast<char*>(workspace);
   const bool bf16 = grad_dtype == HYLO_BF16;
-  float* dh32 = bf16 ? reinterpret_cast<float*>(ws + l.dh) : static_cast<float*>(dh);
+  float* dh32 = bf16 || l.parts > 0 ? reinterpret_cast<float*>(ws + l.dh) : static_cast<float*>(dh);
   float* dW32 = l.dW_direct ? static_cast<float*>(dW) : bf16 ? reinterpret_cast<float*>(ws + l.dW) : static_cast<float*>(dW);
   DeviceState* dev = nullptr;
   CUtensorMap maps[kPipeMaps];
   BwdPipeParams p{};
   int clusters = 0;
-  if ((st = pipe_setup(h, W, N, d, V, tau, token_chunk, dh32, dW32, workspace, l.ctrl, split, &dev, maps, &p, &clusters)) !=
+  if ((st = pipe_setup(h, W, N, d, V, tau, token_chunk, l.width, dh32, dW32, workspace, l.ctrl, split, &dev, maps, &p, &clusters)) !=
       HYLO_OK)
     return st;
   maps[1] = maps[0];  // no teacher: never loaded from
@@ -201,13 +221,15 @@ hylo_status hylo_head_logprobs_backward(const uint16_t* h, const uint16_t* W, in
   if (l.dW_direct && (st = make_map_3d(&maps[7], dW, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d, V, 1, d * 2, 32, 32,
                                        CU_TENSOR_MAP_SWIZZLE_64B)) != HYLO_OK)
     return st;
-  cudaError_t e = cudaMemsetAsync(p.ctrl, 0, kPipeCtrlWords * sizeof(unsigned), stream);
+  if (l.parts > 0 && (st = make_map_3d(&maps[6], dh32, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, d, N, l.parts, d * 4, 32, 32)) != HYLO_OK)
+    return st;
+  cudaError_t e = cudaMemsetAsync(p.ctrl, 0, (kPipeCtrlWords + kGRing) * sizeof(unsigned), stream);
   if (e != cudaSuccess) return cuda_fail(e, "clear the backward's work counters");
-  const HeadGrad g{tokens, lse, entropy, g_logp, g_entropy, 1.0f / tau, l.dW_direct ? 1 : 0};
+  const HeadGrad g{tokens, lse, entropy, g_logp, g_entropy, 1.0f / tau, l.dW_direct ? 1 : 0, l.parts > 0 ? 1 : 0};
   e = launch_bwd_pipe_head(maps, p, g, clusters, stream);
-  if (e == cudaSuccess && bf16) e = launch_round_bf16(dh32, static_cast<uint16_t*>(dh), N * d, dev->sms, stream);
-  if (e == cudaSuccess && bf16 && !l.dW_direct)
-    e = launch_round_bf16(dW32, static_cast<uint16_t*>(dW), V * d, dev->sms, stream);
+  if (e == cudaSuccess && (bf16 || l.parts > 0))
+    e = launch_join_parts(dh32, l.parts > 0 ? static_cast<int>(l.parts) : 1, dh, bf16, N * d, dev->sms, stream);
+  if (e == cudaSuccess && bf16 && !l.dW_direct) e = launch_join_parts(dW32, 1, dW, true, V * d, dev->sms, stream);
   return e == cudaSuccess ? HYLO_OK : cuda_fail(e, "launch head log-probabilities backward");
 }
 

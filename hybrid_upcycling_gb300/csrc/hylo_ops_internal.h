@@ -83,9 +83,10 @@ struct HeadGrad {
   const float* g_entropy;  // or null
   float inv_tau;
   int dw_bf16;             // one token block: map kMapDW is a bf16 tensor of 32 x 32 tiles with 64-byte swizzle
+  int dh_parts;            // map kMapDh is [vocabulary blocks][N][d]: every block's part of dh apart (one token block)
 };
-// n fp32 values rounded to bf16 (16-byte aligned).
-cudaError_t launch_round_bf16(const float* x, uint16_t* y, int64_t n, int sms, cudaStream_t stream);
+// y = the sum over `parts` of x [parts][n] in ascending order, as fp32 or rounded to bf16 (n a multiple of 8, 16-byte aligned).
+cudaError_t launch_join_parts(const float* x, int parts, void* y, bool bf16, int64_t n, int sms, cudaStream_t stream);
 cudaError_t launch_bwd_pipe_head(const CUtensorMap* maps, const BwdPipeParams& p, const HeadGrad& g, int clusters,
                                  cudaStream_t stream);
 

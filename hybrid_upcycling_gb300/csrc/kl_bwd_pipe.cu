@@ -39,7 +39,11 @@
 //
 // The same launch also runs the backward of the token log-probabilities from hidden states
 // (kHead: there is no teacher; G is formed from the student tile, the row's log-sum-exp, entropy
-// and upstream gradients, see HeadGrad). Its F items take one TMEM half, like M items.
+// and upstream gradients, see HeadGrad). Its F items take one TMEM half, like M items. With few tokens
+// the additions into dh_s, one vocabulary block after another, would be a chain over the whole
+// vocabulary on a few clusters (N <= 256, V = 128256: 0.7 of 1.06 ms): there (HeadGrad::dh_parts)
+// every block stores its dh_s products apart, for a sum in fixed order afterwards, and M(b) needs
+// F(b) only, F(b) still M(b-3).
 //
 // TMEM holds two 256-column halves. An M item takes one; an F item takes one for the teacher
 // tile and the other for the student tile. The UMMA warp signals the teacher half as soon as its
@@ -139,6 +143,7 @@ __device__ __forceinline__ int items_m(const BwdPipeParams& p, int b) {
 struct Cursor {
   int j, part, base, size;
   unsigned cum_m;          // M items of the parts passed
+  unsigned cum_ms[kGRing]; // the same, per ring slot
   unsigned cum_f[kGRing];  // F items of the parts passed, per ring slot
   bool end;
 };
@@ -149,16 +154,18 @@ __device__ __forceinline__ void cursor_init(Cursor& c, const BwdPipeParams& p) {
   c.base = 0;
   c.size = items_f(p, 0);
   c.cum_m = 0;
-  for (int s = 0; s < kGRing; ++s) c.cum_f[s] = 0;
+  for (int s = 0; s < kGRing; ++s) c.cum_f[s] = c.cum_ms[s] = 0;
   c.end = false;
 }
 
 __device__ __forceinline__ void cursor_next(Cursor& c, const BwdPipeParams& p) {
   const int b = c.part == 0 ? c.j - 2 : c.j;
-  if (c.part == 0)
+  if (c.part == 0) {
     c.cum_m += 2u * static_cast<unsigned>(c.size);
-  else
+    c.cum_ms[b % kGRing] += 2u * static_cast<unsigned>(c.size);
+  } else {
     c.cum_f[b % kGRing] += 2u * static_cast<unsigned>(c.size);
+  }
   c.base += c.size;
   if (c.part == 0 && c.j < p.B) {
     c.part = 1;
@@ -184,8 +191,12 @@ __device__ __forceinline__ void cursor_next(Cursor& c, const BwdPipeParams& p) {
   c.size = c.part == 0 ? items_m(p, nb) : items_f(p, nb);
 }
 
-// The item with queue index i (the cursor only moves forward; i never decreases per caller).
-__device__ __forceinline__ Item cursor_item(Cursor& c, const BwdPipeParams& p, int i) {
+// Counter of the M items of ring slot s, where M items are counted per slot (parts).
+constexpr unsigned kSlotM = 2 + kGRing;
+
+// The item with queue index i (the cursor only moves forward; i never decreases per caller). parts: M items do not
+// depend on one another.
+__device__ __forceinline__ Item cursor_item(Cursor& c, const BwdPipeParams& p, int i, bool parts) {
   while (!c.end && i >= c.base + c.size) cursor_next(c, p);
   Item it{};
   if (c.end) {
@@ -198,7 +209,10 @@ __device__ __forceinline__ Item cursor_item(Cursor& c, const BwdPipeParams& p, i
   if (c.part == 1) {
     it.kind = kItemF;
     it.idx = local;
-    if (b >= kGRing) {  // every M item of blocks <= b - 3 (the parts passed, minus M(b-2))
+    if (parts) {  // every M item of the blocks that had this ring slot
+      it.ctr0 = kSlotM + static_cast<unsigned>(b % kGRing);
+      it.tgt0 = c.cum_ms[b % kGRing];
+    } else if (b >= kGRing) {  // every M item of blocks <= b - 3 (the parts passed, minus M(b-2))
       it.ctr0 = 1;
       it.tgt0 = c.cum_m - 2u * static_cast<unsigned>(items_m(p, b - 2));
     }
@@ -209,8 +223,10 @@ __device__ __forceinline__ Item cursor_item(Cursor& c, const BwdPipeParams& p, i
     it.idx = local < ndw ? local : local - ndw;
     it.ctr0 = 2 + g.slot;  // every F item of block b
     it.tgt0 = c.cum_f[g.slot];
-    it.ctr1 = 1;           // every M item of blocks < b
-    it.tgt1 = c.cum_m;
+    if (!parts) {
+      it.ctr1 = 1;         // every M item of blocks < b
+      it.tgt1 = c.cum_m;
+    }
   }
   return it;
 }
@@ -306,6 +322,8 @@ template <bool SPLIT, typename Head>
 __global__ void __launch_bounds__(kThreads, 1)
 bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p, const Head head) {
   constexpr bool kHead = !std::is_same<Head, NoHead>::value;
+  bool parts = false;
+  if constexpr (kHead) parts = head.dh_parts != 0;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* staging_all = smem + STAGES * STAGE_BYTES;
@@ -372,7 +390,7 @@ bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p, co
         const int slot = k % kItemDepth;
         const uint32_t par = static_cast<uint32_t>(k / kItemDepth) & 1u;
         if (!wait_bounded<true>(iempty + slot, par ^ 1u, abort_flag, p.ctl, 21)) break;
-        const Item it = cursor_item(cur, p, next_i);
+        const Item it = cursor_item(cur, p, next_i, parts);
         if (it.kind != kItemEnd) {
           next_i = static_cast<int>(atomicAdd(p.ctrl, 1u));  // the next item, fetched ahead
           // the item is published only once what it reads is complete
@@ -731,7 +749,7 @@ bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p, co
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(lead_tempty + sh * 8);
       } else {
-        ctr = 1u;
+        ctr = parts ? kSlotM + static_cast<unsigned>(g.slot) : 1u;
         const int h = hp;
         hp ^= 1;
         const bool w = wait_bounded(tfull + h, uses[h] & 1u, abort_flag, p.ctl, 33);
@@ -742,7 +760,7 @@ bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p, co
         const CUtensorMap* mc = dw ? &maps.m[kMapDW] : &maps.m[kMapDh];
         const int row = (dw ? g.v0 : g.r0) + mi * BN + static_cast<int>(rank) * kBM + q * 32;
         const int rows_total = dw ? p.V : p.N;
-        const bool accumulate = dw ? g.tb > 0 : g.vb > 0;
+        const bool accumulate = dw ? g.tb > 0 : g.vb > 0 && !parts;
         const int col0 = nj * BN + hc * HB;
         const int n_valid = p.d_s - col0;
         const uint32_t acc = lane_base + static_cast<uint32_t>(h * BN);
@@ -791,7 +809,9 @@ bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p, co
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0 && row < rows_total) {
-            if (accumulate)
+            if (kHead && parts && !dw)
+              tma_store_3d(mc, staging, col0 + ch * 32, row, g.vb);
+            else if (accumulate)
               tma_reduce_add_2d(mc, staging, col0 + ch * 32, row);
             else
               tma_store_2d(mc, staging, col0 + ch * 32, row);

@@ -56,8 +56,9 @@ hylo_status hylo_token_logprobs_backward(const void* z, int dtype, int64_t N, in
  * concerned are NaN or infinite). tokens as above. entropy and lse may be NULL; the backward needs lse
  * (and entropy, if g_entropy is given). workspace: at least hylo_head_logprobs_workspace_bytes(),
  * 256-byte aligned, not shared with a call still running on another stream; the forward uses O(N) of it,
- * the backward the G ring of hylo_kl_backward (at most 128 MiB, twice that with split_g) and, for
- * bf16 gradients, the fp32 sums behind them: N d, and V d if N is more than one token block.
+ * the backward the G ring of hylo_kl_backward (at most 128 MiB, twice that with split_g), the fp32
+ * parts that dh is joined from where N <= 1024 (at most 128 MiB) and, for bf16 gradients, the fp32
+ * sums behind them: N d, and V d if N is more than one token block.
  * Returns 0 for invalid sizes; token_chunk <= 0 means 4096; grad_dtype as in the backward. */
 size_t hylo_head_logprobs_workspace_bytes(int64_t N, int64_t d, int64_t V, int64_t token_chunk, int split_g,
                                           int grad_dtype);
