@@ -10,7 +10,7 @@ called directly (the functions of the same names in ``_lib`` check their argumen
 """
 from __future__ import annotations
 
-from typing import NamedTuple, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -187,14 +187,15 @@ class _HeadLogprobs(torch.autograd.Function):
 
 
 def head_logprobs(h: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, tau: float = 1.0, token_chunk: int = 4096,
-                  split_g: bool = False) -> Tuple[torch.Tensor, torch.Tensor]:
+                  split_g: Optional[bool] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Log-probabilities of ``tokens`` [...] (int64) under softmax(h W^T / tau) and the entropies, for final hidden
     states h [..., d] and an LM head W [V, d] in bfloat16 (d a multiple of 8); the logits are never stored.
 
     A negative token is ignored (log-probability 0, no gradient). Both results are differentiable
     with respect to h and W (bfloat16 gradients; the C ABI gives fp32). token_chunk and split_g as in
     fused_hidden_state_kl: the backward's token block, and whether the gradient of the logits is
-    kept to 16 bits of precision instead of 8 inside the gradient products."""
+    kept to 16 bits of precision instead of 8 inside the gradient products (None: for up to 64 tokens, where that
+    rounding does not average out: relative error 3e-3 of the gradients against 1.7e-3 with both terms)."""
     shape = h.shape
     if h.dtype != torch.bfloat16 or W.dtype != torch.bfloat16 or not shape or W.dim() != 2 or shape[-1] != W.shape[1]:
         raise ValueError("h [..., d] and W [V, d] must be bfloat16 with the same hidden size")
@@ -205,7 +206,8 @@ def head_logprobs(h: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, tau: f
     hh, t = (h, tokens) if plain else (h.reshape(-1, shape[-1]), tokens.reshape(-1))
     hh, WW, t = hh.contiguous(), W.contiguous(), t.contiguous()
     if (h.requires_grad or W.requires_grad) and torch.is_grad_enabled():
-        logp, entropy = _HeadLogprobs.apply(hh, WW, t, float(tau), int(token_chunk), bool(split_g), dev)
+        logp, entropy = _HeadLogprobs.apply(hh, WW, t, float(tau), int(token_chunk),
+                                            hh.shape[0] <= 64 if split_g is None else bool(split_g), dev)
     else:
         logp, entropy, _ = _head_forward(hh, WW, t, float(tau), dev, False)
     return (logp, entropy) if plain else (logp.view(tokens.shape), entropy.view(tokens.shape))
