@@ -147,7 +147,7 @@ __device__ __forceinline__ float round_bf16(float w, uint32_t bits) {
 }
 
 // The step with fp32 moments. P, G: types of parameter and gradient; MASTER: the step is taken on fp32 masters.
-// HBM-bound: XXX.
+// HBM-bound: 385M bf16 elements with masters and fp32 gradients in 1640 us, 7.0 TB/s.
 template <typename P, typename G, bool MASTER, int CAP>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamTable<CAP> tab, const AdamWHyper h) {
   constexpr bool kRandomParam = sizeof(P) == 2 && !MASTER;
@@ -244,13 +244,13 @@ struct Raw8 {
   }
 };
 
-__device__ __forceinline__ uint2 load_codes(const uint8_t* p, int64_t i, int left, bool vec) {
+__device__ __forceinline__ uint2 load_codes(const uint8_t* p, int i, int left, bool vec) {
   if (vec && left >= 8) return *reinterpret_cast<const uint2*>(p + i);
   uint2 w = make_uint2(0u, 0u);
   for (int j = 0; j < left; ++j) (j < 4 ? w.x : w.y) |= static_cast<uint32_t>(p[i + j]) << (8 * (j & 3));
   return w;
 }
-__device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int left, bool vec, uint2 w) {
+__device__ __forceinline__ void store_codes(uint8_t* p, int i, int left, bool vec, uint2 w) {
   if (vec && left >= 8) {
     *reinterpret_cast<uint2*>(p + i) = w;
   } else {
@@ -273,27 +273,41 @@ __device__ __forceinline__ uint32_t tops4(uint32_t a, uint32_t b, uint32_t c, ui
   return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
 }
 
+// Small thread blocks, many per SM: their loads and arithmetic then fall at different times (200M bf16 elements
+// without masters: 389 us with 256 threads, 357 with 128).
+constexpr int kThreads8 = 128;
+constexpr int kWarps8 = kThreads8 / 32;
+constexpr int kBlocks8 = 9;  // thread blocks per SM
 // Blocks per warp: enough that a thread block's set-up (finding its tensor, the clip factor) is paid rarely, but no more
-// than leave every SM four thread blocks (200M bf16 elements without masters: 493 us with one, 433 with 4,
-// 404 with 16).
+// than leave every SM its thread blocks (one block per warp: a quarter slower; 32: 3% slower).
 constexpr int kMaxSteps8 = 16;
 
-// The step with 8-bit moments. Eight elements of a lane in packed fp32 pairs.
-// Bound by instructions, not by HBM: XXX.
+// The step with 8-bit moments. Eight elements of a lane in packed fp32 pairs. 200M elements: fp32 parameters and
+// gradients 473 us, bf16 with masters and fp32 gradients 538 us, both at the copy rate of HBM (6.7 TB/s); bf16 with bf16
+// gradients 357 us, 5.6 TB/s: 54 instructions per element, 9 of them for its random bits, at 0.65 per clock
+// and scheduler come near the time of its 10 bytes.
 template <typename P, typename G, bool MASTER, int CAP>
-__global__ void __launch_bounds__(kThreads, 4) adamw8_kernel(const __grid_constant__ AdamTable<CAP> tab, const AdamWHyper h) {
+__global__ void __launch_bounds__(kThreads8, kBlocks8) adamw8_kernel(const __grid_constant__ AdamTable<CAP> tab, const AdamWHyper h) {
   using W = typename std::conditional<MASTER, float, P>::type;
   constexpr bool kRandomParam = sizeof(P) == 2 && !MASTER;
   float gs;
   if (!gradient_factor(h, gs)) return;
   const AdamTensor& t = tab.t[find_entry(tab, blockIdx.x)];
-  const int64_t chunk = static_cast<int64_t>(tab.steps) * (kWarps * kBlock);
   const int lane = threadIdx.x & 31;
   const bool vec = t.vec != 0;
-  const W* wp = MASTER ? reinterpret_cast<const W*>(t.master) : static_cast<const W*>(t.p);
-  uint8_t* mp = static_cast<uint8_t*>(t.m);
-  uint8_t* vp = static_cast<uint8_t*>(t.v);
   const float gm = gs * h.one_minus_beta1, gv = gs * sqrtf(h.one_minus_beta2), rb2 = sqrtf(h.beta2);
+  // Everything of the entry that the loop needs, relative to this thread block's first element and this lane's place.
+  const int64_t first = static_cast<int64_t>(blockIdx.x - t.chunk0) * tab.steps * (kWarps8 * kBlock);
+  const int count = static_cast<int>(min(t.n - first, static_cast<int64_t>(tab.steps) * (kWarps8 * kBlock)));
+  W* const wp = (MASTER ? reinterpret_cast<W*>(t.master) : static_cast<W*>(t.p)) + first;
+  P* const pp = static_cast<P*>(t.p) + first;
+  const G* const gp = static_cast<const G*>(t.g) + first;
+  uint8_t* const mp = static_cast<uint8_t*>(t.m) + first;
+  uint8_t* const vp = static_cast<uint8_t*>(t.v) + first;
+  int8_t* const me = t.me + first / kBlock;
+  int8_t* const ve = t.ve + first / kBlock;
+  const uint64_t pos = t.pos + static_cast<uint64_t>(first);
+  const float decay = t.decay, step = -t.step;
 
   struct Block {
     Raw8<W> w;
@@ -301,25 +315,17 @@ __global__ void __launch_bounds__(kThreads, 4) adamw8_kernel(const __grid_consta
     uint2 m, v;
     float sm, sv;  // the blocks' powers of two
   };
-  auto load = [&](Block& b, int64_t b0) {
-    const int64_t i = b0 + lane * 8;
-    const int left = static_cast<int>(max(int64_t(0), min(int64_t(8), t.n - i)));
-    b.w.load(wp, i, left, vec);
-    b.g.load(static_cast<const G*>(t.g), i, left, vec);
-    b.m = load_codes(mp, i, left, vec);
-    b.v = load_codes(vp, i, left, vec);
-    b.sm = pow2(t.me[b0 / kBlock]);
-    b.sv = pow2(t.ve[b0 / kBlock]);
-  };
-  int64_t b0 = static_cast<int64_t>(blockIdx.x - t.chunk0) * chunk + (threadIdx.x >> 5) * kBlock;
-  if (b0 >= t.n) return;
-  const int64_t end = min(t.n, (static_cast<int64_t>(blockIdx.x - t.chunk0) + 1) * chunk);
 #pragma unroll 1
-  for (; b0 < end; b0 += kWarps * kBlock) {
+  for (int b0 = (threadIdx.x >> 5) * kBlock; b0 < count; b0 += kWarps8 * kBlock) {
+    const int i = b0 + lane * 8;
+    const int left = max(0, min(8, count - i));
     Block cur;
-    load(cur, b0);
-    const int64_t i = b0 + lane * 8;
-    const int left = static_cast<int>(max(int64_t(0), min(int64_t(8), t.n - i)));
+    cur.w.load(wp, i, left, vec);
+    cur.g.load(gp, i, left, vec);
+    cur.m = load_codes(mp, i, left, vec);
+    cur.v = load_codes(vp, i, left, vec);
+    cur.sm = pow2(me[b0 / kBlock]);
+    cur.sv = pow2(ve[b0 / kBlock]);
     const float2 b1 = both(h.beta1 * cur.sm), b2 = both(rb2 * cur.sv);
     float2 w[4], m[4], r[4];
     float mtop = 0.f, rtop = 0.f;
@@ -334,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 4) adamw8_kernel(const __grid_consta
       r[j] = make_float2(sqrt_ftz(v.x), sqrt_ftz(v.y));
       const float2 den = __ffma2_rn(r[j], both(h.rbc2), both(h.eps));
       const float2 u = __fmul2_rn(m[j], make_float2(rcp_ftz(den.x), rcp_ftz(den.y)));
-      w[j] = __ffma2_rn(u, both(-t.step), __fmul2_rn(cur.w.pair(j), both(t.decay)));
+      w[j] = __ffma2_rn(u, both(step), __fmul2_rn(cur.w.pair(j), both(decay)));
       mtop = fmaxf(mtop, fmaxf(fabsf(m[j].x), fabsf(m[j].y)));
       rtop = fmaxf(rtop, fmaxf(r[j].x, r[j].y));
       odd = __ffma2_rn(w[j], make_float2(0.f, 0.f), odd);
@@ -343,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 4) adamw8_kernel(const __grid_consta
     const int er = block_exponent(__reduce_max_sync(~0u, __float_as_uint(rtop)));
     const float2 im = both(pow2(-em)), ir = both(pow2(-er)), low = both(7.52316384526264e-37f);  // 2^-120
     uint32_t bits[8];
-    random8(h.seed, t.pos + static_cast<uint64_t>(i), bits);
+    random8(h.seed, pos + static_cast<uint64_t>(i), bits);
     uint2 mc, rc;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -381,13 +387,13 @@ __global__ void __launch_bounds__(kThreads, 4) adamw8_kernel(const __grid_consta
     store_codes(mp, i, left, vec, mc);
     store_codes(vp, i, left, vec, rc);
     if (lane == 0) {
-      t.me[b0 / kBlock] = static_cast<int8_t>(em);
-      t.ve[b0 / kBlock] = static_cast<int8_t>(er);
+      me[b0 / kBlock] = static_cast<int8_t>(em);
+      ve[b0 / kBlock] = static_cast<int8_t>(er);
     }
     float wf[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) wf[2 * j] = w[j].x, wf[2 * j + 1] = w[j].y;
-    if (MASTER) store8(t.master, i, left, vec, wf);
+    if constexpr (MASTER) store8(wp, i, left, vec, wf);
     if constexpr (kRandomParam) {
       uint32_t wb[8];  // rounded in the upper half
 #pragma unroll
@@ -397,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 4) adamw8_kernel(const __grid_consta
         for (int j = 0; j < 8; ++j)
           if (!isfinite(wf[j])) wb[j] = isnan(wf[j]) ? 0x7fc00000u : __float_as_uint(wf[j]);
       }
-      uint16_t* dst = static_cast<uint16_t*>(t.p) + i;
+      uint16_t* dst = reinterpret_cast<uint16_t*>(pp) + i;
       if (vec && left >= 8) {
         *reinterpret_cast<uint4*>(dst) = make_uint4(__byte_perm(wb[0], wb[1], 0x7632), __byte_perm(wb[2], wb[3], 0x7632),
                                                     __byte_perm(wb[4], wb[5], 0x7632), __byte_perm(wb[6], wb[7], 0x7632));
@@ -407,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 4) adamw8_kernel(const __grid_consta
           if (j < left) dst[j] = static_cast<uint16_t>(wb[j] >> 16);
       }
     } else {
-      store8(static_cast<P*>(t.p), i, left, vec, wf);
+      store8(pp, i, left, vec, wf);
     }
   }
 }
@@ -494,7 +500,8 @@ cudaError_t step_list(const hylo_adamw_tensor* tensors, int count, double bias1,
   AdamTable<CAP> tab;
   int64_t total = 0;
   for (int k = 0; k < count; ++k) total += tensors[k].n;
-  const int64_t fill = total / (static_cast<int64_t>(4) * sms * kChunk);
+  const int64_t unit = BITS8 ? kWarps8 * kBlock : kChunk;  // elements of a thread block and step
+  const int64_t fill = total / (static_cast<int64_t>(kBlocks8) * sms * unit);
   tab.steps = BITS8 ? static_cast<int>(fill < 1 ? 1 : fill > kMaxSteps8 ? kMaxSteps8 : fill) : 1;
   uint64_t pos = 0;
   int i = 0;
@@ -504,7 +511,7 @@ cudaError_t step_list(const hylo_adamw_tensor* tensors, int count, double bias1,
     for (; i < count && tab.count < CAP; ++i) {
       const hylo_adamw_tensor& x = tensors[i];
       const uint64_t padded = static_cast<uint64_t>((x.n + kBlock - 1) / kBlock) * kBlock;
-      const int64_t chunk = static_cast<int64_t>(tab.steps) * kChunk;
+      const int64_t chunk = tab.steps * unit;
       const int64_t need = (x.n + chunk - 1) / chunk;
       if (need > 0) {
         if (chunks + static_cast<uint64_t>(need) > 0x7fffffffu) break;  // the grid is full: next launch
@@ -523,7 +530,7 @@ cudaError_t step_list(const hylo_adamw_tensor* tensors, int count, double bias1,
     }
     if (tab.count == 0) continue;
     if (BITS8)
-      adamw8_kernel<P, G, MASTER, CAP><<<chunks, kThreads, 0, stream>>>(tab, h);
+      adamw8_kernel<P, G, MASTER, CAP><<<chunks, kThreads8, 0, stream>>>(tab, h);
     else
       adamw_kernel<P, G, MASTER, CAP><<<chunks, kThreads, 0, stream>>>(tab, h);
     const cudaError_t e = cudaGetLastError();

@@ -702,11 +702,14 @@ token_logprobs_kernel(const TokenRows in, const TokenOut out, int span, int vec_
   if (S > 1) cluster_wait();
 }
 
+constexpr int kStreamWarps = 8;  // warps of a CTA that shares a row
+
 // Many whole rows with alternatives: eight warps stream row after row and never wait for a selection; a ninth warp joins
 // each row's sums and chooses its alternatives while the next row streams. (8192 x 128256, 16 alternatives: with the eight
 // warps choosing between rows, 489 us; so, XXX us.)
-constexpr int kStreamWarps = 8;
-constexpr int kRowThreads = 32 * (kStreamWarps + 1);
+constexpr int kRowWarps = 8;
+constexpr int kRowThreads = 32 * (kRowWarps + 1);
+constexpr int kRowBlocks = 4;  // thread blocks per SM
 
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
@@ -716,21 +719,21 @@ __device__ __forceinline__ void bar_arrive(int id, int threads) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads, 4)
+__global__ void __launch_bounds__(kRowThreads, kRowBlocks)
 token_logprobs_rows_kernel(const TokenRows in, const TokenOut out, int vec_shift) {
-  __shared__ Sums warp_sums[2][kStreamWarps];
+  __shared__ Sums warp_sums[2][kRowWarps];
   __shared__ uint32_t group_key[2][kMaxGroups];
   __shared__ Choice<1> choice;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // Barriers 1, 2: buffer 0, 1 full; 3, 4: free again.
   int buf = 0;
-  if (warp < kStreamWarps) {
+  if (warp < kRowWarps) {
     bool first[2] = {true, true};
     for (int64_t n = blockIdx.x; n < in.N; n += gridDim.x, buf ^= 1) {
       const Row<T> row(in.z, n * in.ld, in.V);
       if (!(buf == 0 ? first[0] : first[1])) bar_sync(3 + buf, kRowThreads);
       (buf == 0 ? first[0] : first[1]) = false;
-      const Sums r = stream_row<T, kStreamWarps, true>(row, 0, blocks_of(row), vec_shift, in.c, warp, lane, group_key[buf]);
+      const Sums r = stream_row<T, kRowWarps, true>(row, 0, blocks_of(row), vec_shift, in.c, warp, lane, group_key[buf]);
       if (lane == 0) warp_sums[buf][warp] = r;
       __threadfence_block();
       bar_arrive(1 + buf, kRowThreads);
@@ -739,7 +742,7 @@ token_logprobs_rows_kernel(const TokenRows in, const TokenOut out, int vec_shift
     for (int64_t n = blockIdx.x; n < in.N; n += gridDim.x, buf ^= 1) {
       const Row<T> row(in.z, n * in.ld, in.V);
       bar_sync(1 + buf, kRowThreads);
-      const Sums r = join_lanes(warp_sums[buf][lane & (kStreamWarps - 1)], kStreamWarps, in.c);
+      const Sums r = join_lanes(warp_sums[buf][lane & (kRowWarps - 1)], kRowWarps, in.c);
       const float log_s = logf(r.s);
       if (lane == 0) write_row(in, out, n, row, r, log_s);
       best_words<T>(choice, group_key[buf], row, groups_of(row, vec_shift), out.k, lane);
@@ -876,7 +879,7 @@ cudaError_t launch_fwd(const TokenRows& in, const TokenOut& out, const TokenOccu
   if (blocks <= kShortRow && in.N >= 4 * occ.sms)
     return launch_split<T, 1, kTop>(in, out, 1, 32 * occ.sms, blocks, vec_shift, stream);
   const int S = choose_split(in.N, blocks, kTop ? kTopCost : kJoinCost, occ);
-  const int whole = 4 * occ.sms;  // CTAs at once that take whole rows
+  const int whole = kRowBlocks * occ.sms;  // CTAs at once that take whole rows
   if (kTop && in.N > whole) {
     // whole rows, their alternatives chosen beside the streaming: a row costs its words alone
     int i = 0;

@@ -116,7 +116,8 @@ hylo_status hylo_grad_norm(const void* const* grads, const int64_t* sizes, int c
  * that the block's largest magnitude lies in [128, 256) 2^e (e within [-120, 120]; -120 for a
  * block of zeros) and each magnitude x 2^-e is rounded to a neighbouring e4m3 value, up with
  * the probability of the part cut off, so that small steady changes are not lost (to nearest,
- * 0.999 v would round back to v for ever). A non-zero r is never stored as 0.
+ * 0.999 v would round back to v for ever). A non-zero r is never stored as 0. eps must be > 0 (v below
+ * 2^-126 counts as 0). A value that is not finite is stored as NaN.
  * The random bits: element j of tensor i has position c = B_i + j, B_i = the sum of the sizes
  * of the tensors before it, each rounded up to 256; with mix = the 32-bit finaliser of
  * MurmurHash3 (public domain), low/high the halves of c,

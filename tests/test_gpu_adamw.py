@@ -158,6 +158,19 @@ def test_a_norm_that_is_not_finite_skips_the_step(bits, bad):
         assert torch.equal(a, b) if isinstance(a, torch.Tensor) else np.array_equal(a, b)
 
 
+def test_8bit_states_of_values_that_are_not_finite():
+    """Without a norm nothing guards the states: what is not finite becomes NaN, in its own element only (an infinite
+    gradient takes its block's scale with it), and bf16 parameters follow."""
+    n = 600
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        p, g, m, v, _ = model([n], "bf16", torch.float32, 8)
+        g[0][300] = bad
+        adamw_step(p, g, m, v, step=3, seed=1, **HYPER)
+        for s in (m[0], v[0]):
+            assert torch.isnan(s.values()[300]) and torch.isfinite(s.values()).sum() == n - 1
+        assert not torch.isfinite(p[0][300]) and torch.isfinite(p[0]).sum() == n - 1
+
+
 def test_scale_and_clip_do_what_they_say():
     """grad_scale s with gradients g is the step with gradients s g; a norm under max_norm clips nothing."""
     p, g, m, v, _ = model([3000], "fp32", torch.float32, 32)

@@ -80,7 +80,7 @@ def _step(lib, tensors=None, pdt=0, gdt=0, bits=32, b1=0.9, b2=0.999, eps=1e-8, 
 @pytest.mark.parametrize("kw,status", [
     (dict(p=0), -1), (dict(g=0), -1), (dict(m=0), -1), (dict(v=0), -1), (dict(bits=8, me=0), -1),
     (dict(bits=8, ve=0), -1), (dict(pdt=2), -2), (dict(gdt=2), -2), (dict(bits=16), -2), (dict(n=-1), -2),
-    (dict(b1=1.0), -2), (dict(b2=-0.1), -2), (dict(eps=-1.0), -2), (dict(step=0), -2), (dict(w=FAKE), -2),
+    (dict(bits=8, eps=0.0), -2), (dict(b1=1.0), -2), (dict(b2=-0.1), -2), (dict(eps=-1.0), -2), (dict(step=0), -2), (dict(w=FAKE), -2),
     (dict(pdt=1, tensors=[dict(w=FAKE), dict(w=0)]), -2), (dict(b1=float("nan")), -2),
     (dict(p=FAKE + 2), -3), (dict(m=FAKE + 1), -3), (dict(lr=float("inf")), -4), (dict(wd=float("nan")), -4),
     (dict(scale=float("inf")), -4), (dict(norm=FAKE, max_norm=0.0), -4),
