@@ -304,55 +304,72 @@ __device__ void rank_groups(Choice<kWarps>& sh, uint32_t* group_key, int groups,
   if (tid < groups && gt == kk - 1) sh.bound_key = kk == k ? mine & kHigh : 0u;  // fewer groups than k: any word may count
 }
 
-// One warp: a search for the kk-th largest, which takes fewer instructions; sh.sel ascends by position.
+// One warp: a search for the kk-th largest, bit by bit below the bits that the largest and the smallest maximum share,
+// until exactly kk maxima reach t. Fewer instructions than the ranks. sh.sel ascends by position.
 template <typename T, int kWarps>
 __device__ void choose_groups(Choice<kWarps>& sh, const uint32_t* group_key, int groups, int kk, int k) {
   constexpr uint32_t kHigh = Elem<T>::kKeyBits == 32 ? ~0u : ~0u << (32 - Elem<T>::kKeyBits);
   constexpr int kPer = kMaxGroups / 32;
   const int lane = threadIdx.x & 31;
-  uint32_t t = 0;  // two bits at a time from the top: the largest t that at least kk maxima reach
-  {
-    uint32_t key[kPer];
+  uint32_t key[kPer], low = ~0u, high = 0u;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) key[j] = j * 32 + lane < groups ? group_key[j * 32 + lane] & kHigh : 0u;
+  for (int j = 0; j < kPer; ++j) {
+    const bool real = j * 32 + lane < groups;
+    key[j] = real ? group_key[j * 32 + lane] & kHigh : 0u;  // 0: below every key
+    low = real ? min(low, key[j]) : low;
+    high = max(high, key[j]);
+  }
+  low = __reduce_min_sync(~0u, low);
+  high = __reduce_max_sync(~0u, high);
+  uint32_t t = low;  // at least kk maxima reach t
+  if (low != high && groups > kk) {
+    const int top = 31 - __clz(static_cast<int>(low ^ high));
+    t = high & ~((2u << top) - 1u);
 #pragma unroll 1
-    for (int shift = 30; shift + 2 > 32 - Elem<T>::kKeyBits; shift -= 2) {
-      const uint32_t p1 = t | (1u << shift), p2 = t | (2u << shift), p3 = t | (3u << shift);
-      int h1 = 0, h2 = 0, h3 = 0;
+    for (int bit = top; bit >= 32 - Elem<T>::kKeyBits; --bit) {
+      const uint32_t probe = t | (1u << bit);
+      int h0 = 0, h1 = 0;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        h1 += key[j] >= p1;
-        h2 += key[j] >= p2;
-        h3 += key[j] >= p3;
+      for (int j = 0; j < kPer; j += 2) {
+        h0 += key[j] >= probe;
+        h1 += key[j + 1] >= probe;
       }
-      h1 = __reduce_add_sync(~0u, h1 | (h2 << 16));  // at most 256 each
-      h3 = __reduce_add_sync(~0u, h3);
-      t = h3 >= kk ? p3 : (h1 >> 16) >= kk ? p2 : (h1 & 0xffff) >= kk ? p1 : t;
+      const int have = __reduce_add_sync(~0u, h0 + h1);
+      if (have >= kk) t = probe;
+      if (have == kk) break;
     }
   }
   int over = 0;
-#pragma unroll 1
-  for (int g = lane; g < groups; g += 32) over += (group_key[g] & kHigh) > t;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) over += key[j] > t;
   int equal_left = kk - __reduce_add_sync(~0u, over), placed = 0;  // equal maxima: the first groups
   const uint32_t below = (1u << lane) - 1u;
-#pragma unroll 1
-  for (int g0 = 0; g0 < groups; g0 += 32) {
-    const uint32_t key = g0 + lane < groups ? group_key[g0 + lane] & kHigh : 0u;
-    const uint32_t eqs = __ballot_sync(~0u, key == t);
-    const bool take = key > t || (key == t && __popc(eqs & below) < equal_left);
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const uint32_t eqs = __ballot_sync(~0u, key[j] == t);
+    const bool take = key[j] > t || (key[j] == t && __popc(eqs & below) < equal_left);
     const uint32_t takes = __ballot_sync(~0u, take);
-    if (take) sh.sel[placed + __popc(takes & below)] = g0 + lane;
+    if (take) sh.sel[placed + __popc(takes & below)] = j * 32 + lane;
     placed += __popc(takes);
     equal_left -= min(equal_left, __popc(eqs));
   }
   if (lane == 0) sh.bound_key = kk == k ? t : 0u;  // fewer groups than k: any word may be among the k
 }
 
+// 16-byte copy into shared memory in the background of this thread.
+__device__ __forceinline__ void copy_async(uint4* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_u32(dst)), "l"(__cvta_generic_to_global(src)) : "memory");
+}
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // The row's best k words into sh.top, in order, from its group maxima. `tid` counts the threads of the kWarps warps.
-// Begins and ends with a barrier of those.
-template <typename T, int kWarps>
+// Begins and ends with a barrier of those. stage: shared memory for kStage vectors (16 bytes each) through which the chosen
+// groups are read, all of a stage in flight at once; or null: through registers, kFirst per thread.
+constexpr int kStage = 1024;
+
+template <typename T, int kWarps, bool kStaged = false>
 __device__ void best_words(Choice<kWarps>& sh, uint32_t* group_key, const Row<T>& row, const Groups gr, int k,
-                           int tid) {
+                           int tid, uint4* stage = nullptr) {
   constexpr int VE = Elem<T>::kVec;
   constexpr uint32_t kHigh = Elem<T>::kKeyBits == 32 ? ~0u : ~0u << (32 - Elem<T>::kKeyBits);
   constexpr int kCand = Choice<kWarps>::kCand;
@@ -378,6 +395,32 @@ __device__ void best_words(Choice<kWarps>& sh, uint32_t* group_key, const Row<T>
   };
   // The vectors with a word not below the bound are set down in shared memory, and then every thread looks at
   // one word of them. That is all unless very many words equal the bound.
+  auto look = [&](int64_t t, uint4 v) {
+    if ((order_key(Elem<T>::vec_max(v)) & kHigh) >= bound) {
+      const int at = atomicAdd(&sh.hits, 1);
+      if (at < Choice<kWarps>::kHits) {
+        sh.hit_vec[at] = v;
+        sh.hit_at[at] = static_cast<int>(vector_at(t) / VE);
+      }
+    }
+  };
+  if constexpr (kStaged) {
+#pragma unroll 1
+    for (int64_t t0 = 0; t0 < nv; t0 += kStage) {
+      const int m = static_cast<int>(min(nv - t0, static_cast<int64_t>(kStage)));
+#pragma unroll 4
+      for (int i = tid; i < m; i += kWarps * 32) {
+        const int64_t u = vector_at(t0 + i);
+        if (row.inside(u, u + VE))
+          copy_async(stage + i, row.base + u);
+        else
+          stage[i] = row.edge(u);
+      }
+      copy_wait();  // every thread reads back what it copied
+#pragma unroll 4
+      for (int i = tid; i < m; i += kWarps * 32) look(t0 + i, stage[i]);
+    }
+  } else
 #pragma unroll 1
   for (int64_t t0 = tid; t0 < nv; t0 += kWarps * kFirst * 32) {
     uint4 v[kFirst];
@@ -387,13 +430,7 @@ __device__ void best_words(Choice<kWarps>& sh, uint32_t* group_key, const Row<T>
 #pragma unroll
     for (int i = 0; i < kFirst; ++i) {
       const int64_t t = t0 + i * kWarps * 32;
-      if (t < nv && (order_key(Elem<T>::vec_max(v[i])) & kHigh) >= bound) {
-        const int at = atomicAdd(&sh.hits, 1);
-        if (at < Choice<kWarps>::kHits) {
-          sh.hit_vec[at] = v[i];
-          sh.hit_at[at] = static_cast<int>(vector_at(t) / VE);
-        }
-      }
+      if (t < nv) look(t, v[i]);
     }
   }
   sync_warps<kWarps>();
@@ -598,16 +635,20 @@ __device__ __forceinline__ Sums stream_row(const Row<T>& row, int blk0, int blk1
   return join_lanes(r, 32, c);
 }
 
-// Row n's results but the alternatives; one thread.
+// The logit of token t, if it is one.
 template <typename T>
-__device__ __forceinline__ void write_row(const TokenRows& in, const TokenOut& out, int64_t n, const Row<T>& row, const Sums& r,
+__device__ __forceinline__ float token_logit(const TokenRows& in, const Row<T>& row, int64_t t) {
+  return t >= 0 && t < in.V ? Elem<T>::get(row.base[t + row.lead]) : 0.f;
+}
+
+// Row n's results but the alternatives, for its token t of logit zt; one thread.
+__device__ __forceinline__ void write_row(const TokenRows& in, const TokenOut& out, int64_t n, int64_t t, float zt, const Sums& r,
                                           float log_s) {
-  const int64_t t = in.tokens[n];
   float lp = 0.f;
   if (t >= in.V)
     lp = __uint_as_float(0x7fffffffu);
   else if (t >= 0)
-    lp = r.mx == -INFINITY ? -INFINITY : (Elem<T>::get(row.base[t + row.lead]) - r.mx) * in.inv_tau - log_s;
+    lp = r.mx == -INFINITY ? -INFINITY : (zt - r.mx) * in.inv_tau - log_s;
   out.logp[n] = lp;
   if (out.entropy) out.entropy[n] = r.mx == -INFINITY ? 0.f : log_s - kLn2F * r.a / r.s;
   if (out.lse) out.lse[n] = r.mx == -INFINITY ? -INFINITY : r.mx * in.inv_tau + log_s;
@@ -661,6 +702,12 @@ token_logprobs_kernel(const TokenRows in, const TokenOut out, int span, int vec_
 
   for (int64_t n = blockIdx.x / S; n < in.N; n += gridDim.x / S) {
     const Row<T> row(in.z, n * in.ld, in.V);
+    int64_t token = -1;  // thread 0's, early: its logit waits for it
+    float zt = 0.f;
+    if (tid == 0 && q == 0) {
+      token = in.tokens[n];
+      zt = token_logit(in, row, token);
+    }
     const int all_blocks = blocks_of(row);
     const int blk0 = min(all_blocks, static_cast<int>(q) * span), blk1 = min(all_blocks, blk0 + span);
     Sums r = stream_row<T, kWarps, kTop>(row, blk0, blk1, vec_shift, in.c, warp, lane, sh.group_key);
@@ -689,7 +736,7 @@ token_logprobs_kernel(const TokenRows in, const TokenOut out, int span, int vec_
     }
     if (q == 0) {
       const float log_s = logf(r.s);
-      if (tid == 0) write_row(in, out, n, row, r, log_s);
+      if (tid == 0) write_row(in, out, n, token, zt, r, log_s);
       if constexpr (kTop) {
         __syncthreads();  // (one warp: its group maxima)
         best_words<T>(sh.choice, sh.group_key, row, groups_of(row, vec_shift), out.k, tid);
@@ -724,6 +771,7 @@ token_logprobs_rows_kernel(const TokenRows in, const TokenOut out, int vec_shift
   __shared__ Sums warp_sums[2][kRowWarps];
   __shared__ uint32_t group_key[2][kMaxGroups];
   __shared__ Choice<1> choice;
+  __shared__ uint4 stage[kStage];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // Barriers 1, 2: buffer 0, 1 full; 3, 4: free again.
   int buf = 0;
@@ -739,13 +787,20 @@ token_logprobs_rows_kernel(const TokenRows in, const TokenOut out, int vec_shift
       bar_arrive(1 + buf, kRowThreads);
     }
   } else {
-    for (int64_t n = blockIdx.x; n < in.N; n += gridDim.x, buf ^= 1) {
+    // A row's token is loaded two rows ahead and its logit one, so that neither load is waited for.
+    const int64_t stride = gridDim.x;
+    int64_t n0 = blockIdx.x, token = n0 < in.N ? in.tokens[n0] : -1, token1 = n0 + stride < in.N ? in.tokens[n0 + stride] : -1;
+    float zt = n0 < in.N ? token_logit(in, Row<T>(in.z, n0 * in.ld, in.V), token) : 0.f;
+    for (int64_t n = n0; n < in.N; n += stride, buf ^= 1) {
       const Row<T> row(in.z, n * in.ld, in.V);
+      const int64_t token2 = n + 2 * stride < in.N ? in.tokens[n + 2 * stride] : -1;
+      const float zt1 = n + stride < in.N ? token_logit(in, Row<T>(in.z, (n + stride) * in.ld, in.V), token1) : 0.f;
       bar_sync(1 + buf, kRowThreads);
       const Sums r = join_lanes(warp_sums[buf][lane & (kRowWarps - 1)], kRowWarps, in.c);
       const float log_s = logf(r.s);
-      if (lane == 0) write_row(in, out, n, row, r, log_s);
-      best_words<T>(choice, group_key[buf], row, groups_of(row, vec_shift), out.k, lane);
+      if (lane == 0) write_row(in, out, n, token, zt, r, log_s);
+      token = token1, token1 = token2, zt = zt1;
+      best_words<T, 1, true>(choice, group_key[buf], row, groups_of(row, vec_shift), out.k, lane, stage);
       write_top(in, out, n, choice.top, r, log_s, lane, 32);
       __syncwarp();
       if (n + 2 * static_cast<int64_t>(gridDim.x) < in.N) bar_arrive(3 + buf, kRowThreads);  // someone waits for it
