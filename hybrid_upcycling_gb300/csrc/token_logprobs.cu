@@ -395,8 +395,9 @@ __device__ void best_words(Choice<kWarps>& sh, uint32_t* group_key, const Row<T>
   };
   // The vectors with a word not below the bound are set down in shared memory, and then every thread looks at
   // one word of them. That is all unless very many words equal the bound.
+  const float bound_value = bound == 0u ? -INFINITY : key_value(bound);
   auto look = [&](int64_t t, uint4 v) {
-    if ((order_key(Elem<T>::vec_max(v)) & kHigh) >= bound) {
+    if (!(Elem<T>::vec_max(v) < bound_value)) {  // (also a NaN)
       const int at = atomicAdd(&sh.hits, 1);
       if (at < Choice<kWarps>::kHits) {
         sh.hit_vec[at] = v;
@@ -408,13 +409,30 @@ __device__ void best_words(Choice<kWarps>& sh, uint32_t* group_key, const Row<T>
 #pragma unroll 1
     for (int64_t t0 = 0; t0 < nv; t0 += kStage) {
       const int m = static_cast<int>(min(nv - t0, static_cast<int64_t>(kStage)));
+      if (kWarps == 1 && gr.vec_shift >= 5 && (1 << gr.vec_shift) <= kStage) {  // whole groups of whole warp loads
+        const int per = 1 << gr.vec_shift;
+#pragma unroll 1
+        for (int i = 0; i < m; i += per) {
+          const int64_t u = vector_at(t0 + i);
+          const T* src = row.base + u + tid * VE;
+          uint4* dst = stage + i + tid;
+          if (row.inside(u, u + static_cast<int64_t>(per) * VE)) {
+#pragma unroll 2
+            for (int c = 0; c < per; c += 32) copy_async(dst + c, src + c * VE);
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < per; c += 32) dst[c] = row.edge(u + static_cast<int64_t>(c + tid) * VE);
+          }
+        }
+      } else {
 #pragma unroll 4
-      for (int i = tid; i < m; i += kWarps * 32) {
-        const int64_t u = vector_at(t0 + i);
-        if (row.inside(u, u + VE))
-          copy_async(stage + i, row.base + u);
-        else
-          stage[i] = row.edge(u);
+        for (int i = tid; i < m; i += kWarps * 32) {
+          const int64_t u = vector_at(t0 + i);
+          if (row.inside(u, u + VE))
+            copy_async(stage + i, row.base + u);
+          else
+            stage[i] = row.edge(u);
+        }
       }
       copy_wait();  // every thread reads back what it copied
 #pragma unroll 4
@@ -799,9 +817,9 @@ token_logprobs_rows_kernel(const TokenRows in, const TokenOut out, int vec_shift
       const Sums r = join_lanes(warp_sums[buf][lane & (kRowWarps - 1)], kRowWarps, in.c);
       const float log_s = logf(r.s);
       if (lane == 0) write_row(in, out, n, token, zt, r, log_s);
-      token = token1, token1 = token2, zt = zt1;
       best_words<T, 1, true>(choice, group_key[buf], row, groups_of(row, vec_shift), out.k, lane, stage);
       write_top(in, out, n, choice.top, r, log_s, lane, 32);
+      token = token1, token1 = token2, zt = zt1;
       __syncwarp();
       if (n + 2 * static_cast<int64_t>(gridDim.x) < in.N) bar_arrive(3 + buf, kRowThreads);  // someone waits for it
     }
