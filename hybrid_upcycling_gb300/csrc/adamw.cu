@@ -430,7 +430,7 @@ struct NormTable {
   int64_t chunks;
   int count;
 };
-constexpr int kNormTable = 640;
+constexpr int kSmallNorm = 32, kLargeNorm = 640;
 constexpr int kNormVecs = 4;  // 16-byte vectors a thread has in flight
 
 // partials[block] (+)= the sum of squares of the block's chunks.
@@ -556,22 +556,22 @@ cudaError_t step_types(const hylo_adamw_tensor* tensors, int count, int grad_dty
                          : step_any<P, __nv_bfloat16, MASTER, false>(tensors, count, bias1, h, sms, stream);
 }
 
-template <typename G>
+template <int CAP, typename G>
 cudaError_t norm_list(const void* const* grads, const int64_t* sizes, int count, float* norm, float* partials, int sms,
                       cudaStream_t stream) {
   constexpr int64_t kSpan = static_cast<int64_t>(kThreads) * kNormVecs * (16 / sizeof(G));
-  NormTable<kNormTable> tab;
+  NormTable<CAP> tab;
   const int grid = sms * 8 < kNormPartials ? sms * 8 : kNormPartials;
   int i = 0, first = 1;
   do {
     tab.count = 0;
     tab.chunks = 0;
-    for (; i < count && tab.count < kNormTable; ++i) {
+    for (; i < count && tab.count < CAP; ++i) {
       if (sizes[i] == 0) continue;
       tab.t[tab.count++] = NormTensor{grads[i], sizes[i], tab.chunks};
       tab.chunks += (sizes[i] + kSpan - 1) / kSpan;
     }
-    grad_norm_kernel<G, kNormTable><<<grid, kThreads, 0, stream>>>(tab, partials, first);
+    grad_norm_kernel<G, CAP><<<grid, kThreads, 0, stream>>>(tab, partials, first);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     first = 0;
@@ -584,8 +584,12 @@ cudaError_t norm_list(const void* const* grads, const int64_t* sizes, int count,
 
 cudaError_t launch_grad_norm(const void* const* grads, const int64_t* sizes, int count, int dtype, float* norm,
                              float* partials, int sms, cudaStream_t stream) {
-  return dtype == HYLO_F32 ? norm_list<float>(grads, sizes, count, norm, partials, sms, stream)
-                           : norm_list<__nv_bfloat16>(grads, sizes, count, norm, partials, sms, stream);
+  // A short list goes with short kernel parameters.
+  if (count <= kSmallNorm)
+    return dtype == HYLO_F32 ? norm_list<kSmallNorm, float>(grads, sizes, count, norm, partials, sms, stream)
+                             : norm_list<kSmallNorm, __nv_bfloat16>(grads, sizes, count, norm, partials, sms, stream);
+  return dtype == HYLO_F32 ? norm_list<kLargeNorm, float>(grads, sizes, count, norm, partials, sms, stream)
+                           : norm_list<kLargeNorm, __nv_bfloat16>(grads, sizes, count, norm, partials, sms, stream);
 }
 
 cudaError_t launch_adamw(const hylo_adamw_tensor* tensors, int count, int param_dtype, int grad_dtype, int state_bits,

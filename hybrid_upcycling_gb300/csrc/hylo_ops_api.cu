@@ -50,17 +50,20 @@ struct HeadBwd {
   int64_t parts;   // dh is stored in this many parts, or 0
   bool dW_direct;  // dW is written in bf16 by the pipelined backward itself
 };
-// Few tokens: dh in parts, one per vocabulary block. A block is 8192 words (32 G tiles and, at d = 2048, 264 gradient
-// tiles for 76 clusters), less where that leaves fewer than three blocks, more where it makes more than 16. N d is bounded
-// so that a part is at most 8 MiB; with more tokens the chain of additions is short beside the rest.
-constexpr int64_t kPartTokens = 1024, kPartElems = int64_t(1) << 21, kPartWords = 8192, kMaxParts = 16;
+// Few tokens: dh in parts, one per vocabulary block, at most 16 of them. Long blocks wait less for ring slots, short ones
+// spread dh over more clusters, which counts with more tokens. Measured at d = 2048, V = 128256 with blocks of 8192,
+// 12288, 16384 and 24576 words: 256 tokens 642, 550, 587, 534 us; 512 tokens 777, 714, 649, 643; 1024 tokens 1062, 1054,
+// 1075 us (24576 words do not fit the ring). Fewer words where that leaves fewer than three blocks. N d is bounded so that
+// a part is at most 8 MiB; with more tokens the chain of additions is short beside the rest.
+constexpr int64_t kPartTokens = 1024, kPartElems = int64_t(1) << 21, kMaxParts = 16;
+constexpr int64_t part_words(int64_t N) { return N <= 512 ? 24576 : 12288; }
 
 HeadBwd head_bwd_layout(int64_t N, int64_t d, int64_t V, int64_t token_chunk, bool split, int grad_dtype) {
   HeadBwd l{};
   const int64_t R = pipe_rows(N, token_chunk);
   size_t ring = bwd_bytes(N, V, token_chunk);
   if (N <= R && N <= kPartTokens && N * d <= kPartElems) {
-    int64_t w = cdiv(V, kGRing) < kPartWords ? cdiv(V, kGRing) : kPartWords;
+    int64_t w = cdiv(V, kGRing) < part_words(N) ? cdiv(V, kGRing) : part_words(N);
     if (w < cdiv(V, kMaxParts)) w = cdiv(V, kMaxParts);
     w = cdiv(w, 256) * 256;
     if (kGRing * R * w * 2 <= kGBlockBytes) {

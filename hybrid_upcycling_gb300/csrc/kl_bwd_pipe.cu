@@ -41,7 +41,7 @@
 // (kHead: there is no teacher; G is formed from the student tile, the row's log-sum-exp, entropy
 // and upstream gradients, see HeadGrad). Its F items take one TMEM half, like M items. With few tokens
 // the additions into dh_s, one vocabulary block after another, would be a chain over the whole
-// vocabulary on a few clusters (N <= 256, V = 128256: 0.7 of 1.06 ms): there (HeadGrad::dh_parts)
+// vocabulary on a few clusters (N <= 256, V = 128256: 1.06 ms in all against 0.53): there (HeadGrad::dh_parts)
 // every block stores its dh_s products apart, for a sum in fixed order afterwards, and M(b) needs
 // F(b) only, F(b) still M(b-3).
 //
@@ -218,9 +218,14 @@ __device__ __forceinline__ Item cursor_item(Cursor& c, const BwdPipeParams& p, i
     }
   } else {
     const Geo g = geo(p, b);
-    const int ndw = g.vt * p.ntd;
-    it.kind = local < ndw ? kItemDW : kItemDH;
-    it.idx = local < ndw ? local : local - ndw;
+    const int ndw = g.vt * p.ntd, ndh = g.tt * p.ntd;
+    if (parts) {  // dh_s first: with few tokens its items are the long ones
+      it.kind = local < ndh ? kItemDH : kItemDW;
+      it.idx = local < ndh ? local : local - ndh;
+    } else {
+      it.kind = local < ndw ? kItemDW : kItemDH;
+      it.idx = local < ndw ? local : local - ndw;
+    }
     it.ctr0 = 2 + g.slot;  // every F item of block b
     it.tgt0 = c.cum_f[g.slot];
     if (!parts) {
