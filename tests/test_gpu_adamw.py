@@ -139,6 +139,41 @@ def test_grad_norm(dtype, sizes):
     assert torch.equal(a, b)
 
 
+def test_more_tensors_than_one_launch_takes():
+    """700 tensors are those of one flat tensor (fp32, 32-bit states: nothing depends on the list)."""
+    n = 700 * 5
+    flat, g, m, v, _ = model([n], "fp32", torch.float32, 32)
+    parts = [[t.clone().view(700, 5)[i] for i in range(700)] for t in (flat[0], g[0], m[0], v[0])]
+    norm, many = grad_norm(g), grad_norm(parts[1])
+    assert abs(norm.item() - many.item()) <= 64 * U * norm.item()
+    adamw_step(flat, g, m, v, step=4, norm=norm, max_norm=0.1, **HYPER)
+    adamw_step(*parts, step=4, norm=norm, max_norm=0.1, **HYPER)
+    for whole, pieces in zip((flat, g, m, v), parts):
+        assert torch.equal(whole[0], torch.cat(pieces))
+
+
+def test_elements_and_positions_behind_2_to_32():
+    """One bf16 tensor with 8-bit states of 2^32 + 700 elements: its last blocks against the oracle."""
+    n, tail = (1 << 32) + 700, 700
+    p = [torch.zeros(n, dtype=torch.bfloat16, device="cuda")]
+    g = [torch.zeros(n, dtype=torch.bfloat16, device="cuda")]
+    m, v = [State8.zeros_like(p[0])], [State8.zeros_like(p[0])]
+    p[0][-tail:] = torch.randn(tail, device="cuda").bfloat16()
+    g[0][-tail:] = torch.randn(tail, device="cuda").bfloat16()
+    w0, g0 = f64(p[0][-tail:]), f64(g[0][-tail:])
+    norm = grad_norm(g)
+    assert abs(norm.item() - np.linalg.norm(g0)) <= 64 * U * np.linalg.norm(g0)
+    adamw_step(p, g, m, v, step=1, seed=9, **HYPER)
+    rw, rm, rv = oo.adamw(w0, g0, np.zeros(tail), np.zeros(tail), step=1, **HYPER)
+    random = oo.random_bits(9, 1 << 32, tail)
+    at = lambda s: State8(s.codes.view(torch.uint8)[-tail:].clone(), s.exponents[-3:].clone())  # noqa: E731
+    check_codes(at(m[0]), rm, random & np.uint64(0xFFFF), False)
+    check_codes(at(v[0]), np.sqrt(rv), random >> np.uint64(16), True)
+    ulp = np.exp2(np.floor(np.log2(np.abs(rw))) - 7)
+    assert np.all(np.abs(f64(p[0][-tail:]) - rw) <= 1.001 * ulp)
+    assert torch.all(p[0][: 1 << 20] == 0) and torch.all(p[0][(1 << 31) - 500: (1 << 31) + 500] == 0)
+
+
 def test_norm_of_no_elements_and_of_nan():
     z = torch.zeros(0, device="cuda")
     assert grad_norm([z]).item() == 0.0
@@ -257,3 +292,16 @@ def test_mismatched_lists_are_refused():
             bad()
     with pytest.raises(_lib.HyloError):
         adamw_step(p, g, m, v, step=0, lr=0.1)
+
+
+@pytest.mark.parametrize("bits,masters", [(8, False), (32, True)])
+def test_the_example_learns(bits, masters):
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "train_head.py")
+    spec = importlib.util.spec_from_file_location("train_head", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    losses, before, after, top = ex.train(steps=12, tokens=300, hidden=64, vocab=1000, state_bits=bits, masters=masters)
+    assert all(np.isfinite(losses)) and losses[-1] < losses[0] - 0.5 and after > before + 0.5
+    assert top.top_tokens.shape == (4, 5) and torch.all(top.top_logprobs[:, :-1] >= top.top_logprobs[:, 1:])

@@ -137,6 +137,45 @@ def test_ties_and_orders(dtype, N, V, k):
     check(z, torch.arange(6, device="cuda") * 7 % V, 1.0, k)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("N,V,k,shift", [(1300, 9001, 20, 1), (1300, 9001, 64, 0), (700, 600, 20, 3), (700, 2000, 64, 0),
+                                         (640, 130, 64, 0), (650, 5, 5, 2)])
+def test_many_rows_of_every_kind(dtype, N, V, k, shift):
+    """More rows than the GPU holds at once, so that rows follow one another in the same blocks: ordinary rows beside
+    masked, tied, sorted and constant ones."""
+    z, tok = logits(N, V, dtype, seed=N + V, shift=shift)
+    z[1::11] = -float("inf")
+    z[2::11, : V // 2] = -float("inf")
+    z[3::11] = 0.5
+    z[4::11] = torch.linspace(-4, 4, V, device="cuda").to(dtype)
+    z[5::11] = torch.linspace(4, -4, V, device="cuda").to(dtype)
+    z[6::11] = torch.arange(V, device="cuda").remainder(3).to(dtype)
+    z[7::11, 3:] = -float("inf")
+    tok[8::11] = -100
+    check(z, tok, 1.0, k)
+
+
+def test_rows_of_nan():
+    """NaN counts as larger than any number, the lowest index first; every result but the order is NaN."""
+    z = torch.randn(700, 3000, device="cuda")
+    z[::2, 5:2000] = float("nan")
+    z[1::4] = float("nan")
+    for N in (3, 700):
+        r = token_logprobs(z[:N], torch.zeros(N, dtype=torch.int64, device="cuda"), top_k=30)
+        ids = r.top_tokens
+        assert torch.equal(ids[0], torch.arange(5, 35, device="cuda")) and torch.equal(ids[1], torch.arange(30, device="cuda"))
+        assert torch.equal(ids[2], ids[0]) and torch.isnan(r.top_logprobs[:3]).all() and torch.isnan(r.entropy[:3]).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_very_long_row(dtype):
+    """20 million words: groups of many warp loads, and the gradient of the same row."""
+    z, tok = logits(2, 20_000_003, dtype, seed=13)
+    z[1, :-4] = -float("inf")
+    tok[1] = 20_000_001
+    check(z, tok, 1.0, 5)
+
+
 def test_nan_inf_and_tokens_out_of_range():
     z, tok = logits(6, 3000, torch.float32, seed=4)
     z[1, 2500] = float("nan")
