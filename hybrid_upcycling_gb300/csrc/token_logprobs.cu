@@ -771,7 +771,7 @@ constexpr int kStreamWarps = 8;  // warps of a CTA that shares a row
 
 // Many whole rows with alternatives: eight warps stream row after row and never wait for a selection; a ninth warp joins
 // each row's sums and chooses its alternatives while the next row streams. (8192 x 128256, 16 alternatives: with the eight
-// warps choosing between rows, 489 us; so, XXX us.)
+// warps choosing between rows, 489 us; so, 388 us.)
 constexpr int kRowWarps = 8;
 constexpr int kRowThreads = 32 * (kRowWarps + 1);
 constexpr int kRowBlocks = 4;  // thread blocks per SM

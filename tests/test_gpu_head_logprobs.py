@@ -111,6 +111,27 @@ def test_fp32_gradients_of_the_c_abi(split, tol):
     assert torch.equal(dh, again_h) and torch.equal(dW, again_W)
 
 
+@pytest.mark.parametrize("split", [False, True])
+@pytest.mark.parametrize("N,d,V", [(300, 64, 100_000), (700, 64, 60_001), (1, 128, 200_001), (1000, 72, 150_007)])
+def test_gradients_over_many_vocabulary_blocks(N, d, V, split):
+    """Few tokens and many vocabulary blocks, so that G's buffers are used again: the bound of test_gradients, taken
+    also over each stretch of 8192 words and each token alone (1.5 times: fewer elements to average over for a token)."""
+    h, W, tok = inputs(N, d, V, seed=V)
+    tok[0] = V - 1
+    gl, ge = torch.randn(N, device="cuda"), 0.3 * torch.randn(N, device="cuda")
+    h.requires_grad_(), W.requires_grad_()
+    logp, ent = head_logprobs(h, W, tok, split_g=split)
+    dh, dW = torch.autograd.grad([logp, ent], (h, W), [gl, ge])
+    G = oo.token_logprobs_grad(f64(h) @ f64(W).T, tok.cpu().numpy(), 1.0, f64(gl), f64(ge))
+    rel = (1e-4 if split else 4e-3) + 2.0 ** -8
+    ref_h, ref_W = G @ f64(W), G.T @ f64(h)
+    for n in range(N):
+        assert np.linalg.norm(f64(dh[n]) - ref_h[n]) <= 1.5 * rel * np.linalg.norm(ref_h[n]) + 1e-5 * gl.abs().max().item()
+    for v in range(0, V, 8192):
+        ref = ref_W[v:v + 8192]
+        assert np.linalg.norm(f64(dW[v:v + 8192]) - ref) <= rel * np.linalg.norm(ref) + 1e-5 * gl.abs().max().item()
+
+
 def test_gradient_against_differences():
     """Directional differences of the fp64 forward along random directions; bound: G's one rounding to bf16."""
     N, d, V = 6, 16, 40
