@@ -87,6 +87,17 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+class _Once(torch.autograd.Function):
+    """A gradient, as a function of `inputs` whose own derivative is not implemented."""
+    @staticmethod
+    def forward(ctx, grad, *inputs):
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, g):
+        raise RuntimeError("token_logprobs and head_logprobs are differentiable once")
+
+
 class _TokenLogprobs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, z, tokens, tau, k, dev, alternatives):
@@ -108,6 +119,8 @@ class _TokenLogprobs(torch.autograd.Function):
                 z.data_ptr(), _lib.DTYPES[z.dtype], N, V, _row_stride(z), ctx.tau, tokens.data_ptr(), stats.data_ptr(),
                 entropy.data_ptr(), _ptr(g_logp), _ptr(g_entropy), dz.data_ptr(), _row_stride(dz),
                 current_raw_stream(z.get_device())))
+        if torch.is_grad_enabled():  # create_graph
+            dz = _Once.apply(dz, z, g_logp, g_entropy)
         return dz, None, None, None, None, None
 
 
@@ -117,7 +130,7 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, tau: float = 1.0,
 
     logits may have any strides; rows with unit column stride are read in place. A negative token is
     ignored (log-probability 0, no gradient); -inf logits are masked words. logprobs and entropy
-    are differentiable with respect to logits (gradient in the logits' dtype)."""
+    are differentiable once with respect to logits (gradient in the logits' dtype)."""
     shape = logits.shape
     if logits.dtype not in _lib.DTYPES or not shape or shape[-1] < 1:
         raise ValueError("logits must be float32, bfloat16 or float16 with a last dimension of at least one word")
@@ -182,6 +195,8 @@ class _HeadLogprobs(torch.autograd.Function):
             h.data_ptr(), W.data_ptr(), N, d, V, tau, token_chunk, tokens.data_ptr(), lse.data_ptr(), entropy.data_ptr(),
             _ptr(g_logp), _ptr(g_entropy), int(split_g), _BF16, dh.data_ptr(), dW.data_ptr(), ws.data_ptr(), n,
             current_raw_stream(h.get_device())))
+        if torch.is_grad_enabled():  # create_graph
+            dh, dW = (_Once.apply(g, h, W, g_logp, g_entropy) for g in (dh, dW))
         return (dh if ctx.needs_input_grad[0] else None, dW if ctx.needs_input_grad[1] else None, None, None, None, None,
                 None)
 
@@ -191,7 +206,7 @@ def head_logprobs(h: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, tau: f
     """Log-probabilities of ``tokens`` [...] (int64) under softmax(h W^T / tau) and the entropies, for final hidden
     states h [..., d] and an LM head W [V, d] in bfloat16 (d a multiple of 8); the logits are never stored.
 
-    A negative token is ignored (log-probability 0, no gradient). Both results are differentiable
+    A negative token is ignored (log-probability 0, no gradient). Both results are differentiable once
     with respect to h and W (bfloat16 gradients; the C ABI gives fp32). token_chunk and split_g as in
     fused_hidden_state_kl: the backward's token block, and whether the gradient of the logits is
     kept to 16 bits of precision instead of 8 inside the gradient products (None: for up to 64 tokens, where that

@@ -10,6 +10,7 @@ from __future__ import annotations
 from typing import Iterable, List, NamedTuple, Optional, Sequence, Tuple, Union
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import _lib
 
@@ -140,13 +141,15 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
     fields = [x for row in zip(*columns) for x in row]
     _lib.hylo_adamw_step(fields, n, pdt, gdt, bits, betas, eps, int(step), grad_scale, norm, max_norm, int(seed),
                          _lib.current_raw_stream(dev))
+    increment_version(params)  # a backward through the values before the step raises, as after any in-place operation
 
 
 class AdamW:
     """AdamW with its states. params: tensors, or dicts {"params": [...], "lr": ..., "weight_decay": ...} (groups).
 
     state_bits 32 or 8. bfloat16 parameters get fp32 masters unless masters=False. max_norm (optional)
-    clips the global gradient norm of each step; ``last_norm`` is that norm (a device tensor)."""
+    clips the global gradient norm of each step; ``last_norm`` is that norm (a device tensor). A step skipped for a norm
+    that is not finite is counted in ``steps`` (the host does not wait to learn of it)."""
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
                  state_bits: int = 32, masters: bool = True, max_norm: Optional[float] = None, seed: int = 0):
@@ -179,14 +182,14 @@ class AdamW:
             grads = [p.grad for p in self.params]
             if any(g is None for g in grads):
                 raise ValueError("every parameter needs a gradient")
-        self.steps += 1
         self.last_norm = grad_norm(grads) if self.max_norm is not None else None
         lr = [g["lr"] for g in self.groups for _ in g["params"]]
         wd = [g["weight_decay"] for g in self.groups for _ in g["params"]]
-        adamw_step([p.detach() for p in self.params], grads, self.exp_avgs, self.exp_avg_sqs, step=self.steps, lr=lr,
+        adamw_step([p.detach() for p in self.params], grads, self.exp_avgs, self.exp_avg_sqs, step=self.steps + 1, lr=lr,
                    betas=self.betas, eps=self.eps, weight_decay=wd, masters=self.masters, norm=self.last_norm,
                    max_norm=1.0 if self.max_norm is None else self.max_norm, grad_scale=grad_scale,
-                   seed=self.seed + self.steps)
+                   seed=self.seed + self.steps + 1)
+        self.steps += 1
 
     def state_dict(self) -> dict:
         return {"steps": self.steps, "seed": self.seed, "exp_avgs": self.exp_avgs, "exp_avg_sqs": self.exp_avg_sqs,

@@ -279,6 +279,23 @@ def test_optimizer_class_state_and_streams():
         ob.load_state_dict(AdamW(mk(), state_bits=32).state_dict())
 
 
+def test_a_step_is_an_in_place_operation_and_counts_when_it_ran():
+    p = torch.ones(300, device="cuda", requires_grad=True)
+    opt = AdamW([p])
+    loss = (p * p).sum()
+    opt.step([torch.ones(300, device="cuda")])
+    assert opt.steps == 1
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with pytest.raises(ValueError):
+        opt.step([torch.ones(301, device="cuda")])
+    assert opt.steps == 1
+    with torch.inference_mode():
+        q = torch.ones(300, device="cuda")
+        AdamW([q]).step([torch.ones(300, device="cuda")])
+        assert torch.all(q < 1)
+
+
 def test_mismatched_lists_are_refused():
     p, g, m, v, _ = model([300, 20], "fp32", torch.float32, 32)
     for bad in (lambda: adamw_step(p, g[:1], m, v, step=1, lr=0.1), lambda: adamw_step(p, g[::-1], m, v, step=1, lr=0.1),

@@ -10,7 +10,7 @@ import numpy as np
 import pytest
 import torch
 
-from hybrid_upcycling_gb300 import _lib, build, token_logprobs
+from hybrid_upcycling_gb300 import _lib, build, head_logprobs, token_logprobs
 from oracle import ops_oracle as oo
 
 pytestmark = pytest.mark.gpu
@@ -225,6 +225,22 @@ def test_gradient_of_no_rows_and_of_unused_outputs():
     e = z[:0].detach().requires_grad_()
     token_logprobs(e, tok[:0]).entropy.sum().backward()
     assert e.grad.shape == (0, 100)
+
+
+def test_second_derivatives_are_refused():
+    z = torch.randn(4, 50, device="cuda", requires_grad=True)
+    w = torch.randn(4, 50, device="cuda", requires_grad=True)
+    tok = torch.zeros(4, dtype=torch.int64, device="cuda")
+    dz, = torch.autograd.grad(token_logprobs(z, tok).logprobs.sum(), z, create_graph=True)
+    plain, = torch.autograd.grad(token_logprobs(z, tok).logprobs.sum(), z)
+    assert torch.equal(dz, plain)
+    with pytest.raises(RuntimeError, match="differentiable once"):
+        (dz * w).sum().backward()
+    h, W = (torch.randn(n, 16, device="cuda").bfloat16().requires_grad_() for n in (4, 50))
+    grads = torch.autograd.grad(head_logprobs(h, W, tok)[0].sum(), (h, W), create_graph=True)
+    for g in grads:
+        with pytest.raises(RuntimeError, match="differentiable once"):
+            g.float().sum().backward(retain_graph=True)
 
 
 def test_gradient_against_differences():
