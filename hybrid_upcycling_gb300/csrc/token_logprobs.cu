@@ -142,6 +142,7 @@ __device__ __forceinline__ float key_value(uint32_t key) {
   if (key == 0xffffffffu) return __uint_as_float(0x7fffffffu);
   return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
 }
+constexpr uint32_t kMinusInfKey = 0x007fffffu, kInfKey = 0xff800000u;  // those of -inf and inf
 // A candidate: larger is better (larger logit, then lower index).
 __device__ __forceinline__ uint64_t cand_of(uint32_t key, int idx) {
   return (static_cast<uint64_t>(key) << 32) | (0xffffffffu - static_cast<uint32_t>(idx));
@@ -276,6 +277,14 @@ __device__ __forceinline__ void rank_all(Choice<kWarps>& sh, int have, int k, in
   }
 }
 
+// The bound below which no word is looked at, from the kk-th largest group maximum. Where that is -inf (masked words), it is
+// the next key: less than k words lie above -inf, all of them in the chosen groups, and words of -inf are filled in.
+template <typename T>
+__device__ __forceinline__ uint32_t bound_of(uint32_t key) {
+  constexpr uint32_t kHigh = Elem<T>::kKeyBits == 32 ? ~0u : ~0u << (32 - Elem<T>::kKeyBits);
+  return (key & kHigh) == (kMinusInfKey & kHigh) ? (kMinusInfKey & kHigh) + (~kHigh + 1u) : key & kHigh;
+}
+
 // The first kk groups by (maximum, position) into sh.sel, and the kk-th largest maximum (in the leading bits of its
 // key) into sh.bound_key. (Loops are kept rolled here and below: this code runs once per row.)
 //
@@ -301,7 +310,7 @@ __device__ void rank_groups(Choice<kWarps>& sh, uint32_t* group_key, int groups,
   if (!kUnique && eq > 1 && tid < groups)
     for (int g = 0; g < tid; ++g) gt += group_key[g] == mine;
   if (tid < groups && gt < kk) sh.sel[gt] = tid;
-  if (tid < groups && gt == kk - 1) sh.bound_key = kk == k ? mine & kHigh : 0u;  // fewer groups than k: any word may count
+  if (tid < groups && gt == kk - 1) sh.bound_key = kk == k ? bound_of<T>(mine) : 0u;  // fewer groups than k: any word may count
 }
 
 // One warp: a search for the kk-th largest, bit by bit below the bits that the largest and the smallest maximum share,
@@ -353,7 +362,7 @@ __device__ void choose_groups(Choice<kWarps>& sh, const uint32_t* group_key, int
     placed += __popc(takes);
     equal_left -= min(equal_left, __popc(eqs));
   }
-  if (lane == 0) sh.bound_key = kk == k ? t : 0u;  // fewer groups than k: any word may be among the k
+  if (lane == 0) sh.bound_key = kk == k ? bound_of<T>(t) : 0u;  // fewer groups than k: any word may be among the k
 }
 
 // 16-byte copy into shared memory in the background of this thread.
@@ -383,90 +392,125 @@ __device__ void best_words(Choice<kWarps>& sh, uint32_t* group_key, const Row<T>
   else
     choose_groups<T>(sh, group_key, gr.count, kk, k);
   sync_warps<kWarps>();
-  const uint32_t bound = sh.bound_key;
-  const int64_t nv = static_cast<int64_t>(kk) << gr.vec_shift;  // vectors of the chosen groups, in their order
-  auto vector_at = [&](int64_t t) {  // where the t-th of them starts
+  uint32_t bound = sh.bound_key;
+  const int nv = kk << gr.vec_shift;  // vectors of the chosen groups, in their order
+  auto vector_at = [&](int t) {  // where the t-th of them starts
     const int64_t g = sh.sel[t >> gr.vec_shift];
-    return ((g << gr.vec_shift) + (t & ((int64_t(1) << gr.vec_shift) - 1))) * VE;
+    return ((g << gr.vec_shift) + (t & ((1 << gr.vec_shift) - 1))) * VE;
   };
   auto push = [&](uint64_t cd) {
     const int at = atomicAdd(&sh.count, 1);
     if (at < kCand) sh.cand[at] = cd;
   };
-  // The vectors with a word not below the bound are set down in shared memory, and then every thread looks at
-  // one word of them. That is all unless very many words equal the bound.
-  const float bound_value = bound == 0u ? -INFINITY : key_value(bound);
-  auto look = [&](int64_t t, uint4 v) {
-    if (!(Elem<T>::vec_max(v) < bound_value)) {  // (also a NaN)
-      const int at = atomicAdd(&sh.hits, 1);
-      if (at < Choice<kWarps>::kHits) {
-        sh.hit_vec[at] = v;
-        sh.hit_at[at] = static_cast<int>(vector_at(t) / VE);
-      }
+  // Masks tie very many words at one value. If k of the row's first 4 k words equal the bound, the bound can be raised to the
+  // next key: the words above it are all in the chosen groups, and those equal words that are needed are among
+  // these first words. (The same holds for the first words of -inf where the bound was raised above that.) A row of 151936
+  // fp32 words of which a mask leaves five, 8 alternatives: 11.2 us, in the order below 17.8.
+  constexpr uint32_t kNextKey = ~kHigh + 1u;
+  auto first_words = [&](uint32_t value, auto&& use) {
+#pragma unroll 1
+    for (int i = tid; i < 4 * k && row.lead + i < row.end; i += kWarps * 32) {
+      const uint32_t key = order_key(Elem<T>::get(row.base[row.lead + i]));
+      if ((key & kHigh) == value) use(key, i);
     }
   };
-  if constexpr (kStaged) {
+  auto fill_up = [&](int& have) {
+    if (have >= k) return;  // else the bound was raised, and few words reach it
+    sync_warps<kWarps>();
+    first_words(bound - kNextKey, [&](uint32_t key, int i) { push(cand_of(key, i)); });
+    sync_warps<kWarps>();
+    have = sh.count;
+  };
 #pragma unroll 1
-    for (int64_t t0 = 0; t0 < nv; t0 += kStage) {
-      const int m = static_cast<int>(min(nv - t0, static_cast<int64_t>(kStage)));
-      if (kWarps == 1 && gr.vec_shift >= 5 && (1 << gr.vec_shift) <= kStage) {  // whole groups of whole warp loads
-        const int per = 1 << gr.vec_shift;
-#pragma unroll 1
-        for (int i = 0; i < m; i += per) {
-          const int64_t u = vector_at(t0 + i);
-          const T* src = row.base + u + tid * VE;
-          uint4* dst = stage + i + tid;
-          if (row.inside(u, u + static_cast<int64_t>(per) * VE)) {
-#pragma unroll 2
-            for (int c = 0; c < per; c += 32) copy_async(dst + c, src + c * VE);
-          } else {
-#pragma unroll 1
-            for (int c = 0; c < per; c += 32) dst[c] = row.edge(u + static_cast<int64_t>(c + tid) * VE);
-          }
-        }
-      } else {
-#pragma unroll 4
-        for (int i = tid; i < m; i += kWarps * 32) {
-          const int64_t u = vector_at(t0 + i);
-          if (row.inside(u, u + VE))
-            copy_async(stage + i, row.base + u);
-          else
-            stage[i] = row.edge(u);
+  while (true) {
+    // The vectors with a word not below the bound are set down in shared memory, and then every thread looks at
+    // one word of them. That is all unless very many words equal the bound.
+    const float bound_value = bound == 0u ? -INFINITY : key_value(bound);
+    auto look = [&](int t, uint4 v) {
+      if (!(Elem<T>::vec_max(v) < bound_value)) {  // (also a NaN)
+        const int at = atomicAdd(&sh.hits, 1);
+        if (at < Choice<kWarps>::kHits) {
+          sh.hit_vec[at] = v;
+          sh.hit_at[at] = static_cast<int>(vector_at(t) / VE);
         }
       }
-      copy_wait();  // every thread reads back what it copied
+    };
+    if constexpr (kStaged) {
+#pragma unroll 1
+      for (int t0 = 0; t0 < nv; t0 += kStage) {
+        const int m = min(nv - t0, kStage);
+        if (kWarps == 1 && gr.vec_shift >= 5 && (1 << gr.vec_shift) <= kStage) {  // whole groups of whole warp loads
+          const int per = 1 << gr.vec_shift;
+#pragma unroll 1
+          for (int i = 0; i < m; i += per) {
+            const int64_t u = vector_at(t0 + i);
+            const T* src = row.base + u + tid * VE;
+            uint4* dst = stage + i + tid;
+            if (row.inside(u, u + static_cast<int64_t>(per) * VE)) {
+#pragma unroll 2
+              for (int c = 0; c < per; c += 32) copy_async(dst + c, src + c * VE);
+            } else {
+#pragma unroll 1
+              for (int c = 0; c < per; c += 32) dst[c] = row.edge(u + static_cast<int64_t>(c + tid) * VE);
+            }
+          }
+        } else {
 #pragma unroll 4
-      for (int i = tid; i < m; i += kWarps * 32) look(t0 + i, stage[i]);
-    }
-  } else
+          for (int i = tid; i < m; i += kWarps * 32) {
+            const int64_t u = vector_at(t0 + i);
+            if (row.inside(u, u + VE))
+              copy_async(stage + i, row.base + u);
+            else
+              stage[i] = row.edge(u);
+          }
+        }
+        copy_wait();  // every thread reads back what it copied
+#pragma unroll 4
+        for (int i = tid; i < m; i += kWarps * 32) look(t0 + i, stage[i]);
+      }
+    } else
 #pragma unroll 1
-  for (int64_t t0 = tid; t0 < nv; t0 += kWarps * kFirst * 32) {
-    uint4 v[kFirst];
+    for (int t0 = tid; t0 < nv; t0 += kWarps * kFirst * 32) {
+      uint4 v[kFirst];
 #pragma unroll
-    for (int i = 0; i < kFirst; ++i)
-      if (t0 + i * kWarps * 32 < nv) v[i] = row.edge(vector_at(t0 + i * kWarps * 32));
+      for (int i = 0; i < kFirst; ++i)
+        if (t0 + i * kWarps * 32 < nv) v[i] = row.edge(vector_at(t0 + i * kWarps * 32));
 #pragma unroll
-    for (int i = 0; i < kFirst; ++i) {
-      const int64_t t = t0 + i * kWarps * 32;
-      if (t < nv) look(t, v[i]);
-    }
-  }
-  sync_warps<kWarps>();
-  if (sh.hits <= Choice<kWarps>::kHits) {
-    const int words = sh.hits * VE;
-#pragma unroll 1
-    for (int e = tid; e < words; e += kWarps * 32) {
-      const int64_t u = static_cast<int64_t>(sh.hit_at[e / VE]) * VE + e % VE;
-      const uint32_t key = order_key(Elem<T>::get(reinterpret_cast<const T*>(sh.hit_vec)[e]));
-      if ((key & kHigh) >= bound && row.inside(u, u + 1)) push(cand_of(key, static_cast<int>(u - row.lead)));
+      for (int i = 0; i < kFirst; ++i) {
+        const int t = t0 + i * kWarps * 32;
+        if (t < nv) look(t, v[i]);
+      }
     }
     sync_warps<kWarps>();
-    const int have = sh.count;
-    if (have <= kCand) {
-      rank_all(sh, have, k, tid);
+    if (sh.hits <= Choice<kWarps>::kHits) {
+      const int words = sh.hits * VE;
+#pragma unroll 1
+      for (int e = tid; e < words; e += kWarps * 32) {
+        const int64_t u = static_cast<int64_t>(sh.hit_at[e / VE]) * VE + e % VE;
+        const uint32_t key = order_key(Elem<T>::get(reinterpret_cast<const T*>(sh.hit_vec)[e]));
+        if ((key & kHigh) >= bound && row.inside(u, u + 1)) push(cand_of(key, static_cast<int>(u - row.lead)));
+      }
       sync_warps<kWarps>();
-      return;
+      int have = sh.count;
+      fill_up(have);
+      if (have >= k && have <= kCand) {
+        rank_all(sh, have, k, tid);
+        sync_warps<kWarps>();
+        return;
+      }
     }
+    if (bound >= (kInfKey & kHigh)) break;
+    int equal = 0;
+    first_words(bound, [&](uint32_t, int) { ++equal; });
+    if constexpr (kWarps > 1)
+      equal = __syncthreads_count(equal);  // (at most 4 k threads have a word each)
+    else
+      equal = __reduce_add_sync(~0u, equal);
+    if (equal < k) break;
+    bound += kNextKey;
+    sync_warps<kWarps>();
+    if (tid == 0) sh.count = sh.hits = 0;
+    sync_warps<kWarps>();
   }
   // Otherwise in order: the words above the bound, and of those equal to it only the first k.
   sync_warps<kWarps>();
@@ -483,8 +527,8 @@ __device__ void best_words(Choice<kWarps>& sh, uint32_t* group_key, const Row<T>
   sync_warps<kWarps>();
   int equal_before = 0;
 #pragma unroll 1
-  for (int64_t t0 = 0; t0 < nv; t0 += kWarps * kDeep * 32) {
-    const int64_t tw = t0 + warp * kDeep * 32 + lane;
+  for (int t0 = 0; t0 < nv; t0 += kWarps * kDeep * 32) {
+    const int tw = t0 + warp * kDeep * 32 + lane;
     float top[kDeep];
 #pragma unroll
     for (int i = 0; i < kDeep; ++i) top[i] = tw + i * 32 < nv ? Elem<T>::vec_max(row.edge(vector_at(tw + i * 32))) : -INFINITY;
@@ -537,7 +581,8 @@ __device__ void best_words(Choice<kWarps>& sh, uint32_t* group_key, const Row<T>
     }
     sync_warps<kWarps>();
   }
-  const int have = sh.count;
+  int have = sh.count;
+  fill_up(have);
   if (have <= kCand) {
     rank_all(sh, have, k, tid);
     sync_warps<kWarps>();
@@ -547,12 +592,12 @@ __device__ void best_words(Choice<kWarps>& sh, uint32_t* group_key, const Row<T>
   constexpr int kStep = (kCand - HYLO_TOP_MAX) / (32 * VE) * 32;  // vectors
   uint64_t least = static_cast<uint64_t>(bound) << 32;  // candidates are not below it
   int best = 0;
-  for (int64_t t0 = 0; t0 < nv; t0 += kStep) {
+  for (int t0 = 0; t0 < nv; t0 += kStep) {
     sync_warps<kWarps>();
     if (tid == 0) sh.count = best;
     for (int i = tid; i < best; i += kWarps * 32) sh.cand[i] = sh.top[i];
     sync_warps<kWarps>();
-    for (int64_t t = t0 + tid; t < min(nv, t0 + kStep); t += kWarps * 32) {
+    for (int t = t0 + tid; t < min(nv, t0 + kStep); t += kWarps * 32) {
       const int64_t u = vector_at(t);
 #pragma unroll 1
       for (int q = 0; q < VE; ++q) {
@@ -771,7 +816,7 @@ constexpr int kStreamWarps = 8;  // warps of a CTA that shares a row
 
 // Many whole rows with alternatives: eight warps stream row after row and never wait for a selection; a ninth warp joins
 // each row's sums and chooses its alternatives while the next row streams. (8192 x 128256, 16 alternatives: with the eight
-// warps choosing between rows, 489 us; so, 388 us.)
+// warps choosing between rows, 489 us; so, 382 us.)
 constexpr int kRowWarps = 8;
 constexpr int kRowThreads = 32 * (kRowWarps + 1);
 constexpr int kRowBlocks = 4;  // thread blocks per SM

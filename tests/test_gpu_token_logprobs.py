@@ -138,6 +138,25 @@ def test_ties_and_orders(dtype, N, V, k):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("N,V,k", [(11, 128256, 20), (700, 20001, 8), (700, 9001, 64), (660, 300, 64)])
+@pytest.mark.parametrize("mask", [-float("inf"), -1e4, 0.25])
+def test_very_many_equal_words(dtype, N, V, k, mask):
+    """One value in almost all words, for a few rows and for more than are at work at once; the others lie above and
+    below it, at the start, at the end, next to each other, and fewer or more of them than alternatives."""
+    z, tok = logits(N, V, dtype, seed=N + V + k)
+    n = torch.arange(N, device="cuda")
+    v = torch.arange(V, device="cuda")
+    keep = torch.zeros(N, V, dtype=torch.bool, device="cuda")
+    for kind, words in ((0, v < 0), (1, v < k - 1), (2, v >= V - k + 1), (3, v % 97 == 5), (4, v < 3 * k), (5, v < 4 * k),
+                        (6, (v >= V // 3) & (v < V // 3 + 2 * k)), (7, v == V - 1), (8, v >= V - 100), (9, v < V // 2),
+                        (10, v == 0)):
+        keep[n % 11 == kind] = words
+    z = torch.where(keep, z, torch.full_like(z, mask))
+    tok[n % 11 == 8] = V - 1
+    check(z, tok, 1.0, k)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("N,V,k,shift", [(1300, 9001, 20, 1), (1300, 9001, 64, 0), (700, 600, 20, 3), (700, 2000, 64, 0),
                                          (640, 130, 64, 0), (650, 5, 5, 2)])
 def test_many_rows_of_every_kind(dtype, N, V, k, shift):
