@@ -228,7 +228,8 @@ hylo_status hylo_head_logprobs_backward(const uint16_t* h, const uint16_t* W, in
     return st;
   cudaError_t e = cudaMemsetAsync(p.ctrl, 0, (kPipeCtrlWords + kGRing) * sizeof(unsigned), stream);
   if (e != cudaSuccess) return cuda_fail(e, "clear the backward's work counters");
-  const HeadGrad g{tokens, lse, entropy, g_logp, g_entropy, 1.0f / tau, l.dW_direct ? 1 : 0, l.parts > 0 ? 1 : 0};
+  const int order = l.parts > 0 ? kOrderParts : p.TB == 1 || p.VB >= kGRing ? kOrderDh : kOrderChain;
+  const HeadGrad g{tokens, lse, entropy, g_logp, g_entropy, 1.0f / tau, l.dW_direct ? 1 : 0, order};
   e = launch_bwd_pipe_head(maps, p, g, clusters, stream);
   if (e == cudaSuccess && (bf16 || l.parts > 0))
     e = launch_join_parts(dh32, l.parts > 0 ? static_cast<int>(l.parts) : 1, dh, bf16, N * d, dev->sms, stream);

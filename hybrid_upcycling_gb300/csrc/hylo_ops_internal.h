@@ -83,8 +83,16 @@ struct HeadGrad {
   const float* g_entropy;  // or null
   float inv_tau;
   int dw_bf16;             // one token block: map kMapDW is a bf16 tensor of 32 x 32 tiles with 64-byte swizzle
-  int dh_parts;            // map kMapDh is [vocabulary blocks][N][d]: every block's part of dh apart (one token block)
+  int order;               // see below
 };
+// How the items of one block wait for those of others (M(b): products of block b, F(b): its G).
+//   kOrderChain: M(b) needs all of M(b - 1), as the distillation loss.
+//   kOrderDh: only the dh items of block b - 1 (which come first), as dh is what one block after another adds to; dW's
+//     items of one block then do not hold up the next. With several token blocks also dW is added to: the items of the same
+//     words, VB blocks before, are complete if VB >= 3, as then they belong to a block whose ring slot was taken again.
+//   kOrderParts: nothing of M(b - 1). Map kMapDh is [vocabulary blocks][N][d]: every block's part of dh apart (one token
+//     block).
+enum : int { kOrderChain = 0, kOrderDh = 1, kOrderParts = 2 };
 // y = the sum over `parts` of x [parts][n] in ascending order, as fp32 or rounded to bf16 (n a multiple of 8, 16-byte aligned).
 cudaError_t launch_join_parts(const float* x, int parts, void* y, bool bf16, int64_t n, int sms, cudaStream_t stream);
 cudaError_t launch_bwd_pipe_head(const CUtensorMap* maps, const BwdPipeParams& p, const HeadGrad& g, int clusters,

@@ -39,11 +39,13 @@
 //
 // The same launch also runs the backward of the token log-probabilities from hidden states
 // (kHead: there is no teacher; G is formed from the student tile, the row's log-sum-exp, entropy
-// and upstream gradients, see HeadGrad). Its F items take one TMEM half, like M items. With few tokens
-// the additions into dh_s, one vocabulary block after another, would be a chain over the whole
-// vocabulary on a few clusters (N <= 256, V = 128256: 1.06 ms in all against 0.53): there (HeadGrad::dh_parts)
-// every block stores its dh_s products apart, for a sum in fixed order afterwards, and M(b) needs
-// F(b) only, F(b) still M(b-3).
+// and upstream gradients, see HeadGrad). Its F items take one TMEM half, like M items. There M(b) waits for the dh_s items of
+// M(b-1) only, which come first in their block (kOrderDh): dW_s tiles of one block do not meet those of the next, and long
+// dh_s items at a block's end would hold up the next block (1500 tokens, d = 2048, V = 128256: 1.93 ms in the order
+// above, 1.57 so; 2048 tokens 2.30 and 2.08; 4096 tokens and more the same). With few tokens the additions into dh_s are a
+// chain over the whole vocabulary on a few clusters all the same (N <= 256: 0.85 ms in all against 0.53): there
+// (kOrderParts) every block stores its dh_s products apart, for a sum in fixed order afterwards, and M(b) needs F(b)
+// only. F(b) needs M(b-3) always.
 //
 // TMEM holds two 256-column halves. An M item takes one; an F item takes one for the teacher
 // tile and the other for the student tile. The UMMA warp signals the teacher half as soon as its
@@ -137,13 +139,15 @@ __device__ __forceinline__ int items_m(const BwdPipeParams& p, int b) {
   return (g.vt + g.tt) * p.ntd;
 }
 
+__device__ __forceinline__ int items_dh(const BwdPipeParams& p, int b) { return geo(p, b).tt * p.ntd; }
+
 // Walks the queue order part by part: segment j holds M(j-2) (part 0) if 0 <= j-2 < B and F(j)
 // (part 1) if j < B. It keeps, per counter, the completion total of the parts already passed
 // (each CTA of a pair adds 1 per item, so totals count 2 per item).
 struct Cursor {
   int j, part, base, size;
-  unsigned cum_m;          // M items of the parts passed
-  unsigned cum_ms[kGRing]; // the same, per ring slot
+  unsigned cum_m;          // M items of the parts passed (kOrderDh: their dh_s items)
+  unsigned cum_ms[kGRing]; // the same, per ring slot (kOrderDh: their dW_s items)
   unsigned cum_f[kGRing];  // F items of the parts passed, per ring slot
   bool end;
 };
@@ -158,11 +162,12 @@ __device__ __forceinline__ void cursor_init(Cursor& c, const BwdPipeParams& p) {
   c.end = false;
 }
 
-__device__ __forceinline__ void cursor_next(Cursor& c, const BwdPipeParams& p) {
+__device__ __forceinline__ void cursor_next(Cursor& c, const BwdPipeParams& p, int order) {
   const int b = c.part == 0 ? c.j - 2 : c.j;
   if (c.part == 0) {
-    c.cum_m += 2u * static_cast<unsigned>(c.size);
-    c.cum_ms[b % kGRing] += 2u * static_cast<unsigned>(c.size);
+    const int ndh = order == kOrderDh ? items_dh(p, b) : 0;
+    c.cum_m += 2u * static_cast<unsigned>(order == kOrderDh ? ndh : c.size);
+    c.cum_ms[b % kGRing] += 2u * static_cast<unsigned>(c.size - ndh);
   } else {
     c.cum_f[b % kGRing] += 2u * static_cast<unsigned>(c.size);
   }
@@ -191,13 +196,12 @@ __device__ __forceinline__ void cursor_next(Cursor& c, const BwdPipeParams& p) {
   c.size = c.part == 0 ? items_m(p, nb) : items_f(p, nb);
 }
 
-// Counter of the M items of ring slot s, where M items are counted per slot (parts).
+// Counter of the M items of ring slot s, where M items are counted per slot (kOrderParts; kOrderDh: the dW_s items).
 constexpr unsigned kSlotM = 2 + kGRing;
 
-// The item with queue index i (the cursor only moves forward; i never decreases per caller). parts: M items do not
-// depend on one another.
-__device__ __forceinline__ Item cursor_item(Cursor& c, const BwdPipeParams& p, int i, bool parts) {
-  while (!c.end && i >= c.base + c.size) cursor_next(c, p);
+// The item with queue index i (the cursor only moves forward; i never decreases per caller).
+__device__ __forceinline__ Item cursor_item(Cursor& c, const BwdPipeParams& p, int i, int order) {
+  while (!c.end && i >= c.base + c.size) cursor_next(c, p, order);
   Item it{};
   if (c.end) {
     it.kind = kItemEnd;
@@ -209,17 +213,18 @@ __device__ __forceinline__ Item cursor_item(Cursor& c, const BwdPipeParams& p, i
   if (c.part == 1) {
     it.kind = kItemF;
     it.idx = local;
-    if (parts) {  // every M item of the blocks that had this ring slot
+    if (order != kOrderChain) {  // every (kOrderDh: dW_s) item of the blocks that had this ring slot
       it.ctr0 = kSlotM + static_cast<unsigned>(b % kGRing);
       it.tgt0 = c.cum_ms[b % kGRing];
-    } else if (b >= kGRing) {  // every M item of blocks <= b - 3 (the parts passed, minus M(b-2))
-      it.ctr0 = 1;
-      it.tgt0 = c.cum_m - 2u * static_cast<unsigned>(items_m(p, b - 2));
+    }
+    if (order != kOrderParts && b >= kGRing) {  // every M (dh_s) item of blocks <= b - 3 (the parts passed, minus block b - 2's)
+      it.ctr1 = 1;
+      it.tgt1 = c.cum_m - 2u * static_cast<unsigned>(order == kOrderDh ? items_dh(p, b - 2) : items_m(p, b - 2));
     }
   } else {
     const Geo g = geo(p, b);
     const int ndw = g.vt * p.ntd, ndh = g.tt * p.ntd;
-    if (parts) {  // dh_s first: with few tokens its items are the long ones
+    if (order != kOrderChain) {  // dh_s first: they are waited for
       it.kind = local < ndh ? kItemDH : kItemDW;
       it.idx = local < ndh ? local : local - ndh;
     } else {
@@ -228,8 +233,8 @@ __device__ __forceinline__ Item cursor_item(Cursor& c, const BwdPipeParams& p, i
     }
     it.ctr0 = 2 + g.slot;  // every F item of block b
     it.tgt0 = c.cum_f[g.slot];
-    if (!parts) {
-      it.ctr1 = 1;         // every M item of blocks < b
+    if (order != kOrderParts) {
+      it.ctr1 = 1;         // every M (kOrderDh: dh_s) item of blocks < b
       it.tgt1 = c.cum_m;
     }
   }
@@ -327,8 +332,9 @@ template <bool SPLIT, typename Head>
 __global__ void __launch_bounds__(kThreads, 1)
 bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p, const Head head) {
   constexpr bool kHead = !std::is_same<Head, NoHead>::value;
-  bool parts = false;
-  if constexpr (kHead) parts = head.dh_parts != 0;
+  int order = kOrderChain;
+  if constexpr (kHead) order = head.order;
+  const bool parts = order == kOrderParts;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* staging_all = smem + STAGES * STAGE_BYTES;
@@ -395,7 +401,7 @@ bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p, co
         const int slot = k % kItemDepth;
         const uint32_t par = static_cast<uint32_t>(k / kItemDepth) & 1u;
         if (!wait_bounded<true>(iempty + slot, par ^ 1u, abort_flag, p.ctl, 21)) break;
-        const Item it = cursor_item(cur, p, next_i, parts);
+        const Item it = cursor_item(cur, p, next_i, order);
         if (it.kind != kItemEnd) {
           next_i = static_cast<int>(atomicAdd(p.ctrl, 1u));  // the next item, fetched ahead
           // the item is published only once what it reads is complete
@@ -754,7 +760,7 @@ bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p, co
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(lead_tempty + sh * 8);
       } else {
-        ctr = parts ? kSlotM + static_cast<unsigned>(g.slot) : 1u;
+        ctr = parts || (order == kOrderDh && it.kind == kItemDW) ? kSlotM + static_cast<unsigned>(g.slot) : 1u;
         const int h = hp;
         hp ^= 1;
         const bool w = wait_bounded(tfull + h, uses[h] & 1u, abort_flag, p.ctl, 33);

@@ -132,6 +132,28 @@ def test_gradients_over_many_vocabulary_blocks(N, d, V, split):
         assert np.linalg.norm(f64(dW[v:v + 8192]) - ref) <= rel * np.linalg.norm(ref) + 1e-5 * gl.abs().max().item()
 
 
+@pytest.mark.parametrize("N,d,V,chunk", [(1500, 64, 60_001, 4096), (1100, 72, 200_001, 256), (600, 64, 100_001, 256)])
+def test_gradients_over_blocks_of_tokens_and_words(N, d, V, chunk):
+    """Sums over vocabulary blocks (dh) and over token blocks (dW) one after another: five vocabulary blocks of all
+    tokens; five token blocks by three vocabulary blocks; three by two. Bounds as above; and bitwise the same again."""
+    h, W, tok = inputs(N, d, V, seed=V)
+    gl, ge = torch.randn(N, device="cuda"), 0.3 * torch.randn(N, device="cuda")
+    h.requires_grad_(), W.requires_grad_()
+    logp, ent = head_logprobs(h, W, tok, token_chunk=chunk)
+    dh, dW = torch.autograd.grad([logp, ent], (h, W), [gl, ge], retain_graph=True)
+    for _ in range(3):
+        again = torch.autograd.grad([logp, ent], (h, W), [gl, ge], retain_graph=True)
+        assert torch.equal(dh, again[0]) and torch.equal(dW, again[1])
+    G = oo.token_logprobs_grad(f64(h) @ f64(W).T, tok.cpu().numpy(), 1.0, f64(gl), f64(ge))
+    rel = 4e-3 + 2.0 ** -8
+    ref_h, ref_W = G @ f64(W), G.T @ f64(h)
+    for n in range(N):
+        assert np.linalg.norm(f64(dh[n]) - ref_h[n]) <= 1.5 * rel * np.linalg.norm(ref_h[n]) + 1e-5 * gl.abs().max().item()
+    for v in range(0, V, 8192):
+        ref = ref_W[v:v + 8192]
+        assert np.linalg.norm(f64(dW[v:v + 8192]) - ref) <= rel * np.linalg.norm(ref) + 1e-5 * gl.abs().max().item()
+
+
 def test_gradient_against_differences():
     """Directional differences of the fp64 forward along random directions; bound: G's one rounding to bf16."""
     N, d, V = 6, 16, 40
