@@ -144,12 +144,17 @@ head_logprobs_kernel(const __grid_constant__ CUtensorMap tm_h, const __grid_cons
       uint32_t phase = 0, armed = 0;
       bool ok = true;
       const uint32_t full_lead = mapa_shared(smem_u32(full), 0);
+      // One tile of tokens: all clusters read the same few lines of h at once. Each begins elsewhere in the hidden
+      // dimension (256 tokens, d = 4096: 178 us, so 170), and few tokens have copies (see head_copies).
+      const bool rotate = p.N <= 2 * kBM;
+      const int copy = cid % p.copies;
       for (int u = cid; ok && u < p.units; u += ncl) {
         int row0, vt0, vt1, seg;
         unit_range(p, u, row0, vt0, vt1, seg);
         for (int vt = vt0; ok && vt < vt1; ++vt) {
           const int brow = vt * BN + static_cast<int>(rank) * HB;
-          for (int kb = 0; kb < p.kb; ++kb) {
+          int k0 = rotate ? u % p.kb : 0;
+          for (int kb = 0; kb < p.kb; ++kb, k0 = k0 + 1 == p.kb ? 0 : k0 + 1) {
             if (!wait_bounded(empty + stage, phase ^ 1u, abort_flag, p.ctl, 41)) {
               ok = false;
               break;
@@ -160,8 +165,8 @@ head_logprobs_kernel(const __grid_constant__ CUtensorMap tm_h, const __grid_cons
               mbar_arrive_expect_tx(full + stage, 2 * STAGE_BYTES);  // both CTAs' bytes
               armed |= 1u << stage;
             }
-            tma_load_2d_pair(sa, &tm_h, fbar, kb * kBK, row0 + my_rows);
-            tma_load_2d_pair(sa + A_BYTES, &tm_W, fbar, kb * kBK, brow);
+            tma_load_3d_pair(sa, &tm_h, fbar, k0 * kBK, row0 + my_rows, copy);
+            tma_load_2d_pair(sa + A_BYTES, &tm_W, fbar, k0 * kBK, brow);
             if (++stage == STAGES) {
               stage = 0;
               phase ^= 1u;
@@ -293,9 +298,9 @@ head_logprobs_kernel(const __grid_constant__ CUtensorMap tm_h, const __grid_cons
 // 256-row tiles on them. Every warp takes kRows words at a time, its lanes walk the hidden dimension with
 // 16-byte loads of W and the tokens' states in fp32 from shared memory, and the dot products end in
 // a warp reduction; lane t keeps token t's running sums. fp32 multiply-adds: no drift of
-// long tensor-core accumulations. Measured beside the tensor-core path (128256 words): one token, d = 4096 147 us
-// (7.1 TB/s) against 165, d = 2048 78 against 83; two tokens 152 against 165 and 90 against 83; four
-// tokens 172 against 165, where the multiply-adds and not the loads set the time. So it takes one or two.
+// long tensor-core accumulations. Measured beside the tensor-core path (128256 words; d = 4096 172 us and d = 2048 94 us
+// for three or four tokens): one token 147 us (7.1 TB/s) and 78; two tokens 152 and 90; four tokens 172 at d = 4096,
+// where the multiply-adds and not the loads set the time. So it takes one or two.
 constexpr int kFewThreads = 512;
 constexpr int kFewWarps = kFewThreads / 32;
 constexpr int kRows = 4;
@@ -440,6 +445,14 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const float4* __restric
   }
 }
 
+// `copies` copies of x [n], one behind the other.
+__global__ void __launch_bounds__(256) head_copy_kernel(const uint4* __restrict__ x, uint4* __restrict__ y, int n, int copies) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  const uint4 v = x[i];
+  for (int c = 0; c < copies; ++c) y[c * n + i] = v;
+}
+
 cudaLaunchConfig_t head_config(cudaLaunchAttribute* attr, int clusters, cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
@@ -481,6 +494,12 @@ cudaError_t head_prepare(int* max_clusters) {
   cudaLaunchConfig_t cfg = head_config(attr, 1, nullptr);
   cfg.numAttrs = 1;  // occupancy: the cluster shape only
   return cudaOccupancyMaxActiveClusters(max_clusters, head_logprobs_kernel, &cfg);
+}
+
+cudaError_t launch_head_copy(const uint16_t* h, void* copies, int64_t n, int count, cudaStream_t stream) {
+  const int n8 = static_cast<int>(n / 8);
+  head_copy_kernel<<<(n8 + 255) / 256, 256, 0, stream>>>(reinterpret_cast<const uint4*>(h), static_cast<uint4*>(copies), n8, count);
+  return cudaGetLastError();
 }
 
 constexpr int kFewTokens = 2;

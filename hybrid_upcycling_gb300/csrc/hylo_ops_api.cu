@@ -38,9 +38,30 @@ int head_segments(int64_t N) {
   return s > kMaxSegments ? static_cast<int>(s) : kMaxSegments;
 }
 
-// The tokens' logits, then two partial sums per token and segment.
-size_t head_fwd_bytes(int64_t N) {
-  return round256(N * sizeof(float)) + static_cast<size_t>(N) * 2 * head_segments(N) * sizeof(float4);
+// Copies of h in the workspace. All clusters read h all the time, and less than 128 KiB lies in a few of L2's slices, which
+// then hold everything up: 8 tokens of d = 4096, V = 128256 took 190 to 280 us by where h lay, and 172 us with
+// copies of 512 KiB in all. A small LM head is read in a few microseconds, in which the copies cost more.
+constexpr int64_t kHotBytes = 128 << 10, kCopyBytes = 512 << 10, kCopyHeadBytes = 64 << 20;
+int head_copies(int64_t N, int64_t d, int64_t V) {
+  const int64_t bytes = N * d * 2;
+  if (bytes >= kHotBytes || V * d * 2 < kCopyHeadBytes || head_few_fits(N, d)) return 1;
+  return static_cast<int>(cdiv(kCopyBytes, bytes));
+}
+
+// The forward's workspace: the tokens' logits, two partial sums per token and segment, and copies of h.
+struct HeadFwd {
+  size_t part, copies, total;
+};
+HeadFwd head_fwd_layout(int64_t N, int64_t d, int64_t V) {
+  HeadFwd l{};
+  l.part = round256(N * sizeof(float));
+  l.copies = l.total = l.part + static_cast<size_t>(N) * 2 * head_segments(N) * sizeof(float4);
+  const int copies = head_copies(N, d, V);
+  if (copies > 1) {
+    l.copies = round256(l.copies);
+    l.total = l.copies + static_cast<size_t>(copies) * N * d * 2;
+  }
+  return l;
 }
 
 // The backward's workspace: the G ring(s), the counters, and the fp32 sums that are joined or rounded at the end.
@@ -146,7 +167,7 @@ size_t hylo_head_logprobs_workspace_bytes(int64_t N, int64_t d, int64_t V, int64
                                           int grad_dtype) {
   clear_error();
   if (!head_sizes_ok(N, d, V) || (grad_dtype != HYLO_F32 && grad_dtype != HYLO_BF16)) return 0;
-  const size_t f = head_fwd_bytes(N), b = head_bwd_layout(N, d, V, token_chunk, split_g != 0, grad_dtype).total;
+  const size_t f = head_fwd_layout(N, d, V).total, b = head_bwd_layout(N, d, V, token_chunk, split_g != 0, grad_dtype).total;
   return f > b ? f : b;
 }
 
@@ -157,8 +178,8 @@ hylo_status hylo_head_logprobs(const uint16_t* h, const uint16_t* W, int64_t N, 
   if (!logp) return fail(HYLO_ERR_NULL, "logp is NULL");
   if (!aligned(logp, 4) || !aligned(entropy, 4) || !aligned(lse, 4))
     return fail(HYLO_ERR_ALIGN, "output pointers must be 4-byte aligned");
-  hylo_status st = check_head(h, W, N, d, V, tau, tokens, workspace, workspace_bytes,
-                              head_sizes_ok(N, d, V) ? head_fwd_bytes(N) : 0);
+  const HeadFwd l = head_sizes_ok(N, d, V) ? head_fwd_layout(N, d, V) : HeadFwd{};
+  hylo_status st = check_head(h, W, N, d, V, tau, tokens, workspace, workspace_bytes, l.total);
   if (st != HYLO_OK) return st;
   DeviceState* dev = nullptr;
   if ((st = current_device(&dev)) != HYLO_OK) return st;
@@ -169,7 +190,7 @@ hylo_status hylo_head_logprobs(const uint16_t* h, const uint16_t* W, int64_t N, 
   p.inv_tau = 1.0f / tau;
   p.tokens = tokens;
   p.z_token = static_cast<float*>(workspace);
-  p.part = reinterpret_cast<float4*>(static_cast<char*>(workspace) + round256(N * sizeof(float)));
+  p.part = reinterpret_cast<float4*>(static_cast<char*>(workspace) + l.part);
   p.ctl = WaitCtl{dev->status, wait_limit_ns()};
   if (head_few_fits(N, d)) {
     p.slots = dev->sms < 2 * head_segments(N) ? dev->sms : 2 * head_segments(N);
@@ -178,7 +199,14 @@ hylo_status hylo_head_logprobs(const uint16_t* h, const uint16_t* W, int64_t N, 
   }
   CUtensorMap m_h, m_W;
   const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  if ((st = make_map(&m_h, h, bf, d, N, d * 2, kBK, kBM)) != HYLO_OK) return st;
+  p.copies = head_copies(N, d, V);
+  if (p.copies > 1) {
+    void* const copies = static_cast<char*>(workspace) + l.copies;
+    const cudaError_t e = launch_head_copy(h, copies, N * d, p.copies, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "copy the hidden states");
+    h = static_cast<const uint16_t*>(copies);
+  }
+  if ((st = make_map_3d(&m_h, h, bf, d, N, p.copies, d * 2, kBK, kBM)) != HYLO_OK) return st;
   if ((st = make_map(&m_W, W, bf, d, V, d * 2, kBK, kFusedBN / 2)) != HYLO_OK) return st;
   p.kb = static_cast<int>(cdiv(d, kBK));
   p.token_tiles = static_cast<int>(cdiv(N, 2 * kBM));

@@ -55,6 +55,7 @@ struct HeadParams {
   int vtiles;       // ceil(V / 256)
   int nseg;         // vocabulary segments per token tile
   int units;        // token_tiles * nseg
+  int copies;       // of h, which the clusters share out
   float c;          // log2(e) / tau
   float inv_tau;
   const int64_t* tokens;
@@ -66,6 +67,8 @@ struct HeadParams {
 cudaError_t head_prepare(int* max_clusters);
 cudaError_t launch_head_logprobs(const CUtensorMap& h, const CUtensorMap& W, const HeadParams& p, float* logp,
                                  float* entropy, float* lse, int clusters, cudaStream_t stream);
+
+cudaError_t launch_head_copy(const uint16_t* h, void* copies, int64_t n, int count, cudaStream_t stream);
 
 // The forward of few tokens, without the tensor cores; p.slots CTAs.
 bool head_few_fits(int64_t N, int64_t d);

@@ -55,7 +55,7 @@ hylo_status hylo_token_logprobs_backward(const void* z, int dtype, int64_t N, in
  * of 8 in 8..65536. Inputs are meant finite (where they are not, the results of the tokens
  * concerned are NaN or infinite). tokens as above. entropy and lse may be NULL; the backward needs lse
  * (and entropy, if g_entropy is given). workspace: at least hylo_head_logprobs_workspace_bytes(),
- * 256-byte aligned, not shared with a call still running on another stream; the forward uses O(N) of it,
+ * 256-byte aligned, not shared with a call still running on another stream; the forward uses O(N) of it (and up to 640 KiB for copies of few hidden states),
  * the backward the G ring of hylo_kl_backward (at most 128 MiB, twice that with split_g), the fp32
  * parts that dh is joined from where N <= 1024 (at most 128 MiB) and, for bf16 gradients, the fp32
  * sums behind them: N d, and V d if N is more than one token block.

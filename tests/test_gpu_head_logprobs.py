@@ -61,6 +61,20 @@ def test_forward(N, d, V, tau):
     near(ent, H, 2 * tol_of(z, d, V, tau))
 
 
+@pytest.mark.parametrize("N,d,V", [(3, 2048, 20_001), (8, 4096, 9000), (15, 4096, 8193), (31, 2048, 16_400), (32, 2048, 16_400),
+                                   (5, 65536, 600)])
+def test_few_tokens_of_a_large_head(N, d, V):
+    """A head of 64 MiB and more with hidden states of less than 128 KiB, or just that; also in a larger batch."""
+    h, W, tok = inputs(N, d, V, seed=N)
+    logp, ent = head_logprobs(h, W, tok)
+    z = f64(h) @ f64(W).T
+    lp, H, _, _ = oo.token_logprobs(z, tok.cpu().numpy(), 1.0)
+    near(logp, lp, tol_of(z, d, V, 1.0))
+    near(ent, H, 2 * tol_of(z, d, V, 1.0))
+    many, _ = head_logprobs(h.repeat(40, 1), W, tok.repeat(40))
+    near(many.view(40, N)[7], lp, tol_of(z, d, V, 1.0))
+
+
 @pytest.mark.parametrize("split", [False, True])
 @pytest.mark.parametrize("N,d,V,tau,chunk", [
     (1, 8, 3, 1.0, 0), (5, 72, 300, 0.5, 4096), (130, 520, 1000, 2.0, 4096), (700, 256, 5003, 1.0, 256),
