@@ -1,4 +1,5 @@
 // Host side of the C ABI declared in include/hylo_ops.h: argument checks and launches.
+#include <climits>
 #include <cmath>
 
 #include "hylo_host.h"
@@ -67,17 +68,30 @@ HeadFwd head_fwd_layout(int64_t N, int64_t d, int64_t V) {
 // The backward's workspace: the G ring(s), the counters, and the fp32 sums that are joined or rounded at the end.
 struct HeadBwd {
   size_t ctrl, dh, dW, total;
-  int64_t width;   // words of a vocabulary block, or 0 (pipe_width)
-  int64_t parts;   // dh is stored in this many parts, or 0
-  bool dW_direct;  // dW is written in bf16 by the pipelined backward itself
+  int64_t width;     // words of a vocabulary block, or 0 (pipe_width)
+  int64_t parts;     // dh is stored in this many parts, or 0
+  int64_t dh_words;  // words of a part
+  bool dW_direct;    // dW is written in bf16 by the pipelined backward itself
 };
-// Few tokens: dh in parts, one per vocabulary block, at most 16 of them. Long blocks wait less for ring slots, short ones
-// spread dh over more clusters, which counts with more tokens. Measured at d = 2048, V = 128256 with blocks of 8192,
+// Few tokens: dh in parts, one per vocabulary block (at most 16 of those) or several. Long blocks wait less for ring slots,
+// short ones spread dh over more clusters, which counts with more tokens. Measured at d = 2048, V = 128256 with blocks of 8192,
 // 12288, 16384 and 24576 words: 256 tokens 642, 550, 587, 534 us; 512 tokens 777, 714, 649, 643; 1024 tokens 1062, 1054,
 // 1075 us (24576 words do not fit the ring). Fewer words where that leaves fewer than three blocks. N d is bounded so that
 // a part is at most 8 MiB; with more tokens the chain of additions is short beside the rest.
 constexpr int64_t kPartTokens = 1024, kPartElems = int64_t(1) << 21, kMaxParts = 16;
 constexpr int64_t part_words(int64_t N) { return N <= 512 ? 24576 : 12288; }
+// With few 256 x 256 tiles of dh (N d small) a block's words are cut up too, into parts of their own, so that the long
+// products run on more clusters. Measured (1, 2, 3, 4 parts a block; V = 128256 if not said): 256 tokens, d = 2048 538, 462,
+// 475, 486 us, d = 4096 854, 878, 897, 908; 512 tokens, d = 2048 644, 625, 636, 653; 1000 tokens, d = 2048 1077,
+// 1129, 1184, 1197; 800 tokens, d = 1024, V = 32000 242, 183, 183, 174; 1000 tokens, d = 512, V = 151936 795, 527, 463,
+// 435. So up to 16 items a block with one tile of tokens and up to 32 with more, of at least 1024 words.
+constexpr int64_t kPartBytes = int64_t(128) << 20;  // of all parts together
+constexpr int64_t kMinPartWords = 1024;
+int64_t block_parts(int64_t N, int64_t d, int64_t blocks) {
+  const int64_t tiles = cdiv(N, 256) * cdiv(d, 256), fit = kPartBytes / (blocks * N * d * 4);
+  const int64_t want = cdiv(N <= 256 ? 16 : 32, tiles);
+  return want < fit ? want : fit < 1 ? 1 : fit;
+}
 
 HeadBwd head_bwd_layout(int64_t N, int64_t d, int64_t V, int64_t token_chunk, bool split, int grad_dtype) {
   HeadBwd l{};
@@ -89,7 +103,9 @@ HeadBwd head_bwd_layout(int64_t N, int64_t d, int64_t V, int64_t token_chunk, bo
     w = cdiv(w, 256) * 256;
     if (kGRing * R * w * 2 <= kGBlockBytes) {
       l.width = w;
-      l.parts = cdiv(V, w);
+      l.dh_words = cdiv(cdiv(w, block_parts(N, d, cdiv(V, w))), 64) * 64;
+      if (l.dh_words < kMinPartWords) l.dh_words = kMinPartWords;
+      l.parts = (cdiv(V, w) - 1) * cdiv(w, l.dh_words) + cdiv(V - (cdiv(V, w) - 1) * w, l.dh_words);
       ring = static_cast<size_t>(kGRing) * R * w * 2;
     }
   }
@@ -257,7 +273,8 @@ hylo_status hylo_head_logprobs_backward(const uint16_t* h, const uint16_t* W, in
   cudaError_t e = cudaMemsetAsync(p.ctrl, 0, (kPipeCtrlWords + kGRing) * sizeof(unsigned), stream);
   if (e != cudaSuccess) return cuda_fail(e, "clear the backward's work counters");
   const int order = l.parts > 0 ? kOrderParts : p.TB == 1 || p.VB >= kGRing ? kOrderDh : kOrderChain;
-  const HeadGrad g{tokens, lse, entropy, g_logp, g_entropy, 1.0f / tau, l.dW_direct ? 1 : 0, order};
+  const HeadGrad g{tokens, lse, entropy, g_logp, g_entropy, 1.0f / tau, l.dW_direct ? 1 : 0, order,
+                   l.parts > 0 ? static_cast<int>(l.dh_words) : INT_MAX};
   e = launch_bwd_pipe_head(maps, p, g, clusters, stream);
   if (e == cudaSuccess && (bf16 || l.parts > 0))
     e = launch_join_parts(dh32, l.parts > 0 ? static_cast<int>(l.parts) : 1, dh, bf16, N * d, dev->sms, stream);

@@ -87,6 +87,7 @@ struct HeadGrad {
   float inv_tau;
   int dw_bf16;             // one token block: map kMapDW is a bf16 tensor of 32 x 32 tiles with 64-byte swizzle
   int order;               // see below
+  int dh_words;            // kOrderParts: words of a block whose products go into one part (a multiple of 64); else INT_MAX
 };
 // How the items of one block wait for those of others (M(b): products of block b, F(b): its G).
 //   kOrderChain: M(b) needs all of M(b - 1), as the distillation loss.

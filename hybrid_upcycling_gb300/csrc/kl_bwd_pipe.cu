@@ -43,9 +43,9 @@
 // M(b-1) only, which come first in their block (kOrderDh): dW_s tiles of one block do not meet those of the next, and long
 // dh_s items at a block's end would hold up the next block (1500 tokens, d = 2048, V = 128256: 1.93 ms in the order
 // above, 1.57 so; 2048 tokens 2.30 and 2.08; 4096 tokens and more the same). With few tokens the additions into dh_s are a
-// chain over the whole vocabulary on a few clusters all the same (N <= 256: 0.85 ms in all against 0.53): there
-// (kOrderParts) every block stores its dh_s products apart, for a sum in fixed order afterwards, and M(b) needs F(b)
-// only. F(b) needs M(b-3) always.
+// chain over the whole vocabulary on a few clusters all the same (N <= 256: 0.85 ms in all against 0.46): there
+// (kOrderParts) every block stores its dh_s products apart, over all of its words or over stretches of them
+// (HeadGrad::dh_words), for a sum in fixed order afterwards, and M(b) needs F(b) only. F(b) needs M(b-3) always.
 //
 // TMEM holds two 256-column halves. An M item takes one; an F item takes one for the teacher
 // tile and the other for the student tile. The UMMA warp signals the teacher half as soon as its
@@ -54,6 +54,7 @@
 // forming G. Halves are handed out so that the next item's UMMAs always start in the half
 // freed first (after an F item, its teacher half; after an M item, the other half), so the
 // epilogue's work overlaps the UMMAs of the next item instead of stalling them.
+#include <climits>
 #include <cmath>
 #include <type_traits>
 
@@ -112,10 +113,14 @@ struct Geo {
   int r0, v0;   // first token, first word
   int R, Vb;    // tokens, words in the block
   int tt, vt;   // 256-token tiles, 256-word tiles
+  int ds;       // dh_s items per 256 x 256 tile of dh_s
   int slot;     // G ring slot
 };
 
-__device__ __forceinline__ Geo geo(const BwdPipeParams& p, int b) {
+// dhw: words of a dh_s item (a multiple of 64), or all of the block's.
+constexpr int kAllWords = INT_MAX;
+
+__device__ __forceinline__ Geo geo(const BwdPipeParams& p, int b, int dhw = kAllWords) {
   Geo g;
   g.tb = b / p.VB;
   g.vb = b - g.tb * p.VB;
@@ -125,6 +130,7 @@ __device__ __forceinline__ Geo geo(const BwdPipeParams& p, int b) {
   g.Vb = min(p.bw, p.V - g.v0);
   g.tt = (g.R + BN - 1) / BN;
   g.vt = (g.Vb + BN - 1) / BN;
+  g.ds = dhw == kAllWords ? 1 : (g.Vb + dhw - 1) / dhw;
   g.slot = b % kGRing;
   return g;
 }
@@ -134,12 +140,12 @@ __device__ __forceinline__ int items_f(const BwdPipeParams& p, int b) {
   return g.tt * g.vt;
 }
 
-__device__ __forceinline__ int items_m(const BwdPipeParams& p, int b) {
-  const Geo g = geo(p, b);
-  return (g.vt + g.tt) * p.ntd;
+__device__ __forceinline__ int items_m(const BwdPipeParams& p, int b, int dhw) {
+  const Geo g = geo(p, b, dhw);
+  return (g.vt + g.tt * g.ds) * p.ntd;
 }
 
-__device__ __forceinline__ int items_dh(const BwdPipeParams& p, int b) { return geo(p, b).tt * p.ntd; }
+__device__ __forceinline__ int items_dh(const BwdPipeParams& p, int b) { return geo(p, b).tt * p.ntd; }  // (ds = 1)
 
 // Walks the queue order part by part: segment j holds M(j-2) (part 0) if 0 <= j-2 < B and F(j)
 // (part 1) if j < B. It keeps, per counter, the completion total of the parts already passed
@@ -162,7 +168,7 @@ __device__ __forceinline__ void cursor_init(Cursor& c, const BwdPipeParams& p) {
   c.end = false;
 }
 
-__device__ __forceinline__ void cursor_next(Cursor& c, const BwdPipeParams& p, int order) {
+__device__ __forceinline__ void cursor_next(Cursor& c, const BwdPipeParams& p, int order, int dhw) {
   const int b = c.part == 0 ? c.j - 2 : c.j;
   if (c.part == 0) {
     const int ndh = order == kOrderDh ? items_dh(p, b) : 0;
@@ -193,15 +199,15 @@ __device__ __forceinline__ void cursor_next(Cursor& c, const BwdPipeParams& p, i
     }
   }
   const int nb = c.part == 0 ? c.j - 2 : c.j;
-  c.size = c.part == 0 ? items_m(p, nb) : items_f(p, nb);
+  c.size = c.part == 0 ? items_m(p, nb, dhw) : items_f(p, nb);
 }
 
 // Counter of the M items of ring slot s, where M items are counted per slot (kOrderParts; kOrderDh: the dW_s items).
 constexpr unsigned kSlotM = 2 + kGRing;
 
 // The item with queue index i (the cursor only moves forward; i never decreases per caller).
-__device__ __forceinline__ Item cursor_item(Cursor& c, const BwdPipeParams& p, int i, int order) {
-  while (!c.end && i >= c.base + c.size) cursor_next(c, p, order);
+__device__ __forceinline__ Item cursor_item(Cursor& c, const BwdPipeParams& p, int i, int order, int dhw) {
+  while (!c.end && i >= c.base + c.size) cursor_next(c, p, order, dhw);
   Item it{};
   if (c.end) {
     it.kind = kItemEnd;
@@ -219,11 +225,11 @@ __device__ __forceinline__ Item cursor_item(Cursor& c, const BwdPipeParams& p, i
     }
     if (order != kOrderParts && b >= kGRing) {  // every M (dh_s) item of blocks <= b - 3 (the parts passed, minus block b - 2's)
       it.ctr1 = 1;
-      it.tgt1 = c.cum_m - 2u * static_cast<unsigned>(order == kOrderDh ? items_dh(p, b - 2) : items_m(p, b - 2));
+      it.tgt1 = c.cum_m - 2u * static_cast<unsigned>(order == kOrderDh ? items_dh(p, b - 2) : items_m(p, b - 2, dhw));
     }
   } else {
-    const Geo g = geo(p, b);
-    const int ndw = g.vt * p.ntd, ndh = g.tt * p.ntd;
+    const Geo g = geo(p, b, dhw);
+    const int ndw = g.vt * p.ntd, ndh = g.tt * g.ds * p.ntd;
     if (order != kOrderChain) {  // dh_s first: they are waited for
       it.kind = local < ndh ? kItemDH : kItemDW;
       it.idx = local < ndh ? local : local - ndh;
@@ -279,10 +285,16 @@ __device__ __forceinline__ uint64_t slice_desc(bool mn, uint32_t base, int k) {
   return mn ? smem_desc_sw128(base + k * 2048, 8192, 1024) : smem_desc_sw128(base + k * 32, 0, 1024);
 }
 
-// 64-deep k-blocks of an M item (both passes when split).
+// 64-deep k-blocks of an M item's operands: of the block's tokens (dW_s) or of its words from `first` on (dh_s).
+__device__ __forceinline__ int dh_kblocks(const Geo& g, int first, int dhw) { return (min(g.Vb - first, dhw) + kBK - 1) / kBK; }
+// The first word of dh_s item `idx`.
+__device__ __forceinline__ int dh_first(const BwdPipeParams& p, const Geo& g, int idx, int dhw) {
+  return g.ds == 1 ? 0 : idx / (g.tt * p.ntd) * dhw;
+}
+// The same of an M item, both passes when split.
 template <bool SPLIT>
-__device__ __forceinline__ int m_kblocks(const Geo& g, int kind) {
-  const int k = kind == kItemDW ? (g.R + kBK - 1) / kBK : (g.Vb + kBK - 1) / kBK;
+__device__ __forceinline__ int m_kblocks(const BwdPipeParams& p, const Geo& g, const Item& it, int dhw) {
+  const int k = it.kind == kItemDW ? (g.R + kBK - 1) / kBK : dh_kblocks(g, dh_first(p, g, it.idx, dhw), dhw);
   return SPLIT ? 2 * k : k;
 }
 
@@ -335,6 +347,8 @@ bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p, co
   int order = kOrderChain;
   if constexpr (kHead) order = head.order;
   const bool parts = order == kOrderParts;
+  int dhw = kAllWords;
+  if constexpr (kHead) dhw = head.dh_words;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* staging_all = smem + STAGES * STAGE_BYTES;
@@ -401,7 +415,7 @@ bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p, co
         const int slot = k % kItemDepth;
         const uint32_t par = static_cast<uint32_t>(k / kItemDepth) & 1u;
         if (!wait_bounded<true>(iempty + slot, par ^ 1u, abort_flag, p.ctl, 21)) break;
-        const Item it = cursor_item(cur, p, next_i, order);
+        const Item it = cursor_item(cur, p, next_i, order, dhw);
         if (it.kind != kItemEnd) {
           next_i = static_cast<int>(atomicAdd(p.ctrl, 1u));  // the next item, fetched ahead
           // the item is published only once what it reads is complete
@@ -441,7 +455,7 @@ bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p, co
         // Every coordinate is set up once per item: a stage then costs only its wait, its arming
         // and its TMA instructions (the producer, not the tensor cores, limited the M items while
         // it also did this arithmetic per stage).
-        const Geo g = geo(p, it.b);
+        const Geo g = geo(p, it.b, dhw);
         const int r_a = static_cast<int>(rank) * kBM;  // this CTA's rows of the A tile
         const int r_b = static_cast<int>(rank) * HB;   // this CTA's rows of the B tile
         bool fine = true;
@@ -481,7 +495,9 @@ bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p, co
             advance();
           }
         } else {
-          const int mi = it.idx / p.ntd, nj = it.idx - mi * p.ntd;
+          const int first = it.kind == kItemDH ? dh_first(p, g, it.idx, dhw) : 0;
+          const int tile = g.ds == 1 || it.kind != kItemDH ? it.idx : it.idx % (g.tt * p.ntd);
+          const int mi = tile / p.ntd, nj = tile - mi * p.ntd;
           const int mrow = mi * BN + r_a;   // A rows: words (dW_s) or tokens (dh_s) of the block
           const int ncol = nj * BN + r_b;   // B rows: this CTA's d_s columns
           if (it.kind == kItemDW) {  // A = G^T (word-major), B = h_s of the block's tokens; K = tokens
@@ -501,14 +517,14 @@ bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p, co
               }
             }
           } else {  // A = G (token rows, K-major), B = W_s of the block's words; K = words
-            const int nk = (g.Vb + kBK - 1) / kBK;
+            const int nk = dh_kblocks(g, first, dhw);
             for (int term = 0; fine && term < (SPLIT ? 2 : 1); ++term) {
               const int z = g.slot + term * kGRing;
               for (int kk = 0; kk < nk; ++kk) {
                 uint8_t* sa;
                 uint32_t fb;
                 if (!(fine = next(sa, fb))) break;
-                const int k0 = kk * kBK;
+                const int k0 = first + kk * kBK;
                 tma_load_3d_pair(sa, &maps.m[kMapGA], fb, k0, mrow, z);
                 tma_load_2d_pair(sa + A_BYTES, &maps.m[kMapWsB], fb, ncol, g.v0 + k0);
                 tma_load_2d_pair(sa + A_BYTES + 8192, &maps.m[kMapWsB], fb, ncol + 64, g.v0 + k0);
@@ -551,7 +567,7 @@ bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p, co
         const Item it = items[slot];
         mbar_arrive(iempty + slot);
         if (it.kind == kItemEnd) break;
-        const Geo g = geo(p, it.b);
+        const Geo g = geo(p, it.b, dhw);
         if (!kHead && it.kind == kItemF) {
           // teacher tile (K = d_t) into half t = hp, student tile (K = d_s) into the other; each
           // half is awaited just before its own UMMAs, and the teacher half is signalled as soon
@@ -605,7 +621,7 @@ bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p, co
           const bool amn = it.kind == kItemDW;
           const uint32_t idesc = fwd ? kIdescF : amn ? kIdescDW : kIdescDH;
           const uint32_t d = tmem_base + static_cast<uint32_t>(h * BN);
-          const int nkb = fwd ? p.kb_s : m_kblocks<SPLIT>(g, it.kind);
+          const int nkb = fwd ? p.kb_s : m_kblocks<SPLIT>(p, g, it, dhw);
           for (int kb = 0; kb < nkb; ++kb) {
             if (!wait_bounded(full + stage, phase, abort_flag, p.ctl, 30)) {
               ok = false;
@@ -665,7 +681,7 @@ bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p, co
           mbar_arrive_remote(lead_iempty + slot * 8);
       }
       if (it.kind == kItemEnd) break;
-      const Geo g = geo(p, it.b);
+      const Geo g = geo(p, it.b, dhw);
       unsigned ctr;
       if (it.kind == kItemF) {
         ctr = 2u + static_cast<unsigned>(g.slot);
@@ -766,8 +782,10 @@ bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p, co
         const bool w = wait_bounded(tfull + h, uses[h] & 1u, abort_flag, p.ctl, 33);
         if (!__all_sync(0xffffffffu, w)) break;
         tc_fence_after();
-        const int mi = it.idx / p.ntd, nj = it.idx - (it.idx / p.ntd) * p.ntd;
         const bool dw = it.kind == kItemDW;
+        const int sub = dw || g.ds == 1 ? 0 : it.idx / (g.tt * p.ntd);  // which of the dh_s tile's items
+        const int tile = it.idx - sub * g.tt * p.ntd;
+        const int mi = tile / p.ntd, nj = tile - mi * p.ntd;
         const CUtensorMap* mc = dw ? &maps.m[kMapDW] : &maps.m[kMapDh];
         const int row = (dw ? g.v0 : g.r0) + mi * BN + static_cast<int>(rank) * kBM + q * 32;
         const int rows_total = dw ? p.V : p.N;
@@ -775,6 +793,7 @@ bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p, co
         const int col0 = nj * BN + hc * HB;
         const int n_valid = p.d_s - col0;
         const uint32_t acc = lane_base + static_cast<uint32_t>(h * BN);
+        const int part0 = dhw == kAllWords ? g.vb : g.vb * ((p.bw + dhw - 1) / dhw);  // of the block's parts of dh_s
         bool stored = false;
         if constexpr (kHead) {
           // One token block: the tile is dW's final value, and goes out rounded to bf16 (64-byte rows and swizzle, as G).
@@ -821,7 +840,7 @@ bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p, co
           __syncwarp();
           if (lane == 0 && row < rows_total) {
             if (kHead && parts && !dw)
-              tma_store_3d(mc, staging, col0 + ch * 32, row, g.vb);
+              tma_store_3d(mc, staging, col0 + ch * 32, row, part0 + sub);
             else if (accumulate)
               tma_reduce_add_2d(mc, staging, col0 + ch * 32, row);
             else

@@ -158,7 +158,7 @@ def test_head_workspace(lib):
     assert q(1 << 20, 2048, 128256) == (1 << 20) * (4 + 2 * 32 * 16)
     assert q(1, 64, 256) == 3 * 256 * 256 * 2 + 256 + 256  # one part of dh
     assert q(1024, 2048, 128256) == 3 * 1024 * 12288 * 2 + 256 + 11 * 1024 * 2048 * 4  # 11 parts of 8 MiB
-    assert q(512, 2048, 128256) == 3 * 512 * 24576 * 2 + 256 + 6 * 512 * 2048 * 4
+    assert q(512, 2048, 128256) == 3 * 512 * 24576 * 2 + 256 + 11 * 512 * 2048 * 4  # two of a block
     assert q(1025, 2048, 128256) == 3 * 1280 * 17408 * 2 + 256
     bf = dict(grad_dtype=torch.bfloat16)  # the fp32 sums: of dh, and of dW where the tokens are more than one block
     assert q(4096, 2048, 128256, **bf) == ring + 256 + 4096 * 2048 * 4
