@@ -304,21 +304,24 @@ def hylo_head_logprobs(h, W, tokens, tau: float, logp, entropy, lse, workspace, 
 
 def hylo_head_logprobs_backward(h, W, tokens, tau: float, token_chunk: int, lse, entropy, g_logp, g_entropy, dh, dW,
                                 workspace, split_g: bool = False, stream=None) -> None:
-    """Gradients dh [N, d], dW [V, d] (overwritten; both float32 or both bfloat16) for the upstream g_logp, g_entropy
-    [N] (either None)."""
+    """Gradients dh [N, d], dW [V, d] (overwritten; both float32 or both bfloat16; either None) for the upstream g_logp,
+    g_entropy [N] (either None)."""
     N, d, V = _head_dims(h, W)
     _need_cuda(h=h, W=W, tokens=tokens, lse=lse, entropy=entropy, g_logp=g_logp, g_entropy=g_entropy, dh=dh, dW=dW,
                workspace=workspace)
     _need("tokens", tokens, torch.int64, (N,))
     for name, t in (("lse", lse), ("entropy", entropy), ("g_logp", g_logp), ("g_entropy", g_entropy)):
         _need(name, t, torch.float32, (N,))
-    if dh.dtype not in (torch.float32, torch.bfloat16):
+    if dh is None and dW is None:
+        raise ValueError("dh or dW must be given")
+    dtype = (dW if dh is None else dh).dtype
+    if dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("dh and dW must be float32 or bfloat16")
-    _need("dh", dh, dh.dtype, (N, d))
-    _need("dW", dW, dh.dtype, (V, d))
+    _need("dh", dh, dtype, (N, d))
+    _need("dW", dW, dtype, (V, d))
     _check(load().hylo_head_logprobs_backward(h.data_ptr(), W.data_ptr(), N, d, V, float(tau), int(token_chunk),
                                               tokens.data_ptr(), _ptr(lse), _ptr(entropy), _ptr(g_logp),
-                                              _ptr(g_entropy), int(split_g), DTYPES[dh.dtype], _ptr(dh), _ptr(dW),
+                                              _ptr(g_entropy), int(split_g), DTYPES[dtype], _ptr(dh), _ptr(dW),
                                               workspace.data_ptr(),
                                               workspace.numel() * workspace.element_size(), _stream(stream)))
 

@@ -241,7 +241,7 @@ hylo_status hylo_head_logprobs_backward(const uint16_t* h, const uint16_t* W, in
                                         int grad_dtype, void* dh, void* dW, void* workspace, size_t workspace_bytes,
                                         cudaStream_t stream) {
   clear_error();
-  if (!lse || !dh || !dW || (g_entropy && !entropy)) return fail(HYLO_ERR_NULL, "a required pointer is NULL");
+  if (!lse || (!dh && !dW) || (g_entropy && !entropy)) return fail(HYLO_ERR_NULL, "a required pointer is NULL");
   if (grad_dtype != HYLO_F32 && grad_dtype != HYLO_BF16) return fail(HYLO_ERR_DIM, "gradients are fp32 or bf16 (dtype %d)", grad_dtype);
   const bool split = split_g != 0;
   const HeadBwd l = head_sizes_ok(N, d, V) ? head_bwd_layout(N, d, V, token_chunk, split, grad_dtype) : HeadBwd{};
@@ -256,6 +256,9 @@ hylo_status hylo_head_logprobs_backward(const uint16_t* h, const uint16_t* W, in
   const bool bf16 = grad_dtype == HYLO_BF16;
   float* dh32 = bf16 || l.parts > 0 ? reinterpret_cast<float*>(ws + l.dh) : static_cast<float*>(dh);
   float* dW32 = l.dW_direct ? static_cast<float*>(dW) : bf16 ? reinterpret_cast<float*>(ws + l.dW) : static_cast<float*>(dW);
+  // A tensor map has to have some address; of a gradient that is not wanted nothing is stored.
+  if (!dh) dh32 = reinterpret_cast<float*>(ws);
+  if (!dW) dW32 = reinterpret_cast<float*>(ws);
   DeviceState* dev = nullptr;
   CUtensorMap maps[kPipeMaps];
   BwdPipeParams p{};
@@ -265,20 +268,20 @@ hylo_status hylo_head_logprobs_backward(const uint16_t* h, const uint16_t* W, in
     return st;
   maps[1] = maps[0];  // no teacher: never loaded from
   maps[3] = maps[2];
-  if (l.dW_direct && (st = make_map_3d(&maps[7], dW, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d, V, 1, d * 2, 32, 32,
+  if (dW && l.dW_direct && (st = make_map_3d(&maps[7], dW, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d, V, 1, d * 2, 32, 32,
                                        CU_TENSOR_MAP_SWIZZLE_64B)) != HYLO_OK)
     return st;
-  if (l.parts > 0 && (st = make_map_3d(&maps[6], dh32, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, d, N, l.parts, d * 4, 32, 32)) != HYLO_OK)
+  if (dh && l.parts > 0 && (st = make_map_3d(&maps[6], dh32, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, d, N, l.parts, d * 4, 32, 32)) != HYLO_OK)
     return st;
   cudaError_t e = cudaMemsetAsync(p.ctrl, 0, (kPipeCtrlWords + kGRing) * sizeof(unsigned), stream);
   if (e != cudaSuccess) return cuda_fail(e, "clear the backward's work counters");
-  const int order = l.parts > 0 ? kOrderParts : p.TB == 1 || p.VB >= kGRing ? kOrderDh : kOrderChain;
-  const HeadGrad g{tokens, lse, entropy, g_logp, g_entropy, 1.0f / tau, l.dW_direct ? 1 : 0, order,
+  const int order = l.parts > 0 ? kOrderParts : p.TB == 1 || (dh && p.VB >= kGRing) ? kOrderDh : kOrderChain;
+  const HeadGrad g{tokens, lse, entropy, g_logp, g_entropy, 1.0f / tau, l.dW_direct ? 1 : 0, order, dh ? 1 : 0, dW ? 1 : 0,
                    l.parts > 0 ? static_cast<int>(l.dh_words) : INT_MAX};
   e = launch_bwd_pipe_head(maps, p, g, clusters, stream);
-  if (e == cudaSuccess && (bf16 || l.parts > 0))
+  if (e == cudaSuccess && dh && (bf16 || l.parts > 0))
     e = launch_join_parts(dh32, l.parts > 0 ? static_cast<int>(l.parts) : 1, dh, bf16, N * d, dev->sms, stream);
-  if (e == cudaSuccess && bf16 && !l.dW_direct) e = launch_join_parts(dW32, 1, dW, true, V * d, dev->sms, stream);
+  if (e == cudaSuccess && dW && bf16 && !l.dW_direct) e = launch_join_parts(dW32, 1, dW, true, V * d, dev->sms, stream);
   return e == cudaSuccess ? HYLO_OK : cuda_fail(e, "launch head log-probabilities backward");
 }
 

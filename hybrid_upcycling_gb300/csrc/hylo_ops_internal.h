@@ -87,13 +87,16 @@ struct HeadGrad {
   float inv_tau;
   int dw_bf16;             // one token block: map kMapDW is a bf16 tensor of 32 x 32 tiles with 64-byte swizzle
   int order;               // see below
+  int want_dh, want_dw;    // which gradients there are
   int dh_words;            // kOrderParts: words of a block whose products go into one part (a multiple of 64); else INT_MAX
 };
 // How the items of one block wait for those of others (M(b): products of block b, F(b): its G).
 //   kOrderChain: M(b) needs all of M(b - 1), as the distillation loss.
 //   kOrderDh: only the dh items of block b - 1 (which come first), as dh is what one block after another adds to; dW's
-//     items of one block then do not hold up the next. With several token blocks also dW is added to: the items of the same
-//     words, VB blocks before, are complete if VB >= 3, as then they belong to a block whose ring slot was taken again.
+//     items of one block then do not hold up the next. With several token blocks dW is added to as well. Its items of the same
+//     words, VB blocks before, are complete if VB >= 3 and there are dh items: those of block b wait for those of b - 1, so
+//     for F(b - 1), F(b - 2), ..., which had to wait for all of M(b - 4), M(b - 5), ... to take their ring slots; and F(b)
+//     for M(b - 3).
 //   kOrderParts: nothing of M(b - 1). Map kMapDh is [vocabulary blocks][N][d]: every block's part of dh apart (one token
 //     block).
 enum : int { kOrderChain = 0, kOrderDh = 1, kOrderParts = 2 };

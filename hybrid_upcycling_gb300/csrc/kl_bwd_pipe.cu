@@ -140,12 +140,22 @@ __device__ __forceinline__ int items_f(const BwdPipeParams& p, int b) {
   return g.tt * g.vt;
 }
 
-__device__ __forceinline__ int items_m(const BwdPipeParams& p, int b, int dhw) {
-  const Geo g = geo(p, b, dhw);
-  return (g.vt + g.tt * g.ds) * p.ntd;
+// Which M items there are, and how blocks wait for one another (HeadGrad).
+struct Plan {
+  int order;
+  int dhw;
+  bool dh, dw;
+};
+
+__device__ __forceinline__ int items_dw(const BwdPipeParams& p, const Geo& g, const Plan& plan) { return plan.dw ? g.vt * p.ntd : 0; }
+__device__ __forceinline__ int items_dh(const BwdPipeParams& p, const Geo& g, const Plan& plan) {
+  return plan.dh ? g.tt * g.ds * p.ntd : 0;
 }
 
-__device__ __forceinline__ int items_dh(const BwdPipeParams& p, int b) { return geo(p, b).tt * p.ntd; }  // (ds = 1)
+__device__ __forceinline__ int items_m(const BwdPipeParams& p, int b, const Plan& plan) {
+  const Geo g = geo(p, b, plan.dhw);
+  return items_dw(p, g, plan) + items_dh(p, g, plan);
+}
 
 // Walks the queue order part by part: segment j holds M(j-2) (part 0) if 0 <= j-2 < B and F(j)
 // (part 1) if j < B. It keeps, per counter, the completion total of the parts already passed
@@ -168,11 +178,11 @@ __device__ __forceinline__ void cursor_init(Cursor& c, const BwdPipeParams& p) {
   c.end = false;
 }
 
-__device__ __forceinline__ void cursor_next(Cursor& c, const BwdPipeParams& p, int order, int dhw) {
+__device__ __forceinline__ void cursor_next(Cursor& c, const BwdPipeParams& p, const Plan& plan) {
   const int b = c.part == 0 ? c.j - 2 : c.j;
   if (c.part == 0) {
-    const int ndh = order == kOrderDh ? items_dh(p, b) : 0;
-    c.cum_m += 2u * static_cast<unsigned>(order == kOrderDh ? ndh : c.size);
+    const int ndh = plan.order == kOrderDh ? items_dh(p, geo(p, b, plan.dhw), plan) : 0;
+    c.cum_m += 2u * static_cast<unsigned>(plan.order == kOrderDh ? ndh : c.size);
     c.cum_ms[b % kGRing] += 2u * static_cast<unsigned>(c.size - ndh);
   } else {
     c.cum_f[b % kGRing] += 2u * static_cast<unsigned>(c.size);
@@ -199,15 +209,16 @@ __device__ __forceinline__ void cursor_next(Cursor& c, const BwdPipeParams& p, i
     }
   }
   const int nb = c.part == 0 ? c.j - 2 : c.j;
-  c.size = c.part == 0 ? items_m(p, nb, dhw) : items_f(p, nb);
+  c.size = c.part == 0 ? items_m(p, nb, plan) : items_f(p, nb);
 }
 
 // Counter of the M items of ring slot s, where M items are counted per slot (kOrderParts; kOrderDh: the dW_s items).
 constexpr unsigned kSlotM = 2 + kGRing;
 
 // The item with queue index i (the cursor only moves forward; i never decreases per caller).
-__device__ __forceinline__ Item cursor_item(Cursor& c, const BwdPipeParams& p, int i, int order, int dhw) {
-  while (!c.end && i >= c.base + c.size) cursor_next(c, p, order, dhw);
+__device__ __forceinline__ Item cursor_item(Cursor& c, const BwdPipeParams& p, int i, const Plan& plan) {
+  const int order = plan.order;
+  while (!c.end && i >= c.base + c.size) cursor_next(c, p, plan);
   Item it{};
   if (c.end) {
     it.kind = kItemEnd;
@@ -225,11 +236,12 @@ __device__ __forceinline__ Item cursor_item(Cursor& c, const BwdPipeParams& p, i
     }
     if (order != kOrderParts && b >= kGRing) {  // every M (dh_s) item of blocks <= b - 3 (the parts passed, minus block b - 2's)
       it.ctr1 = 1;
-      it.tgt1 = c.cum_m - 2u * static_cast<unsigned>(order == kOrderDh ? items_dh(p, b - 2) : items_m(p, b - 2, dhw));
+      it.tgt1 = c.cum_m - 2u * static_cast<unsigned>(order == kOrderDh ? items_dh(p, geo(p, b - 2, plan.dhw), plan)
+                                                                        : items_m(p, b - 2, plan));
     }
   } else {
-    const Geo g = geo(p, b, dhw);
-    const int ndw = g.vt * p.ntd, ndh = g.tt * g.ds * p.ntd;
+    const Geo g = geo(p, b, plan.dhw);
+    const int ndw = items_dw(p, g, plan), ndh = items_dh(p, g, plan);
     if (order != kOrderChain) {  // dh_s first: they are waited for
       it.kind = local < ndh ? kItemDH : kItemDW;
       it.idx = local < ndh ? local : local - ndh;
@@ -344,11 +356,10 @@ template <bool SPLIT, typename Head>
 __global__ void __launch_bounds__(kThreads, 1)
 bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p, const Head head) {
   constexpr bool kHead = !std::is_same<Head, NoHead>::value;
-  int order = kOrderChain;
-  if constexpr (kHead) order = head.order;
-  const bool parts = order == kOrderParts;
-  int dhw = kAllWords;
-  if constexpr (kHead) dhw = head.dh_words;
+  Plan plan{kOrderChain, kAllWords, true, true};
+  if constexpr (kHead) plan = Plan{head.order, head.dh_words, head.want_dh != 0, head.want_dw != 0};
+  const int dhw = plan.dhw;
+  const bool parts = plan.order == kOrderParts;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* staging_all = smem + STAGES * STAGE_BYTES;
@@ -415,7 +426,7 @@ bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p, co
         const int slot = k % kItemDepth;
         const uint32_t par = static_cast<uint32_t>(k / kItemDepth) & 1u;
         if (!wait_bounded<true>(iempty + slot, par ^ 1u, abort_flag, p.ctl, 21)) break;
-        const Item it = cursor_item(cur, p, next_i, order, dhw);
+        const Item it = cursor_item(cur, p, next_i, plan);
         if (it.kind != kItemEnd) {
           next_i = static_cast<int>(atomicAdd(p.ctrl, 1u));  // the next item, fetched ahead
           // the item is published only once what it reads is complete
@@ -776,7 +787,7 @@ bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p, co
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(lead_tempty + sh * 8);
       } else {
-        ctr = parts || (order == kOrderDh && it.kind == kItemDW) ? kSlotM + static_cast<unsigned>(g.slot) : 1u;
+        ctr = parts || (plan.order == kOrderDh && it.kind == kItemDW) ? kSlotM + static_cast<unsigned>(g.slot) : 1u;
         const int h = hp;
         hp ^= 1;
         const bool w = wait_bounded(tfull + h, uses[h] & 1u, abort_flag, p.ctl, 33);

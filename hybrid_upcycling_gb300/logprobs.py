@@ -186,19 +186,20 @@ class _HeadLogprobs(torch.autograd.Function):
         h, W, tokens, lse, entropy = ctx.saved_tensors
         tau, token_chunk, split_g = ctx.args
         (N, d), V = h.shape, W.shape[0]
+        want_h, want_W = ctx.needs_input_grad[:2]
         if N == 0:
-            return torch.zeros_like(h), torch.zeros_like(W), None, None, None, None, None
-        dh, dW = torch.empty_like(h), torch.empty_like(W)
+            return (torch.zeros_like(h) if want_h else None, torch.zeros_like(W) if want_W else None, None, None, None, None,
+                    None)
+        dh, dW = torch.empty_like(h) if want_h else None, torch.empty_like(W) if want_W else None
         g_logp, g_entropy = _upstream(g_logp), _upstream(g_entropy)
         ws, n = _workspace(N, d, V, token_chunk, split_g, h.device)
         _check(load().hylo_head_logprobs_backward(
             h.data_ptr(), W.data_ptr(), N, d, V, tau, token_chunk, tokens.data_ptr(), lse.data_ptr(), entropy.data_ptr(),
-            _ptr(g_logp), _ptr(g_entropy), int(split_g), _BF16, dh.data_ptr(), dW.data_ptr(), ws.data_ptr(), n,
+            _ptr(g_logp), _ptr(g_entropy), int(split_g), _BF16, _ptr(dh), _ptr(dW), ws.data_ptr(), n,
             current_raw_stream(h.get_device())))
         if torch.is_grad_enabled():  # create_graph
-            dh, dW = (_Once.apply(g, h, W, g_logp, g_entropy) for g in (dh, dW))
-        return (dh if ctx.needs_input_grad[0] else None, dW if ctx.needs_input_grad[1] else None, None, None, None, None,
-                None)
+            dh, dW = (None if g is None else _Once.apply(g, h, W, g_logp, g_entropy) for g in (dh, dW))
+        return dh, dW, None, None, None, None, None
 
 
 def head_logprobs(h: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, tau: float = 1.0, token_chunk: int = 4096,
@@ -207,7 +208,7 @@ def head_logprobs(h: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, tau: f
     states h [..., d] and an LM head W [V, d] in bfloat16 (d a multiple of 8); the logits are never stored.
 
     A negative token is ignored (log-probability 0, no gradient). Both results are differentiable once
-    with respect to h and W (bfloat16 gradients; the C ABI gives fp32). token_chunk and split_g as in
+    with respect to h and W (bfloat16 gradients; the C ABI gives fp32), and only the gradients that are needed are computed. token_chunk and split_g as in
     fused_hidden_state_kl: the backward's token block, and whether the gradient of the logits is
     kept to 16 bits of precision instead of 8 inside the gradient products (None: for up to 64 tokens, where that
     rounding does not average out: relative error 3e-3 of the gradients against 1.7e-3 with both terms)."""

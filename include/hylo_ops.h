@@ -69,8 +69,8 @@ hylo_status hylo_head_logprobs(const uint16_t* h, const uint16_t* W, int64_t N, 
 /* Gradients of sum_n g_logp[n] logp[n] + g_entropy[n] entropy[n]: with G = dL/dz as in
  * hylo_token_logprobs_backward (recomputed tile by tile, rounded to bf16 once, or with split_g != 0
  * kept as two bf16 terms), dh = G W [N, d] and dW = G^T h [V, d], summed in fp32 and OVERWRITTEN as
- * grad_dtype (HYLO_F32 or HYLO_BF16, rounded once). lse and
- * entropy are the forward's for the same inputs. token_chunk as in hylo_kl_backward. Deterministic. */
+ * grad_dtype (HYLO_F32 or HYLO_BF16, rounded once). Either may be NULL: that product is then left
+ * out (frozen hidden states or LM head). lse and entropy are the forward's for the same inputs. token_chunk as in hylo_kl_backward. Deterministic. */
 hylo_status hylo_head_logprobs_backward(const uint16_t* h, const uint16_t* W, int64_t N, int64_t d, int64_t V,
                                         float tau, int64_t token_chunk, const int64_t* tokens, const float* lse,
                                         const float* entropy, const float* g_logp, const float* g_entropy, int split_g,

@@ -168,6 +168,38 @@ def test_gradients_over_blocks_of_tokens_and_words(N, d, V, chunk):
         assert np.linalg.norm(f64(dW[v:v + 8192]) - ref) <= rel * np.linalg.norm(ref) + 1e-5 * gl.abs().max().item()
 
 
+@pytest.mark.parametrize("N,d,V,chunk,split", [(300, 64, 100_000, 4096, False), (1500, 64, 60_001, 4096, False),
+                                               (1100, 72, 200_001, 256, False), (600, 64, 5000, 256, True), (40, 512, 3000, 4096, None)])
+def test_one_gradient_alone_is_that_of_both(N, d, V, chunk, split):
+    """Frozen hidden states or a frozen LM head: the other gradient, bit for bit; fp32 through the C ABI too."""
+    h, W, tok = inputs(N, d, V, seed=N)
+    gl, ge = torch.randn(N, device="cuda"), torch.randn(N, device="cuda")
+
+    def grads(*need):
+        hh, WW = h.detach().clone(), W.detach().clone()
+        for t, n in zip((hh, WW), need):
+            t.requires_grad_(n)
+        out = head_logprobs(hh, WW, tok, token_chunk=chunk, split_g=split)
+        (out[0] @ gl + out[1] @ ge).backward()
+        return hh.grad, WW.grad
+
+    dh, dW = grads(True, True)
+    only_h, only_W = grads(True, False), grads(False, True)
+    assert torch.equal(dh, only_h[0]) and only_h[1] is None and torch.equal(dW, only_W[1]) and only_W[0] is None
+    f = dict(dtype=torch.float32, device="cuda")
+    lp, H, lse = (torch.empty(N, **f) for _ in range(3))
+    ws = torch.empty(_lib.hylo_head_logprobs_workspace_bytes(N, d, V, chunk, bool(split)), dtype=torch.uint8, device="cuda")
+    _lib.hylo_head_logprobs(h, W, tok, 1.0, lp, H, lse, ws)
+    both = torch.empty(N, d, **f), torch.empty(V, d, **f)
+    _lib.hylo_head_logprobs_backward(h, W, tok, 1.0, chunk, lse, H, gl, ge, *both, ws, bool(split))
+    for k in range(2):
+        one = torch.full_like(both[k], float("nan"))
+        _lib.hylo_head_logprobs_backward(h, W, tok, 1.0, chunk, lse, H, gl, ge, *((one, None) if k == 0 else (None, one)), ws,
+                                         bool(split))
+        _lib.hylo_kl_sync_status()
+        assert torch.equal(one, both[k])
+
+
 def test_gradient_against_differences():
     """Directional differences of the fp64 forward along random directions; bound: G's one rounding to bf16."""
     N, d, V = 6, 16, 40

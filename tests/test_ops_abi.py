@@ -140,7 +140,7 @@ def _head_bwd(lib, **kw):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(W=None), -1), (dict(lse=None), -1), (dict(dh=None), -1), (dict(dW=None), -1), (dict(ent=None), -1),
+    (dict(W=None), -1), (dict(lse=None), -1), (dict(dh=None, dW=None), -1), (dict(ent=None), -1), (dict(dh=None, ws=None), -1),
     (dict(N=-1), -2), (dict(d=12), -2), (dict(N=1 << 30, V=1 << 30), -2), (dict(dh=FAKE + 8), -3), (dict(gl=FAKE + 1), -3),
     (dict(tau=float("nan")), -4), (dict(nbytes=256), -5), (dict(dt=2), -2), (dict(dt=-1), -2), (dict(dt=1, dW=FAKE + 2), -3),
 ])
