@@ -285,36 +285,11 @@ __device__ __forceinline__ uint32_t bound_of(uint32_t key) {
   return (key & kHigh) == (kMinusInfKey & kHigh) ? (kMinusInfKey & kHigh) + (~kHigh + 1u) : key & kHigh;
 }
 
-// The first kk groups by (maximum, position) into sh.sel, and the kk-th largest maximum (in the leading bits of its
-// key) into sh.bound_key. (Loops are kept rolled here and below: this code runs once per row.)
-//
-// Eight warps: a thread per group counts the groups before its own. It is the quickest for the few rows that are
-// split over clusters.
-template <typename T, int kWarps>
-__device__ void rank_groups(Choice<kWarps>& sh, uint32_t* group_key, int groups, int kk, int k, int tid) {
-  constexpr uint32_t kHigh = Elem<T>::kKeyBits == 32 ? ~0u : ~0u << (32 - Elem<T>::kKeyBits);
-  static_assert(kWarps * 32 == kMaxGroups, "a thread per group");
-  // Where the key has low bits that do not matter they hold the position, and all keys differ.
-  constexpr bool kUnique = Elem<T>::kKeyBits <= 24;
-  const uint32_t key = tid < groups ? group_key[tid] : 0u;
-  const uint32_t mine = kUnique && tid < groups ? (key & kHigh) | (kMaxGroups - 1 - tid) : key;
-  group_key[tid] = mine;  // (groups that do not exist: 0, before none)
-  sync_warps<kWarps>();
-  int gt = 0, eq = 0;
-#pragma unroll 2
-  for (int g = 0; g < groups; g += 4) {
-    const uint4 o = *reinterpret_cast<const uint4*>(group_key + g);
-    gt += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
-    if (!kUnique) eq += (o.x == mine) + (o.y == mine) + (o.z == mine) + (o.w == mine);
-  }
-  if (!kUnique && eq > 1 && tid < groups)
-    for (int g = 0; g < tid; ++g) gt += group_key[g] == mine;
-  if (tid < groups && gt < kk) sh.sel[gt] = tid;
-  if (tid < groups && gt == kk - 1) sh.bound_key = kk == k ? bound_of<T>(mine) : 0u;  // fewer groups than k: any word may count
-}
-
-// One warp: a search for the kk-th largest, bit by bit below the bits that the largest and the smallest maximum share,
-// until exactly kk maxima reach t. Fewer instructions than the ranks. sh.sel ascends by position.
+// The first kk groups by (maximum, position) into sh.sel, by position, and the bound into sh.bound_key; one warp. A search for
+// the kk-th largest maximum in the leading bits of its key, bit by bit below the bits that the largest and the smallest
+// maximum share, until exactly kk maxima reach t. (A thread per group that counts the groups before its own, 256
+// comparisons each, took longer: one row of 128256 fp32 words with 20 alternatives 10.2 us against 8.5, 600 rows of
+// 1000 words 14.8 against 7.3.) Loops are kept rolled here and below: this code runs once per row.
 template <typename T, int kWarps>
 __device__ void choose_groups(Choice<kWarps>& sh, const uint32_t* group_key, int groups, int kk, int k) {
   constexpr uint32_t kHigh = Elem<T>::kKeyBits == 32 ? ~0u : ~0u << (32 - Elem<T>::kKeyBits);
@@ -377,7 +352,7 @@ __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_all;" 
 constexpr int kStage = 1024;
 
 template <typename T, int kWarps, bool kStaged = false>
-__device__ void best_words(Choice<kWarps>& sh, uint32_t* group_key, const Row<T>& row, const Groups gr, int k,
+__device__ void best_words(Choice<kWarps>& sh, const uint32_t* group_key, const Row<T>& row, const Groups gr, int k,
                            int tid, uint4* stage = nullptr) {
   constexpr int VE = Elem<T>::kVec;
   constexpr uint32_t kHigh = Elem<T>::kKeyBits == 32 ? ~0u : ~0u << (32 - Elem<T>::kKeyBits);
@@ -387,10 +362,7 @@ __device__ void best_words(Choice<kWarps>& sh, uint32_t* group_key, const Row<T>
   const int lane = tid & 31, warp = tid >> 5;
   const int kk = min(k, gr.count);
   if (tid == 0) sh.count = sh.hits = 0;
-  if constexpr (kWarps > 1)
-    rank_groups<T>(sh, group_key, gr.count, kk, k, tid);
-  else
-    choose_groups<T>(sh, group_key, gr.count, kk, k);
+  if (tid < 32) choose_groups<T>(sh, group_key, gr.count, kk, k);
   sync_warps<kWarps>();
   uint32_t bound = sh.bound_key;
   const int nv = kk << gr.vec_shift;  // vectors of the chosen groups, in their order
@@ -515,15 +487,6 @@ __device__ void best_words(Choice<kWarps>& sh, uint32_t* group_key, const Row<T>
   // Otherwise in order: the words above the bound, and of those equal to it only the first k.
   sync_warps<kWarps>();
   if (tid == 0) sh.count = 0;
-  if constexpr (kWarps > 1) {  // the chosen groups by position
-    int mine = 0, before = 0;
-    if (tid < kk) {
-      mine = sh.sel[tid];
-      for (int j = 0; j < kk; ++j) before += sh.sel[j] < mine;
-    }
-    __syncthreads();
-    if (tid < kk) sh.sel[before] = mine;
-  }
   sync_warps<kWarps>();
   int equal_before = 0;
 #pragma unroll 1
