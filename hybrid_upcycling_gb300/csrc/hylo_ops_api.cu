@@ -43,10 +43,12 @@ int head_segments(int64_t N) {
 // then hold everything up: 8 tokens of d = 4096, V = 128256 took 190 to 280 us by where h lay, and 172 us with
 // copies of 512 KiB in all. A small LM head is read in a few microseconds, in which the copies cost more.
 constexpr int64_t kHotBytes = 128 << 10, kCopyBytes = 512 << 10, kCopyHeadBytes = 64 << 20;
+constexpr int64_t kMaxCopies = 64;  // about one for each cluster
 int head_copies(int64_t N, int64_t d, int64_t V) {
   const int64_t bytes = N * d * 2;
   if (bytes >= kHotBytes || V * d * 2 < kCopyHeadBytes || head_few_fits(N, d)) return 1;
-  return static_cast<int>(cdiv(kCopyBytes, bytes));
+  const int64_t copies = cdiv(kCopyBytes, bytes);
+  return static_cast<int>(copies < kMaxCopies ? copies : kMaxCopies);
 }
 
 // The forward's workspace: the tokens' logits, two partial sums per token and segment, and copies of h.

@@ -62,7 +62,7 @@ def test_forward(N, d, V, tau):
 
 
 @pytest.mark.parametrize("N,d,V", [(3, 2048, 20_001), (8, 4096, 9000), (15, 4096, 8193), (31, 2048, 16_400), (32, 2048, 16_400),
-                                   (5, 65536, 600)])
+                                   (5, 65536, 600), (3, 16, 2_100_003)])
 def test_few_tokens_of_a_large_head(N, d, V):
     """A head of 64 MiB and more with hidden states of less than 128 KiB, or just that; also in a larger batch."""
     h, W, tok = inputs(N, d, V, seed=N)
