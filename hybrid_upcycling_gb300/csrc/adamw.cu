@@ -141,6 +141,11 @@ __device__ __forceinline__ void random8(uint32_t seed, uint64_t c, uint32_t (&bi
   for (int j = 0; j < 8; ++j) bits[j] = mix32(start + j);
 }
 
+// The same of one position.
+__device__ __forceinline__ uint32_t random1(uint32_t seed, uint64_t c) {
+  return mix32(static_cast<uint32_t>(c) + mix32(seed + 0x9E3779B9u * (static_cast<uint32_t>(c >> 32) + 1u)));
+}
+
 // w rounded to bf16, up with the probability of the part cut off (w finite).
 __device__ __forceinline__ float round_bf16(float w, uint32_t bits) {
   return __uint_as_float((__float_as_uint(w) + ((bits * 0x9E3779B1u) >> 16)) & 0xffff0000u);
@@ -214,6 +219,10 @@ __device__ __forceinline__ float rcp_ftz(float x) {
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
+// a + b, where a and b are products that have been rounded: a packed product and a packed sum would be compiled to one
+// operation with one rounding.
+__device__ __forceinline__ float2 add_rn(float2 a, float2 b) { return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y)); }
+
 // Eight elements as they lie in memory.
 template <typename T>
 struct Raw8 {
@@ -273,19 +282,30 @@ __device__ __forceinline__ uint32_t tops4(uint32_t a, uint32_t b, uint32_t c, ui
   return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
 }
 
-// Small thread blocks, many per SM: their loads and arithmetic then fall at different times (200M bf16 elements
-// without masters: 389 us with 256 threads, 357 with 128).
-constexpr int kThreads8 = 128;
-constexpr int kWarps8 = kThreads8 / 32;
-constexpr int kBlocks8 = 9;  // thread blocks per SM
-// Blocks per warp: enough that a thread block's set-up (finding its tensor, the clip factor) is paid rarely, but no more
-// than leave every SM its thread blocks (one block per warp: a quarter slower; 32: 3% slower).
-constexpr int kMaxSteps8 = 16;
+// sqrt.approx.ftz is within a relative 2^-23 of the root, so at most 2.5 units in the last place from the root rounded to nearest.
+constexpr uint32_t kRootUlps = 4;
+constexpr float kMinNormal = 1.17549435e-38f;  // 2^-126
+constexpr float kTiny = 7.52316384526264e-37f;  // 2^-120
 
-// The step with 8-bit moments. Eight elements of a lane in packed fp32 pairs. 200M elements: fp32 parameters and
-// gradients 473 us, bf16 with masters and fp32 gradients 538 us, both at the copy rate of HBM (6.7 TB/s); bf16 with bf16
-// gradients 357 us, 5.6 TB/s: 54 instructions per element, 9 of them for its random bits, at 0.65 per clock
-// and scheduler come near the time of its 10 bytes.
+// Thread blocks of one warp, 32 per SM: their loads and arithmetic fall at different times (200M bf16 elements without
+// masters, before the exponents' stores were left out: 461 us with 128 threads, 397 with 64, 367 with 32).
+constexpr int kThreads8 = 32;
+constexpr int kWarps8 = kThreads8 / 32;
+constexpr int kBlocks8 = 32;  // thread blocks per SM
+// Blocks of 256 elements that a warp takes one after another: many where instructions count (bf16 parameters alone), so that its
+// set-up (finding its tensor, the clip factor) is paid rarely, but no more than leave every SM its thread blocks; one where
+// HBM sets the time. Measured with 16 and with 1 (every exponent stored), 200M elements, gradients in bf16 / fp32: bf16 alone
+// 367 / 392 us and 407 / 419; fp32 463 / 516 and 433 / 462; masters 532 / 590 and 472 / 522.
+constexpr int kMaxSteps8 = 16;  // (at most 32)
+
+// The step with 8-bit moments. Eight elements of a lane in packed fp32 pairs. m, v and r are rounded in the order that the
+// interface states, since their last bit can decide a code; the parameter's update is free to fuse. 200M elements, gradients
+// in bf16 / fp32: fp32 432 / 457 us and masters 474 / 507, 6.5 to 7.1 TB/s, HBM's copy rate; bf16 alone 359 / 375, where
+// instructions and waits for loads set the time (9 instructions of an element are its random bits).
+//
+// The root is approximate at first. Where that could change a code (the value within kRootUlps of its random threshold, or the
+// block's largest that close to a power of two; one block in 500), r's codes of the block are left alone until the warp
+// has done its blocks, and then come from roots rounded to nearest. (Those for every element: 5% longer in bf16.)
 template <typename P, typename G, bool MASTER, int CAP>
 __global__ void __launch_bounds__(kThreads8, kBlocks8) adamw8_kernel(const __grid_constant__ AdamTable<CAP> tab, const AdamWHyper h) {
   using W = typename std::conditional<MASTER, float, P>::type;
@@ -295,7 +315,6 @@ __global__ void __launch_bounds__(kThreads8, kBlocks8) adamw8_kernel(const __gri
   const AdamTensor& t = tab.t[find_entry(tab, blockIdx.x)];
   const int lane = threadIdx.x & 31;
   const bool vec = t.vec != 0;
-  const float gm = gs * h.one_minus_beta1, gv = gs * sqrtf(h.one_minus_beta2), rb2 = sqrtf(h.beta2);
   // Everything of the entry that the loop needs, relative to this thread block's first element and this lane's place.
   const int64_t first = static_cast<int64_t>(blockIdx.x - t.chunk0) * tab.steps * (kWarps8 * kBlock);
   const int count = static_cast<int>(min(t.n - first, static_cast<int64_t>(tab.steps) * (kWarps8 * kBlock)));
@@ -315,28 +334,32 @@ __global__ void __launch_bounds__(kThreads8, kBlocks8) adamw8_kernel(const __gri
     uint2 m, v;
     float sm, sv;  // the blocks' powers of two
   };
+  uint32_t again = 0u;  // bit k: the warp's k-th block (of at most kMaxSteps8)
 #pragma unroll 1
   for (int b0 = (threadIdx.x >> 5) * kBlock; b0 < count; b0 += kWarps8 * kBlock) {
     const int i = b0 + lane * 8;
     const int left = max(0, min(8, count - i));
     Block cur;
+    // The exponents first: 32 blocks share a sector, which other SMs write to. For the same reason they are written only where
+    // they change (masters, 200M elements: loaded last 1003 us, first 472 to 519, so 474 to 507; bf16 alone 367 and 359).
+    const int e0 = me[b0 / kBlock], e1 = ve[b0 / kBlock];
     cur.w.load(wp, i, left, vec);
     cur.g.load(gp, i, left, vec);
     cur.m = load_codes(mp, i, left, vec);
     cur.v = load_codes(vp, i, left, vec);
-    cur.sm = pow2(me[b0 / kBlock]);
-    cur.sv = pow2(ve[b0 / kBlock]);
-    const float2 b1 = both(h.beta1 * cur.sm), b2 = both(rb2 * cur.sv);
+    cur.sm = pow2(e0);
+    cur.sv = pow2(e1);
+    const float2 b1 = both(h.beta1 * cur.sm);  // the product with a power of two is exact
     float2 w[4], m[4], r[4];
     float mtop = 0.f, rtop = 0.f;
     float2 odd = make_float2(0.f, 0.f);  // NaN if a value is not finite
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t two = 16 * (j & 1);
-      const float2 g = cur.g.pair(j);
-      m[j] = __ffma2_rn(decode2((j < 2 ? cur.m.x : cur.m.y) >> two & 0xffffu), b1, __fmul2_rn(g, both(gm)));
-      const float2 ro = __fmul2_rn(decode2((j < 2 ? cur.v.x : cur.v.y) >> two & 0xffffu), b2), g2 = __fmul2_rn(g, both(gv));
-      const float2 v = __ffma2_rn(ro, ro, __fmul2_rn(g2, g2));
+      const float2 g = __fmul2_rn(cur.g.pair(j), both(gs));
+      m[j] = add_rn(__fmul2_rn(decode2((j < 2 ? cur.m.x : cur.m.y) >> two & 0xffffu), b1), __fmul2_rn(g, both(h.one_minus_beta1)));
+      const float2 ro = __fmul2_rn(decode2((j < 2 ? cur.v.x : cur.v.y) >> two & 0xffffu), both(cur.sv));
+      const float2 v = add_rn(__fmul2_rn(__fmul2_rn(ro, ro), both(h.beta2)), __fmul2_rn(__fmul2_rn(g, g), both(h.one_minus_beta2)));
       r[j] = make_float2(sqrt_ftz(v.x), sqrt_ftz(v.y));
       const float2 den = __ffma2_rn(r[j], both(h.rbc2), both(h.eps));
       const float2 u = __fmul2_rn(m[j], make_float2(rcp_ftz(den.x), rcp_ftz(den.y)));
@@ -346,11 +369,13 @@ __global__ void __launch_bounds__(kThreads8, kBlocks8) adamw8_kernel(const __gri
       odd = __ffma2_rn(w[j], make_float2(0.f, 0.f), odd);
     }
     const int em = block_exponent(__reduce_max_sync(~0u, __float_as_uint(mtop)));
-    const int er = block_exponent(__reduce_max_sync(~0u, __float_as_uint(rtop)));
-    const float2 im = both(pow2(-em)), ir = both(pow2(-er)), low = both(7.52316384526264e-37f);  // 2^-120
+    const uint32_t rblock = __reduce_max_sync(~0u, __float_as_uint(rtop));
+    const int er = block_exponent(rblock);
+    const float2 im = both(pow2(-em)), ir = both(pow2(-er)), low = both(kTiny);
     uint32_t bits[8];
     random8(h.seed, pos + static_cast<uint64_t>(i), bits);
     uint2 mc, rc;
+    uint32_t close = ~0u;  // least distance of r above its threshold - kRootUlps; a unit in the last place is 16 << 8
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       uint32_t cm[4], cr[4];
@@ -362,6 +387,7 @@ __global__ void __launch_bounds__(kThreads8, kBlocks8) adamw8_kernel(const __gri
         cm[2 * j + 1] = round_code(ym.y, low_random(bits[2 * p2 + 1]));
         cr[2 * j] = round_code(yr.x, high_random(bits[2 * p2]));
         cr[2 * j + 1] = round_code(yr.y, high_random(bits[2 * p2 + 1]));
+        close = min(close, min((cr[2 * j] + 16 * kRootUlps) << 8, (cr[2 * j + 1] + 16 * kRootUlps) << 8));
       }
       const uint32_t signs = tops4(__float_as_uint(m[2 * k].x), __float_as_uint(m[2 * k].y), __float_as_uint(m[2 * k + 1].x),
                                    __float_as_uint(m[2 * k + 1].y)) & 0x80808080u;
@@ -383,12 +409,6 @@ __global__ void __launch_bounds__(kThreads8, kBlocks8) adamw8_kernel(const __gri
         if (!isfinite(rj)) rw |= 0x7fu << at;        // NaN
         if (!isfinite(mj)) mw |= 0x7fu << at;
       }
-    }
-    store_codes(mp, i, left, vec, mc);
-    store_codes(vp, i, left, vec, rc);
-    if (lane == 0) {
-      me[b0 / kBlock] = static_cast<int8_t>(em);
-      ve[b0 / kBlock] = static_cast<int8_t>(er);
     }
     float wf[8];
 #pragma unroll
@@ -415,6 +435,43 @@ __global__ void __launch_bounds__(kThreads8, kBlocks8) adamw8_kernel(const __gri
     } else {
       store8(pp, i, left, vec, wf);
     }
+    store_codes(mp, i, left, vec, mc);
+    if (lane == 0 && em != e0) me[b0 / kBlock] = static_cast<int8_t>(em);
+    // Where an approximate root may lie on the other side of its threshold, or the block's largest of a power of two, r is
+    // left as it was, for the exact roots below.
+    const bool beside = rblock != 0u && ((rblock + kRootUlps) & 0x7fffffu) < 2 * kRootUlps;
+    if (__any_sync(~0u, beside || close < (32 * kRootUlps) << 8)) {
+      again |= 1u << (b0 / (kWarps8 * kBlock));
+    } else {
+      store_codes(vp, i, left, vec, rc);
+      if (lane == 0 && er != e1) ve[b0 / kBlock] = static_cast<int8_t>(er);
+    }
+  }
+#pragma unroll 1
+  for (; again != 0u; again &= again - 1u) {  // rare: r of those blocks from roots rounded to nearest
+    const int b0 = (threadIdx.x >> 5) * kBlock + (__ffs(static_cast<int>(again)) - 1) * (kWarps8 * kBlock);
+    const int i = b0 + lane * 8;
+    const int left = max(0, min(8, count - i));
+    const float sv = pow2(ve[b0 / kBlock]);
+    auto root = [&](int j) {
+      const float g = __fmul_rn(static_cast<float>(gp[i + j]), gs), ro = __fmul_rn(decode2(vp[i + j]).x, sv);
+      const float v = __fadd_rn(__fmul_rn(__fmul_rn(ro, ro), h.beta2), __fmul_rn(__fmul_rn(g, g), h.one_minus_beta2));
+      return v < kMinNormal ? 0.f : __fsqrt_rn(v);
+    };
+    float top = 0.f;
+#pragma unroll 1
+    for (int j = 0; j < left; ++j) top = fmaxf(top, root(j));
+    const int er = block_exponent(__reduce_max_sync(~0u, __float_as_uint(top)));
+#pragma unroll 1
+    for (int j = 0; j < left; ++j) {
+      const float x = root(j);
+      const uint32_t random = high_random(random1(h.seed, pos + static_cast<uint64_t>(i + j)));
+      uint32_t c = max(round_code(x * pow2(-er) * kTiny, random) >> 24, x > 0.f ? 1u : 0u);
+      if (!isfinite(x)) c = 0x7fu;
+      vp[i + j] = static_cast<uint8_t>(c);
+    }
+    __syncwarp();  // every lane has read the old exponent
+    if (lane == 0) ve[b0 / kBlock] = static_cast<int8_t>(er);
   }
 }
 
@@ -513,7 +570,9 @@ cudaError_t step_list(const hylo_adamw_tensor* tensors, int count, double bias1,
   for (int k = 0; k < count; ++k) total += tensors[k].n;
   const int64_t unit = BITS8 ? kWarps8 * kBlock : kChunk;  // elements of a thread block and step
   const int64_t fill = total / (static_cast<int64_t>(kBlocks8) * sms * unit);
-  tab.steps = BITS8 ? static_cast<int>(fill < 1 ? 1 : fill > kMaxSteps8 ? kMaxSteps8 : fill) : 1;
+  tab.steps = BITS8 && sizeof(P) == 2 && !MASTER ? static_cast<int>(fill < 1 ? 1 : fill > kMaxSteps8 ? kMaxSteps8 : fill) : 1;
+  for (int k = 0; k < count; ++k)  // a tensor's thread blocks have to fit a grid (2^40 elements: 4 steps)
+    while (tensors[k].n / (tab.steps * unit) >= (int64_t(1) << 30)) tab.steps *= 2;
   uint64_t pos = 0;
   int i = 0;
   while (i < count) {

@@ -116,8 +116,18 @@ hylo_status hylo_grad_norm(const void* const* grads, const int64_t* sizes, int c
  * that the block's largest magnitude lies in [128, 256) 2^e (e within [-120, 120]; -120 for a
  * block of zeros) and each magnitude x 2^-e is rounded to a neighbouring e4m3 value, up with
  * the probability of the part cut off, so that small steady changes are not lost (to nearest,
- * 0.999 v would round back to v for ever). A non-zero r is never stored as 0. eps must be > 0 (v below
- * 2^-126 counts as 0). A value that is not finite is stored as NaN.
+ * 0.999 v would round back to v for ever). A non-zero r is never stored as 0. eps must be > 0. A value that is not finite is
+ * stored as NaN.
+ * Order of rounding. The last bit of a moment can decide its code, and the next step takes the whole code's
+ * difference into the parameter, so m, v and r are defined to the last bit. With fl the rounding to fp32 (to nearest) of each
+ * single operation, b1, b2, 1 - b1, 1 - b2 rounded from the double arguments, and c from the norm as given:
+ *     c  = min(1, fl(max_norm / fl(norm[0] |grad_scale| + 1e-6))),  s = fl(grad_scale c),  g' = fl(g s)
+ *     m <- fl(fl(b1 m) + fl((1 - b1) g'))
+ *     v <- fl(fl(b2 (r r)) + fl((1 - b2) fl(g' g'))), taken as 0 below 2^-126,  r <- fl(sqrt(v))
+ *     code of x: y = fl(|x| 2^-e), below 2^-6 rounded to a multiple of 2^-29; q = the multiple of the e4m3 step below
+ *     y / step + (16 random bits) 2^-16, exactly
+ * (fl(norm |grad_scale| + 1e-6) is one rounding.) The parameter's own update has no such order; it is within a few fp32
+ * roundings of the formula.
  * The random bits: element j of tensor i has position c = B_i + j, B_i = the sum of the sizes
  * of the tensors before it, each rounded up to 256; with mix = the 32-bit finaliser of
  * MurmurHash3 (public domain), low/high the halves of c,
