@@ -16,6 +16,7 @@
 #include <cuda_fp16.h>
 
 #include "hylo_ops_internal.h"
+#include "row_split.h"
 #include "sm103_ptx.cuh"
 
 namespace hylo {
@@ -710,8 +711,8 @@ struct Shared {
   Choice<kTop ? kWarps : 1> choice;
 };
 
-// A cluster of S CTAs takes a row at a time, each CTA `span` consecutive blocks of it (a multiple of 4, so that a
-// warp's loads never reach into the next CTA's words); the first CTA joins the results.
+// A cluster of S CTAs takes a row at a time, each CTA `span` consecutive blocks of it (row_split.h); the first CTA joins the
+// results.
 template <typename T, int kWarps, bool kTop>
 __global__ void __launch_bounds__(kWarps * 32, 32 / kWarps)
 token_logprobs_kernel(const TokenRows in, const TokenOut out, int span, int vec_shift) {
@@ -734,9 +735,8 @@ token_logprobs_kernel(const TokenRows in, const TokenOut out, int span, int vec_
       token = in.tokens[n];
       zt = token_logit(in, row, token);
     }
-    const int all_blocks = blocks_of(row);
-    const int blk0 = min(all_blocks, static_cast<int>(q) * span), blk1 = min(all_blocks, blk0 + span);
-    Sums r = stream_row<T, kWarps, kTop>(row, blk0, blk1, vec_shift, in.c, warp, lane, sh.group_key);
+    const RowPart part = row_part(blocks_of(row), span, static_cast<int>(q), vec_shift);
+    Sums r = stream_row<T, kWarps, kTop>(row, part.blk0, part.blk1, vec_shift, in.c, warp, lane, sh.group_key);
     if (kWarps > 1) {
       if (lane == 0) sh.warp_sums[warp] = r;
       __syncthreads();
@@ -752,9 +752,7 @@ token_logprobs_kernel(const TokenRows in, const TokenOut out, int span, int vec_
         st_cluster_u32(to + 8, __float_as_uint(r.a));
       }
       if (kTop && q != 0) {
-        const int per = vec_shift < 5 ? 5 - vec_shift : 0, down = vec_shift > 5 ? vec_shift - 5 : 0;
-        const int g1 = ((blk1 << per) + (1 << down) - 1) >> down;
-        for (int g = ((blk0 << per) >> down) + tid; g < g1; g += kWarps * 32)
+        for (int g = part.g0 + tid; g < part.g1; g += kWarps * 32)
           st_cluster_u32(mapa_shared(smem_u32(&sh.group_key[g]), 0), sh.group_key[g]);
       }
       cluster_sync_all();
@@ -938,8 +936,7 @@ cudaLaunchConfig_t split_config(cudaLaunchAttribute* attr, int S, int warps, int
 template <typename T, int kWarps, bool kTop>
 cudaError_t launch_split(const TokenRows& in, const TokenOut& out, int S, int64_t at_once, int64_t blocks, int vec_shift,
                          cudaStream_t stream) {
-  const int64_t unit = vec_shift > 7 ? int64_t(1) << (vec_shift - 5) : 4;  // whole groups, whole warp loads
-  const int span = static_cast<int>(((blocks + S - 1) / S + unit - 1) / unit * unit);
+  const int span = row_span(blocks, S, vec_shift);
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = split_config(attr, S, kWarps, in.N < at_once ? in.N : at_once, stream);
   return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, kWarps, kTop>, in, out, span, vec_shift);
