@@ -26,6 +26,7 @@ STATUS = {
     -6: "HYLO_ERR_CUDA",
     -7: "HYLO_ERR_TIMEOUT",
     -8: "HYLO_ERR_ARCH",
+    -9: "HYLO_ERR_CAPTURE",
 }
 
 EXPORTS = ("hylo_kl_workspace_bytes", "hylo_kl_forward", "hylo_kl_backward", "hylo_kl_sync_status",

@@ -354,6 +354,12 @@ hylo_status hylo_adamw_step(const hylo_adamw_tensor* tensors, int count, int par
   const hylo_status st = current_device(&dev);
   if (st != HYLO_OK) return st;
   if (some < 0) return HYLO_OK;
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  const cudaError_t asked = cudaStreamIsCapturing(stream, &capture);
+  if (asked != cudaSuccess) return cuda_fail(asked, "ask whether the stream is being captured");
+  if (capture != cudaStreamCaptureStatusNone)
+    return fail(HYLO_ERR_CAPTURE, "an AdamW step may not be captured: its step number, learning rates and seed are host values that "
+                                  "every replay would repeat");
   AdamWHyper h;
   h.beta1 = static_cast<float>(beta1);
   h.beta2 = static_cast<float>(beta2);

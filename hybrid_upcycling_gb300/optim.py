@@ -96,7 +96,8 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
     float32 or all bfloat16. exp_avgs and exp_avg_sqs: float32 tensors, or State8 throughout (rounded
     stochastically too). lr and weight_decay: numbers, or one per tensor. grad_scale multiplies the
     gradients. norm (see grad_norm; of the gradients before grad_scale) clips them to max_norm; a norm
-    that is not finite skips the step."""
+    that is not finite skips the step. A step cannot be captured into a CUDA graph: step, lr and seed are host values, which
+    every replay would repeat (grad_norm can)."""
     params, grads = list(params), list(grads)
     n = len(params)
     if not (len(grads) == len(exp_avgs) == len(exp_avg_sqs) == n and (masters is None or len(masters) == n)):

@@ -69,7 +69,8 @@ typedef enum {
   HYLO_ERR_WORKSPACE = -5, /* workspace_bytes is smaller than hylo_kl_workspace_bytes() */
   HYLO_ERR_CUDA = -6,      /* a CUDA runtime or driver call failed (see hylo_kl_last_error) */
   HYLO_ERR_TIMEOUT = -7,   /* a device-side pipeline wait exceeded its limit (device status) */
-  HYLO_ERR_ARCH = -8       /* the current device is not sm_103 */
+  HYLO_ERR_ARCH = -8,      /* the current device is not sm_103 */
+  HYLO_ERR_CAPTURE = -9    /* the call may not be captured into a CUDA graph */
 } hylo_status;
 
 /* Bytes of device workspace that hylo_kl_forward and hylo_kl_backward need for these sizes:

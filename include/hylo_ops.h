@@ -6,7 +6,8 @@
  * Conventions are those of hylo_kl.h: device pointers owned by the caller unless a parameter
  * says otherwise, no allocation by the library, calls asynchronous on `stream`, a status code
  * for argument, architecture and launch errors (hylo_kl_last_error() has the text), no
- * fallback. Calls may be captured into a CUDA graph once one call has run eagerly on the device.
+ * fallback. Calls may be captured into a CUDA graph once one call has run eagerly on the device, all
+ * but hylo_adamw_step.
  */
 #ifndef HYLO_OPS_H
 #define HYLO_OPS_H
@@ -133,7 +134,9 @@ hylo_status hylo_grad_norm(const void* const* grads, const int64_t* sizes, int c
  * MurmurHash3 (public domain), low/high the halves of c,
  *     bits = mix(low(c) + mix(seed + 0x9E3779B9 (high(c) + 1)))   (all modulo 2^32)
  * m takes the low 16 bits, r the high 16, and a bf16 param without master the high 16 of
- * bits * 0x9E3779B1. Pass another seed each step. The same seed and inputs give the same result. */
+ * bits * 0x9E3779B1. Pass another seed each step. The same seed and inputs give the same result.
+ * A step may not be captured into a CUDA graph (HYLO_ERR_CAPTURE): step, the learning rates and seed are the host's, and
+ * every replay would repeat one step's bias corrections and one step's random bits. */
 hylo_status hylo_adamw_step(const hylo_adamw_tensor* tensors, int count, int param_dtype, int grad_dtype,
                             int state_bits, double beta1, double beta2, double eps, int64_t step,
                             float grad_scale, const float* norm, float max_norm, uint32_t seed,
