@@ -13,6 +13,7 @@ from __future__ import annotations
 from typing import NamedTuple, Optional, Tuple
 
 import torch
+from torch.autograd.forward_ad import unpack_dual
 
 from . import _lib
 from ._lib import _check, current_raw_stream, load
@@ -37,6 +38,12 @@ def _on_device(*tensors: torch.Tensor) -> int:
         if t.get_device() != dev:
             raise ValueError(f"every tensor must be on the current CUDA device ({dev})")
     return dev
+
+
+def _no_tangents(*tensors: torch.Tensor) -> None:
+    for t in tensors:
+        if unpack_dual(t).tangent is not None:
+            raise NotImplementedError("token_logprobs and head_logprobs have no forward-mode derivatives")
 
 
 def _row_stride(z: torch.Tensor) -> int:
@@ -130,7 +137,7 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, tau: float = 1.0,
 
     logits may have any strides; rows with unit column stride are read in place. A negative token is
     ignored (log-probability 0, no gradient); -inf logits are masked words. logprobs and entropy
-    are differentiable once with respect to logits (gradient in the logits' dtype)."""
+    are differentiable once, in reverse mode, with respect to logits (gradient in the logits' dtype)."""
     shape = logits.shape
     if logits.dtype not in _lib.DTYPES or not shape or shape[-1] < 1:
         raise ValueError("logits must be float32, bfloat16 or float16 with a last dimension of at least one word")
@@ -138,6 +145,7 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, tau: float = 1.0,
         raise ValueError("tokens must be int64 with the shape of logits without its last dimension")
     if not 0 <= top_k <= min(_lib.TOP_MAX, shape[-1]):
         raise ValueError(f"top_k must be in [0, min(V, {_lib.TOP_MAX})]")
+    _no_tangents(logits)
     dev = _on_device(logits, tokens)
     plain = len(shape) == 2
     z, t = _rows(logits), (tokens if plain else tokens.reshape(-1)).contiguous()
@@ -207,16 +215,18 @@ def head_logprobs(h: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, tau: f
     """Log-probabilities of ``tokens`` [...] (int64) under softmax(h W^T / tau) and the entropies, for final hidden
     states h [..., d] and an LM head W [V, d] in bfloat16 (d a multiple of 8); the logits are never stored.
 
-    A negative token is ignored (log-probability 0, no gradient). Both results are differentiable once
-    with respect to h and W (bfloat16 gradients; the C ABI gives fp32), and only the gradients that are needed are computed. token_chunk and split_g as in
-    fused_hidden_state_kl: the backward's token block, and whether the gradient of the logits is
-    kept to 16 bits of precision instead of 8 inside the gradient products (None: for up to 64 tokens, where that
-    rounding does not average out: relative error 3e-3 of the gradients against 1.7e-3 with both terms)."""
+    A negative token is ignored (log-probability 0, no gradient). Both results are differentiable once, in
+    reverse mode, with respect to h and W (bfloat16 gradients; the C ABI gives fp32), and only the gradients
+    that are needed are computed. token_chunk and split_g as in fused_hidden_state_kl: the backward's token
+    block, and whether the gradient of the logits is kept to 16 bits of precision instead of 8 inside the gradient
+    products (None: for up to 64 tokens, where that rounding does not average out: relative error 3e-3 of the
+    gradients against 1.7e-3 with both terms)."""
     shape = h.shape
     if h.dtype != torch.bfloat16 or W.dtype != torch.bfloat16 or not shape or W.dim() != 2 or shape[-1] != W.shape[1]:
         raise ValueError("h [..., d] and W [V, d] must be bfloat16 with the same hidden size")
     if tokens.dtype != torch.int64 or tokens.shape != shape[:-1]:
         raise ValueError("tokens must be int64 with the shape of h without its last dimension")
+    _no_tangents(h, W)
     dev = _on_device(h, W, tokens)
     plain = len(shape) == 2
     hh, t = (h, tokens) if plain else (h.reshape(-1, shape[-1]), tokens.reshape(-1))
