@@ -33,7 +33,8 @@ EXPORTS = ("hylo_kl_workspace_bytes", "hylo_kl_forward", "hylo_kl_backward", "hy
            "hylo_kl_workspace_bytes_split", "hylo_kl_backward_split",
            "hylo_kl_last_error", "hylo_kl_forward_noalloc", "hylo_kl_selftest_wait_timeout",
            "hylo_fused_kl_logits", "hylo_ild_loss", "hylo_token_logprobs", "hylo_token_logprobs_backward",
-           "hylo_head_logprobs_workspace_bytes", "hylo_head_logprobs", "hylo_head_logprobs_backward",
+           "hylo_head_logprobs_workspace_bytes", "hylo_head_logprobs_forward_workspace_bytes",
+           "hylo_head_logprobs_backward_workspace_bytes", "hylo_head_logprobs", "hylo_head_logprobs_backward",
            "hylo_grad_norm_workspace_bytes", "hylo_grad_norm", "hylo_adamw_step")
 
 DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}  # hylo_dtype
@@ -81,6 +82,10 @@ def load() -> ctypes.CDLL:
     L.hylo_token_logprobs_backward.restype = ctypes.c_int
     L.hylo_head_logprobs_workspace_bytes.argtypes = [i64, i64, i64, i64, i32, i32]
     L.hylo_head_logprobs_workspace_bytes.restype = sz
+    L.hylo_head_logprobs_forward_workspace_bytes.argtypes = [i64, i64, i64]
+    L.hylo_head_logprobs_forward_workspace_bytes.restype = sz
+    L.hylo_head_logprobs_backward_workspace_bytes.argtypes = [i64, i64, i64, i64, i32, i32, i32, i32]
+    L.hylo_head_logprobs_backward_workspace_bytes.restype = sz
     L.hylo_head_logprobs.argtypes = [vp, vp, i64, i64, i64, f32, vp, vp, vp, vp, vp, sz, vp]
     L.hylo_head_logprobs.restype = ctypes.c_int
     L.hylo_head_logprobs_backward.argtypes = [vp, vp, i64, i64, i64, f32, i64, vp, vp, vp, vp, vp, i32, i32, vp, vp, vp, sz,
@@ -289,6 +294,17 @@ def _head_dims(h, W):
 def hylo_head_logprobs_workspace_bytes(N: int, d: int, V: int, token_chunk: int = 4096, split_g: bool = False,
                                        grad_dtype=torch.float32) -> int:
     return int(load().hylo_head_logprobs_workspace_bytes(N, d, V, token_chunk, int(split_g), DTYPES[grad_dtype]))
+
+
+def hylo_head_logprobs_forward_workspace_bytes(N: int, d: int, V: int) -> int:
+    return int(load().hylo_head_logprobs_forward_workspace_bytes(N, d, V))
+
+
+def hylo_head_logprobs_backward_workspace_bytes(N: int, d: int, V: int, token_chunk: int = 4096, split_g: bool = False,
+                                                grad_dtype=torch.float32, want_dh: bool = True,
+                                                want_dW: bool = True) -> int:
+    return int(load().hylo_head_logprobs_backward_workspace_bytes(N, d, V, token_chunk, int(split_g), DTYPES[grad_dtype],
+                                                                  int(want_dh), int(want_dW)))
 
 
 def hylo_head_logprobs(h, W, tokens, tau: float, logp, entropy, lse, workspace, stream=None) -> None:

@@ -67,7 +67,8 @@ HeadFwd head_fwd_layout(int64_t N, int64_t d, int64_t V) {
   return l;
 }
 
-// The backward's workspace: the G ring(s), the counters, and the fp32 sums that are joined or rounded at the end.
+// The backward's workspace: the G ring(s), the counters, and the fp32 sums (of the gradients that are wanted) that are joined or
+// rounded at the end.
 struct HeadBwd {
   size_t ctrl, dh, dW, total;
   int64_t width;     // words of a vocabulary block, or 0 (pipe_width)
@@ -95,7 +96,8 @@ int64_t block_parts(int64_t N, int64_t d, int64_t blocks) {
   return want < fit ? want : fit < 1 ? 1 : fit;
 }
 
-HeadBwd head_bwd_layout(int64_t N, int64_t d, int64_t V, int64_t token_chunk, bool split, int grad_dtype) {
+HeadBwd head_bwd_layout(int64_t N, int64_t d, int64_t V, int64_t token_chunk, bool split, int grad_dtype, bool want_dh,
+                        bool want_dW) {
   HeadBwd l{};
   const int64_t R = pipe_rows(N, token_chunk);
   size_t ring = bwd_bytes(N, V, token_chunk);
@@ -113,11 +115,11 @@ HeadBwd head_bwd_layout(int64_t N, int64_t d, int64_t V, int64_t token_chunk, bo
   }
   l.ctrl = round256(ring) * (split ? 2 : 1);
   l.dh = l.dW = l.total = l.ctrl + kPipeCtrlBytes;
-  if (grad_dtype == HYLO_BF16 || l.parts > 0)
+  if (want_dh && (grad_dtype == HYLO_BF16 || l.parts > 0))
     l.dW = l.total = l.dh + round256(static_cast<size_t>(l.parts > 0 ? l.parts : 1) * N * d * sizeof(float));
   if (grad_dtype == HYLO_BF16) {
     l.dW_direct = N <= R;
-    if (!l.dW_direct) l.total = l.dW + round256(static_cast<size_t>(V) * d * sizeof(float));
+    if (want_dW && !l.dW_direct) l.total = l.dW + round256(static_cast<size_t>(V) * d * sizeof(float));
   }
   return l;
 }
@@ -185,8 +187,21 @@ size_t hylo_head_logprobs_workspace_bytes(int64_t N, int64_t d, int64_t V, int64
                                           int grad_dtype) {
   clear_error();
   if (!head_sizes_ok(N, d, V) || (grad_dtype != HYLO_F32 && grad_dtype != HYLO_BF16)) return 0;
-  const size_t f = head_fwd_layout(N, d, V).total, b = head_bwd_layout(N, d, V, token_chunk, split_g != 0, grad_dtype).total;
+  const size_t f = head_fwd_layout(N, d, V).total;
+  const size_t b = head_bwd_layout(N, d, V, token_chunk, split_g != 0, grad_dtype, true, true).total;
   return f > b ? f : b;
+}
+
+size_t hylo_head_logprobs_forward_workspace_bytes(int64_t N, int64_t d, int64_t V) {
+  clear_error();
+  return head_sizes_ok(N, d, V) ? head_fwd_layout(N, d, V).total : 0;
+}
+
+size_t hylo_head_logprobs_backward_workspace_bytes(int64_t N, int64_t d, int64_t V, int64_t token_chunk, int split_g,
+                                                   int grad_dtype, int want_dh, int want_dW) {
+  clear_error();
+  if (!head_sizes_ok(N, d, V) || (grad_dtype != HYLO_F32 && grad_dtype != HYLO_BF16) || (!want_dh && !want_dW)) return 0;
+  return head_bwd_layout(N, d, V, token_chunk, split_g != 0, grad_dtype, want_dh != 0, want_dW != 0).total;
 }
 
 hylo_status hylo_head_logprobs(const uint16_t* h, const uint16_t* W, int64_t N, int64_t d, int64_t V, float tau,
@@ -246,7 +261,8 @@ hylo_status hylo_head_logprobs_backward(const uint16_t* h, const uint16_t* W, in
   if (!lse || (!dh && !dW) || (g_entropy && !entropy)) return fail(HYLO_ERR_NULL, "a required pointer is NULL");
   if (grad_dtype != HYLO_F32 && grad_dtype != HYLO_BF16) return fail(HYLO_ERR_DIM, "gradients are fp32 or bf16 (dtype %d)", grad_dtype);
   const bool split = split_g != 0;
-  const HeadBwd l = head_sizes_ok(N, d, V) ? head_bwd_layout(N, d, V, token_chunk, split, grad_dtype) : HeadBwd{};
+  const HeadBwd l = head_sizes_ok(N, d, V) ? head_bwd_layout(N, d, V, token_chunk, split, grad_dtype, dh != nullptr, dW != nullptr)
+                                            : HeadBwd{};
   hylo_status st = check_head(h, W, N, d, V, tau, tokens, workspace, workspace_bytes, l.total);
   if (st != HYLO_OK) return st;
   if (!aligned(dh, 16) || !aligned(dW, 16)) return fail(HYLO_ERR_ALIGN, "gradient pointers must be 16-byte aligned");

@@ -161,8 +161,7 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, tau: float = 1.0,
     return TokenLogprobs(logp, entropy, top, ids)
 
 
-def _workspace(N, d, V, token_chunk, split_g, device):
-    n = load().hylo_head_logprobs_workspace_bytes(N, d, V, token_chunk, int(split_g), _BF16)
+def _workspace(n, device):
     if n == 0:
         raise ValueError("invalid sizes (the hidden size must be a multiple of 8 in 8..65536)")
     return _empty(n, dtype=torch.uint8, device=device), n  # from the caching allocator of the current stream
@@ -174,7 +173,7 @@ def _head_forward(h, W, tokens, tau, dev, train):
     logp, entropy = _empty(N, dtype=_f32, device=device), _empty(N, dtype=_f32, device=device)
     lse = _empty(N, dtype=_f32, device=device) if train else None
     if N > 0:
-        ws, n = _workspace(N, d, V, 0, False, device)
+        ws, n = _workspace(load().hylo_head_logprobs_forward_workspace_bytes(N, d, V), device)
         _check(load().hylo_head_logprobs(h.data_ptr(), W.data_ptr(), N, d, V, tau, tokens.data_ptr(), logp.data_ptr(),
                                          entropy.data_ptr(), _ptr(lse), ws.data_ptr(), n, current_raw_stream(dev)))
     return logp, entropy, lse
@@ -200,7 +199,8 @@ class _HeadLogprobs(torch.autograd.Function):
                     None)
         dh, dW = torch.empty_like(h) if want_h else None, torch.empty_like(W) if want_W else None
         g_logp, g_entropy = _upstream(g_logp), _upstream(g_entropy)
-        ws, n = _workspace(N, d, V, token_chunk, split_g, h.device)
+        ws, n = _workspace(load().hylo_head_logprobs_backward_workspace_bytes(
+            N, d, V, token_chunk, int(split_g), _BF16, int(want_h), int(want_W)), h.device)
         _check(load().hylo_head_logprobs_backward(
             h.data_ptr(), W.data_ptr(), N, d, V, tau, token_chunk, tokens.data_ptr(), lse.data_ptr(), entropy.data_ptr(),
             _ptr(g_logp), _ptr(g_entropy), int(split_g), _BF16, _ptr(dh), _ptr(dW), ws.data_ptr(), n,

@@ -55,14 +55,20 @@ hylo_status hylo_token_logprobs_backward(const void* z, int dtype, int64_t N, in
  * states, W [V, d] LM head, bf16 bit patterns, row-major and contiguous, 16-byte aligned, d a multiple
  * of 8 in 8..65536. Inputs are meant finite (where they are not, the results of the tokens
  * concerned are NaN or infinite). tokens as above. entropy and lse may be NULL; the backward needs lse
- * (and entropy, if g_entropy is given). workspace: at least hylo_head_logprobs_workspace_bytes(),
- * 256-byte aligned, not shared with a call still running on another stream; the forward uses O(N) of it (and up to 640 KiB for copies of few hidden states),
- * the backward the G ring of hylo_kl_backward (at most 128 MiB, twice that with split_g), the fp32
- * parts that dh is joined from where N <= 1024 (at most 128 MiB) and, for bf16 gradients, the fp32
- * sums behind them: N d, and V d if N is more than one token block.
- * Returns 0 for invalid sizes; token_chunk <= 0 means 4096; grad_dtype as in the backward. */
+ * (and entropy, if g_entropy is given). workspace: 256-byte aligned, not shared with a call still running
+ * on another stream, and at least as long as the query says. ..._forward_workspace_bytes() is what the
+ * forward needs: O(N), and up to 640 KiB for copies of few hidden states. ..._backward_workspace_bytes() is
+ * what the backward needs for the gradients that are wanted (want_dh: dh is not NULL; want_dW the same):
+ * the G ring of hylo_kl_backward (at most 128 MiB, twice that with split_g), the fp32 parts
+ * that dh is joined from where N <= 1024 (at most 128 MiB) and, for bf16 gradients, the fp32 sums
+ * behind them: N d of dh, and V d of dW if N is more than one token block.
+ * hylo_head_logprobs_workspace_bytes() is enough for both directions with both gradients.
+ * Each returns 0 for invalid sizes; token_chunk <= 0 means 4096; grad_dtype as in the backward. */
 size_t hylo_head_logprobs_workspace_bytes(int64_t N, int64_t d, int64_t V, int64_t token_chunk, int split_g,
                                           int grad_dtype);
+size_t hylo_head_logprobs_forward_workspace_bytes(int64_t N, int64_t d, int64_t V);
+size_t hylo_head_logprobs_backward_workspace_bytes(int64_t N, int64_t d, int64_t V, int64_t token_chunk, int split_g,
+                                                   int grad_dtype, int want_dh, int want_dW);
 hylo_status hylo_head_logprobs(const uint16_t* h, const uint16_t* W, int64_t N, int64_t d, int64_t V, float tau,
                                const int64_t* tokens, float* logp, float* entropy, float* lse, void* workspace,
                                size_t workspace_bytes, cudaStream_t stream);
