@@ -202,10 +202,13 @@ __device__ __forceinline__ float2 decode2(uint32_t two) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// The block's exponent: its largest magnitude (bit pattern `top`) lies in [128, 256) 2^e.
+// The block's exponent: its largest finite magnitude (bit pattern `top`) lies in [128, 256) 2^e.
 __device__ __forceinline__ int block_exponent(uint32_t top) {
   return min(120, max(-120, static_cast<int>(top >> 23) - 127 - 7));
 }
+
+constexpr uint32_t kInfBits = 0x7f800000u;
+__device__ __forceinline__ float finite_or_0(float x) { return isfinite(x) ? x : 0.f; }
 
 __device__ __forceinline__ float sqrt_ftz(float x) {
   float r;
@@ -368,9 +371,18 @@ __global__ void __launch_bounds__(kThreads8, kBlocks8) adamw8_kernel(const __gri
       rtop = fmaxf(rtop, fmaxf(r[j].x, r[j].y));
       odd = __ffma2_rn(w[j], make_float2(0.f, 0.f), odd);
     }
-    const int em = block_exponent(__reduce_max_sync(~0u, __float_as_uint(mtop)));
-    const uint32_t rblock = __reduce_max_sync(~0u, __float_as_uint(rtop));
-    const int er = block_exponent(rblock);
+    uint32_t mblock = __reduce_max_sync(~0u, __float_as_uint(mtop)), rblock = __reduce_max_sync(~0u, __float_as_uint(rtop));
+    if (max(mblock, rblock) >= kInfBits) {  // rare: an infinite value has no part in its block's scale (nor has a NaN, by fmaxf)
+      float a = 0.f, b = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        a = fmaxf(a, fmaxf(finite_or_0(fabsf(m[j].x)), finite_or_0(fabsf(m[j].y))));
+        b = fmaxf(b, fmaxf(finite_or_0(r[j].x), finite_or_0(r[j].y)));
+      }
+      mblock = __reduce_max_sync(~0u, __float_as_uint(a));
+      rblock = __reduce_max_sync(~0u, __float_as_uint(b));
+    }
+    const int em = block_exponent(mblock), er = block_exponent(rblock);
     const float2 im = both(pow2(-em)), ir = both(pow2(-er)), low = both(kTiny);
     uint32_t bits[8];
     random8(h.seed, pos + static_cast<uint64_t>(i), bits);
@@ -460,7 +472,7 @@ __global__ void __launch_bounds__(kThreads8, kBlocks8) adamw8_kernel(const __gri
     };
     float top = 0.f;
 #pragma unroll 1
-    for (int j = 0; j < left; ++j) top = fmaxf(top, root(j));
+    for (int j = 0; j < left; ++j) top = fmaxf(top, finite_or_0(root(j)));
     const int er = block_exponent(__reduce_max_sync(~0u, __float_as_uint(top)));
 #pragma unroll 1
     for (int j = 0; j < left; ++j) {

@@ -120,11 +120,11 @@ hylo_status hylo_grad_norm(const void* const* grads, const int64_t* sizes, int c
  *
  * 8-bit states. m, and r = sqrt(v) for the second moment, are kept as e4m3 codes q with one power of two
  * per 256 consecutive elements of the tensor: value = q 2^e. After the update e is chosen so
- * that the block's largest magnitude lies in [128, 256) 2^e (e within [-120, 120]; -120 for a
+ * that the block's largest finite magnitude lies in [128, 256) 2^e (e within [-120, 120]; -120 for a
  * block of zeros) and each magnitude x 2^-e is rounded to a neighbouring e4m3 value, up with
  * the probability of the part cut off, so that small steady changes are not lost (to nearest,
  * 0.999 v would round back to v for ever). A non-zero r is never stored as 0. eps must be > 0. A value that is not finite is
- * stored as NaN.
+ * stored as NaN and leaves the other elements of its block alone.
  * Order of rounding. The last bit of a moment can decide its code, and the next step takes the whole code's
  * difference into the parameter, so m, v and r are defined to the last bit. With fl the rounding to fp32 (to nearest) of each
  * single operation, b1, b2, 1 - b1, 1 - b2 rounded from the double arguments, and c from the norm as given:
