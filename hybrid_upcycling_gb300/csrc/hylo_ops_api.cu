@@ -1,6 +1,9 @@
 // Host side of the C ABI declared in include/hylo_ops.h: argument checks and launches.
+#include <algorithm>
 #include <climits>
 #include <cmath>
+#include <memory>
+#include <new>
 
 #include "hylo_host.h"
 
@@ -137,6 +140,49 @@ hylo_status check_head(const uint16_t* h, const uint16_t* W, int64_t N, int64_t 
     return fail(HYLO_ERR_TAU, "tau must be finite and > 0, and so must 1 / tau");
   if (workspace_bytes < need)
     return fail(HYLO_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu required", workspace_bytes, need);
+  return HYLO_OK;
+}
+
+// An array of an optimizer step, [begin, end).
+struct Span {
+  uintptr_t begin, end;
+  bool written;
+  int tensor;
+};
+
+// Thread blocks update their elements in any order, so no array that the step writes may overlap another one.
+hylo_status check_apart(const hylo_adamw_tensor* tensors, int count, size_t param_bytes, size_t grad_bytes, size_t state_bytes) {
+  const std::unique_ptr<Span[]> spans(new (std::nothrow) Span[7 * static_cast<size_t>(count)]);
+  if (!spans) return fail(HYLO_ERR_CUDA, "no host memory for %d tensors", count);
+  size_t n = 0;
+  for (int i = 0; i < count; ++i) {
+    const hylo_adamw_tensor& t = tensors[i];
+    if (t.n == 0) continue;
+    auto add = [&](const void* p, size_t bytes, bool written) {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+      if (p) spans[n++] = Span{a, a + bytes, written, i};
+    };
+    const size_t k = static_cast<size_t>(t.n);
+    add(t.param, k * param_bytes, true);
+    add(t.grad, k * grad_bytes, false);
+    add(t.master, k * 4, true);
+    add(t.m, k * state_bytes, true);
+    add(t.v, k * state_bytes, true);
+    if (state_bytes == 1) {
+      add(t.m_exp, (k + 255) / 256, true);
+      add(t.v_exp, (k + 255) / 256, true);
+    }
+  }
+  std::sort(spans.get(), spans.get() + n, [](const Span& a, const Span& b) { return a.begin < b.begin; });
+  Span any{}, written{};  // of those so far, the ones that reach furthest
+  for (size_t i = 0; i < n; ++i) {
+    const Span& s = spans[i];
+    const Span& before = s.written ? any : written;
+    if (s.begin < before.end)
+      return fail(HYLO_ERR_DIM, "arrays of tensors %d and %d overlap, and the step writes to them", before.tensor, s.tensor);
+    if (s.end > any.end) any = s;
+    if (s.written && s.end > written.end) written = s;
+  }
   return HYLO_OK;
 }
 
@@ -366,9 +412,10 @@ hylo_status hylo_adamw_step(const hylo_adamw_tensor* tensors, int count, int par
         !aligned(t.master, 4) || !aligned(t.m, s) || !aligned(t.v, s))
       return fail(HYLO_ERR_ALIGN, "tensor %d is not element-aligned", i);
   }
-  DeviceState* dev = nullptr;
-  const hylo_status st = current_device(&dev);
+  hylo_status st = check_apart(tensors, count, dtype_bytes(param_dtype), dtype_bytes(grad_dtype), state_bits == 8 ? 1 : 4);
   if (st != HYLO_OK) return st;
+  DeviceState* dev = nullptr;
+  if ((st = current_device(&dev)) != HYLO_OK) return st;
   if (some < 0) return HYLO_OK;
   cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
   const cudaError_t asked = cudaStreamIsCapturing(stream, &capture);

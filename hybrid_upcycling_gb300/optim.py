@@ -89,7 +89,7 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
                *, step: int, lr, betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8, weight_decay=0.0,
                masters: Optional[Sequence[torch.Tensor]] = None, norm: Optional[torch.Tensor] = None,
                max_norm: float = 1.0, grad_scale: float = 1.0, seed: int = 0) -> None:
-    """One AdamW step, in place, over lists of tensors (step counts from 1).
+    """One AdamW step, in place, over lists of tensors (step counts from 1). Tensors that are written may not overlap.
 
     params: all float32, or all bfloat16, then with fp32 ``masters`` (the step is taken on those) or without
     (the result is rounded stochastically from ``seed``: pass another one each step). grads: all
@@ -165,6 +165,8 @@ class AdamW:
         self.params = [p for g in self.groups for p in g["params"]]
         if not self.params:
             raise ValueError("AdamW needs at least one parameter")
+        if len({id(p) for p in self.params}) != len(self.params):
+            raise ValueError("a parameter is given to AdamW twice")
         if any(p.dtype != self.params[0].dtype for p in self.params):
             raise ValueError("the parameters of one AdamW must share a dtype")
         def fresh(p):

@@ -84,7 +84,9 @@ hylo_status hylo_head_logprobs_backward(const uint16_t* h, const uint16_t* W, in
                                         int grad_dtype, void* dh, void* dW, void* workspace, size_t workspace_bytes,
                                         cudaStream_t stream);
 
-/* One tensor of an optimizer step. All arrays have `n` elements and start element-aligned. */
+/* One tensor of an optimizer step. All arrays have `n` elements and start element-aligned. No array that
+ * the step writes may overlap another array of the step (a tensor given twice, a gradient that is the
+ * parameter): HYLO_ERR_DIM. Tensors may share a gradient, which is only read. */
 typedef struct {
   void* param;        /* fp32, or bf16 (see hylo_adamw_step) */
   const void* grad;   /* fp32 or bf16 */
