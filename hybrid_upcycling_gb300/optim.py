@@ -158,6 +158,10 @@ class AdamW:
             raise ValueError("state_bits must be 8 or 32")
         params = list(params)
         groups = params if params and isinstance(params[0], dict) else [{"params": params}]
+        for g in groups:
+            extra = set(g) - {"params", "lr", "weight_decay"}
+            if extra:
+                raise ValueError(f"a group of AdamW has its own lr and weight_decay only, not {', '.join(sorted(map(str, extra)))}")
         self.groups = [{"lr": lr, "weight_decay": weight_decay, **g, "params": list(g["params"])} for g in groups]
         self.betas, self.eps, self.max_norm, self.seed = tuple(betas), eps, max_norm, seed
         self.steps = 0
