@@ -12,7 +12,11 @@ using namespace hylo;
 namespace {
 
 bool dtype_ok(int d) { return d == HYLO_F32 || d == HYLO_BF16 || d == HYLO_F16; }
+constexpr float kLog2eHost = 1.4426950408889634f;
 uintptr_t dtype_bytes(int d) { return d == HYLO_F32 ? 4 : 2; }
+
+// The kernels work with 1 / tau and, the larger of the two, log2(e) / tau.
+bool tau_ok(float tau) { return std::isfinite(tau) && tau > 0.f && std::isfinite(kLog2eHost / tau); }
 
 hylo_status check_rows(const void* z, int dtype, int64_t N, int64_t V, int64_t ld, float tau, const int64_t* tokens) {
   if (!z || !tokens) return fail(HYLO_ERR_NULL, "a required pointer is NULL");
@@ -22,13 +26,12 @@ hylo_status check_rows(const void* z, int dtype, int64_t N, int64_t V, int64_t l
                 static_cast<long long>(N), static_cast<long long>(V), static_cast<long long>(ld));
   if (!aligned(z, dtype_bytes(dtype))) return fail(HYLO_ERR_ALIGN, "logits must be element-aligned");
   if (!aligned(tokens, 8)) return fail(HYLO_ERR_ALIGN, "tokens must be 8-byte aligned");
-  if (!(std::isfinite(tau) && tau > 0.f) || !std::isfinite(1.0f / tau))
-    return fail(HYLO_ERR_TAU, "tau must be finite and > 0, and so must 1 / tau");
+  if (!tau_ok(tau)) return fail(HYLO_ERR_TAU, "tau must be finite and > 0, and so must log2(e) / tau");
   return HYLO_OK;
 }
 
 TokenRows rows_of(const void* z, int64_t N, int64_t V, int64_t ld, float tau, const int64_t* tokens) {
-  return TokenRows{z, ld, static_cast<int>(N), static_cast<int>(V), 1.0f / tau, 1.4426950408889634f / tau, tokens};
+  return TokenRows{z, ld, static_cast<int>(N), static_cast<int>(V), 1.0f / tau, kLog2eHost / tau, tokens};
 }
 
 bool head_sizes_ok(int64_t N, int64_t d, int64_t V) {
@@ -136,8 +139,7 @@ hylo_status check_head(const uint16_t* h, const uint16_t* W, int64_t N, int64_t 
   if (!aligned(h, 16) || !aligned(W, 16)) return fail(HYLO_ERR_ALIGN, "h and W must be 16-byte aligned");
   if (!aligned(tokens, 8)) return fail(HYLO_ERR_ALIGN, "tokens must be 8-byte aligned");
   if (!aligned(workspace, 256)) return fail(HYLO_ERR_ALIGN, "workspace must be 256-byte aligned");
-  if (!(std::isfinite(tau) && tau > 0.f) || !std::isfinite(1.0f / tau))
-    return fail(HYLO_ERR_TAU, "tau must be finite and > 0, and so must 1 / tau");
+  if (!tau_ok(tau)) return fail(HYLO_ERR_TAU, "tau must be finite and > 0, and so must log2(e) / tau");
   if (workspace_bytes < need)
     return fail(HYLO_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu required", workspace_bytes, need);
   return HYLO_OK;
@@ -265,7 +267,7 @@ hylo_status hylo_head_logprobs(const uint16_t* h, const uint16_t* W, int64_t N, 
   HeadParams p{};
   p.N = static_cast<int>(N);
   p.V = static_cast<int>(V);
-  p.c = 1.4426950408889634f / tau;
+  p.c = kLog2eHost / tau;
   p.inv_tau = 1.0f / tau;
   p.tokens = tokens;
   p.z_token = static_cast<float*>(workspace);

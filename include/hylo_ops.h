@@ -34,7 +34,7 @@ typedef enum { HYLO_F32 = 0, HYLO_BF16 = 1, HYLO_F16 = 2 } hylo_dtype;
  * logp, lse and top_logp -inf, entropy 0, and a zero gradient. A NaN or +inf anywhere in a row makes
  * logp, entropy, lse and top_logp of that row NaN; for the order of alternatives NaN counts as
  * larger than any number. Equal logits (also -0 and +0) go to the lowest index first.
- * 1 <= N, V <= 2^31 - 1; 0 <= k <= min(V, HYLO_TOP_MAX); tau finite and > 0. Statistics are
+ * 1 <= N, V <= 2^31 - 1; 0 <= k <= min(V, HYLO_TOP_MAX); tau and log2(e) / tau finite and > 0. Statistics are
  * fp32. Results are deterministic. Needs no workspace. */
 hylo_status hylo_token_logprobs(const void* z, int dtype, int64_t N, int64_t V, int64_t ld, float tau,
                                 const int64_t* tokens, int k, float* logp, float* entropy, float* lse,
