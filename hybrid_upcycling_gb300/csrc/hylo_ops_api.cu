@@ -1,5 +1,6 @@
 // Host side of the C ABI declared in include/hylo_ops.h: argument checks and launches.
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <memory>
@@ -393,7 +394,8 @@ hylo_status hylo_adamw_step(const hylo_adamw_tensor* tensors, int count, int par
   if (!(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1) || !(eps >= 0) || !std::isfinite(eps) || step < 1)
     return fail(HYLO_ERR_DIM, "beta1=%g beta2=%g eps=%g step=%lld (0 <= beta < 1, eps >= 0, step >= 1)", beta1, beta2,
                 eps, static_cast<long long>(step));
-  if (state_bits == 8 && !(eps > 0)) return fail(HYLO_ERR_DIM, "8-bit states need eps > 0");
+  // The kernel's reciprocal takes a smaller eps for 0: an element without moments would become 0 / 0.
+  if (state_bits == 8 && !(eps >= FLT_MIN)) return fail(HYLO_ERR_DIM, "8-bit states need eps >= 2^-126");
   if (!std::isfinite(grad_scale) || (norm && !(max_norm > 0)))
     return fail(HYLO_ERR_TAU, "grad_scale must be finite and max_norm > 0");
   int some = -1;  // the first tensor that has elements

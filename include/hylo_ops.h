@@ -125,7 +125,7 @@ hylo_status hylo_grad_norm(const void* const* grads, const int64_t* sizes, int c
  * that the block's largest finite magnitude lies in [128, 256) 2^e (e within [-120, 120]; -120 for a
  * block of zeros) and each magnitude x 2^-e is rounded to a neighbouring e4m3 value, up with
  * the probability of the part cut off, so that small steady changes are not lost (to nearest,
- * 0.999 v would round back to v for ever). A non-zero r is never stored as 0. eps must be > 0. A value that is not finite is
+ * 0.999 v would round back to v for ever). A non-zero r is never stored as 0. eps must be >= 2^-126. A value that is not finite is
  * stored as NaN and leaves the other elements of its block alone.
  * Order of rounding. The last bit of a moment can decide its code, and the next step takes the whole code's
  * difference into the parameter, so m, v and r are defined to the last bit. With fl the rounding to fp32 (to nearest) of each
