@@ -303,8 +303,8 @@ constexpr int kMaxSteps8 = 16;  // (at most 32)
 
 // The step with 8-bit moments. Eight elements of a lane in packed fp32 pairs. m, v and r are rounded in the order that the
 // interface states, since their last bit can decide a code; the parameter's update is free to fuse. 200M elements, gradients
-// in bf16 / fp32: fp32 432 / 457 us and masters 474 / 507, 6.5 to 7.1 TB/s, HBM's copy rate; bf16 alone 359 / 375, where
-// instructions and waits for loads set the time (9 instructions of an element are its random bits).
+// in bf16 / fp32: fp32 430 / 461 us and masters 470 / 508, 6.5 to 7.1 TB/s, HBM's copy rate; bf16 alone 363 / 376, where
+// instructions (57 per element, 9 of them its random bits) and waits for loads set the time.
 //
 // The root is approximate at first. Where that could change a code (the value within kRootUlps of its random threshold, or the
 // block's largest that close to a power of two; one block in 500), r's codes of the block are left alone until the warp

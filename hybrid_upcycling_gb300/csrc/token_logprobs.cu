@@ -279,7 +279,7 @@ __device__ __forceinline__ void rank_all(Choice<kWarps>& sh, int have, int k, in
 }
 
 // The bound below which no word is looked at, from the kk-th largest group maximum. Where that is -inf (masked words), it is
-// the next key: less than k words lie above -inf, all of them in the chosen groups, and words of -inf are filled in.
+// the next key: every word above -inf lies in a chosen group, and if fewer than k do, words of -inf are filled in.
 template <typename T>
 __device__ __forceinline__ uint32_t bound_of(uint32_t key) {
   constexpr uint32_t kHigh = Elem<T>::kKeyBits == 32 ? ~0u : ~0u << (32 - Elem<T>::kKeyBits);
@@ -388,7 +388,7 @@ __device__ void best_words(Choice<kWarps>& sh, const uint32_t* group_key, const 
     }
   };
   auto fill_up = [&](int& have) {
-    if (have >= k) return;  // else the bound was raised, and few words reach it
+    if (have >= k) return;  // else the bound was raised, and the missing words are among the first 4 k: those of the value below it
     sync_warps<kWarps>();
     first_words(bound - kNextKey, [&](uint32_t key, int i) { push(cand_of(key, i)); });
     sync_warps<kWarps>();

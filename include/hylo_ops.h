@@ -32,8 +32,8 @@ typedef enum { HYLO_F32 = 0, HYLO_BF16 = 1, HYLO_F16 = 2 } hylo_dtype;
  * stats [N, 2] receives (max_v z_v, log s), which the backward reads.
  * Logits may be -inf (masked words): such a word has probability 0, and a row of only -inf has
  * logp, lse and top_logp -inf, entropy 0, and a zero gradient. A NaN or +inf anywhere in a row makes
- * logp, entropy, lse and top_logp of that row NaN; for the order of alternatives NaN counts as
- * larger than any number. Equal logits (also -0 and +0) go to the lowest index first.
+ * logp, entropy, lse and top_logp of that row NaN (an ignored token's logp is 0 all the same); for the order of
+ * alternatives NaN counts as larger than any number. Equal logits (also -0 and +0) go to the lowest index first.
  * 1 <= N, V <= 2^31 - 1; 0 <= k <= min(V, HYLO_TOP_MAX); tau and log2(e) / tau finite and > 0. Statistics are
  * fp32. Results are deterministic. Needs no workspace. */
 hylo_status hylo_token_logprobs(const void* z, int dtype, int64_t N, int64_t V, int64_t ld, float tau,
@@ -63,6 +63,8 @@ hylo_status hylo_token_logprobs_backward(const void* z, int dtype, int64_t N, in
  * that dh is joined from where N <= 1024 (at most 128 MiB) and, for bf16 gradients, the fp32 sums
  * behind them: N d of dh, and V d of dW if N is more than one token block.
  * hylo_head_logprobs_workspace_bytes() is enough for both directions with both gradients.
+ * Logits are accumulated like those of hylo_kl_forward (see its accuracy), those of one or two tokens by
+ * fp32 multiply-adds.
  * Each returns 0 for invalid sizes; token_chunk <= 0 means 4096; grad_dtype as in the backward. */
 size_t hylo_head_logprobs_workspace_bytes(int64_t N, int64_t d, int64_t V, int64_t token_chunk, int split_g,
                                           int grad_dtype);
@@ -77,7 +79,8 @@ hylo_status hylo_head_logprobs(const uint16_t* h, const uint16_t* W, int64_t N, 
  * hylo_token_logprobs_backward (recomputed tile by tile, rounded to bf16 once, or with split_g != 0
  * kept as two bf16 terms), dh = G W [N, d] and dW = G^T h [V, d], summed in fp32 and OVERWRITTEN as
  * grad_dtype (HYLO_F32 or HYLO_BF16, rounded once). Either may be NULL: that product is then left
- * out (frozen hidden states or LM head). lse and entropy are the forward's for the same inputs. token_chunk as in hylo_kl_backward. Deterministic. */
+ * out (frozen hidden states or LM head). lse and entropy are the forward's for the same inputs.
+ * token_chunk as in hylo_kl_backward. Deterministic. */
 hylo_status hylo_head_logprobs_backward(const uint16_t* h, const uint16_t* W, int64_t N, int64_t d, int64_t V,
                                         float tau, int64_t token_chunk, const int64_t* tokens, const float* lse,
                                         const float* entropy, const float* g_logp, const float* g_entropy, int split_g,
