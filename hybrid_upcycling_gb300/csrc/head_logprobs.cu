@@ -144,16 +144,15 @@ head_logprobs_kernel(const __grid_constant__ CUtensorMap tm_h, const __grid_cons
       uint32_t phase = 0, armed = 0;
       bool ok = true;
       const uint32_t full_lead = mapa_shared(smem_u32(full), 0);
-      // One tile of tokens: all clusters read the same few lines of h at once. Each begins elsewhere in the hidden
-      // dimension (256 tokens, d = 4096: 178 us, so 170), and few tokens have copies (see head_copies).
-      const bool rotate = p.N <= 2 * kBM;
+      // One tile of tokens: all clusters read the same few lines of h at once. Without a backward each begins elsewhere in the
+      // hidden dimension (256 tokens, d = 4096: 178 us, so 170), and few tokens have copies (see head_copies).
       const int copy = cid % p.copies;
       for (int u = cid; ok && u < p.units; u += ncl) {
         int row0, vt0, vt1, seg;
         unit_range(p, u, row0, vt0, vt1, seg);
         for (int vt = vt0; ok && vt < vt1; ++vt) {
           const int brow = vt * BN + static_cast<int>(rank) * HB;
-          int k0 = rotate ? u % p.kb : 0;
+          int k0 = p.rotate ? u % p.kb : 0;
           for (int kb = 0; kb < p.kb; ++kb, k0 = k0 + 1 == p.kb ? 0 : k0 + 1) {
             if (!wait_bounded(empty + stage, phase ^ 1u, abort_flag, p.ctl, 41)) {
               ok = false;

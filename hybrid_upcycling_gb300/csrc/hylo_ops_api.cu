@@ -53,7 +53,7 @@ constexpr int64_t kHotBytes = 128 << 10, kCopyBytes = 512 << 10, kCopyHeadBytes 
 constexpr int64_t kMaxCopies = 64;  // about one for each cluster
 int head_copies(int64_t N, int64_t d, int64_t V) {
   const int64_t bytes = N * d * 2;
-  if (bytes >= kHotBytes || V * d * 2 < kCopyHeadBytes || head_few_fits(N, d)) return 1;
+  if (bytes >= kHotBytes || V * d * 2 < kCopyHeadBytes) return 1;
   const int64_t copies = cdiv(kCopyBytes, bytes);
   return static_cast<int>(copies < kMaxCopies ? copies : kMaxCopies);
 }
@@ -274,7 +274,11 @@ hylo_status hylo_head_logprobs(const uint16_t* h, const uint16_t* W, int64_t N, 
   p.z_token = static_cast<float*>(workspace);
   p.part = reinterpret_cast<float4*>(static_cast<char*>(workspace) + l.part);
   p.ctl = WaitCtl{dev->status, wait_limit_ns()};
-  if (head_few_fits(N, d)) {
+  // With lse a backward may follow. It takes exp(z - lse) of logits that it computes again for probabilities, and 1 - p of a
+  // confident token loses as many digits as those differ from the forward's: both then accumulate alike. (Otherwise: 1 - p =
+  // 1e-3, d = 4096: gradients of one token 8% off by dot products here, of 64 tokens 1% off by rotated starts.)
+  p.rotate = !lse && N <= 2 * kBM;
+  if (!lse && head_few_fits(N, d)) {
     p.slots = dev->sms < 2 * head_segments(N) ? dev->sms : 2 * head_segments(N);
     const cudaError_t e = launch_head_few(h, W, static_cast<int>(d), p, logp, entropy, lse, stream);
     return e == cudaSuccess ? HYLO_OK : cuda_fail(e, "launch head log-probabilities of few tokens");

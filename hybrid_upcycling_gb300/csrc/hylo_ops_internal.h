@@ -56,6 +56,7 @@ struct HeadParams {
   int nseg;         // vocabulary segments per token tile
   int units;        // token_tiles * nseg
   int copies;       // of h, which the clusters share out
+  bool rotate;      // clusters start at different depths of the hidden dimension
   float c;          // log2(e) / tau
   float inv_tau;
   const int64_t* tokens;

@@ -64,7 +64,8 @@ hylo_status hylo_token_logprobs_backward(const void* z, int dtype, int64_t N, in
  * behind them: N d of dh, and V d of dW if N is more than one token block.
  * hylo_head_logprobs_workspace_bytes() is enough for both directions with both gradients.
  * Logits are accumulated like those of hylo_kl_forward (see its accuracy), those of one or two tokens by
- * fp32 multiply-adds.
+ * fp32 multiply-adds. Where lse is asked for, they are accumulated as the backward will accumulate them again, so
+ * that its probabilities exp(z - lse) are those of the forward to a few fp32 roundings of lse.
  * Each returns 0 for invalid sizes; token_chunk <= 0 means 4096; grad_dtype as in the backward. */
 size_t hylo_head_logprobs_workspace_bytes(int64_t N, int64_t d, int64_t V, int64_t token_chunk, int split_g,
                                           int grad_dtype);
