@@ -9,8 +9,10 @@
 // Roles (384 threads per CTA): warp 0 issues the TMA loads, warp 1 of the even CTA owns TMEM and
 // issues the UMMAs for the pair, warps 4..11 are the epilogue: warp w reads TMEM lanes
 // 32 (w % 4) .. + 31, one token row per thread, warps 4..7 columns 0..127 of a 256-column tile,
-// warps 8..11 the other half. TMEM holds two tiles, so that a tile is folded while the next
-// one is computed. Every (token, vocabulary segment, column half) writes its sums to a slot of
+// warps 8..11 the other half. TMEM holds two tiles, so that one is read while the next is
+// computed. A deep hidden dimension is accumulated in parts (kLogitDepth), one TMEM tile after another, which the
+// epilogue adds up in registers before it folds them (hence setmaxnreg: 56 registers per thread for warpgroup 0, 224 for
+// the others). Every (token, vocabulary segment, column half) writes its sums to a slot of
 // its own; nothing is added in an order that could change.
 #include "hylo_ops_internal.h"
 
@@ -23,6 +25,9 @@ constexpr float kLn2F = 0.6931471805599453f;
 constexpr int kEpiWarps = 8;
 constexpr int kEpiWarp0 = 4;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+constexpr int kRegsControl = 56;         // per thread, warpgroup 0 (TMA, UMMA)
+constexpr int kRegsEpilogue = 224;       // per thread, warpgroups 1 and 2
+static_assert(128 * kRegsControl + 256 * kRegsEpilogue <= kThreads * 168, "register split of the launch's 168 per thread");
 constexpr int BN = 256;                 // vocabulary columns of a pair tile
 constexpr int HB = BN / 2;              // W rows staged per CTA; columns per epilogue warp
 constexpr int A_BYTES = kBM * kBK * 2;
@@ -54,6 +59,19 @@ __device__ __forceinline__ void rebase(Sums& r, float mx, float c) {
   r.mx = mx;
 }
 
+// Adds 32 columns of a TMEM tile.
+__device__ __forceinline__ void add32(float (&z)[32], uint32_t taddr) {
+  float v[32];
+  tmem_ld32(taddr, v);
+  tmem_ld_wait();
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const float2 s = __fadd2_rn(make_float2(z[2 * j], z[2 * j + 1]), make_float2(v[2 * j], v[2 * j + 1]));
+    z[2 * j] = s.x;
+    z[2 * j + 1] = s.y;
+  }
+}
+
 // Folds 32 logits; MASKED: only the first `valid` of them exist.
 template <bool MASKED>
 __device__ __forceinline__ void fold32(Sums& r, const float (&z)[32], int valid, float c) {
@@ -62,11 +80,11 @@ __device__ __forceinline__ void fold32(Sums& r, const float (&z)[32], int valid,
   for (int j = 0; j < 32; ++j)
     if (!MASKED || j < valid) mx = fmaxf(mx, z[j]);
   rebase(r, mx, c);
-  const float2 c2 = make_float2(c, c), nm = make_float2(-mx * c, -mx * c);
+  const float2 c2 = make_float2(c, c), nm = make_float2(-mx, -mx);  // the difference first: it is exact where it matters
   float2 s = make_float2(0.f, 0.f), a = s;
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
-    float2 y = __ffma2_rn(make_float2(z[2 * j], z[2 * j + 1]), c2, nm);
+    float2 y = __fmul2_rn(__fadd2_rn(make_float2(z[2 * j], z[2 * j + 1]), nm), c2);
     if (MASKED) {
       if (2 * j >= valid) y.x = -1024.f;  // 2^-1024 is 0
       if (2 * j + 1 >= valid) y.y = -1024.f;
@@ -137,6 +155,7 @@ head_logprobs_kernel(const __grid_constant__ CUtensorMap tm_h, const __grid_cons
   const uint32_t tmem_base = *tmem_slot;
   const int my_rows = static_cast<int>(rank) * kBM;
 
+  if (warp < kEpiWarp0) setmaxnreg_dec<kRegsControl>();  // each warpgroup changes its registers at once
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer (both CTAs)
     if (lane == 0) {
@@ -144,16 +163,13 @@ head_logprobs_kernel(const __grid_constant__ CUtensorMap tm_h, const __grid_cons
       uint32_t phase = 0, armed = 0;
       bool ok = true;
       const uint32_t full_lead = mapa_shared(smem_u32(full), 0);
-      // One tile of tokens: all clusters read the same few lines of h at once. Without a backward each begins elsewhere in the
-      // hidden dimension (256 tokens, d = 4096: 178 us, so 170), and few tokens have copies (see head_copies).
       const int copy = cid % p.copies;
       for (int u = cid; ok && u < p.units; u += ncl) {
         int row0, vt0, vt1, seg;
         unit_range(p, u, row0, vt0, vt1, seg);
         for (int vt = vt0; ok && vt < vt1; ++vt) {
           const int brow = vt * BN + static_cast<int>(rank) * HB;
-          int k0 = p.rotate ? u % p.kb : 0;
-          for (int kb = 0; kb < p.kb; ++kb, k0 = k0 + 1 == p.kb ? 0 : k0 + 1) {
+          for (int kb = 0; kb < p.kb; ++kb) {
             if (!wait_bounded(empty + stage, phase ^ 1u, abort_flag, p.ctl, 41)) {
               ok = false;
               break;
@@ -164,8 +180,8 @@ head_logprobs_kernel(const __grid_constant__ CUtensorMap tm_h, const __grid_cons
               mbar_arrive_expect_tx(full + stage, 2 * STAGE_BYTES);  // both CTAs' bytes
               armed |= 1u << stage;
             }
-            tma_load_3d_pair(sa, &tm_h, fbar, k0 * kBK, row0 + my_rows, copy);
-            tma_load_2d_pair(sa + A_BYTES, &tm_W, fbar, k0 * kBK, brow);
+            tma_load_3d_pair(sa, &tm_h, fbar, kb * kBK, row0 + my_rows, copy);
+            tma_load_2d_pair(sa + A_BYTES, &tm_W, fbar, kb * kBK, brow);
             if (++stage == STAGES) {
               stage = 0;
               phase ^= 1u;
@@ -192,7 +208,7 @@ head_logprobs_kernel(const __grid_constant__ CUtensorMap tm_h, const __grid_cons
       for (int u = cid; ok && u < p.units; u += ncl) {
         int row0, vt0, vt1, seg;
         unit_range(p, u, row0, vt0, vt1, seg);
-        for (int vt = vt0; ok && vt < vt1; ++vt, ++lt) {
+        for (int i = vt0 * p.depths; ok && i < vt1 * p.depths; ++i, ++lt) {
           const int h = lt & 1;
           if (!wait_bounded(tempty + h, (static_cast<uint32_t>(lt >> 1) & 1u) ^ 1u, abort_flag, p.ctl, 42)) {
             ok = false;
@@ -200,7 +216,8 @@ head_logprobs_kernel(const __grid_constant__ CUtensorMap tm_h, const __grid_cons
           }
           tc_fence_after();
           const uint32_t d = tmem_base + static_cast<uint32_t>(h * BN);
-          for (int kb = 0; kb < p.kb; ++kb) {
+          const int depth = min(kLogitDepth, p.kb - i % p.depths * kLogitDepth);
+          for (int kb = 0; kb < depth; ++kb) {
             if (!wait_bounded(full + stage, phase, abort_flag, p.ctl, 43)) {
               ok = false;
               break;
@@ -231,6 +248,7 @@ head_logprobs_kernel(const __grid_constant__ CUtensorMap tm_h, const __grid_cons
     }
   } else if (warp >= kEpiWarp0) {
     // ------------------------------------------------------------------ epilogue (both CTAs)
+    setmaxnreg_inc<kRegsEpilogue>();
     const int q = warp & 3;                 // TMEM lane quarter this warp may access
     const int hc = (warp - kEpiWarp0) >> 2;  // column half
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(hc * HB);
@@ -245,38 +263,43 @@ head_logprobs_kernel(const __grid_constant__ CUtensorMap tm_h, const __grid_cons
       // the row's own column of this warp's half, relative to vocabulary column 0 of the half
       const int tcol = want >= 0 && want < p.V ? static_cast<int>(want) : -1;
       Sums r{-INFINITY, 0.f, 0.f};
-      for (int vt = vt0; vt < vt1; ++vt, ++lt) {
-        const int h = lt & 1;
-        const bool w = wait_bounded(tfull + h, static_cast<uint32_t>(lt >> 1) & 1u, abort_flag, p.ctl, 44);
-        if (!__all_sync(0xffffffffu, w)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const int col_base = vt * BN + hc * HB;
+      for (int vt = vt0; ok && vt < vt1; ++vt) {
+        float z[HB / 32][32] = {};  // this row's logits, the sum of its parts
 #pragma unroll 1
+        for (int part = 0; part < p.depths; ++part, ++lt) {
+          const int h = lt & 1;
+          const bool w = wait_bounded(tfull + h, static_cast<uint32_t>(lt >> 1) & 1u, abort_flag, p.ctl, 44);
+          if (!__all_sync(0xffffffffu, w)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t half = lane_base + static_cast<uint32_t>(h * BN);
+#pragma unroll
+          for (int ch = 0; ch < HB / 32; ++ch) add32(z[ch], half + ch * 32);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(lead_tempty + h * 8);
+        }
+        if (!ok) break;
+        const int col_base = vt * BN + hc * HB;
+#pragma unroll
         for (int ch = 0; ch < HB / 32; ++ch) {
           const int col = col_base + ch * 32;
           const int valid = p.V - col;
-          if (valid <= 0) break;
-          float z[32];
-          tmem_ld32(lane_base + static_cast<uint32_t>(h * BN + ch * 32), z);
-          tmem_ld_wait();
+          if (valid <= 0) continue;
           const int rel = tcol - col;
           if (__any_sync(0xffffffffu, rel >= 0 && rel < 32)) {
             float zt = 0.f;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) zt = j == rel ? z[j] : zt;
+            for (int j = 0; j < 32; ++j) zt = j == rel ? z[ch][j] : zt;
             if (rel >= 0 && rel < 32) p.z_token[token] = zt;
           }
           if (valid >= 32)
-            fold32<false>(r, z, 32, p.c);
+            fold32<false>(r, z[ch], 32, p.c);
           else
-            fold32<true>(r, z, valid, p.c);
+            fold32<true>(r, z[ch], valid, p.c);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(lead_tempty + h * 8);
       }
       if (!ok) break;
       if (token < p.N)

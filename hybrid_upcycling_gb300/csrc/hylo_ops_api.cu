@@ -275,9 +275,8 @@ hylo_status hylo_head_logprobs(const uint16_t* h, const uint16_t* W, int64_t N, 
   p.part = reinterpret_cast<float4*>(static_cast<char*>(workspace) + l.part);
   p.ctl = WaitCtl{dev->status, wait_limit_ns()};
   // With lse a backward may follow. It takes exp(z - lse) of logits that it computes again for probabilities, and 1 - p of a
-  // confident token loses as many digits as those differ from the forward's: both then accumulate alike. (Otherwise: 1 - p =
-  // 1e-3, d = 4096: gradients of one token 8% off by dot products here, of 64 tokens 1% off by rotated starts.)
-  p.rotate = !lse && N <= 2 * kBM;
+  // confident token loses as many digits as those differ from the forward's: both then accumulate alike. (With dot products
+  // here the gradients of one token with 1 - p = 1e-3 and d = 4096 were 8% off.)
   if (!lse && head_few_fits(N, d)) {
     p.slots = dev->sms < 2 * head_segments(N) ? dev->sms : 2 * head_segments(N);
     const cudaError_t e = launch_head_few(h, W, static_cast<int>(d), p, logp, entropy, lse, stream);
@@ -295,6 +294,7 @@ hylo_status hylo_head_logprobs(const uint16_t* h, const uint16_t* W, int64_t N, 
   if ((st = make_map_3d(&m_h, h, bf, d, N, p.copies, d * 2, kBK, kBM)) != HYLO_OK) return st;
   if ((st = make_map(&m_W, W, bf, d, V, d * 2, kBK, kFusedBN / 2)) != HYLO_OK) return st;
   p.kb = static_cast<int>(cdiv(d, kBK));
+  p.depths = static_cast<int>(cdiv(p.kb, kLogitDepth));
   p.token_tiles = static_cast<int>(cdiv(N, 2 * kBM));
   p.vtiles = static_cast<int>(cdiv(V, kFusedBN));
   p.nseg = choose_segments(p.token_tiles, p.vtiles, dev->head_clusters, head_segments(N));

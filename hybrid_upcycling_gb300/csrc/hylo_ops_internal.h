@@ -47,16 +47,24 @@ cudaError_t launch_token_logprobs(const TokenRows& in, const TokenOut& out, int 
                                   cudaStream_t stream);
 cudaError_t launch_token_logprobs_bwd(const TokenRows& in, const TokenGrad& g, int dtype, int sms, cudaStream_t stream);
 
+// The tensor cores cut the sum off at fp32's last bit after every 16 products, which carries a logit towards 0 by up to
+// 2^-24 of it per step. So the logits of the log-probabilities from hidden states are accumulated over at most this many
+// 64-wide k-blocks at a time, and these partial sums added up in registers, rounded to nearest. Log-probabilities of 8
+// tokens, d = 4096, V = 32000: in one go 1.5e-5 off, so 4e-6; with half the depth 2e-6, but the reads of TMEM then hold up the
+// tensor cores (8192 tokens, d = 2048 2107 us in one go, 2102 to 2152 so, 2150 to 2209 with half the depth; 3 tokens, d = 4096
+// 182, 180 and 200).
+constexpr int kLogitDepth = 16;
+
 // Forward of the log-probabilities from hidden states (head_logprobs.cu).
 struct HeadParams {
   int N, V;
   int kb;           // 64-wide k-blocks of d
+  int depths;       // ceil(kb / kLogitDepth)
   int token_tiles;  // ceil(N / 256)
   int vtiles;       // ceil(V / 256)
   int nseg;         // vocabulary segments per token tile
   int units;        // token_tiles * nseg
   int copies;       // of h, which the clusters share out
-  bool rotate;      // clusters start at different depths of the hidden dimension
   float c;          // log2(e) / tau
   float inv_tau;
   const int64_t* tokens;

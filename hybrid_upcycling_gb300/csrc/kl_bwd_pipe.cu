@@ -39,7 +39,8 @@
 //
 // The same launch also runs the backward of the token log-probabilities from hidden states
 // (kHead: there is no teacher; G is formed from the student tile, the row's log-sum-exp, entropy
-// and upstream gradients, see HeadGrad). Its F items take one TMEM half, like M items. There M(b) waits for the dh_s items of
+// and upstream gradients, see HeadGrad). Its F items take one TMEM half, like M items, or several one after another (kLogitDepth), as
+// the forward of those log-probabilities does. There M(b) waits for the dh_s items of
 // M(b-1) only, which come first in their block (kOrderDh): dW_s tiles of one block do not meet those of the next, and long
 // dh_s items at a block's end would hold up the next block (1500 tokens, d = 2048, V = 128256: 1.93 ms in the order
 // above, 1.57 so; 2048 tokens 2.30 and 2.08; 4096 tokens and more the same). With few tokens the additions into dh_s are a
@@ -621,40 +622,45 @@ bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p, co
           ++uses[0];
           ++uses[1];
         } else {
-          const int h = hp;
-          hp ^= 1;
-          if (!wait_bounded(tempty + h, (uses[h] & 1u) ^ 1u, abort_flag, p.ctl, 29)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const bool fwd = kHead && it.kind == kItemF;  // one tile z = h W^T
+          const bool fwd = kHead && it.kind == kItemF;  // one tile z = h W^T, in parts of kLogitDepth k-blocks
           const bool amn = it.kind == kItemDW;
           const uint32_t idesc = fwd ? kIdescF : amn ? kIdescDW : kIdescDH;
-          const uint32_t d = tmem_base + static_cast<uint32_t>(h * BN);
           const int nkb = fwd ? p.kb_s : m_kblocks<SPLIT>(p, g, it, dhw);
-          for (int kb = 0; kb < nkb; ++kb) {
-            if (!wait_bounded(full + stage, phase, abort_flag, p.ctl, 30)) {
+          const int depth = fwd ? kLogitDepth : nkb;
+          for (int first = 0; ok && first < nkb; first += depth) {
+            const int h = hp;
+            hp ^= 1;
+            if (!wait_bounded(tempty + h, (uses[h] & 1u) ^ 1u, abort_flag, p.ctl, 29)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES);
-            const uint32_t sb = sa + A_BYTES;
+            const uint32_t d = tmem_base + static_cast<uint32_t>(h * BN);
+            const int n = min(depth, nkb - first);
+            for (int kb = 0; kb < n; ++kb) {
+              if (!wait_bounded(full + stage, phase, abort_flag, p.ctl, 30)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES);
+              const uint32_t sb = sa + A_BYTES;
 #pragma unroll
-            for (int q = 0; q < kBK / 16; ++q) {
-              umma_bf16_pair(d, slice_desc(amn, sa, q), slice_desc(!fwd, sb, q), idesc, (kb > 0 || q > 0) ? 1u : 0u);
+              for (int q = 0; q < kBK / 16; ++q) {
+                umma_bf16_pair(d, slice_desc(amn, sa, q), slice_desc(!fwd, sb, q), idesc, (kb > 0 || q > 0) ? 1u : 0u);
+              }
+              umma_commit_pair(empty + stage, 0x3);
+              issued = true;
+              if (++stage == STAGES) {
+                stage = 0;
+                phase ^= 1u;
+              }
             }
-            umma_commit_pair(empty + stage, 0x3);
-            issued = true;
-            if (++stage == STAGES) {
-              stage = 0;
-              phase ^= 1u;
-            }
+            if (!ok) break;
+            umma_commit_pair(tfull + h, 0x3);
+            ++uses[h];
           }
           if (!ok) break;
-          umma_commit_pair(tfull + h, 0x3);
-          ++uses[h];
         }
       }
       if (!ok && issued) {
@@ -708,9 +714,40 @@ bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p, co
           bs = ls_ * kLog2e;
           ngl = -(p.lse_gap != nullptr ? p.lse_gap[token] : ls_ - lt_) * kLog2e;
         }
-        const int t = hp, sh = kHead ? hp : hp ^ 1;
-        float zt[kHead ? 1 : HB];
-        if constexpr (!kHead) {
+        const int t = hp, sh = hp ^ 1;
+        float zt[HB];
+        if constexpr (kHead) {
+          // all 128 logits of this row and column half, added up from the parts, each of which gives its half back at once
+#pragma unroll
+          for (int j = 0; j < HB; ++j) zt[j] = 0.f;
+          bool fine = true;
+#pragma unroll 1
+          for (int first = 0; first < p.kb_s; first += kLogitDepth) {
+            const int h = hp;
+            fine = wait_bounded(tfull + h, uses[h] & 1u, abort_flag, p.ctl, 32);
+            fine = __all_sync(0xffffffffu, fine);
+            if (!fine) break;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < HB / 32; ++c) {
+              float v[32];
+              tmem_ld32(lane_base + static_cast<uint32_t>(h * BN + c * 32), v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 32; j += 2) {
+                const float2 s = __fadd2_rn(make_float2(zt[32 * c + j], zt[32 * c + j + 1]), make_float2(v[j], v[j + 1]));
+                zt[32 * c + j] = s.x;
+                zt[32 * c + j + 1] = s.y;
+              }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(lead_tempty + h * 8);
+            ++uses[h];
+            hp ^= 1;
+          }
+          if (!fine) break;
+        } else {
           // the teacher tile: all 128 logits of this row and column half into registers, then the
           // half goes back to the UMMAs
           const bool wt = wait_bounded(tfull + t, uses[t] & 1u, abort_flag, p.ctl, 32);
@@ -723,13 +760,10 @@ bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p, co
           __syncwarp();
           if (lane == 0) mbar_arrive_remote(lead_tempty + t * 8);
         }
-        const bool ws = wait_bounded(tfull + sh, uses[sh] & 1u, abort_flag, p.ctl, 32);
-        if (!__all_sync(0xffffffffu, ws)) break;
-        tc_fence_after();
-        if constexpr (kHead) {
-          ++uses[sh];
-          hp ^= 1;
-        } else {
+        if constexpr (!kHead) {
+          const bool ws = wait_bounded(tfull + sh, uses[sh] & 1u, abort_flag, p.ctl, 32);
+          if (!__all_sync(0xffffffffu, ws)) break;
+          tc_fence_after();
           ++uses[0];
           ++uses[1];
         }
@@ -739,9 +773,14 @@ bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p, co
 #pragma unroll
         for (int c = 0; c < HB / 32; ++c) {
           float zs[32];
-          tmem_ld32(lane_base + static_cast<uint32_t>(sh * BN + c * 32), zs);
-          tmem_ld_wait();
-          if constexpr (kHead) head_grad32(hr, zs, g.v0 + col_local + c * 32, p.c);
+          if constexpr (kHead) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) zs[j] = zt[32 * c + j];
+            head_grad32(hr, zs, g.v0 + col_local + c * 32, p.c);
+          } else {
+            tmem_ld32(lane_base + static_cast<uint32_t>(sh * BN + c * 32), zs);
+            tmem_ld_wait();
+          }
           const int vcols = g.Vb - (col_local + c * 32);  // columns of this chunk inside the vocabulary
           uint32_t pk[16], pl[16];  // G in bf16 and (split) its bf16 rounding remainder
 #pragma unroll
@@ -783,9 +822,11 @@ bwd_pipe_kernel(const __grid_constant__ PipeMaps maps, const BwdPipeParams p, co
             bulk_commit_group();
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(lead_tempty + sh * 8);
+        if constexpr (!kHead) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(lead_tempty + sh * 8);
+        }
       } else {
         ctr = parts || (plan.order == kOrderDh && it.kind == kItemDW) ? kSlotM + static_cast<unsigned>(g.slot) : 1u;
         const int h = hp;

@@ -63,9 +63,11 @@ hylo_status hylo_token_logprobs_backward(const void* z, int dtype, int64_t N, in
  * that dh is joined from where N <= 1024 (at most 128 MiB) and, for bf16 gradients, the fp32 sums
  * behind them: N d of dh, and V d of dW if N is more than one token block.
  * hylo_head_logprobs_workspace_bytes() is enough for both directions with both gradients.
- * Logits are accumulated like those of hylo_kl_forward (see its accuracy), those of one or two tokens by
- * fp32 multiply-adds. Where lse is asked for, they are accumulated as the backward will accumulate them again, so
- * that its probabilities exp(z - lse) are those of the forward to a few fp32 roundings of lse.
+ * Accuracy: a logit is accumulated by the tensor cores in fp32 over at most 64 steps of 16 products, and these sums
+ * are added up rounded to nearest, which can drift by up to 2^-18 of the logits' scale in one direction whatever d is
+ * (measured 3e-7 of it). Without lse, those of one or two tokens are fp32 multiply-adds. Where lse is asked for,
+ * they are accumulated as the backward will accumulate them again, so that its probabilities
+ * exp(z - lse) are those of the forward to a few fp32 roundings of lse.
  * Each returns 0 for invalid sizes; token_chunk <= 0 means 4096; grad_dtype as in the backward. */
 size_t hylo_head_logprobs_workspace_bytes(int64_t N, int64_t d, int64_t V, int64_t token_chunk, int split_g,
                                           int grad_dtype);
