@@ -320,7 +320,7 @@ head_logprobs_kernel(const __grid_constant__ CUtensorMap tm_h, const __grid_cons
 // 256-row tiles on them. Every warp takes kRows words at a time, its lanes walk the hidden dimension with
 // 16-byte loads of W and the tokens' states in fp32 from shared memory, and the dot products end in
 // a warp reduction; lane t keeps token t's running sums. fp32 multiply-adds: no drift of
-// long tensor-core accumulations. Measured beside the tensor-core path (128256 words; d = 4096 172 us and d = 2048 94 us
+// long tensor-core accumulations. Measured beside the tensor-core path (128256 words; d = 4096 177 us and d = 2048 95 us
 // for three or four tokens): one token 147 us (7.1 TB/s) and 78; two tokens 152 and 90; four tokens 172 at d = 4096,
 // where the multiply-adds and not the loads set the time. So it takes one or two.
 constexpr int kFewThreads = 512;

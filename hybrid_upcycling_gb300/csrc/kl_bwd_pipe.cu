@@ -39,11 +39,11 @@
 //
 // The same launch also runs the backward of the token log-probabilities from hidden states
 // (kHead: there is no teacher; G is formed from the student tile, the row's log-sum-exp, entropy
-// and upstream gradients, see HeadGrad). Its F items take one TMEM half, like M items, or several one after another (kLogitDepth), as
-// the forward of those log-probabilities does. There M(b) waits for the dh_s items of
-// M(b-1) only, which come first in their block (kOrderDh): dW_s tiles of one block do not meet those of the next, and long
+// and upstream gradients, see HeadGrad). Its F items take one TMEM half, like M items, or the halves in turn
+// where the hidden dimension is accumulated in parts (kLogitDepth), as in the forward of those log-probabilities: both
+// then have the same logits. M(b) waits there for the dh_s items of M(b-1) only, which come first in their block (kOrderDh): dW_s tiles of one block do not meet those of the next, and long
 // dh_s items at a block's end would hold up the next block (1500 tokens, d = 2048, V = 128256: 1.93 ms in the order
-// above, 1.57 so; 2048 tokens 2.30 and 2.08; 4096 tokens and more the same). With few tokens the additions into dh_s are a
+// above, 1.57 so; 2048 tokens 2.30 and 2.08; 4096 tokens and more the same; logits in one part). With few tokens the additions into dh_s are a
 // chain over the whole vocabulary on a few clusters all the same (N <= 256: 0.85 ms in all against 0.46): there
 // (kOrderParts) every block stores its dh_s products apart, over all of its words or over stretches of them
 // (HeadGrad::dh_words), for a sum in fixed order afterwards, and M(b) needs F(b) only. F(b) needs M(b-3) always.
