@@ -46,9 +46,10 @@ int head_segments(int64_t N) {
   return s > kMaxSegments ? static_cast<int>(s) : kMaxSegments;
 }
 
-// Copies of h in the workspace. All clusters read h all the time, and less than 128 KiB lies in a few of L2's slices, which
-// then hold everything up: 8 tokens of d = 4096, V = 128256 took 190 to 280 us by where h lay, and 172 us (179
-// with logits in parts, kLogitDepth) with copies of 512 KiB in all. A small LM head is read in a few microseconds, in which the copies cost more.
+// Copies of h in the workspace. All clusters read h all the time, and less than 128 KiB lies in a few of L2's slices,
+// which then hold everything up: 8 tokens of d = 4096, V = 128256 took 190 to 280 us by where h lay, and 172 us (179
+// with logits in parts, kLogitDepth) with copies of 512 KiB in all. A small LM head is read in a few microseconds, in
+// which the copies cost more.
 constexpr int64_t kHotBytes = 128 << 10, kCopyBytes = 512 << 10, kCopyHeadBytes = 64 << 20;
 constexpr int64_t kMaxCopies = 64;  // about one for each cluster
 int head_copies(int64_t N, int64_t d, int64_t V) {
@@ -83,18 +84,20 @@ struct HeadBwd {
   int64_t dh_words;  // words of a part
   bool dW_direct;    // dW is written in bf16 by the pipelined backward itself
 };
-// Few tokens: dh in parts, one per vocabulary block (at most 16 of those) or several. Long blocks wait less for ring slots,
-// short ones spread dh over more clusters, which counts with more tokens. Measured at d = 2048, V = 128256 with blocks of 8192,
-// 12288, 16384 and 24576 words: 256 tokens 642, 550, 587, 534 us; 512 tokens 777, 714, 649, 643; 1024 tokens 1062, 1054,
-// 1075 us (24576 words do not fit the ring; all before the logits came in parts, which adds 1 to 4% in every case). Fewer words where that leaves fewer than three blocks. N d is bounded so that
-// a part is at most 8 MiB; with more tokens the chain of additions is short beside the rest.
+// Few tokens: dh in parts, one per vocabulary block (at most 16 of those) or several. Long blocks wait less for ring
+// slots, short ones spread dh over more clusters, which counts with more tokens. Measured at d = 2048, V = 128256 with
+// blocks of 8192, 12288, 16384 and 24576 words: 256 tokens 642, 550, 587, 534 us; 512 tokens 777, 714, 649, 643; 1024
+// tokens 1062, 1054, 1075 us (24576 words do not fit the ring; all before the logits came in parts, which adds 1 to 4%
+// in every case). Fewer words where that leaves fewer than three blocks. N d is bounded so that a part is at most 8 MiB;
+// with more tokens the chain of additions is short beside the rest.
 constexpr int64_t kPartTokens = 1024, kPartElems = int64_t(1) << 21, kMaxParts = 16;
 constexpr int64_t part_words(int64_t N) { return N <= 512 ? 24576 : 12288; }
 // With few 256 x 256 tiles of dh (N d small) a block's words are cut up too, into parts of their own, so that the long
-// products run on more clusters. Measured (1, 2, 3, 4 parts a block; V = 128256 if not said): 256 tokens, d = 2048 538, 462,
-// 475, 486 us, d = 4096 854, 878, 897, 908; 512 tokens, d = 2048 644, 625, 636, 653; 1000 tokens, d = 2048 1077,
-// 1129, 1184, 1197 (again before the parts of logits); 800 tokens, d = 1024, V = 32000 242, 183, 183, 174; 1000 tokens, d = 512, V = 151936 795, 527, 463,
-// 435. So up to 16 items a block with one tile of tokens and up to 32 with more, of at least 1024 words.
+// products run on more clusters. Measured (1, 2, 3, 4 parts a block; V = 128256 if not said): 256 tokens, d = 2048 538,
+// 462, 475, 486 us, d = 4096 854, 878, 897, 908; 512 tokens, d = 2048 644, 625, 636, 653; 1000 tokens, d = 2048 1077,
+// 1129, 1184, 1197 (again before the parts of logits); 800 tokens, d = 1024, V = 32000 242, 183, 183, 174; 1000 tokens,
+// d = 512, V = 151936 795, 527, 463, 435. So up to 16 items a block with one tile of tokens and up to 32 with more, of
+// at least 1024 words.
 constexpr int64_t kPartBytes = int64_t(128) << 20;  // of all parts together
 constexpr int64_t kMinPartWords = 1024;
 int64_t block_parts(int64_t N, int64_t d, int64_t blocks) {
