@@ -35,7 +35,8 @@ EXPORTS = ("hylo_kl_workspace_bytes", "hylo_kl_forward", "hylo_kl_backward", "hy
            "hylo_fused_kl_logits", "hylo_ild_loss", "hylo_token_logprobs", "hylo_token_logprobs_backward",
            "hylo_head_logprobs_workspace_bytes", "hylo_head_logprobs_forward_workspace_bytes",
            "hylo_head_logprobs_backward_workspace_bytes", "hylo_head_logprobs", "hylo_head_logprobs_backward",
-           "hylo_grad_norm_workspace_bytes", "hylo_grad_norm", "hylo_adamw_step")
+           "hylo_grad_norm_workspace_bytes", "hylo_grad_norm", "hylo_adamw_step",
+           "hylo_norm", "hylo_norm_backward_workspace_bytes", "hylo_norm_backward")
 
 DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}  # hylo_dtype
 TOP_MAX = 64  # HYLO_TOP_MAX
@@ -97,6 +98,12 @@ def load() -> ctypes.CDLL:
     L.hylo_grad_norm.restype = ctypes.c_int
     L.hylo_adamw_step.argtypes = [vp, i32, i32, i32, i32, f64, f64, f64, i64, f32, vp, f32, ctypes.c_uint32, vp]
     L.hylo_adamw_step.restype = ctypes.c_int
+    L.hylo_norm.argtypes = [vp, vp, i32, i64, i64, i64, i64, vp, vp, i32, i32, f64, vp, vp, vp, vp]
+    L.hylo_norm.restype = ctypes.c_int
+    L.hylo_norm_backward_workspace_bytes.argtypes = [i64, i64]
+    L.hylo_norm_backward_workspace_bytes.restype = sz
+    L.hylo_norm_backward.argtypes = [vp, i32, i64, i64, i64, vp, i32, i32, vp, vp, i64, vp, i64, vp, vp, vp, vp, sz, vp]
+    L.hylo_norm_backward.restype = ctypes.c_int
     L.hylo_kl_selftest_wait_timeout.argtypes = [ctypes.c_int, vp]
     L.hylo_kl_selftest_wait_timeout.restype = ctypes.c_int
     L.hylo_kl_sync_status.argtypes = [vp]
@@ -364,6 +371,59 @@ def hylo_adamw_step(fields, count: int, param_dtype, grad_dtype, state_bits: int
     table = struct.pack("=" + ADAMW_TENSOR * count, *fields)
     _check(load().hylo_adamw_step(table, count, DTYPES[param_dtype], DTYPES[grad_dtype], state_bits, betas[0], betas[1],
                                   eps, step, grad_scale, _ptr(norm), max_norm, seed & 0xFFFFFFFF, _stream(stream)))
+
+
+def _gain_dtype(x, weight, bias) -> int:
+    gains = [t for t in (weight, bias) if t is not None]
+    for t in gains:
+        _need("weight and bias", t, gains[0].dtype, (x.shape[1],))
+        if t.dtype not in (x.dtype, torch.float32):
+            raise ValueError("weight and bias must have the dtype of x or be float32")
+    return DTYPES[gains[0].dtype if gains else x.dtype]
+
+
+def hylo_norm(x, residual, weight, bias, rms: bool, eps: float, sum, y, stats=None, stream=None) -> None:
+    """Layer norm or RMS norm of rows x [N, d] (fp32, bf16 or fp16; unit column stride), with a residual or None."""
+    if x.dtype not in DTYPES:
+        raise ValueError("x must be float32, bfloat16 or float16")
+    ldx = _row_stride("x", x)
+    N, d = x.shape
+    _need_cuda(x=x, residual=residual, weight=weight, bias=bias, sum=sum, y=y, stats=stats)
+    if residual is not None and (residual.dtype != x.dtype or residual.shape != x.shape):
+        raise ValueError("residual must have the dtype and shape of x")
+    ldr = 0 if residual is None else _row_stride("residual", residual)
+    for name, t in (("sum", sum), ("y", y)):
+        _need(name, t, x.dtype, (N, d))
+    _need("stats", stats, torch.float32, (N, 2))
+    _check(load().hylo_norm(x.data_ptr(), _ptr(residual), DTYPES[x.dtype], N, d, ldx, ldr, _ptr(weight), _ptr(bias),
+                            _gain_dtype(x, weight, bias), int(rms), float(eps), _ptr(sum), y.data_ptr(), _ptr(stats),
+                            _stream(stream)))
+
+
+def hylo_norm_backward_workspace_bytes(N: int, d: int) -> int:
+    return int(load().hylo_norm_backward_workspace_bytes(N, d))
+
+
+def hylo_norm_backward(s, weight, rms: bool, stats, dy, dsum, dx, dweight, dbias, workspace, stream=None) -> None:
+    """Gradients dx [N, d], dweight and dbias [d] (overwritten; any of them None) for the upstream dy and dsum (or None)."""
+    if s.dtype not in DTYPES:
+        raise ValueError("s must be float32, bfloat16 or float16")
+    lds = _row_stride("s", s)
+    N, d = s.shape
+    _need_cuda(s=s, weight=weight, stats=stats, dy=dy, dsum=dsum, dx=dx, dweight=dweight, dbias=dbias, workspace=workspace)
+    for name, t in (("dy", dy), ("dsum", dsum)):
+        if t is not None and (t.dtype != s.dtype or t.shape != s.shape):
+            raise ValueError(f"{name} must have the dtype and shape of s")
+    _need("stats", stats, torch.float32, (N, 2))
+    _need("dx", dx, s.dtype, (N, d))
+    gains = [t for t in (weight, dweight, dbias) if t is not None]
+    for t in gains:
+        _need("weight, dweight and dbias", t, gains[0].dtype, (d,))
+    _check(load().hylo_norm_backward(
+        s.data_ptr(), DTYPES[s.dtype], N, d, lds, _ptr(weight), DTYPES[gains[0].dtype if gains else s.dtype], int(rms),
+        stats.data_ptr(), dy.data_ptr(), _row_stride("dy", dy), _ptr(dsum), 0 if dsum is None else _row_stride("dsum", dsum),
+        _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def hylo_kl_selftest_wait_timeout(limit_ms: int, stream=None) -> None:

@@ -192,6 +192,45 @@ hylo_status check_apart(const hylo_adamw_tensor* tensors, int count, size_t para
   return HYLO_OK;
 }
 
+bool norm_sizes_ok(int64_t N, int64_t d) { return N >= 1 && N <= 0x7fffffffLL && d >= 1 && d <= (int64_t(1) << 20); }
+bool stride_ok(int64_t ld, int64_t d) { return ld >= d && ld <= (int64_t(1) << 40); }
+
+hylo_status check_norm(const void* x, int dtype, int64_t N, int64_t d, int64_t ldx, const void* weight, const void* bias, int gain_dtype) {
+  if (!x) return fail(HYLO_ERR_NULL, "a required pointer is NULL");
+  if (!dtype_ok(dtype) || (gain_dtype != dtype && gain_dtype != HYLO_F32))
+    return fail(HYLO_ERR_DIM, "dtype=%d gain_dtype=%d (weight and bias are of the rows' type or fp32)", dtype, gain_dtype);
+  if (!norm_sizes_ok(N, d) || !stride_ok(ldx, d))
+    return fail(HYLO_ERR_DIM, "invalid sizes N=%lld d=%lld, row stride %lld (need 1 <= N < 2^31, 1 <= d <= 2^20, stride >= d)",
+                static_cast<long long>(N), static_cast<long long>(d), static_cast<long long>(ldx));
+  if (!aligned(x, dtype_bytes(dtype)) || !aligned(weight, dtype_bytes(gain_dtype)) || !aligned(bias, dtype_bytes(gain_dtype)))
+    return fail(HYLO_ERR_ALIGN, "pointers must be aligned to their elements");
+  return HYLO_OK;
+}
+
+// Bytes from the first element of N rows of d elements to behind the last.
+uintptr_t span(int64_t N, int64_t d, int64_t ld, uintptr_t bytes) { return (static_cast<uintptr_t>(N - 1) * ld + d) * bytes; }
+
+struct Range {
+  const void* p;  // or null
+  uintptr_t bytes;
+};
+
+// No output may overlap an input or another output.
+template <size_t A, size_t B>
+hylo_status check_disjoint(const Range (&out)[A], const Range (&in)[B]) {
+  auto meet = [](const Range& a, const Range& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && x < y + b.bytes && y < x + a.bytes;
+  };
+  for (size_t i = 0; i < A; ++i) {
+    for (size_t j = 0; j < B; ++j)
+      if (meet(out[i], in[j])) return fail(HYLO_ERR_DIM, "an output overlaps an input");
+    for (size_t j = 0; j < i; ++j)
+      if (meet(out[i], out[j])) return fail(HYLO_ERR_DIM, "two outputs overlap");
+  }
+  return HYLO_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -448,6 +487,69 @@ hylo_status hylo_adamw_step(const hylo_adamw_tensor* tensors, int count, int par
   const double bias1 = 1.0 - std::pow(beta1, static_cast<double>(step));
   const cudaError_t e = launch_adamw(tensors, count, param_dtype, grad_dtype, state_bits, tensors[some].master != nullptr, bias1, h, dev->sms, stream);
   return e == cudaSuccess ? HYLO_OK : cuda_fail(e, "launch AdamW");
+}
+
+size_t hylo_norm_backward_workspace_bytes(int64_t N, int64_t d) {
+  clear_error();
+  if (!norm_sizes_ok(N, d)) return 0;
+  return 2 * sizeof(float) * static_cast<size_t>(norm_parts(N, static_cast<int>(d))) * static_cast<size_t>(d);
+}
+
+hylo_status hylo_norm(const void* x, const void* residual, int dtype, int64_t N, int64_t d, int64_t ldx, int64_t ldr,
+                      const void* weight, const void* bias, int gain_dtype, int rms, double eps, void* sum, void* y,
+                      float* stats, cudaStream_t stream) {
+  clear_error();
+  hylo_status st = check_norm(x, dtype, N, d, ldx, weight, bias, gain_dtype);
+  if (st != HYLO_OK) return st;
+  if (!y || (residual != nullptr) != (sum != nullptr)) return fail(HYLO_ERR_NULL, "y is required, and sum with a residual and only then");
+  if (residual && !stride_ok(ldr, d)) return fail(HYLO_ERR_DIM, "invalid row stride %lld of the residual", static_cast<long long>(ldr));
+  const uintptr_t e = dtype_bytes(dtype);
+  if (!aligned(residual, e) || !aligned(sum, e) || !aligned(y, e) || !aligned(stats, 8))
+    return fail(HYLO_ERR_ALIGN, "pointers must be aligned to their elements (stats: 8 bytes)");
+  if (!(eps >= 0) || !std::isfinite(static_cast<float>(eps))) return fail(HYLO_ERR_TAU, "eps must be finite and >= 0");
+  const uintptr_t rows = span(N, d, d, e);
+  const Range out[] = {{sum, rows}, {y, rows}, {stats, static_cast<uintptr_t>(N) * 8}};
+  const Range in[] = {{x, span(N, d, ldx, e)}, {residual, span(N, d, ldr, e)}, {weight, d * dtype_bytes(gain_dtype)}, {bias, d * dtype_bytes(gain_dtype)}};
+  if ((st = check_disjoint(out, in)) != HYLO_OK) return st;
+  DeviceState* dev = nullptr;
+  if ((st = current_device(&dev)) != HYLO_OK) return st;
+  NormParams p{};
+  p.x = x, p.residual = residual, p.ldx = ldx, p.ldr = ldr, p.N = N, p.d = static_cast<int>(d), p.rms = rms != 0;
+  p.eps = static_cast<float>(eps), p.weight = weight, p.bias = bias, p.gain_f32 = gain_dtype == HYLO_F32, p.sum = sum, p.y = y;
+  p.stats = reinterpret_cast<float2*>(stats);
+  const cudaError_t err = launch_norm(p, dtype, dev->sms, stream);
+  return err == cudaSuccess ? HYLO_OK : cuda_fail(err, "launch norm");
+}
+
+hylo_status hylo_norm_backward(const void* s, int dtype, int64_t N, int64_t d, int64_t lds, const void* weight,
+                               int gain_dtype, int rms, const float* stats, const void* dy, int64_t lddy,
+                               const void* dsum, int64_t ldds, void* dx, void* dweight, void* dbias, void* workspace,
+                               size_t workspace_bytes, cudaStream_t stream) {
+  clear_error();
+  hylo_status st = check_norm(s, dtype, N, d, lds, weight, nullptr, gain_dtype);
+  if (st != HYLO_OK) return st;
+  if (!stats || !dy || ((dweight || dbias) && !workspace)) return fail(HYLO_ERR_NULL, "a required pointer is NULL");
+  if (!stride_ok(lddy, d) || (dsum && !stride_ok(ldds, d))) return fail(HYLO_ERR_DIM, "invalid row stride of a gradient");
+  const uintptr_t e = dtype_bytes(dtype), ge = dtype_bytes(gain_dtype);
+  if (!aligned(stats, 8) || !aligned(dy, e) || !aligned(dsum, e) || !aligned(dx, e) || !aligned(dweight, ge) || !aligned(dbias, ge) ||
+      !aligned(workspace, 16))
+    return fail(HYLO_ERR_ALIGN, "pointers must be aligned to their elements (stats: 8 bytes, workspace: 16 bytes)");
+  const bool columns = dweight || dbias;
+  const size_t need = columns ? 2 * sizeof(float) * static_cast<size_t>(norm_parts(N, static_cast<int>(d))) * static_cast<size_t>(d) : 0;
+  if (workspace_bytes < need)
+    return fail(HYLO_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu required", workspace_bytes, need);
+  const Range out[] = {{dx, span(N, d, d, e)}, {dweight, d * ge}, {dbias, d * ge}, {columns ? workspace : nullptr, need}};
+  const Range in[] = {{s, span(N, d, lds, e)}, {dy, span(N, d, lddy, e)}, {dsum, span(N, d, ldds, e)}, {weight, d * ge}, {stats, static_cast<uintptr_t>(N) * 8}};
+  if ((st = check_disjoint(out, in)) != HYLO_OK) return st;
+  DeviceState* dev = nullptr;
+  if ((st = current_device(&dev)) != HYLO_OK) return st;
+  if (!dx && !columns) return HYLO_OK;
+  NormParams p{};
+  p.x = s, p.ldx = lds, p.N = N, p.d = static_cast<int>(d), p.rms = rms != 0, p.weight = weight, p.gain_f32 = gain_dtype == HYLO_F32;
+  p.stats = reinterpret_cast<float2*>(const_cast<float*>(stats));
+  const NormGrad q{dy, dsum, lddy, ldds, dx, columns ? static_cast<float*>(workspace) : nullptr, dweight != nullptr, dbias != nullptr, dweight, dbias};
+  const cudaError_t err = launch_norm_bwd(p, q, dtype, norm_parts(N, p.d), dev->sms, stream);
+  return err == cudaSuccess ? HYLO_OK : cuda_fail(err, "launch norm backward");
 }
 
 }  // extern "C"

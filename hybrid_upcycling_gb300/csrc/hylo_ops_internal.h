@@ -130,4 +130,37 @@ struct AdamWHyper {
 cudaError_t launch_adamw(const hylo_adamw_tensor* tensors, int count, int param_dtype, int grad_dtype, int state_bits,
                          bool masters, double bias1, const AdamWHyper& h, int sms, cudaStream_t stream);
 
+// Layer norm and RMS norm (norm.cu).
+struct NormParams {
+  const void* x;         // [N, d], row stride ldx: the forward's input, the backward's normalised rows
+  const void* residual;  // [N, d], row stride ldr, or null
+  int64_t ldx, ldr;
+  int64_t N;
+  int d;
+  int rms;
+  float eps;
+  const void* weight;    // [d] or null
+  const void* bias;      // [d] or null
+  int gain_f32;          // weight and bias are fp32, not of the type of x
+  void* sum;             // [N, d], with a residual
+  void* y;               // [N, d]
+  float2* stats;         // (mean, 1 / deviation) [N], or null in a forward
+  int threads;           // threads that share a row, set by the launch
+};
+struct NormGrad {
+  const void* dy;    // [N, d], row stride lddy
+  const void* dsum;  // [N, d], row stride ldds, or null
+  int64_t lddy, ldds;
+  void* dx;          // [N, d] or null
+  float* part;       // [2][parts][d], or null: no column sums are wanted
+  int want_dw, want_db;
+  void* dw;
+  void* db;
+};
+// Widest rows whose gradients are formed in one reading, and the rows of `part`, one per CTA (or stretch of rows).
+constexpr int kNormFusedCols = 8192;
+int norm_parts(int64_t N, int d);
+cudaError_t launch_norm(const NormParams& p, int dtype, int sms, cudaStream_t stream);
+cudaError_t launch_norm_bwd(const NormParams& p, const NormGrad& q, int dtype, int parts, int sms, cudaStream_t stream);
+
 }  // namespace hylo

@@ -1,7 +1,7 @@
 /*
  * hylo_ops.h — C ABI of the operators that stand beside the distillation losses of hylo_kl.h
- * (GB300, sm_103a): log-probabilities of given tokens, and the AdamW step that applies the
- * gradients.
+ * (GB300, sm_103a): log-probabilities of given tokens, the AdamW step that applies the
+ * gradients, and the norms of the hidden states.
  *
  * Conventions are those of hylo_kl.h: device pointers owned by the caller unless a parameter
  * says otherwise, no allocation by the library, calls asynchronous on `stream`, a status code
@@ -155,6 +155,33 @@ hylo_status hylo_adamw_step(const hylo_adamw_tensor* tensors, int count, int par
                             int state_bits, double beta1, double beta2, double eps, int64_t step,
                             float grad_scale, const float* norm, float max_norm, uint32_t seed,
                             cudaStream_t stream);
+
+/* Layer norm (rms = 0) or RMS norm (rms != 0) of rows, with the sum of two streams in front. Per row:
+ *     s = x + residual, rounded to `dtype` (s = x if residual is NULL);  mu = mean(s) (RMS: 0)
+ *     r = 1 / sqrt(mean((s - mu)^2) + eps),  y = (s - mu) r weight + bias
+ * x, residual: [N, d] of `dtype` (HYLO_F32, HYLO_BF16, HYLO_F16), row strides ldx, ldr >= d elements; y, sum: [N, d],
+ * contiguous. weight, bias: [d] or NULL (1 and 0), both of gain_dtype, which is dtype or HYLO_F32. All element-aligned; rows of
+ * 16-byte vectors are fastest. sum receives s and is required with a residual (NULL without). stats [N, 2] receives (mu, r),
+ * which the backward reads, or is NULL. y and sum may not overlap the inputs or each other. 1 <= N <= 2^31 - 1,
+ * 1 <= d <= 2^20, eps finite and >= 0. Statistics are fp32: where mean((s - mu)^2) exceeds fp32's range the row's y is that of r = 0.
+ * With eps = 0 a row without deviation has r infinite, and NaN. Deterministic. */
+hylo_status hylo_norm(const void* x, const void* residual, int dtype, int64_t N, int64_t d, int64_t ldx, int64_t ldr,
+                      const void* weight, const void* bias, int gain_dtype, int rms, double eps, void* sum, void* y,
+                      float* stats, cudaStream_t stream);
+
+/* Its gradients. s is the forward's sum, or x without a residual (row stride lds); stats the forward's; dy [N, d] (row stride
+ * lddy) the gradient of y, dsum [N, d] (row stride ldds) that of sum, or NULL:
+ *     g = dy weight,  xh = (s - mu) r,  dx = r (g - mean(g) - xh mean(g xh)) + dsum   (RMS: without mean(g))
+ *     dweight = sum over rows of dy xh,  dbias = sum over rows of dy
+ * dx [N, d] contiguous, of `dtype` (x and residual have the same gradient); dweight, dbias [d] of gain_dtype (summed in fp32,
+ * rounded once). Any of the three may be NULL: it is left out. They are OVERWRITTEN and may not overlap the inputs or each
+ * other. workspace: 16-byte aligned, at least hylo_norm_backward_workspace_bytes() (0 for invalid sizes), not shared
+ * with a call still running on another stream; may be NULL without dweight and dbias. Deterministic: sums in a fixed order. */
+size_t hylo_norm_backward_workspace_bytes(int64_t N, int64_t d);
+hylo_status hylo_norm_backward(const void* s, int dtype, int64_t N, int64_t d, int64_t lds, const void* weight,
+                               int gain_dtype, int rms, const float* stats, const void* dy, int64_t lddy,
+                               const void* dsum, int64_t ldds, void* dx, void* dweight, void* dbias, void* workspace,
+                               size_t workspace_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -92,3 +92,28 @@ def adamw(w, g, m, v, *, step, lr, betas, eps, weight_decay, clip: float = 1.0):
     w = np.asarray(w, np.float64) * (1 - lr * weight_decay)
     w = w - lr * (m / (1 - b1 ** step)) / (np.sqrt(v / (1 - b2 ** step)) + eps)
     return w, m, v
+
+
+# ------------------------------------------------------------------------------------------------ norms
+def norm(s, weight, bias, eps: float, rms: bool):
+    """(y, mean [N, 1], 1 / deviation [N, 1]) of rows s [N, d]; weight and bias [d] or None."""
+    s = np.asarray(s, np.float64)
+    mu = np.zeros((s.shape[0], 1)) if rms else s.mean(axis=1, keepdims=True)
+    r = 1 / np.sqrt(((s - mu) ** 2).mean(axis=1, keepdims=True) + eps)
+    y = (s - mu) * r
+    if weight is not None:
+        y = y * weight
+    return (y if bias is None else y + bias), mu, r
+
+
+def norm_grad(s, weight, eps: float, rms: bool, dy):
+    """Gradients (ds, dweight, dbias) of sum(dy y), from the derivatives of mean and deviation one by one."""
+    s, dy = np.asarray(s, np.float64), np.asarray(dy, np.float64)
+    _, mu, r = norm(s, None, None, eps, rms)
+    c, d = s - mu, s.shape[1]
+    g = dy if weight is None else dy * weight
+    dr = (g * c).sum(axis=1, keepdims=True)             # y = c r
+    dvar = -0.5 * r ** 3 * dr                           # r = (var + eps)^(-1/2)
+    dc = g * r + dvar * 2 * c / d                       # var = mean(c^2)
+    ds = dc if rms else dc - dc.mean(axis=1, keepdims=True)
+    return ds, (dy * c * r).sum(axis=0), dy.sum(axis=0)
