@@ -36,7 +36,8 @@ EXPORTS = ("hylo_kl_workspace_bytes", "hylo_kl_forward", "hylo_kl_backward", "hy
            "hylo_head_logprobs_workspace_bytes", "hylo_head_logprobs_forward_workspace_bytes",
            "hylo_head_logprobs_backward_workspace_bytes", "hylo_head_logprobs", "hylo_head_logprobs_backward",
            "hylo_grad_norm_workspace_bytes", "hylo_grad_norm", "hylo_adamw_step",
-           "hylo_norm", "hylo_norm_backward_workspace_bytes", "hylo_norm_backward")
+           "hylo_norm", "hylo_norm_backward_workspace_bytes", "hylo_norm_backward",
+           "hylo_orthogonalize_workspace_bytes", "hylo_orthogonalize", "hylo_muon_workspace_bytes", "hylo_muon_step")
 
 DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}  # hylo_dtype
 TOP_MAX = 64  # HYLO_TOP_MAX
@@ -104,6 +105,14 @@ def load() -> ctypes.CDLL:
     L.hylo_norm_backward_workspace_bytes.restype = sz
     L.hylo_norm_backward.argtypes = [vp, i32, i64, i64, i64, vp, i32, i32, vp, vp, i64, vp, i64, vp, vp, vp, vp, sz, vp]
     L.hylo_norm_backward.restype = ctypes.c_int
+    L.hylo_orthogonalize_workspace_bytes.argtypes = [vp, i32]
+    L.hylo_orthogonalize_workspace_bytes.restype = sz
+    L.hylo_orthogonalize.argtypes = [vp, i32, i32, i32, i32, vp, f64, vp, sz, vp]
+    L.hylo_orthogonalize.restype = ctypes.c_int
+    L.hylo_muon_workspace_bytes.argtypes = [vp, i32]
+    L.hylo_muon_workspace_bytes.restype = sz
+    L.hylo_muon_step.argtypes = [vp, i32, i32, i32, f64, i32, i32, vp, f64, f32, vp, f32, ctypes.c_uint32, vp, sz, vp]
+    L.hylo_muon_step.restype = ctypes.c_int
     L.hylo_kl_selftest_wait_timeout.argtypes = [ctypes.c_int, vp]
     L.hylo_kl_selftest_wait_timeout.restype = ctypes.c_int
     L.hylo_kl_sync_status.argtypes = [vp]
@@ -424,6 +433,35 @@ def hylo_norm_backward(s, weight, rms: bool, stats, dy, dsum, dx, dweight, dbias
         stats.data_ptr(), dy.data_ptr(), _row_stride("dy", dy), _ptr(dsum), 0 if dsum is None else _row_stride("dsum", dsum),
         _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(workspace),
         0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+ORTH_MATRIX = "QQqqq"       # hylo_orth_matrix: two pointers, rows, cols, row stride
+MUON_TENSOR = "QQQQqqddd"   # hylo_muon_tensor: four pointers, rows, cols, lr, weight_decay, scale
+
+
+def hylo_orthogonalize_workspace_bytes(table: bytes, count: int) -> int:
+    return int(load().hylo_orthogonalize_workspace_bytes(table, count))
+
+
+def hylo_orthogonalize(table: bytes, count: int, dtype, out_dtype, coefficients, eps: float, workspace, stream=None) -> None:
+    """Orthogonalises `count` matrices; table: their packed hylo_orth_matrix structures (see muon.orthogonalize);
+    coefficients: three numbers for each step."""
+    k = (ctypes.c_double * len(coefficients))(*coefficients)
+    _check(load().hylo_orthogonalize(table, count, DTYPES[dtype], DTYPES[out_dtype], len(coefficients) // 3, k, eps,
+                                     workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def hylo_muon_workspace_bytes(table: bytes, count: int) -> int:
+    return int(load().hylo_muon_workspace_bytes(table, count))
+
+
+def hylo_muon_step(table: bytes, count: int, param_dtype, grad_dtype, momentum: float, nesterov: bool, coefficients, eps: float,
+                   grad_scale: float, norm, max_norm: float, seed: int, workspace, stream=None) -> None:
+    """One Muon step; table: the packed hylo_muon_tensor structures of all matrices (see muon.muon_step)."""
+    k = (ctypes.c_double * len(coefficients))(*coefficients)
+    _check(load().hylo_muon_step(table, count, DTYPES[param_dtype], DTYPES[grad_dtype], momentum, int(nesterov),
+                                 len(coefficients) // 3, k, eps, grad_scale, _ptr(norm), max_norm, seed & 0xFFFFFFFF,
+                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def hylo_kl_selftest_wait_timeout(limit_ms: int, stream=None) -> None:

@@ -18,6 +18,7 @@ struct DeviceState {
   int logits_clusters = 0; // clusters of the logits kernel resident at once
   int pipe_clusters = 0;   // 2-CTA clusters of the pipelined backward resident at once
   int head_clusters = 0;   // 2-CTA clusters of the head log-probability kernel resident at once
+  int muon_clusters = 0;   // 2-CTA clusters of the orthogonalised updates' products resident at once
   TokenOccupancy token;    // of the token log-probability kernels
   unsigned pace_epoch = 0;  // epoch of the last paced fused launch on this device
   int* status = nullptr;
@@ -44,6 +45,15 @@ hylo_status make_map_3d(CUtensorMap* m, const void* base, CUtensorMapDataType dt
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// An array of an optimizer step, [begin, end).
+struct Span {
+  uintptr_t begin, end;
+  bool written;
+  int tensor;
+};
+// Thread blocks update their elements in any order, so no array that the step writes may overlap another one. Sorts the spans.
+hylo_status check_spans(Span* spans, size_t n);
 
 inline size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 

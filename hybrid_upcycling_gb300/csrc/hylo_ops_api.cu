@@ -10,6 +10,22 @@
 
 using namespace hylo;
 
+namespace hylo {
+hylo_status check_spans(Span* spans, size_t n) {
+  std::sort(spans, spans + n, [](const Span& a, const Span& b) { return a.begin < b.begin; });
+  Span any{}, written{};  // of those so far, the ones that reach furthest
+  for (size_t i = 0; i < n; ++i) {
+    const Span& s = spans[i];
+    const Span& before = s.written ? any : written;
+    if (s.begin < before.end)
+      return fail(HYLO_ERR_DIM, "arrays of tensors %d and %d overlap, and the step writes to them", before.tensor, s.tensor);
+    if (s.end > any.end) any = s;
+    if (s.written && s.end > written.end) written = s;
+  }
+  return HYLO_OK;
+}
+}  // namespace hylo
+
 namespace {
 
 bool dtype_ok(int d) { return d == HYLO_F32 || d == HYLO_BF16 || d == HYLO_F16; }
@@ -149,14 +165,6 @@ hylo_status check_head(const uint16_t* h, const uint16_t* W, int64_t N, int64_t 
   return HYLO_OK;
 }
 
-// An array of an optimizer step, [begin, end).
-struct Span {
-  uintptr_t begin, end;
-  bool written;
-  int tensor;
-};
-
-// Thread blocks update their elements in any order, so no array that the step writes may overlap another one.
 hylo_status check_apart(const hylo_adamw_tensor* tensors, int count, size_t param_bytes, size_t grad_bytes, size_t state_bytes) {
   const std::unique_ptr<Span[]> spans(new (std::nothrow) Span[7 * static_cast<size_t>(count)]);
   if (!spans) return fail(HYLO_ERR_CUDA, "no host memory for %d tensors", count);
@@ -179,17 +187,7 @@ hylo_status check_apart(const hylo_adamw_tensor* tensors, int count, size_t para
       add(t.v_exp, (k + 255) / 256, true);
     }
   }
-  std::sort(spans.get(), spans.get() + n, [](const Span& a, const Span& b) { return a.begin < b.begin; });
-  Span any{}, written{};  // of those so far, the ones that reach furthest
-  for (size_t i = 0; i < n; ++i) {
-    const Span& s = spans[i];
-    const Span& before = s.written ? any : written;
-    if (s.begin < before.end)
-      return fail(HYLO_ERR_DIM, "arrays of tensors %d and %d overlap, and the step writes to them", before.tensor, s.tensor);
-    if (s.end > any.end) any = s;
-    if (s.written && s.end > written.end) written = s;
-  }
-  return HYLO_OK;
+  return check_spans(spans.get(), n);
 }
 
 bool norm_sizes_ok(int64_t N, int64_t d) { return N >= 1 && N <= 0x7fffffffLL && d >= 1 && d <= (int64_t(1) << 20); }

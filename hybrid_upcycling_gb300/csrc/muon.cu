@@ -1,0 +1,365 @@
+// The elementwise kernels around the Newton-Schulz products of orthogonalised updates: momentum and sums of squares, the scaled
+// update as fp16 panels, and the parameters' step (or the result) from the last X. HBM bounds all three; the layout of the
+// workspace is in muon.h.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cmath>
+
+#include "hylo_ops_internal.h"
+#include "muon.h"
+
+namespace hylo {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+__device__ __forceinline__ void from_float(float x, float* y) { *y = x; }
+__device__ __forceinline__ void from_float(float x, __nv_bfloat16* y) { *y = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void from_float(float x, __half* y) { *y = __float2half_rn(x); }
+
+template <typename T>
+struct alignas(16) Pack16 {
+  T v[16 / sizeof(T)];
+};
+
+// Eight elements at p, `left` of which exist; missing ones are 0.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int left, bool vec, float* z) {
+  if (vec && left >= 8) {
+    constexpr int E = 16 / sizeof(T);
+#pragma unroll
+    for (int k = 0; k < 8 / E; ++k) {
+      const Pack16<T> a = reinterpret_cast<const Pack16<T>*>(p)[k];
+#pragma unroll
+      for (int j = 0; j < E; ++j) z[k * E + j] = to_float(a.v[j]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z[j] = j < left ? to_float(p[j]) : 0.f;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, int left, bool vec, const float* z) {
+  if (vec && left >= 8) {
+    constexpr int E = 16 / sizeof(T);
+#pragma unroll
+    for (int k = 0; k < 8 / E; ++k) {
+      Pack16<T> a;
+#pragma unroll
+      for (int j = 0; j < E; ++j) from_float(z[k * E + j], &a.v[j]);
+      reinterpret_cast<Pack16<T>*>(p)[k] = a;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < left) from_float(z[j], p + j);
+  }
+}
+
+// The factor on the gradients; false if the step is skipped.
+__device__ __forceinline__ bool gradient_factor(const MuonHyper& h, float& gs) {
+  gs = h.grad_scale;
+  if (h.norm != nullptr) {
+    const float norm = h.norm[0];
+    if (!isfinite(norm)) return false;
+    gs *= fminf(1.f, h.max_norm / (norm * fabsf(h.grad_scale) + 1e-6f));
+  }
+  return true;
+}
+
+__device__ __forceinline__ uint32_t mix32(uint32_t x) {  // the finaliser of MurmurHash3
+  x = (x ^ (x >> 16)) * 0x85EBCA6Bu;
+  x = (x ^ (x >> 13)) * 0xC2B2AE35u;
+  return x ^ (x >> 16);
+}
+__device__ __forceinline__ uint32_t random1(uint32_t seed, uint64_t c) {
+  return mix32(static_cast<uint32_t>(c) + mix32(seed + 0x9E3779B9u * (static_cast<uint32_t>(c >> 32) + 1u)));
+}
+
+template <uint32_t MuonMat::* START>
+__device__ __forceinline__ int find_mat(const MuonTable& tab, uint32_t b) {
+  int lo = 0, hi = tab.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (tab.t[mid].*START <= b)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+// The update before it is orthogonalised, from the gradient (scaled) and the momentum after this step's.
+__device__ __forceinline__ float update_of(const MuonHyper& h, float g, float m) {
+  return h.nesterov ? fmaf(h.mu, m, h.one_minus_mu * g) : m;
+}
+
+__device__ __forceinline__ float block_sum(float v, float* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) s += red[i];
+  return s;
+}
+
+// Momentum, and the sums of squares of the update. Squares of very small and very large values leave fp32's range, so there are
+// three sums, of x 2^80, x and x 2^-80, of which square_sum() takes one that did not. A thread block's pieces of
+// eight elements of a row lie `parts` blocks apart, whatever the row stride, so that results do not depend on it.
+constexpr float kUp = 0x1p80f, kDown = 0x1p-80f;
+template <typename T>
+__global__ void __launch_bounds__(kThreads) muon_sums_kernel(const __grid_constant__ MuonTable tab, const MuonHyper h) {
+  __shared__ float red[kThreads / 32];
+  float gs = 1.f;
+  if (h.muon && !gradient_factor(h, gs)) return;
+  const MuonMat& t = tab.t[find_mat<&MuonMat::sum0>(tab, blockIdx.x)];
+  const uint32_t per_row = static_cast<uint32_t>(t.cols + 7) / 8;
+  const int64_t pieces = static_cast<int64_t>(per_row) * t.rows;
+  const bool vec = t.src_vec != 0;
+  const T* src = static_cast<const T*>(t.src);
+  float sum[kMuonSums] = {0.f, 0.f, 0.f};
+  for (int64_t piece = static_cast<int64_t>(blockIdx.x - t.sum0) * kThreads + threadIdx.x; piece < pieces;
+       piece += static_cast<int64_t>(t.parts) * kThreads) {
+    const int64_t r = pieces < (int64_t(1) << 32) ? static_cast<uint32_t>(piece) / per_row : piece / per_row;
+    const int c = static_cast<int>(piece - r * per_row) * 8, left = min(8, t.cols - c);
+    float x[8];
+    load8(src + r * t.ld + c, left, vec, x);
+    if (h.muon) {  // gradients and momentum have no gaps
+      float m[8];
+      load8(t.mom + r * t.ld + c, left, vec, m);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float g = x[j] * gs;
+        m[j] = fmaf(h.mu, m[j], h.one_minus_mu * g);
+        x[j] = update_of(h, g, m[j]);
+      }
+      store8(t.mom + r * t.ld + c, left, vec, m);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float up = x[j] * kUp, down = x[j] * kDown;
+      sum[0] = fmaf(up, up, sum[0]);
+      sum[1] = fmaf(x[j], x[j], sum[1]);
+      sum[2] = fmaf(down, down, sum[2]);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kMuonSums; ++k) {
+    const float s = block_sum(sum[k], red);
+    if (threadIdx.x == 0) h.sums[static_cast<int64_t>(blockIdx.x) * kMuonSums + k] = s;
+  }
+}
+
+// Two factors whose product is scale / (norm + eps): one alone could leave fp32's range. NaN if the norm is not finite.
+__device__ __forceinline__ float2 scale_factors(const MuonMat& t, const MuonHyper& h, double* red) {
+  double s[kMuonSums] = {0.0, 0.0, 0.0};
+  for (uint32_t i = threadIdx.x; i < t.parts; i += kThreads) {
+    const float* a = h.sums + static_cast<int64_t>(t.sum0 + i) * kMuonSums;
+#pragma unroll
+    for (int k = 0; k < kMuonSums; ++k) s[k] += static_cast<double>(a[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < kMuonSums; ++k) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
+    if ((threadIdx.x & 31) == 0) red[k * (kThreads / 32) + (threadIdx.x >> 5)] = s[k];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kMuonSums; ++k) {
+    s[k] = 0.0;
+    for (int i = 0; i < kThreads / 32; ++i) s[k] += red[k * (kThreads / 32) + i];
+  }
+  // all sums of magnitudes below 2^-20: x 2^80 stays below 2^60 and loses nothing; inf: x 2^-80 does not overflow
+  const double norm = s[1] < 0x1p-40 ? sqrt(s[0]) * 0x1p-80 : isfinite(s[1]) ? sqrt(s[1]) : sqrt(s[2]) * 0x1p80;
+  const double f = norm > 0.0 || h.eps > 0.f ? static_cast<double>(h.scale_in) / (norm + h.eps) : 0.0;
+  if (!isfinite(norm)) return make_float2(__int_as_float(0x7fffffff), 1.f);
+  const double first = f > 0x1p100 ? 0x1p100 : f < 0x1p-100 ? 0x1p-100 : 1.0;
+  return make_float2(static_cast<float>(f / first), static_cast<float>(first));
+}
+
+__device__ __forceinline__ void put_panel(const MuonHyper& h, const MuonMat& t, size_t at, const float* u, float2 f) {
+  uint32_t hi[4], lo[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float a = u[2 * j] * f.y * f.x, b = u[2 * j + 1] * f.y * f.x;
+    const __half2 p = __floats2half2_rn(a, b);
+    const float2 r = __half22float2(p);
+    const __half2 q = __floats2half2_rn(a - r.x, b - r.y);
+    hi[j] = *reinterpret_cast<const uint32_t*>(&p);
+    lo[j] = *reinterpret_cast<const uint32_t*>(&q);
+  }
+  *reinterpret_cast<uint4*>(h.ws + static_cast<size_t>(t.x) * 128 + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+  *reinterpret_cast<uint4*>(h.ws + static_cast<size_t>(t.lo) * 128 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+}
+
+// X's panels from the scaled update, with their zero padding: 64 x 64 blocks of the matrix, kFillBlocks a thread block along its
+// rows; a tall matrix is transposed through shared memory.
+constexpr int kFillBlocks = 8;
+template <typename T>
+__global__ void __launch_bounds__(kThreads) muon_fill_kernel(const __grid_constant__ MuonTable tab, const MuonHyper h) {
+  __shared__ double red[kMuonSums * (kThreads / 32)];
+  __shared__ float tile[64][65];
+  const MuonMat& t = tab.t[find_mat<&MuonMat::fill0>(tab, blockIdx.x)];
+  float gs = 1.f;
+  const bool skipped = h.muon && !gradient_factor(h, gs);
+  float2 f = make_float2(0.f, 0.f);
+  if (!skipped) f = scale_factors(t, h, red);
+  const int down = t.tall ? t.np : t.mp, across = t.tall ? t.mp : t.np;  // padded rows and columns of the matrix
+  const int wide = across / 64, local = static_cast<int>(blockIdx.x - t.fill0);
+  const int per = (wide + kFillBlocks - 1) / kFillBlocks;
+  const int br = local / per, bc0 = (local - br * per) * kFillBlocks;
+  if (br * 64 >= down) return;
+  for (int bc = bc0; bc < min(wide, bc0 + kFillBlocks); ++bc) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int rr = half * 32 + static_cast<int>(threadIdx.x >> 3), cc = static_cast<int>(threadIdx.x & 7) * 8;
+      const int r = br * 64 + rr, c = bc * 64 + cc;
+      float u[8];
+      const int left = r < t.rows && !skipped ? max(0, min(8, t.cols - c)) : 0;
+      load8(static_cast<const T*>(t.src) + static_cast<int64_t>(r) * t.ld + c, left, t.src_vec != 0, u);
+      if (h.muon) {
+        float m[8];
+        load8(t.mom + static_cast<int64_t>(r) * t.ld + c, left, t.src_vec != 0, m);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = update_of(h, u[j] * gs, m[j]);
+      }
+      if (t.tall) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) tile[rr][cc + j] = u[j];
+      } else {
+        put_panel(h, t, (static_cast<size_t>(bc) * t.mp + r) * 128 + cc * 2, u, f);
+      }
+    }
+    if (t.tall) {
+      __syncthreads();
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int xr = half * 32 + static_cast<int>(threadIdx.x >> 3), xc = static_cast<int>(threadIdx.x & 7) * 8;
+        float u[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = tile[xc + j][xr];
+        put_panel(h, t, (static_cast<size_t>(br) * t.mp + bc * 64 + xr) * 128 + xc * 2, u, f);
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// The result, or the parameters' step, from the last X: O = X unscale.
+template <typename T, bool MUON, bool MASTER>
+__global__ void __launch_bounds__(kThreads) muon_apply_kernel(const __grid_constant__ MuonTable tab, const MuonHyper h) {
+  __shared__ float tile[64][65];
+  const MuonMat& t = tab.t[find_mat<&MuonMat::apply0>(tab, blockIdx.x)];
+  float gs = 1.f;
+  if (MUON && !gradient_factor(h, gs)) return;
+  const int wide = (t.cols + 63) / 64, local = static_cast<int>(blockIdx.x - t.apply0);
+  const int per = (wide + kFillBlocks - 1) / kFillBlocks;
+  const int br = local / per, bc0 = (local - br * per) * kFillBlocks;
+  for (int bc = bc0; bc < min(wide, bc0 + kFillBlocks); ++bc) {
+    if (t.tall) {
+      __syncthreads();
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int xr = half * 32 + static_cast<int>(threadIdx.x >> 3), xc = static_cast<int>(threadIdx.x & 7) * 8;
+        float u[8];
+        load8(reinterpret_cast<const __half*>(h.ws + static_cast<size_t>(t.fin) * 128 +
+                                              (static_cast<size_t>(br) * t.mp + bc * 64 + xr) * 128 + xc * 2), 8, true, u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) tile[xc + j][xr] = u[j];
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int rr = half * 32 + static_cast<int>(threadIdx.x >> 3), cc = static_cast<int>(threadIdx.x & 7) * 8;
+      const int r = br * 64 + rr, c = bc * 64 + cc;
+      const int left = r < t.rows ? max(0, min(8, t.cols - c)) : 0;
+      if (left == 0) continue;
+      float o[8];
+      if (t.tall) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = tile[rr][cc + j];
+      } else {
+        load8(reinterpret_cast<const __half*>(h.ws + static_cast<size_t>(t.fin) * 128 +
+                                              (static_cast<size_t>(bc) * t.mp + r) * 128 + cc * 2), 8, true, o);
+      }
+      const int64_t i = static_cast<int64_t>(r) * t.cols + c;
+      const bool vec = t.dst_vec != 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] *= h.unscale;
+      if (MUON) {
+        float w[8];
+        if (MASTER)
+          load8(t.master + i, left, vec, w);
+        else
+          load8(static_cast<const T*>(t.dst) + i, left, vec, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = fmaf(w[j], t.decay, -t.step * o[j]);
+        if (MASTER) store8(t.master + i, left, vec, o);
+        if (!MASTER && sizeof(T) == 2) {  // rounded up with the probability of the part cut off
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t bits = random1(h.seed, t.pos + static_cast<uint64_t>(i + j)) * 0x9E3779B1u;
+            if (isfinite(o[j])) o[j] = __uint_as_float((__float_as_uint(o[j]) + (bits >> 16)) & 0xffff0000u);
+          }
+        }
+      }
+      store8(static_cast<T*>(t.dst) + i, left, vec, o);
+    }
+  }
+}
+
+uint32_t blocks(int rows, int cols) {
+  return static_cast<uint32_t>((rows + 63) / 64) * static_cast<uint32_t>(((cols + 63) / 64 + kFillBlocks - 1) / kFillBlocks);
+}
+
+}  // namespace
+
+uint32_t muon_fill_blocks(int mp, int np, bool tall) { return tall ? blocks(np, mp) : blocks(mp, np); }
+uint32_t muon_apply_blocks(int rows, int cols) { return blocks(rows, cols); }
+
+cudaError_t launch_muon_sums(const MuonTable& t, const MuonHyper& h, int dtype, uint32_t ctas, cudaStream_t stream) {
+  if (dtype == HYLO_F32)
+    muon_sums_kernel<float><<<ctas, kThreads, 0, stream>>>(t, h);
+  else if (dtype == HYLO_BF16)
+    muon_sums_kernel<__nv_bfloat16><<<ctas, kThreads, 0, stream>>>(t, h);
+  else
+    muon_sums_kernel<__half><<<ctas, kThreads, 0, stream>>>(t, h);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_muon_fill(const MuonTable& t, const MuonHyper& h, int dtype, uint32_t ctas, cudaStream_t stream) {
+  if (dtype == HYLO_F32)
+    muon_fill_kernel<float><<<ctas, kThreads, 0, stream>>>(t, h);
+  else if (dtype == HYLO_BF16)
+    muon_fill_kernel<__nv_bfloat16><<<ctas, kThreads, 0, stream>>>(t, h);
+  else
+    muon_fill_kernel<__half><<<ctas, kThreads, 0, stream>>>(t, h);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_muon_apply(const MuonTable& t, const MuonHyper& h, int dtype, bool masters, uint32_t ctas, cudaStream_t stream) {
+  if (!h.muon) {
+    if (dtype == HYLO_BF16)
+      muon_apply_kernel<__nv_bfloat16, false, false><<<ctas, kThreads, 0, stream>>>(t, h);
+    else
+      muon_apply_kernel<__half, false, false><<<ctas, kThreads, 0, stream>>>(t, h);
+  } else if (dtype == HYLO_F32) {
+    muon_apply_kernel<float, true, false><<<ctas, kThreads, 0, stream>>>(t, h);
+  } else if (masters) {
+    muon_apply_kernel<__nv_bfloat16, true, true><<<ctas, kThreads, 0, stream>>>(t, h);
+  } else {
+    muon_apply_kernel<__nv_bfloat16, true, false><<<ctas, kThreads, 0, stream>>>(t, h);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace hylo

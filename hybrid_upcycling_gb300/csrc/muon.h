@@ -1,0 +1,90 @@
+// Shared by the host side and the kernels of the orthogonalised updates (muon.cu, muon_gemm.cu): the layout of a group of
+// matrices in the workspace.
+//
+// A group's matrices live in the workspace as fp16 in panels of 64 columns: element (r, c) of a matrix whose panels have `mp`
+// rows, with `base` its first row of 128 bytes, lies in row base + (c / 64) mp + r, column c % 64. So the whole workspace is
+// one tensor of 64 columns for the TMA loads, and a block of 64 rows and 64 columns, 8 KiB in one piece, serves as an operand
+// whose rows are summed over as well as one whose columns are. X has at most as many rows as columns (a tall matrix is
+// transposed) and is padded with zeros to multiples of 256; the padding stays zero in every product.
+#pragma once
+
+#include <cstdint>
+
+#include "hylo_internal.h"
+
+namespace hylo {
+
+constexpr int kMuonMats = 64;     // matrices of a group at most
+constexpr int kMuonParts = 1024;  // partial sums of squares of a matrix at most
+constexpr int kMuonSums = 3;      // of magnitudes near 2^-80, 1 and 2^80
+
+// One matrix as the elementwise kernels see it.
+struct MuonMat {
+  const void* src;  // the matrix (orthogonalize) or the gradient
+  int64_t ld;       // its row stride
+  float* mom;       // momentum
+  void* dst;        // the result, or the parameter
+  float* master;
+  uint64_t pos;     // position of element 0 in the list (random bits)
+  float decay, step;  // w <- decay w - step O
+  int rows, cols;
+  int m, n;         // X is [m, n], m <= n: the matrix, or its transpose if tall
+  int mp, np;       // rounded up to multiples of 256
+  int tall, src_vec, dst_vec;
+  uint32_t x, lo, fin;      // first 128-byte rows of X's two terms, and of the last X
+  uint32_t sum0, parts;     // first partial sum, and how many
+  uint32_t fill0, apply0;   // first thread blocks of the kernels that fill X and apply the result
+};
+struct MuonTable {
+  MuonMat t[kMuonMats];
+  int count;
+};
+
+// The same as the products see it.
+struct MuonGemmMat {
+  uint32_t x[2], lo, a, b;  // first 128-byte rows
+  int mt, nt;               // 256-row tiles of m and n
+  int kn, km;               // 64-deep k-blocks of n and m
+  int sym0, rect0;          // first 256 x 256 tiles of the symmetric products and of B X
+};
+// Products are summed by the tensor cores over at most this many 64-deep k-blocks at a time.
+constexpr int kMuonDepth = 128;
+constexpr int64_t kMuonScratch = int64_t(128) * 256 * 4;  // bytes of a CTA's fp32 sums in between
+enum : int { kMuonGram = 0, kMuonPoly = 1, kMuonApply = 2 };
+struct MuonGemmParams {
+  MuonGemmMat t[kMuonMats];
+  int count;
+  int tiles;      // 256 x 256 tiles
+  int cur;        // which of x[2] is read
+  float acc;      // factor on the sum of products
+  float add;      // factor on A (kMuonPoly) or X (kMuonApply)
+  int want_lo;    // kMuonApply: write the second term of X too
+  uint8_t* ws;
+  uint8_t* scratch;  // kMuonScratch bytes for each CTA, where some sum is longer than kMuonDepth
+  WaitCtl ctl;
+};
+cudaError_t muon_gemm_prepare(int* max_clusters);
+cudaError_t launch_muon_gemm(int phase, const CUtensorMap& ws, const MuonGemmParams& p, int clusters, cudaStream_t stream);
+
+struct MuonHyper {
+  int muon;        // momentum and parameters, not just the matrices
+  int nesterov;
+  float mu, one_minus_mu;
+  float grad_scale;
+  const float* norm;  // or null
+  float max_norm;
+  float eps;
+  float scale_in;  // X's scale of the first step, a power of two
+  float unscale;   // 1 / that of the last X
+  uint32_t seed;
+  uint8_t* ws;
+  float* sums;     // [parts][kMuonSums] of the group
+};
+// Thread blocks of the kernels that fill X and apply the result, for one matrix.
+uint32_t muon_fill_blocks(int mp, int np, bool tall);
+uint32_t muon_apply_blocks(int rows, int cols);
+cudaError_t launch_muon_sums(const MuonTable& t, const MuonHyper& h, int dtype, uint32_t ctas, cudaStream_t stream);
+cudaError_t launch_muon_fill(const MuonTable& t, const MuonHyper& h, int dtype, uint32_t ctas, cudaStream_t stream);
+cudaError_t launch_muon_apply(const MuonTable& t, const MuonHyper& h, int dtype, bool masters, uint32_t ctas, cudaStream_t stream);
+
+}  // namespace hylo

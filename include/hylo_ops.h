@@ -1,13 +1,13 @@
 /*
  * hylo_ops.h — C ABI of the operators that stand beside the distillation losses of hylo_kl.h
- * (GB300, sm_103a): log-probabilities of given tokens, the AdamW step that applies the
- * gradients, and the norms of the hidden states.
+ * (GB300, sm_103a): log-probabilities of given tokens, the AdamW and Muon steps that apply the
+ * gradients, orthogonalised matrices, and the norms of the hidden states.
  *
  * Conventions are those of hylo_kl.h: device pointers owned by the caller unless a parameter
  * says otherwise, no allocation by the library, calls asynchronous on `stream`, a status code
  * for argument, architecture and launch errors (hylo_kl_last_error() has the text), no
  * fallback. Calls may be captured into a CUDA graph once one call has run eagerly on the device, all
- * but hylo_adamw_step.
+ * but hylo_adamw_step and hylo_muon_step.
  */
 #ifndef HYLO_OPS_H
 #define HYLO_OPS_H
@@ -182,6 +182,52 @@ hylo_status hylo_norm_backward(const void* s, int dtype, int64_t N, int64_t d, i
                                int gain_dtype, int rms, const float* stats, const void* dy, int64_t lddy,
                                const void* dsum, int64_t ldds, void* dx, void* dweight, void* dbias, void* workspace,
                                size_t workspace_bytes, cudaStream_t stream);
+
+/* Orthogonalised matrices. Each matrix M of the list (HOST array, not kept) is scaled to X = M / (|M| + eps), |M| its Frobenius
+ * norm, and `steps` Newton-Schulz steps with coefficients[3 k ..] = (a, b, c) of step k (HOST array [steps][3]) follow:
+ *     A = X X^T,  X <- a X + (b A + c A^2) X
+ * which leaves M's singular vectors and takes each singular value s to a s + b s^3 + c s^5, step by step (of a matrix with
+ * more rows than columns X is the transpose). x: [rows, cols] of `dtype` (fp32, bf16 or fp16), row stride ld >= cols; out:
+ * [rows, cols] contiguous, of out_dtype (HYLO_BF16 or HYLO_F16). rows, cols <= 2^20, the shorter at most 16384; a
+ * matrix without elements is skipped. 1 <= steps <= 32. Coefficients with which singular values could pass 2^20 are refused.
+ * A matrix of zeros gives zeros; NaN or infinity anywhere in a matrix makes that whole result NaN, and leaves the others alone. No
+ * output may overlap anything else. workspace: 256-byte aligned, hylo_orthogonalize_workspace_bytes() of the same list
+ * (0 for invalid sizes; 6 bytes per element and 4 per element of A, padded, for matrices of together 512 MiB or one larger
+ * one), not shared with a call still running on another stream.
+ * Accuracy: products of fp16 numbers scaled by powers of two, fp32 sums, X as two fp16 terms where it is added: 1e-3 to 2e-3 of
+ * the result's norm after five steps with the usual coefficients. Deterministic, and independent of the other matrices in the list. */
+typedef struct {
+  const void* x;
+  void* out;
+  int64_t rows, cols, ld;
+} hylo_orth_matrix;
+size_t hylo_orthogonalize_workspace_bytes(const hylo_orth_matrix* matrices, int count);
+hylo_status hylo_orthogonalize(const hylo_orth_matrix* matrices, int count, int dtype, int out_dtype, int steps,
+                               const double* coefficients, double eps, void* workspace, size_t workspace_bytes,
+                               cudaStream_t stream);
+
+/* One Muon step over `count` matrices (HOST array, not kept), all contiguous:
+ *     g' = g * grad_scale * c,  c = min(1, max_norm / (norm[0] * |grad_scale| + 1e-6))  (1 without norm)
+ *     m <- momentum m + (1 - momentum) g',   u = momentum m + (1 - momentum) g' (nesterov != 0) or m
+ *     w <- w (1 - lr weight_decay) - lr scale O(u),   O as in hylo_orthogonalize (its accuracy is that of the step)
+ * param, grad, master, momentum: as param, grad, master and m of hylo_adamw_step with 32-bit states, with the same rules for
+ * masters, for overlaps (HYLO_ERR_DIM), for a norm that is not finite (nothing is written) and for capture (HYLO_ERR_CAPTURE),
+ * and the same random bits where a bf16 param without master is rounded. Sizes, steps, coefficients, eps and workspace
+ * as in hylo_orthogonalize. momentum in [0, 1). */
+typedef struct {
+  void* param;
+  const void* grad;
+  float* master;
+  float* momentum;
+  int64_t rows, cols;
+  double lr;
+  double weight_decay;
+  double scale;
+} hylo_muon_tensor;
+size_t hylo_muon_workspace_bytes(const hylo_muon_tensor* tensors, int count);
+hylo_status hylo_muon_step(const hylo_muon_tensor* tensors, int count, int param_dtype, int grad_dtype, double momentum,
+                           int nesterov, int steps, const double* coefficients, double eps, float grad_scale, const float* norm,
+                           float max_norm, uint32_t seed, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -117,3 +117,57 @@ def norm_grad(s, weight, eps: float, rms: bool, dy):
     dc = g * r + dvar * 2 * c / d                       # var = mean(c^2)
     ds = dc if rms else dc - dc.mean(axis=1, keepdims=True)
     return ds, (dy * c * r).sum(axis=0), dy.sum(axis=0)
+
+
+# ------------------------------------------------------------------------------- orthogonalised updates
+MUON = (3.4445, -4.7750, 2.0315)
+
+
+def orthogonalize(x, coefficients=(MUON,) * 5, eps: float = 1e-7) -> np.ndarray:
+    """Newton-Schulz steps from x / (|x| + eps), one (a, b, c) a step; a matrix of zeros gives zeros."""
+    x = np.asarray(x, np.float64)
+    norm = np.sqrt((x ** 2).sum())
+    if norm == 0:
+        return np.zeros_like(x)
+    x = x / (norm + eps)
+    if x.shape[0] > x.shape[1]:
+        return _steps(x.T, coefficients).T
+    return _steps(x, coefficients)
+
+
+def _steps(x, coefficients):
+    for a, b, c in coefficients:
+        g = x @ x.T
+        x = a * x + (b * g + c * (g @ g)) @ x
+    return x
+
+
+def orthogonalize_fp16(x, coefficients=(MUON,) * 5, eps: float = 1e-7) -> np.ndarray:
+    """The same with the roundings of the fp16 scheme: X as two fp16 terms, the products with the first; A and
+    B = b A + c A^2 in fp16, all scaled far from fp16's limits; sums exact."""
+    def half(v):  # fp16 of v 2^14 (entries are at most about 3)
+        return (v * 2.0 ** 14).astype(np.float16).astype(np.float64) / 2.0 ** 14
+
+    x = np.asarray(x, np.float64)
+    norm = np.sqrt((x ** 2).sum())
+    if norm == 0:
+        return np.zeros_like(x)
+    x = x / (norm + eps)
+    tall = x.shape[0] > x.shape[1]
+    if tall:
+        x = x.T
+    for a, b, c in coefficients:
+        hi = half(x)
+        lo = half(x - hi)
+        g = half(hi @ hi.T)
+        x = a * (hi + lo) + half(b * g + c * (g @ g)) @ hi
+    x = half(x)
+    return x.T if tall else x
+
+
+def muon(w, g, m, *, lr, momentum, nesterov, weight_decay, scale, coefficients=(MUON,) * 5, eps=1e-7):
+    """One step in fp64: (w, m)."""
+    w, g, m = (np.asarray(t, np.float64) for t in (w, g, m))
+    m = momentum * m + (1 - momentum) * g
+    u = momentum * m + (1 - momentum) * g if nesterov else m
+    return w * (1 - lr * weight_decay) - lr * scale * orthogonalize(u, coefficients, eps), m
