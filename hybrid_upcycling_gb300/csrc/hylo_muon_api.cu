@@ -12,7 +12,7 @@ using namespace hylo;
 namespace {
 
 constexpr int64_t kMaxSide = int64_t(1) << 20, kMaxShort = 16384;
-constexpr int kMaxSteps = 32;
+constexpr int kMaxSteps = kMuonStepsMax;
 // Matrices that go through the products together: enough tiles for every SM, and no more memory than that takes.
 constexpr int64_t kGroupRows = (int64_t(512) << 20) / 128;
 
@@ -59,7 +59,9 @@ struct Group {
   int first, last, mats;
   int64_t rows, parts;
   bool deep;  // some sum is longer than the tensor cores take at a time
-  size_t scratch_at() const { return static_cast<size_t>(rows) * 128 + round256(static_cast<size_t>(parts) * kMuonSums * sizeof(float)); }
+  size_t sums_at() const { return static_cast<size_t>(rows) * 128; }
+  size_t ctrl_at() const { return sums_at() + round256(static_cast<size_t>(parts) * kMuonSums * sizeof(float)); }
+  size_t scratch_at() const { return ctrl_at() + round256(kMuonCtrlWords * sizeof(unsigned)); }
   size_t bytes() const { return scratch_at() + (deep ? 2 * kMaxClusters * kMuonScratch : 0); }
 };
 template <typename T>
@@ -147,6 +149,10 @@ hylo_status plan_steps(int steps, const double* coefficients, double eps, Steps*
   return HYLO_OK;
 }
 
+// 256 x 256 tiles read fewer operands per product, 256 x 128 ones leave fewer SMs idle: the rounds of tiles decide, one of
+// narrow tiles counting 5/8 of one of wide tiles.
+int halve(int64_t tiles, int clusters) { return 5 * cdiv(2 * tiles, clusters) < 8 * cdiv(tiles, clusters) ? 1 : 0; }
+
 bool aligned_rows(const void* p, int64_t ld, uintptr_t bytes) { return aligned(p, 16) && ld * bytes % 16 == 0; }
 
 // All launches of one list. dtype: of the matrices or gradients; out_dtype: of the results or parameters.
@@ -163,11 +169,10 @@ hylo_status run(const T* list, int count, int dtype, int out_dtype, bool masters
   for (int i = 0; i < count;) {
     const Group group = next_group(list, count, i);
     MuonTable tab;
-    MuonGemmParams p;
-    tab.count = p.count = 0;
+    tab.count = 0;
+    MuonPipe p{};
     int64_t row = 0;
-    uint32_t sums = 0, fill = 0, apply = 0;
-    int sym = 0, rect = 0;
+    uint32_t sums = 0, fill = 0;
     for (; i < group.last; ++i) {
       const Item x = item_of(list[i]);
       const uint64_t start = pos;
@@ -175,58 +180,50 @@ hylo_status run(const T* list, int count, int dtype, int out_dtype, bool masters
       if (x.rows == 0 || x.cols == 0) continue;
       const Shape d = shape_of(x.rows, x.cols);
       MuonMat& t = tab.t[tab.count++];
-      MuonGemmMat& g = p.t[p.count++];
-      g.x[0] = static_cast<uint32_t>(row);
-      g.x[1] = static_cast<uint32_t>(row + d.x_rows);
-      g.lo = static_cast<uint32_t>(row + 2 * d.x_rows);
-      g.a = static_cast<uint32_t>(row + 3 * d.x_rows);
-      g.b = static_cast<uint32_t>(row + 3 * d.x_rows + d.a_rows);
-      row += rows_of(d);
-      g.mt = static_cast<int>(d.mp / 256);
-      g.nt = static_cast<int>(d.np / 256);
-      g.kn = static_cast<int>(cdiv(d.n, 64));
-      g.km = static_cast<int>(cdiv(d.m, 64));
-      g.sym0 = sym;
-      g.rect0 = rect;
-      sym += g.mt * (g.mt + 1) / 2;
-      rect += g.mt * g.nt;
       t = MuonMat{};
       t.src = x.src, t.ld = x.ld, t.mom = x.mom, t.dst = x.dst, t.master = x.master, t.pos = start;
       t.decay = static_cast<float>(x.decay), t.step = static_cast<float>(x.step);
       t.rows = static_cast<int>(x.rows), t.cols = static_cast<int>(x.cols);
-      t.m = static_cast<int>(d.m), t.n = static_cast<int>(d.n), t.mp = static_cast<int>(d.mp), t.np = static_cast<int>(d.np);
+      t.mt = static_cast<int>(d.mp / 256), t.nt = static_cast<int>(d.np / 256);
+      t.kn = static_cast<int>(cdiv(d.n, 64)), t.km = static_cast<int>(cdiv(d.m, 64));
       t.tall = x.rows > x.cols;
       t.src_vec = aligned_rows(x.src, x.ld, bytes_of(dtype)) && (!x.mom || aligned_rows(x.mom, x.cols, 4));
       t.dst_vec = aligned_rows(x.dst, x.cols, bytes_of(out_dtype)) && (!x.master || aligned_rows(x.master, x.cols, 4));
-      t.x = g.x[0], t.lo = g.lo, t.fin = g.x[s.count & 1];
-      t.sum0 = sums, t.parts = static_cast<uint32_t>(d.parts), t.fill0 = fill, t.apply0 = apply;
+      t.x[0] = static_cast<uint32_t>(row);
+      t.x[1] = static_cast<uint32_t>(row + d.x_rows);
+      t.lo = static_cast<uint32_t>(row + 2 * d.x_rows);
+      t.a = static_cast<uint32_t>(row + 3 * d.x_rows);
+      t.b = static_cast<uint32_t>(row + 3 * d.x_rows + d.a_rows);
+      t.sum0 = sums, t.parts = static_cast<uint32_t>(d.parts), t.fill0 = fill;
+      t.sym0 = p.sym, t.rect0 = p.rect;
+      row += rows_of(d);
       sums += t.parts;
-      fill += muon_fill_blocks(t.mp, t.np, t.tall != 0);
-      apply += muon_apply_blocks(t.rows, t.cols);
+      fill += muon_fill_blocks(t);
+      p.sym += t.mt * (t.mt + 1) / 2;
+      p.rect += t.mt * t.nt;
     }
     if (tab.count == 0) continue;
-    CUtensorMap map;
-    if ((st = make_map(&map, ws, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 64, row, 128, 64, 64)) != HYLO_OK) return st;
-    h.sums = reinterpret_cast<float*>(h.ws + static_cast<size_t>(row) * 128);
-    p.ws = h.ws;
+    CUtensorMap load, part;
+    if ((st = make_map(&load, ws, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 64, row, 128, 64, 64)) != HYLO_OK ||
+        (st = make_map(&part, ws, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 64, row, 128, 64, 32)) != HYLO_OK)
+      return st;
+    h.sums = reinterpret_cast<float*>(h.ws + group.sums_at());
+    h.ctrl = p.ctrl = reinterpret_cast<unsigned*>(h.ws + group.ctrl_at());
     p.scratch = h.ws + group.scratch_at();
     p.ctl = WaitCtl{dev->status, wait_limit_ns()};
+    p.steps = s.count;
+    p.sym_half = halve(p.sym, dev->muon_clusters), p.rect_half = halve(p.rect, dev->muon_clusters);
+    for (int k = 0; k < s.count; ++k) {
+      const double *c = s.k + 3 * k, x = s.x[k], a = s.a[k], b = s.b[k], next = s.x[k + 1];
+      p.acc[k][kMuonGram] = static_cast<float>(a / (x * x));
+      p.acc[k][kMuonPoly] = static_cast<float>(c[2] * b / (a * a)), p.add[k][kMuonPoly] = static_cast<float>(c[1] * b / a);
+      p.acc[k][kMuonApply] = static_cast<float>(next / (b * x)), p.add[k][kMuonApply] = static_cast<float>(c[0] * next / x);
+    }
+    const int out = !h.muon ? out_dtype == HYLO_BF16 ? kMuonOutBf16 : kMuonOutF16
+                            : out_dtype == HYLO_F32 ? kMuonParamF32 : masters ? kMuonParamMaster : kMuonParamBf16;
     cudaError_t e = launch_muon_sums(tab, h, dtype, sums, stream);
     if (e == cudaSuccess) e = launch_muon_fill(tab, h, dtype, fill, stream);
-    for (int k = 0; k < s.count && e == cudaSuccess; ++k) {
-      const double *c = s.k + 3 * k, x = s.x[k], a = s.a[k], b = s.b[k];
-      p.cur = k & 1;
-      p.want_lo = k + 1 < s.count;
-      p.tiles = sym;
-      p.acc = static_cast<float>(a / (x * x)), p.add = 0.f;
-      e = launch_muon_gemm(kMuonGram, map, p, dev->muon_clusters, stream);
-      p.acc = static_cast<float>(c[2] * b / (a * a)), p.add = static_cast<float>(c[1] * b / a);
-      if (e == cudaSuccess) e = launch_muon_gemm(kMuonPoly, map, p, dev->muon_clusters, stream);
-      p.tiles = rect;
-      p.acc = static_cast<float>(s.x[k + 1] / (b * x)), p.add = static_cast<float>(c[0] * s.x[k + 1] / x);
-      if (e == cudaSuccess) e = launch_muon_gemm(kMuonApply, map, p, dev->muon_clusters, stream);
-    }
-    if (e == cudaSuccess) e = launch_muon_apply(tab, h, out_dtype, masters, apply, stream);
+    if (e == cudaSuccess) e = launch_muon_pipe(load, part, tab, p, h, out, dev->muon_clusters, stream);
     if (e != cudaSuccess) return cuda_fail(e, "launch orthogonalised updates");
   }
   return HYLO_OK;

@@ -1,6 +1,5 @@
-// The elementwise kernels around the Newton-Schulz products of orthogonalised updates: momentum and sums of squares, the scaled
-// update as fp16 panels, and the parameters' step (or the result) from the last X. HBM bounds all three; the layout of the
-// workspace is in muon.h.
+// The elementwise kernels around the Newton-Schulz products of orthogonalised updates: momentum and sums of squares, and
+// the scaled update as fp16 panels. HBM bounds both; the layout of the workspace is in muon.h, the parameters' step in muon_pipe.cu.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -18,8 +17,6 @@ __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
 __device__ __forceinline__ void from_float(float x, float* y) { *y = x; }
-__device__ __forceinline__ void from_float(float x, __nv_bfloat16* y) { *y = __float2bfloat16_rn(x); }
-__device__ __forceinline__ void from_float(float x, __half* y) { *y = __float2half_rn(x); }
 
 template <typename T>
 struct alignas(16) Pack16 {
@@ -71,15 +68,6 @@ __device__ __forceinline__ bool gradient_factor(const MuonHyper& h, float& gs) {
   return true;
 }
 
-__device__ __forceinline__ uint32_t mix32(uint32_t x) {  // the finaliser of MurmurHash3
-  x = (x ^ (x >> 16)) * 0x85EBCA6Bu;
-  x = (x ^ (x >> 13)) * 0xC2B2AE35u;
-  return x ^ (x >> 16);
-}
-__device__ __forceinline__ uint32_t random1(uint32_t seed, uint64_t c) {
-  return mix32(static_cast<uint32_t>(c) + mix32(seed + 0x9E3779B9u * (static_cast<uint32_t>(c >> 32) + 1u)));
-}
-
 template <uint32_t MuonMat::* START>
 __device__ __forceinline__ int find_mat(const MuonTable& tab, uint32_t b) {
   int lo = 0, hi = tab.count - 1;
@@ -117,6 +105,7 @@ constexpr float kUp = 0x1p80f, kDown = 0x1p-80f;
 template <typename T>
 __global__ void __launch_bounds__(kThreads) muon_sums_kernel(const __grid_constant__ MuonTable tab, const MuonHyper h) {
   __shared__ float red[kThreads / 32];
+  if (blockIdx.x == 0 && threadIdx.x < kMuonCtrlWords) h.ctrl[threadIdx.x] = 0u;
   float gs = 1.f;
   if (h.muon && !gradient_factor(h, gs)) return;
   const MuonMat& t = tab.t[find_mat<&MuonMat::sum0>(tab, blockIdx.x)];
@@ -196,7 +185,7 @@ __device__ __forceinline__ void put_panel(const MuonHyper& h, const MuonMat& t, 
     hi[j] = *reinterpret_cast<const uint32_t*>(&p);
     lo[j] = *reinterpret_cast<const uint32_t*>(&q);
   }
-  *reinterpret_cast<uint4*>(h.ws + static_cast<size_t>(t.x) * 128 + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+  *reinterpret_cast<uint4*>(h.ws + static_cast<size_t>(t.x[0]) * 128 + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
   *reinterpret_cast<uint4*>(h.ws + static_cast<size_t>(t.lo) * 128 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
 }
 
@@ -212,11 +201,9 @@ __global__ void __launch_bounds__(kThreads) muon_fill_kernel(const __grid_consta
   const bool skipped = h.muon && !gradient_factor(h, gs);
   float2 f = make_float2(0.f, 0.f);
   if (!skipped) f = scale_factors(t, h, red);
-  const int down = t.tall ? t.np : t.mp, across = t.tall ? t.mp : t.np;  // padded rows and columns of the matrix
-  const int wide = across / 64, local = static_cast<int>(blockIdx.x - t.fill0);
+  const int wide = (t.tall ? t.mt : t.nt) * 4, mp = t.mt * 256, local = static_cast<int>(blockIdx.x - t.fill0);
   const int per = (wide + kFillBlocks - 1) / kFillBlocks;
   const int br = local / per, bc0 = (local - br * per) * kFillBlocks;
-  if (br * 64 >= down) return;
   for (int bc = bc0; bc < min(wide, bc0 + kFillBlocks); ++bc) {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -235,7 +222,7 @@ __global__ void __launch_bounds__(kThreads) muon_fill_kernel(const __grid_consta
 #pragma unroll
         for (int j = 0; j < 8; ++j) tile[rr][cc + j] = u[j];
       } else {
-        put_panel(h, t, (static_cast<size_t>(bc) * t.mp + r) * 128 + cc * 2, u, f);
+        put_panel(h, t, (static_cast<size_t>(bc) * mp + r) * 128 + cc * 2, u, f);
       }
     }
     if (t.tall) {
@@ -246,85 +233,19 @@ __global__ void __launch_bounds__(kThreads) muon_fill_kernel(const __grid_consta
         float u[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) u[j] = tile[xc + j][xr];
-        put_panel(h, t, (static_cast<size_t>(br) * t.mp + bc * 64 + xr) * 128 + xc * 2, u, f);
+        put_panel(h, t, (static_cast<size_t>(br) * mp + bc * 64 + xr) * 128 + xc * 2, u, f);
       }
       __syncthreads();
     }
   }
-}
-
-// The result, or the parameters' step, from the last X: O = X unscale.
-template <typename T, bool MUON, bool MASTER>
-__global__ void __launch_bounds__(kThreads) muon_apply_kernel(const __grid_constant__ MuonTable tab, const MuonHyper h) {
-  __shared__ float tile[64][65];
-  const MuonMat& t = tab.t[find_mat<&MuonMat::apply0>(tab, blockIdx.x)];
-  float gs = 1.f;
-  if (MUON && !gradient_factor(h, gs)) return;
-  const int wide = (t.cols + 63) / 64, local = static_cast<int>(blockIdx.x - t.apply0);
-  const int per = (wide + kFillBlocks - 1) / kFillBlocks;
-  const int br = local / per, bc0 = (local - br * per) * kFillBlocks;
-  for (int bc = bc0; bc < min(wide, bc0 + kFillBlocks); ++bc) {
-    if (t.tall) {
-      __syncthreads();
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int xr = half * 32 + static_cast<int>(threadIdx.x >> 3), xc = static_cast<int>(threadIdx.x & 7) * 8;
-        float u[8];
-        load8(reinterpret_cast<const __half*>(h.ws + static_cast<size_t>(t.fin) * 128 +
-                                              (static_cast<size_t>(br) * t.mp + bc * 64 + xr) * 128 + xc * 2), 8, true, u);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) tile[xc + j][xr] = u[j];
-      }
-      __syncthreads();
-    }
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int rr = half * 32 + static_cast<int>(threadIdx.x >> 3), cc = static_cast<int>(threadIdx.x & 7) * 8;
-      const int r = br * 64 + rr, c = bc * 64 + cc;
-      const int left = r < t.rows ? max(0, min(8, t.cols - c)) : 0;
-      if (left == 0) continue;
-      float o[8];
-      if (t.tall) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = tile[rr][cc + j];
-      } else {
-        load8(reinterpret_cast<const __half*>(h.ws + static_cast<size_t>(t.fin) * 128 +
-                                              (static_cast<size_t>(bc) * t.mp + r) * 128 + cc * 2), 8, true, o);
-      }
-      const int64_t i = static_cast<int64_t>(r) * t.cols + c;
-      const bool vec = t.dst_vec != 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] *= h.unscale;
-      if (MUON) {
-        float w[8];
-        if (MASTER)
-          load8(t.master + i, left, vec, w);
-        else
-          load8(static_cast<const T*>(t.dst) + i, left, vec, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = fmaf(w[j], t.decay, -t.step * o[j]);
-        if (MASTER) store8(t.master + i, left, vec, o);
-        if (!MASTER && sizeof(T) == 2) {  // rounded up with the probability of the part cut off
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint32_t bits = random1(h.seed, t.pos + static_cast<uint64_t>(i + j)) * 0x9E3779B1u;
-            if (isfinite(o[j])) o[j] = __uint_as_float((__float_as_uint(o[j]) + (bits >> 16)) & 0xffff0000u);
-          }
-        }
-      }
-      store8(static_cast<T*>(t.dst) + i, left, vec, o);
-    }
-  }
-}
-
-uint32_t blocks(int rows, int cols) {
-  return static_cast<uint32_t>((rows + 63) / 64) * static_cast<uint32_t>(((cols + 63) / 64 + kFillBlocks - 1) / kFillBlocks);
 }
 
 }  // namespace
 
-uint32_t muon_fill_blocks(int mp, int np, bool tall) { return tall ? blocks(np, mp) : blocks(mp, np); }
-uint32_t muon_apply_blocks(int rows, int cols) { return blocks(rows, cols); }
+uint32_t muon_fill_blocks(const MuonMat& t) {
+  const int down = (t.tall ? t.nt : t.mt) * 4, across = (t.tall ? t.mt : t.nt) * 4;  // 64 x 64 blocks
+  return static_cast<uint32_t>(down) * static_cast<uint32_t>((across + kFillBlocks - 1) / kFillBlocks);
+}
 
 cudaError_t launch_muon_sums(const MuonTable& t, const MuonHyper& h, int dtype, uint32_t ctas, cudaStream_t stream) {
   if (dtype == HYLO_F32)
@@ -343,22 +264,6 @@ cudaError_t launch_muon_fill(const MuonTable& t, const MuonHyper& h, int dtype, 
     muon_fill_kernel<__nv_bfloat16><<<ctas, kThreads, 0, stream>>>(t, h);
   else
     muon_fill_kernel<__half><<<ctas, kThreads, 0, stream>>>(t, h);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_muon_apply(const MuonTable& t, const MuonHyper& h, int dtype, bool masters, uint32_t ctas, cudaStream_t stream) {
-  if (!h.muon) {
-    if (dtype == HYLO_BF16)
-      muon_apply_kernel<__nv_bfloat16, false, false><<<ctas, kThreads, 0, stream>>>(t, h);
-    else
-      muon_apply_kernel<__half, false, false><<<ctas, kThreads, 0, stream>>>(t, h);
-  } else if (dtype == HYLO_F32) {
-    muon_apply_kernel<float, true, false><<<ctas, kThreads, 0, stream>>>(t, h);
-  } else if (masters) {
-    muon_apply_kernel<__nv_bfloat16, true, true><<<ctas, kThreads, 0, stream>>>(t, h);
-  } else {
-    muon_apply_kernel<__nv_bfloat16, true, false><<<ctas, kThreads, 0, stream>>>(t, h);
-  }
   return cudaGetLastError();
 }
 

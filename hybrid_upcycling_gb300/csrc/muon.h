@@ -1,4 +1,4 @@
-// Shared by the host side and the kernels of the orthogonalised updates (muon.cu, muon_gemm.cu): the layout of a group of
+// Shared by the host side and the kernels of the orthogonalised updates (muon.cu, muon_pipe.cu): the layout of a group of
 // matrices in the workspace.
 //
 // A group's matrices live in the workspace as fp16 in panels of 64 columns: element (r, c) of a matrix whose panels have `mp`
@@ -18,7 +18,9 @@ constexpr int kMuonMats = 64;     // matrices of a group at most
 constexpr int kMuonParts = 1024;  // partial sums of squares of a matrix at most
 constexpr int kMuonSums = 3;      // of magnitudes near 2^-80, 1 and 2^80
 
-// One matrix as the elementwise kernels see it.
+constexpr int kMuonStepsMax = 32;
+
+// One matrix of a group.
 struct MuonMat {
   const void* src;  // the matrix (orthogonalize) or the gradient
   int64_t ld;       // its row stride
@@ -28,43 +30,35 @@ struct MuonMat {
   uint64_t pos;     // position of element 0 in the list (random bits)
   float decay, step;  // w <- decay w - step O
   int rows, cols;
-  int m, n;         // X is [m, n], m <= n: the matrix, or its transpose if tall
-  int mp, np;       // rounded up to multiples of 256
+  int mt, nt;       // X is [m, n], m <= n (the matrix, or its transpose if tall): 256-row and 256-column tiles
+  int kn, km;       // 64-deep k-blocks of n and m
   int tall, src_vec, dst_vec;
-  uint32_t x, lo, fin;      // first 128-byte rows of X's two terms, and of the last X
+  uint32_t x[2], lo, a, b;  // first 128-byte rows of X before even and odd steps, its second term, A and B
   uint32_t sum0, parts;     // first partial sum, and how many
-  uint32_t fill0, apply0;   // first thread blocks of the kernels that fill X and apply the result
+  uint32_t fill0;           // first thread block of the kernel that fills X
+  int sym0, rect0;          // first 256 x 256 tiles, among the group's, of the symmetric products and of B X
 };
 struct MuonTable {
   MuonMat t[kMuonMats];
   int count;
 };
 
-// The same as the products see it.
-struct MuonGemmMat {
-  uint32_t x[2], lo, a, b;  // first 128-byte rows
-  int mt, nt;               // 256-row tiles of m and n
-  int kn, km;               // 64-deep k-blocks of n and m
-  int sym0, rect0;          // first 256 x 256 tiles of the symmetric products and of B X
-};
 // Products are summed by the tensor cores over at most this many 64-deep k-blocks at a time.
 constexpr int kMuonDepth = 128;
 constexpr int64_t kMuonScratch = int64_t(128) * 256 * 4;  // bytes of a CTA's fp32 sums in between
+
 enum : int { kMuonGram = 0, kMuonPoly = 1, kMuonApply = 2 };
-struct MuonGemmParams {
-  MuonGemmMat t[kMuonMats];
-  int count;
-  int tiles;      // 256 x 256 tiles
-  int cur;        // which of x[2] is read
-  float acc;      // factor on the sum of products
-  float add;      // factor on A (kMuonPoly) or X (kMuonApply)
-  int want_lo;    // kMuonApply: write the second term of X too
-  uint8_t* ws;
-  uint8_t* scratch;  // kMuonScratch bytes for each CTA, where some sum is longer than kMuonDepth
+enum : int { kMuonOutBf16 = 0, kMuonOutF16, kMuonParamF32, kMuonParamBf16, kMuonParamMaster };  // what the last product writes
+struct MuonPipe {
+  int steps;
+  int sym, rect;            // 256 x 256 tiles of the group
+  int sym_half, rect_half;  // 1: work items of 256 x 128, so that there are twice as many
+  float acc[kMuonStepsMax][3], add[kMuonStepsMax][3];  // factors on the sum of products, and on A (Poly) or X (Apply)
+  unsigned* ctrl;           // [0] work queue, [1 + matrix] work done; zero at launch
+  uint8_t* scratch;         // kMuonScratch bytes for each CTA, where some sum is longer than kMuonDepth
   WaitCtl ctl;
 };
-cudaError_t muon_gemm_prepare(int* max_clusters);
-cudaError_t launch_muon_gemm(int phase, const CUtensorMap& ws, const MuonGemmParams& p, int clusters, cudaStream_t stream);
+constexpr int kMuonCtrlWords = 1 + kMuonMats;
 
 struct MuonHyper {
   int muon;        // momentum and parameters, not just the matrices
@@ -79,12 +73,16 @@ struct MuonHyper {
   uint32_t seed;
   uint8_t* ws;
   float* sums;     // [parts][kMuonSums] of the group
+  unsigned* ctrl;  // MuonPipe's, cleared on the way
 };
-// Thread blocks of the kernels that fill X and apply the result, for one matrix.
-uint32_t muon_fill_blocks(int mp, int np, bool tall);
-uint32_t muon_apply_blocks(int rows, int cols);
+// Thread blocks of the kernel that fills X, for one matrix.
+uint32_t muon_fill_blocks(const MuonMat& t);
 cudaError_t launch_muon_sums(const MuonTable& t, const MuonHyper& h, int dtype, uint32_t ctas, cudaStream_t stream);
 cudaError_t launch_muon_fill(const MuonTable& t, const MuonHyper& h, int dtype, uint32_t ctas, cudaStream_t stream);
-cudaError_t launch_muon_apply(const MuonTable& t, const MuonHyper& h, int dtype, bool masters, uint32_t ctas, cudaStream_t stream);
+// All products of all steps; the last one writes the results or steps the parameters (`out`). load: boxes of 64 columns and 64
+// rows of the workspace; part: 64 columns and 32 rows.
+cudaError_t muon_pipe_prepare(int* max_clusters);
+cudaError_t launch_muon_pipe(const CUtensorMap& load, const CUtensorMap& part, const MuonTable& t, const MuonPipe& p, const MuonHyper& h,
+                             int out, int clusters, cudaStream_t stream);
 
 }  // namespace hylo

@@ -1,0 +1,733 @@
+// The Newton-Schulz steps X <- a X + (b A + c A^2) X, A = X X^T, of a group of matrices, on the tensor cores in one persistent launch.
+//
+// Three products a step: Gram forms A, Poly B = b A + c A^2, Apply the next X; the last Apply writes the results, or steps
+// the parameters. A and B are symmetric, so only their 256 x 256 tiles on and above the diagonal are computed and stored. An
+// operand block that lies below it is read as its mirror image: the tensor cores take either order of an operand ("major"), which
+// is a bit of the instruction, set for each block. So half of the products of Gram and Poly are saved without a copy of the mirror
+// image.
+//
+// Operands are fp16 scaled by powers of two (bf16 would round eight times coarser for the same time, and a matrix whose singular
+// values are at most about 1 needs no more range); sums are fp32. X is kept as two fp16 terms, 22 bits: the products read the
+// first one, a X both. So rounding X does not meet the factor a = 3.4 of the small singular values five times over (a matrix of
+// low rank and noise: error 2e-2 with one term, 4e-4 with two).
+//
+// The tensor cores cut every product of a sum off at about 2^-24 of the sum so far, which carries it towards 0 (A of a row of
+// 100 000 elements came out 3e-3 too small), so at most kMuonDepth k-blocks are summed there; longer sums go through fp32 numbers in
+// the CTA's part of the workspace, rounded to nearest.
+//
+// Work items are 256 x 256 tiles (256 x 128 where there are few), taken from a queue in the order step, product, matrix, tile. One
+// may start once every earlier item of its matrix is done, which a counter per matrix tells: what it reads is then complete, and
+// what it overwrites is no longer read. With several matrices the tail of one's product is filled with the next one's items;
+// every item waits for earlier ones only, which running CTAs hold, so the launch cannot deadlock whatever the residency.
+//
+// A CTA pair takes an item: warp 2 of the even CTA fetches it, waits for its matrix and publishes it to both CTAs; warp 0 of each CTA
+// loads by TMA; one thread of warp 1 of the even CTA issues the products; eight warps of each CTA take the sums out of TMEM, whose two
+// halves alternate. These read and write X, A and B through shared memory by TMA, 32 rows and 64 columns at a time: straight
+// from the registers, where a lane has a row, every access touches 32 lines, and the tiles of Apply took twice as long.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "muon.h"
+
+namespace hylo {
+namespace {
+
+constexpr int kEpiWarps = 8, kEpiWarp0 = 4, kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+constexpr int A_BYTES = kBM * kBK * 2;      // 16 KB: this CTA's 128 rows of A
+constexpr int STAGE_BYTES = 2 * A_BYTES;    // and up to 128 rows (columns) of B
+constexpr int STAGES = 5;
+constexpr int PART_BYTES = 4096;            // 32 rows x 64 columns of fp16
+constexpr int STAGING_BYTES = kEpiWarps * 2 * PART_BYTES;  // two terms a warp, or 32 x 64 fp32 numbers
+constexpr int kItemDepth = 3;
+constexpr int ITEM_OFF = STAGES * STAGE_BYTES + STAGING_BYTES;
+constexpr int BAR_OFF = ITEM_OFF + kItemDepth * 32;
+constexpr int NBARS = 2 * STAGES + 4 + 2 * kItemDepth + kEpiWarps + 1;  // full, empty, tfull[2], tempty[2], ifull, iempty, parts, drain
+constexpr int SMEM = 1024 + BAR_OFF + NBARS * 8 + 16;
+static_assert(SMEM <= 232448, "shared memory budget");
+constexpr int kItemConsumers = 2 * (1 + kEpiWarps) + 1;  // producers and epilogue warps of both CTAs, the issuer
+constexpr uint32_t kDone = 2 * kEpiWarps;                // what an item adds to its matrix's counter: one per epilogue warp
+
+// fp16 A and B, fp32 sums.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+constexpr uint32_t kAMajor = 1u << 15, kBMajor = 1u << 16;
+
+struct Item {
+  int product;  // kMuonGram, kMuonPoly, kMuonApply, or -1: no more
+  int step, mat;
+  int i, j;     // 256-row tile, tile of 256 or 128 columns
+  int half;     // 1: 128 columns
+  int big;      // 256-column tile
+  unsigned need;  // the matrix's counter once all earlier items are done
+};
+static_assert(sizeof(Item) == 32, "item size");
+
+__device__ __forceinline__ Item item_at(const MuonTable& tab, const MuonPipe& p, unsigned index) {
+  const unsigned sym = static_cast<unsigned>(p.sym) << p.sym_half, rect = static_cast<unsigned>(p.rect) << p.rect_half;
+  const unsigned per_step = 2 * sym + rect;
+  Item it{};
+  it.step = static_cast<int>(index / per_step);
+  if (it.step >= p.steps) {
+    it.product = -1;
+    return it;
+  }
+  unsigned r = index - static_cast<unsigned>(it.step) * per_step;
+  it.product = r < sym ? kMuonGram : r < 2 * sym ? kMuonPoly : kMuonApply;
+  r -= it.product == kMuonGram ? 0u : it.product == kMuonPoly ? sym : 2 * sym;
+  const bool apply = it.product == kMuonApply;
+  it.half = apply ? p.rect_half : p.sym_half;
+  const int t = static_cast<int>(r >> it.half);
+  int lo = 0, hi = tab.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if ((apply ? tab.t[mid].rect0 : tab.t[mid].sym0) <= t)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const MuonMat& m = tab.t[lo];
+  it.mat = lo;
+  if (apply) {
+    const int local = t - m.rect0;
+    it.big = local / m.mt;
+    it.i = local - it.big * m.mt;
+  } else {  // column by column of the upper triangle: local = big (big + 1) / 2 + i
+    const int local = t - m.sym0;
+    int big = static_cast<int>((sqrtf(8.f * static_cast<float>(local) + 1.f) - 1.f) * 0.5f);
+    while (big * (big + 1) / 2 > local) --big;
+    while ((big + 1) * (big + 2) / 2 <= local) ++big;
+    it.big = big;
+    it.i = local - big * (big + 1) / 2;
+  }
+  it.j = it.half ? it.big * 2 + static_cast<int>(r & 1u) : it.big;
+  const unsigned own_sym = static_cast<unsigned>(m.mt * (m.mt + 1) / 2) << p.sym_half, own_rect = static_cast<unsigned>(m.mt * m.nt) << p.rect_half;
+  it.need = kDone * (static_cast<unsigned>(it.step) * (2 * own_sym + own_rect) + static_cast<unsigned>(it.product) * own_sym);
+  return it;
+}
+
+__device__ __forceinline__ int kblocks(const MuonMat& m, const Item& it) { return it.product == kMuonGram ? m.kn : m.km; }
+// Whether k-block kb of an operand of Poly or Apply comes from its mirror image: it lies left of 256-row tile `tile`.
+__device__ __forceinline__ bool mirrored(int kb, int tile) { return (kb >> 2) < tile; }
+
+__device__ __forceinline__ uint64_t slice_desc(bool mn, uint32_t base, int k) {
+  return mn ? smem_desc_sw128(base + k * 2048, 8192, 1024) : smem_desc_sw128(base + k * 32, 0, 1024);
+}
+
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, unsigned long long limit_ns) {
+  const uint32_t a = smem_u32(bar);
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(a, parity)) {
+    if (globaltimer_ns() - t0 > limit_ns) return;
+  }
+}
+
+// Waits for *ctr >= target (acquire); false on abort or time-out.
+__device__ __forceinline__ bool wait_count(const unsigned* ctr, unsigned target, volatile int* abort_flag, const WaitCtl& ctl) {
+  if (target == 0u || ld_acquire_gpu(ctr) >= target) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    __nanosleep(32);
+    if (ld_acquire_gpu(ctr) >= target) return true;
+    if ((it & 7u) == 0) {
+      if (*abort_flag) return false;
+      if (globaltimer_ns() - t0 > ctl.limit_ns) {
+        *abort_flag = 1;
+        atomicCAS(ctl.status, 0, kDevTimeoutBase + 41);
+        return false;
+      }
+    }
+  }
+}
+
+// rows64 x 64 rows from `row` on and 64 columns from 64 kb on of a matrix whose panels have mp rows. mirror: the block is stored as
+// its mirror image, 64 rows from 64 kb on and the columns `row`, ..., and arrives in MN-major order.
+__device__ __forceinline__ void load_rows(uint8_t* dst, const CUtensorMap* map, uint32_t bar, uint32_t base, int mp, int row, int kb,
+                                          bool mirror, int rows64) {
+  const int at = static_cast<int>(base) + (mirror ? row / 64 * mp + kb * 64 : kb * mp + row), next = mirror ? mp : 64;
+  tma_load_2d_pair(dst, map, bar, 0, at);
+  if (rows64 == 2) tma_load_2d_pair(dst + 8192, map, bar, 0, at + next);
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_f16x2(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
+// ---- what becomes of O
+__device__ __forceinline__ uint32_t mix32(uint32_t x) {  // the finaliser of MurmurHash3
+  x = (x ^ (x >> 16)) * 0x85EBCA6Bu;
+  x = (x ^ (x >> 13)) * 0xC2B2AE35u;
+  return x ^ (x >> 16);
+}
+// bf16 of w, rounded up with the probability of the part cut off; c: the element's position in the list.
+__device__ __forceinline__ float round_random(float w, uint32_t seed, uint64_t c) {
+  if (!isfinite(w)) return w;
+  const uint32_t bits = mix32(static_cast<uint32_t>(c) + mix32(seed + 0x9E3779B9u * (static_cast<uint32_t>(c >> 32) + 1u)));
+  return __uint_as_float((__float_as_uint(w) + ((bits * 0x9E3779B1u) >> 16)) & 0xffff0000u);
+}
+
+// Elements e, ..., e + N - 1 of the result or parameter (N = 4: 16-byte vectors of fp32).
+template <int OUT, int N>
+__device__ __forceinline__ void finish(const MuonMat& m, uint32_t seed, int64_t e, const float (&w)[N], float (&o)[N]) {
+  if (OUT == kMuonOutBf16 || OUT == kMuonOutF16) {
+    if constexpr (N == 4) {
+      uint2 v;
+      if (OUT == kMuonOutBf16)
+        v = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+      else
+        v = make_uint2(pack_f16x2(o[0], o[1]), pack_f16x2(o[2], o[3]));
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(m.dst) + e) = v;
+    } else {
+      if (OUT == kMuonOutBf16)
+        static_cast<__nv_bfloat16*>(m.dst)[e] = __float2bfloat16_rn(o[0]);
+      else
+        static_cast<__half*>(m.dst)[e] = __float2half_rn(o[0]);
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < N; ++j) o[j] = fmaf(w[j], m.decay, -m.step * o[j]);
+  if (OUT != kMuonParamBf16) {
+    float* f = (OUT == kMuonParamF32 ? static_cast<float*>(m.dst) : m.master) + e;
+    if constexpr (N == 4)
+      *reinterpret_cast<float4*>(f) = make_float4(o[0], o[1], o[2], o[3]);
+    else
+      f[0] = o[0];
+  }
+  if (OUT == kMuonParamF32) return;
+  if (OUT == kMuonParamBf16) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) o[j] = round_random(o[j], seed, m.pos + static_cast<uint64_t>(e + j));
+  }
+  if constexpr (N == 4)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(m.dst) + e) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+  else
+    static_cast<__nv_bfloat16*>(m.dst)[e] = __float2bfloat16_rn(o[0]);
+}
+template <int OUT, int N>
+__device__ __forceinline__ void read_param(const MuonMat& m, int64_t e, float (&w)[N]) {
+  if (OUT == kMuonParamF32 || OUT == kMuonParamMaster) {
+    const float* f = (OUT == kMuonParamF32 ? static_cast<const float*>(m.dst) : m.master) + e;
+    if constexpr (N == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(f);
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else {
+      w[0] = f[0];
+    }
+  } else if (OUT == kMuonParamBf16) {
+    const uint16_t* f = static_cast<const uint16_t*>(m.dst) + e;
+    if constexpr (N == 4) {
+      const uint2 v = *reinterpret_cast<const uint2*>(f);
+      w[0] = __uint_as_float(v.x << 16), w[1] = __uint_as_float(v.x & 0xffff0000u);
+      w[2] = __uint_as_float(v.y << 16), w[3] = __uint_as_float(v.y & 0xffff0000u);
+    } else {
+      w[0] = __uint_as_float(static_cast<uint32_t>(f[0]) << 16);
+    }
+  }
+}
+
+// O's 32 rows from `row` on and 64 columns from `col` on (of X), of which this lane has one row in o.
+template <int OUT>
+__device__ __forceinline__ void finish_part(const MuonMat& m, uint32_t seed, int row, int col, int lane, uint32_t staging, float (&o)[64]) {
+  if (m.tall) {  // X's rows are the matrix's columns: 32 lanes write consecutive elements
+    const int c = row + lane;
+    if (c < m.cols) {
+#pragma unroll
+      for (int j0 = 0; j0 < 64; j0 += 16) {
+        float w[16][1];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          w[j][0] = 0.f;
+          if (col + j0 + j < m.rows) read_param<OUT, 1>(m, static_cast<int64_t>(col + j0 + j) * m.cols + c, w[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          float v[1] = {o[j0 + j]};
+          if (col + j0 + j < m.rows) finish<OUT, 1>(m, seed, static_cast<int64_t>(col + j0 + j) * m.cols + c, w[j], v);
+        }
+      }
+    }
+    return;
+  }
+  // Through shared memory: rows of 64 fp32 numbers, 16-byte chunks swizzled by the row.
+#pragma unroll
+  for (int k = 0; k < 16; ++k)
+    st_shared_v4(staging + lane * 256 + (k ^ (lane & 7)) * 16, __float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]),
+                 __float_as_uint(o[4 * k + 2]), __float_as_uint(o[4 * k + 3]));
+  __syncwarp();
+  const int k = lane & 15, c = col + 4 * k;
+  if (m.dst_vec && c + 4 <= m.cols) {
+#pragma unroll
+    for (int r0 = 0; r0 < 32; r0 += 16) {
+      float w[8][4];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int r = row + r0 + 2 * q + (lane >> 4);
+        if (r < m.rows) read_param<OUT, 4>(m, static_cast<int64_t>(r) * m.cols + c, w[q]);
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int rr = r0 + 2 * q + (lane >> 4);
+        const uint4 u = ld_shared_v4(staging + rr * 256 + (k ^ (rr & 7)) * 16);
+        float v[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
+        if (row + rr < m.rows) finish<OUT, 4>(m, seed, static_cast<int64_t>(row + rr) * m.cols + c, w[q], v);
+      }
+    }
+  } else {
+    for (int rr = lane >> 4; rr < 32; rr += 2) {
+      const uint4 u = ld_shared_v4(staging + rr * 256 + (k ^ (rr & 7)) * 16);
+      const float all[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (row + rr < m.rows && c + j < m.cols) {
+          float w[1] = {0.f}, v[1] = {all[j]};
+          const int64_t e = static_cast<int64_t>(row + rr) * m.cols + c + j;
+          read_param<OUT, 1>(m, e, w);
+          finish<OUT, 1>(m, seed, e, w, v);
+        }
+      }
+    }
+  }
+  __syncwarp();
+}
+
+template <int OUT>
+__global__ void __launch_bounds__(kThreads, 1)
+muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap part_map, const __grid_constant__ MuonTable tab,
+                 const __grid_constant__ MuonPipe p, const MuonHyper hyper) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* staging_all = smem + STAGES * STAGE_BYTES;
+  Item* items = reinterpret_cast<Item*>(smem + ITEM_OFF);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + BAR_OFF);  // used in the even CTA
+  uint64_t* empty = full + STAGES;                                // both CTAs
+  uint64_t* tfull = empty + STAGES;                               // both CTAs: TMEM half written
+  uint64_t* tempty = tfull + 2;                                   // even CTA: half read by both CTAs
+  uint64_t* ifull = tempty + 2;                                   // both CTAs: item slot published
+  uint64_t* iempty = ifull + kItemDepth;                          // even CTA: item slot released
+  uint64_t* parts = iempty + kItemDepth;                          // an epilogue warp's loads
+  uint64_t* drain = parts + kEpiWarps;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+    }
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(tfull + h, 1);
+      mbar_init(tempty + h, 2 * kEpiWarps);
+    }
+    for (int k = 0; k < kItemDepth; ++k) {
+      mbar_init(ifull + k, 1);
+      mbar_init(iempty + k, kItemConsumers);
+    }
+    for (int w = 0; w < kEpiWarps; ++w) mbar_init(parts + w, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (threadIdx.x == 32) {
+    prefetch_tmap(&map);
+    prefetch_tmap(&part_map);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // barriers of both CTAs initialised before any cross-CTA signal
+  tc_fence_after();
+  grid_dep_wait();
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp == 2) {
+    // ------------------------------------------------------------------ scheduler (even CTA)
+    if (lane == 0 && rank == 0) {
+      const uint32_t peer_items = mapa_shared(smem_u32(items), 1), peer_ifull = mapa_shared(smem_u32(ifull), 1);
+      unsigned next = atomicAdd(p.ctrl, 1u);
+      for (int k = 0;; ++k) {
+        const int slot = k % kItemDepth;
+        const uint32_t par = static_cast<uint32_t>(k / kItemDepth) & 1u;
+        if (!wait_bounded<true>(iempty + slot, par ^ 1u, abort_flag, p.ctl, 42)) break;
+        const Item it = item_at(tab, p, next);
+        if (it.product >= 0) {
+          next = atomicAdd(p.ctrl, 1u);  // the next item, fetched ahead
+          if (!wait_count(p.ctrl + 1 + it.mat, it.need, abort_flag, p.ctl)) break;
+        }
+        items[slot] = it;
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&it);
+        for (int q = 0; q < 8; ++q) st_cluster_u32(peer_items + slot * 32 + q * 4, w[q]);
+        mbar_arrive(ifull + slot);
+        mbar_arrive_remote(peer_ifull + slot * 8);
+        if (it.product < 0) break;
+      }
+    }
+  } else if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer (both CTAs)
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, armed = 0;
+      const uint32_t lead_iempty = mapa_shared(smem_u32(iempty), 0), full_lead = mapa_shared(smem_u32(full), 0);
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        const int slot = k % kItemDepth;
+        const uint32_t par = static_cast<uint32_t>(k / kItemDepth) & 1u;
+        if (!wait_bounded<true>(ifull + slot, par, abort_flag, p.ctl, 43)) break;
+        const Item it = items[slot];
+        if (rank == 0)
+          mbar_arrive(iempty + slot);
+        else
+          mbar_arrive_remote(lead_iempty + slot * 8);
+        if (it.product < 0) break;
+        fence_proxy_async_global();  // what it reads was stored by TMA in other CTAs, or by the kernel before
+        const MuonMat& m = tab.t[it.mat];
+        const int mp = m.mt * 256, nk = kblocks(m, it), cur = it.step & 1, wide = it.half ? 128 : 256;
+        const uint32_t abase = it.product == kMuonGram ? m.x[cur] : it.product == kMuonPoly ? m.a : m.b;
+        const uint32_t bbase = it.product == kMuonPoly ? m.a : m.x[cur];
+        const int arow = it.i * 256 + static_cast<int>(rank) * kBM, brow = it.j * wide + static_cast<int>(rank) * (wide / 2);
+        const int brows64 = it.half ? 1 : 2;
+        const uint32_t bytes = 2u * (A_BYTES + static_cast<uint32_t>(wide / 2) * kBK * 2u);  // both CTAs'
+        for (int kb = 0; kb < nk; ++kb) {
+          if (!wait_bounded(empty + stage, phase ^ 1u, abort_flag, p.ctl, 44)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sa = smem + stage * STAGE_BYTES;
+          const uint32_t fb = full_lead + static_cast<uint32_t>(stage) * 8u;
+          if (rank == 0) {
+            mbar_arrive_expect_tx(full + stage, bytes);
+            armed |= 1u << stage;
+          }
+          load_rows(sa, &map, fb, abase, mp, arow, kb, it.product != kMuonGram && mirrored(kb, it.i), 2);
+          // B of Apply is X, 64 of its rows and this CTA's columns, which lie like a mirror image's
+          load_rows(sa + A_BYTES, &map, fb, bbase, mp, brow, kb, it.product == kMuonApply || (it.product == kMuonPoly && mirrored(kb, it.big)),
+                    brows64);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {  // let every armed load land before the CTA can exit
+        for (int s = 0; s < STAGES; ++s)
+          if (armed & (1u << s)) drain_wait(full + s, s < stage ? phase : (phase ^ 1u), 100000000ull);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ UMMA issuer (even CTA)
+    if (lane == 0 && rank == 0) {
+      int stage = 0, h = 0;
+      uint32_t phase = 0, uses[2] = {0u, 0u};
+      bool ok = true, issued = false;
+      for (int k = 0; ok; ++k) {
+        const int slot = k % kItemDepth;
+        const uint32_t par = static_cast<uint32_t>(k / kItemDepth) & 1u;
+        if (!wait_bounded(ifull + slot, par, abort_flag, p.ctl, 45)) {
+          ok = false;
+          break;
+        }
+        const Item it = items[slot];
+        mbar_arrive(iempty + slot);
+        if (it.product < 0) break;
+        const int nk = kblocks(tab.t[it.mat], it);
+        const uint32_t idesc0 = idesc_f16_f32(2 * kBM, it.half ? 128 : 256);
+        for (int from = 0; ok && from < nk; from += kMuonDepth) {
+          if (!wait_bounded(tempty + h, (uses[h] & 1u) ^ 1u, abort_flag, p.ctl, 46)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d = tmem_base + static_cast<uint32_t>(h * 256);
+          for (int kb = from; kb < min(nk, from + kMuonDepth); ++kb) {
+            if (!wait_bounded(full + stage, phase, abort_flag, p.ctl, 47)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES), sb = sa + A_BYTES;
+            const bool amn = it.product != kMuonGram && mirrored(kb, it.i);
+            const bool bmn = it.product == kMuonApply || (it.product == kMuonPoly && mirrored(kb, it.big));
+            const uint32_t idesc = idesc0 | (amn ? kAMajor : 0u) | (bmn ? kBMajor : 0u);
+#pragma unroll
+            for (int q = 0; q < kBK / 16; ++q)
+              umma_bf16_pair(d, slice_desc(amn, sa, q), slice_desc(bmn, sb, q), idesc, (kb > from || q > 0) ? 1u : 0u);
+            umma_commit_pair(empty + stage, 0x3);
+            issued = true;
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+          if (!ok) break;
+          umma_commit_pair(tfull + h, 0x3);
+          ++uses[h];
+          h ^= 1;
+        }
+      }
+      if (!ok && issued) {
+        umma_commit_pair(drain, 0x1);
+        drain_wait(drain, 0, 100000000ull);
+      }
+    }
+  } else if (warp >= kEpiWarp0) {
+    // ------------------------------------------------------------------ epilogue (both CTAs)
+    const int e = warp - kEpiWarp0, q = warp & 3, hc = e >> 2;  // lane quarter, column half
+    const uint32_t lead_tempty = mapa_shared(smem_u32(tempty), 0), lead_iempty = mapa_shared(smem_u32(iempty), 0);
+    uint8_t* staging = staging_all + e * 2 * PART_BYTES;
+    const uint32_t stage_a = smem_u32(staging), line = stage_a + lane * 128;  // this lane's row of the first term
+    uint64_t* loads = parts + e;
+    uint32_t uses[2] = {0u, 0u}, loaded = 0;
+    int h = 0;
+    bool skip = false;  // a Muon step whose norm is not finite changes nothing
+    if (hyper.norm != nullptr) skip = !isfinite(hyper.norm[0]);
+    for (int k = 0;; ++k) {
+      const int slot = k % kItemDepth;
+      const uint32_t par = static_cast<uint32_t>(k / kItemDepth) & 1u;
+      bool got = wait_bounded<true>(ifull + slot, par, abort_flag, p.ctl, 48);
+      if (!__all_sync(0xffffffffu, got)) break;
+      const Item it = items[slot];
+      __syncwarp();
+      if (lane == 0) {
+        if (rank == 0)
+          mbar_arrive(iempty + slot);
+        else
+          mbar_arrive_remote(lead_iempty + slot * 8);
+      }
+      if (it.product < 0) break;
+      const MuonMat& m = tab.t[it.mat];
+      const int mp = m.mt * 256, nk = kblocks(m, it), cur = it.step & 1, units = it.half ? 1 : 2;
+      const bool apply = it.product == kMuonApply, last = apply && it.step + 1 == p.steps, two = apply;
+      const uint32_t out = it.product == kMuonGram ? m.a : it.product == kMuonPoly ? m.b : m.x[cur ^ 1];
+      const uint32_t add = it.product == kMuonPoly ? m.a : m.x[cur];
+      const int row = it.i * 256 + static_cast<int>(rank) * kBM + q * 32;
+      const int col0 = (2 * it.j + hc) * 64 * units;
+      auto part_row = [&](uint32_t base, int u) { return static_cast<int>(base) + (col0 / 64 + u) * mp + row; };
+      auto load_part = [&](int u) {
+        mbar_arrive_expect_tx(loads, two ? 2 * PART_BYTES : PART_BYTES);
+        tma_load_2d(staging, &part_map, loads, 0, part_row(add, u));
+        if (two) tma_load_2d(staging + PART_BYTES, &part_map, loads, 0, part_row(m.lo, u));
+      };
+      if (lane == 0 && it.product != kMuonGram) {
+        fence_proxy_async_global();
+        load_part(0);
+      }
+      // Of a long sum all but the last stretch, added up in the workspace: [BN / 64][8][32 lanes] of this warp.
+      const bool deep = nk > kMuonDepth;
+      float4* scratch = nullptr;
+      if (deep) scratch = reinterpret_cast<float4*>(p.scratch + static_cast<size_t>(blockIdx.x) * kMuonScratch + static_cast<size_t>(e) * (kMuonScratch / kEpiWarps)) + lane;
+      const uint32_t lanes = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+      for (int from = 0; from + kMuonDepth < nk; from += kMuonDepth) {
+        got = __all_sync(0xffffffffu, wait_bounded(tfull + h, uses[h] & 1u, abort_flag, p.ctl, 49));
+        if (!got) break;
+        tc_fence_after();
+        for (int c = 0; c < 2 * units; ++c) {
+          float v[32];
+          tmem_ld32(lanes + static_cast<uint32_t>(h * 256 + hc * 64 * units + c * 32), v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float4 x = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            if (from > 0) {
+              const float4 y = scratch[(c * 8 + j) * 32];
+              x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+            }
+            scratch[(c * 8 + j) * 32] = x;
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(lead_tempty + h * 8);
+        ++uses[h];
+        h ^= 1;
+      }
+      if (!got) break;
+      got = wait_bounded(tfull + h, uses[h] & 1u, abort_flag, p.ctl, 50);
+      if (!__all_sync(0xffffffffu, got)) break;
+      tc_fence_after();
+      const float acc = p.acc[it.step][it.product], fac = p.add[it.step][it.product];
+      for (int u = 0; u < units; ++u) {
+        float v[64];
+        tmem_ld32_at(lanes + static_cast<uint32_t>(h * 256 + (hc * units + u) * 64), v);
+        tmem_ld32_at(lanes + static_cast<uint32_t>(h * 256 + (hc * units + u) * 64 + 32), v + 32);
+        tmem_ld_wait();
+        if (u == units - 1) {  // the half is free for the next item but one
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(lead_tempty + h * 8);
+        }
+        if (deep) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float4 y = scratch[(u * 16 + j) * 32];
+            v[4 * j] += y.x, v[4 * j + 1] += y.y, v[4 * j + 2] += y.z, v[4 * j + 3] += y.w;
+          }
+        }
+        if (it.product != kMuonGram) {
+          got = __all_sync(0xffffffffu, wait_bounded(loads, loaded & 1u, abort_flag, p.ctl, 51));
+          if (!got) break;
+          ++loaded;
+        } else if (u > 0) {
+          if (lane == 0) bulk_wait_group_read<0>();  // the store of the part before has read the staging
+          __syncwarp();
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {  // 16-byte chunks, where the 128-byte swizzle has them
+          const uint32_t at = line + static_cast<uint32_t>((c ^ (lane & 7)) * 16);
+          float x[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = v[8 * c + j] * acc;
+          if (it.product != kMuonGram) {
+            const uint4 w = ld_shared_v4(at);
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+            uint32_t ll[4] = {0u, 0u, 0u, 0u};
+            if (apply) {
+              const uint4 l = ld_shared_v4(at + PART_BYTES);
+              ll[0] = l.x, ll[1] = l.y, ll[2] = l.z, ll[3] = l.w;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 f = unpack_f16x2(ww[j]), g = unpack_f16x2(ll[j]);
+              x[2 * j] = fmaf(f.x + g.x, fac, x[2 * j]);
+              x[2 * j + 1] = fmaf(f.y + g.y, fac, x[2 * j + 1]);
+            }
+          }
+          if (last) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[8 * c + j] = x[j];
+          } else {
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[j] = pack_f16x2(x[2 * j], x[2 * j + 1]);
+            st_shared_v4(at, o[0], o[1], o[2], o[3]);
+            if (apply) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float2 f = unpack_f16x2(o[j]);
+                o[j] = pack_f16x2(x[2 * j] - f.x, x[2 * j + 1] - f.y);
+              }
+              st_shared_v4(at + PART_BYTES, o[0], o[1], o[2], o[3]);
+            }
+          }
+        }
+        if (last) {
+          __syncwarp();  // every lane has read its part of the staging, which is written again
+#pragma unroll
+          for (int j = 0; j < 64; ++j) {  // as fp16, like every X
+            v[j] = __half2float(__float2half_rn(v[j])) * hyper.unscale;
+          }
+          if (!skip) finish_part<OUT>(m, hyper.seed, row, col0 + u * 64, lane, stage_a, v);
+          if (u + 1 < units) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) load_part(u + 1);
+          }
+          continue;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(&part_map, staging, 0, part_row(out, u));
+          if (apply) tma_store_2d(&part_map, staging + PART_BYTES, 0, part_row(m.lo, u));
+          bulk_commit_group();
+          if (u + 1 < units && it.product != kMuonGram) {
+            bulk_wait_group_read<0>();
+            load_part(u + 1);
+          }
+        }
+      }
+      if (!got) break;
+      ++uses[h];
+      h ^= 1;
+      if (last) {
+        fence_proxy_async_smem();  // the staging goes back to TMA
+        __syncwarp();
+      } else if (lane == 0) {
+        bulk_wait_group<0>();  // the stores are complete
+        fence_proxy_async_global();
+        red_release_gpu_add(p.ctrl + 1 + it.mat, 1u);
+      }
+      __syncwarp();
+    }
+    if (lane == 0) bulk_wait_group<0>();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // no cross-CTA signal may target a CTA that has exited
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+cudaLaunchConfig_t pipe_config(cudaLaunchAttribute* attr, int clusters, cudaStream_t stream) {
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see grid_dep_wait()
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * clusters, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = SMEM;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cfg;
+}
+
+template <int OUT>
+cudaError_t prepare_one(int* max_clusters) {
+  cudaError_t e = cudaFuncSetAttribute(muon_pipe_kernel<OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = pipe_config(attr, 1, nullptr);
+  cfg.numAttrs = 1;  // occupancy: the cluster shape only
+  int n = 0;
+  e = cudaOccupancyMaxActiveClusters(&n, muon_pipe_kernel<OUT>, &cfg);
+  if (e == cudaSuccess && n < *max_clusters) *max_clusters = n;
+  return e;
+}
+
+}  // namespace
+
+cudaError_t muon_pipe_prepare(int* max_clusters) {
+  *max_clusters = kMaxClusters;
+  cudaError_t e = prepare_one<kMuonOutBf16>(max_clusters);
+  if (e == cudaSuccess) e = prepare_one<kMuonOutF16>(max_clusters);
+  if (e == cudaSuccess) e = prepare_one<kMuonParamF32>(max_clusters);
+  if (e == cudaSuccess) e = prepare_one<kMuonParamBf16>(max_clusters);
+  if (e == cudaSuccess) e = prepare_one<kMuonParamMaster>(max_clusters);
+  return e;
+}
+
+cudaError_t launch_muon_pipe(const CUtensorMap& load, const CUtensorMap& part, const MuonTable& t, const MuonPipe& p, const MuonHyper& h,
+                             int out, int clusters, cudaStream_t stream) {
+  const int64_t sym = static_cast<int64_t>(p.sym) << p.sym_half, rect = static_cast<int64_t>(p.rect) << p.rect_half;
+  const int64_t most = sym > rect ? sym : rect;  // items that can run at once
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = pipe_config(attr, static_cast<int>(most < clusters ? most : clusters), stream);
+  switch (out) {
+    case kMuonOutBf16: return cudaLaunchKernelEx(&cfg, muon_pipe_kernel<kMuonOutBf16>, load, part, t, p, h);
+    case kMuonOutF16: return cudaLaunchKernelEx(&cfg, muon_pipe_kernel<kMuonOutF16>, load, part, t, p, h);
+    case kMuonParamF32: return cudaLaunchKernelEx(&cfg, muon_pipe_kernel<kMuonParamF32>, load, part, t, p, h);
+    case kMuonParamBf16: return cudaLaunchKernelEx(&cfg, muon_pipe_kernel<kMuonParamBf16>, load, part, t, p, h);
+    default: return cudaLaunchKernelEx(&cfg, muon_pipe_kernel<kMuonParamMaster>, load, part, t, p, h);
+  }
+}
+
+}  // namespace hylo
