@@ -149,10 +149,6 @@ hylo_status plan_steps(int steps, const double* coefficients, double eps, Steps*
   return HYLO_OK;
 }
 
-// 256 x 256 tiles read fewer operands per product, 256 x 128 ones leave fewer SMs idle: the rounds of tiles decide, one of
-// narrow tiles counting 5/8 of one of wide tiles.
-int halve(int64_t tiles, int clusters) { return 5 * cdiv(2 * tiles, clusters) < 8 * cdiv(tiles, clusters) ? 1 : 0; }
-
 bool aligned_rows(const void* p, int64_t ld, uintptr_t bytes) { return aligned(p, 16) && ld * bytes % 16 == 0; }
 
 // All launches of one list. dtype: of the matrices or gradients; out_dtype: of the results or parameters.
@@ -205,14 +201,13 @@ hylo_status run(const T* list, int count, int dtype, int out_dtype, bool masters
     if (tab.count == 0) continue;
     CUtensorMap load, part;
     if ((st = make_map(&load, ws, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 64, row, 128, 64, 64)) != HYLO_OK ||
-        (st = make_map(&part, ws, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 64, row, 128, 64, 32)) != HYLO_OK)
+        (st = make_map(&part, ws, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 64, row, 128, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) != HYLO_OK)
       return st;
     h.sums = reinterpret_cast<float*>(h.ws + group.sums_at());
     h.ctrl = p.ctrl = reinterpret_cast<unsigned*>(h.ws + group.ctrl_at());
     p.scratch = h.ws + group.scratch_at();
     p.ctl = WaitCtl{dev->status, wait_limit_ns()};
     p.steps = s.count;
-    p.sym_half = halve(p.sym, dev->muon_clusters), p.rect_half = halve(p.rect, dev->muon_clusters);
     for (int k = 0; k < s.count; ++k) {
       const double *c = s.k + 3 * k, x = s.x[k], a = s.a[k], b = s.b[k], next = s.x[k + 1];
       p.acc[k][kMuonGram] = static_cast<float>(a / (x * x));

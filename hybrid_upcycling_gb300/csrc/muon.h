@@ -52,7 +52,6 @@ enum : int { kMuonOutBf16 = 0, kMuonOutF16, kMuonParamF32, kMuonParamBf16, kMuon
 struct MuonPipe {
   int steps;
   int sym, rect;            // 256 x 256 tiles of the group
-  int sym_half, rect_half;  // 1: work items of 256 x 128, so that there are twice as many
   float acc[kMuonStepsMax][3], add[kMuonStepsMax][3];  // factors on the sum of products, and on A (Poly) or X (Apply)
   unsigned* ctrl;           // [0] work queue, [1 + matrix] work done; zero at launch
   uint8_t* scratch;         // kMuonScratch bytes for each CTA, where some sum is longer than kMuonDepth
@@ -80,7 +79,7 @@ uint32_t muon_fill_blocks(const MuonMat& t);
 cudaError_t launch_muon_sums(const MuonTable& t, const MuonHyper& h, int dtype, uint32_t ctas, cudaStream_t stream);
 cudaError_t launch_muon_fill(const MuonTable& t, const MuonHyper& h, int dtype, uint32_t ctas, cudaStream_t stream);
 // All products of all steps; the last one writes the results or steps the parameters (`out`). load: boxes of 64 columns and 64
-// rows of the workspace; part: 64 columns and 32 rows.
+// rows of the workspace; part: 32 columns and 32 rows, 64-byte swizzle.
 cudaError_t muon_pipe_prepare(int* max_clusters);
 cudaError_t launch_muon_pipe(const CUtensorMap& load, const CUtensorMap& part, const MuonTable& t, const MuonPipe& p, const MuonHyper& h,
                              int out, int clusters, cudaStream_t stream);

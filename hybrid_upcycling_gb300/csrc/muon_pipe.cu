@@ -15,14 +15,15 @@
 // 100 000 elements came out 3e-3 too small), so at most kMuonDepth k-blocks are summed there; longer sums go through fp32 numbers in
 // the CTA's part of the workspace, rounded to nearest.
 //
-// Work items are 256 x 256 tiles (256 x 128 where there are few), taken from a queue in the order step, product, matrix, tile. One
+// Work items are 256 x 256 tiles (narrower ones read more operands per product, whose latency the six stages then no longer cover:
+// 256 x 128 took as long), taken from a queue in the order step, product, matrix, tile. One
 // may start once every earlier item of its matrix is done, which a counter per matrix tells: what it reads is then complete, and
 // what it overwrites is no longer read. With several matrices the tail of one's product is filled with the next one's items;
 // every item waits for earlier ones only, which running CTAs hold, so the launch cannot deadlock whatever the residency.
 //
 // A CTA pair takes an item: warp 2 of the even CTA fetches it, waits for its matrix and publishes it to both CTAs; warp 0 of each CTA
 // loads by TMA; one thread of warp 1 of the even CTA issues the products; eight warps of each CTA take the sums out of TMEM, whose two
-// halves alternate. These read and write X, A and B through shared memory by TMA, 32 rows and 64 columns at a time: straight
+// halves alternate. These read and write X, A and B through shared memory by TMA, 32 rows and 32 columns at a time: straight
 // from the registers, where a lane has a row, every access touches 32 lines, and the tiles of Apply took twice as long.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -34,11 +35,12 @@ namespace {
 
 constexpr int kEpiWarps = 8, kEpiWarp0 = 4, kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr int A_BYTES = kBM * kBK * 2;      // 16 KB: this CTA's 128 rows of A
-constexpr int STAGE_BYTES = 2 * A_BYTES;    // and up to 128 rows (columns) of B
-constexpr int STAGES = 5;
-constexpr int PART_BYTES = 4096;            // 32 rows x 64 columns of fp16
-constexpr int STAGING_BYTES = kEpiWarps * 2 * PART_BYTES;  // two terms a warp, or 32 x 64 fp32 numbers
-constexpr int kItemDepth = 3;
+constexpr int STAGE_BYTES = 2 * A_BYTES;    // and 128 rows (columns) of B
+constexpr int STAGES = 6;
+constexpr int PART_BYTES = 2048;            // 32 rows x 32 columns of fp16
+constexpr int STAGING_BYTES = kEpiWarps * 2 * PART_BYTES;  // two terms a warp, or 32 x 32 fp32 numbers
+constexpr int kUnits = 4;                   // such parts of a warp's 32 rows x 128 columns
+constexpr int kItemDepth = 2;
 constexpr int ITEM_OFF = STAGES * STAGE_BYTES + STAGING_BYTES;
 constexpr int BAR_OFF = ITEM_OFF + kItemDepth * 32;
 constexpr int NBARS = 2 * STAGES + 4 + 2 * kItemDepth + kEpiWarps + 1;  // full, empty, tfull[2], tempty[2], ifull, iempty, parts, drain
@@ -56,16 +58,14 @@ constexpr uint32_t kAMajor = 1u << 15, kBMajor = 1u << 16;
 struct Item {
   int product;  // kMuonGram, kMuonPoly, kMuonApply, or -1: no more
   int step, mat;
-  int i, j;     // 256-row tile, tile of 256 or 128 columns
-  int half;     // 1: 128 columns
-  int big;      // 256-column tile
+  int i, j;     // 256-row tile, 256-column tile
   unsigned need;  // the matrix's counter once all earlier items are done
+  int pad[2];
 };
 static_assert(sizeof(Item) == 32, "item size");
 
 __device__ __forceinline__ Item item_at(const MuonTable& tab, const MuonPipe& p, unsigned index) {
-  const unsigned sym = static_cast<unsigned>(p.sym) << p.sym_half, rect = static_cast<unsigned>(p.rect) << p.rect_half;
-  const unsigned per_step = 2 * sym + rect;
+  const unsigned sym = static_cast<unsigned>(p.sym), per_step = 2 * sym + static_cast<unsigned>(p.rect);
   Item it{};
   it.step = static_cast<int>(index / per_step);
   if (it.step >= p.steps) {
@@ -74,10 +74,9 @@ __device__ __forceinline__ Item item_at(const MuonTable& tab, const MuonPipe& p,
   }
   unsigned r = index - static_cast<unsigned>(it.step) * per_step;
   it.product = r < sym ? kMuonGram : r < 2 * sym ? kMuonPoly : kMuonApply;
-  r -= it.product == kMuonGram ? 0u : it.product == kMuonPoly ? sym : 2 * sym;
+  r -= static_cast<unsigned>(it.product) * sym;
   const bool apply = it.product == kMuonApply;
-  it.half = apply ? p.rect_half : p.sym_half;
-  const int t = static_cast<int>(r >> it.half);
+  const int t = static_cast<int>(r);
   int lo = 0, hi = tab.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -90,18 +89,17 @@ __device__ __forceinline__ Item item_at(const MuonTable& tab, const MuonPipe& p,
   it.mat = lo;
   if (apply) {
     const int local = t - m.rect0;
-    it.big = local / m.mt;
-    it.i = local - it.big * m.mt;
-  } else {  // column by column of the upper triangle: local = big (big + 1) / 2 + i
+    it.j = local / m.mt;
+    it.i = local - it.j * m.mt;
+  } else {  // column by column of the upper triangle: local = j (j + 1) / 2 + i
     const int local = t - m.sym0;
-    int big = static_cast<int>((sqrtf(8.f * static_cast<float>(local) + 1.f) - 1.f) * 0.5f);
-    while (big * (big + 1) / 2 > local) --big;
-    while ((big + 1) * (big + 2) / 2 <= local) ++big;
-    it.big = big;
-    it.i = local - big * (big + 1) / 2;
+    int j = static_cast<int>((sqrtf(8.f * static_cast<float>(local) + 1.f) - 1.f) * 0.5f);
+    while (j * (j + 1) / 2 > local) --j;
+    while ((j + 1) * (j + 2) / 2 <= local) ++j;
+    it.j = j;
+    it.i = local - j * (j + 1) / 2;
   }
-  it.j = it.half ? it.big * 2 + static_cast<int>(r & 1u) : it.big;
-  const unsigned own_sym = static_cast<unsigned>(m.mt * (m.mt + 1) / 2) << p.sym_half, own_rect = static_cast<unsigned>(m.mt * m.nt) << p.rect_half;
+  const unsigned own_sym = static_cast<unsigned>(m.mt * (m.mt + 1) / 2), own_rect = static_cast<unsigned>(m.mt * m.nt);
   it.need = kDone * (static_cast<unsigned>(it.step) * (2 * own_sym + own_rect) + static_cast<unsigned>(it.product) * own_sym);
   return it;
 }
@@ -140,13 +138,13 @@ __device__ __forceinline__ bool wait_count(const unsigned* ctr, unsigned target,
   }
 }
 
-// rows64 x 64 rows from `row` on and 64 columns from 64 kb on of a matrix whose panels have mp rows. mirror: the block is stored as
+// 128 rows from `row` on and 64 columns from 64 kb on of a matrix whose panels have mp rows. mirror: the block is stored as
 // its mirror image, 64 rows from 64 kb on and the columns `row`, ..., and arrives in MN-major order.
 __device__ __forceinline__ void load_rows(uint8_t* dst, const CUtensorMap* map, uint32_t bar, uint32_t base, int mp, int row, int kb,
-                                          bool mirror, int rows64) {
+                                          bool mirror) {
   const int at = static_cast<int>(base) + (mirror ? row / 64 * mp + kb * 64 : kb * mp + row), next = mirror ? mp : 64;
   tma_load_2d_pair(dst, map, bar, 0, at);
-  if (rows64 == 2) tma_load_2d_pair(dst + 8192, map, bar, 0, at + next);
+  tma_load_2d_pair(dst + 8192, map, bar, 0, at + next);
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -233,14 +231,14 @@ __device__ __forceinline__ void read_param(const MuonMat& m, int64_t e, float (&
   }
 }
 
-// O's 32 rows from `row` on and 64 columns from `col` on (of X), of which this lane has one row in o.
+// O's 32 rows from `row` on and 32 columns from `col` on (of X), of which this lane has one row in o.
 template <int OUT>
-__device__ __forceinline__ void finish_part(const MuonMat& m, uint32_t seed, int row, int col, int lane, uint32_t staging, float (&o)[64]) {
+__device__ __forceinline__ void finish_part(const MuonMat& m, uint32_t seed, int row, int col, int lane, uint32_t staging, float (&o)[32]) {
   if (m.tall) {  // X's rows are the matrix's columns: 32 lanes write consecutive elements
     const int c = row + lane;
     if (c < m.cols) {
 #pragma unroll
-      for (int j0 = 0; j0 < 64; j0 += 16) {
+      for (int j0 = 0; j0 < 32; j0 += 16) {
         float w[16][1];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
@@ -256,39 +254,34 @@ __device__ __forceinline__ void finish_part(const MuonMat& m, uint32_t seed, int
     }
     return;
   }
-  // Through shared memory: rows of 64 fp32 numbers, 16-byte chunks swizzled by the row.
+  // Through shared memory: rows of 32 fp32 numbers, 16-byte chunks swizzled by the row.
 #pragma unroll
-  for (int k = 0; k < 16; ++k)
-    st_shared_v4(staging + lane * 256 + (k ^ (lane & 7)) * 16, __float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]),
+  for (int k = 0; k < 8; ++k)
+    st_shared_v4(staging + lane * 128 + (k ^ (lane & 7)) * 16, __float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]),
                  __float_as_uint(o[4 * k + 2]), __float_as_uint(o[4 * k + 3]));
   __syncwarp();
-  const int k = lane & 15, c = col + 4 * k;
+  const int k = lane & 7, c = col + 4 * k, r1 = lane >> 3;  // eight lanes a row
   if (m.dst_vec && c + 4 <= m.cols) {
+    float w[8][4];
 #pragma unroll
-    for (int r0 = 0; r0 < 32; r0 += 16) {
-      float w[8][4];
+    for (int q = 0; q < 8; ++q)
+      if (row + 4 * q + r1 < m.rows) read_param<OUT, 4>(m, static_cast<int64_t>(row + 4 * q + r1) * m.cols + c, w[q]);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const int r = row + r0 + 2 * q + (lane >> 4);
-        if (r < m.rows) read_param<OUT, 4>(m, static_cast<int64_t>(r) * m.cols + c, w[q]);
-      }
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const int rr = r0 + 2 * q + (lane >> 4);
-        const uint4 u = ld_shared_v4(staging + rr * 256 + (k ^ (rr & 7)) * 16);
-        float v[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
-        if (row + rr < m.rows) finish<OUT, 4>(m, seed, static_cast<int64_t>(row + rr) * m.cols + c, w[q], v);
-      }
+    for (int q = 0; q < 8; ++q) {
+      const int r = 4 * q + r1;
+      const uint4 u = ld_shared_v4(staging + r * 128 + (k ^ (r & 7)) * 16);
+      float v[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
+      if (row + r < m.rows) finish<OUT, 4>(m, seed, static_cast<int64_t>(row + r) * m.cols + c, w[q], v);
     }
   } else {
-    for (int rr = lane >> 4; rr < 32; rr += 2) {
-      const uint4 u = ld_shared_v4(staging + rr * 256 + (k ^ (rr & 7)) * 16);
+    for (int r = r1; r < 32; r += 4) {
+      const uint4 u = ld_shared_v4(staging + r * 128 + (k ^ (r & 7)) * 16);
       const float all[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if (row + rr < m.rows && c + j < m.cols) {
+        if (row + r < m.rows && c + j < m.cols) {
           float w[1] = {0.f}, v[1] = {all[j]};
-          const int64_t e = static_cast<int64_t>(row + rr) * m.cols + c + j;
+          const int64_t e = static_cast<int64_t>(row + r) * m.cols + c + j;
           read_param<OUT, 1>(m, e, w);
           finish<OUT, 1>(m, seed, e, w, v);
         }
@@ -357,16 +350,12 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
     // ------------------------------------------------------------------ scheduler (even CTA)
     if (lane == 0 && rank == 0) {
       const uint32_t peer_items = mapa_shared(smem_u32(items), 1), peer_ifull = mapa_shared(smem_u32(ifull), 1);
-      unsigned next = atomicAdd(p.ctrl, 1u);
       for (int k = 0;; ++k) {
         const int slot = k % kItemDepth;
         const uint32_t par = static_cast<uint32_t>(k / kItemDepth) & 1u;
         if (!wait_bounded<true>(iempty + slot, par ^ 1u, abort_flag, p.ctl, 42)) break;
-        const Item it = item_at(tab, p, next);
-        if (it.product >= 0) {
-          next = atomicAdd(p.ctrl, 1u);  // the next item, fetched ahead
-          if (!wait_count(p.ctrl + 1 + it.mat, it.need, abort_flag, p.ctl)) break;
-        }
+        const Item it = item_at(tab, p, atomicAdd(p.ctrl, 1u));
+        if (it.product >= 0 && !wait_count(p.ctrl + 1 + it.mat, it.need, abort_flag, p.ctl)) break;
         items[slot] = it;
         const uint32_t* w = reinterpret_cast<const uint32_t*>(&it);
         for (int q = 0; q < 8; ++q) st_cluster_u32(peer_items + slot * 32 + q * 4, w[q]);
@@ -394,12 +383,10 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
         if (it.product < 0) break;
         fence_proxy_async_global();  // what it reads was stored by TMA in other CTAs, or by the kernel before
         const MuonMat& m = tab.t[it.mat];
-        const int mp = m.mt * 256, nk = kblocks(m, it), cur = it.step & 1, wide = it.half ? 128 : 256;
+        const int mp = m.mt * 256, nk = kblocks(m, it), cur = it.step & 1;
         const uint32_t abase = it.product == kMuonGram ? m.x[cur] : it.product == kMuonPoly ? m.a : m.b;
         const uint32_t bbase = it.product == kMuonPoly ? m.a : m.x[cur];
-        const int arow = it.i * 256 + static_cast<int>(rank) * kBM, brow = it.j * wide + static_cast<int>(rank) * (wide / 2);
-        const int brows64 = it.half ? 1 : 2;
-        const uint32_t bytes = 2u * (A_BYTES + static_cast<uint32_t>(wide / 2) * kBK * 2u);  // both CTAs'
+        const int arow = it.i * 256 + static_cast<int>(rank) * kBM, brow = it.j * 256 + static_cast<int>(rank) * kBM;
         for (int kb = 0; kb < nk; ++kb) {
           if (!wait_bounded(empty + stage, phase ^ 1u, abort_flag, p.ctl, 44)) {
             ok = false;
@@ -408,13 +395,12 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
           uint8_t* sa = smem + stage * STAGE_BYTES;
           const uint32_t fb = full_lead + static_cast<uint32_t>(stage) * 8u;
           if (rank == 0) {
-            mbar_arrive_expect_tx(full + stage, bytes);
+            mbar_arrive_expect_tx(full + stage, 2 * STAGE_BYTES);  // both CTAs' bytes
             armed |= 1u << stage;
           }
-          load_rows(sa, &map, fb, abase, mp, arow, kb, it.product != kMuonGram && mirrored(kb, it.i), 2);
+          load_rows(sa, &map, fb, abase, mp, arow, kb, it.product != kMuonGram && mirrored(kb, it.i));
           // B of Apply is X, 64 of its rows and this CTA's columns, which lie like a mirror image's
-          load_rows(sa + A_BYTES, &map, fb, bbase, mp, brow, kb, it.product == kMuonApply || (it.product == kMuonPoly && mirrored(kb, it.big)),
-                    brows64);
+          load_rows(sa + A_BYTES, &map, fb, bbase, mp, brow, kb, it.product == kMuonApply || (it.product == kMuonPoly && mirrored(kb, it.j)));
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -443,7 +429,6 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
         mbar_arrive(iempty + slot);
         if (it.product < 0) break;
         const int nk = kblocks(tab.t[it.mat], it);
-        const uint32_t idesc0 = idesc_f16_f32(2 * kBM, it.half ? 128 : 256);
         for (int from = 0; ok && from < nk; from += kMuonDepth) {
           if (!wait_bounded(tempty + h, (uses[h] & 1u) ^ 1u, abort_flag, p.ctl, 46)) {
             ok = false;
@@ -459,8 +444,8 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
             tc_fence_after();
             const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES), sb = sa + A_BYTES;
             const bool amn = it.product != kMuonGram && mirrored(kb, it.i);
-            const bool bmn = it.product == kMuonApply || (it.product == kMuonPoly && mirrored(kb, it.big));
-            const uint32_t idesc = idesc0 | (amn ? kAMajor : 0u) | (bmn ? kBMajor : 0u);
+            const bool bmn = it.product == kMuonApply || (it.product == kMuonPoly && mirrored(kb, it.j));
+            const uint32_t idesc = idesc_f16_f32(2 * kBM, 256) | (amn ? kAMajor : 0u) | (bmn ? kBMajor : 0u);
 #pragma unroll
             for (int q = 0; q < kBK / 16; ++q)
               umma_bf16_pair(d, slice_desc(amn, sa, q), slice_desc(bmn, sb, q), idesc, (kb > from || q > 0) ? 1u : 0u);
@@ -487,7 +472,7 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
     const int e = warp - kEpiWarp0, q = warp & 3, hc = e >> 2;  // lane quarter, column half
     const uint32_t lead_tempty = mapa_shared(smem_u32(tempty), 0), lead_iempty = mapa_shared(smem_u32(iempty), 0);
     uint8_t* staging = staging_all + e * 2 * PART_BYTES;
-    const uint32_t stage_a = smem_u32(staging), line = stage_a + lane * 128;  // this lane's row of the first term
+    const uint32_t stage_a = smem_u32(staging), line = stage_a + lane * 64;  // this lane's row of the first term
     uint64_t* loads = parts + e;
     uint32_t uses[2] = {0u, 0u}, loaded = 0;
     int h = 0;
@@ -508,23 +493,23 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
       }
       if (it.product < 0) break;
       const MuonMat& m = tab.t[it.mat];
-      const int mp = m.mt * 256, nk = kblocks(m, it), cur = it.step & 1, units = it.half ? 1 : 2;
+      const int mp = m.mt * 256, nk = kblocks(m, it), cur = it.step & 1;
       const bool apply = it.product == kMuonApply, last = apply && it.step + 1 == p.steps, two = apply;
       const uint32_t out = it.product == kMuonGram ? m.a : it.product == kMuonPoly ? m.b : m.x[cur ^ 1];
       const uint32_t add = it.product == kMuonPoly ? m.a : m.x[cur];
       const int row = it.i * 256 + static_cast<int>(rank) * kBM + q * 32;
-      const int col0 = (2 * it.j + hc) * 64 * units;
-      auto part_row = [&](uint32_t base, int u) { return static_cast<int>(base) + (col0 / 64 + u) * mp + row; };
+      const int col0 = (2 * it.j + hc) * 128;
+      auto part_row = [&](uint32_t base, int u) { return static_cast<int>(base) + (col0 / 64 + u / 2) * mp + row; };
       auto load_part = [&](int u) {
         mbar_arrive_expect_tx(loads, two ? 2 * PART_BYTES : PART_BYTES);
-        tma_load_2d(staging, &part_map, loads, 0, part_row(add, u));
-        if (two) tma_load_2d(staging + PART_BYTES, &part_map, loads, 0, part_row(m.lo, u));
+        tma_load_2d(staging, &part_map, loads, (u & 1) * 32, part_row(add, u));
+        if (two) tma_load_2d(staging + PART_BYTES, &part_map, loads, (u & 1) * 32, part_row(m.lo, u));
       };
       if (lane == 0 && it.product != kMuonGram) {
         fence_proxy_async_global();
         load_part(0);
       }
-      // Of a long sum all but the last stretch, added up in the workspace: [BN / 64][8][32 lanes] of this warp.
+      // Of a long sum all but the last stretch, added up in the workspace: [kUnits][8][32 lanes] of this warp.
       const bool deep = nk > kMuonDepth;
       float4* scratch = nullptr;
       if (deep) scratch = reinterpret_cast<float4*>(p.scratch + static_cast<size_t>(blockIdx.x) * kMuonScratch + static_cast<size_t>(e) * (kMuonScratch / kEpiWarps)) + lane;
@@ -533,9 +518,9 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
         got = __all_sync(0xffffffffu, wait_bounded(tfull + h, uses[h] & 1u, abort_flag, p.ctl, 49));
         if (!got) break;
         tc_fence_after();
-        for (int c = 0; c < 2 * units; ++c) {
+        for (int c = 0; c < kUnits; ++c) {
           float v[32];
-          tmem_ld32(lanes + static_cast<uint32_t>(h * 256 + hc * 64 * units + c * 32), v);
+          tmem_ld32(lanes + static_cast<uint32_t>(h * 256 + hc * 128 + c * 32), v);
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -558,20 +543,19 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after();
       const float acc = p.acc[it.step][it.product], fac = p.add[it.step][it.product];
-      for (int u = 0; u < units; ++u) {
-        float v[64];
-        tmem_ld32_at(lanes + static_cast<uint32_t>(h * 256 + (hc * units + u) * 64), v);
-        tmem_ld32_at(lanes + static_cast<uint32_t>(h * 256 + (hc * units + u) * 64 + 32), v + 32);
+      for (int u = 0; u < kUnits; ++u) {
+        float v[32];
+        tmem_ld32(lanes + static_cast<uint32_t>(h * 256 + hc * 128 + u * 32), v);
         tmem_ld_wait();
-        if (u == units - 1) {  // the half is free for the next item but one
+        if (u == kUnits - 1) {  // the half is free for the next item but one
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_remote(lead_tempty + h * 8);
         }
         if (deep) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float4 y = scratch[(u * 16 + j) * 32];
+          for (int j = 0; j < 8; ++j) {
+            const float4 y = scratch[(u * 8 + j) * 32];
             v[4 * j] += y.x, v[4 * j + 1] += y.y, v[4 * j + 2] += y.z, v[4 * j + 3] += y.w;
           }
         }
@@ -584,8 +568,8 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
           __syncwarp();
         }
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {  // 16-byte chunks, where the 128-byte swizzle has them
-          const uint32_t at = line + static_cast<uint32_t>((c ^ (lane & 7)) * 16);
+        for (int c = 0; c < 4; ++c) {  // 16-byte chunks, where the 64-byte swizzle has them
+          const uint32_t at = line + static_cast<uint32_t>((c ^ ((lane >> 1) & 3)) * 16);
           float x[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) x[j] = v[8 * c + j] * acc;
@@ -625,11 +609,11 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
         if (last) {
           __syncwarp();  // every lane has read its part of the staging, which is written again
 #pragma unroll
-          for (int j = 0; j < 64; ++j) {  // as fp16, like every X
+          for (int j = 0; j < 32; ++j) {  // as fp16, like every X
             v[j] = __half2float(__float2half_rn(v[j])) * hyper.unscale;
           }
-          if (!skip) finish_part<OUT>(m, hyper.seed, row, col0 + u * 64, lane, stage_a, v);
-          if (u + 1 < units) {
+          if (!skip) finish_part<OUT>(m, hyper.seed, row, col0 + u * 32, lane, stage_a, v);
+          if (u + 1 < kUnits) {
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) load_part(u + 1);
@@ -639,10 +623,10 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          tma_store_2d(&part_map, staging, 0, part_row(out, u));
-          if (apply) tma_store_2d(&part_map, staging + PART_BYTES, 0, part_row(m.lo, u));
+          tma_store_2d(&part_map, staging, (u & 1) * 32, part_row(out, u));
+          if (apply) tma_store_2d(&part_map, staging + PART_BYTES, (u & 1) * 32, part_row(m.lo, u));
           bulk_commit_group();
-          if (u + 1 < units && it.product != kMuonGram) {
+          if (u + 1 < kUnits && it.product != kMuonGram) {
             bulk_wait_group_read<0>();
             load_part(u + 1);
           }
@@ -717,10 +701,9 @@ cudaError_t muon_pipe_prepare(int* max_clusters) {
 
 cudaError_t launch_muon_pipe(const CUtensorMap& load, const CUtensorMap& part, const MuonTable& t, const MuonPipe& p, const MuonHyper& h,
                              int out, int clusters, cudaStream_t stream) {
-  const int64_t sym = static_cast<int64_t>(p.sym) << p.sym_half, rect = static_cast<int64_t>(p.rect) << p.rect_half;
-  const int64_t most = sym > rect ? sym : rect;  // items that can run at once
+  const int most = p.sym > p.rect ? p.sym : p.rect;  // items that can run at once
   cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = pipe_config(attr, static_cast<int>(most < clusters ? most : clusters), stream);
+  cudaLaunchConfig_t cfg = pipe_config(attr, most < clusters ? most : clusters, stream);
   switch (out) {
     case kMuonOutBf16: return cudaLaunchKernelEx(&cfg, muon_pipe_kernel<kMuonOutBf16>, load, part, t, p, h);
     case kMuonOutF16: return cudaLaunchKernelEx(&cfg, muon_pipe_kernel<kMuonOutF16>, load, part, t, p, h);
