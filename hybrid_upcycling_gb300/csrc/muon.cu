@@ -174,22 +174,26 @@ __device__ __forceinline__ float2 scale_factors(const MuonMat& t, const MuonHype
   return make_float2(static_cast<float>(f / first), static_cast<float>(first));
 }
 
-__device__ __forceinline__ void put_panel(const MuonHyper& h, const MuonMat& t, size_t at, const float* u, float2 f) {
+// Eight columns from c on of X's row r.
+__device__ __forceinline__ void put_x(const MuonHyper& h, const MuonMat& t, int r, int c, const float* u, float2 f) {
   uint32_t hi[4], lo[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float a = u[2 * j] * f.y * f.x, b = u[2 * j + 1] * f.y * f.x;
     const __half2 p = __floats2half2_rn(a, b);
-    const float2 r = __half22float2(p);
-    const __half2 q = __floats2half2_rn(a - r.x, b - r.y);
+    const float2 r2 = __half22float2(p);
+    const __half2 q = __floats2half2_rn(a - r2.x, b - r2.y);
     hi[j] = *reinterpret_cast<const uint32_t*>(&p);
     lo[j] = *reinterpret_cast<const uint32_t*>(&q);
   }
+  const size_t at = (static_cast<size_t>(c >> 6) * t.mt * 256 + r) * 128 + (c & 63) * 2;
   *reinterpret_cast<uint4*>(h.ws + static_cast<size_t>(t.x[0]) * 128 + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-  *reinterpret_cast<uint4*>(h.ws + static_cast<size_t>(t.lo) * 128 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  const int warp = (r >> 5 & 3) + (c >> 7 & 1) * 4;
+  reinterpret_cast<uint4*>(h.ws + static_cast<size_t>(t.lo) * 128)[muon_lo_chunk((c >> 8) * t.mt + (r >> 8), r >> 7 & 1, warp) +
+                                                                  (c >> 3 & 15) * 32 + (r & 31)] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
 }
 
-// X's panels from the scaled update, with their zero padding: 64 x 64 blocks of the matrix, kFillBlocks a thread block along its
+// X's panels from the scaled update, padded with zeros to whole k-blocks: 64 x 64 blocks of the matrix, kFillBlocks a thread block along its
 // rows; a tall matrix is transposed through shared memory.
 constexpr int kFillBlocks = 8;
 template <typename T>
@@ -201,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) muon_fill_kernel(const __grid_consta
   const bool skipped = h.muon && !gradient_factor(h, gs);
   float2 f = make_float2(0.f, 0.f);
   if (!skipped) f = scale_factors(t, h, red);
-  const int wide = (t.tall ? t.mt : t.nt) * 4, mp = t.mt * 256, local = static_cast<int>(blockIdx.x - t.fill0);
+  const int wide = t.tall ? t.km : t.kn, local = static_cast<int>(blockIdx.x - t.fill0);
   const int per = (wide + kFillBlocks - 1) / kFillBlocks;
   const int br = local / per, bc0 = (local - br * per) * kFillBlocks;
   for (int bc = bc0; bc < min(wide, bc0 + kFillBlocks); ++bc) {
@@ -222,7 +226,7 @@ __global__ void __launch_bounds__(kThreads) muon_fill_kernel(const __grid_consta
 #pragma unroll
         for (int j = 0; j < 8; ++j) tile[rr][cc + j] = u[j];
       } else {
-        put_panel(h, t, (static_cast<size_t>(bc) * mp + r) * 128 + cc * 2, u, f);
+        put_x(h, t, r, c, u, f);
       }
     }
     if (t.tall) {
@@ -233,7 +237,7 @@ __global__ void __launch_bounds__(kThreads) muon_fill_kernel(const __grid_consta
         float u[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) u[j] = tile[xc + j][xr];
-        put_panel(h, t, (static_cast<size_t>(br) * mp + bc * 64 + xr) * 128 + xc * 2, u, f);
+        put_x(h, t, bc * 64 + xr, br * 64 + xc, u, f);
       }
       __syncthreads();
     }
@@ -243,7 +247,7 @@ __global__ void __launch_bounds__(kThreads) muon_fill_kernel(const __grid_consta
 }  // namespace
 
 uint32_t muon_fill_blocks(const MuonMat& t) {
-  const int down = (t.tall ? t.nt : t.mt) * 4, across = (t.tall ? t.mt : t.nt) * 4;  // 64 x 64 blocks
+  const int down = t.tall ? t.kn : t.km, across = t.tall ? t.km : t.kn;  // 64 x 64 blocks
   return static_cast<uint32_t>(down) * static_cast<uint32_t>((across + kFillBlocks - 1) / kFillBlocks);
 }
 

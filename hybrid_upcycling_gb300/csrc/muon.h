@@ -5,7 +5,8 @@
 // rows, with `base` its first row of 128 bytes, lies in row base + (c / 64) mp + r, column c % 64. So the whole workspace is
 // one tensor of 64 columns for the TMA loads, and a block of 64 rows and 64 columns, 8 KiB in one piece, serves as an operand
 // whose rows are summed over as well as one whose columns are. X has at most as many rows as columns (a tall matrix is
-// transposed) and is padded with zeros to multiples of 256; the padding stays zero in every product.
+// transposed) and is padded with zeros to multiples of 64, which stay zero in every product. Tiles reach to multiples of 256; what
+// lies there is neither written nor has a part in any other row or column.
 #pragma once
 
 #include <cstdint>
@@ -19,6 +20,13 @@ constexpr int kMuonParts = 1024;  // partial sums of squares of a matrix at most
 constexpr int kMuonSums = 3;      // of magnitudes near 2^-80, 1 and 2^80
 
 constexpr int kMuonStepsMax = 32;
+
+// X's second term lies in the order in which the epilogue's lanes take it: [256 x 256 tile][CTA of the pair: 128 rows][warp: 32
+// rows (warp % 4) and 128 columns (warp / 4)][32 columns][8 columns][row], in chunks of 16 bytes (8 columns).
+constexpr int kMuonLoUnits = 4;
+__host__ __device__ constexpr int64_t muon_lo_chunk(int tile, int rank, int warp) {
+  return ((static_cast<int64_t>(tile) * 2 + rank) * 8 + warp) * (kMuonLoUnits * 4 * 32);
+}
 
 // One matrix of a group.
 struct MuonMat {

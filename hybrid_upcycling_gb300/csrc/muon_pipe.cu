@@ -23,8 +23,9 @@
 //
 // A CTA pair takes an item: warp 2 of the even CTA fetches it, waits for its matrix and publishes it to both CTAs; warp 0 of each CTA
 // loads by TMA; one thread of warp 1 of the even CTA issues the products; eight warps of each CTA take the sums out of TMEM, whose two
-// halves alternate. These read and write X, A and B through shared memory by TMA, 32 rows and 32 columns at a time: straight
-// from the registers, where a lane has a row, every access touches 32 lines, and the tiles of Apply took twice as long.
+// halves alternate. These read and write X, A and B through shared memory by TMA, 32 rows and 32 columns at a time, the
+// next part on its way while one is formed: straight from the registers, where a lane has a row, every access touches 32 lines, and
+// the tiles of Apply took twice as long.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -38,12 +39,12 @@ constexpr int A_BYTES = kBM * kBK * 2;      // 16 KB: this CTA's 128 rows of A
 constexpr int STAGE_BYTES = 2 * A_BYTES;    // and 128 rows (columns) of B
 constexpr int STAGES = 6;
 constexpr int PART_BYTES = 2048;            // 32 rows x 32 columns of fp16
-constexpr int STAGING_BYTES = kEpiWarps * 2 * PART_BYTES;  // two terms a warp, or 32 x 32 fp32 numbers
-constexpr int kUnits = 4;                   // such parts of a warp's 32 rows x 128 columns
+constexpr int STAGING_BYTES = kEpiWarps * 2 * PART_BYTES;  // two parts a warp, or 32 x 32 fp32 numbers
+constexpr int kUnits = kMuonLoUnits;        // such parts of a warp's 32 rows x 128 columns
 constexpr int kItemDepth = 2;
 constexpr int ITEM_OFF = STAGES * STAGE_BYTES + STAGING_BYTES;
 constexpr int BAR_OFF = ITEM_OFF + kItemDepth * 32;
-constexpr int NBARS = 2 * STAGES + 4 + 2 * kItemDepth + kEpiWarps + 1;  // full, empty, tfull[2], tempty[2], ifull, iempty, parts, drain
+constexpr int NBARS = 2 * STAGES + 4 + 2 * kItemDepth + 2 * kEpiWarps + 1;  // full, empty, tfull[2], tempty[2], ifull, iempty, parts, drain
 constexpr int SMEM = 1024 + BAR_OFF + NBARS * 8 + 16;
 static_assert(SMEM <= 232448, "shared memory budget");
 constexpr int kItemConsumers = 2 * (1 + kEpiWarps) + 1;  // producers and epilogue warps of both CTAs, the issuer
@@ -305,8 +306,8 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
   uint64_t* tempty = tfull + 2;                                   // even CTA: half read by both CTAs
   uint64_t* ifull = tempty + 2;                                   // both CTAs: item slot published
   uint64_t* iempty = ifull + kItemDepth;                          // even CTA: item slot released
-  uint64_t* parts = iempty + kItemDepth;                          // an epilogue warp's loads
-  uint64_t* drain = parts + kEpiWarps;
+  uint64_t* parts = iempty + kItemDepth;                          // an epilogue warp's loads, two each
+  uint64_t* drain = parts + 2 * kEpiWarps;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -326,7 +327,7 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
       mbar_init(ifull + k, 1);
       mbar_init(iempty + k, kItemConsumers);
     }
-    for (int w = 0; w < kEpiWarps; ++w) mbar_init(parts + w, 1);
+    for (int w = 0; w < 2 * kEpiWarps; ++w) mbar_init(parts + w, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -473,8 +474,8 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
     const uint32_t lead_tempty = mapa_shared(smem_u32(tempty), 0), lead_iempty = mapa_shared(smem_u32(iempty), 0);
     uint8_t* staging = staging_all + e * 2 * PART_BYTES;
     const uint32_t stage_a = smem_u32(staging), line = stage_a + lane * 64;  // this lane's row of the first term
-    uint64_t* loads = parts + e;
-    uint32_t uses[2] = {0u, 0u}, loaded = 0;
+    uint64_t* loads = parts + 2 * e;
+    uint32_t uses[2] = {0u, 0u}, loaded[2] = {0u, 0u};
     int h = 0;
     bool skip = false;  // a Muon step whose norm is not finite changes nothing
     if (hyper.norm != nullptr) skip = !isfinite(hyper.norm[0]);
@@ -494,20 +495,32 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
       if (it.product < 0) break;
       const MuonMat& m = tab.t[it.mat];
       const int mp = m.mt * 256, nk = kblocks(m, it), cur = it.step & 1;
-      const bool apply = it.product == kMuonApply, last = apply && it.step + 1 == p.steps, two = apply;
+      const bool apply = it.product == kMuonApply, last = apply && it.step + 1 == p.steps;
       const uint32_t out = it.product == kMuonGram ? m.a : it.product == kMuonPoly ? m.b : m.x[cur ^ 1];
       const uint32_t add = it.product == kMuonPoly ? m.a : m.x[cur];
-      const int row = it.i * 256 + static_cast<int>(rank) * kBM + q * 32;
-      const int col0 = (2 * it.j + hc) * 128;
+      const int row = it.i * 256 + static_cast<int>(rank) * kBM + q * 32, col0 = (2 * it.j + hc) * 128;
+      // Rows and columns behind the last 64-deep k-block are never read as such: their parts are left out.
+      const int wide = (apply ? m.kn : m.km) * 64 - col0;
+      const int nu = row >= m.km * 64 || wide <= 0 ? 0 : wide >= 32 * kUnits ? kUnits : wide / 32;
+      // X's second term, which only the epilogue of the same tile reads again, lies in the order of its lanes.
+      uint4* lo = reinterpret_cast<uint4*>(hyper.ws + static_cast<size_t>(m.lo) * 128) +
+                  muon_lo_chunk(it.j * m.mt + it.i, static_cast<int>(rank), e) + lane;
+      uint4 ahead[4];
+      auto read_lo = [&](int u) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) ahead[c] = __ldcg(lo + (u * 4 + c) * 32);  // written on another SM: not from L1
+      };
       auto part_row = [&](uint32_t base, int u) { return static_cast<int>(base) + (col0 / 64 + u / 2) * mp + row; };
       auto load_part = [&](int u) {
-        mbar_arrive_expect_tx(loads, two ? 2 * PART_BYTES : PART_BYTES);
-        tma_load_2d(staging, &part_map, loads, (u & 1) * 32, part_row(add, u));
-        if (two) tma_load_2d(staging + PART_BYTES, &part_map, loads, (u & 1) * 32, part_row(m.lo, u));
+        mbar_arrive_expect_tx(loads + (u & 1), PART_BYTES);
+        tma_load_2d(staging + (u & 1) * PART_BYTES, &part_map, loads + (u & 1), (u & 1) * 32, part_row(add, u));
       };
-      if (lane == 0 && it.product != kMuonGram) {
-        fence_proxy_async_global();
-        load_part(0);
+      if (nu > 0 && it.product != kMuonGram) {
+        if (lane == 0) {
+          fence_proxy_async_global();
+          load_part(0);
+        }
+        if (apply) read_lo(0);
       }
       // Of a long sum all but the last stretch, added up in the workspace: [kUnits][8][32 lanes] of this warp.
       const bool deep = nk > kMuonDepth;
@@ -543,15 +556,19 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after();
       const float acc = p.acc[it.step][it.product], fac = p.add[it.step][it.product];
-      for (int u = 0; u < kUnits; ++u) {
+      for (int u = 0; u < nu; ++u) {
+        if (lane == 0) {  // the part before last has left this one's place, or the part before the next one's
+          if (it.product == kMuonGram) {
+            bulk_wait_group_read<1>();
+          } else if (u + 1 < nu && !last) {
+            bulk_wait_group_read<0>();
+            load_part(u + 1);
+          }
+        }
+        __syncwarp();
         float v[32];
         tmem_ld32(lanes + static_cast<uint32_t>(h * 256 + hc * 128 + u * 32), v);
         tmem_ld_wait();
-        if (u == kUnits - 1) {  // the half is free for the next item but one
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_remote(lead_tempty + h * 8);
-        }
         if (deep) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -559,38 +576,40 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
             v[4 * j] += y.x, v[4 * j + 1] += y.y, v[4 * j + 2] += y.z, v[4 * j + 3] += y.w;
           }
         }
-        if (it.product != kMuonGram) {
-          got = __all_sync(0xffffffffu, wait_bounded(loads, loaded & 1u, abort_flag, p.ctl, 51));
-          if (!got) break;
-          ++loaded;
-        } else if (u > 0) {
-          if (lane == 0) bulk_wait_group_read<0>();  // the store of the part before has read the staging
-          __syncwarp();
+        uint32_t l[16];
+        if (apply) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) l[4 * c] = ahead[c].x, l[4 * c + 1] = ahead[c].y, l[4 * c + 2] = ahead[c].z, l[4 * c + 3] = ahead[c].w;
+          if (u + 1 < nu) read_lo(u + 1);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 16; ++c) l[c] = 0u;
         }
+        if (it.product != kMuonGram) {
+          got = __all_sync(0xffffffffu, wait_bounded(loads + (u & 1), loaded[u & 1] & 1u, abort_flag, p.ctl, 51));
+          if (!got) break;
+          ++loaded[u & 1];
+        }
+        const uint32_t place = line + static_cast<uint32_t>((u & 1) * PART_BYTES);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {  // 16-byte chunks, where the 64-byte swizzle has them
-          const uint32_t at = line + static_cast<uint32_t>((c ^ ((lane >> 1) & 3)) * 16);
+          const uint32_t at = place + static_cast<uint32_t>((c ^ ((lane >> 1) & 3)) * 16);
           float x[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) x[j] = v[8 * c + j] * acc;
           if (it.product != kMuonGram) {
             const uint4 w = ld_shared_v4(at);
             const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-            uint32_t ll[4] = {0u, 0u, 0u, 0u};
-            if (apply) {
-              const uint4 l = ld_shared_v4(at + PART_BYTES);
-              ll[0] = l.x, ll[1] = l.y, ll[2] = l.z, ll[3] = l.w;
-            }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float2 f = unpack_f16x2(ww[j]), g = unpack_f16x2(ll[j]);
+              const float2 f = unpack_f16x2(ww[j]), g = unpack_f16x2(l[4 * c + j]);
               x[2 * j] = fmaf(f.x + g.x, fac, x[2 * j]);
               x[2 * j + 1] = fmaf(f.y + g.y, fac, x[2 * j + 1]);
             }
           }
           if (last) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[8 * c + j] = x[j];
+            for (int j = 0; j < 8; ++j) v[8 * c + j] = __half2float(__float2half_rn(x[j])) * hyper.unscale;  // as fp16, like every X
           } else {
             uint32_t o[4];
 #pragma unroll
@@ -602,47 +621,38 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
                 const float2 f = unpack_f16x2(o[j]);
                 o[j] = pack_f16x2(x[2 * j] - f.x, x[2 * j + 1] - f.y);
               }
-              st_shared_v4(at + PART_BYTES, o[0], o[1], o[2], o[3]);
+              lo[(u * 4 + c) * 32] = make_uint4(o[0], o[1], o[2], o[3]);
             }
           }
         }
         if (last) {
           __syncwarp();  // every lane has read its part of the staging, which is written again
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {  // as fp16, like every X
-            v[j] = __half2float(__float2half_rn(v[j])) * hyper.unscale;
-          }
           if (!skip) finish_part<OUT>(m, hyper.seed, row, col0 + u * 32, lane, stage_a, v);
-          if (u + 1 < kUnits) {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) load_part(u + 1);
-          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && u + 1 < nu) load_part(u + 1);
           continue;
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          tma_store_2d(&part_map, staging, (u & 1) * 32, part_row(out, u));
-          if (apply) tma_store_2d(&part_map, staging + PART_BYTES, (u & 1) * 32, part_row(m.lo, u));
+          tma_store_2d(&part_map, staging + (u & 1) * PART_BYTES, (u & 1) * 32, part_row(out, u));
           bulk_commit_group();
-          if (u + 1 < kUnits && it.product != kMuonGram) {
-            bulk_wait_group_read<0>();
-            load_part(u + 1);
-          }
         }
       }
       if (!got) break;
+      tc_fence_before();  // the half is free for the next item but one
+      __syncwarp();       // and every lane's second terms are stored
+      if (lane == 0) {
+        mbar_arrive_remote(lead_tempty + h * 8);
+        if (!last) {
+          bulk_wait_group<0>();  // the stores are complete
+          fence_proxy_async_global();
+          red_release_gpu_add(p.ctrl + 1 + it.mat, 1u);
+        }
+      }
       ++uses[h];
       h ^= 1;
-      if (last) {
-        fence_proxy_async_smem();  // the staging goes back to TMA
-        __syncwarp();
-      } else if (lane == 0) {
-        bulk_wait_group<0>();  // the stores are complete
-        fence_proxy_async_global();
-        red_release_gpu_add(p.ctrl + 1 + it.mat, 1u);
-      }
       __syncwarp();
     }
     if (lane == 0) bulk_wait_group<0>();
