@@ -35,10 +35,9 @@ unsigned long long wait_limit_ns();
 // The current device's state, set up on first use; HYLO_ERR_ARCH if it is not sm_103.
 hylo_status current_device(DeviceState** out);
 
-// 2-D tensor map, zero fill outside the tensor.
+// 2-D tensor map, 128-byte swizzle, zero fill outside the tensor.
 hylo_status make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t inner, uint64_t outer,
-                     uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
-                     CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
+                     uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer);
 // 3-D tensor map [outer2][outer1][inner] (contiguous), zero fill outside.
 hylo_status make_map_3d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t inner, uint64_t outer1,
                         uint64_t outer2, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer1,

@@ -199,10 +199,8 @@ hylo_status run(const T* list, int count, int dtype, int out_dtype, bool masters
       p.rect += t.mt * t.nt;
     }
     if (tab.count == 0) continue;
-    CUtensorMap load, part;
-    if ((st = make_map(&load, ws, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 64, row, 128, 64, 64)) != HYLO_OK ||
-        (st = make_map(&part, ws, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 64, row, 128, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) != HYLO_OK)
-      return st;
+    CUtensorMap load;
+    if ((st = make_map(&load, ws, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 64, row, 128, 64, 64)) != HYLO_OK) return st;
     h.sums = reinterpret_cast<float*>(h.ws + group.sums_at());
     h.ctrl = p.ctrl = reinterpret_cast<unsigned*>(h.ws + group.ctrl_at());
     p.scratch = h.ws + group.scratch_at();
@@ -218,7 +216,7 @@ hylo_status run(const T* list, int count, int dtype, int out_dtype, bool masters
                             : out_dtype == HYLO_F32 ? kMuonParamF32 : masters ? kMuonParamMaster : kMuonParamBf16;
     cudaError_t e = launch_muon_sums(tab, h, dtype, sums, stream);
     if (e == cudaSuccess) e = launch_muon_fill(tab, h, dtype, fill, stream);
-    if (e == cudaSuccess) e = launch_muon_pipe(load, part, tab, p, h, out, dev->muon_clusters, stream);
+    if (e == cudaSuccess) e = launch_muon_pipe(load, tab, p, h, out, dev->muon_clusters, stream);
     if (e != cudaSuccess) return cuda_fail(e, "launch orthogonalised updates");
   }
   return HYLO_OK;

@@ -189,8 +189,8 @@ __device__ __forceinline__ void put_x(const MuonHyper& h, const MuonMat& t, int 
   const size_t at = (static_cast<size_t>(c >> 6) * t.mt * 256 + r) * 128 + (c & 63) * 2;
   *reinterpret_cast<uint4*>(h.ws + static_cast<size_t>(t.x[0]) * 128 + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
   const int warp = (r >> 5 & 3) + (c >> 7 & 1) * 4;
-  reinterpret_cast<uint4*>(h.ws + static_cast<size_t>(t.lo) * 128)[muon_lo_chunk((c >> 8) * t.mt + (r >> 8), r >> 7 & 1, warp) +
-                                                                  (c >> 3 & 15) * 32 + (r & 31)] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  const int64_t sector = muon_lo_sector((c >> 8) * t.mt + (r >> 8), r >> 7 & 1, warp) + (c >> 4 & 7) * 32 + (r & 31);
+  *reinterpret_cast<uint4*>(h.ws + static_cast<size_t>(t.lo) * 128 + sector * 32 + (c & 8) * 2) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
 }
 
 // X's panels from the scaled update, padded with zeros to whole k-blocks: 64 x 64 blocks of the matrix, kFillBlocks a thread block along its

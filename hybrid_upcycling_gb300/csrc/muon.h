@@ -22,10 +22,10 @@ constexpr int kMuonSums = 3;      // of magnitudes near 2^-80, 1 and 2^80
 constexpr int kMuonStepsMax = 32;
 
 // X's second term lies in the order in which the epilogue's lanes take it: [256 x 256 tile][CTA of the pair: 128 rows][warp: 32
-// rows (warp % 4) and 128 columns (warp / 4)][32 columns][8 columns][row], in chunks of 16 bytes (8 columns).
+// rows (warp % 4) and 128 columns (warp / 4)][32 columns][16 columns][row], in sectors of 32 bytes (16 columns).
 constexpr int kMuonLoUnits = 4;
-__host__ __device__ constexpr int64_t muon_lo_chunk(int tile, int rank, int warp) {
-  return ((static_cast<int64_t>(tile) * 2 + rank) * 8 + warp) * (kMuonLoUnits * 4 * 32);
+__host__ __device__ constexpr int64_t muon_lo_sector(int tile, int rank, int warp) {
+  return ((static_cast<int64_t>(tile) * 2 + rank) * 8 + warp) * (kMuonLoUnits * 2 * 32);
 }
 
 // One matrix of a group.
@@ -87,9 +87,9 @@ uint32_t muon_fill_blocks(const MuonMat& t);
 cudaError_t launch_muon_sums(const MuonTable& t, const MuonHyper& h, int dtype, uint32_t ctas, cudaStream_t stream);
 cudaError_t launch_muon_fill(const MuonTable& t, const MuonHyper& h, int dtype, uint32_t ctas, cudaStream_t stream);
 // All products of all steps; the last one writes the results or steps the parameters (`out`). load: boxes of 64 columns and 64
-// rows of the workspace; part: 32 columns and 32 rows, 64-byte swizzle.
+// rows of the workspace.
 cudaError_t muon_pipe_prepare(int* max_clusters);
-cudaError_t launch_muon_pipe(const CUtensorMap& load, const CUtensorMap& part, const MuonTable& t, const MuonPipe& p, const MuonHyper& h,
+cudaError_t launch_muon_pipe(const CUtensorMap& load, const MuonTable& t, const MuonPipe& p, const MuonHyper& h,
                              int out, int clusters, cudaStream_t stream);
 
 }  // namespace hylo

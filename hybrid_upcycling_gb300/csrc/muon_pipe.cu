@@ -23,9 +23,9 @@
 //
 // A CTA pair takes an item: warp 2 of the even CTA fetches it, waits for its matrix and publishes it to both CTAs; warp 0 of each CTA
 // loads by TMA; one thread of warp 1 of the even CTA issues the products; eight warps of each CTA take the sums out of TMEM, whose two
-// halves alternate. These read and write X, A and B through shared memory by TMA, 32 rows and 32 columns at a time, the
-// next part on its way while one is formed: straight from the registers, where a lane has a row, every access touches 32 lines, and
-// the tiles of Apply took twice as long.
+// halves alternate. These add X or A and write the next X, A or B, 32 rows and 32 columns at a time, the next ones on their way, with a
+// lane to a row and 32 bytes, a whole sector, an access. (With 16 bytes an access and nothing ahead the tiles of Apply took twice as
+// long; parts through shared memory by TMA are as fast as this where there is much to do and slower where there is little.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -35,16 +35,17 @@ namespace hylo {
 namespace {
 
 constexpr int kEpiWarps = 8, kEpiWarp0 = 4, kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+constexpr int kRegsControl = 96, kRegsEpilogue = 200;  // per thread of warpgroup 0, and of the two of the epilogue
+static_assert(128 * kRegsControl + 256 * kRegsEpilogue <= kThreads * 168, "register split");
 constexpr int A_BYTES = kBM * kBK * 2;      // 16 KB: this CTA's 128 rows of A
 constexpr int STAGE_BYTES = 2 * A_BYTES;    // and 128 rows (columns) of B
 constexpr int STAGES = 6;
-constexpr int PART_BYTES = 2048;            // 32 rows x 32 columns of fp16
-constexpr int STAGING_BYTES = kEpiWarps * 2 * PART_BYTES;  // two parts a warp, or 32 x 32 fp32 numbers
+constexpr int STAGING_BYTES = kEpiWarps * 4096;  // 32 x 32 fp32 numbers a warp
 constexpr int kUnits = kMuonLoUnits;        // such parts of a warp's 32 rows x 128 columns
 constexpr int kItemDepth = 2;
 constexpr int ITEM_OFF = STAGES * STAGE_BYTES + STAGING_BYTES;
 constexpr int BAR_OFF = ITEM_OFF + kItemDepth * 32;
-constexpr int NBARS = 2 * STAGES + 4 + 2 * kItemDepth + 2 * kEpiWarps + 1;  // full, empty, tfull[2], tempty[2], ifull, iempty, parts, drain
+constexpr int NBARS = 2 * STAGES + 4 + 2 * kItemDepth + 1;  // full, empty, tfull[2], tempty[2], ifull, iempty, drain
 constexpr int SMEM = 1024 + BAR_OFF + NBARS * 8 + 16;
 static_assert(SMEM <= 232448, "shared memory budget");
 constexpr int kItemConsumers = 2 * (1 + kEpiWarps) + 1;  // producers and epilogue warps of both CTAs, the issuer
@@ -153,6 +154,15 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ float2 unpack_f16x2(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+// 32 bytes, a whole sector, a lane. The load is coherent: the bytes may have been written on another SM.
+__device__ __forceinline__ void ld_sector(const void* p, uint32_t* r) {
+  asm volatile("ld.relaxed.gpu.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]) : "l"(p) : "memory");
+}
+__device__ __forceinline__ void st_sector(void* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               :: "l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
+}
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
@@ -294,8 +304,8 @@ __device__ __forceinline__ void finish_part(const MuonMat& m, uint32_t seed, int
 
 template <int OUT>
 __global__ void __launch_bounds__(kThreads, 1)
-muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap part_map, const __grid_constant__ MuonTable tab,
-                 const __grid_constant__ MuonPipe p, const MuonHyper hyper) {
+muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ MuonTable tab, const __grid_constant__ MuonPipe p,
+                  const MuonHyper hyper) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* staging_all = smem + STAGES * STAGE_BYTES;
@@ -306,8 +316,7 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
   uint64_t* tempty = tfull + 2;                                   // even CTA: half read by both CTAs
   uint64_t* ifull = tempty + 2;                                   // both CTAs: item slot published
   uint64_t* iempty = ifull + kItemDepth;                          // even CTA: item slot released
-  uint64_t* parts = iempty + kItemDepth;                          // an epilogue warp's loads, two each
-  uint64_t* drain = parts + 2 * kEpiWarps;
+  uint64_t* drain = iempty + kItemDepth;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -327,15 +336,11 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
       mbar_init(ifull + k, 1);
       mbar_init(iempty + k, kItemConsumers);
     }
-    for (int w = 0; w < 2 * kEpiWarps; ++w) mbar_init(parts + w, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (threadIdx.x == 32) {
-    prefetch_tmap(&map);
-    prefetch_tmap(&part_map);
-  }
+  if (threadIdx.x == 32) prefetch_tmap(&map);
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, 512);
     tmem_relinquish_pair();
@@ -347,6 +352,7 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
   grid_dep_wait();
   const uint32_t tmem_base = *tmem_slot;
 
+  if (warp < kEpiWarp0) setmaxnreg_dec<kRegsControl>();  // each warpgroup changes its registers at once
   if (warp == 2) {
     // ------------------------------------------------------------------ scheduler (even CTA)
     if (lane == 0 && rank == 0) {
@@ -382,7 +388,7 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
         else
           mbar_arrive_remote(lead_iempty + slot * 8);
         if (it.product < 0) break;
-        fence_proxy_async_global();  // what it reads was stored by TMA in other CTAs, or by the kernel before
+        fence_proxy_async_global();  // what it reads was stored in other CTAs, or by the kernel before
         const MuonMat& m = tab.t[it.mat];
         const int mp = m.mt * 256, nk = kblocks(m, it), cur = it.step & 1;
         const uint32_t abase = it.product == kMuonGram ? m.x[cur] : it.product == kMuonPoly ? m.a : m.b;
@@ -470,12 +476,11 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
     }
   } else if (warp >= kEpiWarp0) {
     // ------------------------------------------------------------------ epilogue (both CTAs)
+    setmaxnreg_inc<kRegsEpilogue>();
     const int e = warp - kEpiWarp0, q = warp & 3, hc = e >> 2;  // lane quarter, column half
     const uint32_t lead_tempty = mapa_shared(smem_u32(tempty), 0), lead_iempty = mapa_shared(smem_u32(iempty), 0);
-    uint8_t* staging = staging_all + e * 2 * PART_BYTES;
-    const uint32_t stage_a = smem_u32(staging), line = stage_a + lane * 64;  // this lane's row of the first term
-    uint64_t* loads = parts + 2 * e;
-    uint32_t uses[2] = {0u, 0u}, loaded[2] = {0u, 0u};
+    const uint32_t staging = smem_u32(staging_all + e * STAGING_BYTES / kEpiWarps);
+    uint32_t uses[2] = {0u, 0u};
     int h = 0;
     bool skip = false;  // a Muon step whose norm is not finite changes nothing
     if (hyper.norm != nullptr) skip = !isfinite(hyper.norm[0]);
@@ -503,25 +508,25 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
       const int wide = (apply ? m.kn : m.km) * 64 - col0;
       const int nu = row >= m.km * 64 || wide <= 0 ? 0 : wide >= 32 * kUnits ? kUnits : wide / 32;
       // X's second term, which only the epilogue of the same tile reads again, lies in the order of its lanes.
-      uint4* lo = reinterpret_cast<uint4*>(hyper.ws + static_cast<size_t>(m.lo) * 128) +
-                  muon_lo_chunk(it.j * m.mt + it.i, static_cast<int>(rank), e) + lane;
-      uint4 ahead[4];
-      auto read_lo = [&](int u) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) ahead[c] = __ldcg(lo + (u * 4 + c) * 32);  // written on another SM: not from L1
+      uint8_t* lo = hyper.ws + static_cast<size_t>(m.lo) * 128 + muon_lo_sector(it.j * m.mt + it.i, static_cast<int>(rank), e) * 32 + lane * 32;
+      auto part = [&](uint32_t base, int u) {  // this lane's row of part u
+        return hyper.ws + (static_cast<size_t>(base) + static_cast<size_t>(col0 / 64 + u / 2) * mp + row + lane) * 128 + (u & 1) * 64;
       };
-      auto part_row = [&](uint32_t base, int u) { return static_cast<int>(base) + (col0 / 64 + u / 2) * mp + row; };
-      auto load_part = [&](int u) {
-        mbar_arrive_expect_tx(loads + (u & 1), PART_BYTES);
-        tma_load_2d(staging + (u & 1) * PART_BYTES, &part_map, loads + (u & 1), (u & 1) * 32, part_row(add, u));
-      };
-      if (nu > 0 && it.product != kMuonGram) {
-        if (lane == 0) {
-          fence_proxy_async_global();
-          load_part(0);
+      uint32_t hi1[16], lo1[16];  // of the next part
+      auto read_ahead = [&](int u) {
+        if (it.product != kMuonGram && u < nu) {
+          const uint8_t* a = part(add, u);
+          ld_sector(a, hi1);
+          ld_sector(a + 32, hi1 + 8);
+          if (apply) {
+            ld_sector(lo + u * 2048, lo1);
+            ld_sector(lo + u * 2048 + 1024, lo1 + 8);
+          }
         }
-        if (apply) read_lo(0);
-      }
+      };
+#pragma unroll
+      for (int j = 0; j < 16; ++j) hi1[j] = lo1[j] = 0u;
+      read_ahead(0);
       // Of a long sum all but the last stretch, added up in the workspace: [kUnits][8][32 lanes] of this warp.
       const bool deep = nk > kMuonDepth;
       float4* scratch = nullptr;
@@ -556,16 +561,12 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after();
       const float acc = p.acc[it.step][it.product], fac = p.add[it.step][it.product];
+#pragma unroll 1
       for (int u = 0; u < nu; ++u) {
-        if (lane == 0) {  // the part before last has left this one's place, or the part before the next one's
-          if (it.product == kMuonGram) {
-            bulk_wait_group_read<1>();
-          } else if (u + 1 < nu && !last) {
-            bulk_wait_group_read<0>();
-            load_part(u + 1);
-          }
-        }
-        __syncwarp();
+        uint32_t w[16], l[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) w[j] = hi1[j], l[j] = lo1[j];
+        read_ahead(u + 1);
         float v[32];
         tmem_ld32(lanes + static_cast<uint32_t>(h * 256 + hc * 128 + u * 32), v);
         tmem_ld_wait();
@@ -576,86 +577,46 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
             v[4 * j] += y.x, v[4 * j + 1] += y.y, v[4 * j + 2] += y.z, v[4 * j + 3] += y.w;
           }
         }
-        uint32_t l[16];
-        if (apply) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) l[4 * c] = ahead[c].x, l[4 * c + 1] = ahead[c].y, l[4 * c + 2] = ahead[c].z, l[4 * c + 3] = ahead[c].w;
-          if (u + 1 < nu) read_lo(u + 1);
-        } else {
-#pragma unroll
-          for (int c = 0; c < 16; ++c) l[c] = 0u;
-        }
-        if (it.product != kMuonGram) {
-          got = __all_sync(0xffffffffu, wait_bounded(loads + (u & 1), loaded[u & 1] & 1u, abort_flag, p.ctl, 51));
-          if (!got) break;
-          ++loaded[u & 1];
-        }
-        const uint32_t place = line + static_cast<uint32_t>((u & 1) * PART_BYTES);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {  // 16-byte chunks, where the 64-byte swizzle has them
-          const uint32_t at = place + static_cast<uint32_t>((c ^ ((lane >> 1) & 3)) * 16);
-          float x[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = v[8 * c + j] * acc;
-          if (it.product != kMuonGram) {
-            const uint4 w = ld_shared_v4(at);
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 f = unpack_f16x2(ww[j]), g = unpack_f16x2(l[4 * c + j]);
-              x[2 * j] = fmaf(f.x + g.x, fac, x[2 * j]);
-              x[2 * j + 1] = fmaf(f.y + g.y, fac, x[2 * j + 1]);
-            }
-          }
-          if (last) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[8 * c + j] = __half2float(__float2half_rn(x[j])) * hyper.unscale;  // as fp16, like every X
-          } else {
-            uint32_t o[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[j] = pack_f16x2(x[2 * j], x[2 * j + 1]);
-            st_shared_v4(at, o[0], o[1], o[2], o[3]);
-            if (apply) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float2 f = unpack_f16x2(o[j]);
-                o[j] = pack_f16x2(x[2 * j] - f.x, x[2 * j + 1] - f.y);
-              }
-              lo[(u * 4 + c) * 32] = make_uint4(o[0], o[1], o[2], o[3]);
-            }
-          }
+        for (int j = 0; j < 16; ++j) {  // A has nothing added: its w and l are zeros
+          const float2 f = unpack_f16x2(w[j]), g = unpack_f16x2(l[j]);
+          v[2 * j] = fmaf(f.x + g.x, fac, v[2 * j] * acc);
+          v[2 * j + 1] = fmaf(f.y + g.y, fac, v[2 * j + 1] * acc);
+          w[j] = pack_f16x2(v[2 * j], v[2 * j + 1]);
         }
         if (last) {
-          __syncwarp();  // every lane has read its part of the staging, which is written again
-          if (!skip) finish_part<OUT>(m, hyper.seed, row, col0 + u * 32, lane, stage_a, v);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0 && u + 1 < nu) load_part(u + 1);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {  // as fp16, like every X
+            const float2 f = unpack_f16x2(w[j]);
+            v[2 * j] = f.x * hyper.unscale;
+            v[2 * j + 1] = f.y * hyper.unscale;
+          }
+          if (!skip) finish_part<OUT>(m, hyper.seed, row, col0 + u * 32, lane, staging, v);
           continue;
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_2d(&part_map, staging + (u & 1) * PART_BYTES, (u & 1) * 32, part_row(out, u));
-          bulk_commit_group();
+        uint8_t* dst = part(out, u);
+        st_sector(dst, w);
+        st_sector(dst + 32, w + 8);
+        if (apply) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float2 f = unpack_f16x2(w[j]);
+            l[j] = pack_f16x2(v[2 * j] - f.x, v[2 * j + 1] - f.y);
+          }
+          st_sector(lo + u * 2048, l);
+          st_sector(lo + u * 2048 + 1024, l + 8);
         }
       }
-      if (!got) break;
       tc_fence_before();  // the half is free for the next item but one
-      __syncwarp();       // and every lane's second terms are stored
+      if (!last) fence_proxy_async_global();  // what this lane has stored will be loaded by TMA
+      __syncwarp();
       if (lane == 0) {
         mbar_arrive_remote(lead_tempty + h * 8);
-        if (!last) {
-          bulk_wait_group<0>();  // the stores are complete
-          fence_proxy_async_global();
-          red_release_gpu_add(p.ctrl + 1 + it.mat, 1u);
-        }
+        if (!last) red_release_gpu_add(p.ctrl + 1 + it.mat, 1u);  // every lane's stores are ordered before it by the barrier
       }
       ++uses[h];
       h ^= 1;
-      __syncwarp();
     }
-    if (lane == 0) bulk_wait_group<0>();
   }
 
   tc_fence_before();
@@ -709,17 +670,17 @@ cudaError_t muon_pipe_prepare(int* max_clusters) {
   return e;
 }
 
-cudaError_t launch_muon_pipe(const CUtensorMap& load, const CUtensorMap& part, const MuonTable& t, const MuonPipe& p, const MuonHyper& h,
-                             int out, int clusters, cudaStream_t stream) {
+cudaError_t launch_muon_pipe(const CUtensorMap& load, const MuonTable& t, const MuonPipe& p, const MuonHyper& h, int out,
+                             int clusters, cudaStream_t stream) {
   const int most = p.sym > p.rect ? p.sym : p.rect;  // items that can run at once
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = pipe_config(attr, most < clusters ? most : clusters, stream);
   switch (out) {
-    case kMuonOutBf16: return cudaLaunchKernelEx(&cfg, muon_pipe_kernel<kMuonOutBf16>, load, part, t, p, h);
-    case kMuonOutF16: return cudaLaunchKernelEx(&cfg, muon_pipe_kernel<kMuonOutF16>, load, part, t, p, h);
-    case kMuonParamF32: return cudaLaunchKernelEx(&cfg, muon_pipe_kernel<kMuonParamF32>, load, part, t, p, h);
-    case kMuonParamBf16: return cudaLaunchKernelEx(&cfg, muon_pipe_kernel<kMuonParamBf16>, load, part, t, p, h);
-    default: return cudaLaunchKernelEx(&cfg, muon_pipe_kernel<kMuonParamMaster>, load, part, t, p, h);
+    case kMuonOutBf16: return cudaLaunchKernelEx(&cfg, muon_pipe_kernel<kMuonOutBf16>, load, t, p, h);
+    case kMuonOutF16: return cudaLaunchKernelEx(&cfg, muon_pipe_kernel<kMuonOutF16>, load, t, p, h);
+    case kMuonParamF32: return cudaLaunchKernelEx(&cfg, muon_pipe_kernel<kMuonParamF32>, load, t, p, h);
+    case kMuonParamBf16: return cudaLaunchKernelEx(&cfg, muon_pipe_kernel<kMuonParamBf16>, load, t, p, h);
+    default: return cudaLaunchKernelEx(&cfg, muon_pipe_kernel<kMuonParamMaster>, load, t, p, h);
   }
 }
 
