@@ -156,9 +156,10 @@ struct NormGrad {
   int want_dw, want_db;
   void* dw;
   void* db;
+  int cta_cols;      // columns of a CTA of a cluster, set by the launch
 };
-// Widest rows whose gradients are formed in one reading, and the rows of `part`, one per CTA (or stretch of rows).
-constexpr int kNormFusedCols = 8192;
+// Widest rows (fp32: half of it) whose gradients are formed in one reading, and how many rows of `part` there may be.
+constexpr int kNormFusedCols = 65536;
 int norm_parts(int64_t N, int d);
 cudaError_t launch_norm(const NormParams& p, int dtype, int sms, cudaStream_t stream);
 cudaError_t launch_norm_bwd(const NormParams& p, const NormGrad& q, int dtype, int parts, int sms, cudaStream_t stream);

@@ -5,11 +5,22 @@
 //   g = dy w,  dx = r (g - mean(g) - xh mean(g xh)) + dsum   (RMS: without mean(g))
 //   dw = sum over rows of dy xh,  db = sum over rows of dy
 //
-// HBM bounds both passes. A row is held in registers by the threads that share it, C columns each, so each input crosses HBM
-// once and the variance is taken around the mean. The backward keeps the columns' sums of dw and db in registers over all
-// rows of a CTA and writes them once; a second small kernel adds the CTAs' sums up in a fixed order.
+// HBM bounds both passes, so each input is read once and what is still needed of it stays in registers, in its own type.
+//
+// Rows of 16-byte vectors: every thread copies the vectors that it will use itself into its own places of a ring in shared memory
+// (cp.async), several rows ahead, so that an SM has 100 KB and more on their way without a register or a barrier for them. (One row
+// ahead in registers: 0.5 of HBM's rate in the backward, and rows that wait for one another in the forward.) Other rows go by
+// single elements through registers.
+//
+// Backward: a thread takes the same columns of all rows of its CTA, so that the sums of dw and db stay in registers; each CTA
+// writes them once and a second small kernel adds them up in a fixed order. Rows of more than 4096 columns are shared by a cluster
+// of CTAs of up to 8192 columns, which exchange their sums through distributed shared memory and form a row's dx only after
+// the next row's sums, so that nobody waits for the exchange.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <atomic>
+#include <type_traits>
 
 #include "hylo_ops_internal.h"
 
@@ -28,10 +39,49 @@ __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { re
 template <>
 __device__ __forceinline__ __half from_float<__half>(float x) { return __float2half_rn(x); }
 
-// VB elements at p, as fp32 (VB elements of T are one access of up to 16 bytes).
+// VB elements as they lie in memory (one access of up to 16 bytes). Two at a time are converted by one instruction.
 template <typename T, int VB>
 struct alignas(VB * sizeof(T)) Pack {
   T v[VB];
+  __device__ __forceinline__ void get(float* x) const {
+    if constexpr (sizeof(T) == 2 && VB % 2 == 0) {
+#pragma unroll
+      for (int j = 0; j < VB; j += 2) {
+        const uint32_t w = reinterpret_cast<const uint32_t*>(v)[j / 2];
+        if constexpr (std::is_same<T, __half>::value) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+          x[j] = f.x, x[j + 1] = f.y;
+        } else {
+          x[j] = __uint_as_float(w << 16), x[j + 1] = __uint_as_float(w & 0xffff0000u);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < VB; ++j) x[j] = to_float(v[j]);
+    }
+  }
+  __device__ __forceinline__ void set(const float* x) {
+    if constexpr (sizeof(T) == 2 && VB % 2 == 0) {
+#pragma unroll
+      for (int j = 0; j < VB; j += 2) {
+        uint32_t w;
+        if constexpr (std::is_same<T, __half>::value) {
+          const __half2 h = __floats2half2_rn(x[j], x[j + 1]);
+          w = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+          w = pack_bf16x2(x[j], x[j + 1]);
+        }
+        reinterpret_cast<uint32_t*>(v)[j / 2] = w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < VB; ++j) v[j] = from_float<T>(x[j]);
+    }
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int j = 0; j < VB; ++j) v[j] = from_float<T>(0.f);
+  }
 };
 
 template <typename T, int VB>
@@ -40,17 +90,14 @@ __device__ __forceinline__ void load(const T* p, float* out) {
     load<T, VB / 2>(p, out);
     load<T, VB / 2>(p + VB / 2, out + VB / 2);
   } else {
-    const Pack<T, VB> a = *reinterpret_cast<const Pack<T, VB>*>(p);
-#pragma unroll
-    for (int j = 0; j < VB; ++j) out[j] = to_float(a.v[j]);
+    reinterpret_cast<const Pack<T, VB>*>(p)->get(out);
   }
 }
 
 template <typename T, int VB>
 __device__ __forceinline__ void store(T* p, const float* x) {
   Pack<T, VB> a;
-#pragma unroll
-  for (int j = 0; j < VB; ++j) a.v[j] = from_float<T>(x[j]);
+  a.set(x);
   *reinterpret_cast<Pack<T, VB>*>(p) = a;
 }
 
@@ -81,96 +128,295 @@ __device__ __forceinline__ void row_sums(float (&v)[M], int threads, float* red)
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < M; ++i) v[i] = lane < warps ? red[i * 32 + lane] : 0.f;
-  for (int o = 16; o > 0; o >>= 1) {
+  int top = 16;
+  while (top >= warps) top >>= 1;
+  for (int o = top; o > 0; o >>= 1) {
 #pragma unroll
     for (int i = 0; i < M; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
   }
+  if (top < 16) {
+#pragma unroll
+    for (int i = 0; i < M; ++i) v[i] = __shfl_sync(0xffffffffu, v[i], 0);
+  }
 }
 
-// One row at a time for each group of p.threads threads, K vectors of VB columns a thread.
-template <typename T, int VB, int K>
-__global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormParams p) {
+// Two fp32 operations by one instruction.
+__device__ __forceinline__ float2 two(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 pair(const float* x) { return make_float2(x[0], x[1]); }
+// x <- (x - mu) r, in this order: r may be large beside 1 / mu. CENTRE false: mu is 0.
+template <bool CENTRE, int N>
+__device__ __forceinline__ void normalise(float (&x)[N], float mu, float r) {
+#pragma unroll
+  for (int j = 0; j + 1 < N; j += 2) {
+    float2 y = pair(x + j);
+    if (CENTRE) y = __fadd2_rn(y, two(-mu));
+    y = __fmul2_rn(y, two(r));
+    x[j] = y.x, x[j + 1] = y.y;
+  }
+  if constexpr (N % 2 == 1) x[N - 1] = (CENTRE ? x[N - 1] - mu : x[N - 1]) * r;
+}
+template <int N>
+__device__ __forceinline__ void times(float (&x)[N], const float (&a)[N]) {
+#pragma unroll
+  for (int j = 0; j + 1 < N; j += 2) {
+    const float2 y = __fmul2_rn(pair(x + j), pair(a + j));
+    x[j] = y.x, x[j + 1] = y.y;
+  }
+  if constexpr (N % 2 == 1) x[N - 1] *= a[N - 1];
+}
+template <int N>
+__device__ __forceinline__ void plus(float (&x)[N], const float (&a)[N]) {
+#pragma unroll
+  for (int j = 0; j + 1 < N; j += 2) {
+    const float2 y = __fadd2_rn(pair(x + j), pair(a + j));
+    x[j] = y.x, x[j + 1] = y.y;
+  }
+  if constexpr (N % 2 == 1) x[N - 1] += a[N - 1];
+}
+
+// y of a thread's vectors k0, ..., k0 + KB - 1 of one row. All gains are loaded before the first one is used.
+template <typename T, typename G, int VB, int KC, int KB>
+__device__ __forceinline__ void write_row(const NormParams& p, T* y, const Pack<T, VB> (&raw)[KC], int k0, int t, float mu, float rstd) {
+  float w[KB][VB], b[KB][VB];
+#pragma unroll
+  for (int k = 0; k < KB; ++k) {
+    const int c = ((k0 + k) * p.threads + t) * VB;
+#pragma unroll
+    for (int j = 0; j < VB; ++j) w[k][j] = 1.f, b[k][j] = 0.f;
+    if (p.weight != nullptr && c < p.d) load<G, VB>(static_cast<const G*>(p.weight) + c, w[k]);
+    if (p.bias != nullptr && c < p.d) load<G, VB>(static_cast<const G*>(p.bias) + c, b[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < KB; ++k) {
+    const int c = ((k0 + k) * p.threads + t) * VB;
+    float x[VB];
+    raw[k0 + k].get(x);
+    normalise<true>(x, mu, rstd);
+    times(x, w[k]);
+    if (p.bias != nullptr) plus(x, b[k]);
+    if (c < p.d) store<T, VB>(y + c, x);
+  }
+}
+
+// KR rows at a time for each group of p.threads threads, KC vectors of VB columns a thread and row.
+template <typename T, int VB, int KC, int KR>
+__global__ void __launch_bounds__(KC * KR == 1 ? 1024 : 512) norm_fwd_kernel(const NormParams p) {
+  using V = Pack<T, VB>;
+  __shared__ float red[2][KR * 32];
+  const int group = threadIdx.x / p.threads, t = threadIdx.x - group * p.threads;
+  const int groups = blockDim.x / p.threads;
+  const float inv_d = 1.f / static_cast<float>(p.d);
+  const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * groups + group) * KR;
+  V raw[KR][KC];
+#pragma unroll
+  for (int r = 0; r < KR; ++r) {
+    const T* x = static_cast<const T*>(p.x) + (row0 + r) * p.ldx;
+#pragma unroll
+    for (int k = 0; k < KC; ++k) {
+      const int c = (k * p.threads + t) * VB;
+      raw[r][k].clear();
+      if (row0 + r < p.N && c < p.d) raw[r][k] = *reinterpret_cast<const V*>(x + c);
+    }
+  }
+  if (p.residual != nullptr) {
+    V more[KR][KC];
+#pragma unroll
+    for (int r = 0; r < KR; ++r) {
+      const T* x = static_cast<const T*>(p.residual) + (row0 + r) * p.ldr;
+#pragma unroll
+      for (int k = 0; k < KC; ++k) {
+        const int c = (k * p.threads + t) * VB;
+        more[r][k].clear();
+        if (row0 + r < p.N && c < p.d) more[r][k] = *reinterpret_cast<const V*>(x + c);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < KR; ++r) {
+      T* sum = static_cast<T*>(p.sum) + (row0 + r) * p.d;
+#pragma unroll
+      for (int k = 0; k < KC; ++k) {
+        const int c = (k * p.threads + t) * VB;
+        float a[VB], b[VB];
+        raw[r][k].get(a);
+        more[r][k].get(b);
+        plus(a, b);
+        raw[r][k].set(a);  // as the next layer reads it
+        if (row0 + r < p.N && c < p.d) *reinterpret_cast<V*>(sum + c) = raw[r][k];
+      }
+    }
+  }
+  float mu[KR], v[KR];
+#pragma unroll
+  for (int r = 0; r < KR; ++r) mu[r] = 0.f;
+  if (!p.rms) {
+#pragma unroll
+    for (int r = 0; r < KR; ++r) {
+      float sum[VB];
+#pragma unroll
+      for (int j = 0; j < VB; ++j) sum[j] = 0.f;
+#pragma unroll
+      for (int k = 0; k < KC; ++k) {
+        float a[VB];
+        raw[r][k].get(a);
+        plus(sum, a);
+      }
+#pragma unroll
+      for (int j = 0; j < VB; ++j) mu[r] += sum[j];
+    }
+    row_sums(mu, p.threads, red[0]);
+#pragma unroll
+    for (int r = 0; r < KR; ++r) mu[r] *= inv_d;
+  }
+#pragma unroll
+  for (int r = 0; r < KR; ++r) {
+    float2 sum = two(0.f);
+    v[r] = 0.f;
+#pragma unroll
+    for (int k = 0; k < KC; ++k) {
+      if ((k * p.threads + t) * VB < p.d) {
+        float a[VB];
+        raw[r][k].get(a);
+#pragma unroll
+        for (int j = 0; j + 1 < VB; j += 2) {
+          const float2 x = __fadd2_rn(pair(a + j), two(-mu[r]));
+          sum = __ffma2_rn(x, x, sum);
+        }
+        if constexpr (VB == 1) v[r] = fmaf(a[0] - mu[r], a[0] - mu[r], v[r]);
+      }
+    }
+    v[r] += sum.x + sum.y;
+  }
+  row_sums(v, p.threads, red[1]);
+#pragma unroll
+  for (int r = 0; r < KR; ++r) {
+    if (row0 + r >= p.N) break;
+    const float rstd = rsqrtf(fmaf(v[r], inv_d, p.eps));
+    if (t == 0 && p.stats != nullptr) p.stats[row0 + r] = make_float2(mu[r], rstd);
+    T* y = static_cast<T*>(p.y) + (row0 + r) * p.d;
+    constexpr int KB = KC < 4 ? KC : 4;
+#pragma unroll
+    for (int k = 0; k < KC; k += KB) {
+      if (p.gain_f32)
+        write_row<T, float, VB, KC, KB>(p, y, raw[r], k, t, mu[r], rstd);
+      else
+        write_row<T, T, VB, KC, KB>(p, y, raw[r], k, t, mu[r], rstd);
+    }
+  }
+}
+
+// 16 bytes from global to shared memory, or 16 zero bytes.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
+template <typename V>
+__device__ __forceinline__ V shared_vector(uint32_t a) {
+  V v;
+  uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a) : "memory");
+  return v;
+}
+
+// One row at a time for each group of p.threads threads, KC vectors a thread, S - 1 rows on their way.
+template <typename T, int KC, int S, bool RES>
+__global__ void __launch_bounds__(512) norm_fwd_ring_kernel(const NormParams p) {
+  constexpr int VB = 16 / sizeof(T);
+  using V = Pack<T, VB>;
+  extern __shared__ __align__(16) uint8_t ring[];  // [S][streams][KC][threads]
   __shared__ float red[2][32];
   const int group = threadIdx.x / p.threads, t = threadIdx.x - group * p.threads;
   const int groups = blockDim.x / p.threads;
   const float inv_d = 1.f / static_cast<float>(p.d);
-  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * groups; row0 < p.N; row0 += static_cast<int64_t>(gridDim.x) * groups) {
-    const int64_t row = row0 + group;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  const uint32_t vec = blockDim.x * 16, mine = smem_u32(ring) + threadIdx.x * 16;
+  auto place = [&](int slot, int stream, int k) { return mine + static_cast<uint32_t>((slot * (RES ? 2 : 1) + stream) * KC + k) * vec; };
+  auto fetch = [&](int slot, int64_t row) {
     const bool live = row < p.N;
-    const T* x = static_cast<const T*>(p.x) + row * p.ldx;
-    float s[K * VB];
+    const T* x = static_cast<const T*>(p.x) + (live ? row * p.ldx : 0);
+    const T* r = static_cast<const T*>(p.residual) + (live ? row * p.ldr : 0);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
+    for (int k = 0; k < KC; ++k) {
       const int c = (k * p.threads + t) * VB;
-      if (live && c < p.d) {
-        load<T, VB>(x + c, s + k * VB);
-      } else {
-#pragma unroll
-        for (int j = 0; j < VB; ++j) s[k * VB + j] = 0.f;
-      }
+      const bool there = live && c < p.d;
+      copy16(place(slot, 0, k), x + (there ? c : 0), there);
+      if (RES) copy16(place(slot, 1, k), r + (there ? c : 0), there);
     }
-    if (p.residual != nullptr) {
-      const T* r = static_cast<const T*>(p.residual) + row * p.ldr;
+    copy_commit();
+  };
+  int64_t row = static_cast<int64_t>(blockIdx.x) * groups + group;
+  int64_t base = static_cast<int64_t>(blockIdx.x) * groups;  // of the CTA: all its threads take part in every sum
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) fetch(i, row + i * step);
+  int slot = 0, ahead = S - 1, flip = 0;
+  for (; base < p.N; base += step, row += step) {
+    fetch(ahead, row + (S - 1) * step);
+    copy_wait<S - 1>();
+    const bool live = row < p.N;
+    V raw[KC];
+#pragma unroll
+    for (int k = 0; k < KC; ++k) raw[k] = shared_vector<V>(place(slot, 0, k));
+    if (RES) {
       T* sum = static_cast<T*>(p.sum) + row * p.d;
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
+      for (int k = 0; k < KC; ++k) {
         const int c = (k * p.threads + t) * VB;
-        if (live && c < p.d) {
-          float a[VB];
-          load<T, VB>(r + c, a);
-#pragma unroll
-          for (int j = 0; j < VB; ++j) s[k * VB + j] = to_float(from_float<T>(s[k * VB + j] + a[j]));  // as the next layer reads it
-          store<T, VB>(sum + c, s + k * VB);
-        }
+        float a[VB], b[VB];
+        raw[k].get(a);
+        shared_vector<V>(place(slot, 1, k)).get(b);
+        plus(a, b);
+        raw[k].set(a);  // as the next layer reads it
+        if (live && c < p.d) *reinterpret_cast<V*>(sum + c) = raw[k];
       }
     }
+    slot = slot + 1 == S ? 0 : slot + 1;
+    ahead = ahead + 1 == S ? 0 : ahead + 1;
     float mu = 0.f;
     if (!p.rms) {
-      float v[1] = {0.f};
+      float sum[VB], v[1] = {0.f};
 #pragma unroll
-      for (int j = 0; j < K * VB; ++j) v[0] += s[j];
-      row_sums(v, p.threads, red[0]);
+      for (int j = 0; j < VB; ++j) sum[j] = 0.f;
+#pragma unroll
+      for (int k = 0; k < KC; ++k) {
+        float a[VB];
+        raw[k].get(a);
+        plus(sum, a);
+      }
+#pragma unroll
+      for (int j = 0; j < VB; ++j) v[0] += sum[j];
+      row_sums(v, p.threads, red[flip]);
+      flip ^= 1;
       mu = v[0] * inv_d;
     }
-    float v[1] = {0.f};
+    float v[1];
+    float2 sum = two(0.f);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * p.threads + t) * VB;
-      if (c < p.d) {
-#pragma unroll
-        for (int j = 0; j < VB; ++j) {
-          s[k * VB + j] -= mu;
-          v[0] = fmaf(s[k * VB + j], s[k * VB + j], v[0]);
-        }
-      }
-    }
-    row_sums(v, p.threads, red[1]);
-    const float rstd = rsqrtf(fmaf(v[0], inv_d, p.eps));
-    if (live && t == 0 && p.stats != nullptr) p.stats[row] = make_float2(mu, rstd);
-    T* y = static_cast<T*>(p.y) + row * p.d;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * p.threads + t) * VB;
-      if (live && c < p.d) {
+    for (int k = 0; k < KC; ++k) {
+      if ((k * p.threads + t) * VB < p.d) {
         float a[VB];
-        if (p.weight != nullptr) {
-          load_gain<T, VB>(p.weight, p.gain_f32, c, a);
+        raw[k].get(a);
 #pragma unroll
-          for (int j = 0; j < VB; ++j) s[k * VB + j] = s[k * VB + j] * rstd * a[j];
-        } else {
-#pragma unroll
-          for (int j = 0; j < VB; ++j) s[k * VB + j] *= rstd;
+        for (int j = 0; j < VB; j += 2) {
+          const float2 x = __fadd2_rn(pair(a + j), two(-mu));
+          sum = __ffma2_rn(x, x, sum);
         }
-        if (p.bias != nullptr) {
-          load_gain<T, VB>(p.bias, p.gain_f32, c, a);
-#pragma unroll
-          for (int j = 0; j < VB; ++j) s[k * VB + j] += a[j];
-        }
-        store<T, VB>(y + c, s + k * VB);
       }
     }
-    if (p.rms && p.threads > 32) __syncthreads();  // red[1] is written again by the next row
+    v[0] = sum.x + sum.y;
+    row_sums(v, p.threads, red[flip]);
+    flip ^= 1;
+    const float rstd = rsqrtf(fmaf(v[0], inv_d, p.eps));
+    if (live) {
+      if (t == 0 && p.stats != nullptr) p.stats[row] = make_float2(mu, rstd);
+      T* y = static_cast<T*>(p.y) + row * p.d;
+      if (p.gain_f32)
+        write_row<T, float, VB, KC, KC>(p, y, raw, 0, t, mu, rstd);
+      else
+        write_row<T, T, VB, KC, KC>(p, y, raw, 0, t, mu, rstd);
+    }
   }
+  copy_wait<0>();
 }
 
 // Rows too wide for the registers: a CTA reads its row again for each of the three steps.
@@ -234,101 +480,73 @@ __global__ void __launch_bounds__(1024) norm_fwd_wide_kernel(const NormParams p)
   }
 }
 
-// The gradients, with the columns' sums of this CTA's rows: part [2][CTAs][d] (dw, then db).
-template <typename T, int VB, int K>
-__global__ void __launch_bounds__(1024) norm_bwd_kernel(const NormParams p, const NormGrad q) {
-  constexpr int C = K * VB;
-  extern __shared__ float shared[];  // [2][2][32] sums of rows, then [groups][d] columns' sums where a CTA has several groups
-  const int group = threadIdx.x / p.threads, t = threadIdx.x - group * p.threads;
-  const int groups = blockDim.x / p.threads;
-  const float inv_d = 1.f / static_cast<float>(p.d);
-  float dw[C], db[C];
+// Totals over the CTA of M values a thread, for all threads. A warp halves the values that a lane carries with every exchange, so
+// that 32 / M lanes end with one each; `red` holds [warps][M]: another one for each of two consecutive calls.
+template <int M>
+__device__ __forceinline__ void column_totals(float (&v)[M], float* red) {
+  static_assert((M & (M - 1)) == 0 && M <= 16);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  int owned = 0;  // which value v[0] is in the end
 #pragma unroll
-  for (int j = 0; j < C; ++j) dw[j] = db[j] = 0.f;
-  int flip = 0;
-  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * groups; row0 < p.N; row0 += static_cast<int64_t>(gridDim.x) * groups) {
-    const int64_t row = row0 + group;
-    const bool live = row < p.N;
-    const T* s = static_cast<const T*>(p.x) + row * p.ldx;
-    const T* dy = static_cast<const T*>(q.dy) + row * q.lddy;
-    float xh[C], g[C];
-    const float2 st = live ? p.stats[row] : make_float2(0.f, 0.f);
+  for (int half = M / 2, bit = 16; half > 0; half >>= 1, bit >>= 1) {
+    const bool up = (lane & bit) != 0;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * p.threads + t) * VB;
-      if (live && c < p.d) {
-        load<T, VB>(s + c, xh + k * VB);
-        load<T, VB>(dy + c, g + k * VB);
-      } else {
-#pragma unroll
-        for (int j = 0; j < VB; ++j) {
-          xh[k * VB + j] = st.x;
-          g[k * VB + j] = 0.f;
-        }
-      }
+    for (int i = 0; i < half; ++i) {
+      const float send = up ? v[i] : v[i + half];
+      const float keep = up ? v[i + half] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
     }
-    float v[2] = {0.f, 0.f};
+    owned += up ? half : 0;
+  }
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * p.threads + t) * VB;
-      float a[VB];
-      if (p.weight != nullptr && c < p.d) load_gain<T, VB>(p.weight, p.gain_f32, c, a);
+  for (int bit = 16 / M; bit > 0; bit >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], bit);
+  if ((lane & (32 / M - 1)) == 0) red[warp * M + owned] = v[0];
+  __syncthreads();
+  // lane l: value l % M of the warps l / M, l / M + 32 / M, ...
+  float sum = 0.f;
+  for (int w = lane / M; w < warps; w += 32 / M) sum += red[w * M + (lane & (M - 1))];
 #pragma unroll
-      for (int j = k * VB; j < (k + 1) * VB; ++j) {
-        xh[j] = (xh[j] - st.x) * st.y;
-        dw[j] = fmaf(g[j], xh[j], dw[j]);
-        db[j] += g[j];
-        if (p.weight != nullptr && c < p.d) g[j] *= a[j - k * VB];
-        v[0] = fmaf(g[j], xh[j], v[0]);
-        v[1] += g[j];
-      }
-    }
-    if (q.dx == nullptr) continue;
-    row_sums(v, p.threads, shared + flip * 64);
-    flip ^= 1;
-    const float c1 = v[0] * inv_d, c2 = p.rms ? 0.f : v[1] * inv_d;
-    T* dx = static_cast<T*>(q.dx) + row * p.d;
+  for (int bit = 16; bit >= M; bit >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, bit);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * p.threads + t) * VB;
-      if (live && c < p.d) {
+  for (int i = 0; i < M; ++i) v[i] = __shfl_sync(0xffffffffu, sum, i);
+}
+
+// One vector's part in dw, db and the two sums of its row. x: normalised values, g: dy.
+template <bool RMS, int N>
+__device__ __forceinline__ void column_step(const float (&x)[N], const float (&g)[N], const float* w, float* dw, float* db, float2& sx, float2& sg) {
 #pragma unroll
-        for (int j = k * VB; j < (k + 1) * VB; ++j) g[j] = st.y * (g[j] - c2 - xh[j] * c1);
-        if (q.dsum != nullptr) {
-          float a[VB];
-          load<T, VB>(static_cast<const T*>(q.dsum) + row * q.ldds + c, a);
-#pragma unroll
-          for (int j = 0; j < VB; ++j) g[k * VB + j] += a[j];
-        }
-        store<T, VB>(dx + c, g + k * VB);
-      }
+  for (int j = 0; j < N; j += 2) {
+    const float2 gj = pair(g + j), xj = pair(x + j), gw = __fmul2_rn(gj, pair(w + j)), d = __ffma2_rn(gj, xj, pair(dw + j));
+    dw[j] = d.x, dw[j + 1] = d.y;
+    sx = __ffma2_rn(gw, xj, sx);
+    if (!RMS) {
+      const float2 e = __fadd2_rn(gj, pair(db + j));
+      db[j] = e.x, db[j + 1] = e.y;
+      sg = __fadd2_rn(gw, sg);
     }
   }
-  grid_dep_launch();
-  if (q.part == nullptr) return;
-  float* part = q.part + static_cast<int64_t>(blockIdx.x) * p.d;
-  const int64_t second = static_cast<int64_t>(gridDim.x) * p.d;
-  if (groups == 1) {
+}
+
+// g <- r g w + c2 + c1 x
+template <int N>
+__device__ __forceinline__ void row_step(const float (&x)[N], float (&g)[N], const float* w, float r, float c1, float c2) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * p.threads + t) * VB;
-      if (c < p.d) {
-        if (q.want_dw) store<float, (VB > 4 ? 4 : VB)>(part + c, dw + k * VB);
-        if (q.want_db) store<float, (VB > 4 ? 4 : VB)>(part + second + c, db + k * VB);
-        if constexpr (VB > 4) {
-          if (q.want_dw) store<float, 4>(part + c + 4, dw + k * VB + 4);
-          if (q.want_db) store<float, 4>(part + second + c + 4, db + k * VB + 4);
-        }
-      }
-    }
-    return;
+  for (int j = 0; j < N; j += 2) {
+    const float2 gw = __fmul2_rn(pair(g + j), pair(w + j));
+    const float2 y = __ffma2_rn(pair(x + j), two(c1), __ffma2_rn(gw, two(r), two(c2)));
+    g[j] = y.x, g[j + 1] = y.y;
   }
-  float* cols = shared + 128;
+}
+
+// The columns' sums of a CTA whose groups of threads have rows of their own; cols: [groups][d] floats of shared memory.
+template <int C, int VB>
+__device__ __forceinline__ void add_groups(const NormParams& p, const NormGrad& q, const float (&dw)[C], const float (&db)[C], int group,
+                                           int groups, int t, float* cols, float* part, int64_t second) {
   for (int pass = 0; pass < 2; ++pass) {
     if (pass == 0 ? !q.want_dw : !q.want_db) continue;
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
+    for (int k = 0; k < C / VB; ++k) {
       const int c = (k * p.threads + t) * VB;
       if (c < p.d) {
 #pragma unroll
@@ -337,9 +555,342 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(const NormParams p, cons
     }
     __syncthreads();
     for (int c = threadIdx.x; c < p.d; c += blockDim.x) {
-      float a = 0.f;
-      for (int i = 0; i < groups; ++i) a += cols[i * p.d + c];
-      part[pass * second + c] = a;
+      float sum = 0.f;
+      for (int i = 0; i < groups; ++i) sum += cols[i * p.d + c];
+      part[pass * second + c] = sum;
+    }
+  }
+}
+
+// The gradients for rows of single elements: eight columns a thread, p.threads apart, in registers.
+template <typename T>
+__global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p, const NormGrad q) {
+  constexpr int C = 8;
+  extern __shared__ __align__(16) float shared[];  // [2][32][2] sums of rows; then [groups][d] columns' sums where a CTA has several groups
+  const int group = threadIdx.x / p.threads, t = threadIdx.x - group * p.threads;
+  const int groups = blockDim.x / p.threads;
+  const float inv_d = 1.f / static_cast<float>(p.d);
+  float dw[C], db[C], w[C];
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    const int c = j * p.threads + t;
+    dw[j] = db[j] = 0.f, w[j] = 1.f;
+    if (p.weight != nullptr && c < p.d) load_gain<T, 1>(p.weight, p.gain_f32, c, w + j);
+  }
+  int flip = 0;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * groups; base < p.N; base += step) {
+    const int64_t row = base + group;
+    const bool live = row < p.N;
+    const float2 st = live ? p.stats[row] : make_float2(0.f, 0.f);
+    T a[C], b[C], e[C];
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const int c = j * p.threads + t;
+      const bool there = live && c < p.d;
+      a[j] = b[j] = e[j] = from_float<T>(0.f);
+      if (there) a[j] = static_cast<const T*>(p.x)[row * p.ldx + c];
+      if (there) b[j] = static_cast<const T*>(q.dy)[row * q.lddy + c];
+      if (there && q.dsum != nullptr) e[j] = static_cast<const T*>(q.dsum)[row * q.ldds + c];
+    }
+    float x[C], g[C], v[2] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < C; ++j) x[j] = to_float(a[j]), g[j] = to_float(b[j]);
+    normalise<true>(x, st.x, st.y);
+    float2 sx = two(0.f), sg = two(0.f);
+    column_step<false>(x, g, w, dw, db, sx, sg);
+    if (q.dx == nullptr) continue;
+    v[0] = sx.x + sx.y, v[1] = sg.x + sg.y;
+    if (p.threads <= 32) {
+      for (int o = p.threads >> 1; o > 0; o >>= 1) {
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+        v[1] += __shfl_xor_sync(0xffffffffu, v[1], o);
+      }
+    } else {
+      column_totals<2>(v, shared + flip * 64);
+      flip ^= 1;
+    }
+    row_step(x, g, w, st.y, -st.y * v[0] * inv_d, p.rms ? 0.f : -st.y * v[1] * inv_d);
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const int c = j * p.threads + t;
+      if (live && c < p.d) static_cast<T*>(q.dx)[row * p.d + c] = from_float<T>(q.dsum != nullptr ? g[j] + to_float(e[j]) : g[j]);
+    }
+  }
+  grid_dep_launch();
+  if (q.part == nullptr) return;
+  float* part = q.part + static_cast<int64_t>(blockIdx.x) * p.d;
+  const int64_t second = static_cast<int64_t>(gridDim.x) * p.d;
+  if (groups > 1) {
+    add_groups<C, 1>(p, q, dw, db, group, groups, t, shared + 128, part, second);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    const int c = j * p.threads + t;
+    if (c < p.d) {
+      if (q.want_dw) part[c] = dw[j];
+      if (q.want_db) part[second + c] = db[j];
+    }
+  }
+}
+
+// The gradients for rows of 16-byte vectors: as above, R rows of a group at a time and S - 1 times as many on their way.
+template <typename T, int KC, int R, int S, bool RMS, bool DSUM>
+__global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const NormParams p, const NormGrad q) {
+  constexpr int VB = 16 / sizeof(T), C = KC * VB, STREAMS = DSUM ? 3 : 2;
+  using V = Pack<T, VB>;
+  extern __shared__ __align__(16) float shared[];  // [2][32][2 R] sums of rows, then the ring [S][streams][R][KC][threads], or columns' sums
+  uint8_t* ring = reinterpret_cast<uint8_t*>(shared + 128 * R);
+  const int group = threadIdx.x / p.threads, t = threadIdx.x - group * p.threads;
+  const int groups = blockDim.x / p.threads;
+  const float inv_d = 1.f / static_cast<float>(p.d);
+  const uint32_t vec = blockDim.x * 16, mine = smem_u32(ring) + threadIdx.x * 16;
+  auto place = [&](int slot, int stream, int r, int k) { return mine + static_cast<uint32_t>(((slot * STREAMS + stream) * R + r) * KC + k) * vec; };
+  float dw[C], db[C], w[C];
+#pragma unroll
+  for (int j = 0; j < C; ++j) dw[j] = db[j] = 0.f, w[j] = 1.f;
+  if (p.weight != nullptr) {
+#pragma unroll
+    for (int k = 0; k < KC; ++k) {
+      const int c = (k * p.threads + t) * VB;
+      if (c < p.d) load_gain<T, VB>(p.weight, p.gain_f32, c, w + k * VB);
+    }
+  }
+  auto fetch = [&](int slot, int64_t row0) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool live = row0 + r < p.N;
+      const int64_t row = live ? row0 + r : 0;
+#pragma unroll
+      for (int k = 0; k < KC; ++k) {
+        const int c = (k * p.threads + t) * VB;
+        const bool there = live && c < p.d;
+        const int at = there ? c : 0;
+        copy16(place(slot, 0, r, k), static_cast<const T*>(p.x) + row * p.ldx + at, there);
+        copy16(place(slot, 1, r, k), static_cast<const T*>(q.dy) + row * q.lddy + at, there);
+        if (DSUM) copy16(place(slot, 2, r, k), static_cast<const T*>(q.dsum) + row * q.ldds + at, there);
+      }
+    }
+    copy_commit();
+  };
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups * R;
+  int64_t row0 = (static_cast<int64_t>(blockIdx.x) * groups + group) * R;
+  int64_t base = static_cast<int64_t>(blockIdx.x) * groups * R;  // of the CTA: all its threads take part in every sum
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) fetch(i, row0 + i * step);
+  float2 st[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) st[r] = row0 + r < p.N ? p.stats[row0 + r] : make_float2(0.f, 0.f);
+  int slot = 0, ahead = S - 1, flip = 0;
+  for (; base < p.N; base += step, row0 += step) {
+    fetch(ahead, row0 + (S - 1) * step);
+    ahead = ahead + 1 == S ? 0 : ahead + 1;
+    float2 now[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      now[r] = st[r];
+      st[r] = row0 + step + r < p.N ? p.stats[row0 + step + r] : make_float2(0.f, 0.f);
+    }
+    copy_wait<S - 1>();
+    float v[2 * R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float2 sg = two(0.f), sx = two(0.f);
+#pragma unroll
+      for (int k = 0; k < KC; ++k) {
+        float x[VB], g[VB];
+        shared_vector<V>(place(slot, 0, r, k)).get(x);
+        shared_vector<V>(place(slot, 1, r, k)).get(g);  // zeros behind the last column
+        normalise<!RMS>(x, now[r].x, now[r].y);
+        column_step<RMS>(x, g, w + k * VB, dw + k * VB, db + k * VB, sx, sg);
+      }
+      v[2 * r] = sx.x + sx.y;
+      v[2 * r + 1] = sg.x + sg.y;
+    }
+    if (q.dx != nullptr) {
+      if (p.threads <= 32) {
+        for (int o = p.threads >> 1; o > 0; o >>= 1) {
+#pragma unroll
+          for (int i = 0; i < 2 * R; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        }
+      } else {
+        column_totals<2 * R>(v, shared + flip * 64 * R);
+        flip ^= 1;
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float c1 = -now[r].y * v[2 * r] * inv_d, c2 = RMS || p.rms ? 0.f : -now[r].y * v[2 * r + 1] * inv_d;
+        T* dx = static_cast<T*>(q.dx) + (row0 + r) * p.d;
+#pragma unroll
+        for (int k = 0; k < KC; ++k) {
+          const int c = (k * p.threads + t) * VB;
+          float x[VB], g[VB];
+          shared_vector<V>(place(slot, 0, r, k)).get(x);
+          shared_vector<V>(place(slot, 1, r, k)).get(g);
+          normalise<!RMS>(x, now[r].x, now[r].y);
+          row_step(x, g, w + k * VB, now[r].y, c1, c2);
+          if (DSUM) {
+            float more[VB];
+            shared_vector<V>(place(slot, 2, r, k)).get(more);
+            plus(g, more);
+          }
+          if (row0 + r < p.N && c < p.d) store<T, VB>(dx + c, g);
+        }
+      }
+    }
+    slot = slot + 1 == S ? 0 : slot + 1;
+  }
+  grid_dep_launch();
+  copy_wait<0>();
+  if (q.part == nullptr) return;
+  float* part = q.part + static_cast<int64_t>(blockIdx.x) * p.d;
+  const int64_t second = static_cast<int64_t>(gridDim.x) * p.d;
+  if (groups == 1) {
+#pragma unroll
+    for (int k = 0; k < KC; ++k) {
+      const int c = (k * p.threads + t) * VB;
+      if (c < p.d) {
+#pragma unroll
+        for (int j = 0; j < VB; j += 4) {
+          if (q.want_dw) store<float, 4>(part + c + j, dw + k * VB + j);
+          if (q.want_db) store<float, 4>(part + second + c + j, db + k * VB + j);
+        }
+      }
+    }
+  } else {
+    add_groups<C, VB>(p, q, dw, db, group, groups, t, reinterpret_cast<float*>(ring), part, second);
+  }
+}
+
+// The same for rows that a cluster shares, q.cta_cols columns a CTA, one row at a time. Order of a turn: the sums of row i; the
+// totals of row i - 1, which the CTAs have exchanged meanwhile; the exchange of row i; dx of row i - 1.
+template <typename T, int KC, int S, bool RMS, bool DSUM>
+__global__ void __launch_bounds__(512) norm_bwd_cluster_kernel(const NormParams p, const NormGrad q) {
+  constexpr int VB = 16 / sizeof(T), C = KC * VB, STREAMS = DSUM ? 3 : 2;
+  using V = Pack<T, VB>;
+  extern __shared__ __align__(16) float shared[];  // [2][16 warps][2] sums, [3][8 CTAs][2] exchanged ones, then the ring [S][streams][KC][threads]
+  float* across = shared + 64;
+  uint8_t* ring = reinterpret_cast<uint8_t*>(shared + 128);
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, warps = blockDim.x >> 5;
+  const uint32_t rank = cluster_ctarank(), ctas = gridDim.x;
+  const int first = static_cast<int>(rank) * q.cta_cols, end = min(p.d, first + q.cta_cols);
+  const float inv_d = 1.f / static_cast<float>(p.d);
+  const uint32_t vec = blockDim.x * 16, mine = smem_u32(ring) + t * 16;
+  auto place = [&](int slot, int stream, int k) { return mine + static_cast<uint32_t>((slot * STREAMS + stream) * KC + k) * vec; };
+  float dw[C], db[C], w[C];
+#pragma unroll
+  for (int j = 0; j < C; ++j) dw[j] = db[j] = 0.f, w[j] = 1.f;
+  if (p.weight != nullptr) {
+#pragma unroll
+    for (int k = 0; k < KC; ++k) {
+      const int c = first + (k * blockDim.x + t) * VB;
+      if (c < end) load_gain<T, VB>(p.weight, p.gain_f32, c, w + k * VB);
+    }
+  }
+  auto fetch = [&](int slot, int64_t i) {
+    const bool live = i < p.N;
+    const int64_t row = live ? i : 0;
+#pragma unroll
+    for (int k = 0; k < KC; ++k) {
+      const int c = first + (k * static_cast<int>(blockDim.x) + t) * VB;
+      const bool there = live && c < end;
+      const int at = there ? c : 0;
+      copy16(place(slot, 0, k), static_cast<const T*>(p.x) + row * p.ldx + at, there);
+      copy16(place(slot, 1, k), static_cast<const T*>(q.dy) + row * q.lddy + at, there);
+      if (DSUM) copy16(place(slot, 2, k), static_cast<const T*>(q.dsum) + row * q.ldds + at, there);
+    }
+    copy_commit();
+  };
+  const int64_t step = gridDim.y;
+  int64_t row = blockIdx.y;
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) fetch(i, row + i * step);
+  cluster_sync_all();  // every CTA is there before its shared memory is written to
+  float2 now = row < p.N ? p.stats[row] : make_float2(0.f, 0.f), before = now;
+  int slot = 0, last = 0, i = 0;
+  auto finish = [&](int64_t r, float2 st, int from, int turn) {  // dx of row r, whose sums were exchanged in this turn
+    float a = 0.f, b = 0.f;
+    for (uint32_t c = 0; c < ctas; ++c) {
+      a += across[(turn % 3) * 16 + c * 2];
+      b += across[(turn % 3) * 16 + c * 2 + 1];
+    }
+    const float c1 = -st.y * a * inv_d, c2 = RMS || p.rms ? 0.f : -st.y * b * inv_d;
+    T* dx = static_cast<T*>(q.dx) + r * p.d;
+#pragma unroll
+    for (int k = 0; k < KC; ++k) {
+      const int c = first + (k * static_cast<int>(blockDim.x) + t) * VB;
+      float x[VB], g[VB];
+      shared_vector<V>(place(from, 0, k)).get(x);
+      shared_vector<V>(place(from, 1, k)).get(g);
+      normalise<!RMS>(x, st.x, st.y);
+      row_step(x, g, w + k * VB, st.y, c1, c2);
+      if (DSUM) {
+        float more[VB];
+        shared_vector<V>(place(from, 2, k)).get(more);
+        plus(g, more);
+      }
+      if (c < end) store<T, VB>(dx + c, g);
+    }
+  };
+  for (; row < p.N; row += step, ++i) {
+    copy_wait<S - 2>();
+    const float2 next = row + step < p.N ? p.stats[row + step] : make_float2(0.f, 0.f);
+    float2 sg = two(0.f), sx = two(0.f);
+#pragma unroll
+    for (int k = 0; k < KC; ++k) {
+      float x[VB], g[VB];
+      shared_vector<V>(place(slot, 0, k)).get(x);
+      shared_vector<V>(place(slot, 1, k)).get(g);
+      normalise<!RMS>(x, now.x, now.y);
+      column_step<RMS>(x, g, w + k * VB, dw + k * VB, db + k * VB, sx, sg);
+    }
+    if (q.dx != nullptr) {
+      float a = sx.x + sx.y, b = sg.x + sg.y;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+      }
+      float* red = shared + (i & 1) * 32;
+      if (lane == 0) red[warp * 2] = a, red[warp * 2 + 1] = b;
+      __syncthreads();
+      if (i > 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      if (t < 2) {
+        float sum = 0.f;
+        for (int j = 0; j < warps; ++j) sum += red[j * 2 + t];
+        for (uint32_t c = 0; c < ctas; ++c)
+          st_cluster_u32(mapa_shared(smem_u32(across + (i % 3) * 16 + rank * 2 + t), c), __float_as_uint(sum));
+      }
+      asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+      if (i > 0) finish(row - step, before, last, i - 1);
+    }
+    before = now;
+    now = next;
+    last = slot;
+    slot = slot + 1 == S ? 0 : slot + 1;
+    // the place of the row before, or with the first row the one that is still free
+    fetch((i + S - 1) % S, row + (S - 1) * step);
+  }
+  if (q.dx != nullptr && i > 0) {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    finish(row - step, before, last, i - 1);
+  }
+  grid_dep_launch();
+  copy_wait<0>();
+  if (q.part != nullptr) {
+    float* part = q.part + static_cast<int64_t>(blockIdx.y) * p.d;
+    const int64_t second = static_cast<int64_t>(gridDim.y) * p.d;
+#pragma unroll
+    for (int k = 0; k < KC; ++k) {
+      const int c = first + (k * static_cast<int>(blockDim.x) + t) * VB;
+      if (c < end) {
+#pragma unroll
+        for (int j = 0; j < VB; j += 4) {
+          if (q.want_dw) store<float, 4>(part + c + j, dw + k * VB + j);
+          if (q.want_db) store<float, 4>(part + second + c + j, db + k * VB + j);
+        }
+      }
     }
   }
 }
@@ -458,24 +1009,64 @@ bool vectors(const void* p, int64_t ld, int64_t N, int64_t bytes, int64_t unit) 
 
 int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-constexpr int kBwdCols = 8;    // columns of a thread in the backward: 16 sums, and a row's 1024 threads have 64 registers each
-constexpr int kGridSms = 152;  // the workspace's size may not depend on the device
+constexpr int kBwdCols = 8;     // columns of a thread in the backward
+constexpr int kCtaCols = 4096;  // columns of a CTA of 512 threads; wider rows go to a cluster, 8192 columns (fp32 4096) a CTA
+constexpr int kGridSms = 152;   // the workspace's size may not depend on the device
+constexpr int kSmemPerSm = 225 << 10;
 
-template <typename T, int VB, int K>
-cudaError_t fwd(NormParams p, int sms, cudaStream_t stream) {
-  p.threads = round_threads(cdiv64(p.d, VB * K));
+// Lets a kernel have more than 48 KiB of dynamic shared memory, once on each device.
+template <auto KERNEL>
+cudaError_t allow_smem() {
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (done.load(std::memory_order_relaxed) >> dev & 1)) return e;
+  e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerSm);
+  if (e == cudaSuccess) done.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return e;
+}
+
+unsigned blocks_for(int64_t blocks, int64_t most) { return static_cast<unsigned>(blocks < most ? blocks : most); }
+
+template <typename T, int VB, int KC, int KR>
+cudaError_t fwd(NormParams p, cudaStream_t stream) {
+  p.threads = round_threads(cdiv64(p.d, VB * KC));
   const int cta = p.threads > 32 ? p.threads : 128;
-  const int64_t blocks = cdiv64(p.N, cta / p.threads), most = static_cast<int64_t>(sms) * (2048 / cta);
-  return launch(norm_fwd_kernel<T, VB, K>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), cta, 0, stream, false, p);
+  const int64_t blocks = cdiv64(p.N, static_cast<int64_t>(cta / p.threads) * KR);
+  return launch(norm_fwd_kernel<T, VB, KC, KR>, dim3(static_cast<unsigned>(blocks)), cta, 0, stream, false, p);
+}
+
+template <typename T, int KC, int S, bool RES>
+cudaError_t fwd_ring(NormParams p, int sms, cudaStream_t stream) {
+  p.threads = round_threads(cdiv64(p.d, 16 / sizeof(T) * KC));
+  const int cta = p.threads > 32 ? p.threads : 128, smem = S * (RES ? 2 : 1) * KC * 16 * cta;
+  const cudaError_t e = allow_smem<norm_fwd_ring_kernel<T, KC, S, RES>>();
+  if (e != cudaSuccess) return e;
+  const int by_smem = kSmemPerSm / (smem + 1280), by_threads = (KC == 4 ? 640 : 1024) / cta;  // the registers of 96 or 64 a thread
+  const int64_t most = static_cast<int64_t>(sms) * (by_smem < by_threads ? by_smem : by_threads);
+  return launch(norm_fwd_ring_kernel<T, KC, S, RES>, dim3(blocks_for(cdiv64(p.N, cta / p.threads), most)), cta, smem, stream, false, p);
+}
+
+template <typename T, bool RES>
+cudaError_t fwd_rings(const NormParams& p, int sms, cudaStream_t stream) {
+  constexpr int VB = 16 / sizeof(T);
+  if (p.d <= 32 * VB) return fwd_ring<T, 1, 8, RES>(p, sms, stream);
+  if (p.d <= 64 * VB) return fwd_ring<T, 2, 8, RES>(p, sms, stream);
+  if (!RES || p.d <= 256 * 4 * VB) return fwd_ring<T, 4, 4, RES>(p, sms, stream);
+  return fwd_ring<T, 4, 3, RES>(p, sms, stream);  // four rows of two streams would not fit
 }
 
 template <typename T, int VB>
 cudaError_t fwd_cols(const NormParams& p, int sms, cudaStream_t stream) {
-  if (p.d <= 512 || (p.d <= 8192 && p.N <= 2 * sms)) return fwd<T, VB, 8 / VB>(p, sms, stream);
-  if (p.d <= 16384) return fwd<T, VB, 16 / VB>(p, sms, stream);
-  if (p.d <= 32768) return fwd<T, VB, 32 / VB>(p, sms, stream);
-  const int64_t most = 2 * static_cast<int64_t>(sms);
-  return launch(norm_fwd_wide_kernel<T, VB>, dim3(static_cast<unsigned>(p.N < most ? p.N : most)), 1024, 0, stream, false, p);
+  if constexpr (VB == 1) {
+    if (p.d <= 1024 && p.N <= 4 * sms) return fwd<T, 1, 1, 1>(p, stream);
+    if (p.d <= 128) return fwd<T, 1, 4, 2>(p, stream);
+    if (p.d <= 512 * 16) return fwd<T, 1, 16, 1>(p, stream);
+  } else {
+    if (p.d <= 1024 * VB && p.N <= 4 * sms) return fwd<T, VB, 1, 1>(p, stream);  // few rows: what counts is the time of one
+    if (p.d <= 512 * 4 * VB) return p.residual ? fwd_rings<T, true>(p, sms, stream) : fwd_rings<T, false>(p, sms, stream);
+  }
+  return launch(norm_fwd_wide_kernel<T, VB>, dim3(blocks_for(p.N, 2 * static_cast<int64_t>(sms))), 1024, 0, stream, false, p);
 }
 
 template <typename T>
@@ -488,53 +1079,96 @@ cudaError_t fwd_type(const NormParams& p, int sms, cudaStream_t stream) {
   return vec ? fwd_cols<T, VB>(p, sms, stream) : fwd_cols<T, 1>(p, sms, stream);
 }
 
-template <typename T, int VB, int K>
-cudaError_t bwd(NormParams p, const NormGrad& q, int ctas, cudaStream_t stream) {
-  static_assert(VB * K == kBwdCols);
+template <typename T, bool RMS, bool DSUM>
+cudaError_t bwd_ring(NormParams p, const NormGrad& q, int* parts, cudaStream_t stream) {
+  constexpr int KC = kBwdCols * sizeof(T) / 16, R = sizeof(T) == 2 ? 2 : 1, S = 4;
   p.threads = round_threads(cdiv64(p.d, kBwdCols));
-  const int cta = p.threads > 32 ? p.threads : 128;
-  const int groups = cta / p.threads;
-  const size_t smem = 128 * sizeof(float) + (groups > 1 ? static_cast<size_t>(groups) * p.d * sizeof(float) : 0);
-  return launch(norm_bwd_kernel<T, VB, K>, dim3(ctas), cta, smem, stream, false, p, q);
+  const int cta = p.threads > 32 ? p.threads : 128, groups = cta / p.threads;
+  const cudaError_t e = allow_smem<norm_bwd_ring_kernel<T, KC, R, S, RMS, DSUM>>();
+  if (e != cudaSuccess) return e;
+  size_t smem = static_cast<size_t>(S) * (DSUM ? 3 : 2) * R * KC * 16 * cta;
+  if (groups > 1 && static_cast<size_t>(groups) * p.d * sizeof(float) > smem) smem = static_cast<size_t>(groups) * p.d * sizeof(float);
+  *parts = static_cast<int>(blocks_for(cdiv64(p.N, static_cast<int64_t>(groups) * R), *parts));
+  return launch(norm_bwd_ring_kernel<T, KC, R, S, RMS, DSUM>, dim3(*parts), cta, 128 * R * sizeof(float) + smem, stream, false, p, q);
 }
 
+template <typename T, bool RMS, bool DSUM>
+cudaError_t bwd_cluster(NormParams p, NormGrad q, int* parts, cudaStream_t stream) {
+  constexpr int KC = 2, S = 4, cols = KC * 16 / sizeof(T);
+  const int ctas = static_cast<int>(cdiv64(p.d, 512 * cols));
+  const int cta = static_cast<int>(cdiv64(cdiv64(p.d, ctas), 32 * cols) * 32);
+  q.cta_cols = cta * cols;
+  const cudaError_t e = allow_smem<norm_bwd_cluster_kernel<T, KC, S, RMS, DSUM>>();
+  if (e != cudaSuccess) return e;
+  *parts = static_cast<int>(blocks_for(p.N, *parts < kGridSms / ctas ? *parts : kGridSms / ctas));
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas, *parts);
+  cfg.blockDim = dim3(cta);
+  cfg.dynamicSmemBytes = 512 + S * (DSUM ? 3 : 2) * KC * 16 * cta;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = ctas;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, norm_bwd_cluster_kernel<T, KC, S, RMS, DSUM>, p, q);
+}
+
+template <typename T, bool RMS, bool DSUM>
+cudaError_t bwd_vectors(const NormParams& p, const NormGrad& q, int* parts, cudaStream_t stream) {
+  return p.d <= kCtaCols ? bwd_ring<T, RMS, DSUM>(p, q, parts, stream) : bwd_cluster<T, RMS, DSUM>(p, q, parts, stream);
+}
+
+// *parts: rows of q.part that there may be, and how many were written.
 template <typename T, int VB>
-cudaError_t bwd_cols(const NormParams& p, const NormGrad& q, int ctas, int sms, cudaStream_t stream) {
-  if (p.d <= kNormFusedCols) return bwd<T, VB, kBwdCols / VB>(p, q, ctas, stream);
-  cudaError_t e = cudaSuccess;
-  if (q.dx != nullptr) {
-    const int64_t most = 2 * static_cast<int64_t>(sms);
-    e = launch(norm_bwd_wide_kernel<T, VB>, dim3(static_cast<unsigned>(p.N < most ? p.N : most)), 1024, 0, stream, false, p, q);
+cudaError_t bwd_cols(NormParams p, const NormGrad& q, int* parts, int sms, cudaStream_t stream) {
+  if constexpr (VB > 1) {
+    if (p.d <= (sizeof(T) == 2 ? kNormFusedCols : kNormFusedCols / 2)) {
+      if (p.rms && !q.want_db) return q.dsum ? bwd_vectors<T, true, true>(p, q, parts, stream) : bwd_vectors<T, true, false>(p, q, parts, stream);
+      return q.dsum ? bwd_vectors<T, false, true>(p, q, parts, stream) : bwd_vectors<T, false, false>(p, q, parts, stream);
+    }
+  } else if (p.d <= kCtaCols) {
+    p.threads = round_threads(cdiv64(p.d, kBwdCols));
+    const int cta = p.threads > 32 ? p.threads : 128, groups = cta / p.threads;
+    *parts = static_cast<int>(blocks_for(cdiv64(p.N, groups), *parts));
+    const size_t smem = (128 + (groups > 1 ? groups * p.d : 0)) * sizeof(float);
+    return launch(norm_bwd_kernel<T>, dim3(*parts), cta, smem, stream, false, p, q);
   }
+  cudaError_t e = cudaSuccess;
+  if (q.dx != nullptr)
+    e = launch(norm_bwd_wide_kernel<T, VB>, dim3(blocks_for(p.N, 2 * static_cast<int64_t>(sms))), 1024, 0, stream, false, p, q);
+  *parts = static_cast<int>(blocks_for(p.N, *parts));
   if (e == cudaSuccess && q.part != nullptr)
-    e = launch(norm_columns_kernel<T>, dim3(static_cast<unsigned>(cdiv64(p.d, 256)), ctas), 256, 0, stream, false, p, q);
+    e = launch(norm_columns_kernel<T>, dim3(static_cast<unsigned>(cdiv64(p.d, 256)), *parts), 256, 0, stream, false, p, q);
   return e;
 }
 
 template <typename T>
-cudaError_t bwd_type(const NormParams& p, const NormGrad& q, int ctas, int sms, cudaStream_t stream) {
+cudaError_t bwd_type(const NormParams& p, const NormGrad& q, int parts, int sms, cudaStream_t stream) {
   constexpr int VB = 16 / sizeof(T);
   const int64_t e = sizeof(T), ge = p.gain_f32 ? 4 : e;
   const bool vec = p.d % VB == 0 && vectors(p.x, p.ldx, p.N, e, 16) && vectors(q.dy, q.lddy, p.N, e, 16) &&
                    vectors(q.dsum, q.ldds, p.N, e, 16) && vectors(q.dx, p.d, p.N, e, 16) && vectors(p.weight, 0, 1, ge, 16);
-  cudaError_t err = vec ? bwd_cols<T, VB>(p, q, ctas, sms, stream) : bwd_cols<T, 1>(p, q, ctas, sms, stream);
+  cudaError_t err = vec ? bwd_cols<T, VB>(p, q, &parts, sms, stream) : bwd_cols<T, 1>(p, q, &parts, sms, stream);
   if (err != cudaSuccess || q.part == nullptr) return err;
   const dim3 grid(static_cast<unsigned>(cdiv64(p.d, 32)), q.want_dw && q.want_db ? 2 : 1);
   void* dw = q.want_dw ? q.dw : nullptr;
-  if (p.gain_f32) return launch(norm_join_kernel<float>, grid, 32 * kSlices, 0, stream, true, q.part, ctas, p.d, dw, q.db);
-  return launch(norm_join_kernel<T>, grid, 32 * kSlices, 0, stream, true, q.part, ctas, p.d, dw, q.db);
+  if (p.gain_f32) return launch(norm_join_kernel<float>, grid, 32 * kSlices, 0, stream, true, q.part, parts, p.d, dw, q.db);
+  return launch(norm_join_kernel<T>, grid, 32 * kSlices, 0, stream, true, q.part, parts, p.d, dw, q.db);
 }
 
 }  // namespace
 
 int norm_parts(int64_t N, int d) {
-  if (d > kNormFusedCols) {
-    const int64_t want = cdiv64(8 * kGridSms, cdiv64(d, 256));
-    return static_cast<int>(N < want ? N : want);
+  int64_t most;
+  if (d > kCtaCols) {  // one cluster an SM for each of its CTAs, or stretches of rows that fill the SMs with 256 columns each
+    const int64_t clusters = d > kNormFusedCols ? 0 : kGridSms / cdiv64(d, 2 * kCtaCols), stretches = cdiv64(8 * kGridSms, cdiv64(d, 256));
+    most = clusters > stretches ? clusters : stretches;
+  } else {
+    most = kGridSms * (512 / (d > 256 ? round_threads(cdiv64(d, kBwdCols)) : 128));  // 512 threads an SM
   }
-  const int threads = round_threads(cdiv64(d, kBwdCols)), cta = threads > 32 ? threads : 128;
-  const int64_t blocks = cdiv64(N, cta / threads), most = kGridSms * (1024 / cta);
-  return static_cast<int>(blocks < most ? blocks : most);
+  return static_cast<int>(N < most ? N : most);
 }
 
 cudaError_t launch_norm(const NormParams& p, int dtype, int sms, cudaStream_t stream) {
