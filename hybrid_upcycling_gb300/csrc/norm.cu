@@ -319,101 +319,239 @@ __device__ __forceinline__ V shared_vector(uint32_t a) {
   return v;
 }
 
-// One row at a time for each group of p.threads threads, KC vectors a thread, S - 1 rows on their way.
-template <typename T, int KC, int S, bool RES>
-__global__ void __launch_bounds__(512) norm_fwd_ring_kernel(const NormParams p) {
-  constexpr int VB = 16 / sizeof(T);
-  using V = Pack<T, VB>;
-  extern __shared__ __align__(16) uint8_t ring[];  // [S][streams][KC][threads]
-  __shared__ float red[2][32];
-  const int group = threadIdx.x / p.threads, t = threadIdx.x - group * p.threads;
-  const int groups = blockDim.x / p.threads;
-  const float inv_d = 1.f / static_cast<float>(p.d);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
-  const uint32_t vec = blockDim.x * 16, mine = smem_u32(ring) + threadIdx.x * 16;
-  auto place = [&](int slot, int stream, int k) { return mine + static_cast<uint32_t>((slot * (RES ? 2 : 1) + stream) * KC + k) * vec; };
-  auto fetch = [&](int slot, int64_t row) {
-    const bool live = row < p.N;
-    const T* x = static_cast<const T*>(p.x) + (live ? row * p.ldx : 0);
-    const T* r = static_cast<const T*>(p.residual) + (live ? row * p.ldr : 0);
+// Totals over the CTA of M values a thread, for all threads. A warp halves the values that a lane carries with every exchange, so
+// that 32 / M lanes end with one each; `red` holds [warps][M]: another one for each of two consecutive calls.
+template <int M>
+__device__ __forceinline__ void column_totals(float (&v)[M], float* red) {
+  static_assert((M & (M - 1)) == 0 && M <= 16);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  int owned = 0;  // which value v[0] is in the end
 #pragma unroll
-    for (int k = 0; k < KC; ++k) {
-      const int c = (k * p.threads + t) * VB;
-      const bool there = live && c < p.d;
-      copy16(place(slot, 0, k), x + (there ? c : 0), there);
-      if (RES) copy16(place(slot, 1, k), r + (there ? c : 0), there);
+  for (int half = M / 2, bit = 16; half > 0; half >>= 1, bit >>= 1) {
+    const bool up = (lane & bit) != 0;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float send = up ? v[i] : v[i + half];
+      const float keep = up ? v[i + half] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
     }
-    copy_commit();
-  };
-  int64_t row = static_cast<int64_t>(blockIdx.x) * groups + group;
-  int64_t base = static_cast<int64_t>(blockIdx.x) * groups;  // of the CTA: all its threads take part in every sum
+    owned += up ? half : 0;
+  }
 #pragma unroll
-  for (int i = 0; i < S - 1; ++i) fetch(i, row + i * step);
-  int slot = 0, ahead = S - 1, flip = 0;
-  for (; base < p.N; base += step, row += step) {
-    fetch(ahead, row + (S - 1) * step);
-    copy_wait<S - 1>();
-    const bool live = row < p.N;
-    V raw[KC];
+  for (int bit = 16 / M; bit > 0; bit >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], bit);
+  if ((lane & (32 / M - 1)) == 0) red[warp * M + owned] = v[0];
+  __syncthreads();
+  // lane l: value l % M of the warps l / M, l / M + 32 / M, ...
+  float sum = 0.f;
+  for (int w = lane / M; w < warps; w += 32 / M) sum += red[w * M + (lane & (M - 1))];
 #pragma unroll
-    for (int k = 0; k < KC; ++k) raw[k] = shared_vector<V>(place(slot, 0, k));
-    if (RES) {
-      T* sum = static_cast<T*>(p.sum) + row * p.d;
+  for (int bit = 16; bit >= M; bit >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, bit);
 #pragma unroll
-      for (int k = 0; k < KC; ++k) {
-        const int c = (k * p.threads + t) * VB;
-        float a[VB], b[VB];
-        raw[k].get(a);
-        shared_vector<V>(place(slot, 1, k)).get(b);
-        plus(a, b);
-        raw[k].set(a);  // as the next layer reads it
-        if (live && c < p.d) *reinterpret_cast<V*>(sum + c) = raw[k];
-      }
+  for (int i = 0; i < M; ++i) v[i] = __shfl_sync(0xffffffffu, sum, i);
+}
+
+// Means and sums of squared distances from them, of R rows: exactly as by two readings within a warp, then joined over the warps by
+// sum of M2 + count (mean - total mean)^2. counts: columns of this warp and, by warp, in shared memory; red [warps][R][2].
+template <int R, int KC, int VB, typename V>
+__device__ __forceinline__ void row_moments(const V (&raw)[R][KC], const NormParams& p, int t, float count, const float* counts, float* red,
+                                            float inv_d, float (&mu)[R], float (&m2)[R]) {
+  const int width = p.threads < 32 ? p.threads : 32;
+  float m[R], s[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    float sum[VB];
+#pragma unroll
+    for (int j = 0; j < VB; ++j) sum[j] = 0.f;
+#pragma unroll
+    for (int k = 0; k < KC; ++k) {  // zeros behind the last column
+      float a[VB];
+      raw[r][k].get(a);
+      plus(sum, a);
     }
-    slot = slot + 1 == S ? 0 : slot + 1;
-    ahead = ahead + 1 == S ? 0 : ahead + 1;
-    float mu = 0.f;
-    if (!p.rms) {
-      float sum[VB], v[1] = {0.f};
+    m[r] = 0.f;
 #pragma unroll
-      for (int j = 0; j < VB; ++j) sum[j] = 0.f;
+    for (int j = 0; j < VB; ++j) m[r] += sum[j];
+  }
+  for (int o = width >> 1; o > 0; o >>= 1) {
 #pragma unroll
-      for (int k = 0; k < KC; ++k) {
-        float a[VB];
-        raw[k].get(a);
-        plus(sum, a);
-      }
+    for (int r = 0; r < R; ++r) m[r] += __shfl_xor_sync(0xffffffffu, m[r], o);
+  }
+  const float inv = count > 0.f ? 1.f / count : 0.f;
 #pragma unroll
-      for (int j = 0; j < VB; ++j) v[0] += sum[j];
-      row_sums(v, p.threads, red[flip]);
-      flip ^= 1;
-      mu = v[0] * inv_d;
-    }
-    float v[1];
+  for (int r = 0; r < R; ++r) {
+    m[r] *= inv;
     float2 sum = two(0.f);
 #pragma unroll
     for (int k = 0; k < KC; ++k) {
       if ((k * p.threads + t) * VB < p.d) {
         float a[VB];
-        raw[k].get(a);
+        raw[r][k].get(a);
 #pragma unroll
         for (int j = 0; j < VB; j += 2) {
-          const float2 x = __fadd2_rn(pair(a + j), two(-mu));
+          const float2 x = __fadd2_rn(pair(a + j), two(-m[r]));
           sum = __ffma2_rn(x, x, sum);
         }
       }
     }
-    v[0] = sum.x + sum.y;
-    row_sums(v, p.threads, red[flip]);
+    s[r] = sum.x + sum.y;
+  }
+  for (int o = width >> 1; o > 0; o >>= 1) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) s[r] += __shfl_xor_sync(0xffffffffu, s[r], o);
+  }
+  if (p.threads <= 32) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) mu[r] = m[r], m2[r] = s[r];
+    return;
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  if (lane == 0) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) red[(warp * R + r) * 2] = m[r], red[(warp * R + r) * 2 + 1] = s[r];
+  }
+  __syncthreads();
+  static_assert(R <= 2);
+  const int row = R == 2 ? lane >> 4 : 0, w = R == 2 ? lane & 15 : lane;  // 16 warps at most
+  float mw = 0.f, sw = 0.f, cw = 0.f;
+  if (w < warps) mw = red[(w * R + row) * 2], sw = red[(w * R + row) * 2 + 1], cw = counts[w];
+  float total = cw * mw;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  total *= inv_d;
+  float all = fmaf(cw * (mw - total), mw - total, sw);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    mu[r] = __shfl_sync(0xffffffffu, total, r * 16);
+    m2[r] = __shfl_sync(0xffffffffu, all, r * 16);
+  }
+}
+
+// R rows at a time for each group of p.threads threads, KC vectors a thread and row, S - 1 times as many rows on their way. RMS:
+// neither means nor a bias.
+template <typename T, int KC, int R, int S, bool RMS, bool RES>
+__global__ void __launch_bounds__(512) norm_fwd_ring_kernel(const NormParams p) {
+  constexpr int VB = 16 / sizeof(T), C = KC * VB, STREAMS = RES ? 2 : 1;
+  using V = Pack<T, VB>;
+  extern __shared__ __align__(16) uint8_t ring[];  // [S][streams][R][KC][threads]
+  __shared__ float red[2][16 * R * 2], counts[16];
+  const int group = threadIdx.x / p.threads, t = threadIdx.x - group * p.threads;
+  const int groups = blockDim.x / p.threads;
+  const float inv_d = 1.f / static_cast<float>(p.d);
+  const uint32_t vec = blockDim.x * 16, mine = smem_u32(ring) + threadIdx.x * 16;
+  auto place = [&](int slot, int stream, int r, int k) { return mine + static_cast<uint32_t>(((slot * STREAMS + stream) * R + r) * KC + k) * vec; };
+  auto fetch = [&](int slot, int64_t row0) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool live = row0 + r < p.N;
+      const int64_t row = live ? row0 + r : 0;
+#pragma unroll
+      for (int k = 0; k < KC; ++k) {
+        const int c = (k * p.threads + t) * VB;
+        const bool there = live && c < p.d;
+        const int at = there ? c : 0;
+        copy16(place(slot, 0, r, k), static_cast<const T*>(p.x) + row * p.ldx + at, there);
+        if (RES) copy16(place(slot, 1, r, k), static_cast<const T*>(p.residual) + row * p.ldr + at, there);
+      }
+    }
+    copy_commit();
+  };
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups * R;
+  int64_t row0 = (static_cast<int64_t>(blockIdx.x) * groups + group) * R;
+  int64_t base = static_cast<int64_t>(blockIdx.x) * groups * R;  // of the CTA: all its threads take part in every sum
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) fetch(i, row0 + i * step);
+  float w[C], b[RMS ? 1 : C], count = 0.f;
+  b[0] = 0.f;
+#pragma unroll
+  for (int k = 0; k < KC; ++k) {
+    const int c = (k * p.threads + t) * VB;
+#pragma unroll
+    for (int j = k * VB; j < (k + 1) * VB; ++j) {
+      w[j] = 1.f;
+      if (!RMS) b[j] = 0.f;
+    }
+    if (c < p.d) {
+      count += VB;
+      if (p.weight != nullptr) load_gain<T, VB>(p.weight, p.gain_f32, c, w + k * VB);
+      if (!RMS && p.bias != nullptr) load_gain<T, VB>(p.bias, p.gain_f32, c, b + k * VB);
+    }
+  }
+  if (!RMS) {
+    for (int o = (p.threads < 32 ? p.threads : 32) >> 1; o > 0; o >>= 1) count += __shfl_xor_sync(0xffffffffu, count, o);
+    if ((threadIdx.x & 31) == 0) counts[threadIdx.x >> 5] = count;  // read after the first row's barrier
+  }
+  int slot = 0, ahead = S - 1, flip = 0;
+  for (; base < p.N; base += step, row0 += step) {
+    fetch(ahead, row0 + (S - 1) * step);
+    ahead = ahead + 1 == S ? 0 : ahead + 1;
+    copy_wait<S - 1>();
+    V raw[R][KC];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+      for (int k = 0; k < KC; ++k) {
+        raw[r][k] = shared_vector<V>(place(slot, 0, r, k));
+        if (RES) {
+          const int c = (k * p.threads + t) * VB;
+          float x[VB], y[VB];
+          raw[r][k].get(x);
+          shared_vector<V>(place(slot, 1, r, k)).get(y);
+          plus(x, y);
+          raw[r][k].set(x);  // as the next layer reads it
+          if (row0 + r < p.N && c < p.d) *reinterpret_cast<V*>(static_cast<T*>(p.sum) + (row0 + r) * p.d + c) = raw[r][k];
+        }
+      }
+    }
+    slot = slot + 1 == S ? 0 : slot + 1;
+    float mu[R], m2[R];
+    if constexpr (RMS) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float2 sum = two(0.f);
+#pragma unroll
+        for (int k = 0; k < KC; ++k) {
+          float x[VB];
+          raw[r][k].get(x);
+#pragma unroll
+          for (int j = 0; j < VB; j += 2) sum = __ffma2_rn(pair(x + j), pair(x + j), sum);
+        }
+        mu[r] = 0.f;
+        m2[r] = sum.x + sum.y;
+      }
+      if (p.threads <= 32) {
+        for (int o = p.threads >> 1; o > 0; o >>= 1) {
+#pragma unroll
+          for (int r = 0; r < R; ++r) m2[r] += __shfl_xor_sync(0xffffffffu, m2[r], o);
+        }
+      } else {
+        column_totals<R>(m2, red[flip]);
+      }
+    } else {
+      row_moments<R, KC, VB>(raw, p, t, count, counts, red[flip], inv_d, mu, m2);
+    }
     flip ^= 1;
-    const float rstd = rsqrtf(fmaf(v[0], inv_d, p.eps));
-    if (live) {
-      if (t == 0 && p.stats != nullptr) p.stats[row] = make_float2(mu, rstd);
-      T* y = static_cast<T*>(p.y) + row * p.d;
-      if (p.gain_f32)
-        write_row<T, float, VB, KC, KC>(p, y, raw, 0, t, mu, rstd);
-      else
-        write_row<T, T, VB, KC, KC>(p, y, raw, 0, t, mu, rstd);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float rstd = rsqrtf(fmaf(m2[r], inv_d, p.eps));
+      const bool live = row0 + r < p.N;
+      if (live && t == 0 && p.stats != nullptr) p.stats[row0 + r] = make_float2(mu[r], rstd);
+      T* y = static_cast<T*>(p.y) + (row0 + r) * p.d;
+#pragma unroll
+      for (int k = 0; k < KC; ++k) {
+        const int c = (k * p.threads + t) * VB;
+        float x[VB];
+        raw[r][k].get(x);
+        normalise<!RMS>(x, mu[r], rstd);
+#pragma unroll
+        for (int j = 0; j < VB; j += 2) {
+          float2 v = __fmul2_rn(pair(x + j), pair(w + k * VB + j));
+          if (!RMS) v = __fadd2_rn(v, pair(b + k * VB + j));
+          x[j] = v.x, x[j + 1] = v.y;
+        }
+        if (live && c < p.d) store<T, VB>(y + c, x);
+      }
     }
   }
   copy_wait<0>();
@@ -478,37 +616,6 @@ __global__ void __launch_bounds__(1024) norm_fwd_wide_kernel(const NormParams p)
     }
     __syncthreads();  // both halves of red are written again by the next row
   }
-}
-
-// Totals over the CTA of M values a thread, for all threads. A warp halves the values that a lane carries with every exchange, so
-// that 32 / M lanes end with one each; `red` holds [warps][M]: another one for each of two consecutive calls.
-template <int M>
-__device__ __forceinline__ void column_totals(float (&v)[M], float* red) {
-  static_assert((M & (M - 1)) == 0 && M <= 16);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  int owned = 0;  // which value v[0] is in the end
-#pragma unroll
-  for (int half = M / 2, bit = 16; half > 0; half >>= 1, bit >>= 1) {
-    const bool up = (lane & bit) != 0;
-#pragma unroll
-    for (int i = 0; i < half; ++i) {
-      const float send = up ? v[i] : v[i + half];
-      const float keep = up ? v[i + half] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
-    }
-    owned += up ? half : 0;
-  }
-#pragma unroll
-  for (int bit = 16 / M; bit > 0; bit >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], bit);
-  if ((lane & (32 / M - 1)) == 0) red[warp * M + owned] = v[0];
-  __syncthreads();
-  // lane l: value l % M of the warps l / M, l / M + 32 / M, ...
-  float sum = 0.f;
-  for (int w = lane / M; w < warps; w += 32 / M) sum += red[w * M + (lane & (M - 1))];
-#pragma unroll
-  for (int bit = 16; bit >= M; bit >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, bit);
-#pragma unroll
-  for (int i = 0; i < M; ++i) v[i] = __shfl_sync(0xffffffffu, sum, i);
 }
 
 // One vector's part in dw, db and the two sums of its row. x: normalised values, g: dy.
@@ -1036,24 +1143,25 @@ cudaError_t fwd(NormParams p, cudaStream_t stream) {
   return launch(norm_fwd_kernel<T, VB, KC, KR>, dim3(static_cast<unsigned>(blocks)), cta, 0, stream, false, p);
 }
 
-template <typename T, int KC, int S, bool RES>
+template <typename T, int KC, int R, int S, bool RMS, bool RES>
 cudaError_t fwd_ring(NormParams p, int sms, cudaStream_t stream) {
   p.threads = round_threads(cdiv64(p.d, 16 / sizeof(T) * KC));
-  const int cta = p.threads > 32 ? p.threads : 128, smem = S * (RES ? 2 : 1) * KC * 16 * cta;
-  const cudaError_t e = allow_smem<norm_fwd_ring_kernel<T, KC, S, RES>>();
+  const int cta = p.threads > 32 ? p.threads : 128, smem = S * (RES ? 2 : 1) * R * KC * 16 * cta;
+  const cudaError_t e = allow_smem<norm_fwd_ring_kernel<T, KC, R, S, RMS, RES>>();
   if (e != cudaSuccess) return e;
-  const int by_smem = kSmemPerSm / (smem + 1280), by_threads = (KC == 4 ? 640 : 1024) / cta;  // the registers of 96 or 64 a thread
+  const int by_smem = kSmemPerSm / (smem + 1536), by_threads = (KC * 16 / sizeof(T) > 8 ? 512 : 768) / cta;
   const int64_t most = static_cast<int64_t>(sms) * (by_smem < by_threads ? by_smem : by_threads);
-  return launch(norm_fwd_ring_kernel<T, KC, S, RES>, dim3(blocks_for(cdiv64(p.N, cta / p.threads), most)), cta, smem, stream, false, p);
+  return launch(norm_fwd_ring_kernel<T, KC, R, S, RMS, RES>, dim3(blocks_for(cdiv64(p.N, static_cast<int64_t>(cta / p.threads) * R), most)), cta,
+                smem, stream, false, p);
 }
 
-template <typename T, bool RES>
+// Eight columns a thread, two rows at a time; of rows of more than 4096 columns 16 or 32 columns, one row at a time.
+template <typename T, bool RMS, bool RES>
 cudaError_t fwd_rings(const NormParams& p, int sms, cudaStream_t stream) {
-  constexpr int VB = 16 / sizeof(T);
-  if (p.d <= 32 * VB) return fwd_ring<T, 1, 8, RES>(p, sms, stream);
-  if (p.d <= 64 * VB) return fwd_ring<T, 2, 8, RES>(p, sms, stream);
-  if (!RES || p.d <= 256 * 4 * VB) return fwd_ring<T, 4, 4, RES>(p, sms, stream);
-  return fwd_ring<T, 4, 3, RES>(p, sms, stream);  // four rows of two streams would not fit
+  constexpr int K8 = 8 * sizeof(T) / 16;
+  if (p.d <= 512 * 8) return fwd_ring<T, K8, sizeof(T) == 2 ? 2 : 1, 4, RMS, RES>(p, sms, stream);
+  if (p.d <= 512 * 16) return fwd_ring<T, 2 * K8, 1, RES && sizeof(T) == 4 ? 3 : 4, RMS, RES>(p, sms, stream);
+  return fwd_ring<T, 4 * K8, 1, sizeof(T) == 4 || RES ? 3 : 4, RMS, RES>(p, sms, stream);
 }
 
 template <typename T, int VB>
@@ -1064,7 +1172,10 @@ cudaError_t fwd_cols(const NormParams& p, int sms, cudaStream_t stream) {
     if (p.d <= 512 * 16) return fwd<T, 1, 16, 1>(p, stream);
   } else {
     if (p.d <= 1024 * VB && p.N <= 4 * sms) return fwd<T, VB, 1, 1>(p, stream);  // few rows: what counts is the time of one
-    if (p.d <= 512 * 4 * VB) return p.residual ? fwd_rings<T, true>(p, sms, stream) : fwd_rings<T, false>(p, sms, stream);
+    if (p.d <= (sizeof(T) == 4 && p.residual ? 512 * 16 : 512 * 32)) {  // what the ring has room for
+      if (p.rms && p.bias == nullptr) return p.residual ? fwd_rings<T, true, true>(p, sms, stream) : fwd_rings<T, true, false>(p, sms, stream);
+      return p.residual ? fwd_rings<T, false, true>(p, sms, stream) : fwd_rings<T, false, false>(p, sms, stream);
+    }
   }
   return launch(norm_fwd_wide_kernel<T, VB>, dim3(blocks_for(p.N, 2 * static_cast<int64_t>(sms))), 1024, 0, stream, false, p);
 }
