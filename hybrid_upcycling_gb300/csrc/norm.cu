@@ -431,7 +431,7 @@ __device__ __forceinline__ void row_moments(const V (&raw)[R][KC], const NormPar
 // R rows at a time for each group of p.threads threads, KC vectors a thread and row, S - 1 times as many rows on their way. RMS:
 // neither means nor a bias.
 template <typename T, int KC, int R, int S, bool RMS, bool RES>
-__global__ void __launch_bounds__(512) norm_fwd_ring_kernel(const NormParams p) {
+__global__ void __launch_bounds__(512, 1) norm_fwd_ring_kernel(const NormParams p) {
   constexpr int VB = 16 / sizeof(T), C = KC * VB, STREAMS = RES ? 2 : 1;
   using V = Pack<T, VB>;
   extern __shared__ __align__(16) uint8_t ring[];  // [S][streams][R][KC][threads]
@@ -557,6 +557,215 @@ __global__ void __launch_bounds__(512) norm_fwd_ring_kernel(const NormParams p) 
   copy_wait<0>();
 }
 
+// ---- Rows that are not made of 16-byte vectors (an odd width, stride or start). Their bytes still come as whole 16-byte vectors of
+// memory into the ring, shifted by the row's start modulo 16, and are taken apart there: a warp has 32 C consecutive columns, a lane every 32nd
+// of them (fewer lanes where a row takes part of a warp), so that a warp reads and writes consecutive elements. What
+// these kernels cost is instructions: warps whose columns all exist go without a test for each (51 instructions an element with them). A vector's bytes in front of or behind the row belong to the
+// same tensor, except in front of its first element and behind its last one, which are not read.
+struct OddRows {
+  uintptr_t base, end;  // of the tensor
+  int64_t stride;       // bytes
+};
+template <typename T>
+__device__ __forceinline__ OddRows odd_rows(const void* p, int64_t ld, const NormParams& n) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return OddRows{a, a + static_cast<uintptr_t>(((n.N - 1) * ld + n.d) * static_cast<int64_t>(sizeof(T))), ld * static_cast<int64_t>(sizeof(T))};
+}
+// The group's threads copy row `row` to dst (16-byte aligned); its first element arrives at dst + odd_shift().
+__device__ __forceinline__ int odd_shift(const OddRows& x, int64_t row) { return static_cast<int>((x.base + row * x.stride) & 15); }
+template <typename T>
+__device__ __forceinline__ void odd_fetch(const OddRows& x, int64_t row, int d, uint32_t dst, int t, int threads) {
+  const uintptr_t a = x.base + row * x.stride, last = a + static_cast<uintptr_t>(d) * sizeof(T);
+  uintptr_t v = (a & ~static_cast<uintptr_t>(15)) + static_cast<uintptr_t>(t) * 16;
+  for (dst += t * 16; v < last; v += static_cast<uintptr_t>(threads) * 16, dst += threads * 16) {
+    if (v < x.base) {  // the tensor begins inside this vector
+      for (uintptr_t e = x.base; e < v + 16 && e < x.end; e += sizeof(T)) {
+        const T y = *reinterpret_cast<const T*>(e);
+        const uint32_t at = dst + static_cast<uint32_t>(e - v);
+        if constexpr (sizeof(T) == 2)
+          asm volatile("st.shared.u16 [%0], %1;" :: "r"(at), "h"(*reinterpret_cast<const uint16_t*>(&y)) : "memory");
+        else
+          asm volatile("st.shared.u32 [%0], %1;" :: "r"(at), "r"(*reinterpret_cast<const uint32_t*>(&y)) : "memory");
+      }
+    } else {
+      const uintptr_t left = x.end - v;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(v), "r"(left < 16 ? static_cast<int>(left) : 16) : "memory");
+    }
+  }
+}
+// A thread's C columns c0, c0 + L, ..., of a row: in the ring (0 behind the last one) and in memory. WHOLE: they all exist.
+template <bool WHOLE, typename T, int C>
+__device__ __forceinline__ void odd_read(const uint8_t* row, int c0, int L, int d, float (&x)[C]) {
+  const T* a = reinterpret_cast<const T*>(row) + c0;
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    if (WHOLE)
+      x[j] = to_float(a[j * 32]);
+    else
+      x[j] = c0 + j * L < d ? to_float(a[j * L]) : 0.f;
+  }
+}
+template <bool WHOLE, typename T, int C>
+__device__ __forceinline__ void odd_write(T* row, int c0, int L, int d, const float (&x)[C]) {
+  T* a = row + c0;
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    if (WHOLE)
+      a[j * 32] = from_float<T>(x[j]);
+    else if (c0 + j * L < d)
+      a[j * L] = from_float<T>(x[j]);
+  }
+}
+__device__ __forceinline__ void group_barrier(int threads) {
+  if (threads <= 32)
+    __syncwarp();
+  else
+    __syncthreads();
+}
+// Sums over the threads of a group.
+template <int M>
+__device__ __forceinline__ void group_totals(float (&v)[M], int threads, float* red) {
+  if (threads <= 32) {
+    for (int o = threads >> 1; o > 0; o >>= 1) {
+#pragma unroll
+      for (int i = 0; i < M; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    }
+  } else {
+    column_totals<M>(v, red);
+  }
+}
+__host__ __device__ constexpr int odd_bytes(int d, int size) { return (d * size + 15) / 16 * 16 + 16; }
+
+template <typename T, int C, int R, int S>
+__global__ void __launch_bounds__(512, 1) norm_fwd_odd_kernel(const NormParams p) {
+  extern __shared__ __align__(16) uint8_t ring[];  // [groups][S][streams][R][odd_bytes]
+  __shared__ float red[2][16 * R];
+  const int group = threadIdx.x / p.threads, t = threadIdx.x - group * p.threads, groups = blockDim.x / p.threads;
+  const int streams = p.residual != nullptr ? 2 : 1, bytes = odd_bytes(p.d, sizeof(T));
+  const int L = p.threads < 32 ? p.threads : 32, c0 = (t >> 5) * 32 * C + (t & 31);
+  const bool whole = L == 32 && ((t >> 5) + 1) * 32 * C <= p.d;
+  uint8_t* mine = ring + static_cast<size_t>(group) * S * streams * R * bytes;
+  auto place = [&](int slot, int stream, int r) { return mine + ((slot * streams + stream) * R + r) * bytes; };
+  const OddRows x0 = odd_rows<T>(p.x, p.ldx, p), x1 = odd_rows<T>(p.residual, p.ldr, p);
+  const float inv_d = 1.f / static_cast<float>(p.d);
+  auto fetch = [&](int slot, int64_t row0) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (row0 + r < p.N) {
+        odd_fetch<T>(x0, row0 + r, p.d, smem_u32(place(slot, 0, r)), t, p.threads);
+        if (streams == 2) odd_fetch<T>(x1, row0 + r, p.d, smem_u32(place(slot, 1, r)), t, p.threads);
+      }
+    }
+    copy_commit();
+  };
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups * R;
+  int64_t row0 = (static_cast<int64_t>(blockIdx.x) * groups + group) * R;
+  int64_t base = static_cast<int64_t>(blockIdx.x) * groups * R;  // of the CTA: all its threads take part in every barrier
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) fetch(i, row0 + i * step);
+  float w[C], b[C];
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    const int c = c0 + j * L;
+    w[j] = 1.f, b[j] = 0.f;
+    if (p.weight != nullptr && c < p.d) load_gain<T, 1>(p.weight, p.gain_f32, c, w + j);
+    if (p.bias != nullptr && c < p.d) load_gain<T, 1>(p.bias, p.gain_f32, c, b + j);
+  }
+  int slot = 0, ahead = S - 1, flip = 0;
+  float x[R][C], mu[R], m2[R];
+  auto read = [&](auto all) {
+    constexpr bool WHOLE = decltype(all)::value;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      mu[r] = 0.f;
+      if (row0 + r < p.N) {
+        odd_read<WHOLE, T, C>(place(slot, 0, r) + odd_shift(x0, row0 + r), c0, L, p.d, x[r]);
+        if (streams == 2) {
+          float y[C];
+          odd_read<WHOLE, T, C>(place(slot, 1, r) + odd_shift(x1, row0 + r), c0, L, p.d, y);
+          plus(x[r], y);
+#pragma unroll
+          for (int j = 0; j < C; ++j) x[r][j] = to_float(from_float<T>(x[r][j]));  // as the next layer reads it
+          odd_write<WHOLE, T, C>(static_cast<T*>(p.sum) + (row0 + r) * p.d, c0, L, p.d, x[r]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < C; ++j) x[r][j] = 0.f;
+      }
+    }
+  };
+  auto square = [&](auto all) {
+    constexpr bool WHOLE = decltype(all)::value;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float2 sum = two(0.f);
+#pragma unroll
+      for (int j = 0; j < C; j += 2) {
+        const float2 y = __fadd2_rn(pair(x[r] + j), two(-mu[r]));
+        x[r][j] = y.x, x[r][j + 1] = y.y;
+        float2 z = y;
+        if (!WHOLE) {  // columns that do not exist
+          if (c0 + j * L >= p.d) z.x = 0.f;
+          if (c0 + (j + 1) * L >= p.d) z.y = 0.f;
+        }
+        sum = __ffma2_rn(z, z, sum);
+      }
+      m2[r] = sum.x + sum.y;
+    }
+  };
+  auto write = [&](auto all) {
+    constexpr bool WHOLE = decltype(all)::value;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (row0 + r < p.N) {
+        const float rstd = rsqrtf(fmaf(m2[r], inv_d, p.eps));
+        if (t == 0 && p.stats != nullptr) p.stats[row0 + r] = make_float2(mu[r], rstd);
+        normalise<false>(x[r], 0.f, rstd);
+        times(x[r], w);
+        plus(x[r], b);
+        odd_write<WHOLE, T, C>(static_cast<T*>(p.y) + (row0 + r) * p.d, c0, L, p.d, x[r]);
+      }
+    }
+  };
+  const std::true_type yes;
+  const std::false_type no;
+  for (; base < p.N; base += step, row0 += step) {
+    copy_wait<S - 2>();
+    group_barrier(p.threads);  // the rows are there, and those of the turn before have been read
+    fetch(ahead, row0 + (S - 1) * step);
+    ahead = ahead + 1 == S ? 0 : ahead + 1;
+    if (whole)
+      read(yes);
+    else
+      read(no);
+    slot = slot + 1 == S ? 0 : slot + 1;
+    if (!p.rms) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float2 sum = two(0.f);
+#pragma unroll
+        for (int j = 0; j < C; j += 2) sum = __fadd2_rn(pair(x[r] + j), sum);
+        mu[r] = sum.x + sum.y;
+      }
+      group_totals<R>(mu, p.threads, red[flip]);
+      flip ^= 1;
+#pragma unroll
+      for (int r = 0; r < R; ++r) mu[r] *= inv_d;
+    }
+    if (whole)
+      square(yes);
+    else
+      square(no);
+    group_totals<R>(m2, p.threads, red[flip]);
+    flip ^= 1;
+    if (whole)
+      write(yes);
+    else
+      write(no);
+  }
+  copy_wait<0>();
+}
+
 // Rows too wide for the registers: a CTA reads its row again for each of the three steps.
 template <typename T, int VB>
 __global__ void __launch_bounds__(1024) norm_fwd_wide_kernel(const NormParams p) {
@@ -669,72 +878,94 @@ __device__ __forceinline__ void add_groups(const NormParams& p, const NormGrad& 
   }
 }
 
-// The gradients for rows of single elements: eight columns a thread, p.threads apart, in registers.
-template <typename T>
-__global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p, const NormGrad q) {
-  constexpr int C = 8;
-  extern __shared__ __align__(16) float shared[];  // [2][32][2] sums of rows; then [groups][d] columns' sums where a CTA has several groups
-  const int group = threadIdx.x / p.threads, t = threadIdx.x - group * p.threads;
-  const int groups = blockDim.x / p.threads;
+// The gradients of such rows, one at a time.
+template <typename T, int C, int S>
+__global__ void __launch_bounds__(512, 1) norm_bwd_odd_kernel(const NormParams p, const NormGrad q) {
+  extern __shared__ __align__(16) float shared[];  // [2][32] sums of rows, then the ring [groups][S][streams][odd_bytes], or columns' sums
+  uint8_t* ring = reinterpret_cast<uint8_t*>(shared + 64);
+  const int group = threadIdx.x / p.threads, t = threadIdx.x - group * p.threads, groups = blockDim.x / p.threads;
+  const int streams = q.dsum != nullptr ? 3 : 2, bytes = odd_bytes(p.d, sizeof(T));
+  const int L = p.threads < 32 ? p.threads : 32, c0 = (t >> 5) * 32 * C + (t & 31);
+  const bool whole = L == 32 && ((t >> 5) + 1) * 32 * C <= p.d;
+  uint8_t* mine = ring + static_cast<size_t>(group) * S * streams * bytes;
+  auto place = [&](int slot, int stream) { return mine + (slot * streams + stream) * bytes; };
+  const OddRows x0 = odd_rows<T>(p.x, p.ldx, p), x1 = odd_rows<T>(q.dy, q.lddy, p), x2 = odd_rows<T>(q.dsum, q.ldds, p);
   const float inv_d = 1.f / static_cast<float>(p.d);
+  auto fetch = [&](int slot, int64_t row) {
+    if (row < p.N) {
+      odd_fetch<T>(x0, row, p.d, smem_u32(place(slot, 0)), t, p.threads);
+      odd_fetch<T>(x1, row, p.d, smem_u32(place(slot, 1)), t, p.threads);
+      if (streams == 3) odd_fetch<T>(x2, row, p.d, smem_u32(place(slot, 2)), t, p.threads);
+    }
+    copy_commit();
+  };
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * groups + group;
+  int64_t base = static_cast<int64_t>(blockIdx.x) * groups;  // of the CTA: all its threads take part in every barrier
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) fetch(i, row + i * step);
   float dw[C], db[C], w[C];
 #pragma unroll
   for (int j = 0; j < C; ++j) {
-    const int c = j * p.threads + t;
+    const int c = c0 + j * L;
     dw[j] = db[j] = 0.f, w[j] = 1.f;
     if (p.weight != nullptr && c < p.d) load_gain<T, 1>(p.weight, p.gain_f32, c, w + j);
   }
-  int flip = 0;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * groups; base < p.N; base += step) {
-    const int64_t row = base + group;
+  int slot = 0, ahead = S - 1, flip = 0;
+  float x[C], g[C], more[C];
+  auto read = [&](auto all) {
+    constexpr bool WHOLE = decltype(all)::value;
+    odd_read<WHOLE, T, C>(place(slot, 0) + odd_shift(x0, row), c0, L, p.d, x);
+    odd_read<WHOLE, T, C>(place(slot, 1) + odd_shift(x1, row), c0, L, p.d, g);
+    if (streams == 3) odd_read<WHOLE, T, C>(place(slot, 2) + odd_shift(x2, row), c0, L, p.d, more);
+  };
+  const std::true_type yes;
+  const std::false_type no;
+  for (; base < p.N; base += step, row += step) {
     const bool live = row < p.N;
     const float2 st = live ? p.stats[row] : make_float2(0.f, 0.f);
-    T a[C], b[C], e[C];
+    copy_wait<S - 2>();
+    group_barrier(p.threads);  // the rows are there, and those of the turn before have been read
+    fetch(ahead, row + (S - 1) * step);
+    ahead = ahead + 1 == S ? 0 : ahead + 1;
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-      const int c = j * p.threads + t;
-      const bool there = live && c < p.d;
-      a[j] = b[j] = e[j] = from_float<T>(0.f);
-      if (there) a[j] = static_cast<const T*>(p.x)[row * p.ldx + c];
-      if (there) b[j] = static_cast<const T*>(q.dy)[row * q.lddy + c];
-      if (there && q.dsum != nullptr) e[j] = static_cast<const T*>(q.dsum)[row * q.ldds + c];
+    for (int j = 0; j < C; ++j) x[j] = g[j] = more[j] = 0.f;
+    if (live) {
+      if (whole)
+        read(yes);
+      else
+        read(no);
     }
-    float x[C], g[C], v[2] = {0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < C; ++j) x[j] = to_float(a[j]), g[j] = to_float(b[j]);
+    slot = slot + 1 == S ? 0 : slot + 1;
     normalise<true>(x, st.x, st.y);
     float2 sx = two(0.f), sg = two(0.f);
     column_step<false>(x, g, w, dw, db, sx, sg);
     if (q.dx == nullptr) continue;
-    v[0] = sx.x + sx.y, v[1] = sg.x + sg.y;
-    if (p.threads <= 32) {
-      for (int o = p.threads >> 1; o > 0; o >>= 1) {
-        v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
-        v[1] += __shfl_xor_sync(0xffffffffu, v[1], o);
-      }
-    } else {
-      column_totals<2>(v, shared + flip * 64);
-      flip ^= 1;
-    }
+    float v[2] = {sx.x + sx.y, sg.x + sg.y};
+    group_totals<2>(v, p.threads, shared + flip * 32);
+    flip ^= 1;
     row_step(x, g, w, st.y, -st.y * v[0] * inv_d, p.rms ? 0.f : -st.y * v[1] * inv_d);
-#pragma unroll
-    for (int j = 0; j < C; ++j) {
-      const int c = j * p.threads + t;
-      if (live && c < p.d) static_cast<T*>(q.dx)[row * p.d + c] = from_float<T>(q.dsum != nullptr ? g[j] + to_float(e[j]) : g[j]);
+    if (streams == 3) plus(g, more);
+    T* dx = static_cast<T*>(q.dx) + row * p.d;
+    if (live) {
+      if (whole)
+        odd_write<true, T, C>(dx, c0, L, p.d, g);
+      else
+        odd_write<false, T, C>(dx, c0, L, p.d, g);
     }
   }
   grid_dep_launch();
+  copy_wait<0>();
   if (q.part == nullptr) return;
   float* part = q.part + static_cast<int64_t>(blockIdx.x) * p.d;
   const int64_t second = static_cast<int64_t>(gridDim.x) * p.d;
   if (groups > 1) {
-    add_groups<C, 1>(p, q, dw, db, group, groups, t, shared + 128, part, second);
+    add_groups<C, 1>(p, q, dw, db, group, groups, t, reinterpret_cast<float*>(ring), part, second);  // begins with a barrier; threads <= 32
     return;
   }
 #pragma unroll
   for (int j = 0; j < C; ++j) {
-    const int c = j * p.threads + t;
+    const int c = c0 + j * L;
     if (c < p.d) {
       if (q.want_dw) part[c] = dw[j];
       if (q.want_db) part[second + c] = db[j];
@@ -744,7 +975,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p, const
 
 // The gradients for rows of 16-byte vectors: as above, R rows of a group at a time and S - 1 times as many on their way.
 template <typename T, int KC, int R, int S, bool RMS, bool DSUM>
-__global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const NormParams p, const NormGrad q) {
+__global__ void __launch_bounds__(512, 1) norm_bwd_ring_kernel(const NormParams p, const NormGrad q) {
   constexpr int VB = 16 / sizeof(T), C = KC * VB, STREAMS = DSUM ? 3 : 2;
   using V = Pack<T, VB>;
   extern __shared__ __align__(16) float shared[];  // [2][32][2 R] sums of rows, then the ring [S][streams][R][KC][threads], or columns' sums
@@ -866,14 +1097,14 @@ __global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const NormParams p, 
       }
     }
   } else {
-    add_groups<C, VB>(p, q, dw, db, group, groups, t, reinterpret_cast<float*>(ring), part, second);
+    add_groups<C, VB>(p, q, dw, db, group, groups, t, reinterpret_cast<float*>(ring), part, second);  // begins with a barrier
   }
 }
 
 // The same for rows that a cluster shares, q.cta_cols columns a CTA, one row at a time. Order of a turn: the sums of row i; the
 // totals of row i - 1, which the CTAs have exchanged meanwhile; the exchange of row i; dx of row i - 1.
 template <typename T, int KC, int S, bool RMS, bool DSUM>
-__global__ void __launch_bounds__(512) norm_bwd_cluster_kernel(const NormParams p, const NormGrad q) {
+__global__ void __launch_bounds__(512, 1) norm_bwd_cluster_kernel(const NormParams p, const NormGrad q) {
   constexpr int VB = 16 / sizeof(T), C = KC * VB, STREAMS = DSUM ? 3 : 2;
   using V = Pack<T, VB>;
   extern __shared__ __align__(16) float shared[];  // [2][16 warps][2] sums, [3][8 CTAs][2] exchanged ones, then the ring [S][streams][KC][threads]
@@ -1155,6 +1386,18 @@ cudaError_t fwd_ring(NormParams p, int sms, cudaStream_t stream) {
                 smem, stream, false, p);
 }
 
+template <typename T, int C, int R, int S>
+cudaError_t fwd_odd(NormParams p, int sms, cudaStream_t stream) {
+  p.threads = round_threads(cdiv64(p.d, C));
+  const int cta = p.threads > 32 ? p.threads : 128, groups = cta / p.threads;
+  const int smem = groups * S * (p.residual ? 2 : 1) * R * odd_bytes(p.d, sizeof(T));
+  const cudaError_t e = allow_smem<norm_fwd_odd_kernel<T, C, R, S>>();
+  if (e != cudaSuccess) return e;
+  const int by_smem = kSmemPerSm / (smem + 1536), by_threads = 512 / cta;
+  const int64_t most = static_cast<int64_t>(sms) * (by_smem < by_threads ? by_smem : by_threads);
+  return launch(norm_fwd_odd_kernel<T, C, R, S>, dim3(blocks_for(cdiv64(p.N, static_cast<int64_t>(groups) * R), most)), cta, smem, stream, false, p);
+}
+
 // Eight columns a thread, two rows at a time; of rows of more than 4096 columns 16 or 32 columns, one row at a time.
 template <typename T, bool RMS, bool RES>
 cudaError_t fwd_rings(const NormParams& p, int sms, cudaStream_t stream) {
@@ -1167,9 +1410,10 @@ cudaError_t fwd_rings(const NormParams& p, int sms, cudaStream_t stream) {
 template <typename T, int VB>
 cudaError_t fwd_cols(const NormParams& p, int sms, cudaStream_t stream) {
   if constexpr (VB == 1) {
-    if (p.d <= 1024 && p.N <= 4 * sms) return fwd<T, 1, 1, 1>(p, stream);
-    if (p.d <= 128) return fwd<T, 1, 4, 2>(p, stream);
-    if (p.d <= 512 * 16) return fwd<T, 1, 16, 1>(p, stream);
+    if (p.d <= 1024 && p.N <= 2 * sms) return fwd<T, 1, 1, 1>(p, stream);
+    if (p.d <= 512 * 8) return fwd_odd<T, 8, sizeof(T) == 2 ? 2 : 1, 4>(p, sms, stream);
+    if (p.d <= 512 * 16) return fwd_odd<T, 16, 1, 3>(p, sms, stream);
+    if (p.d <= 512 * 32 && (sizeof(T) == 2 || p.residual == nullptr)) return fwd_odd<T, 32, 1, 3>(p, sms, stream);
   } else {
     if (p.d <= 1024 * VB && p.N <= 4 * sms) return fwd<T, VB, 1, 1>(p, stream);  // few rows: what counts is the time of one
     if (p.d <= (sizeof(T) == 4 && p.residual ? 512 * 16 : 512 * 32)) {  // what the ring has room for
@@ -1231,6 +1475,18 @@ cudaError_t bwd_vectors(const NormParams& p, const NormGrad& q, int* parts, cuda
   return p.d <= kCtaCols ? bwd_ring<T, RMS, DSUM>(p, q, parts, stream) : bwd_cluster<T, RMS, DSUM>(p, q, parts, stream);
 }
 
+template <typename T, int C, int S>
+cudaError_t bwd_odd(NormParams p, const NormGrad& q, int* parts, cudaStream_t stream) {
+  p.threads = round_threads(cdiv64(p.d, C));
+  const int cta = p.threads > 32 ? p.threads : 128, groups = cta / p.threads;
+  const cudaError_t e = allow_smem<norm_bwd_odd_kernel<T, C, S>>();
+  if (e != cudaSuccess) return e;
+  size_t smem = static_cast<size_t>(groups) * S * (q.dsum ? 3 : 2) * odd_bytes(p.d, sizeof(T));
+  if (groups > 1 && static_cast<size_t>(groups) * p.d * sizeof(float) > smem) smem = static_cast<size_t>(groups) * p.d * sizeof(float);
+  *parts = static_cast<int>(blocks_for(cdiv64(p.N, groups), *parts));
+  return launch(norm_bwd_odd_kernel<T, C, S>, dim3(*parts), cta, 64 * sizeof(float) + smem, stream, false, p, q);
+}
+
 // *parts: rows of q.part that there may be, and how many were written.
 template <typename T, int VB>
 cudaError_t bwd_cols(NormParams p, const NormGrad& q, int* parts, int sms, cudaStream_t stream) {
@@ -1239,12 +1495,9 @@ cudaError_t bwd_cols(NormParams p, const NormGrad& q, int* parts, int sms, cudaS
       if (p.rms && !q.want_db) return q.dsum ? bwd_vectors<T, true, true>(p, q, parts, stream) : bwd_vectors<T, true, false>(p, q, parts, stream);
       return q.dsum ? bwd_vectors<T, false, true>(p, q, parts, stream) : bwd_vectors<T, false, false>(p, q, parts, stream);
     }
-  } else if (p.d <= kCtaCols) {
-    p.threads = round_threads(cdiv64(p.d, kBwdCols));
-    const int cta = p.threads > 32 ? p.threads : 128, groups = cta / p.threads;
-    *parts = static_cast<int>(blocks_for(cdiv64(p.N, groups), *parts));
-    const size_t smem = (128 + (groups > 1 ? groups * p.d : 0)) * sizeof(float);
-    return launch(norm_bwd_kernel<T>, dim3(*parts), cta, smem, stream, false, p, q);
+  } else {
+    if (p.d <= kCtaCols) return bwd_odd<T, 8, 4>(p, q, parts, stream);
+    if (p.d <= 2 * kCtaCols) return bwd_odd<T, 16, sizeof(T) == 2 ? 4 : 2>(p, q, parts, stream);
   }
   cudaError_t e = cudaSuccess;
   if (q.dx != nullptr)
