@@ -593,27 +593,29 @@ __device__ __forceinline__ void odd_fetch(const OddRows& x, int64_t row, int d, 
     }
   }
 }
-// A thread's C columns c0, c0 + L, ..., of a row: in the ring (0 behind the last one) and in memory. WHOLE: they all exist.
-template <bool WHOLE, typename T, int C>
-__device__ __forceinline__ void odd_read(const uint8_t* row, int c0, int L, int d, float (&x)[C]) {
+// A thread's C columns c0, c0 + L, ..., of which the first `n` exist, of a row: in the ring (0 behind the last one) and in memory.
+// MODE kAll: all exist; kSome: L is 32; kFew: L is less.
+enum : int { kAll = 0, kSome = 1, kFew = 2 };
+template <int MODE>
+using Mode = std::integral_constant<int, MODE>;
+template <int MODE, typename T, int C>
+__device__ __forceinline__ void odd_read(const uint8_t* row, int c0, int L, int n, float (&x)[C]) {
   const T* a = reinterpret_cast<const T*>(row) + c0;
 #pragma unroll
   for (int j = 0; j < C; ++j) {
-    if (WHOLE)
-      x[j] = to_float(a[j * 32]);
-    else
-      x[j] = c0 + j * L < d ? to_float(a[j * L]) : 0.f;
+    const int at = MODE == kFew ? j * L : j * 32;
+    T y = from_float<T>(0.f);
+    if (MODE == kAll || j < n) y = a[at];
+    x[j] = to_float(y);
   }
 }
-template <bool WHOLE, typename T, int C>
-__device__ __forceinline__ void odd_write(T* row, int c0, int L, int d, const float (&x)[C]) {
+template <int MODE, typename T, int C>
+__device__ __forceinline__ void odd_write(T* row, int c0, int L, int n, const float (&x)[C]) {
   T* a = row + c0;
 #pragma unroll
   for (int j = 0; j < C; ++j) {
-    if (WHOLE)
-      a[j * 32] = from_float<T>(x[j]);
-    else if (c0 + j * L < d)
-      a[j * L] = from_float<T>(x[j]);
+    const T y = from_float<T>(x[j]);
+    if (MODE == kAll || j < n) a[MODE == kFew ? j * L : j * 32] = y;
   }
 }
 __device__ __forceinline__ void group_barrier(int threads) {
@@ -643,7 +645,7 @@ __global__ void __launch_bounds__(512, 1) norm_fwd_odd_kernel(const NormParams p
   const int group = threadIdx.x / p.threads, t = threadIdx.x - group * p.threads, groups = blockDim.x / p.threads;
   const int streams = p.residual != nullptr ? 2 : 1, bytes = odd_bytes(p.d, sizeof(T));
   const int L = p.threads < 32 ? p.threads : 32, c0 = (t >> 5) * 32 * C + (t & 31);
-  const bool whole = L == 32 && ((t >> 5) + 1) * 32 * C <= p.d;
+  const int n = c0 < p.d ? min(C, (p.d - c0 + L - 1) / L) : 0, mode = L < 32 ? kFew : ((t >> 5) + 1) * 32 * C <= p.d ? kAll : kSome;
   uint8_t* mine = ring + static_cast<size_t>(group) * S * streams * R * bytes;
   auto place = [&](int slot, int stream, int r) { return mine + ((slot * streams + stream) * R + r) * bytes; };
   const OddRows x0 = odd_rows<T>(p.x, p.ldx, p), x1 = odd_rows<T>(p.residual, p.ldr, p);
@@ -673,20 +675,20 @@ __global__ void __launch_bounds__(512, 1) norm_fwd_odd_kernel(const NormParams p
   }
   int slot = 0, ahead = S - 1, flip = 0;
   float x[R][C], mu[R], m2[R];
-  auto read = [&](auto all) {
-    constexpr bool WHOLE = decltype(all)::value;
+  auto read = [&](auto m) {
+    constexpr int MODE = decltype(m)::value;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       mu[r] = 0.f;
       if (row0 + r < p.N) {
-        odd_read<WHOLE, T, C>(place(slot, 0, r) + odd_shift(x0, row0 + r), c0, L, p.d, x[r]);
+        odd_read<MODE, T, C>(place(slot, 0, r) + odd_shift(x0, row0 + r), c0, L, n, x[r]);
         if (streams == 2) {
           float y[C];
-          odd_read<WHOLE, T, C>(place(slot, 1, r) + odd_shift(x1, row0 + r), c0, L, p.d, y);
+          odd_read<MODE, T, C>(place(slot, 1, r) + odd_shift(x1, row0 + r), c0, L, n, y);
           plus(x[r], y);
 #pragma unroll
           for (int j = 0; j < C; ++j) x[r][j] = to_float(from_float<T>(x[r][j]));  // as the next layer reads it
-          odd_write<WHOLE, T, C>(static_cast<T*>(p.sum) + (row0 + r) * p.d, c0, L, p.d, x[r]);
+          odd_write<MODE, T, C>(static_cast<T*>(p.sum) + (row0 + r) * p.d, c0, L, n, x[r]);
         }
       } else {
 #pragma unroll
@@ -694,8 +696,8 @@ __global__ void __launch_bounds__(512, 1) norm_fwd_odd_kernel(const NormParams p
       }
     }
   };
-  auto square = [&](auto all) {
-    constexpr bool WHOLE = decltype(all)::value;
+  auto square = [&](auto m) {
+    constexpr int MODE = decltype(m)::value;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       float2 sum = two(0.f);
@@ -704,17 +706,17 @@ __global__ void __launch_bounds__(512, 1) norm_fwd_odd_kernel(const NormParams p
         const float2 y = __fadd2_rn(pair(x[r] + j), two(-mu[r]));
         x[r][j] = y.x, x[r][j + 1] = y.y;
         float2 z = y;
-        if (!WHOLE) {  // columns that do not exist
-          if (c0 + j * L >= p.d) z.x = 0.f;
-          if (c0 + (j + 1) * L >= p.d) z.y = 0.f;
+        if (MODE != kAll) {
+          if (j >= n) z.x = 0.f;
+          if (j + 1 >= n) z.y = 0.f;
         }
         sum = __ffma2_rn(z, z, sum);
       }
       m2[r] = sum.x + sum.y;
     }
   };
-  auto write = [&](auto all) {
-    constexpr bool WHOLE = decltype(all)::value;
+  auto write = [&](auto m) {
+    constexpr int MODE = decltype(m)::value;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       if (row0 + r < p.N) {
@@ -723,21 +725,24 @@ __global__ void __launch_bounds__(512, 1) norm_fwd_odd_kernel(const NormParams p
         normalise<false>(x[r], 0.f, rstd);
         times(x[r], w);
         plus(x[r], b);
-        odd_write<WHOLE, T, C>(static_cast<T*>(p.y) + (row0 + r) * p.d, c0, L, p.d, x[r]);
+        odd_write<MODE, T, C>(static_cast<T*>(p.y) + (row0 + r) * p.d, c0, L, n, x[r]);
       }
     }
   };
-  const std::true_type yes;
-  const std::false_type no;
+  auto by_mode = [&](auto f) {
+    if (mode == kAll)
+      f(Mode<kAll>{});
+    else if (mode == kSome)
+      f(Mode<kSome>{});
+    else
+      f(Mode<kFew>{});
+  };
   for (; base < p.N; base += step, row0 += step) {
     copy_wait<S - 2>();
     group_barrier(p.threads);  // the rows are there, and those of the turn before have been read
     fetch(ahead, row0 + (S - 1) * step);
     ahead = ahead + 1 == S ? 0 : ahead + 1;
-    if (whole)
-      read(yes);
-    else
-      read(no);
+    by_mode(read);
     slot = slot + 1 == S ? 0 : slot + 1;
     if (!p.rms) {
 #pragma unroll
@@ -752,16 +757,10 @@ __global__ void __launch_bounds__(512, 1) norm_fwd_odd_kernel(const NormParams p
 #pragma unroll
       for (int r = 0; r < R; ++r) mu[r] *= inv_d;
     }
-    if (whole)
-      square(yes);
-    else
-      square(no);
+    by_mode(square);
     group_totals<R>(m2, p.threads, red[flip]);
     flip ^= 1;
-    if (whole)
-      write(yes);
-    else
-      write(no);
+    by_mode(write);
   }
   copy_wait<0>();
 }
@@ -886,7 +885,7 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_odd_kernel(const NormParams p
   const int group = threadIdx.x / p.threads, t = threadIdx.x - group * p.threads, groups = blockDim.x / p.threads;
   const int streams = q.dsum != nullptr ? 3 : 2, bytes = odd_bytes(p.d, sizeof(T));
   const int L = p.threads < 32 ? p.threads : 32, c0 = (t >> 5) * 32 * C + (t & 31);
-  const bool whole = L == 32 && ((t >> 5) + 1) * 32 * C <= p.d;
+  const int n = c0 < p.d ? min(C, (p.d - c0 + L - 1) / L) : 0, mode = L < 32 ? kFew : ((t >> 5) + 1) * 32 * C <= p.d ? kAll : kSome;
   uint8_t* mine = ring + static_cast<size_t>(group) * S * streams * bytes;
   auto place = [&](int slot, int stream) { return mine + (slot * streams + stream) * bytes; };
   const OddRows x0 = odd_rows<T>(p.x, p.ldx, p), x1 = odd_rows<T>(q.dy, q.lddy, p), x2 = odd_rows<T>(q.dsum, q.ldds, p);
@@ -913,14 +912,20 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_odd_kernel(const NormParams p
   }
   int slot = 0, ahead = S - 1, flip = 0;
   float x[C], g[C], more[C];
-  auto read = [&](auto all) {
-    constexpr bool WHOLE = decltype(all)::value;
-    odd_read<WHOLE, T, C>(place(slot, 0) + odd_shift(x0, row), c0, L, p.d, x);
-    odd_read<WHOLE, T, C>(place(slot, 1) + odd_shift(x1, row), c0, L, p.d, g);
-    if (streams == 3) odd_read<WHOLE, T, C>(place(slot, 2) + odd_shift(x2, row), c0, L, p.d, more);
+  auto read = [&](auto m) {
+    constexpr int MODE = decltype(m)::value;
+    odd_read<MODE, T, C>(place(slot, 0) + odd_shift(x0, row), c0, L, n, x);
+    odd_read<MODE, T, C>(place(slot, 1) + odd_shift(x1, row), c0, L, n, g);
+    if (streams == 3) odd_read<MODE, T, C>(place(slot, 2) + odd_shift(x2, row), c0, L, n, more);
   };
-  const std::true_type yes;
-  const std::false_type no;
+  auto by_mode = [&](auto f) {
+    if (mode == kAll)
+      f(Mode<kAll>{});
+    else if (mode == kSome)
+      f(Mode<kSome>{});
+    else
+      f(Mode<kFew>{});
+  };
   for (; base < p.N; base += step, row += step) {
     const bool live = row < p.N;
     const float2 st = live ? p.stats[row] : make_float2(0.f, 0.f);
@@ -930,12 +935,7 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_odd_kernel(const NormParams p
     ahead = ahead + 1 == S ? 0 : ahead + 1;
 #pragma unroll
     for (int j = 0; j < C; ++j) x[j] = g[j] = more[j] = 0.f;
-    if (live) {
-      if (whole)
-        read(yes);
-      else
-        read(no);
-    }
+    if (live) by_mode(read);
     slot = slot + 1 == S ? 0 : slot + 1;
     normalise<true>(x, st.x, st.y);
     float2 sx = two(0.f), sg = two(0.f);
@@ -947,12 +947,7 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_odd_kernel(const NormParams p
     row_step(x, g, w, st.y, -st.y * v[0] * inv_d, p.rms ? 0.f : -st.y * v[1] * inv_d);
     if (streams == 3) plus(g, more);
     T* dx = static_cast<T*>(q.dx) + row * p.d;
-    if (live) {
-      if (whole)
-        odd_write<true, T, C>(dx, c0, L, p.d, g);
-      else
-        odd_write<false, T, C>(dx, c0, L, p.d, g);
-    }
+    if (live) by_mode([&](auto m) { odd_write<decltype(m)::value, T, C>(dx, c0, L, n, g); });
   }
   grid_dep_launch();
   copy_wait<0>();
