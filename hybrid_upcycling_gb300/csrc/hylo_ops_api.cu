@@ -545,7 +545,8 @@ hylo_status hylo_norm_backward(const void* s, int dtype, int64_t N, int64_t d, i
   NormParams p{};
   p.x = s, p.ldx = lds, p.N = N, p.d = static_cast<int>(d), p.rms = rms != 0, p.weight = weight, p.gain_f32 = gain_dtype == HYLO_F32;
   p.stats = reinterpret_cast<float2*>(const_cast<float*>(stats));
-  const NormGrad q{dy, dsum, lddy, ldds, dx, columns ? static_cast<float*>(workspace) : nullptr, dweight != nullptr, dbias != nullptr, dweight, dbias, 0};
+  const NormGrad q{dy, dsum, lddy, ldds, dx, columns ? static_cast<float*>(workspace) : nullptr, dweight != nullptr, dbias != nullptr, dweight, dbias, 0,
+                   WaitCtl{dev->status, wait_limit_ns()}};
   const cudaError_t err = launch_norm_bwd(p, q, dtype, norm_parts(N, p.d), dev->sms, stream);
   return err == cudaSuccess ? HYLO_OK : cuda_fail(err, "launch norm backward");
 }

@@ -157,6 +157,7 @@ struct NormGrad {
   void* dw;
   void* db;
   int cta_cols;      // columns of a CTA of a cluster, set by the launch
+  WaitCtl ctl;
 };
 // Widest rows (fp32: half of it) whose gradients are formed in one reading, and how many rows of `part` there may be.
 constexpr int kNormFusedCols = 65536;

@@ -1096,14 +1096,22 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_ring_kernel(const NormParams 
   }
 }
 
-// The same for rows that a cluster shares, q.cta_cols columns a CTA, one row at a time. Order of a turn: the sums of row i; the
-// totals of row i - 1, which the CTAs have exchanged meanwhile; the exchange of row i; dx of row i - 1.
+// The same for rows that a cluster shares, q.cta_cols columns a CTA, one row at a time. Order of a turn: the sums of row i; the wait
+// for those of row i - 1, which the CTAs have sent one another meanwhile; the sending of row i's; dx of row i - 1. The sums
+// arrive with st.async, counted on a barrier of the CTA that receives them (a cluster barrier a turn took twice as long). Three
+// places for them are enough: a CTA sends row i + 3's only after it has this CTA's of row i + 2, sent after all here were done with row i's.
+__device__ __forceinline__ void send_pair(uint32_t to, float a, float b, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];"
+               :: "r"(to), "r"(__float_as_uint(a)), "r"(__float_as_uint(b)), "r"(bar) : "memory");
+}
 template <typename T, int KC, int S, bool RMS, bool DSUM>
 __global__ void __launch_bounds__(512, 1) norm_bwd_cluster_kernel(const NormParams p, const NormGrad q) {
   constexpr int VB = 16 / sizeof(T), C = KC * VB, STREAMS = DSUM ? 3 : 2;
   using V = Pack<T, VB>;
   extern __shared__ __align__(16) float shared[];  // [2][16 warps][2] sums, [3][8 CTAs][2] exchanged ones, then the ring [S][streams][KC][threads]
   float* across = shared + 64;
+  __shared__ uint64_t arrived[3];
+  __shared__ int given_up;
   uint8_t* ring = reinterpret_cast<uint8_t*>(shared + 128);
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, warps = blockDim.x >> 5;
   const uint32_t rank = cluster_ctarank(), ctas = gridDim.x;
@@ -1139,7 +1147,12 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_cluster_kernel(const NormPara
   int64_t row = blockIdx.y;
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) fetch(i, row + i * step);
-  cluster_sync_all();  // every CTA is there before its shared memory is written to
+  if (t == 0) {
+    for (int j = 0; j < 3; ++j) mbar_init(arrived + j, 1);
+    given_up = 0;
+    fence_mbar_init();
+  }
+  cluster_sync_all();  // every CTA's barriers are there before it is written to
   float2 now = row < p.N ? p.stats[row] : make_float2(0.f, 0.f), before = now;
   int slot = 0, last = 0, i = 0;
   auto finish = [&](int64_t r, float2 st, int from, int turn) {  // dx of row r, whose sums were exchanged in this turn
@@ -1166,6 +1179,9 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_cluster_kernel(const NormPara
       if (c < end) store<T, VB>(dx + c, g);
     }
   };
+  auto take = [&](int turn) {  // the sums of that turn, or a time-out that ends the kernel
+    if (!wait_bounded(arrived + turn % 3, static_cast<uint32_t>(turn / 3) & 1u, &given_up, q.ctl, 61)) given_up = 1;
+  };
   for (; row < p.N; row += step, ++i) {
     copy_wait<S - 2>();
     const float2 next = row + step < p.N ? p.stats[row + step] : make_float2(0.f, 0.f);
@@ -1187,15 +1203,18 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_cluster_kernel(const NormPara
       }
       float* red = shared + (i & 1) * 32;
       if (lane == 0) red[warp * 2] = a, red[warp * 2 + 1] = b;
+      if (t == 0 && i > 0) take(i - 1);
       __syncthreads();
-      if (i > 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-      if (t < 2) {
-        float sum = 0.f;
-        for (int j = 0; j < warps; ++j) sum += red[j * 2 + t];
-        for (uint32_t c = 0; c < ctas; ++c)
-          st_cluster_u32(mapa_shared(smem_u32(across + (i % 3) * 16 + rank * 2 + t), c), __float_as_uint(sum));
+      if (given_up) break;
+      if (warp == 0) {  // lane: sum lane / 16 of warp lane % 16
+        float sum = (lane & 15) < warps ? red[(lane & 15) * 2 + (lane >> 4)] : 0.f;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float other = __shfl_xor_sync(0xffffffffu, sum, 16);
+        if (lane == 0) mbar_arrive_expect_tx(arrived + i % 3, ctas * 8);
+        if (lane < static_cast<int>(ctas))  // every lane tells one CTA
+          send_pair(mapa_shared(smem_u32(across + (i % 3) * 16 + rank * 2), lane), sum, other, mapa_shared(smem_u32(arrived + i % 3), lane));
       }
-      asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
       if (i > 0) finish(row - step, before, last, i - 1);
     }
     before = now;
@@ -1206,8 +1225,9 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_cluster_kernel(const NormPara
     fetch((i + S - 1) % S, row + (S - 1) * step);
   }
   if (q.dx != nullptr && i > 0) {
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    finish(row - step, before, last, i - 1);
+    if (t == 0 && !given_up) take(i - 1);
+    __syncthreads();
+    if (!given_up) finish(row - step, before, last, i - 1);
   }
   grid_dep_launch();
   copy_wait<0>();
@@ -1226,6 +1246,7 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_cluster_kernel(const NormPara
       }
     }
   }
+  cluster_sync_all();  // no CTA leaves while another one may still send to it
 }
 
 // dx of rows too wide for the registers.
@@ -1445,16 +1466,19 @@ cudaError_t bwd_ring(NormParams p, const NormGrad& q, int* parts, cudaStream_t s
 template <typename T, bool RMS, bool DSUM>
 cudaError_t bwd_cluster(NormParams p, NormGrad q, int* parts, cudaStream_t stream) {
   constexpr int KC = 2, S = 4, cols = KC * 16 / sizeof(T);
-  const int ctas = static_cast<int>(cdiv64(p.d, 512 * cols));
+  const int threads = 512;
+  const int ctas = static_cast<int>(cdiv64(p.d, threads * cols));
   const int cta = static_cast<int>(cdiv64(cdiv64(p.d, ctas), 32 * cols) * 32);
   q.cta_cols = cta * cols;
   const cudaError_t e = allow_smem<norm_bwd_cluster_kernel<T, KC, S, RMS, DSUM>>();
   if (e != cudaSuccess) return e;
-  *parts = static_cast<int>(blocks_for(p.N, *parts < kGridSms / ctas ? *parts : kGridSms / ctas));
+  const int smem = 512 + S * (DSUM ? 3 : 2) * KC * 16 * cta, by_smem = kSmemPerSm / (smem + 1280), by_threads = (RMS ? 672 : 576) / cta;
+  const int64_t most = static_cast<int64_t>(kGridSms / ctas) * (by_smem < by_threads ? by_smem : by_threads);
+  *parts = static_cast<int>(blocks_for(p.N, *parts < most ? *parts : most));
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(ctas, *parts);
   cfg.blockDim = dim3(cta);
-  cfg.dynamicSmemBytes = 512 + S * (DSUM ? 3 : 2) * KC * 16 * cta;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -1521,8 +1545,8 @@ cudaError_t bwd_type(const NormParams& p, const NormGrad& q, int parts, int sms,
 
 int norm_parts(int64_t N, int d) {
   int64_t most;
-  if (d > kCtaCols) {  // one cluster an SM for each of its CTAs, or stretches of rows that fill the SMs with 256 columns each
-    const int64_t clusters = d > kNormFusedCols ? 0 : kGridSms / cdiv64(d, 2 * kCtaCols), stretches = cdiv64(8 * kGridSms, cdiv64(d, 256));
+  if (d > kCtaCols) {  // clusters (of fp32 rows of one or two CTAs, two an SM), or stretches of rows that fill the SMs with 256 columns each
+    const int64_t clusters = d > kNormFusedCols ? 0 : 2 * kGridSms / cdiv64(d, 2 * kCtaCols), stretches = cdiv64(8 * kGridSms, cdiv64(d, 256));
     most = clusters > stretches ? clusters : stretches;
   } else {
     most = kGridSms * (512 / (d > 256 ? round_threads(cdiv64(d, kBwdCols)) : 128));  // 512 threads an SM
