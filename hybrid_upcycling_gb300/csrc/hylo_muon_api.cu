@@ -190,15 +190,22 @@ hylo_status run(const T* list, int count, int dtype, int out_dtype, bool masters
       t.lo = static_cast<uint32_t>(row + 2 * d.x_rows);
       t.a = static_cast<uint32_t>(row + 3 * d.x_rows);
       t.b = static_cast<uint32_t>(row + 3 * d.x_rows + d.a_rows);
-      t.sum0 = sums, t.parts = static_cast<uint32_t>(d.parts), t.fill0 = fill;
+      t.sum0 = sums, t.parts = static_cast<uint32_t>(d.parts);
       t.sym0 = p.sym, t.rect0 = p.rect;
       row += rows_of(d);
       sums += t.parts;
-      fill += muon_fill_blocks(t);
       p.sym += t.mt * (t.mt + 1) / 2;
       p.rect += t.mt * t.nt;
     }
     if (tab.count == 0) continue;
+    // One 64 x 64 block a thread block where there are few (each waits for the norm first), up to eight where there are many.
+    int64_t blocks = 0;
+    for (int k = 0; k < tab.count; ++k) blocks += static_cast<int64_t>(tab.t[k].kn) * tab.t[k].km;
+    h.fill_blocks = static_cast<int>(blocks / (8 * dev->sms) < 1 ? 1 : blocks / (8 * dev->sms) > 8 ? 8 : blocks / (8 * dev->sms));
+    for (int k = 0; k < tab.count; ++k) {
+      tab.t[k].fill0 = fill;
+      fill += muon_fill_ctas(tab.t[k], h.fill_blocks);
+    }
     CUtensorMap load;
     if ((st = make_map(&load, ws, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 64, row, 128, 64, 64)) != HYLO_OK) return st;
     h.sums = reinterpret_cast<float*>(h.ws + group.sums_at());
@@ -206,6 +213,7 @@ hylo_status run(const T* list, int count, int dtype, int out_dtype, bool masters
     p.scratch = h.ws + group.scratch_at();
     p.ctl = WaitCtl{dev->status, wait_limit_ns()};
     p.steps = s.count;
+    p.sym_half = 2 * p.sym <= dev->muon_clusters, p.rect_half = 2 * p.rect <= dev->muon_clusters;
     for (int k = 0; k < s.count; ++k) {
       const double *c = s.k + 3 * k, x = s.x[k], a = s.a[k], b = s.b[k], next = s.x[k + 1];
       p.acc[k][kMuonGram] = static_cast<float>(a / (x * x));

@@ -146,13 +146,14 @@ __global__ void __launch_bounds__(kThreads) muon_sums_kernel(const __grid_consta
   }
 }
 
-// Two factors whose product is scale / (norm + eps): one alone could leave fp32's range. NaN if the norm is not finite.
-__device__ __forceinline__ float2 scale_factors(const MuonMat& t, const MuonHyper& h, double* red) {
-  double s[kMuonSums] = {0.0, 0.0, 0.0};
+// Two factors whose product is scale / (norm + eps): one alone could leave fp32's range. NaN if the norm is not finite. One thread
+// works in 64 bits, which are slow here.
+__device__ __forceinline__ float2 scale_factors(const MuonMat& t, const MuonHyper& h, float* red) {
+  float s[kMuonSums] = {0.f, 0.f, 0.f};
   for (uint32_t i = threadIdx.x; i < t.parts; i += kThreads) {
     const float* a = h.sums + static_cast<int64_t>(t.sum0 + i) * kMuonSums;
 #pragma unroll
-    for (int k = 0; k < kMuonSums; ++k) s[k] += static_cast<double>(a[k]);
+    for (int k = 0; k < kMuonSums; ++k) s[k] += a[k];
   }
 #pragma unroll
   for (int k = 0; k < kMuonSums; ++k) {
@@ -161,17 +162,23 @@ __device__ __forceinline__ float2 scale_factors(const MuonMat& t, const MuonHype
     if ((threadIdx.x & 31) == 0) red[k * (kThreads / 32) + (threadIdx.x >> 5)] = s[k];
   }
   __syncthreads();
+  if (threadIdx.x == 0) {
 #pragma unroll
-  for (int k = 0; k < kMuonSums; ++k) {
-    s[k] = 0.0;
-    for (int i = 0; i < kThreads / 32; ++i) s[k] += red[k * (kThreads / 32) + i];
+    for (int k = 0; k < kMuonSums; ++k) {
+      s[k] = 0.f;
+      for (int i = 0; i < kThreads / 32; ++i) s[k] += red[k * (kThreads / 32) + i];
+    }
+    // all sums of magnitudes below 2^-20: x 2^80 stays below 2^60 and loses nothing; inf: x 2^-80 does not overflow
+    const double root = sqrt(static_cast<double>(s[1] < 0x1p-40f ? s[0] : isfinite(s[1]) ? s[1] : s[2]));
+    const double norm = s[1] < 0x1p-40f ? root * 0x1p-80 : isfinite(s[1]) ? root : root * 0x1p80;
+    const double f = norm > 0.0 || h.eps > 0.f ? static_cast<double>(h.scale_in) / (norm + h.eps) : 0.0;
+    const double first = f > 0x1p100 ? 0x1p100 : f < 0x1p-100 ? 0x1p-100 : 1.0;
+    const bool fine = isfinite(norm);
+    red[0] = fine ? static_cast<float>(f / first) : __int_as_float(0x7fffffff);
+    red[1] = fine ? static_cast<float>(first) : 1.f;
   }
-  // all sums of magnitudes below 2^-20: x 2^80 stays below 2^60 and loses nothing; inf: x 2^-80 does not overflow
-  const double norm = s[1] < 0x1p-40 ? sqrt(s[0]) * 0x1p-80 : isfinite(s[1]) ? sqrt(s[1]) : sqrt(s[2]) * 0x1p80;
-  const double f = norm > 0.0 || h.eps > 0.f ? static_cast<double>(h.scale_in) / (norm + h.eps) : 0.0;
-  if (!isfinite(norm)) return make_float2(__int_as_float(0x7fffffff), 1.f);
-  const double first = f > 0x1p100 ? 0x1p100 : f < 0x1p-100 ? 0x1p-100 : 1.0;
-  return make_float2(static_cast<float>(f / first), static_cast<float>(first));
+  __syncthreads();
+  return make_float2(red[0], red[1]);
 }
 
 // Eight columns from c on of X's row r.
@@ -193,12 +200,11 @@ __device__ __forceinline__ void put_x(const MuonHyper& h, const MuonMat& t, int 
   *reinterpret_cast<uint4*>(h.ws + static_cast<size_t>(t.lo) * 128 + sector * 32 + (c & 8) * 2) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
 }
 
-// X's panels from the scaled update, padded with zeros to whole k-blocks: 64 x 64 blocks of the matrix, kFillBlocks a thread block along its
+// X's panels from the scaled update, padded with zeros to whole k-blocks: 64 x 64 blocks of the matrix, h.fill_blocks a thread block along its
 // rows; a tall matrix is transposed through shared memory.
-constexpr int kFillBlocks = 8;
 template <typename T>
 __global__ void __launch_bounds__(kThreads) muon_fill_kernel(const __grid_constant__ MuonTable tab, const MuonHyper h) {
-  __shared__ double red[kMuonSums * (kThreads / 32)];
+  __shared__ float red[kMuonSums * (kThreads / 32)];
   __shared__ float tile[64][65];
   const MuonMat& t = tab.t[find_mat<&MuonMat::fill0>(tab, blockIdx.x)];
   float gs = 1.f;
@@ -206,9 +212,9 @@ __global__ void __launch_bounds__(kThreads) muon_fill_kernel(const __grid_consta
   float2 f = make_float2(0.f, 0.f);
   if (!skipped) f = scale_factors(t, h, red);
   const int wide = t.tall ? t.km : t.kn, local = static_cast<int>(blockIdx.x - t.fill0);
-  const int per = (wide + kFillBlocks - 1) / kFillBlocks;
-  const int br = local / per, bc0 = (local - br * per) * kFillBlocks;
-  for (int bc = bc0; bc < min(wide, bc0 + kFillBlocks); ++bc) {
+  const int per = (wide + h.fill_blocks - 1) / h.fill_blocks;
+  const int br = local / per, bc0 = (local - br * per) * h.fill_blocks;
+  for (int bc = bc0; bc < min(wide, bc0 + h.fill_blocks); ++bc) {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int rr = half * 32 + static_cast<int>(threadIdx.x >> 3), cc = static_cast<int>(threadIdx.x & 7) * 8;
@@ -246,9 +252,9 @@ __global__ void __launch_bounds__(kThreads) muon_fill_kernel(const __grid_consta
 
 }  // namespace
 
-uint32_t muon_fill_blocks(const MuonMat& t) {
+uint32_t muon_fill_ctas(const MuonMat& t, int blocks) {
   const int down = t.tall ? t.kn : t.km, across = t.tall ? t.km : t.kn;  // 64 x 64 blocks
-  return static_cast<uint32_t>(down) * static_cast<uint32_t>((across + kFillBlocks - 1) / kFillBlocks);
+  return static_cast<uint32_t>(down) * static_cast<uint32_t>((across + blocks - 1) / blocks);
 }
 
 cudaError_t launch_muon_sums(const MuonTable& t, const MuonHyper& h, int dtype, uint32_t ctas, cudaStream_t stream) {

@@ -60,6 +60,7 @@ enum : int { kMuonOutBf16 = 0, kMuonOutF16, kMuonParamF32, kMuonParamBf16, kMuon
 struct MuonPipe {
   int steps;
   int sym, rect;            // 256 x 256 tiles of the group
+  int sym_half, rect_half;  // 1: work items of 256 x 128, so that there are twice as many
   float acc[kMuonStepsMax][3], add[kMuonStepsMax][3];  // factors on the sum of products, and on A (Poly) or X (Apply)
   unsigned* ctrl;           // [0] work queue, [1 + matrix] work done; zero at launch
   uint8_t* scratch;         // kMuonScratch bytes for each CTA, where some sum is longer than kMuonDepth
@@ -78,12 +79,13 @@ struct MuonHyper {
   float scale_in;  // X's scale of the first step, a power of two
   float unscale;   // 1 / that of the last X
   uint32_t seed;
+  int fill_blocks;
   uint8_t* ws;
   float* sums;     // [parts][kMuonSums] of the group
   unsigned* ctrl;  // MuonPipe's, cleared on the way
 };
-// Thread blocks of the kernel that fills X, for one matrix.
-uint32_t muon_fill_blocks(const MuonMat& t);
+// Thread blocks of the kernel that fills X, for one matrix, if each fills up to `blocks` blocks of 64 x 64.
+uint32_t muon_fill_ctas(const MuonMat& t, int blocks);
 cudaError_t launch_muon_sums(const MuonTable& t, const MuonHyper& h, int dtype, uint32_t ctas, cudaStream_t stream);
 cudaError_t launch_muon_fill(const MuonTable& t, const MuonHyper& h, int dtype, uint32_t ctas, cudaStream_t stream);
 // All products of all steps; the last one writes the results or steps the parameters (`out`). load: boxes of 64 columns and 64

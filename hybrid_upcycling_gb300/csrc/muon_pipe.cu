@@ -15,11 +15,12 @@
 // 100 000 elements came out 3e-3 too small), so at most kMuonDepth k-blocks are summed there; longer sums go through fp32 numbers in
 // the CTA's part of the workspace, rounded to nearest.
 //
-// Work items are 256 x 256 tiles (narrower ones read more operands per product, whose latency the six stages then no longer cover:
-// 256 x 128 took as long), taken from a queue in the order step, product, matrix, tile. One
+// Work items are 256 x 256 tiles, taken from a queue in the order step, product, matrix, tile. One
 // may start once every earlier item of its matrix is done, which a counter per matrix tells: what it reads is then complete, and
 // what it overwrites is no longer read. With several matrices the tail of one's product is filled with the next one's items;
-// every item waits for earlier ones only, which running CTAs hold, so the launch cannot deadlock whatever the residency.
+// every item waits for earlier ones only, which running CTAs hold, so the launch cannot deadlock whatever the residency. Where a product
+// leaves half of the clusters idle, items are 256 x 128: their products take as long (more operands are read for each, whose latency
+// the six stages then do not cover), what follows half as long.
 //
 // A CTA pair takes an item: warp 2 of the even CTA fetches it, waits for its matrix and publishes it to both CTAs; warp 0 of each CTA
 // loads by TMA; one thread of warp 1 of the even CTA issues the products; eight warps of each CTA take the sums out of TMEM, whose two
@@ -61,13 +62,14 @@ struct Item {
   int product;  // kMuonGram, kMuonPoly, kMuonApply, or -1: no more
   int step, mat;
   int i, j;     // 256-row tile, 256-column tile
+  int half;     // -1, or 0 or 1: the tile's first or second 128 columns only
   unsigned need;  // the matrix's counter once all earlier items are done
-  int pad[2];
+  int pad;
 };
 static_assert(sizeof(Item) == 32, "item size");
 
 __device__ __forceinline__ Item item_at(const MuonTable& tab, const MuonPipe& p, unsigned index) {
-  const unsigned sym = static_cast<unsigned>(p.sym), per_step = 2 * sym + static_cast<unsigned>(p.rect);
+  const unsigned sym = static_cast<unsigned>(p.sym) << p.sym_half, per_step = 2 * sym + (static_cast<unsigned>(p.rect) << p.rect_half);
   Item it{};
   it.step = static_cast<int>(index / per_step);
   if (it.step >= p.steps) {
@@ -78,7 +80,8 @@ __device__ __forceinline__ Item item_at(const MuonTable& tab, const MuonPipe& p,
   it.product = r < sym ? kMuonGram : r < 2 * sym ? kMuonPoly : kMuonApply;
   r -= static_cast<unsigned>(it.product) * sym;
   const bool apply = it.product == kMuonApply;
-  const int t = static_cast<int>(r);
+  const int halves = apply ? p.rect_half : p.sym_half, t = static_cast<int>(r >> halves);
+  it.half = halves ? static_cast<int>(r & 1u) : -1;
   int lo = 0, hi = tab.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -101,7 +104,7 @@ __device__ __forceinline__ Item item_at(const MuonTable& tab, const MuonPipe& p,
     it.j = j;
     it.i = local - j * (j + 1) / 2;
   }
-  const unsigned own_sym = static_cast<unsigned>(m.mt * (m.mt + 1) / 2), own_rect = static_cast<unsigned>(m.mt * m.nt);
+  const unsigned own_sym = static_cast<unsigned>(m.mt * (m.mt + 1) / 2) << p.sym_half, own_rect = static_cast<unsigned>(m.mt * m.nt) << p.rect_half;
   it.need = kDone * (static_cast<unsigned>(it.step) * (2 * own_sym + own_rect) + static_cast<unsigned>(it.product) * own_sym);
   return it;
 }
@@ -140,13 +143,13 @@ __device__ __forceinline__ bool wait_count(const unsigned* ctr, unsigned target,
   }
 }
 
-// 128 rows from `row` on and 64 columns from 64 kb on of a matrix whose panels have mp rows. mirror: the block is stored as
+// 128 rows (64 unless `both`) from `row` on and 64 columns from 64 kb on of a matrix whose panels have mp rows. mirror: the block is stored as
 // its mirror image, 64 rows from 64 kb on and the columns `row`, ..., and arrives in MN-major order.
 __device__ __forceinline__ void load_rows(uint8_t* dst, const CUtensorMap* map, uint32_t bar, uint32_t base, int mp, int row, int kb,
-                                          bool mirror) {
+                                          bool mirror, bool both) {
   const int at = static_cast<int>(base) + (mirror ? row / 64 * mp + kb * 64 : kb * mp + row), next = mirror ? mp : 64;
   tma_load_2d_pair(dst, map, bar, 0, at);
-  tma_load_2d_pair(dst + 8192, map, bar, 0, at + next);
+  if (both) tma_load_2d_pair(dst + 8192, map, bar, 0, at + next);
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -393,7 +396,8 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
         const int mp = m.mt * 256, nk = kblocks(m, it), cur = it.step & 1;
         const uint32_t abase = it.product == kMuonGram ? m.x[cur] : it.product == kMuonPoly ? m.a : m.b;
         const uint32_t bbase = it.product == kMuonPoly ? m.a : m.x[cur];
-        const int arow = it.i * 256 + static_cast<int>(rank) * kBM, brow = it.j * 256 + static_cast<int>(rank) * kBM;
+        const int arow = it.i * 256 + static_cast<int>(rank) * kBM, brow = it.j * 256 + (it.half < 0 ? static_cast<int>(rank) * kBM : it.half * 128 + static_cast<int>(rank) * 64);
+        const uint32_t bytes = it.half < 0 ? 2u * STAGE_BYTES : 2u * (A_BYTES + A_BYTES / 2);  // both CTAs'
         for (int kb = 0; kb < nk; ++kb) {
           if (!wait_bounded(empty + stage, phase ^ 1u, abort_flag, p.ctl, 44)) {
             ok = false;
@@ -402,12 +406,13 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
           uint8_t* sa = smem + stage * STAGE_BYTES;
           const uint32_t fb = full_lead + static_cast<uint32_t>(stage) * 8u;
           if (rank == 0) {
-            mbar_arrive_expect_tx(full + stage, 2 * STAGE_BYTES);  // both CTAs' bytes
+            mbar_arrive_expect_tx(full + stage, bytes);
             armed |= 1u << stage;
           }
-          load_rows(sa, &map, fb, abase, mp, arow, kb, it.product != kMuonGram && mirrored(kb, it.i));
+          load_rows(sa, &map, fb, abase, mp, arow, kb, it.product != kMuonGram && mirrored(kb, it.i), true);
           // B of Apply is X, 64 of its rows and this CTA's columns, which lie like a mirror image's
-          load_rows(sa + A_BYTES, &map, fb, bbase, mp, brow, kb, it.product == kMuonApply || (it.product == kMuonPoly && mirrored(kb, it.j)));
+          load_rows(sa + A_BYTES, &map, fb, bbase, mp, brow, kb, it.product == kMuonApply || (it.product == kMuonPoly && mirrored(kb, it.j)),
+                    it.half < 0);
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -436,6 +441,7 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
         mbar_arrive(iempty + slot);
         if (it.product < 0) break;
         const int nk = kblocks(tab.t[it.mat], it);
+        const uint32_t idesc0 = idesc_f16_f32(2 * kBM, it.half < 0 ? 256 : 128);
         for (int from = 0; ok && from < nk; from += kMuonDepth) {
           if (!wait_bounded(tempty + h, (uses[h] & 1u) ^ 1u, abort_flag, p.ctl, 46)) {
             ok = false;
@@ -452,7 +458,7 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
             const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES), sb = sa + A_BYTES;
             const bool amn = it.product != kMuonGram && mirrored(kb, it.i);
             const bool bmn = it.product == kMuonApply || (it.product == kMuonPoly && mirrored(kb, it.j));
-            const uint32_t idesc = idesc_f16_f32(2 * kBM, 256) | (amn ? kAMajor : 0u) | (bmn ? kBMajor : 0u);
+            const uint32_t idesc = idesc0 | (amn ? kAMajor : 0u) | (bmn ? kBMajor : 0u);
 #pragma unroll
             for (int q = 0; q < kBK / 16; ++q)
               umma_bf16_pair(d, slice_desc(amn, sa, q), slice_desc(bmn, sb, q), idesc, (kb > from || q > 0) ? 1u : 0u);
@@ -503,12 +509,15 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
       const bool apply = it.product == kMuonApply, last = apply && it.step + 1 == p.steps;
       const uint32_t out = it.product == kMuonGram ? m.a : it.product == kMuonPoly ? m.b : m.x[cur ^ 1];
       const uint32_t add = it.product == kMuonPoly ? m.a : m.x[cur];
-      const int row = it.i * 256 + static_cast<int>(rank) * kBM + q * 32, col0 = (2 * it.j + hc) * 128;
+      const int row = it.i * 256 + static_cast<int>(rank) * kBM + q * 32;
+      // This warp's columns of the accumulator and of the matrix: 128, or 64 of half a tile.
+      const int units = it.half < 0 ? kUnits : kUnits / 2, acc0 = hc * 32 * units;
+      const int col0 = it.j * 256 + (it.half < 0 ? 0 : it.half * 128) + acc0;
       // Rows and columns behind the last 64-deep k-block are never read as such: their parts are left out.
       const int wide = (apply ? m.kn : m.km) * 64 - col0;
-      const int nu = row >= m.km * 64 || wide <= 0 ? 0 : wide >= 32 * kUnits ? kUnits : wide / 32;
+      const int nu = row >= m.km * 64 || wide <= 0 ? 0 : wide >= 32 * units ? units : wide / 32;
       // X's second term, which only the epilogue of the same tile reads again, lies in the order of its lanes.
-      uint8_t* lo = hyper.ws + static_cast<size_t>(m.lo) * 128 + muon_lo_sector(it.j * m.mt + it.i, static_cast<int>(rank), e) * 32 + lane * 32;
+      uint8_t* lo = hyper.ws + static_cast<size_t>(m.lo) * 128 + (muon_lo_sector(it.j * m.mt + it.i, static_cast<int>(rank), q + (col0 >> 7 & 1) * 4) + (col0 >> 5 & 3) * 64 + lane) * 32;
       auto part = [&](uint32_t base, int u) {  // this lane's row of part u
         return hyper.ws + (static_cast<size_t>(base) + static_cast<size_t>(col0 / 64 + u / 2) * mp + row + lane) * 128 + (u & 1) * 64;
       };
@@ -536,9 +545,9 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
         got = __all_sync(0xffffffffu, wait_bounded(tfull + h, uses[h] & 1u, abort_flag, p.ctl, 49));
         if (!got) break;
         tc_fence_after();
-        for (int c = 0; c < kUnits; ++c) {
+        for (int c = 0; c < units; ++c) {
           float v[32];
-          tmem_ld32(lanes + static_cast<uint32_t>(h * 256 + hc * 128 + c * 32), v);
+          tmem_ld32(lanes + static_cast<uint32_t>(h * 256 + acc0 + c * 32), v);
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -568,7 +577,7 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
         for (int j = 0; j < 16; ++j) w[j] = hi1[j], l[j] = lo1[j];
         read_ahead(u + 1);
         float v[32];
-        tmem_ld32(lanes + static_cast<uint32_t>(h * 256 + hc * 128 + u * 32), v);
+        tmem_ld32(lanes + static_cast<uint32_t>(h * 256 + acc0 + u * 32), v);
         tmem_ld_wait();
         if (deep) {
 #pragma unroll
@@ -672,7 +681,7 @@ cudaError_t muon_pipe_prepare(int* max_clusters) {
 
 cudaError_t launch_muon_pipe(const CUtensorMap& load, const MuonTable& t, const MuonPipe& p, const MuonHyper& h, int out,
                              int clusters, cudaStream_t stream) {
-  const int most = p.sym > p.rect ? p.sym : p.rect;  // items that can run at once
+  const int sym = p.sym << p.sym_half, rect = p.rect << p.rect_half, most = sym > rect ? sym : rect;  // items that can run at once
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = pipe_config(attr, most < clusters ? most : clusters, stream);
   switch (out) {
