@@ -13,8 +13,9 @@ namespace {
 
 constexpr int64_t kMaxSide = int64_t(1) << 20, kMaxShort = 16384;
 constexpr int kMaxSteps = kMuonStepsMax;
-// Matrices that go through the products together: enough tiles for every SM, and no more memory than that takes.
-constexpr int64_t kGroupRows = (int64_t(512) << 20) / 128;
+// Matrices that go through the products together: enough tiles for every SM (two layers' matrices 3.65 ms in groups of half as
+// much, 3.55 so), and no more memory than that takes.
+constexpr int64_t kGroupRows = (int64_t(1024) << 20) / 128;
 
 uintptr_t bytes_of(int dtype) { return dtype == HYLO_F32 ? 4 : 2; }
 
@@ -54,19 +55,37 @@ Shape shape_of(int64_t rows, int64_t cols) {
 // 128-byte rows: X twice, its second term, A and B.
 int64_t rows_of(const Shape& s) { return 3 * s.x_rows + 2 * s.a_rows; }
 
+// The sum of an item of Gram (K = n) is split where the group has so few that clusters would be idle beside a long one. A 64-deep
+// k-block takes 550 cycles and a part 3500 to be written, read and added, so sqrt(n / 64 / 6.4) parts. bf16, without and with:
+// 256 x 16384 512 and 292 us, 2048 x 8192 619 and 588, 1 x 100000 2.38 ms and 0.48; sums half as long are even (1024 x 4096 292
+// and 299).
+constexpr int64_t kSplitClusters = 76, kSplitFrom = 128, kMaxSplits = 64;
+int64_t splits_of(const Shape& s, int64_t group_tiles) {
+  const int64_t kn = cdiv(s.n, 64), room = kSplitClusters / group_tiles;
+  if (kn < kSplitFrom || room < 2) return 1;
+  const int64_t n = static_cast<int64_t>(std::sqrt(static_cast<double>(kn) / 6.4));
+  return n < room ? n : room < kMaxSplits ? room : kMaxSplits;
+}
+int64_t sym_tiles(const Shape& s) { return (s.mp / 256) * (s.mp / 256 + 1) / 2; }
+
 // Items [first, last) that go through the products together; empty ones among them take no place.
 struct Group {
   int first, last, mats;
   int64_t rows, parts;
-  bool deep;  // some sum is longer than the tensor cores take at a time
+  bool deep;      // some sum is longer than the tensor cores take at a time
+  int64_t tiles;  // of Gram
+  int64_t split_tiles, split_items;
   size_t sums_at() const { return static_cast<size_t>(rows) * 128; }
   size_t ctrl_at() const { return sums_at() + round256(static_cast<size_t>(parts) * kMuonSums * sizeof(float)); }
-  size_t scratch_at() const { return ctrl_at() + round256(kMuonCtrlWords * sizeof(unsigned)); }
-  size_t bytes() const { return scratch_at() + (deep ? 2 * kMaxClusters * kMuonScratch : 0); }
+  int ctrl_words() const { return kMuonCtrlWords + static_cast<int>(split_tiles) * 16; }
+  size_t scratch_at() const { return ctrl_at() + round256(ctrl_words() * sizeof(unsigned)); }
+  size_t splits_at() const { return scratch_at() + (deep ? 2 * kMaxClusters * kMuonScratch : 0); }
+  size_t bytes() const { return splits_at() + static_cast<size_t>(split_items) * 2 * kMuonScratch; }
 };
 template <typename T>
 Group next_group(const T* list, int count, int first) {
-  Group g{first, first, 0, 0, 0, false};
+  Group g{};
+  g.first = g.last = first;
   for (; g.last < count; ++g.last) {
     const Item x = item_of(list[g.last]);
     if (x.rows == 0 || x.cols == 0) continue;
@@ -75,7 +94,15 @@ Group next_group(const T* list, int count, int first) {
     ++g.mats;
     g.rows += rows_of(s);
     g.parts += s.parts;
-    g.deep |= s.n > kMuonDepth * 64;
+    g.tiles += sym_tiles(s);
+  }
+  for (int i = first; i < g.last; ++i) {
+    const Item x = item_of(list[i]);
+    if (x.rows == 0 || x.cols == 0) continue;
+    const Shape s = shape_of(x.rows, x.cols);
+    const int64_t splits = splits_of(s, g.tiles);
+    if (splits > 1) g.split_tiles += sym_tiles(s), g.split_items += sym_tiles(s) * splits;
+    g.deep |= cdiv(cdiv(s.n, 64), splits) > kMuonDepth || s.m > kMuonDepth * 64;
   }
   return g;
 }
@@ -169,6 +196,7 @@ hylo_status run(const T* list, int count, int dtype, int out_dtype, bool masters
     MuonPipe p{};
     int64_t row = 0;
     uint32_t sums = 0, fill = 0;
+    int split = 0, parts = 0;
     for (; i < group.last; ++i) {
       const Item x = item_of(list[i]);
       const uint64_t start = pos;
@@ -191,11 +219,13 @@ hylo_status run(const T* list, int count, int dtype, int out_dtype, bool masters
       t.a = static_cast<uint32_t>(row + 3 * d.x_rows);
       t.b = static_cast<uint32_t>(row + 3 * d.x_rows + d.a_rows);
       t.sum0 = sums, t.parts = static_cast<uint32_t>(d.parts);
-      t.sym0 = p.sym, t.rect0 = p.rect;
+      t.splits = static_cast<int>(splits_of(d, group.tiles)), t.split0 = split, t.part0 = parts;
+      for (int k = 0; k < 3; ++k) t.item0[k] = p.items[k];
+      const int sym = t.mt * (t.mt + 1) / 2;
+      if (t.splits > 1) split += sym, parts += sym * t.splits;
+      p.items[kMuonGram] += sym * t.splits, p.items[kMuonPoly] += sym, p.items[kMuonApply] += t.mt * t.nt;
       row += rows_of(d);
       sums += t.parts;
-      p.sym += t.mt * (t.mt + 1) / 2;
-      p.rect += t.mt * t.nt;
     }
     if (tab.count == 0) continue;
     // One 64 x 64 block a thread block where there are few (each waits for the norm first), up to eight where there are many.
@@ -210,10 +240,12 @@ hylo_status run(const T* list, int count, int dtype, int out_dtype, bool masters
     if ((st = make_map(&load, ws, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 64, row, 128, 64, 64)) != HYLO_OK) return st;
     h.sums = reinterpret_cast<float*>(h.ws + group.sums_at());
     h.ctrl = p.ctrl = reinterpret_cast<unsigned*>(h.ws + group.ctrl_at());
+    h.ctrl_words = group.ctrl_words();
     p.scratch = h.ws + group.scratch_at();
+    p.parts = h.ws + group.splits_at();
     p.ctl = WaitCtl{dev->status, wait_limit_ns()};
     p.steps = s.count;
-    p.sym_half = 2 * p.sym <= dev->muon_clusters, p.rect_half = 2 * p.rect <= dev->muon_clusters;
+    for (int k = 0; k < 3; ++k) p.half[k] = 2 * p.items[k] <= dev->muon_clusters && (k != kMuonGram || split == 0);
     for (int k = 0; k < s.count; ++k) {
       const double *c = s.k + 3 * k, x = s.x[k], a = s.a[k], b = s.b[k], next = s.x[k + 1];
       p.acc[k][kMuonGram] = static_cast<float>(a / (x * x));
@@ -224,7 +256,7 @@ hylo_status run(const T* list, int count, int dtype, int out_dtype, bool masters
                             : out_dtype == HYLO_F32 ? kMuonParamF32 : masters ? kMuonParamMaster : kMuonParamBf16;
     cudaError_t e = launch_muon_sums(tab, h, dtype, sums, stream);
     if (e == cudaSuccess) e = launch_muon_fill(tab, h, dtype, fill, stream);
-    if (e == cudaSuccess) e = launch_muon_pipe(load, tab, p, h, out, dev->muon_clusters, stream);
+    if (e == cudaSuccess) e = launch_muon_pipe(load, tab, p, h, out, split > 0, dev->muon_clusters, stream);
     if (e != cudaSuccess) return cuda_fail(e, "launch orthogonalised updates");
   }
   return HYLO_OK;

@@ -105,7 +105,9 @@ constexpr float kUp = 0x1p80f, kDown = 0x1p-80f;
 template <typename T>
 __global__ void __launch_bounds__(kThreads) muon_sums_kernel(const __grid_constant__ MuonTable tab, const MuonHyper h) {
   __shared__ float red[kThreads / 32];
-  if (blockIdx.x == 0 && threadIdx.x < kMuonCtrlWords) h.ctrl[threadIdx.x] = 0u;
+  if (blockIdx.x == 0) {
+    for (int i = threadIdx.x; i < h.ctrl_words; i += kThreads) h.ctrl[i] = 0u;
+  }
   float gs = 1.f;
   if (h.muon && !gradient_factor(h, gs)) return;
   const MuonMat& t = tab.t[find_mat<&MuonMat::sum0>(tab, blockIdx.x)];

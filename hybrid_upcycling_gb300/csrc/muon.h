@@ -44,7 +44,8 @@ struct MuonMat {
   uint32_t x[2], lo, a, b;  // first 128-byte rows of X before even and odd steps, its second term, A and B
   uint32_t sum0, parts;     // first partial sum, and how many
   uint32_t fill0;           // first thread block of the kernel that fills X
-  int sym0, rect0;          // first 256 x 256 tiles, among the group's, of the symmetric products and of B X
+  int item0[3];             // first work items, among the group's, of each product (before they are halved)
+  int splits, split0, part0;  // parts of the sum of an item of Gram; its first tile, and part, among the group's split ones
 };
 struct MuonTable {
   MuonMat t[kMuonMats];
@@ -59,14 +60,15 @@ enum : int { kMuonGram = 0, kMuonPoly = 1, kMuonApply = 2 };
 enum : int { kMuonOutBf16 = 0, kMuonOutF16, kMuonParamF32, kMuonParamBf16, kMuonParamMaster };  // what the last product writes
 struct MuonPipe {
   int steps;
-  int sym, rect;            // 256 x 256 tiles of the group
-  int sym_half, rect_half;  // 1: work items of 256 x 128, so that there are twice as many
+  int items[3];             // work items of the group for each product: 256 x 256 tiles, of Gram times its splits
+  int half[3];              // 1: work items of 256 x 128, so that there are twice as many
   float acc[kMuonStepsMax][3], add[kMuonStepsMax][3];  // factors on the sum of products, and on A (Poly) or X (Apply)
-  unsigned* ctrl;           // [0] work queue, [1 + matrix] work done; zero at launch
+  unsigned* ctrl;           // [0] work queue, [1 + matrix] work done, then [split tile][16 warps] parts done; zero at launch
+  uint8_t* parts;           // sums of split items [split items][2 CTAs][8 warps][16 KiB], as fp32 in the order of the lanes
   uint8_t* scratch;         // kMuonScratch bytes for each CTA, where some sum is longer than kMuonDepth
   WaitCtl ctl;
 };
-constexpr int kMuonCtrlWords = 1 + kMuonMats;
+constexpr int kMuonCtrlWords = 1 + kMuonMats;  // before the split tiles'
 
 struct MuonHyper {
   int muon;        // momentum and parameters, not just the matrices
@@ -83,6 +85,7 @@ struct MuonHyper {
   uint8_t* ws;
   float* sums;     // [parts][kMuonSums] of the group
   unsigned* ctrl;  // MuonPipe's, cleared on the way
+  int ctrl_words;
 };
 // Thread blocks of the kernel that fills X, for one matrix, if each fills up to `blocks` blocks of 64 x 64.
 uint32_t muon_fill_ctas(const MuonMat& t, int blocks);
@@ -92,6 +95,6 @@ cudaError_t launch_muon_fill(const MuonTable& t, const MuonHyper& h, int dtype, 
 // rows of the workspace.
 cudaError_t muon_pipe_prepare(int* max_clusters);
 cudaError_t launch_muon_pipe(const CUtensorMap& load, const MuonTable& t, const MuonPipe& p, const MuonHyper& h,
-                             int out, int clusters, cudaStream_t stream);
+                             int out, bool split, int clusters, cudaStream_t stream);
 
 }  // namespace hylo

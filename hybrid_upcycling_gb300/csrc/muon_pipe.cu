@@ -22,6 +22,9 @@
 // leaves half of the clusters idle, items are 256 x 128: their products take as long (more operands are read for each, whose latency
 // the six stages then do not cover), what follows half as long.
 //
+// Long sums of few items of Gram are split among items of their own; their fp32 parts meet in the workspace, and each warp of the
+// epilogue that finds all parts of its 32 rows there adds them up in a fixed order.
+//
 // A CTA pair takes an item: warp 2 of the even CTA fetches it, waits for its matrix and publishes it to both CTAs; warp 0 of each CTA
 // loads by TMA; one thread of warp 1 of the even CTA issues the products; eight warps of each CTA take the sums out of TMEM, whose two
 // halves alternate. These add X or A and write the next X, A or B, 32 rows and 32 columns at a time, the next ones on their way, with a
@@ -64,12 +67,18 @@ struct Item {
   int i, j;     // 256-row tile, 256-column tile
   int half;     // -1, or 0 or 1: the tile's first or second 128 columns only
   unsigned need;  // the matrix's counter once all earlier items are done
-  int pad;
+  int part;       // of the sum of a split item
 };
 static_assert(sizeof(Item) == 32, "item size");
 
+template <bool SPLIT>
 __device__ __forceinline__ Item item_at(const MuonTable& tab, const MuonPipe& p, unsigned index) {
-  const unsigned sym = static_cast<unsigned>(p.sym) << p.sym_half, per_step = 2 * sym + (static_cast<unsigned>(p.rect) << p.rect_half);
+  unsigned counts[3], per_step = 0;
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    counts[k] = static_cast<unsigned>(p.items[k]) << p.half[k];
+    per_step += counts[k];
+  }
   Item it{};
   it.step = static_cast<int>(index / per_step);
   if (it.step >= p.steps) {
@@ -77,39 +86,51 @@ __device__ __forceinline__ Item item_at(const MuonTable& tab, const MuonPipe& p,
     return it;
   }
   unsigned r = index - static_cast<unsigned>(it.step) * per_step;
-  it.product = r < sym ? kMuonGram : r < 2 * sym ? kMuonPoly : kMuonApply;
-  r -= static_cast<unsigned>(it.product) * sym;
-  const bool apply = it.product == kMuonApply;
-  const int halves = apply ? p.rect_half : p.sym_half, t = static_cast<int>(r >> halves);
+  it.product = r < counts[0] ? kMuonGram : r < counts[0] + counts[1] ? kMuonPoly : kMuonApply;
+  r -= it.product == kMuonGram ? 0u : it.product == kMuonPoly ? counts[0] : counts[0] + counts[1];
+  const int halves = p.half[it.product], t = static_cast<int>(r >> halves);
   it.half = halves ? static_cast<int>(r & 1u) : -1;
   int lo = 0, hi = tab.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if ((apply ? tab.t[mid].rect0 : tab.t[mid].sym0) <= t)
+    if (tab.t[mid].item0[it.product] <= t)
       lo = mid;
     else
       hi = mid - 1;
   }
   const MuonMat& m = tab.t[lo];
   it.mat = lo;
-  if (apply) {
-    const int local = t - m.rect0;
+  int local = t - m.item0[it.product];
+  if (it.product == kMuonApply) {
     it.j = local / m.mt;
     it.i = local - it.j * m.mt;
-  } else {  // column by column of the upper triangle: local = j (j + 1) / 2 + i
-    const int local = t - m.sym0;
+  } else {  // column by column of the upper triangle: j (j + 1) / 2 + i
+    if (SPLIT && it.product == kMuonGram && m.splits > 1) {
+      it.part = local % m.splits;
+      local /= m.splits;
+    }
     int j = static_cast<int>((sqrtf(8.f * static_cast<float>(local) + 1.f) - 1.f) * 0.5f);
     while (j * (j + 1) / 2 > local) --j;
     while ((j + 1) * (j + 2) / 2 <= local) ++j;
     it.j = j;
     it.i = local - j * (j + 1) / 2;
   }
-  const unsigned own_sym = static_cast<unsigned>(m.mt * (m.mt + 1) / 2) << p.sym_half, own_rect = static_cast<unsigned>(m.mt * m.nt) << p.rect_half;
-  it.need = kDone * (static_cast<unsigned>(it.step) * (2 * own_sym + own_rect) + static_cast<unsigned>(it.product) * own_sym);
+  const unsigned sym = static_cast<unsigned>(m.mt * (m.mt + 1) / 2), gram = (SPLIT ? sym * static_cast<unsigned>(m.splits) : sym) << p.half[0], poly = sym << p.half[1];
+  const unsigned all = gram + poly + (static_cast<unsigned>(m.mt * m.nt) << p.half[2]);
+  it.need = kDone * (static_cast<unsigned>(it.step) * all + (it.product == kMuonGram ? 0u : it.product == kMuonPoly ? gram : gram + poly));
   return it;
 }
 
-__device__ __forceinline__ int kblocks(const MuonMat& m, const Item& it) { return it.product == kMuonGram ? m.kn : m.km; }
+// The k-blocks of an item: [first, end).
+struct Range {
+  int first, end;
+};
+template <bool SPLIT>
+__device__ __forceinline__ Range kblocks(const MuonMat& m, const Item& it) {
+  if (it.product != kMuonGram) return Range{0, m.km};
+  if (!SPLIT || m.splits == 1) return Range{0, m.kn};
+  return Range{static_cast<int>(static_cast<int64_t>(m.kn) * it.part / m.splits), static_cast<int>(static_cast<int64_t>(m.kn) * (it.part + 1) / m.splits)};
+}
 // Whether k-block kb of an operand of Poly or Apply comes from its mirror image: it lies left of 256-row tile `tile`.
 __device__ __forceinline__ bool mirrored(int kb, int tile) { return (kb >> 2) < tile; }
 
@@ -305,7 +326,8 @@ __device__ __forceinline__ void finish_part(const MuonMat& m, uint32_t seed, int
   __syncwarp();
 }
 
-template <int OUT>
+// SPLIT: the group has split sums. Their code costs other groups up to 4 % (two layers' matrices 3.73 ms with it, 3.60 without).
+template <int OUT, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ MuonTable tab, const __grid_constant__ MuonPipe p,
                   const MuonHyper hyper) {
@@ -364,7 +386,7 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
         const int slot = k % kItemDepth;
         const uint32_t par = static_cast<uint32_t>(k / kItemDepth) & 1u;
         if (!wait_bounded<true>(iempty + slot, par ^ 1u, abort_flag, p.ctl, 42)) break;
-        const Item it = item_at(tab, p, atomicAdd(p.ctrl, 1u));
+        const Item it = item_at<SPLIT>(tab, p, atomicAdd(p.ctrl, 1u));
         if (it.product >= 0 && !wait_count(p.ctrl + 1 + it.mat, it.need, abort_flag, p.ctl)) break;
         items[slot] = it;
         const uint32_t* w = reinterpret_cast<const uint32_t*>(&it);
@@ -393,12 +415,13 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
         if (it.product < 0) break;
         fence_proxy_async_global();  // what it reads was stored in other CTAs, or by the kernel before
         const MuonMat& m = tab.t[it.mat];
-        const int mp = m.mt * 256, nk = kblocks(m, it), cur = it.step & 1;
+        const int mp = m.mt * 256, cur = it.step & 1;
+        const Range range = kblocks<SPLIT>(m, it);
         const uint32_t abase = it.product == kMuonGram ? m.x[cur] : it.product == kMuonPoly ? m.a : m.b;
         const uint32_t bbase = it.product == kMuonPoly ? m.a : m.x[cur];
         const int arow = it.i * 256 + static_cast<int>(rank) * kBM, brow = it.j * 256 + (it.half < 0 ? static_cast<int>(rank) * kBM : it.half * 128 + static_cast<int>(rank) * 64);
         const uint32_t bytes = it.half < 0 ? 2u * STAGE_BYTES : 2u * (A_BYTES + A_BYTES / 2);  // both CTAs'
-        for (int kb = 0; kb < nk; ++kb) {
+        for (int kb = range.first; kb < range.end; ++kb) {
           if (!wait_bounded(empty + stage, phase ^ 1u, abort_flag, p.ctl, 44)) {
             ok = false;
             break;
@@ -440,16 +463,16 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
         const Item it = items[slot];
         mbar_arrive(iempty + slot);
         if (it.product < 0) break;
-        const int nk = kblocks(tab.t[it.mat], it);
+        const Range range = kblocks<SPLIT>(tab.t[it.mat], it);
         const uint32_t idesc0 = idesc_f16_f32(2 * kBM, it.half < 0 ? 256 : 128);
-        for (int from = 0; ok && from < nk; from += kMuonDepth) {
+        for (int from = range.first; ok && from < range.end; from += kMuonDepth) {
           if (!wait_bounded(tempty + h, (uses[h] & 1u) ^ 1u, abort_flag, p.ctl, 46)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t d = tmem_base + static_cast<uint32_t>(h * 256);
-          for (int kb = from; kb < min(nk, from + kMuonDepth); ++kb) {
+          for (int kb = from; kb < min(range.end, from + kMuonDepth); ++kb) {
             if (!wait_bounded(full + stage, phase, abort_flag, p.ctl, 47)) {
               ok = false;
               break;
@@ -505,7 +528,8 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
       }
       if (it.product < 0) break;
       const MuonMat& m = tab.t[it.mat];
-      const int mp = m.mt * 256, nk = kblocks(m, it), cur = it.step & 1;
+      const Range range = kblocks<SPLIT>(m, it);
+      const int mp = m.mt * 256, nk = range.end - range.first, cur = it.step & 1;
       const bool apply = it.product == kMuonApply, last = apply && it.step + 1 == p.steps;
       const uint32_t out = it.product == kMuonGram ? m.a : it.product == kMuonPoly ? m.b : m.x[cur ^ 1];
       const uint32_t add = it.product == kMuonPoly ? m.a : m.x[cur];
@@ -515,7 +539,7 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
       const int col0 = it.j * 256 + (it.half < 0 ? 0 : it.half * 128) + acc0;
       // Rows and columns behind the last 64-deep k-block are never read as such: their parts are left out.
       const int wide = (apply ? m.kn : m.km) * 64 - col0;
-      const int nu = row >= m.km * 64 || wide <= 0 ? 0 : wide >= 32 * units ? units : wide / 32;
+      int nu = row >= m.km * 64 || wide <= 0 ? 0 : wide >= 32 * units ? units : wide / 32;
       // X's second term, which only the epilogue of the same tile reads again, lies in the order of its lanes.
       uint8_t* lo = hyper.ws + static_cast<size_t>(m.lo) * 128 + (muon_lo_sector(it.j * m.mt + it.i, static_cast<int>(rank), q + (col0 >> 7 & 1) * 4) + (col0 >> 5 & 3) * 64 + lane) * 32;
       auto part = [&](uint32_t base, int u) {  // this lane's row of part u
@@ -569,6 +593,38 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
       got = wait_bounded(tfull + h, uses[h] & 1u, abort_flag, p.ctl, 50);
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after();
+      // A part of a split sum goes to the workspace; the warp that comes last adds all parts up, in their order.
+      const float4* all = nullptr;  // this lane's place in the first part
+      if (SPLIT && it.product == kMuonGram && m.splits > 1 && nu > 0) {
+        const int tile = it.j * (it.j + 1) / 2 + it.i;
+        uint8_t* at = p.parts + ((static_cast<size_t>(m.part0) + static_cast<size_t>(tile) * m.splits) * 2 + rank) * kMuonScratch + e * (kMuonScratch / kEpiWarps);
+        float4* own = reinterpret_cast<float4*>(at + static_cast<size_t>(it.part) * 2 * kMuonScratch) + lane;
+        all = reinterpret_cast<const float4*>(at) + lane;
+        for (int u = 0; u < nu; ++u) {
+          float v[32];
+          tmem_ld32(lanes + static_cast<uint32_t>(h * 256 + acc0 + u * 32), v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float4 x = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            if (deep) {
+              const float4 y = scratch[(u * 8 + j) * 32];
+              x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+            }
+            own[(u * 8 + j) * 32] = x;
+          }
+        }
+        __syncwarp();
+        unsigned done = 0;
+        if (lane == 0) {
+          __threadfence();  // every lane's stores, ordered before it by the barrier
+          done = atomicAdd(p.ctrl + kMuonCtrlWords + (m.split0 + tile) * 16 + rank * kEpiWarps + e, 1u) + 1u;
+          __threadfence();
+        }
+        done = __shfl_sync(0xffffffffu, done, 0);
+        __syncwarp();
+        if (done % static_cast<unsigned>(m.splits) != 0u) nu = 0;  // others are to come
+      }
       const float acc = p.acc[it.step][it.product], fac = p.add[it.step][it.product];
 #pragma unroll 1
       for (int u = 0; u < nu; ++u) {
@@ -577,13 +633,33 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
         for (int j = 0; j < 16; ++j) w[j] = hi1[j], l[j] = lo1[j];
         read_ahead(u + 1);
         float v[32];
-        tmem_ld32(lanes + static_cast<uint32_t>(h * 256 + acc0 + u * 32), v);
-        tmem_ld_wait();
-        if (deep) {
+        if (SPLIT && all != nullptr) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float4 y = scratch[(u * 8 + j) * 32];
-            v[4 * j] += y.x, v[4 * j + 1] += y.y, v[4 * j + 2] += y.z, v[4 * j + 3] += y.w;
+          for (int j = 0; j < 32; ++j) v[j] = 0.f;
+          for (int part = 0; part < m.splits; part += 2) {  // two on their way at a time
+            const float4* a = all + static_cast<size_t>(part) * 2 * (kMuonScratch / 16);
+            const float4* b = part + 1 < m.splits ? a + 2 * (kMuonScratch / 16) : nullptr;
+            float4 x[8], y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {  // written on other SMs: not from L1
+              x[j] = __ldcg(a + (u * 8 + j) * 32);
+              y[j] = b != nullptr ? __ldcg(b + (u * 8 + j) * 32) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              v[4 * j] = v[4 * j] + x[j].x + y[j].x, v[4 * j + 1] = v[4 * j + 1] + x[j].y + y[j].y;
+              v[4 * j + 2] = v[4 * j + 2] + x[j].z + y[j].z, v[4 * j + 3] = v[4 * j + 3] + x[j].w + y[j].w;
+            }
+          }
+        } else {
+          tmem_ld32(lanes + static_cast<uint32_t>(h * 256 + acc0 + u * 32), v);
+          tmem_ld_wait();
+          if (deep) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float4 y = scratch[(u * 8 + j) * 32];
+              v[4 * j] += y.x, v[4 * j + 1] += y.y, v[4 * j + 2] += y.z, v[4 * j + 3] += y.w;
+            }
           }
         }
 #pragma unroll
@@ -654,43 +730,44 @@ cudaLaunchConfig_t pipe_config(cudaLaunchAttribute* attr, int clusters, cudaStre
   return cfg;
 }
 
-template <int OUT>
-cudaError_t prepare_one(int* max_clusters) {
-  cudaError_t e = cudaFuncSetAttribute(muon_pipe_kernel<OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-  if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = pipe_config(attr, 1, nullptr);
-  cfg.numAttrs = 1;  // occupancy: the cluster shape only
-  int n = 0;
-  e = cudaOccupancyMaxActiveClusters(&n, muon_pipe_kernel<OUT>, &cfg);
-  if (e == cudaSuccess && n < *max_clusters) *max_clusters = n;
-  return e;
+template <bool SPLIT>
+const void* kernel_for(int out) {
+  switch (out) {
+    case kMuonOutBf16: return reinterpret_cast<const void*>(muon_pipe_kernel<kMuonOutBf16, SPLIT>);
+    case kMuonOutF16: return reinterpret_cast<const void*>(muon_pipe_kernel<kMuonOutF16, SPLIT>);
+    case kMuonParamF32: return reinterpret_cast<const void*>(muon_pipe_kernel<kMuonParamF32, SPLIT>);
+    case kMuonParamBf16: return reinterpret_cast<const void*>(muon_pipe_kernel<kMuonParamBf16, SPLIT>);
+    default: return reinterpret_cast<const void*>(muon_pipe_kernel<kMuonParamMaster, SPLIT>);
+  }
 }
+const void* kernel_for(int out, bool split) { return split ? kernel_for<true>(out) : kernel_for<false>(out); }
 
 }  // namespace
 
 cudaError_t muon_pipe_prepare(int* max_clusters) {
   *max_clusters = kMaxClusters;
-  cudaError_t e = prepare_one<kMuonOutBf16>(max_clusters);
-  if (e == cudaSuccess) e = prepare_one<kMuonOutF16>(max_clusters);
-  if (e == cudaSuccess) e = prepare_one<kMuonParamF32>(max_clusters);
-  if (e == cudaSuccess) e = prepare_one<kMuonParamBf16>(max_clusters);
-  if (e == cudaSuccess) e = prepare_one<kMuonParamMaster>(max_clusters);
-  return e;
+  for (int k = 0; k <= 2 * kMuonParamMaster + 1; ++k) {
+    const void* f = kernel_for(k / 2, k % 2 != 0);
+    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = pipe_config(attr, 1, nullptr);
+    cfg.numAttrs = 1;  // occupancy: the cluster shape only
+    int n = 0;
+    if ((e = cudaOccupancyMaxActiveClusters(&n, f, &cfg)) != cudaSuccess) return e;
+    if (n < *max_clusters) *max_clusters = n;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_muon_pipe(const CUtensorMap& load, const MuonTable& t, const MuonPipe& p, const MuonHyper& h, int out,
-                             int clusters, cudaStream_t stream) {
-  const int sym = p.sym << p.sym_half, rect = p.rect << p.rect_half, most = sym > rect ? sym : rect;  // items that can run at once
+                             bool split, int clusters, cudaStream_t stream) {
+  int most = 0;  // items that can run at once
+  for (int k = 0; k < 3; ++k) most = p.items[k] << p.half[k] > most ? p.items[k] << p.half[k] : most;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = pipe_config(attr, most < clusters ? most : clusters, stream);
-  switch (out) {
-    case kMuonOutBf16: return cudaLaunchKernelEx(&cfg, muon_pipe_kernel<kMuonOutBf16>, load, t, p, h);
-    case kMuonOutF16: return cudaLaunchKernelEx(&cfg, muon_pipe_kernel<kMuonOutF16>, load, t, p, h);
-    case kMuonParamF32: return cudaLaunchKernelEx(&cfg, muon_pipe_kernel<kMuonParamF32>, load, t, p, h);
-    case kMuonParamBf16: return cudaLaunchKernelEx(&cfg, muon_pipe_kernel<kMuonParamBf16>, load, t, p, h);
-    default: return cudaLaunchKernelEx(&cfg, muon_pipe_kernel<kMuonParamMaster>, load, t, p, h);
-  }
+  void* args[] = {const_cast<CUtensorMap*>(&load), const_cast<MuonTable*>(&t), const_cast<MuonPipe*>(&p), const_cast<MuonHyper*>(&h)};
+  return cudaLaunchKernelExC(&cfg, kernel_for(out, split), args);
 }
 
 }  // namespace hylo

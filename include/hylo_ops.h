@@ -192,10 +192,11 @@ hylo_status hylo_norm_backward(const void* s, int dtype, int64_t N, int64_t d, i
  * matrix without elements is skipped. 1 <= steps <= 32. Coefficients with which singular values could pass 2^20 are refused.
  * A matrix of zeros gives zeros; NaN or infinity anywhere in a matrix makes that whole result NaN, and leaves the others alone. No
  * output may overlap anything else. workspace: 256-byte aligned, hylo_orthogonalize_workspace_bytes() of the same list
- * (0 for invalid sizes; 6 bytes per element and 4 per element of A, padded, for matrices of together 512 MiB or one larger
- * one), not shared with a call still running on another stream.
+ * (0 for invalid sizes; 6 bytes per element and 4 per element of A, padded, for matrices of together 1 GiB or one larger
+ * one, and parts of long sums), not shared with a call still running on another stream.
  * Accuracy: products of fp16 numbers scaled by powers of two, fp32 sums, X as two fp16 terms where it is added: 1e-3 to 2e-3 of
- * the result's norm after five steps with the usual coefficients. Deterministic, and independent of the other matrices in the list. */
+ * the result's norm after five steps with the usual coefficients. Deterministic: the same list gives the same bits (with other
+ * matrices in the list, the sums of a matrix with a side of more than 8128 may be added up in another order). */
 typedef struct {
   const void* x;
   void* out;

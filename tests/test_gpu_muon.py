@@ -73,7 +73,7 @@ def test_sizes(rows, cols, kind):
 @pytest.mark.parametrize("dtype", list(DT))
 @pytest.mark.parametrize("out", ["bf16", "fp16"])
 def test_types_strides_and_lists(dtype, out):
-    """A list gives what each matrix gives alone, bit for bit, whatever its strides."""
+    """A list of matrices whose sums are not split gives what each gives alone, bit for bit, whatever its strides."""
     dt, out = DT[dtype], DT[out]
     mats = []
     for i, (r, c, pad) in enumerate([(70, 300, 0), (300, 70, 3), (257, 300, 1), (64, 64, 8), (1, 50, 5), (50, 1, 5), (400, 512, 0)]):
@@ -105,10 +105,25 @@ def test_many_matrices_in_several_groups():
     ys = orthogonalize(mats, dtype=torch.float16)
     for x, y in zip(mats[::13], ys[::13]):
         near(y, f64(x), torch.float16)
-    big = [matrix(1024, 8192, i) for i in range(12)]  # 12 x 52 MiB of workspace: more than one group's
-    ys = orthogonalize(big)
-    for i in (0, 8, 11):
-        assert torch.equal(ys[i], orthogonalize(big[i]))
+    big = [matrix(1024, 8192, i) for i in range(24)]  # 24 x 52 MiB of workspace: more than one group's
+    ys = orthogonalize(big, dtype=torch.float16)
+    again = orthogonalize(big, dtype=torch.float16)
+    assert all(torch.equal(a, b) for a, b in zip(ys, again))
+    near(ys[23], f64(big[23]), torch.float16)
+
+
+@pytest.mark.parametrize("shapes", [[(100, 9000)], [(300, 8129), (1030, 8250)], [(5, 70_000), (600, 8191), (40, 50)], [(9000, 1100)],
+                                    [(1, 300_000)], [(20, 600_000)]])
+def test_split_sums(shapes):
+    """Sums of A in parts, some of them longer than the tensor cores take at a time; bit for bit the same every time."""
+    xs = [matrix(r, c, r) for r, c in shapes]
+    ys = orthogonalize(xs, dtype=torch.float16)
+    _lib.hylo_kl_sync_status()
+    for x, y in zip(xs, ys):
+        near(y, f64(x), torch.float16)
+    near(orthogonalize(xs, steps=1, dtype=torch.float16)[0], f64(xs[0]), torch.float16, (oo.MUON,))
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(ys, orthogonalize(xs, dtype=torch.float16)))
 
 
 @pytest.mark.parametrize("k,steps", [((1.5, -0.5, 0.0), 12), ((2.0, -1.5, 0.5), 6), ((3.4445, -4.775, 2.0315), 1)])

@@ -70,12 +70,14 @@ def test_workspace(lib):
             lib.hylo_muon_workspace_bytes(b"".join(struct.pack("=" + _lib.MUON_TENSOR, P, G, W, M, r, c, 0, 0, 1) for r, c in shapes), len(shapes))
         return lib.hylo_orthogonalize_workspace_bytes(table, len(shapes))
 
-    square, ctrl = 5 * 256 * 256 * 2, 512  # X twice, its second term, A, B; the work's counters
+    square, ctrl, part = 5 * 256 * 256 * 2, 512, 256 * 1024  # X twice, its second term, A, B; the work's counters; one part of a tile's sum
     assert q((200, 200)) == square + 256 + ctrl and q((200, 200), (0, 5)) == square + 256 + ctrl
     assert q((1, 1), (256, 256)) == 2 * square + 256 + ctrl
-    assert q((2048, 8192)) == q((8192, 2048)) == 3 * 2048 * 8192 * 2 + 2 * 2048 * 2048 * 2 + 1024 * 12 + ctrl
-    assert q(*[(2048, 8192)] * 100) <= 513 << 20 and q(*[(64, 64)] * 1000) == 64 * square + 64 * 12 + ctrl
-    assert q((200, 8193)) == 256 * (3 * 8448 + 2 * 256) * 2 + 256 * 10 + ctrl + 256 * 128 * 1024  # sums of over 8192 products
+    # 36 tiles leave room for two parts of their sums each, one tile for as many as are worth while
+    assert q((2048, 8192)) == q((8192, 2048)) == 3 * 2048 * 8192 * 2 + 2 * 2048 * 2048 * 2 + 1024 * 12 + 2816 + 36 * 2 * part
+    assert q(*[(2048, 8192)] * 100) <= 1025 << 20 and q(*[(64, 64)] * 1000) == 64 * square + 64 * 12 + ctrl
+    assert q((200, 8193)) == 256 * (3 * 8448 + 2 * 256) * 2 + 256 * 10 + ctrl + 4 * part
+    assert q((100, 1 << 20)) == 256 * (3 * (1 << 20) + 2 * 256) * 2 + 1024 * 12 + ctrl + 50 * part + 256 * 128 * 1024  # deep parts
     assert q((0, 0)) == ctrl and q((1 << 21, 1)) == 0
 
 
