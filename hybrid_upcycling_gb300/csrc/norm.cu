@@ -174,134 +174,52 @@ __device__ __forceinline__ void plus(float (&x)[N], const float (&a)[N]) {
   if constexpr (N % 2 == 1) x[N - 1] += a[N - 1];
 }
 
-// y of a thread's vectors k0, ..., k0 + KB - 1 of one row. All gains are loaded before the first one is used.
-template <typename T, typename G, int VB, int KC, int KB>
-__device__ __forceinline__ void write_row(const NormParams& p, T* y, const Pack<T, VB> (&raw)[KC], int k0, int t, float mu, float rstd) {
-  float w[KB][VB], b[KB][VB];
-#pragma unroll
-  for (int k = 0; k < KB; ++k) {
-    const int c = ((k0 + k) * p.threads + t) * VB;
-#pragma unroll
-    for (int j = 0; j < VB; ++j) w[k][j] = 1.f, b[k][j] = 0.f;
-    if (p.weight != nullptr && c < p.d) load<G, VB>(static_cast<const G*>(p.weight) + c, w[k]);
-    if (p.bias != nullptr && c < p.d) load<G, VB>(static_cast<const G*>(p.bias) + c, b[k]);
-  }
-#pragma unroll
-  for (int k = 0; k < KB; ++k) {
-    const int c = ((k0 + k) * p.threads + t) * VB;
-    float x[VB];
-    raw[k0 + k].get(x);
-    normalise<true>(x, mu, rstd);
-    times(x, w[k]);
-    if (p.bias != nullptr) plus(x, b[k]);
-    if (c < p.d) store<T, VB>(y + c, x);
-  }
-}
-
-// KR rows at a time for each group of p.threads threads, KC vectors of VB columns a thread and row.
-template <typename T, int VB, int KC, int KR>
-__global__ void __launch_bounds__(KC * KR == 1 ? 1024 : 512) norm_fwd_kernel(const NormParams p) {
+// Few rows, each by a group of p.threads threads that have one vector of VB columns: what counts is the time of one row.
+template <typename T, int VB>
+__global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormParams p) {
   using V = Pack<T, VB>;
-  __shared__ float red[2][KR * 32];
-  const int group = threadIdx.x / p.threads, t = threadIdx.x - group * p.threads;
-  const int groups = blockDim.x / p.threads;
+  __shared__ float red[2][32];
+  const int group = threadIdx.x / p.threads, t = threadIdx.x - group * p.threads, c = t * VB;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / p.threads) + group;
+  const bool mine = row < p.N && c < p.d;
   const float inv_d = 1.f / static_cast<float>(p.d);
-  const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * groups + group) * KR;
-  V raw[KR][KC];
-#pragma unroll
-  for (int r = 0; r < KR; ++r) {
-    const T* x = static_cast<const T*>(p.x) + (row0 + r) * p.ldx;
-#pragma unroll
-    for (int k = 0; k < KC; ++k) {
-      const int c = (k * p.threads + t) * VB;
-      raw[r][k].clear();
-      if (row0 + r < p.N && c < p.d) raw[r][k] = *reinterpret_cast<const V*>(x + c);
-    }
+  V raw;
+  raw.clear();
+  if (mine) raw = *reinterpret_cast<const V*>(static_cast<const T*>(p.x) + row * p.ldx + c);
+  float x[VB];
+  if (p.residual != nullptr && mine) {
+    const V more = *reinterpret_cast<const V*>(static_cast<const T*>(p.residual) + row * p.ldr + c);
+    float a[VB];
+    raw.get(x);
+    more.get(a);
+    plus(x, a);
+    raw.set(x);  // as the next layer reads it
+    *reinterpret_cast<V*>(static_cast<T*>(p.sum) + row * p.d + c) = raw;
   }
-  if (p.residual != nullptr) {
-    V more[KR][KC];
-#pragma unroll
-    for (int r = 0; r < KR; ++r) {
-      const T* x = static_cast<const T*>(p.residual) + (row0 + r) * p.ldr;
-#pragma unroll
-      for (int k = 0; k < KC; ++k) {
-        const int c = (k * p.threads + t) * VB;
-        more[r][k].clear();
-        if (row0 + r < p.N && c < p.d) more[r][k] = *reinterpret_cast<const V*>(x + c);
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < KR; ++r) {
-      T* sum = static_cast<T*>(p.sum) + (row0 + r) * p.d;
-#pragma unroll
-      for (int k = 0; k < KC; ++k) {
-        const int c = (k * p.threads + t) * VB;
-        float a[VB], b[VB];
-        raw[r][k].get(a);
-        more[r][k].get(b);
-        plus(a, b);
-        raw[r][k].set(a);  // as the next layer reads it
-        if (row0 + r < p.N && c < p.d) *reinterpret_cast<V*>(sum + c) = raw[r][k];
-      }
-    }
-  }
-  float mu[KR], v[KR];
-#pragma unroll
-  for (int r = 0; r < KR; ++r) mu[r] = 0.f;
+  raw.get(x);
+  float mu[1] = {0.f}, v[1] = {0.f};
   if (!p.rms) {
 #pragma unroll
-    for (int r = 0; r < KR; ++r) {
-      float sum[VB];
-#pragma unroll
-      for (int j = 0; j < VB; ++j) sum[j] = 0.f;
-#pragma unroll
-      for (int k = 0; k < KC; ++k) {
-        float a[VB];
-        raw[r][k].get(a);
-        plus(sum, a);
-      }
-#pragma unroll
-      for (int j = 0; j < VB; ++j) mu[r] += sum[j];
-    }
+    for (int j = 0; j < VB; ++j) mu[0] += x[j];
     row_sums(mu, p.threads, red[0]);
-#pragma unroll
-    for (int r = 0; r < KR; ++r) mu[r] *= inv_d;
+    mu[0] *= inv_d;
   }
+  if (mine) {
 #pragma unroll
-  for (int r = 0; r < KR; ++r) {
-    float2 sum = two(0.f);
-    v[r] = 0.f;
-#pragma unroll
-    for (int k = 0; k < KC; ++k) {
-      if ((k * p.threads + t) * VB < p.d) {
-        float a[VB];
-        raw[r][k].get(a);
-#pragma unroll
-        for (int j = 0; j + 1 < VB; j += 2) {
-          const float2 x = __fadd2_rn(pair(a + j), two(-mu[r]));
-          sum = __ffma2_rn(x, x, sum);
-        }
-        if constexpr (VB == 1) v[r] = fmaf(a[0] - mu[r], a[0] - mu[r], v[r]);
-      }
-    }
-    v[r] += sum.x + sum.y;
+    for (int j = 0; j < VB; ++j) v[0] = fmaf(x[j] - mu[0], x[j] - mu[0], v[0]);
   }
   row_sums(v, p.threads, red[1]);
-#pragma unroll
-  for (int r = 0; r < KR; ++r) {
-    if (row0 + r >= p.N) break;
-    const float rstd = rsqrtf(fmaf(v[r], inv_d, p.eps));
-    if (t == 0 && p.stats != nullptr) p.stats[row0 + r] = make_float2(mu[r], rstd);
-    T* y = static_cast<T*>(p.y) + (row0 + r) * p.d;
-    constexpr int KB = KC < 4 ? KC : 4;
-#pragma unroll
-    for (int k = 0; k < KC; k += KB) {
-      if (p.gain_f32)
-        write_row<T, float, VB, KC, KB>(p, y, raw[r], k, t, mu[r], rstd);
-      else
-        write_row<T, T, VB, KC, KB>(p, y, raw[r], k, t, mu[r], rstd);
-    }
-  }
+  if (row >= p.N) return;
+  const float rstd = rsqrtf(fmaf(v[0], inv_d, p.eps));
+  if (t == 0 && p.stats != nullptr) p.stats[row] = make_float2(mu[0], rstd);
+  if (!mine) return;
+  float w[VB], b[VB];  // (asked for before the sums, their conversion holds up the row: 2.37 us for 64 x 4096, 2.24 so)
+  if (p.weight != nullptr) load_gain<T, VB>(p.weight, p.gain_f32, c, w);
+  if (p.bias != nullptr) load_gain<T, VB>(p.bias, p.gain_f32, c, b);
+  normalise<true>(x, mu[0], rstd);
+  if (p.weight != nullptr) times(x, w);
+  if (p.bias != nullptr) plus(x, b);
+  store<T, VB>(static_cast<T*>(p.y) + row * p.d + c, x);
 }
 
 // 16 bytes from global to shared memory, or 16 zero bytes.
@@ -429,7 +347,8 @@ __device__ __forceinline__ void row_moments(const V (&raw)[R][KC], const NormPar
 }
 
 // R rows at a time for each group of p.threads threads, KC vectors a thread and row, S - 1 times as many rows on their way. RMS:
-// neither means nor a bias.
+// neither means nor a bias. bf16 with two streams 65536 x 2048 180 us (0.88 of a copy's rate), 8192 x 4096 49; 4096 x 16384 52;
+// fp32 8192 x 8192 93. What is left there is the start and the end, 6 us, and the barrier of a turn.
 template <typename T, int KC, int R, int S, bool RMS, bool RES>
 __global__ void __launch_bounds__(512, 1) norm_fwd_ring_kernel(const NormParams p) {
   constexpr int VB = 16 / sizeof(T), C = KC * VB, STREAMS = RES ? 2 : 1;
@@ -558,10 +477,11 @@ __global__ void __launch_bounds__(512, 1) norm_fwd_ring_kernel(const NormParams 
 }
 
 // ---- Rows that are not made of 16-byte vectors (an odd width, stride or start). Their bytes still come as whole 16-byte vectors of
-// memory into the ring, shifted by the row's start modulo 16, and are taken apart there: a warp has 32 C consecutive columns, a lane every 32nd
-// of them (fewer lanes where a row takes part of a warp), so that a warp reads and writes consecutive elements. What
-// these kernels cost is instructions: warps whose columns all exist go without a test for each (51 instructions an element with them). A vector's bytes in front of or behind the row belong to the
-// same tensor, except in front of its first element and behind its last one, which are not read.
+// memory into the ring, shifted by the row's start modulo 16, and are taken apart there: a warp has 32 C consecutive columns, a lane
+// every 32nd of them (fewer lanes where a row takes part of a warp), so that a warp reads and writes consecutive elements. What these
+// kernels cost is instructions: warps whose columns all exist go without a test for each (51 instructions an element with them).
+// 65536 x 1001 bf16 110 us forward and 138 backward, fp32 128 and 156 (0.60 and 0.74 of a copy's rate). A vector's bytes in front
+// of or behind the row belong to the same tensor, except in front of its first element and behind its last one, which are not read.
 struct OddRows {
   uintptr_t base, end;  // of the tensor
   int64_t stride;       // bytes
@@ -765,7 +685,8 @@ __global__ void __launch_bounds__(512, 1) norm_fwd_odd_kernel(const NormParams p
   copy_wait<0>();
 }
 
-// Rows too wide for the registers: a CTA reads its row again for each of the three steps.
+// Rows too wide for the registers: a CTA reads its row again for each of the three steps, from L2 (2048 x 100000 bf16 with a
+// residual 546 us, 0.44 of a copy's rate by what has to be read).
 template <typename T, int VB>
 __global__ void __launch_bounds__(1024) norm_fwd_wide_kernel(const NormParams p) {
   __shared__ float red[2][32];
@@ -968,7 +889,8 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_odd_kernel(const NormParams p
   }
 }
 
-// The gradients for rows of 16-byte vectors: as above, R rows of a group at a time and S - 1 times as many on their way.
+// The gradients for rows of 16-byte vectors: as above, R rows of a group at a time and S - 1 times as many on their way. bf16 with
+// dsum 65536 x 2048 165 us (0.96 of a copy's rate), 8192 x 4096 50; fp32 65536 x 512 79.
 template <typename T, int KC, int R, int S, bool RMS, bool DSUM>
 __global__ void __launch_bounds__(512, 1) norm_bwd_ring_kernel(const NormParams p, const NormGrad q) {
   constexpr int VB = 16 / sizeof(T), C = KC * VB, STREAMS = DSUM ? 3 : 2;
@@ -1099,7 +1021,8 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_ring_kernel(const NormParams 
 // The same for rows that a cluster shares, q.cta_cols columns a CTA, one row at a time. Order of a turn: the sums of row i; the wait
 // for those of row i - 1, which the CTAs have sent one another meanwhile; the sending of row i's; dx of row i - 1. The sums
 // arrive with st.async, counted on a barrier of the CTA that receives them (a cluster barrier a turn took twice as long). Three
-// places for them are enough: a CTA sends row i + 3's only after it has this CTA's of row i + 2, sent after all here were done with row i's.
+// places for them are enough: a CTA sends row i + 3's only after it has this CTA's of row i + 2, sent after all here were done with
+// row i's. bf16 16384 x 5120 90 us (0.82 of a copy's rate), 4096 x 16384 87; fp32 8192 x 8192 141.
 __device__ __forceinline__ void send_pair(uint32_t to, float a, float b, uint32_t bar) {
   asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];"
                :: "r"(to), "r"(__float_as_uint(a)), "r"(__float_as_uint(b)), "r"(bar) : "memory");
@@ -1249,7 +1172,7 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_cluster_kernel(const NormPara
   cluster_sync_all();  // no CTA leaves while another one may still send to it
 }
 
-// dx of rows too wide for the registers.
+// dx of rows too wide for the registers (2048 x 100000 bf16 with dsum 509 us, 0.47 of a copy's rate; dw and db as much as 314 more).
 template <typename T, int VB>
 __global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(const NormParams p, const NormGrad q) {
   __shared__ float red[2][32];
@@ -1295,7 +1218,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(const NormParams p,
   }
 }
 
-// The columns' sums of rows blockIdx.y, blockIdx.y + gridDim.y, ... for 1024 / sizeof(T) columns a CTA, read once more.
+// The columns' sums of rows blockIdx.y, blockIdx.y + gridDim.y, ... for 256 columns a CTA, read once more.
 template <typename T>
 __global__ void __launch_bounds__(256) norm_columns_kernel(const NormParams p, const NormGrad q) {
   const int c = blockIdx.x * 256 + threadIdx.x;
@@ -1382,12 +1305,12 @@ cudaError_t allow_smem() {
 
 unsigned blocks_for(int64_t blocks, int64_t most) { return static_cast<unsigned>(blocks < most ? blocks : most); }
 
-template <typename T, int VB, int KC, int KR>
+template <typename T, int VB>
 cudaError_t fwd(NormParams p, cudaStream_t stream) {
-  p.threads = round_threads(cdiv64(p.d, VB * KC));
+  p.threads = round_threads(cdiv64(p.d, VB));
   const int cta = p.threads > 32 ? p.threads : 128;
-  const int64_t blocks = cdiv64(p.N, static_cast<int64_t>(cta / p.threads) * KR);
-  return launch(norm_fwd_kernel<T, VB, KC, KR>, dim3(static_cast<unsigned>(blocks)), cta, 0, stream, false, p);
+  const int64_t blocks = cdiv64(p.N, cta / p.threads);
+  return launch(norm_fwd_kernel<T, VB>, dim3(static_cast<unsigned>(blocks)), cta, 0, stream, false, p);
 }
 
 template <typename T, int KC, int R, int S, bool RMS, bool RES>
@@ -1426,12 +1349,12 @@ cudaError_t fwd_rings(const NormParams& p, int sms, cudaStream_t stream) {
 template <typename T, int VB>
 cudaError_t fwd_cols(const NormParams& p, int sms, cudaStream_t stream) {
   if constexpr (VB == 1) {
-    if (p.d <= 1024 && p.N <= 2 * sms) return fwd<T, 1, 1, 1>(p, stream);
+    if (p.d <= 1024 && p.N <= 2 * sms) return fwd<T, 1>(p, stream);
     if (p.d <= 512 * 8) return fwd_odd<T, 8, sizeof(T) == 2 ? 2 : 1, 4>(p, sms, stream);
     if (p.d <= 512 * 16) return fwd_odd<T, 16, 1, 3>(p, sms, stream);
     if (p.d <= 512 * 32 && (sizeof(T) == 2 || p.residual == nullptr)) return fwd_odd<T, 32, 1, 3>(p, sms, stream);
   } else {
-    if (p.d <= 1024 * VB && p.N <= 4 * sms) return fwd<T, VB, 1, 1>(p, stream);  // few rows: what counts is the time of one
+    if (p.d <= 1024 * VB && p.N <= 4 * sms) return fwd<T, VB>(p, stream);
     if (p.d <= (sizeof(T) == 4 && p.residual ? 512 * 16 : 512 * 32)) {  // what the ring has room for
       if (p.rms && p.bias == nullptr) return p.residual ? fwd_rings<T, true, true>(p, sms, stream) : fwd_rings<T, true, false>(p, sms, stream);
       return p.residual ? fwd_rings<T, false, true>(p, sms, stream) : fwd_rings<T, false, false>(p, sms, stream);
