@@ -56,7 +56,8 @@ def orthogonalize(matrices: Union[torch.Tensor, Iterable[torch.Tensor]], steps: 
 
     matrices: a list of tensors [..., m, n], all float32, bfloat16 or float16, leading dimensions being a batch of matrices, or
     one such tensor. Rows or columns with unit stride are read in place. Returns contiguous tensors (or one) of ``dtype``,
-    bfloat16 or float16: the products take fp16 numbers, 1e-3 to 2e-3 of the result's norm. coefficients: (a, b, c), or one
+    bfloat16 or float16: the products take fp16 numbers, 1e-3 to 2e-3 of the result's norm (up to
+    4e-3 for a single row). coefficients: (a, b, c), or one
     triple for each step. Not differentiable."""
     single = isinstance(matrices, torch.Tensor)
     tensors = [matrices] if single else list(matrices)

@@ -195,7 +195,7 @@ hylo_status hylo_norm_backward(const void* s, int dtype, int64_t N, int64_t d, i
  * (0 for invalid sizes; 6 bytes per element and 4 per element of A, padded, for matrices of together 1 GiB or one larger
  * one, and parts of long sums), not shared with a call still running on another stream.
  * Accuracy: products of fp16 numbers scaled by powers of two, fp32 sums, X as two fp16 terms where it is added: 1e-3 to 2e-3 of
- * the result's norm after five steps with the usual coefficients. Deterministic: the same list gives the same bits (with other
+ * the result's norm after five steps with the usual coefficients, up to 4e-3 where few singular values share it (one row). Deterministic: the same list gives the same bits (with other
  * matrices in the list, the sums of a matrix with a side of more than 8128 may be added up in another order). */
 typedef struct {
   const void* x;
