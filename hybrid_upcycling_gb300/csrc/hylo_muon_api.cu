@@ -13,8 +13,8 @@ namespace {
 
 constexpr int64_t kMaxSide = int64_t(1) << 20, kMaxShort = 16384;
 constexpr int kMaxSteps = kMuonStepsMax;
-// Matrices that go through the products together: enough tiles for every SM (two layers' matrices 3.65 ms in groups of half as
-// much, 3.55 so), and no more memory than that takes.
+// Matrices that go through the products together: enough tiles for every SM (groups of half as much take 3 % longer), and no
+// more memory than that takes.
 constexpr int64_t kGroupRows = (int64_t(1024) << 20) / 128;
 
 uintptr_t bytes_of(int dtype) { return dtype == HYLO_F32 ? 4 : 2; }
