@@ -19,8 +19,8 @@
 // may start once every earlier item of its matrix is done, which a counter per matrix tells: what it reads is then complete, and
 // what it overwrites is no longer read. With several matrices the tail of one's product is filled with the next one's items;
 // every item waits for earlier ones only, which running CTAs hold, so the launch cannot deadlock whatever the residency. Where a product
-// leaves half of the clusters idle, items are 256 x 128: their products take as long (more operands are read for each, whose latency
-// the six stages then do not cover), what follows half as long.
+// leaves half of the clusters idle, items are 256 x 128: their products take as long (an instruction of half as many columns takes the
+// same 134 cycles, and eight smaller stages instead of six gave nothing), what follows half as long.
 //
 // Long sums of few items of Gram are split among items of their own; their fp32 parts meet in the workspace, and each warp of the
 // epilogue that finds all parts of its 32 rows there adds them up in a fixed order.
