@@ -19,8 +19,8 @@
 // may start once every earlier item of its matrix is done, which a counter per matrix tells: what it reads is then complete, and
 // what it overwrites is no longer read. With several matrices the tail of one's product is filled with the next one's items;
 // every item waits for earlier ones only, which running CTAs hold, so the launch cannot deadlock whatever the residency. Where a product
-// leaves half of the clusters idle, items are 256 x 128: their products take as long (an instruction of half as many columns takes the
-// same 134 cycles, and eight smaller stages instead of six gave nothing), what follows half as long.
+// leaves half of the clusters idle, items are 256 x 128: their products take as long (546 cycles for a 64-deep block either way: what
+// one thread needs to wait for a stage, issue four products and commit them), what follows half as long.
 //
 // Long sums of few items of Gram are split among items of their own; their fp32 parts meet in the workspace, and each warp of the
 // epilogue that finds all parts of its 32 rows there adds them up in a fixed order.
@@ -32,7 +32,7 @@
 // long; parts through shared memory by TMA are as fast as this where there is much to do and slower where there is little.)
 //
 // What bounds it: the tensor cores, at the clock that the power cap leaves. Four 2048 x 8192 matrices 1.44 ms, the tensor pipe 82 %
-// active; an Apply item of K = 2048 21 500 cycles (16 400 at the tensor cores' rate, the rest operands on their way), its epilogue
+// active; an Apply item of K = 2048 21 500 cycles (16 400 at the tensor cores' rate, the rest the issue beside the epilogue), its epilogue
 // 15 000 beside the next one's products. One 2048 x 2048: 0.26 ms, each product a chain of queue, copies, products and epilogue.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
