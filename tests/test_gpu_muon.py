@@ -352,3 +352,20 @@ def test_overlapping_arrays_are_refused():
     for args in (([w, w], [g, g], [m, m.clone()]), ([w], [w], [m]), ([w], [g], [w]), ([w], [m], [m])):
         with pytest.raises(_lib.HyloError, match="overlap"):
             muon_step(*args, lr=0.1)
+
+
+def test_vectors_as_matrices_and_a_batch_of_experts():
+    """Parameters of one row, of one column, and a batch, with and without masters, in one optimiser."""
+    torch.manual_seed(1)
+    shapes = [(1, 300), (300, 1), (4, 24, 50), (2, 2, 16, 16), (0, 8)]
+    for masters in (True, False):
+        ps = [torch.randn(s, device="cuda").bfloat16().requires_grad_() for s in shapes]
+        opt = Muon(ps, lr=0.1, masters=masters, momentum=0.0, nesterov=False, adjust=None)
+        gs = [torch.randn_like(p) for p in ps]
+        before = [p.detach().clone() for p in ps]
+        opt.step(gs)
+        for p, b, g in zip(ps, before, gs):
+            want = f64(b) - 0.1 * f64(orthogonalize(g, dtype=torch.float16))
+            # half a bf16 step to nearest, a whole one (2^-7) rounded at random; fp32 roundings besides
+            unit = 2.0 ** -8 if masters else 2.0 ** -7
+            assert np.all(np.abs(f64(p) - want) <= unit * np.abs(want) * (1 + 2.0 ** -7) + 1e-6)

@@ -321,3 +321,50 @@ def test_second_derivatives_and_tangents_are_refused():
     with torch.autograd.forward_ad.dual_level():
         with pytest.raises(NotImplementedError):
             rms_norm(torch.autograd.forward_ad.make_dual(x.detach(), torch.ones_like(x)), w)
+
+
+def test_the_same_tensor_twice_and_gradients_of_their_own():
+    x, r, w, _, dy, ds = make(20, 72, torch.float32, "same", False, True)
+    a, b = (t.detach().clone().requires_grad_() for t in (x, x))
+    y, s = rms_norm(a, w, residual=b)
+    torch.autograd.backward((y, s), (dy, ds))
+    assert torch.equal(a.grad, b.grad) and a.grad.data_ptr() != b.grad.data_ptr()  # one may be scaled in place without the other
+    c = x.detach().clone().requires_grad_()
+    y2, s2 = rms_norm(c, w, residual=c)
+    torch.autograd.backward((y2, s2), (dy, ds))
+    assert torch.equal(y2, y) and torch.equal(c.grad, 2 * a.grad)
+    v = w.detach().clone().requires_grad_()  # one gain for two norms, as tied layers have it
+    one = torch.autograd.grad(rms_norm(x, v), v, dy)[0] + torch.autograd.grad(rms_norm(r, v), v, dy)[0]
+    two = torch.autograd.grad((rms_norm(x, v), rms_norm(r, v)), v, (dy, dy))[0]
+    assert torch.equal(one, two)
+    with torch.inference_mode():
+        assert torch.equal(rms_norm(x, w), rms_norm(x.clone(), w))
+
+
+def test_two_threads_with_a_stream_each():
+    import threading
+    jobs = []
+    for i, d in enumerate((520, 6000)):
+        x, _, w, b, dy, _ = make(300, d, torch.bfloat16, "fp32", True, False, seed=i)
+        x, w, b = (t.detach().clone().requires_grad_() for t in (x, w, b))
+        y = layer_norm(x, w, b)
+        jobs.append((x, w, b, dy, (y,) + torch.autograd.grad(y, (x, w, b), dy)))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(job):
+        x, w, b, dy, ref = job
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                y = layer_norm(x, w, b)
+                got = (y,) + torch.autograd.grad(y, (x, w, b), dy)
+                torch.cuda.current_stream().synchronize()
+                if not all(torch.equal(p, q) for p, q in zip(got, ref)):
+                    wrong.append(x.shape)
+
+    threads = [threading.Thread(target=work, args=(j,)) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
