@@ -19,8 +19,8 @@
 // may start once every earlier item of its matrix is done, which a counter per matrix tells: what it reads is then complete, and
 // what it overwrites is no longer read. With several matrices the tail of one's product is filled with the next one's items;
 // every item waits for earlier ones only, which running CTAs hold, so the launch cannot deadlock whatever the residency. Where a product
-// leaves half of the clusters idle, items are 256 x 128: their products take as long (546 cycles for a 64-deep block either way: what
-// one thread needs to wait for a stage, issue four products and commit them), what follows half as long.
+// leaves half of the clusters idle, items are 256 x 128: and take half as long, 296 cycles for a 64-deep block and 550 at
+// most for a whole tile's. (Eight stages of their size instead of six: the same or slower.)
 //
 // Long sums of few items of Gram are split among items of their own; their fp32 parts meet in the workspace, and each warp of the
 // epilogue that finds all parts of its 32 rows there adds them up in a fixed order.
@@ -31,9 +31,9 @@
 // lane to a row and 32 bytes, a whole sector, an access. (With 16 bytes an access and nothing ahead the tiles of Apply took twice as
 // long; parts through shared memory by TMA are as fast as this where there is much to do and slower where there is little.)
 //
-// What bounds it: the tensor cores, at the clock that the power cap leaves. Four 2048 x 8192 matrices 1.44 ms, the tensor pipe 82 %
-// active; an Apply item of K = 2048 21 500 cycles (16 400 at the tensor cores' rate, the rest the issue beside the epilogue), its epilogue
-// 15 000 beside the next one's products. One 2048 x 2048: 0.26 ms, each product a chain of queue, copies, products and epilogue.
+// What bounds it: the tensor cores, at the clock that the power cap leaves. Four 2048 x 8192 matrices 1.38 ms, the tensor pipe 85 %
+// active; an Apply item of K = 2048 19 000 cycles (16 400 at the tensor cores' rate), its epilogue 16 000 beside the next one's
+// products. One 2048 x 2048: 0.22 ms, each product a chain of queue, copies, products and epilogue.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -142,6 +142,15 @@ __device__ __forceinline__ bool mirrored(int kb, int tile) { return (kb >> 2) < 
 
 __device__ __forceinline__ uint64_t slice_desc(bool mn, uint32_t base, int k) {
   return mn ? smem_desc_sw128(base + k * 2048, 8192, 1024) : smem_desc_sw128(base + k * 32, 0, 1024);
+}
+
+// One lane of a converged warp, the same every time. The compiler knows that code behind it runs in one thread; behind lane == 0 it does
+// not, and each operand of the copies and products, which have to be uniform, costs a detour (one 2048 x 2048 matrix 262 us so, 223
+// with the chosen lane; a 64-deep block of products of half a tile 546 cycles and 296).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(is));
+  return is != 0;
 }
 
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, unsigned long long limit_ns) {
@@ -276,7 +285,7 @@ __device__ __forceinline__ const Stored<OUT>* old_values(const MuonMat& m) {
 }
 
 // Asks for the old values of 32 rows and 32 `units` columns. (Without this, with a branch around each element's step and a hash more for it
-// an item of the last product took 58 000 cycles in bf16 and 34 000 with masters; now 26 000 and 21 000, beside 20 000 for the products.)
+// an item of the last product took 58 000 cycles in bf16 and 34 000 with masters; now 23 500 and 20 000, beside 15 000 to 19 000 for the products.)
 template <int OUT>
 __device__ __forceinline__ void prefetch_old(const MuonMat& m, int row, int col, int units, int lane) {
   constexpr int LINE = 128 / sizeof(Stored<OUT>);
@@ -451,7 +460,7 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
     }
   } else if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer (both CTAs)
-    if (lane == 0) {
+    if (elect_one()) {
       int stage = 0;
       uint32_t phase = 0, armed = 0;
       const uint32_t lead_iempty = mapa_shared(smem_u32(iempty), 0), full_lead = mapa_shared(smem_u32(full), 0);
@@ -502,7 +511,7 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ UMMA issuer (even CTA)
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && elect_one()) {
       int stage = 0, h = 0;
       uint32_t phase = 0, uses[2] = {0u, 0u};
       bool ok = true, issued = false;
@@ -535,9 +544,11 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
             const bool amn = it.product != kMuonGram && mirrored(kb, it.i);
             const bool bmn = it.product == kMuonApply || (it.product == kMuonPoly && mirrored(kb, it.j));
             const uint32_t idesc = idesc0 | (amn ? kAMajor : 0u) | (bmn ? kBMajor : 0u);
+            const uint64_t a0 = slice_desc(amn, sa, 0), b0 = slice_desc(bmn, sb, 0);
+            const uint32_t astep = amn ? 2048 >> 4 : 32 >> 4, bstep = bmn ? 2048 >> 4 : 32 >> 4;
 #pragma unroll
             for (int q = 0; q < kBK / 16; ++q)
-              umma_bf16_pair(d, slice_desc(amn, sa, q), slice_desc(bmn, sb, q), idesc, (kb > from || q > 0) ? 1u : 0u);
+              umma_bf16_pair(d, a0 + q * astep, b0 + q * bstep, idesc, (kb > from || q > 0) ? 1u : 0u);
             umma_commit_pair(empty + stage, 0x3);
             issued = true;
             if (++stage == STAGES) {
