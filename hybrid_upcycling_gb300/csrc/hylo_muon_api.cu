@@ -107,6 +107,21 @@ Group next_group(const T* list, int count, int first) {
   return g;
 }
 
+// Whether the upper triangles' products are done sooner by halves of tiles, 296 cycles for a 64-deep block, than by whole ones, 500:
+// by the longest item and by all of them shared out. (5003 x 520, 1000 x 1001 and 8192 x 2048 together 612 us with whole tiles, 560
+// so. Apply, whose epilogue is as long as its products, gains only where every cluster has one half: one 2048 x 2048 221 us, 227
+// with its 64 tiles halved.)
+bool halves_are_sooner(const MuonTable& tab, int64_t clusters, int MuonMat::*depth) {
+  int64_t longest = 0, work = 0;
+  for (int i = 0; i < tab.count; ++i) {
+    const MuonMat& t = tab.t[i];
+    longest = t.*depth > longest ? t.*depth : longest;
+    work += static_cast<int64_t>(t.mt) * (t.mt + 1) / 2 * (t.*depth);
+  }
+  longest *= clusters;
+  return 296 * (longest > 2 * work ? longest : 2 * work) < 500 * (longest > work ? longest : work);
+}
+
 template <typename T>
 size_t workspace(const T* list, int count) {
   size_t most = 256;
@@ -245,7 +260,9 @@ hylo_status run(const T* list, int count, int dtype, int out_dtype, bool masters
     p.parts = h.ws + group.splits_at();
     p.ctl = WaitCtl{dev->status, wait_limit_ns()};
     p.steps = s.count;
-    for (int k = 0; k < 3; ++k) p.half[k] = 2 * p.items[k] <= dev->muon_clusters && (k != kMuonGram || split == 0);
+    p.half[kMuonApply] = 2 * p.items[kMuonApply] <= dev->muon_clusters;
+    p.half[kMuonGram] = split == 0 && halves_are_sooner(tab, dev->muon_clusters, &MuonMat::kn);
+    p.half[kMuonPoly] = halves_are_sooner(tab, dev->muon_clusters, &MuonMat::km);
     for (int k = 0; k < s.count; ++k) {
       const double *c = s.k + 3 * k, x = s.x[k], a = s.a[k], b = s.b[k], next = s.x[k + 1];
       p.acc[k][kMuonGram] = static_cast<float>(a / (x * x));

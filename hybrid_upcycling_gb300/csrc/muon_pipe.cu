@@ -18,9 +18,9 @@
 // Work items are 256 x 256 tiles, taken from a queue in the order step, product, matrix, tile. One
 // may start once every earlier item of its matrix is done, which a counter per matrix tells: what it reads is then complete, and
 // what it overwrites is no longer read. With several matrices the tail of one's product is filled with the next one's items;
-// every item waits for earlier ones only, which running CTAs hold, so the launch cannot deadlock whatever the residency. Where a product
-// leaves half of the clusters idle, items are 256 x 128: and take half as long, 296 cycles for a 64-deep block and 550 at
-// most for a whole tile's. (Eight stages of their size instead of six: the same or slower.)
+// every item waits for earlier ones only, which running CTAs hold, so the launch cannot deadlock whatever the residency. Where whole
+// tiles of a product would leave clusters idle, items are 256 x 128 and take little more than half as long, 296 cycles for a 64-deep
+// block, a whole tile's 500 to 590. (Eight stages of their size instead of six: the same or slower.)
 //
 // Long sums of few items of Gram are split among items of their own; their fp32 parts meet in the workspace, and each warp of the
 // epilogue that finds all parts of its 32 rows there adds them up in a fixed order.
