@@ -1102,8 +1102,8 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_cluster_kernel(const NormPara
       if (c < end) store<T, VB>(dx + c, g);
     }
   };
-  auto take = [&](int turn) {  // the sums of that turn, or a time-out that ends the kernel
-    if (!wait_bounded(arrived + turn % 3, static_cast<uint32_t>(turn / 3) & 1u, &given_up, q.ctl, 61)) given_up = 1;
+  auto take = [&](int turn) {  // the sums of that turn, which other CTAs release at cluster scope, or a time-out that ends the kernel
+    if (!wait_bounded<true>(arrived + turn % 3, static_cast<uint32_t>(turn / 3) & 1u, &given_up, q.ctl, 61)) given_up = 1;
   };
   for (; row < p.N; row += step, ++i) {
     copy_wait<S - 2>();
