@@ -347,9 +347,9 @@ __device__ __forceinline__ void row_moments(const V (&raw)[R][KC], const NormPar
 }
 
 // R rows at a time for each group of p.threads threads, KC vectors a thread and row, S - 1 times as many rows on their way. RMS:
-// neither means nor a bias. bf16 with two streams 65536 x 2048 180 us (0.88 of a copy's rate), 8192 x 4096 49; 4096 x 16384 52;
+// no means; BIAS: room for one. bf16 with two streams 65536 x 2048 180 us (0.88 of a copy's rate), 8192 x 4096 49; 4096 x 16384 52;
 // fp32 8192 x 8192 93. What is left there is the start and the end, 6 us, and the barrier of a turn.
-template <typename T, int KC, int R, int S, bool RMS, bool RES>
+template <typename T, int KC, int R, int S, bool RMS, bool BIAS, bool RES>
 __global__ void __launch_bounds__(512, 1) norm_fwd_ring_kernel(const NormParams p) {
   constexpr int VB = 16 / sizeof(T), C = KC * VB, STREAMS = RES ? 2 : 1;
   using V = Pack<T, VB>;
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(512, 1) norm_fwd_ring_kernel(const NormParams 
   int64_t base = static_cast<int64_t>(blockIdx.x) * groups * R;  // of the CTA: all its threads take part in every sum
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) fetch(i, row0 + i * step);
-  float w[C], b[RMS ? 1 : C], count = 0.f;
+  float w[C], b[BIAS ? C : 1], count = 0.f;
   b[0] = 0.f;
 #pragma unroll
   for (int k = 0; k < KC; ++k) {
@@ -389,12 +389,12 @@ __global__ void __launch_bounds__(512, 1) norm_fwd_ring_kernel(const NormParams 
 #pragma unroll
     for (int j = k * VB; j < (k + 1) * VB; ++j) {
       w[j] = 1.f;
-      if (!RMS) b[j] = 0.f;
+      if (BIAS) b[j] = 0.f;
     }
     if (c < p.d) {
       count += VB;
       if (p.weight != nullptr) load_gain<T, VB>(p.weight, p.gain_f32, c, w + k * VB);
-      if (!RMS && p.bias != nullptr) load_gain<T, VB>(p.bias, p.gain_f32, c, b + k * VB);
+      if (BIAS && p.bias != nullptr) load_gain<T, VB>(p.bias, p.gain_f32, c, b + k * VB);
     }
   }
   if (!RMS) {
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(512, 1) norm_fwd_ring_kernel(const NormParams 
 #pragma unroll
         for (int j = 0; j < VB; j += 2) {
           float2 v = __fmul2_rn(pair(x + j), pair(w + k * VB + j));
-          if (!RMS) v = __fadd2_rn(v, pair(b + k * VB + j));
+          if (BIAS) v = __fadd2_rn(v, pair(b + k * VB + j));
           x[j] = v.x, x[j + 1] = v.y;
         }
         if (live && c < p.d) store<T, VB>(y + c, x);
@@ -1313,15 +1313,15 @@ cudaError_t fwd(NormParams p, cudaStream_t stream) {
   return launch(norm_fwd_kernel<T, VB>, dim3(static_cast<unsigned>(blocks)), cta, 0, stream, false, p);
 }
 
-template <typename T, int KC, int R, int S, bool RMS, bool RES>
+template <typename T, int KC, int R, int S, bool RMS, bool BIAS, bool RES>
 cudaError_t fwd_ring(NormParams p, int sms, cudaStream_t stream) {
   p.threads = round_threads(cdiv64(p.d, 16 / sizeof(T) * KC));
   const int cta = p.threads > 32 ? p.threads : 128, smem = S * (RES ? 2 : 1) * R * KC * 16 * cta;
-  const cudaError_t e = allow_smem<norm_fwd_ring_kernel<T, KC, R, S, RMS, RES>>();
+  const cudaError_t e = allow_smem<norm_fwd_ring_kernel<T, KC, R, S, RMS, BIAS, RES>>();
   if (e != cudaSuccess) return e;
   const int by_smem = kSmemPerSm / (smem + 1536), by_threads = (KC * 16 / sizeof(T) > 8 ? 512 : 768) / cta;
   const int64_t most = static_cast<int64_t>(sms) * (by_smem < by_threads ? by_smem : by_threads);
-  return launch(norm_fwd_ring_kernel<T, KC, R, S, RMS, RES>, dim3(blocks_for(cdiv64(p.N, static_cast<int64_t>(cta / p.threads) * R), most)), cta,
+  return launch(norm_fwd_ring_kernel<T, KC, R, S, RMS, BIAS, RES>, dim3(blocks_for(cdiv64(p.N, static_cast<int64_t>(cta / p.threads) * R), most)), cta,
                 smem, stream, false, p);
 }
 
@@ -1338,12 +1338,12 @@ cudaError_t fwd_odd(NormParams p, int sms, cudaStream_t stream) {
 }
 
 // Eight columns a thread, two rows at a time; of rows of more than 4096 columns 16 or 32 columns, one row at a time.
-template <typename T, bool RMS, bool RES>
+template <typename T, bool RMS, bool BIAS, bool RES>
 cudaError_t fwd_rings(const NormParams& p, int sms, cudaStream_t stream) {
   constexpr int K8 = 8 * sizeof(T) / 16;
-  if (p.d <= 512 * 8) return fwd_ring<T, K8, sizeof(T) == 2 ? 2 : 1, 4, RMS, RES>(p, sms, stream);
-  if (p.d <= 512 * 16) return fwd_ring<T, 2 * K8, 1, RES && sizeof(T) == 4 ? 3 : 4, RMS, RES>(p, sms, stream);
-  return fwd_ring<T, 4 * K8, 1, sizeof(T) == 4 || RES ? 3 : 4, RMS, RES>(p, sms, stream);
+  if (p.d <= 512 * 8) return fwd_ring<T, K8, sizeof(T) == 2 ? 2 : 1, 4, RMS, BIAS, RES>(p, sms, stream);
+  if (p.d <= 512 * 16) return fwd_ring<T, 2 * K8, 1, RES && sizeof(T) == 4 ? 3 : 4, RMS, BIAS, RES>(p, sms, stream);
+  return fwd_ring<T, 4 * K8, 1, sizeof(T) == 4 || RES ? 3 : 4, RMS, BIAS, RES>(p, sms, stream);
 }
 
 template <typename T, int VB>
@@ -1356,8 +1356,9 @@ cudaError_t fwd_cols(const NormParams& p, int sms, cudaStream_t stream) {
   } else {
     if (p.d <= 1024 * VB && p.N <= 4 * sms) return fwd<T, VB>(p, stream);
     if (p.d <= (sizeof(T) == 4 && p.residual ? 512 * 16 : 512 * 32)) {  // what the ring has room for
-      if (p.rms && p.bias == nullptr) return p.residual ? fwd_rings<T, true, true>(p, sms, stream) : fwd_rings<T, true, false>(p, sms, stream);
-      return p.residual ? fwd_rings<T, false, true>(p, sms, stream) : fwd_rings<T, false, false>(p, sms, stream);
+      if (!p.rms) return p.residual ? fwd_rings<T, false, true, true>(p, sms, stream) : fwd_rings<T, false, true, false>(p, sms, stream);
+      if (p.bias == nullptr) return p.residual ? fwd_rings<T, true, false, true>(p, sms, stream) : fwd_rings<T, true, false, false>(p, sms, stream);
+      return p.residual ? fwd_rings<T, true, true, true>(p, sms, stream) : fwd_rings<T, true, true, false>(p, sms, stream);
     }
   }
   return launch(norm_fwd_wide_kernel<T, VB>, dim3(blocks_for(p.N, 2 * static_cast<int64_t>(sms))), 1024, 0, stream, false, p);
