@@ -74,6 +74,9 @@ def orthogonalize(matrices: Union[torch.Tensor, Iterable[torch.Tensor]], steps: 
     for x in tensors:
         y, flipped = _upright(x.detach())
         r = torch.empty(y.shape, dtype=dtype, device=x.device)
+        out.append(r.transpose(-1, -2) if flipped else r)
+        if r.numel() == 0:
+            continue
         kept.append(y)
         rows, cols = y.shape[-2:]
         ld = y.stride(-2) if rows > 1 else cols
@@ -89,7 +92,6 @@ def orthogonalize(matrices: Union[torch.Tensor, Iterable[torch.Tensor]], steps: 
         else:
             fields += (y.data_ptr(), r.data_ptr(), rows, cols, ld)
             count += 1
-        out.append(r.transpose(-1, -2) if flipped else r)
     if count:
         device = tensors[0].device
         table = struct.pack("=" + _lib.ORTH_MATRIX * count, *fields)
