@@ -11,6 +11,7 @@ import struct
 from typing import Iterable, List, Optional, Sequence, Tuple, Union
 
 import torch
+from torch.autograd.forward_ad import unpack_dual
 from torch.autograd.graph import increment_version
 
 from . import _lib
@@ -49,6 +50,18 @@ def _upright(x: torch.Tensor) -> Tuple[torch.Tensor, bool]:
     return x, flipped
 
 
+class _Result(torch.autograd.Function):
+    """A result as a function of its matrix, of which no derivative is implemented."""
+    @staticmethod
+    def forward(ctx, result, matrix):
+        ctx.mark_dirty(result)  # the tensor itself, not a view: it may be written in place
+        return result
+
+    @staticmethod
+    def backward(ctx, g):
+        raise RuntimeError("orthogonalize is not differentiable: detach its matrices or its results")
+
+
 def orthogonalize(matrices: Union[torch.Tensor, Iterable[torch.Tensor]], steps: int = 5,
                   coefficients: Coefficients = COEFFICIENTS, eps: float = 1e-7, dtype: torch.dtype = torch.bfloat16):
     """The matrices with their singular values brought near 1, by ``steps`` Newton-Schulz steps from X = M / (|M| + eps):
@@ -56,14 +69,16 @@ def orthogonalize(matrices: Union[torch.Tensor, Iterable[torch.Tensor]], steps: 
 
     matrices: a list of tensors [..., m, n], all float32, bfloat16 or float16, leading dimensions being a batch of matrices, or
     one such tensor. Rows or columns with unit stride are read in place. Returns contiguous tensors (or one) of ``dtype``,
-    bfloat16 or float16: the products take fp16 numbers, 1e-3 to 2e-3 of the result's norm (up to
-    4e-3 for a single row). coefficients: (a, b, c), or one
-    triple for each step. Not differentiable."""
+    bfloat16 or float16: the products take fp16 numbers, 1e-3 to 2e-3 of the result's norm (up to 4e-3 for a single row).
+    coefficients: (a, b, c), or one triple for each step. Not differentiable: a backward through a result raises, and
+    forward-mode tensors are refused."""
     single = isinstance(matrices, torch.Tensor)
     tensors = [matrices] if single else list(matrices)
     if dtype not in (torch.bfloat16, torch.float16):
         raise ValueError("dtype must be bfloat16 or float16")
     k = _coefficients(coefficients, steps)
+    if any(unpack_dual(x).tangent is not None for x in tensors):
+        raise NotImplementedError("orthogonalize has no forward-mode derivatives")
     for x in tensors:
         if x.dim() < 2 or x.dtype not in _lib.DTYPES or x.dtype != tensors[0].dtype:
             raise ValueError("matrices must be [..., m, n], all float32, all bfloat16 or all float16")
@@ -98,6 +113,8 @@ def orthogonalize(matrices: Union[torch.Tensor, Iterable[torch.Tensor]], steps: 
         ws = _workspace(_lib.hylo_orthogonalize_workspace_bytes(table, count), device)
         _lib.hylo_orthogonalize(table, count, tensors[0].dtype, dtype, k, float(eps), ws, _lib.current_raw_stream(device.index))
     out = [r.contiguous() for r in out]  # a copy of what was read by its columns
+    if torch.is_grad_enabled():
+        out = [_Result.apply(r, x) if x.requires_grad else r for r, x in zip(out, tensors)]
     return out[0] if single else out
 
 
