@@ -18,7 +18,7 @@ struct DeviceState {
   int logits_clusters = 0; // clusters of the logits kernel resident at once
   int pipe_clusters = 0;   // 2-CTA clusters of the pipelined backward resident at once
   int head_clusters = 0;   // 2-CTA clusters of the head log-probability kernel resident at once
-  int muon_clusters = 0;   // 2-CTA clusters of the orthogonalised updates' products resident at once
+  int muon_clusters = 0;   // 2-CTA clusters of the orthogonalised updates' products resident at once, set by the first of them
   TokenOccupancy token;    // of the token log-probability kernels
   unsigned pace_epoch = 0;  // epoch of the last paced fused launch on this device
   int* status = nullptr;

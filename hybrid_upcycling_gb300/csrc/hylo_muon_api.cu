@@ -2,6 +2,7 @@
 // the workspace, the scales of every step, and the launches.
 #include <cmath>
 #include <memory>
+#include <mutex>
 #include <new>
 
 #include "hylo_host.h"
@@ -193,12 +194,29 @@ hylo_status plan_steps(int steps, const double* coefficients, double eps, Steps*
 
 bool aligned_rows(const void* p, int64_t ld, uintptr_t bytes) { return aligned(p, 16) && ld * bytes % 16 == 0; }
 
+// The current device with the products' kernels set up: by the first call that needs them, so that a device on which their clusters do
+// not fit runs everything else.
+hylo_status muon_device(DeviceState** out) {
+  static std::mutex mu;
+  const hylo_status st = current_device(out);
+  if (st != HYLO_OK) return st;
+  std::lock_guard<std::mutex> lock(mu);
+  int& clusters = (*out)->muon_clusters;
+  if (clusters > 0) return HYLO_OK;
+  int n = 0;
+  const cudaError_t e = muon_pipe_prepare(&n);
+  if (e != cudaSuccess) return cuda_fail(e, "set-up of the orthogonalised updates' kernels");
+  if (n < 1) return fail(HYLO_ERR_CUDA, "no thread-block cluster of the orthogonalised updates' kernels fits on the device");
+  clusters = n;
+  return HYLO_OK;
+}
+
 // All launches of one list. dtype: of the matrices or gradients; out_dtype: of the results or parameters.
 template <typename T>
 hylo_status run(const T* list, int count, int dtype, int out_dtype, bool masters, const Steps& s, MuonHyper h, void* ws,
                 cudaStream_t stream) {
   DeviceState* dev = nullptr;
-  hylo_status st = current_device(&dev);
+  hylo_status st = muon_device(&dev);
   if (st != HYLO_OK) return st;
   uint64_t pos = 0;
   h.scale_in = static_cast<float>(s.x[0]);
