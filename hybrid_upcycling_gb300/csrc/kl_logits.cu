@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1) kl_logits_kernel(const LogitsPara
         const size_t n1 = static_cast<size_t>(cl) + static_cast<size_t>(k) * ncl;
         const size_t n2 = n1 - static_cast<size_t>(kLag) * ncl;
         for (int ch = 0; ch < nchunks; ++ch) {
-          if (!wait_bounded(empty + stage, phase ^ 1u, abort_flag, p.ctl, 21)) {
+          if (!wait_bounded(empty + stage, phase ^ 1u, abort_flag, p.ctl, 81)) {
             ok = false;
             break;
           }
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) kl_logits_kernel(const LogitsPara
       if (p2) {  // the values of row k - kLag, published by its merging warp
         const int b2 = (k - kLag) & 1;
         const bool w = wait_bounded(vals_full + b2, static_cast<uint32_t>((k - kLag) >> 1) & 1u, abort_flag,
-                                    p.ctl, 26);
+                                    p.ctl, 86);
         if (!__all_sync(0xffffffffu, w)) break;
         bt = rowvals[b2].bt;
         bs = rowvals[b2].bs;
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1) kl_logits_kernel(const LogitsPara
       RowStats rs{-INFINITY, 0.f, -INFINITY, 0.f, 0.f, 0.f, false};
       uint16_t* dz_row = p2 ? p.dz + static_cast<size_t>(n2) * p.ld : nullptr;
       for (int ch = 0; ch < nchunks; ++ch) {
-        const bool w = wait_bounded(full + stage, phase, abort_flag, p.ctl, 22);
+        const bool w = wait_bounded(full + stage, phase, abort_flag, p.ctl, 82);
         if (!__all_sync(0xffffffffu, w)) {
           ok = false;
           break;
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) kl_logits_kernel(const LogitsPara
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) merge_any(rs, shfl_stats(rs, off), p.c);
       {
-        const bool w = wait_bounded(red_empty + b, use ^ 1u, abort_flag, p.ctl, 23);
+        const bool w = wait_bounded(red_empty + b, use ^ 1u, abort_flag, p.ctl, 83);
         if (!__all_sync(0xffffffffu, w)) break;
       }
       if (lane == 0) {
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) kl_logits_kernel(const LogitsPara
       if (warp != k % kConsumerWarps) continue;
       // ---- merging warp of row n1
       {
-        const bool w = wait_bounded(red_full + b, use, abort_flag, p.ctl, 24);
+        const bool w = wait_bounded(red_full + b, use, abort_flag, p.ctl, 84);
         if (!__all_sync(0xffffffffu, w)) break;
       }
       RowStats r = lane < kConsumerWarps ? warp_stats[b * kConsumerWarps + lane]
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) kl_logits_kernel(const LogitsPara
       r = bcast_stats(r);  // lane 0's merge order, the same bits in every lane
       // this CTA's slot b in every peer must have been read (row k - 2) before it is rewritten
       {
-        const bool w = wait_bounded<true>(xempty + b, use ^ 1u, abort_flag, p.ctl, 25);
+        const bool w = wait_bounded<true>(xempty + b, use ^ 1u, abort_flag, p.ctl, 85);
         if (!__all_sync(0xffffffffu, w)) break;
       }
       if (lane < kSplit) {  // lane j hands this slice's statistics to CTA j of the cluster
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) kl_logits_kernel(const LogitsPara
         mbar_arrive_remote(mapa_shared(smem_u32(xfull + b), lane));
       }
       {
-        const bool w = wait_bounded<true>(xfull + b, use, abort_flag, p.ctl, 27);
+        const bool w = wait_bounded<true>(xfull + b, use, abort_flag, p.ctl, 87);
         if (!__all_sync(0xffffffffu, w)) break;
       }
       RowStats m{-INFINITY, 0.f, -INFINITY, 0.f, 0.f, 0.f, false};

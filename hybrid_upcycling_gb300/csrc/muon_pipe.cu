@@ -172,7 +172,7 @@ __device__ __forceinline__ bool wait_count(const unsigned* ctr, unsigned target,
       if (*abort_flag) return false;
       if (globaltimer_ns() - t0 > ctl.limit_ns) {
         *abort_flag = 1;
-        atomicCAS(ctl.status, 0, kDevTimeoutBase + 41);
+        atomicCAS(ctl.status, 0, kDevTimeoutBase + 71);
         return false;
       }
     }
@@ -447,7 +447,7 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
       for (int k = 0;; ++k) {
         const int slot = k % kItemDepth;
         const uint32_t par = static_cast<uint32_t>(k / kItemDepth) & 1u;
-        if (!wait_bounded<true>(iempty + slot, par ^ 1u, abort_flag, p.ctl, 42)) break;
+        if (!wait_bounded<true>(iempty + slot, par ^ 1u, abort_flag, p.ctl, 72)) break;
         const Item it = item_at<SPLIT>(tab, p, atomicAdd(p.ctrl, 1u));
         if (it.product >= 0 && !wait_count(p.ctrl + 1 + it.mat, it.need, abort_flag, p.ctl)) break;
         items[slot] = it;
@@ -468,7 +468,7 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
       for (int k = 0; ok; ++k) {
         const int slot = k % kItemDepth;
         const uint32_t par = static_cast<uint32_t>(k / kItemDepth) & 1u;
-        if (!wait_bounded<true>(ifull + slot, par, abort_flag, p.ctl, 43)) break;
+        if (!wait_bounded<true>(ifull + slot, par, abort_flag, p.ctl, 73)) break;
         const Item it = items[slot];
         if (rank == 0)
           mbar_arrive(iempty + slot);
@@ -484,7 +484,7 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
         const int arow = it.i * 256 + static_cast<int>(rank) * kBM, brow = it.j * 256 + (it.half < 0 ? static_cast<int>(rank) * kBM : it.half * 128 + static_cast<int>(rank) * 64);
         const uint32_t bytes = it.half < 0 ? 2u * STAGE_BYTES : 2u * (A_BYTES + A_BYTES / 2);  // both CTAs'
         for (int kb = range.first; kb < range.end; ++kb) {
-          if (!wait_bounded(empty + stage, phase ^ 1u, abort_flag, p.ctl, 44)) {
+          if (!wait_bounded(empty + stage, phase ^ 1u, abort_flag, p.ctl, 74)) {
             ok = false;
             break;
           }
@@ -518,7 +518,7 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
       for (int k = 0; ok; ++k) {
         const int slot = k % kItemDepth;
         const uint32_t par = static_cast<uint32_t>(k / kItemDepth) & 1u;
-        if (!wait_bounded(ifull + slot, par, abort_flag, p.ctl, 45)) {
+        if (!wait_bounded(ifull + slot, par, abort_flag, p.ctl, 75)) {
           ok = false;
           break;
         }
@@ -528,14 +528,14 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
         const Range range = kblocks<SPLIT>(tab.t[it.mat], it);
         const uint32_t idesc0 = idesc_f16_f32(2 * kBM, it.half < 0 ? 256 : 128);
         for (int from = range.first; ok && from < range.end; from += kMuonDepth) {
-          if (!wait_bounded(tempty + h, (uses[h] & 1u) ^ 1u, abort_flag, p.ctl, 46)) {
+          if (!wait_bounded(tempty + h, (uses[h] & 1u) ^ 1u, abort_flag, p.ctl, 76)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t d = tmem_base + static_cast<uint32_t>(h * 256);
           for (int kb = from; kb < min(range.end, from + kMuonDepth); ++kb) {
-            if (!wait_bounded(full + stage, phase, abort_flag, p.ctl, 47)) {
+            if (!wait_bounded(full + stage, phase, abort_flag, p.ctl, 77)) {
               ok = false;
               break;
             }
@@ -580,7 +580,7 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
     for (int k = 0;; ++k) {
       const int slot = k % kItemDepth;
       const uint32_t par = static_cast<uint32_t>(k / kItemDepth) & 1u;
-      bool got = wait_bounded<true>(ifull + slot, par, abort_flag, p.ctl, 48);
+      bool got = wait_bounded<true>(ifull + slot, par, abort_flag, p.ctl, 78);
       if (!__all_sync(0xffffffffu, got)) break;
       const Item it = items[slot];
       __syncwarp();
@@ -632,7 +632,7 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
       if (deep) scratch = reinterpret_cast<float4*>(p.scratch + static_cast<size_t>(blockIdx.x) * kMuonScratch + static_cast<size_t>(e) * (kMuonScratch / kEpiWarps)) + lane;
       const uint32_t lanes = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
       for (int from = 0; from + kMuonDepth < nk; from += kMuonDepth) {
-        got = __all_sync(0xffffffffu, wait_bounded(tfull + h, uses[h] & 1u, abort_flag, p.ctl, 49));
+        got = __all_sync(0xffffffffu, wait_bounded(tfull + h, uses[h] & 1u, abort_flag, p.ctl, 79));
         if (!got) break;
         tc_fence_after();
         for (int c = 0; c < units; ++c) {
@@ -656,7 +656,7 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
         h ^= 1;
       }
       if (!got) break;
-      got = wait_bounded(tfull + h, uses[h] & 1u, abort_flag, p.ctl, 50);
+      got = wait_bounded(tfull + h, uses[h] & 1u, abort_flag, p.ctl, 80);
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after();
       // A part of a split sum goes to the workspace; the warp that comes last adds all parts up, in their order.

@@ -111,7 +111,8 @@ enum : int { kDevTimeoutBase = 0x1000 };
 
 // Waits until the phase with parity `parity` of `bar` has completed. Returns false if the
 // CTA's abort flag is raised or the time limit passes (then it raises the flag itself and
-// records kDevTimeoutBase + site in the status word).
+// records kDevTimeoutBase + site in the status word). A site names its source file: kl_fused.cu has those from 1 on,
+// kl_bwd_pipe.cu from 21, head_logprobs.cu 41, norm.cu 61, muon_pipe.cu 71, kl_logits.cu 81, the self-test 99.
 // kClusterAcquire: wait with cluster-scope acquire (see mbar_try_wait_cluster).
 template <bool kClusterAcquire = false>
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
