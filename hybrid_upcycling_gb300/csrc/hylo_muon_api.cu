@@ -108,10 +108,10 @@ Group next_group(const T* list, int count, int first) {
   return g;
 }
 
-// Whether the upper triangles' products are done sooner by halves of tiles, 296 cycles for a 64-deep block, than by whole ones, 500:
-// by the longest item and by all of them shared out. (5003 x 520, 1000 x 1001 and 8192 x 2048 together 612 us with whole tiles, 560
-// so. Apply, whose epilogue is as long as its products, gains only where every cluster has one half: one 2048 x 2048 221 us, 227
-// with its 64 tiles halved.)
+// Whether the upper triangles' products are done sooner by halves of tiles, 296 cycles for a 64-deep block, than by whole ones, 512
+// (the tensor cores' rate; 517 over the 128 blocks of a 2048 x 8192 matrix's items): by the longest item and by all of them shared
+// out. (5003 x 520, 1000 x 1001 and 8192 x 2048 together 612 us with whole tiles, 560 so. Apply, whose epilogue is as long as its
+// products, gains only where every cluster has one half: one 2048 x 2048 221 us, 227 with its 64 tiles halved.)
 bool halves_are_sooner(const MuonTable& tab, int64_t clusters, int MuonMat::*depth) {
   int64_t longest = 0, work = 0;
   for (int i = 0; i < tab.count; ++i) {
@@ -120,7 +120,7 @@ bool halves_are_sooner(const MuonTable& tab, int64_t clusters, int MuonMat::*dep
     work += static_cast<int64_t>(t.mt) * (t.mt + 1) / 2 * (t.*depth);
   }
   longest *= clusters;
-  return 296 * (longest > 2 * work ? longest : 2 * work) < 500 * (longest > work ? longest : work);
+  return 296 * (longest > 2 * work ? longest : 2 * work) < 512 * (longest > work ? longest : work);
 }
 
 template <typename T>

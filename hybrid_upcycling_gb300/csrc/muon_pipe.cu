@@ -20,7 +20,7 @@
 // what it overwrites is no longer read. With several matrices the tail of one's product is filled with the next one's items;
 // every item waits for earlier ones only, which running CTAs hold, so the launch cannot deadlock whatever the residency. Where whole
 // tiles of a product would leave clusters idle, items are 256 x 128 and take little more than half as long, 296 cycles for a 64-deep
-// block, a whole tile's 500 to 590. (Eight stages of their size instead of six: the same or slower.)
+// block, a whole tile's 512 (the tensor cores' rate) to 590. (Eight stages of their size instead of six: the same or slower.)
 //
 // Long sums of few items of Gram are split among items of their own; their fp32 parts meet in the workspace, and each warp of the
 // epilogue that finds all parts of its 32 rows there adds them up in a fixed order.
@@ -32,8 +32,8 @@
 // long; parts through shared memory by TMA are as fast as this where there is much to do and slower where there is little.)
 //
 // What bounds it: the tensor cores, at the clock that the power cap leaves. Four 2048 x 8192 matrices 1.38 ms, the tensor pipe 85 %
-// active; an Apply item of K = 2048 19 000 cycles (16 400 at the tensor cores' rate), its epilogue 16 000 beside the next one's
-// products. One 2048 x 2048: 0.22 ms, each product a chain of queue, copies, products and epilogue.
+// active; an item of Gram, K = 8192, 66 200 cycles (65 500 at the tensor cores' rate), one of Apply, K = 2048, 17 800 (16 400), its epilogue
+// 11 500 beside the next one's products. One 2048 x 2048: 0.22 ms, each product a chain of queue, copies, products and epilogue.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
