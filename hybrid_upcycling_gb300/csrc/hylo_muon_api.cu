@@ -59,7 +59,7 @@ int64_t rows_of(const Shape& s) { return 3 * s.x_rows + 2 * s.a_rows; }
 // The sum of an item of Gram (K = n) is split where the group has so few that clusters would be idle beside a long one. A 64-deep
 // k-block takes 550 cycles and a part 3500 to be written, read and added, so sqrt(n / 64 / 6.4) parts. bf16, without and with:
 // 256 x 16384 512 and 292 us, 2048 x 8192 619 and 588, 1 x 100000 2.38 ms and 0.48; sums half as long are even (1024 x 4096 292
-// and 299).
+// and 299). The clusters are those of a whole GPU: the workspace's size may not depend on the device.
 constexpr int64_t kSplitClusters = 76, kSplitFrom = 128, kMaxSplits = 64;
 int64_t splits_of(const Shape& s, int64_t group_tiles) {
   const int64_t kn = cdiv(s.n, 64), room = kSplitClusters / group_tiles;

@@ -740,7 +740,7 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
         }
         if (last) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {  // as fp16, like every X
+          for (int j = 0; j < 16; ++j) {  // O as orthogonalize gives it in fp16, in every type: 1e-4 of its norm beside the products' 1e-3
             const float2 f = unpack_f16x2(w[j]);
             v[2 * j] = f.x * hyper.unscale;
             v[2 * j + 1] = f.y * hyper.unscale;

@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(512, 1) norm_fwd_ring_kernel(const NormParams 
 // memory into the ring, shifted by the row's start modulo 16, and are taken apart there: a warp has 32 C consecutive columns, a lane
 // every 32nd of them (fewer lanes where a row takes part of a warp), so that a warp reads and writes consecutive elements. What these
 // kernels cost is instructions: warps whose columns all exist go without a test for each (51 instructions an element with them).
-// 65536 x 1001 bf16 110 us forward and 138 backward, fp32 128 and 156 (0.60 and 0.74 of a copy's rate). A vector's bytes in front
+// 65536 x 1001 bf16 110 us forward and 138 backward (0.35 and 0.42 of a copy's rate), fp32 128 and 156 (0.60 and 0.74). A vector's bytes in front
 // of or behind the row belong to the same tensor, except in front of its first element and behind its last one, which are not read.
 struct OddRows {
   uintptr_t base, end;  // of the tensor
@@ -1022,7 +1022,7 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_ring_kernel(const NormParams 
 // for those of row i - 1, which the CTAs have sent one another meanwhile; the sending of row i's; dx of row i - 1. The sums
 // arrive with st.async, counted on a barrier of the CTA that receives them (a cluster barrier a turn took twice as long). Three
 // places for them are enough: a CTA sends row i + 3's only after it has this CTA's of row i + 2, sent after all here were done with
-// row i's. bf16 16384 x 5120 90 us (0.82 of a copy's rate), 4096 x 16384 87; fp32 8192 x 8192 141.
+// row i's. bf16 16384 x 5120 90 us (0.82 of a copy's rate), 4096 x 16384 87; fp32 8192 x 8192 141, 8192 x 16384 496 (0.48: an exchange a row, 38 rows at a time).
 __device__ __forceinline__ void send_pair(uint32_t to, float a, float b, uint32_t bar) {
   asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];"
                :: "r"(to), "r"(__float_as_uint(a)), "r"(__float_as_uint(b)), "r"(bar) : "memory");

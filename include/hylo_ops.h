@@ -163,7 +163,8 @@ hylo_status hylo_adamw_step(const hylo_adamw_tensor* tensors, int count, int par
  * contiguous. weight, bias: [d] or NULL (1 and 0), both of gain_dtype, which is dtype or HYLO_F32. All element-aligned; rows of
  * 16-byte vectors are fastest. sum receives s and is required with a residual (NULL without). stats [N, 2] receives (mu, r),
  * which the backward reads, or is NULL. y and sum may not overlap the inputs or each other. 1 <= N <= 2^31 - 1,
- * 1 <= d <= 2^20, eps finite and >= 0. Statistics are fp32: where mean((s - mu)^2) exceeds fp32's range the row's y is that of r = 0.
+ * 1 <= d <= 2^20, eps finite and >= 0. Statistics are fp32: where mean((s - mu)^2) exceeds fp32's range the row's y is that of r = 0
+ * (RMS norm of a row with infinite elements: NaN there, 0 elsewhere; a NaN makes the row NaN).
  * With eps = 0 a row without deviation has r infinite, and NaN. Deterministic. */
 hylo_status hylo_norm(const void* x, const void* residual, int dtype, int64_t N, int64_t d, int64_t ldx, int64_t ldr,
                       const void* weight, const void* bias, int gain_dtype, int rms, double eps, void* sum, void* y,
@@ -195,8 +196,9 @@ hylo_status hylo_norm_backward(const void* s, int dtype, int64_t N, int64_t d, i
  * (0 for invalid sizes; 6 bytes per element and 4 per element of A, padded, for matrices of together 1 GiB or one larger
  * one, and parts of long sums), not shared with a call still running on another stream.
  * Accuracy: products of fp16 numbers scaled by powers of two, fp32 sums, X as two fp16 terms where it is added: 1e-3 to 2e-3 of
- * the result's norm after five steps with the usual coefficients, up to 4e-3 where few singular values share it (one row). Deterministic: the same list gives the same bits (with other
- * matrices in the list, the sums of a matrix with a side of more than 8128 may be added up in another order). */
+ * the result's norm after five steps with the usual coefficients, up to 4e-3 where few singular values share it (one row).
+ * Deterministic: the same list gives the same bits (with other matrices in the list, the sums of a matrix with a side of more
+ * than 8128 may be added up in another order). */
 typedef struct {
   const void* x;
   void* out;
@@ -210,7 +212,7 @@ hylo_status hylo_orthogonalize(const hylo_orth_matrix* matrices, int count, int 
 /* One Muon step over `count` matrices (HOST array, not kept), all contiguous:
  *     g' = g * grad_scale * c,  c = min(1, max_norm / (norm[0] * |grad_scale| + 1e-6))  (1 without norm)
  *     m <- momentum m + (1 - momentum) g',   u = momentum m + (1 - momentum) g' (nesterov != 0) or m
- *     w <- w (1 - lr weight_decay) - lr scale O(u),   O as in hylo_orthogonalize (its accuracy is that of the step)
+ *     w <- w (1 - lr weight_decay) - lr scale O(u),   O as in hylo_orthogonalize, in fp16 (its accuracy is that of the step)
  * param, grad, master, momentum: as param, grad, master and m of hylo_adamw_step with 32-bit states, with the same rules for
  * masters, for overlaps (HYLO_ERR_DIM), for a norm that is not finite (nothing is written) and for capture (HYLO_ERR_CAPTURE),
  * and the same random bits where a bf16 param without master is rounded. Sizes, steps, coefficients, eps and workspace
