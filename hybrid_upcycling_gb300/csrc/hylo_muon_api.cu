@@ -33,7 +33,9 @@ struct Item {
   int64_t rows, cols, ld;
   double decay, step;
 };
-Item item_of(const hylo_orth_matrix& x) { return Item{x.x, x.out, nullptr, nullptr, x.rows, x.cols, x.rows == 1 ? x.cols : x.ld, 1.0, 0.0}; }
+Item item_of(const hylo_orth_matrix& x) {
+  return Item{x.x, x.out, nullptr, nullptr, x.rows, x.cols, x.rows == 1 ? x.cols : x.ld, 1.0, 0.0};
+}
 Item item_of(const hylo_muon_tensor& x) {
   return Item{x.grad, x.param, x.master, x.momentum, x.rows, x.cols, x.cols, 1.0 - x.lr * x.weight_decay, x.lr * x.scale};
 }
@@ -394,7 +396,8 @@ hylo_status hylo_muon_step(const hylo_muon_tensor* tensors, int count, int param
     if ((t.master != nullptr) != (tensors[some].master != nullptr) || (t.master && param_dtype == HYLO_F32))
       return fail(HYLO_ERR_DIM, "tensor %d: masters go with bf16 parameters, for all tensors or none", i);
     if (!t.param || !t.grad || !t.momentum) return fail(HYLO_ERR_NULL, "a required pointer of tensor %d is NULL", i);
-    if (!aligned(t.param, bytes_of(param_dtype)) || !aligned(t.grad, bytes_of(grad_dtype)) || !aligned(t.master, 4) || !aligned(t.momentum, 4))
+    if (!aligned(t.param, bytes_of(param_dtype)) || !aligned(t.grad, bytes_of(grad_dtype)) || !aligned(t.master, 4) ||
+        !aligned(t.momentum, 4))
       return fail(HYLO_ERR_ALIGN, "tensor %d is not element-aligned", i);
     const uintptr_t k = static_cast<uintptr_t>(t.rows) * t.cols;
     add_span(spans.get(), &n, t.param, k * bytes_of(param_dtype), true, i);
@@ -412,7 +415,8 @@ hylo_status hylo_muon_step(const hylo_muon_tensor* tensors, int count, int param
   const cudaError_t asked = cudaStreamIsCapturing(stream, &capture);
   if (asked != cudaSuccess) return cuda_fail(asked, "ask whether the stream is being captured");
   if (capture != cudaStreamCaptureStatusNone)
-    return fail(HYLO_ERR_CAPTURE, "a Muon step may not be captured: its learning rates and seed are host values that every replay would repeat");
+    return fail(HYLO_ERR_CAPTURE,
+                "a Muon step may not be captured: its learning rates and seed are host values that every replay would repeat");
   MuonHyper h{};
   h.muon = 1;
   h.nesterov = nesterov != 0;

@@ -507,7 +507,8 @@ hylo_status hylo_norm(const void* x, const void* residual, int dtype, int64_t N,
   if (!(eps >= 0) || !std::isfinite(static_cast<float>(eps))) return fail(HYLO_ERR_TAU, "eps must be finite and >= 0");
   const uintptr_t rows = span(N, d, d, e);
   const Range out[] = {{sum, rows}, {y, rows}, {stats, static_cast<uintptr_t>(N) * 8}};
-  const Range in[] = {{x, span(N, d, ldx, e)}, {residual, span(N, d, ldr, e)}, {weight, d * dtype_bytes(gain_dtype)}, {bias, d * dtype_bytes(gain_dtype)}};
+  const uintptr_t gain = d * dtype_bytes(gain_dtype);
+  const Range in[] = {{x, span(N, d, ldx, e)}, {residual, span(N, d, ldr, e)}, {weight, gain}, {bias, gain}};
   if ((st = check_disjoint(out, in)) != HYLO_OK) return st;
   DeviceState* dev = nullptr;
   if ((st = current_device(&dev)) != HYLO_OK) return st;
@@ -537,7 +538,8 @@ hylo_status hylo_norm_backward(const void* s, int dtype, int64_t N, int64_t d, i
   if (workspace_bytes < need)
     return fail(HYLO_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu required", workspace_bytes, need);
   const Range out[] = {{dx, span(N, d, d, e)}, {dweight, d * ge}, {dbias, d * ge}, {columns ? workspace : nullptr, need}};
-  const Range in[] = {{s, span(N, d, lds, e)}, {dy, span(N, d, lddy, e)}, {dsum, span(N, d, ldds, e)}, {weight, d * ge}, {stats, static_cast<uintptr_t>(N) * 8}};
+  const Range in[] = {{s, span(N, d, lds, e)}, {dy, span(N, d, lddy, e)}, {dsum, span(N, d, ldds, e)}, {weight, d * ge},
+                      {stats, static_cast<uintptr_t>(N) * 8}};
   if ((st = check_disjoint(out, in)) != HYLO_OK) return st;
   DeviceState* dev = nullptr;
   if ((st = current_device(&dev)) != HYLO_OK) return st;
@@ -545,8 +547,8 @@ hylo_status hylo_norm_backward(const void* s, int dtype, int64_t N, int64_t d, i
   NormParams p{};
   p.x = s, p.ldx = lds, p.N = N, p.d = static_cast<int>(d), p.rms = rms != 0, p.weight = weight, p.gain_f32 = gain_dtype == HYLO_F32;
   p.stats = reinterpret_cast<float2*>(const_cast<float*>(stats));
-  const NormGrad q{dy, dsum, lddy, ldds, dx, columns ? static_cast<float*>(workspace) : nullptr, dweight != nullptr, dbias != nullptr, dweight, dbias, 0,
-                   WaitCtl{dev->status, wait_limit_ns()}};
+  const NormGrad q{dy, dsum, lddy, ldds, dx, columns ? static_cast<float*>(workspace) : nullptr, dweight != nullptr,
+                   dbias != nullptr, dweight, dbias, 0, WaitCtl{dev->status, wait_limit_ns()}};
   const cudaError_t err = launch_norm_bwd(p, q, dtype, norm_parts(N, p.d), dev->sms, stream);
   return err == cudaSuccess ? HYLO_OK : cuda_fail(err, "launch norm backward");
 }

@@ -204,8 +204,8 @@ __device__ __forceinline__ void put_x(const MuonHyper& h, const MuonMat& t, int 
   *reinterpret_cast<uint4*>(h.ws + static_cast<size_t>(t.lo) * 128 + sector * 32 + (c & 8) * 2) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
 }
 
-// X's panels from the scaled update, padded with zeros to whole k-blocks: 64 x 64 blocks of the matrix, h.fill_blocks a thread block along its
-// rows; a tall matrix is transposed through shared memory.
+// X's panels from the scaled update, padded with zeros to whole k-blocks: 64 x 64 blocks of the matrix, h.fill_blocks a thread block
+// along its rows; a tall matrix is transposed through shared memory.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) muon_fill_kernel(const __grid_constant__ MuonTable tab, const MuonHyper h) {
   __shared__ float red[kMuonSums * (kThreads / 32)];

@@ -32,8 +32,8 @@
 // long; parts through shared memory by TMA are as fast as this where there is much to do and slower where there is little.)
 //
 // What bounds it: the tensor cores, at the clock that the power cap leaves. Four 2048 x 8192 matrices 1.38 ms, the tensor pipe 85 %
-// active; an item of Gram, K = 8192, 66 200 cycles (65 500 at the tensor cores' rate), one of Apply, K = 2048, 17 800 (16 400), its epilogue
-// 11 500 beside the next one's products. One 2048 x 2048: 0.22 ms, each product a chain of queue, copies, products and epilogue.
+// active; an item of Gram, K = 8192, 66 200 cycles (65 500 at the tensor cores' rate), one of Apply, K = 2048, 17 800 (16 400), its
+// epilogue 11 500 beside the next one's products. One 2048 x 2048: 0.22 ms, each product a chain of queue, copies, products and epilogue.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -121,7 +121,8 @@ __device__ __forceinline__ Item item_at(const MuonTable& tab, const MuonPipe& p,
     it.j = j;
     it.i = local - j * (j + 1) / 2;
   }
-  const unsigned sym = static_cast<unsigned>(m.mt * (m.mt + 1) / 2), gram = (SPLIT ? sym * static_cast<unsigned>(m.splits) : sym) << p.half[0], poly = sym << p.half[1];
+  const unsigned sym = static_cast<unsigned>(m.mt * (m.mt + 1) / 2), poly = sym << p.half[1];
+  const unsigned gram = (SPLIT ? sym * static_cast<unsigned>(m.splits) : sym) << p.half[0];
   const unsigned all = gram + poly + (static_cast<unsigned>(m.mt * m.nt) << p.half[2]);
   it.need = kDone * (static_cast<unsigned>(it.step) * all + (it.product == kMuonGram ? 0u : it.product == kMuonPoly ? gram : gram + poly));
   return it;
@@ -135,7 +136,8 @@ template <bool SPLIT>
 __device__ __forceinline__ Range kblocks(const MuonMat& m, const Item& it) {
   if (it.product != kMuonGram) return Range{0, m.km};
   if (!SPLIT || m.splits == 1) return Range{0, m.kn};
-  return Range{static_cast<int>(static_cast<int64_t>(m.kn) * it.part / m.splits), static_cast<int>(static_cast<int64_t>(m.kn) * (it.part + 1) / m.splits)};
+  const int64_t kn = m.kn;
+  return Range{static_cast<int>(kn * it.part / m.splits), static_cast<int>(kn * (it.part + 1) / m.splits)};
 }
 // Whether k-block kb of an operand of Poly or Apply comes from its mirror image: it lies left of 256-row tile `tile`.
 __device__ __forceinline__ bool mirrored(int kb, int tile) { return (kb >> 2) < tile; }
@@ -179,8 +181,8 @@ __device__ __forceinline__ bool wait_count(const unsigned* ctr, unsigned target,
   }
 }
 
-// 128 rows (64 unless `both`) from `row` on and 64 columns from 64 kb on of a matrix whose panels have mp rows. mirror: the block is stored as
-// its mirror image, 64 rows from 64 kb on and the columns `row`, ..., and arrives in MN-major order.
+// 128 rows (64 unless `both`) from `row` on and 64 columns from 64 kb on of a matrix whose panels have mp rows. mirror: the block is
+// stored as its mirror image, 64 rows from 64 kb on and the columns `row`, ..., and arrives in MN-major order.
 __device__ __forceinline__ void load_rows(uint8_t* dst, const CUtensorMap* map, uint32_t bar, uint32_t base, int mp, int row, int kb,
                                           bool mirror, bool both) {
   const int at = static_cast<int>(base) + (mirror ? row / 64 * mp + kb * 64 : kb * mp + row), next = mirror ? mp : 64;
@@ -217,10 +219,12 @@ __device__ __forceinline__ float ld_shared_f32(uint32_t a) {
 // Stores where `ok`, as one predicated access: behind a branch goes what is stored too, one element's work after another's (a bf16
 // item of a tall matrix 32 800 cycles, so 28 900).
 __device__ __forceinline__ void store_if(bool ok, uint16_t* p, uint32_t v) {
-  asm volatile("{ .reg .pred q; setp.ne.u32 q, %2, 0; @q st.global.u16 [%0], %1; }" :: "l"(p), "h"(static_cast<uint16_t>(v)), "r"(static_cast<uint32_t>(ok)) : "memory");
+  asm volatile("{ .reg .pred q; setp.ne.u32 q, %2, 0; @q st.global.u16 [%0], %1; }"
+               :: "l"(p), "h"(static_cast<uint16_t>(v)), "r"(static_cast<uint32_t>(ok)) : "memory");
 }
 __device__ __forceinline__ void store_if(bool ok, float* p, float v) {
-  asm volatile("{ .reg .pred q; setp.ne.u32 q, %2, 0; @q st.global.f32 [%0], %1; }" :: "l"(p), "f"(v), "r"(static_cast<uint32_t>(ok)) : "memory");
+  asm volatile("{ .reg .pred q; setp.ne.u32 q, %2, 0; @q st.global.f32 [%0], %1; }"
+               :: "l"(p), "f"(v), "r"(static_cast<uint32_t>(ok)) : "memory");
 }
 __device__ __forceinline__ void store_if(bool ok, uint16_t* p, uint2 v) {
   asm volatile("{ .reg .pred q; setp.ne.u32 q, %3, 0; @q st.global.v2.b32 [%0], {%1, %2}; }"
@@ -285,7 +289,8 @@ __device__ __forceinline__ const Stored<OUT>* old_values(const MuonMat& m) {
 }
 
 // Asks for the old values of 32 rows and 32 `units` columns. (Without this, with a branch around each element's step and a hash more for it
-// an item of the last product took 58 000 cycles in bf16 and 34 000 with masters; now 23 500 and 20 000, beside 15 000 to 19 000 for the products.)
+// an item of the last product took 58 000 cycles in bf16 and 34 000 with masters; now 23 500 and 20 000, beside 15 000 to 19 000 for the
+// products.)
 template <int OUT>
 __device__ __forceinline__ void prefetch_old(const MuonMat& m, int row, int col, int units, int lane) {
   constexpr int LINE = 128 / sizeof(Stored<OUT>);
@@ -334,8 +339,8 @@ template <int OUT>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) { return OUT == kMuonOutF16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi); }
 
 template <int OUT>
-__device__ __forceinline__ void finish_part(const MuonMat& m, uint32_t seed, const Place& at, int lane, uint32_t staging, const uint32_t (&w)[32],
-                                            float (&o)[32]) {
+__device__ __forceinline__ void finish_part(const MuonMat& m, uint32_t seed, const Place& at, int lane, uint32_t staging,
+                                            const uint32_t (&w)[32], float (&o)[32]) {
   const RandomKeys keys(seed, m.pos + static_cast<uint64_t>(at.e));
   float* f = (OUT == kMuonParamF32 ? static_cast<float*>(m.dst) : m.master) + at.e;  // written unless the results have 16 bits
   uint16_t* d = static_cast<uint16_t*>(m.dst) + at.e;                                // written unless OUT is kMuonParamF32
@@ -481,7 +486,8 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
         const Range range = kblocks<SPLIT>(m, it);
         const uint32_t abase = it.product == kMuonGram ? m.x[cur] : it.product == kMuonPoly ? m.a : m.b;
         const uint32_t bbase = it.product == kMuonPoly ? m.a : m.x[cur];
-        const int arow = it.i * 256 + static_cast<int>(rank) * kBM, brow = it.j * 256 + (it.half < 0 ? static_cast<int>(rank) * kBM : it.half * 128 + static_cast<int>(rank) * 64);
+        const int pair = static_cast<int>(rank), arow = it.i * 256 + pair * kBM;
+        const int brow = it.j * 256 + (it.half < 0 ? pair * kBM : it.half * 128 + pair * 64);
         const uint32_t bytes = it.half < 0 ? 2u * STAGE_BYTES : 2u * (A_BYTES + A_BYTES / 2);  // both CTAs'
         for (int kb = range.first; kb < range.end; ++kb) {
           if (!wait_bounded(empty + stage, phase ^ 1u, abort_flag, p.ctl, 74)) {
@@ -496,8 +502,8 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
           }
           load_rows(sa, &map, fb, abase, mp, arow, kb, it.product != kMuonGram && mirrored(kb, it.i), true);
           // B of Apply is X, 64 of its rows and this CTA's columns, which lie like a mirror image's
-          load_rows(sa + A_BYTES, &map, fb, bbase, mp, brow, kb, it.product == kMuonApply || (it.product == kMuonPoly && mirrored(kb, it.j)),
-                    it.half < 0);
+          load_rows(sa + A_BYTES, &map, fb, bbase, mp, brow, kb,
+                    it.product == kMuonApply || (it.product == kMuonPoly && mirrored(kb, it.j)), it.half < 0);
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -605,7 +611,9 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
       const int wide = (apply ? m.kn : m.km) * 64 - col0;
       int nu = row >= m.km * 64 || wide <= 0 ? 0 : wide >= 32 * units ? units : wide / 32;
       // X's second term, which only the epilogue of the same tile reads again, lies in the order of its lanes.
-      uint8_t* lo = hyper.ws + static_cast<size_t>(m.lo) * 128 + (muon_lo_sector(it.j * m.mt + it.i, static_cast<int>(rank), q + (col0 >> 7 & 1) * 4) + (col0 >> 5 & 3) * 64 + lane) * 32;
+      const int64_t sector =
+          muon_lo_sector(it.j * m.mt + it.i, static_cast<int>(rank), q + (col0 >> 7 & 1) * 4) + (col0 >> 5 & 3) * 64 + lane;
+      uint8_t* lo = hyper.ws + static_cast<size_t>(m.lo) * 128 + sector * 32;
       auto part = [&](uint32_t base, int u) {  // this lane's row of part u
         return hyper.ws + (static_cast<size_t>(base) + static_cast<size_t>(col0 / 64 + u / 2) * mp + row + lane) * 128 + (u & 1) * 64;
       };
@@ -629,7 +637,9 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
       // Of a long sum all but the last stretch, added up in the workspace: [kUnits][8][32 lanes] of this warp.
       const bool deep = nk > kMuonDepth;
       float4* scratch = nullptr;
-      if (deep) scratch = reinterpret_cast<float4*>(p.scratch + static_cast<size_t>(blockIdx.x) * kMuonScratch + static_cast<size_t>(e) * (kMuonScratch / kEpiWarps)) + lane;
+      if (deep)
+        scratch = reinterpret_cast<float4*>(p.scratch + blockIdx.x * static_cast<size_t>(kMuonScratch) +
+                                            static_cast<size_t>(e) * (kMuonScratch / kEpiWarps)) + lane;
       const uint32_t lanes = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
       for (int from = 0; from + kMuonDepth < nk; from += kMuonDepth) {
         got = __all_sync(0xffffffffu, wait_bounded(tfull + h, uses[h] & 1u, abort_flag, p.ctl, 79));
@@ -663,7 +673,8 @@ muon_pipe_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
       const float4* all = nullptr;  // this lane's place in the first part
       if (SPLIT && it.product == kMuonGram && m.splits > 1 && nu > 0) {
         const int tile = it.j * (it.j + 1) / 2 + it.i;
-        uint8_t* at = p.parts + ((static_cast<size_t>(m.part0) + static_cast<size_t>(tile) * m.splits) * 2 + rank) * kMuonScratch + e * (kMuonScratch / kEpiWarps);
+        uint8_t* at = p.parts + ((static_cast<size_t>(m.part0) + static_cast<size_t>(tile) * m.splits) * 2 + rank) * kMuonScratch +
+                      e * (kMuonScratch / kEpiWarps);
         float4* own = reinterpret_cast<float4*>(at + static_cast<size_t>(it.part) * 2 * kMuonScratch) + lane;
         all = reinterpret_cast<const float4*>(at) + lane;
         for (int u = 0; u < nu; ++u) {

@@ -359,7 +359,9 @@ __global__ void __launch_bounds__(512, 1) norm_fwd_ring_kernel(const NormParams 
   const int groups = blockDim.x / p.threads;
   const float inv_d = 1.f / static_cast<float>(p.d);
   const uint32_t vec = blockDim.x * 16, mine = smem_u32(ring) + threadIdx.x * 16;
-  auto place = [&](int slot, int stream, int r, int k) { return mine + static_cast<uint32_t>(((slot * STREAMS + stream) * R + r) * KC + k) * vec; };
+  auto place = [&](int slot, int stream, int r, int k) {
+    return mine + static_cast<uint32_t>(((slot * STREAMS + stream) * R + r) * KC + k) * vec;
+  };
   auto fetch = [&](int slot, int64_t row0) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -476,12 +478,13 @@ __global__ void __launch_bounds__(512, 1) norm_fwd_ring_kernel(const NormParams 
   copy_wait<0>();
 }
 
-// ---- Rows that are not made of 16-byte vectors (an odd width, stride or start). Their bytes still come as whole 16-byte vectors of
-// memory into the ring, shifted by the row's start modulo 16, and are taken apart there: a warp has 32 C consecutive columns, a lane
-// every 32nd of them (fewer lanes where a row takes part of a warp), so that a warp reads and writes consecutive elements. What these
-// kernels cost is instructions: warps whose columns all exist go without a test for each (51 instructions an element with them).
-// 65536 x 1001 bf16 110 us forward and 138 backward (0.35 and 0.42 of a copy's rate), fp32 128 and 156 (0.60 and 0.74). A vector's bytes in front
-// of or behind the row belong to the same tensor, except in front of its first element and behind its last one, which are not read.
+// ---- Rows that are not made of 16-byte vectors (an odd width, stride or start). Their bytes still come as whole 16-byte vectors
+// of memory into the ring, shifted by the row's start modulo 16, and are taken apart there: a warp has 32 C consecutive columns, a
+// lane every 32nd of them (fewer lanes where a row takes part of a warp), so that a warp reads and writes consecutive elements.
+// What these kernels cost is instructions: warps whose columns all exist go without a test for each (51 instructions an element
+// with them). 65536 x 1001 bf16 110 us forward and 138 backward (0.35 and 0.42 of a copy's rate), fp32 128 and 156 (0.60 and
+// 0.74). A vector's bytes in front of or behind the row belong to the same tensor, except in front of its first element and behind
+// its last one, which are not read.
 struct OddRows {
   uintptr_t base, end;  // of the tensor
   int64_t stride;       // bytes
@@ -489,7 +492,8 @@ struct OddRows {
 template <typename T>
 __device__ __forceinline__ OddRows odd_rows(const void* p, int64_t ld, const NormParams& n) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  return OddRows{a, a + static_cast<uintptr_t>(((n.N - 1) * ld + n.d) * static_cast<int64_t>(sizeof(T))), ld * static_cast<int64_t>(sizeof(T))};
+  constexpr int64_t E = sizeof(T);
+  return OddRows{a, a + static_cast<uintptr_t>(((n.N - 1) * ld + n.d) * E), ld * E};
 }
 // The group's threads copy row `row` to dst (16-byte aligned); its first element arrives at dst + odd_shift().
 __device__ __forceinline__ int odd_shift(const OddRows& x, int64_t row) { return static_cast<int>((x.base + row * x.stride) & 15); }
@@ -509,7 +513,8 @@ __device__ __forceinline__ void odd_fetch(const OddRows& x, int64_t row, int d, 
       }
     } else {
       const uintptr_t left = x.end - v;
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(v), "r"(left < 16 ? static_cast<int>(left) : 16) : "memory");
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                   :: "r"(dst), "l"(v), "r"(left < 16 ? static_cast<int>(left) : 16) : "memory");
     }
   }
 }
@@ -749,7 +754,8 @@ __global__ void __launch_bounds__(1024) norm_fwd_wide_kernel(const NormParams p)
 
 // One vector's part in dw, db and the two sums of its row. x: normalised values, g: dy.
 template <bool RMS, int N>
-__device__ __forceinline__ void column_step(const float (&x)[N], const float (&g)[N], const float* w, float* dw, float* db, float2& sx, float2& sg) {
+__device__ __forceinline__ void column_step(const float (&x)[N], const float (&g)[N], const float* w, float* dw, float* db, float2& sx,
+                                            float2& sg) {
 #pragma unroll
   for (int j = 0; j < N; j += 2) {
     const float2 gj = pair(g + j), xj = pair(x + j), gw = __fmul2_rn(gj, pair(w + j)), d = __ffma2_rn(gj, xj, pair(dw + j));
@@ -895,13 +901,16 @@ template <typename T, int KC, int R, int S, bool RMS, bool DSUM>
 __global__ void __launch_bounds__(512, 1) norm_bwd_ring_kernel(const NormParams p, const NormGrad q) {
   constexpr int VB = 16 / sizeof(T), C = KC * VB, STREAMS = DSUM ? 3 : 2;
   using V = Pack<T, VB>;
-  extern __shared__ __align__(16) float shared[];  // [2][32][2 R] sums of rows, then the ring [S][streams][R][KC][threads], or columns' sums
+  // [2][32][2 R] sums of rows, then the ring [S][streams][R][KC][threads], or columns' sums
+  extern __shared__ __align__(16) float shared[];
   uint8_t* ring = reinterpret_cast<uint8_t*>(shared + 128 * R);
   const int group = threadIdx.x / p.threads, t = threadIdx.x - group * p.threads;
   const int groups = blockDim.x / p.threads;
   const float inv_d = 1.f / static_cast<float>(p.d);
   const uint32_t vec = blockDim.x * 16, mine = smem_u32(ring) + threadIdx.x * 16;
-  auto place = [&](int slot, int stream, int r, int k) { return mine + static_cast<uint32_t>(((slot * STREAMS + stream) * R + r) * KC + k) * vec; };
+  auto place = [&](int slot, int stream, int r, int k) {
+    return mine + static_cast<uint32_t>(((slot * STREAMS + stream) * R + r) * KC + k) * vec;
+  };
   float dw[C], db[C], w[C];
 #pragma unroll
   for (int j = 0; j < C; ++j) dw[j] = db[j] = 0.f, w[j] = 1.f;
@@ -1022,7 +1031,8 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_ring_kernel(const NormParams 
 // for those of row i - 1, which the CTAs have sent one another meanwhile; the sending of row i's; dx of row i - 1. The sums
 // arrive with st.async, counted on a barrier of the CTA that receives them (a cluster barrier a turn took twice as long). Three
 // places for them are enough: a CTA sends row i + 3's only after it has this CTA's of row i + 2, sent after all here were done with
-// row i's. bf16 16384 x 5120 90 us (0.82 of a copy's rate), 4096 x 16384 87; fp32 8192 x 8192 141, 8192 x 16384 496 (0.48: an exchange a row, 38 rows at a time).
+// row i's. bf16 16384 x 5120 90 us (0.82 of a copy's rate), 4096 x 16384 87; fp32 8192 x 8192 141, 8192 x 16384 496 (0.48: an exchange
+// a row, 38 rows at a time).
 __device__ __forceinline__ void send_pair(uint32_t to, float a, float b, uint32_t bar) {
   asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];"
                :: "r"(to), "r"(__float_as_uint(a)), "r"(__float_as_uint(b)), "r"(bar) : "memory");
@@ -1031,7 +1041,8 @@ template <typename T, int KC, int S, bool RMS, bool DSUM>
 __global__ void __launch_bounds__(512, 1) norm_bwd_cluster_kernel(const NormParams p, const NormGrad q) {
   constexpr int VB = 16 / sizeof(T), C = KC * VB, STREAMS = DSUM ? 3 : 2;
   using V = Pack<T, VB>;
-  extern __shared__ __align__(16) float shared[];  // [2][16 warps][2] sums, [3][8 CTAs][2] exchanged ones, then the ring [S][streams][KC][threads]
+  // [2][16 warps][2] sums, [3][8 CTAs][2] exchanged ones, then the ring [S][streams][KC][threads]
+  extern __shared__ __align__(16) float shared[];
   float* across = shared + 64;
   __shared__ uint64_t arrived[3];
   __shared__ int given_up;
@@ -1136,7 +1147,8 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_cluster_kernel(const NormPara
         const float other = __shfl_xor_sync(0xffffffffu, sum, 16);
         if (lane == 0) mbar_arrive_expect_tx(arrived + i % 3, ctas * 8);
         if (lane < static_cast<int>(ctas))  // every lane tells one CTA
-          send_pair(mapa_shared(smem_u32(across + (i % 3) * 16 + rank * 2), lane), sum, other, mapa_shared(smem_u32(arrived + i % 3), lane));
+          send_pair(mapa_shared(smem_u32(across + (i % 3) * 16 + rank * 2), lane), sum, other,
+                    mapa_shared(smem_u32(arrived + i % 3), lane));
       }
       if (i > 0) finish(row - step, before, last, i - 1);
     }
@@ -1321,8 +1333,8 @@ cudaError_t fwd_ring(NormParams p, int sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int by_smem = kSmemPerSm / (smem + 1536), by_threads = (KC * 16 / sizeof(T) > 8 ? 512 : 768) / cta;
   const int64_t most = static_cast<int64_t>(sms) * (by_smem < by_threads ? by_smem : by_threads);
-  return launch(norm_fwd_ring_kernel<T, KC, R, S, RMS, BIAS, RES>, dim3(blocks_for(cdiv64(p.N, static_cast<int64_t>(cta / p.threads) * R), most)), cta,
-                smem, stream, false, p);
+  const int64_t blocks = cdiv64(p.N, static_cast<int64_t>(cta / p.threads) * R);
+  return launch(norm_fwd_ring_kernel<T, KC, R, S, RMS, BIAS, RES>, dim3(blocks_for(blocks, most)), cta, smem, stream, false, p);
 }
 
 template <typename T, int C, int R, int S>
@@ -1334,7 +1346,8 @@ cudaError_t fwd_odd(NormParams p, int sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int by_smem = kSmemPerSm / (smem + 1536), by_threads = 512 / cta;
   const int64_t most = static_cast<int64_t>(sms) * (by_smem < by_threads ? by_smem : by_threads);
-  return launch(norm_fwd_odd_kernel<T, C, R, S>, dim3(blocks_for(cdiv64(p.N, static_cast<int64_t>(groups) * R), most)), cta, smem, stream, false, p);
+  const int64_t blocks = cdiv64(p.N, static_cast<int64_t>(groups) * R);
+  return launch(norm_fwd_odd_kernel<T, C, R, S>, dim3(blocks_for(blocks, most)), cta, smem, stream, false, p);
 }
 
 // Eight columns a thread, two rows at a time; of rows of more than 4096 columns 16 or 32 columns, one row at a time.
@@ -1356,9 +1369,10 @@ cudaError_t fwd_cols(const NormParams& p, int sms, cudaStream_t stream) {
   } else {
     if (p.d <= 1024 * VB && p.N <= 4 * sms) return fwd<T, VB>(p, stream);
     if (p.d <= (sizeof(T) == 4 && p.residual ? 512 * 16 : 512 * 32)) {  // what the ring has room for
-      if (!p.rms) return p.residual ? fwd_rings<T, false, true, true>(p, sms, stream) : fwd_rings<T, false, true, false>(p, sms, stream);
-      if (p.bias == nullptr) return p.residual ? fwd_rings<T, true, false, true>(p, sms, stream) : fwd_rings<T, true, false, false>(p, sms, stream);
-      return p.residual ? fwd_rings<T, true, true, true>(p, sms, stream) : fwd_rings<T, true, true, false>(p, sms, stream);
+      const bool res = p.residual != nullptr;
+      if (!p.rms) return res ? fwd_rings<T, false, true, true>(p, sms, stream) : fwd_rings<T, false, true, false>(p, sms, stream);
+      if (!p.bias) return res ? fwd_rings<T, true, false, true>(p, sms, stream) : fwd_rings<T, true, false, false>(p, sms, stream);
+      return res ? fwd_rings<T, true, true, true>(p, sms, stream) : fwd_rings<T, true, true, false>(p, sms, stream);
     }
   }
   return launch(norm_fwd_wide_kernel<T, VB>, dim3(blocks_for(p.N, 2 * static_cast<int64_t>(sms))), 1024, 0, stream, false, p);
@@ -1435,7 +1449,8 @@ template <typename T, int VB>
 cudaError_t bwd_cols(NormParams p, const NormGrad& q, int* parts, int sms, cudaStream_t stream) {
   if constexpr (VB > 1) {
     if (p.d <= (sizeof(T) == 2 ? kNormFusedCols : kNormFusedCols / 2)) {
-      if (p.rms && !q.want_db) return q.dsum ? bwd_vectors<T, true, true>(p, q, parts, stream) : bwd_vectors<T, true, false>(p, q, parts, stream);
+      if (p.rms && !q.want_db)
+        return q.dsum ? bwd_vectors<T, true, true>(p, q, parts, stream) : bwd_vectors<T, true, false>(p, q, parts, stream);
       return q.dsum ? bwd_vectors<T, false, true>(p, q, parts, stream) : bwd_vectors<T, false, false>(p, q, parts, stream);
     }
   } else {
@@ -1469,8 +1484,10 @@ cudaError_t bwd_type(const NormParams& p, const NormGrad& q, int parts, int sms,
 
 int norm_parts(int64_t N, int d) {
   int64_t most;
-  if (d > kCtaCols) {  // clusters (of fp32 rows of one or two CTAs, two an SM), or stretches of rows that fill the SMs with 256 columns each
-    const int64_t clusters = d > kNormFusedCols ? 0 : 2 * kGridSms / cdiv64(d, 2 * kCtaCols), stretches = cdiv64(8 * kGridSms, cdiv64(d, 256));
+  // Clusters (of fp32 rows of one or two CTAs, two an SM), or stretches of rows that fill the SMs with 256 columns each.
+  if (d > kCtaCols) {
+    const int64_t clusters = d > kNormFusedCols ? 0 : 2 * kGridSms / cdiv64(d, 2 * kCtaCols);
+    const int64_t stretches = cdiv64(8 * kGridSms, cdiv64(d, 256));
     most = clusters > stretches ? clusters : stretches;
   } else {
     most = kGridSms * (512 / (d > 256 ? round_threads(cdiv64(d, kBwdCols)) : 128));  // 512 threads an SM
